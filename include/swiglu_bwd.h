@@ -345,6 +345,119 @@ swg_status group_norm_bwd(const void* dy, const void* x, const void* gamma, void
                           int64_t G, float eps, swg_dtype dtype, void* workspace,
                           size_t workspace_bytes, swg_stream_t stream);
 
+/* ---- layer norm ---------------------------------------------------------------
+ * No counterpart on the pages: the norm in front of a SwiGLU block. For each of
+ * M rows of N elements,
+ *   h = x + residual, rounded to `dtype` (h = x when residual is NULL)
+ *   mean = sum h / N, var = sum (h - mean)^2 / N (biased), rstd = 1/sqrt(var + eps)
+ *   y = (h - mean) rstd gamma + beta
+ * x, residual: [M, N] of `dtype`, rows ldx / ldr elements apart (a leading
+ * dimension of at least N, or 0 for one row shared by all). gamma, beta: [N] of
+ * `wdtype`, which is `dtype` or fp32; either may be NULL (1, 0). Outputs are
+ * contiguous: h [M, N] (required with a residual, else NULL), y [M, N], and
+ * stats [M, 2] fp32 = (mean, rstd), which the backward takes.
+ * layer_norm_bwd: with x the normalised tensor (h when there was a residual),
+ * x_hat = (x - mean) rstd and g = dy gamma,
+ *   dx     = rstd (g - mean(g) - x_hat mean(g x_hat)) + dh
+ *   dgamma = sum over rows of dy x_hat,  dbeta = sum over rows of dy
+ * dh [M, N] (NULL: 0) is the gradient that reaches h past the norm (a residual
+ * stream's); dx is then the gradient of x and of the residual alike. dgamma,
+ * dbeta ([N] of wdtype) are optional; when either is given `workspace` must hold
+ * layer_norm_bwd_workspace_size(M, N) bytes (16-byte aligned), else
+ * SWG_ERR_WORKSPACE.
+ * fp32 arithmetic, fixed orders of summation (bitwise reproducible), one
+ * rounding (RNE) for each output. Any M >= 0 and 0 <= N < 2^31; pointers aligned
+ * to their element size (SWG_ERR_UNSUPPORTED otherwise); 16-byte aligned rows are
+ * the fast case. M == 0 or N == 0: nothing is launched but zeros for dgamma,
+ * dbeta. Errors: negative sizes, a leading dimension of 1 .. N - 1 or below 0
+ * (M > 1), an unknown dtype, a wdtype that is neither dtype nor fp32, a negative
+ * or NaN eps, a residual without h or h without a residual, outputs that overlap
+ * inputs or each other -> SWG_ERR_PARAM_INVALID; a missing tensor
+ * -> SWG_ERR_NULLPTR; N or M >= 2^31 -> SWG_ERR_UNSUPPORTED. */
+swg_status layer_norm_fwd(const void* x, const void* residual, const void* gamma,
+                          const void* beta, void* h, void* y, float* stats, int64_t M,
+                          int64_t N, int64_t ldx, int64_t ldr, float eps, swg_dtype dtype,
+                          swg_dtype wdtype, swg_stream_t stream);
+size_t layer_norm_bwd_workspace_size(int64_t M, int64_t N);
+swg_status layer_norm_bwd(const void* dy, const void* x, const float* stats,
+                          const void* gamma, const void* dh, void* dx, void* dgamma,
+                          void* dbeta, int64_t M, int64_t N, int64_t lddy, int64_t ldx,
+                          int64_t lddh, swg_dtype dtype, swg_dtype wdtype, void* workspace,
+                          size_t workspace_bytes, swg_stream_t stream);
+
+/* index types of targets and teacher ids */
+typedef enum { SWG_I32 = 0, SWG_I64 = 1 } swg_itype;
+
+/* ---- log probabilities of given tokens ----------------------------------------
+ * No counterpart on the pages. For each of T rows of V logits (of `dtype`, rows
+ * ld elements apart: ld >= V, or 0 for one row shared by all) at a temperature
+ * tau > 0:
+ *   d_j = (z_j - max z) / tau, s = sum exp(d_j), ln p_j = d_j - ln s
+ *   logp = ln p_target, entropy = -sum p ln p, stats = (max z, s)
+ *   top_idx, top_logp [T, top_k]: the top_k largest logits, in descending order,
+ *     equal ones by the lower index, and their ln p (top_k <= min(V, 32))
+ * A target equal to ignore_index gives logp 0; any other target outside [0, V)
+ * gives NaN. targets may be NULL (then logp is too). A logit of -inf has
+ * probability 0 and ln p = -inf; a row of nothing else has stats (-inf, 0),
+ * entropy 0 and ln p = -inf everywhere. A NaN or +inf logit makes the row's
+ * results NaN; among the alternatives a NaN ranks with -inf.
+ * token_logprobs_bwd, from the forward's stats (and entropy, with dentropy):
+ *   dz_j = (1/tau) (dlogp ([j = target] - p_j) - dentropy p_j (ln p_j + entropy))
+ * dlogp counts as 0 where the target is ignored; dentropy may be NULL, and
+ * targets and dlogp may be NULL together. A row of -inf has gradient 0. dlogits
+ * [T, V], rows ldo apart (>= V), may be the logits themselves (same pointer and
+ * leading dimension), and overlaps no other input.
+ * fp32 arithmetic, bitwise reproducible, one rounding (RNE) for each output.
+ * T == 0: nothing is launched. Errors: T < 0, V < 1, a bad leading dimension,
+ * dtype, itype, top_k or temperature (not finite and positive), overlapping
+ * buffers -> SWG_ERR_PARAM_INVALID; missing tensors -> SWG_ERR_NULLPTR; pointers
+ * not aligned to their element size, T or V >= 2^31 - 1 -> SWG_ERR_UNSUPPORTED. */
+swg_status token_logprobs_fwd(const void* logits, const void* targets, float* logp,
+                              float* entropy, float* stats, float* top_logp,
+                              int64_t* top_idx, int64_t T, int64_t V, int64_t ld, int top_k,
+                              float temperature, int64_t ignore_index, swg_dtype dtype,
+                              swg_itype itype, swg_stream_t stream);
+swg_status token_logprobs_bwd(const float* dlogp, const void* logits, const void* targets,
+                              const float* stats, const float* dentropy,
+                              const float* entropy, void* dlogits, int64_t T, int64_t V,
+                              int64_t ld, int64_t ldo, float temperature,
+                              int64_t ignore_index, swg_dtype dtype, swg_itype itype,
+                              swg_stream_t stream);
+
+/* ---- distillation from a teacher's top logits ----------------------------------
+ * No counterpart on the pages. A row's teacher is K <= 1024 entries: ids [T, K]
+ * (of `itype`) and logits [T, K] (of `tdtype`: fp32, fp16 or bf16), both
+ * contiguous; an id outside [0, V) marks an absent entry, an id that comes twice
+ * counts twice. With the student's logits z ([T, V] of `dtype`, rows ld apart),
+ * both sides at the temperature tau > 0:
+ *   q = softmax of the entries' t / tau, ln p as in token_logprobs_fwd
+ *   loss  = sum_k q_k (ln q_k - ln p_{i_k}), stats = (max z, sum exp((z - max z) / tau))
+ *   dz_j  = (weight / tau) (Q p_j - sum of the q_k with i_k = j)
+ * Q = 1, or 0 for a row without entries (all absent, or all -inf): its loss is 0
+ * and it has no gradient. The loss is +inf where an entry of positive q has a
+ * student logit of -inf. weight [T] is the loss's upstream gradient (1 / T for a
+ * mean; padding tokens 0, which gives a gradient of exactly 0); the loss and the
+ * stats do not depend on it. No tau^2 factor is applied: it belongs in weight.
+ * distill_fwd gives loss [T] and stats [T, 2] (fp32), distill_bwd the gradient
+ * from saved stats, distill_fwd_bwd everything from one read of the logits where
+ * a row fits on the chip. dlogits, leading dimensions, arithmetic, rounding,
+ * NaNs and errors as in token_logprobs_*; K < 1 -> SWG_ERR_PARAM_INVALID,
+ * K > 1024 -> SWG_ERR_UNSUPPORTED. */
+swg_status distill_fwd(const void* logits, const void* ids, const void* teacher, float* loss,
+                       float* stats, int64_t T, int64_t V, int64_t ld, int64_t K,
+                       float temperature, swg_dtype dtype, swg_dtype tdtype, swg_itype itype,
+                       swg_stream_t stream);
+swg_status distill_bwd(const float* weight, const void* logits, const void* ids,
+                       const void* teacher, const float* stats, void* dlogits, int64_t T,
+                       int64_t V, int64_t ld, int64_t ldo, int64_t K, float temperature,
+                       swg_dtype dtype, swg_dtype tdtype, swg_itype itype,
+                       swg_stream_t stream);
+swg_status distill_fwd_bwd(const void* logits, const void* ids, const void* teacher,
+                           const float* weight, float* loss, float* stats, void* dlogits,
+                           int64_t T, int64_t V, int64_t ld, int64_t ldo, int64_t K,
+                           float temperature, swg_dtype dtype, swg_dtype tdtype,
+                           swg_itype itype, swg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

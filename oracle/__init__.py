@@ -21,6 +21,9 @@ It restates, in plain numpy float64, what two pages define:
 * The GroupNorm backward of the Ascend C backward blog post (its GroupNorm
   section, both printed versions): dx by the post's formula, dgamma and dbeta
   by their standard definitions: `group_norm.py`.
+* Layer norm, log probabilities of given tokens and distillation from a
+  teacher's top logits by their standard definitions (no page prints them):
+  `layer_norm.py`, `vocabulary.py`.
 
 Library primitives used as steps: numpy.exp, numpy matmul, numpy.sum, numpy.mean.
 Parity status: every function here is pinned by the `-m "not gpu"` tests
@@ -48,3 +51,12 @@ from .swiglu import (  # noqa: F401
 from .swish import swish_fwd, swish_grad  # noqa: F401
 from .activations import act_grad, gelu_grad, hardswish_grad, silu_act_grad  # noqa: F401
 from .group_norm import group_norm_bwd, group_norm_fwd, group_norm_stats  # noqa: F401
+from .layer_norm import layer_norm_bwd, layer_norm_fwd  # noqa: F401
+from .vocabulary import (  # noqa: F401
+    distill_bwd,
+    distill_fwd,
+    row_softmax,
+    teacher_probs,
+    token_logprobs_bwd,
+    token_logprobs_fwd,
+)

@@ -9,6 +9,7 @@ library is missing the import of this module raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -51,6 +52,9 @@ EXPORTS = (
     "group_norm_bwd_workspace_size", "group_norm_bwd",
     "swiglu_bwd_host_workspace_size", "swiglu_bwd_host",
     "swg_inject_stall",
+    "layer_norm_fwd", "layer_norm_bwd_workspace_size", "layer_norm_bwd",
+    "token_logprobs_fwd", "token_logprobs_bwd",
+    "distill_fwd", "distill_bwd", "distill_fwd_bwd",
 )
 
 
@@ -112,6 +116,23 @@ def _load() -> ctypes.CDLL:
     lib.swiglu_bwd_w_fused_workspace_size.restype = SZ
     lib.swiglu_bwd_w_fused.argtypes = [P] * 8 + [I64, I64, I64, P, SZ, P]
     lib.swiglu_bwd_w_fused.restype = st
+    I, F = ctypes.c_int, ctypes.c_float
+    lib.layer_norm_fwd.argtypes = [P] * 7 + [I64] * 4 + [F, I, I, P]
+    lib.layer_norm_fwd.restype = st
+    lib.layer_norm_bwd_workspace_size.argtypes = [I64, I64]
+    lib.layer_norm_bwd_workspace_size.restype = SZ
+    lib.layer_norm_bwd.argtypes = [P] * 8 + [I64] * 5 + [I, I, P, SZ, P]
+    lib.layer_norm_bwd.restype = st
+    lib.token_logprobs_fwd.argtypes = [P] * 7 + [I64] * 3 + [I, F, I64, I, I, P]
+    lib.token_logprobs_fwd.restype = st
+    lib.token_logprobs_bwd.argtypes = [P] * 7 + [I64] * 4 + [F, I64, I, I, P]
+    lib.token_logprobs_bwd.restype = st
+    lib.distill_fwd.argtypes = [P] * 5 + [I64] * 4 + [F, I, I, I, P]
+    lib.distill_fwd.restype = st
+    lib.distill_bwd.argtypes = [P] * 6 + [I64] * 5 + [F, I, I, I, P]
+    lib.distill_bwd.restype = st
+    lib.distill_fwd_bwd.argtypes = [P] * 7 + [I64] * 5 + [F, I, I, I, P]
+    lib.distill_fwd_bwd.restype = st
     return lib
 
 
@@ -528,3 +549,293 @@ def swiglu_bwd_b_noalloc(dy, g, fc, dg=None, dfc=None, db_g=None, db_fc=None, st
                  dfc.data_ptr(), db_g.data_ptr(), db_fc.data_ptr(), M, N, _stream(stream, dev)),
            "swiglu_bwd_b_noalloc")
     return dg, dfc, db_g, db_fc
+
+
+# ------------------------------------------------------------- row-wise operators
+def _on_stream(fn):
+    """Give a row-wise operator its `stream` argument: with one, everything the call does (copies of
+    strided inputs, allocations, kernels) is on that stream, and the caller's tensors are recorded
+    on it, so that their memory is not handed out again before it has run."""
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        tensors = [t for t in (*args, *kwargs.values(), *(kwargs.get("out") or {}).values())
+                   if isinstance(t, torch.Tensor) and t.is_cuda]
+        if not tensors:
+            return fn(*args, **kwargs)  # raises
+        dev = tensors[0].device
+        handle = _stream(stream, dev)
+        s = torch.cuda.default_stream(dev) if handle == 0 else torch.cuda.ExternalStream(handle, device=dev)
+        with torch.cuda.stream(s):
+            out = fn(*args, **kwargs)
+        for t in tensors:
+            t.record_stream(s)
+        return out
+
+    return call
+
+
+def _run(what, fn, dev, *args):
+    """One C call on `dev` and its current stream; raises on an error status."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, stream)
+    else:
+        status = _call(dev, fn, *args, stream)
+    if status != SWG_OK:
+        _check(status, what)
+
+
+def _row_tensor(t, name):
+    """A tensor [..., N] as the kernels take it: (tensor, rows, N, row stride in elements, dtype code).
+    Rows may lie apart (a slice of wider rows) or be one shared row; anything else is copied."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
+    if t.dim() == 2:
+        M, N = t.shape
+        ld, step = t.stride()
+        if M <= 1:
+            ld = N
+        if (step == 1 or N <= 1) and (ld >= N or ld == 0):
+            return t, M, N, ld, code
+        return t.contiguous(), M, N, N, code
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    N = t.shape[-1]
+    M = 1
+    for d in t.shape[:-1]:
+        M *= d
+    return t.contiguous(), M, N, N, code
+
+
+def _like_rows(t, name, x, shape):
+    """A second input of x's shape and dtype: (tensor, row stride); (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if isinstance(t, torch.Tensor) and (t.dtype != x.dtype or t.shape != shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)} and dtype {x.dtype}, got {tuple(t.shape)}, {t.dtype}")
+    t, _, _, ld, _ = _row_tensor(t, name)
+    return t, ld
+
+
+def _vector(t, name, n, dtypes, device):
+    """A dense tensor of n elements of one of `dtypes` on `device` (None stays None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes or t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements of {' or '.join(map(str, dtypes))}, "
+                         f"got {t.numel()} of {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"all tensors must be on one device: got {device} and {t.device}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+_F32 = (torch.float32,)
+_INDEX = (torch.int64, torch.int32)
+
+
+def _norm_weights(gamma, beta, N, x):
+    """gamma and beta (either None) checked, with their common dtype code."""
+    allowed = (x.dtype, torch.float32)
+    gamma = _vector(gamma, "gamma", N, allowed, x.device)
+    beta = _vector(beta, "beta", N, allowed if gamma is None else (gamma.dtype,), x.device)
+    w = gamma if gamma is not None else beta
+    return gamma, beta, w.dtype if w is not None else x.dtype
+
+
+@_on_stream
+def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, out: dict | None = None) -> dict:
+    """Layer norm of x [..., N] over its last dimension (fp32/fp16/bf16): a dict of y and stats [M, 2]
+    (fp32 mean and 1/sqrt(var + eps) of the M rows), and of h = x + residual, the tensor that is
+    normalised, when a residual of x's shape is given. gamma, beta [N] (x's dtype or fp32, both the
+    same) may be None. `out` may supply any of the outputs; stream: the stream to run on."""
+    shape = x.shape if isinstance(x, torch.Tensor) else None
+    xt, M, N, ldx, code = _row_tensor(x, "x")
+    res, ldr = _like_rows(residual, "residual", xt, shape)
+    gamma, beta, wdtype = _norm_weights(gamma, beta, N, xt)
+    dev = xt.device
+    if out is None:
+        out = {"y": torch.empty(shape, dtype=xt.dtype, device=dev),
+               "stats": torch.empty((M, 2), dtype=torch.float32, device=dev)}
+        if res is not None:
+            out["h"] = torch.empty(shape, dtype=xt.dtype, device=dev)
+    else:
+        out = dict(out)
+        out["y"] = _out(out.get("y"), shape, xt.dtype, dev, "y")
+        out["stats"] = _out(out.get("stats"), (M, 2), torch.float32, dev, "stats")
+        if res is not None:
+            out["h"] = _out(out.get("h"), shape, xt.dtype, dev, "h")
+    if res is not None and res.device != dev:
+        _device_of(xt, res)
+    _run("layer_norm_fwd", lib.layer_norm_fwd, dev, xt.data_ptr(), _ptr(res), _ptr(gamma), _ptr(beta),
+         out["h"].data_ptr() if res is not None else None, out["y"].data_ptr(), out["stats"].data_ptr(), M, N, ldx,
+         ldr, eps, code, _DTYPE[wdtype])
+    return out
+
+
+def layer_norm_bwd_workspace_size(M: int, N: int) -> int:
+    return lib.layer_norm_bwd_workspace_size(M, N)
+
+
+@_on_stream
+def layer_norm_bwd(dy, x, stats, gamma=None, dh=None, params: bool = True, dx=None, dgamma=None, dbeta=None,
+                   workspace=None):
+    """Layer norm backward: (dx, dgamma, dbeta) for dy and x [..., N], x being the tensor that was
+    normalised (the forward's h when it had a residual) and stats the forward's. gamma may be None (1);
+    dgamma and dbeta have its dtype (x's without it) and are None when params is False. dh, if given, is
+    the gradient that reaches the normalised tensor past the norm: it is added to dx."""
+    shape = x.shape if isinstance(x, torch.Tensor) else None
+    xt, M, N, ldx, code = _row_tensor(x, "x")
+    if dy is None:
+        raise TypeError("dy must be a CUDA tensor")
+    dyt, lddy = _like_rows(dy, "dy", xt, shape)
+    dht, lddh = _like_rows(dh, "dh", xt, shape)
+    dev = xt.device
+    stats = _vector(stats, "stats", 2 * M, _F32, dev)
+    if stats is None:
+        raise TypeError("stats must be a CUDA tensor")
+    gamma, _, wdtype = _norm_weights(gamma, None, N, xt)
+    dx = torch.empty(shape, dtype=xt.dtype, device=dev) if dx is None else _out(dx, shape, xt.dtype, dev, "dx")
+    ws = None
+    if params:
+        dgamma = _out(dgamma, (N,), wdtype, dev, "dgamma")
+        dbeta = _out(dbeta, (N,), wdtype, dev, "dbeta")
+        ws = _workspace(_call(dev, lib.layer_norm_bwd_workspace_size, M, N) if torch.cuda.current_device() != dev.index
+                        else lib.layer_norm_bwd_workspace_size(M, N), dev, workspace)
+    else:
+        dgamma = dbeta = None
+    _device_of(xt, dyt, dht, ws)
+    _run("layer_norm_bwd", lib.layer_norm_bwd, dev, dyt.data_ptr(), xt.data_ptr(), stats.data_ptr(), _ptr(gamma),
+         _ptr(dht), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta), M, N, lddy, ldx, lddh, code, _DTYPE[wdtype], _ptr(ws),
+         _nbytes(ws))
+    return dx, dgamma, dbeta
+
+
+def _dlogits(t, shape, x, M, N):
+    """The gradient's buffer: allocated, or the caller's, with dense rows that may lie apart (the
+    logits themselves, for instance): (tensor, row stride)."""
+    if t is None:
+        return torch.empty(shape, dtype=x.dtype, device=x.device), N
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.device == x.device and t.dtype == x.dtype and t.shape == shape:
+        if t.is_contiguous():
+            return t, N
+        if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= N:
+            return t, t.stride(0)
+    raise ValueError(f"dlogits must be a {x.dtype} CUDA tensor of shape {tuple(shape)} on {x.device} with dense rows")
+
+
+@_on_stream
+def token_logprobs_fwd(logits, targets=None, top_k: int = 0, temperature: float = 1.0, ignore_index: int = -100,
+                       out: dict | None = None) -> dict:
+    """Log probabilities of the given tokens under softmax(logits / temperature), logits [..., V]
+    (fp32/fp16/bf16, rows may lie apart): a dict of logp [...] (absent without targets; 0 where the
+    target is ignore_index, NaN for another target outside the vocabulary), entropy [...], stats [T, 2]
+    for the backward, and with top_k (at most 32) top_logp and top_idx [..., top_k], the largest logits
+    in descending order, equal ones by the lower index. targets: int64 or int32 of logits' leading
+    shape. `out` may supply any of the outputs; stream: the stream to run on."""
+    lead = logits.shape[:-1] if isinstance(logits, torch.Tensor) else None
+    z, T, V, ld, code = _row_tensor(logits, "logits")
+    dev = z.device
+    targets = _vector(targets, "targets", T, _INDEX, dev)
+    given = out or {}
+    f32, mk = torch.float32, (lambda k, shape, dt: torch.empty(shape, dtype=dt, device=dev) if given.get(k) is None
+                              else _out(given[k], shape, dt, dev, k))
+    out = {"entropy": mk("entropy", lead, f32), "stats": mk("stats", (T, 2), f32)}
+    if targets is not None:
+        out["logp"] = mk("logp", lead, f32)
+    if top_k > 0:
+        out["top_logp"] = mk("top_logp", (*lead, top_k), f32)
+        out["top_idx"] = mk("top_idx", (*lead, top_k), torch.int64)
+    _run("token_logprobs_fwd", lib.token_logprobs_fwd, dev, z.data_ptr(), _ptr(targets), _ptr(out.get("logp")),
+         out["entropy"].data_ptr(), out["stats"].data_ptr(), _ptr(out.get("top_logp")), _ptr(out.get("top_idx")),
+         T, V, ld, top_k, temperature, ignore_index, code, _itype(targets))
+    return out
+
+
+def _itype(t):
+    return 0 if t is not None and t.dtype == torch.int32 else 1
+
+
+@_on_stream
+def token_logprobs_bwd(dlogp, logits, targets, stats, dentropy=None, entropy=None, temperature: float = 1.0,
+                       ignore_index: int = -100, dlogits=None):
+    """The gradient of token_logprobs_fwd with respect to the logits, from its stats (and its entropy,
+    when dentropy is given). dlogp and targets may be None together. dlogits may be the logits
+    themselves."""
+    shape = logits.shape if isinstance(logits, torch.Tensor) else None
+    z, T, V, ld, code = _row_tensor(logits, "logits")
+    dev = z.device
+    targets = _vector(targets, "targets", T, _INDEX, dev)
+    dlogp = _vector(dlogp, "dlogp", T, _F32, dev)
+    dentropy, entropy = _vector(dentropy, "dentropy", T, _F32, dev), _vector(entropy, "entropy", T, _F32, dev)
+    stats = _vector(stats, "stats", 2 * T, _F32, dev)
+    dlogits, ldo = _dlogits(dlogits, shape, z, T, V)
+    _run("token_logprobs_bwd", lib.token_logprobs_bwd, dev, _ptr(dlogp), z.data_ptr(), _ptr(targets), _ptr(stats),
+         _ptr(dentropy), _ptr(entropy), dlogits.data_ptr(), T, V, ld, ldo, temperature, ignore_index, code,
+         _itype(targets))
+    return dlogits
+
+
+def _distill_inputs(logits, teacher_ids, teacher_logits):
+    shape = logits.shape if isinstance(logits, torch.Tensor) else None
+    z, T, V, ld, code = _row_tensor(logits, "logits")
+    if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() < 1 or teacher_ids.shape[:-1] != shape[:-1]:
+        raise ValueError(f"teacher_ids must have the shape {tuple(shape[:-1])} + (K,)")
+    K = teacher_ids.shape[-1]
+    ids = _vector(teacher_ids, "teacher_ids", T * K, _INDEX, z.device)
+    tl = _vector(teacher_logits, "teacher_logits", T * K, tuple(_DTYPE), z.device)
+    if tl is None:
+        raise TypeError("teacher_logits must be a CUDA tensor")
+    return shape, z, T, V, ld, code, ids, tl, K
+
+
+@_on_stream
+def distill_fwd(logits, teacher_ids, teacher_logits, temperature: float = 1.0, out: dict | None = None) -> dict:
+    """Distillation loss of student logits [..., V] (fp32/fp16/bf16, rows may lie apart) against a
+    teacher's top logits: teacher_ids [..., K] (int64 or int32; outside the vocabulary: absent) and
+    teacher_logits [..., K] (fp32/fp16/bf16). A dict of loss [...] = sum q (ln q - ln p), q the softmax of
+    the entries and p the student's, both at `temperature`, and stats [T, 2] for the backward."""
+    shape, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
+    given = out or {}
+    out = {"loss": _out(given.get("loss"), shape[:-1], torch.float32, z.device, "loss"),
+           "stats": _out(given.get("stats"), (T, 2), torch.float32, z.device, "stats")}
+    _run("distill_fwd", lib.distill_fwd, z.device, z.data_ptr(), ids.data_ptr(), tl.data_ptr(),
+         out["loss"].data_ptr(), out["stats"].data_ptr(), T, V, ld, K, temperature, code, _DTYPE[tl.dtype], _itype(ids))
+    return out
+
+
+@_on_stream
+def distill_bwd(weight, logits, teacher_ids, teacher_logits, stats, temperature: float = 1.0, dlogits=None):
+    """The gradient of sum(weight * loss) with respect to the logits, weight [...] fp32, from the
+    forward's stats. dlogits may be the logits themselves."""
+    shape, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
+    weight, stats = _vector(weight, "weight", T, _F32, z.device), _vector(stats, "stats", 2 * T, _F32, z.device)
+    dlogits, ldo = _dlogits(dlogits, shape, z, T, V)
+    _run("distill_bwd", lib.distill_bwd, z.device, _ptr(weight), z.data_ptr(), ids.data_ptr(), tl.data_ptr(),
+         _ptr(stats), dlogits.data_ptr(), T, V, ld, ldo, K, temperature, code, _DTYPE[tl.dtype], _itype(ids))
+    return dlogits
+
+
+@_on_stream
+def distill_fwd_bwd(logits, teacher_ids, teacher_logits, weight, temperature: float = 1.0,
+                    out: dict | None = None) -> dict:
+    """distill_fwd and distill_bwd in one call, for a weight known beforehand (1 / T for a mean): a dict of
+    loss, stats and dlogits. Where a row fits on the chip the logits are read once. `out` may supply any
+    of the outputs; out["dlogits"] may be the logits themselves."""
+    shape, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
+    weight = _vector(weight, "weight", T, _F32, z.device)
+    given = out or {}
+    out = {"loss": _out(given.get("loss"), shape[:-1], torch.float32, z.device, "loss"),
+           "stats": _out(given.get("stats"), (T, 2), torch.float32, z.device, "stats")}
+    out["dlogits"], ldo = _dlogits(given.get("dlogits"), shape, z, T, V)
+    _run("distill_fwd_bwd", lib.distill_fwd_bwd, z.device, z.data_ptr(), ids.data_ptr(), tl.data_ptr(), _ptr(weight),
+         out["loss"].data_ptr(), out["stats"].data_ptr(), out["dlogits"].data_ptr(), T, V, ld, ldo, K, temperature,
+         code, _DTYPE[tl.dtype], _itype(ids))
+    return out

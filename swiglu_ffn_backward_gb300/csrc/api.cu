@@ -815,4 +815,242 @@ swg_status swiglu_bwd(const void* x, const void* w_g, const void* w_fc, const vo
   return cuda_status(e);
 }
 
+// ---------------------------------------------------------------- row-wise operators
+namespace {
+
+inline bool known_dtype(int d) { return d == SWG_F32 || d == SWG_F16 || d == SWG_BF16; }
+inline int64_t dtype_bytes(int d) { return d == SWG_F32 ? 4 : 2; }
+inline bool aligned_to(const void* p, int64_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) == 0;
+}
+constexpr int64_t kMaxLd = int64_t(1) << 40;
+// offsets in bytes of rows x n elements stay far inside 64 bits
+inline bool too_large(int64_t rows, int64_t n) { return n > 0 && rows > (int64_t(1) << 58) / n; }
+
+// rows of n elements ld apart: an input may share one row (ld 0), an output's rows are apart
+inline bool ld_ok(int64_t ld, int64_t rows, int64_t n, bool output) {
+  return rows <= 1 || ld >= n || (ld == 0 && !output);
+}
+// the bytes that such a tensor spans
+inline Range rows_rng(const void* p, int64_t rows, int64_t n, int64_t ld, int64_t es) {
+  return rng(p, p == nullptr || rows <= 0 || n <= 0 ? 0 : ((rows > 1 ? (rows - 1) * ld : 0) + n) * es);
+}
+
+// the checks that token_logprobs_* and distill_* share
+swg_status check_vocab(const void* logits, int64_t T, int64_t V, int64_t ld, float temperature, int dtype, int itype) {
+  if (T < 0 || V < 1 || !known_dtype(dtype) || (itype != SWG_I32 && itype != SWG_I64)) return SWG_ERR_PARAM_INVALID;
+  const float inv = 1.0f / temperature;
+  if (!(temperature > 0.0f) || !(inv > 0.0f) || inv > 3e38f) return SWG_ERR_PARAM_INVALID;
+  if (!ld_ok(ld, T, V, false)) return SWG_ERR_PARAM_INVALID;
+  if (T >= kMaxDim || V >= kMaxDim || too_large(T, V) || (T > 1 && (ld > kMaxLd || too_large(T, ld))))
+    return SWG_ERR_UNSUPPORTED;
+  if (!aligned_to(logits, dtype_bytes(dtype))) return SWG_ERR_UNSUPPORTED;
+  return SWG_OK;
+}
+// dlogits against the logits (the same tensor, or apart from it) and the other inputs
+swg_status check_dlogits(const void* dlogits, int64_t ldo, const void* logits, int64_t ld, int64_t T, int64_t V,
+                         int dtype, const Range* ins, int nin) {
+  const int64_t es = dtype_bytes(dtype);
+  if (!ld_ok(ldo, T, V, true)) return SWG_ERR_PARAM_INVALID;
+  if ((T > 1 && (ldo > kMaxLd || too_large(T, ldo))) || !aligned_to(dlogits, es)) return SWG_ERR_UNSUPPORTED;
+  const Range o = rows_rng(dlogits, T, V, ldo, es);
+  const bool same = dlogits == logits && (T <= 1 || ldo == ld);
+  if (!same && overlap(o, rows_rng(logits, T, V, ld, es))) return SWG_ERR_PARAM_INVALID;
+  return any_overlap(&o, 1, ins, nin) ? SWG_ERR_PARAM_INVALID : SWG_OK;
+}
+
+}  // namespace
+
+swg_status layer_norm_fwd(const void* x, const void* residual, const void* gamma, const void* beta, void* h, void* y,
+                          float* stats, int64_t M, int64_t N, int64_t ldx, int64_t ldr, float eps, swg_dtype dtype,
+                          swg_dtype wdtype, swg_stream_t stream) {
+  if (!known_dtype(dtype) || (wdtype != dtype && wdtype != SWG_F32)) return SWG_ERR_PARAM_INVALID;
+  if (M < 0 || N < 0 || !(eps >= 0.0f)) return SWG_ERR_PARAM_INVALID;
+  if (!ld_ok(ldx, M, N, false) || (residual != nullptr && !ld_ok(ldr, M, N, false))) return SWG_ERR_PARAM_INVALID;
+  if (M >= kMaxDim || N >= kMaxDim || too_large(M, N)) return SWG_ERR_UNSUPPORTED;
+  for (const int64_t ld : {ldx, residual != nullptr ? ldr : 0})
+    if (M > 1 && (ld > kMaxLd || too_large(M, ld))) return SWG_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return SWG_OK;
+  if (x == nullptr || y == nullptr || stats == nullptr) return SWG_ERR_NULLPTR;
+  if ((residual == nullptr) != (h == nullptr)) return SWG_ERR_PARAM_INVALID;
+  const int64_t es = dtype_bytes(dtype), ws = dtype_bytes(wdtype);
+  if (!aligned_to(x, es) || !aligned_to(residual, es) || !aligned_to(h, es) || !aligned_to(y, es) ||
+      !aligned_to(gamma, ws) || !aligned_to(beta, ws) || !aligned_to(stats, 4))
+    return SWG_ERR_UNSUPPORTED;
+  const Range outs[] = {rng(y, M * N * es), rng(h, h ? M * N * es : 0), rng(stats, M * 8)};
+  const Range ins[] = {rows_rng(x, M, N, ldx, es), rows_rng(residual, M, N, ldr, es), rng(gamma, gamma ? N * ws : 0),
+                       rng(beta, beta ? N * ws : 0)};
+  if (any_overlap(outs, 3, ins, 4)) return SWG_ERR_PARAM_INVALID;
+  const swg_status st = check_device();
+  if (st != SWG_OK) return st;
+  const swg::LnFwdArgs a{x, residual, gamma, beta, h, y, stats, M, N, M > 1 ? ldx : 0, M > 1 ? ldr : 0, eps,
+                         static_cast<int>(wdtype)};
+  return cuda_status(swg::launch_layer_norm_fwd(a, static_cast<int>(dtype), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t layer_norm_bwd_workspace_size(int64_t M, int64_t N) {
+  if (M <= 0 || N <= 0 || M >= kMaxDim || N >= kMaxDim) return 0;
+  return swg::ln_workspace_bytes(M, N);
+}
+
+swg_status layer_norm_bwd(const void* dy, const void* x, const float* stats, const void* gamma, const void* dh,
+                          void* dx, void* dgamma, void* dbeta, int64_t M, int64_t N, int64_t lddy, int64_t ldx,
+                          int64_t lddh, swg_dtype dtype, swg_dtype wdtype, void* workspace, size_t workspace_bytes,
+                          swg_stream_t stream) {
+  if (!known_dtype(dtype) || (wdtype != dtype && wdtype != SWG_F32)) return SWG_ERR_PARAM_INVALID;
+  if (M < 0 || N < 0) return SWG_ERR_PARAM_INVALID;
+  if (!ld_ok(lddy, M, N, false) || !ld_ok(ldx, M, N, false) || (dh != nullptr && !ld_ok(lddh, M, N, false)))
+    return SWG_ERR_PARAM_INVALID;
+  if (M >= kMaxDim || N >= kMaxDim || too_large(M, N)) return SWG_ERR_UNSUPPORTED;
+  for (const int64_t ld : {lddy, ldx, dh != nullptr ? lddh : 0})
+    if (M > 1 && (ld > kMaxLd || too_large(M, ld))) return SWG_ERR_UNSUPPORTED;
+  if (N == 0) return SWG_OK;
+  const int64_t es = dtype_bytes(dtype), ws = dtype_bytes(wdtype);
+  if (!aligned_to(dy, es) || !aligned_to(x, es) || !aligned_to(dh, es) || !aligned_to(dx, es) ||
+      !aligned_to(stats, 4) || !aligned_to(gamma, ws) || !aligned_to(dgamma, ws) || !aligned_to(dbeta, ws))
+    return SWG_ERR_UNSUPPORTED;
+  if (M > 0 && (dy == nullptr || x == nullptr || stats == nullptr || dx == nullptr)) return SWG_ERR_NULLPTR;
+  const Range outs[] = {rng(dx, M * N * es), rng(dgamma, dgamma ? N * ws : 0), rng(dbeta, dbeta ? N * ws : 0)};
+  const Range ins[] = {rows_rng(dy, M, N, lddy, es), rows_rng(x, M, N, ldx, es), rows_rng(dh, M, N, lddh, es),
+                       rng(stats, M * 8), rng(gamma, gamma ? N * ws : 0)};
+  if (any_overlap(outs, 3, ins, 5)) return SWG_ERR_PARAM_INVALID;
+  const bool params = dgamma != nullptr || dbeta != nullptr;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    if (!params) return SWG_OK;
+    const swg_status s = check_device();
+    if (s != SWG_OK) return s;
+    if (dgamma != nullptr && cudaMemsetAsync(dgamma, 0, static_cast<size_t>(N * ws), st) != cudaSuccess)
+      return SWG_ERR_CUDA;
+    if (dbeta != nullptr && cudaMemsetAsync(dbeta, 0, static_cast<size_t>(N * ws), st) != cudaSuccess)
+      return SWG_ERR_CUDA;
+    return SWG_OK;
+  }
+  if (params) {
+    const size_t need = swg::ln_workspace_bytes(M, N);
+    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return SWG_ERR_WORKSPACE;
+    const Range w = rng(workspace, static_cast<int64_t>(need));
+    if (any_overlap(&w, 1, outs, 3) || any_overlap(&w, 1, ins, 5)) return SWG_ERR_PARAM_INVALID;
+  }
+  const swg_status s = check_device();
+  if (s != SWG_OK) return s;
+  const swg::LnBwdArgs a{dy, x, stats, gamma, dh, dx, dgamma, dbeta, params ? static_cast<float*>(workspace) : nullptr,
+                         M, N, M > 1 ? lddy : 0, M > 1 ? ldx : 0, M > 1 ? lddh : 0, static_cast<int>(wdtype)};
+  return cuda_status(swg::launch_layer_norm_bwd(a, static_cast<int>(dtype), st));
+}
+
+swg_status token_logprobs_fwd(const void* logits, const void* targets, float* logp, float* entropy, float* stats,
+                              float* top_logp, int64_t* top_idx, int64_t T, int64_t V, int64_t ld, int top_k,
+                              float temperature, int64_t ignore_index, swg_dtype dtype, swg_itype itype,
+                              swg_stream_t stream) {
+  const swg_status st = check_vocab(logits, T, V, ld, temperature, dtype, itype);
+  if (st != SWG_OK) return st;
+  if (top_k < 0 || top_k > swg::kMaxTop || top_k > V) return SWG_ERR_PARAM_INVALID;
+  if (T == 0) return SWG_OK;
+  if (logits == nullptr || entropy == nullptr || stats == nullptr || (targets != nullptr && logp == nullptr) ||
+      (top_k > 0 && (top_logp == nullptr || top_idx == nullptr)))
+    return SWG_ERR_NULLPTR;
+  const int64_t is = itype == SWG_I64 ? 8 : 4;
+  if (!aligned_to(targets, is) || !aligned_to(logp, 4) || !aligned_to(entropy, 4) || !aligned_to(stats, 4) ||
+      !aligned_to(top_logp, 4) || !aligned_to(top_idx, 8))
+    return SWG_ERR_UNSUPPORTED;
+  const Range outs[] = {rng(logp, targets ? T * 4 : 0), rng(entropy, T * 4), rng(stats, T * 8),
+                        rng(top_logp, T * top_k * 4), rng(top_idx, T * top_k * 8)};
+  const Range ins[] = {rows_rng(logits, T, V, ld, dtype_bytes(dtype)), rng(targets, targets ? T * is : 0)};
+  if (any_overlap(outs, 5, ins, 2)) return SWG_ERR_PARAM_INVALID;
+  const swg_status dv = check_device();
+  if (dv != SWG_OK) return dv;
+  const swg::TlpFwdArgs a{logits, targets, logp, entropy, stats, top_logp, top_idx, T, V, T > 1 ? ld : 0,
+                          ignore_index, top_k, itype == SWG_I64, 1.0f / temperature};
+  return cuda_status(
+      swg::launch_token_logprobs_fwd(a, static_cast<int>(dtype), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+swg_status token_logprobs_bwd(const float* dlogp, const void* logits, const void* targets, const float* stats,
+                              const float* dentropy, const float* entropy, void* dlogits, int64_t T, int64_t V,
+                              int64_t ld, int64_t ldo, float temperature, int64_t ignore_index, swg_dtype dtype,
+                              swg_itype itype, swg_stream_t stream) {
+  const swg_status st = check_vocab(logits, T, V, ld, temperature, dtype, itype);
+  if (st != SWG_OK) return st;
+  if (T == 0) return SWG_OK;
+  if (logits == nullptr || stats == nullptr || dlogits == nullptr || (targets != nullptr && dlogp == nullptr) ||
+      (dentropy != nullptr && entropy == nullptr))
+    return SWG_ERR_NULLPTR;
+  const int64_t is = itype == SWG_I64 ? 8 : 4;
+  if (!aligned_to(targets, is) || !aligned_to(dlogp, 4) || !aligned_to(entropy, 4) || !aligned_to(stats, 4) ||
+      !aligned_to(dentropy, 4))
+    return SWG_ERR_UNSUPPORTED;
+  const Range ins[] = {rng(targets, targets ? T * is : 0), rng(dlogp, dlogp ? T * 4 : 0), rng(stats, T * 8),
+                       rng(entropy, dentropy ? T * 4 : 0), rng(dentropy, dentropy ? T * 4 : 0)};
+  const swg_status al = check_dlogits(dlogits, ldo, logits, ld, T, V, dtype, ins, 5);
+  if (al != SWG_OK) return al;
+  const swg_status dv = check_device();
+  if (dv != SWG_OK) return dv;
+  const swg::TlpBwdArgs a{logits, targets, stats, dlogp, entropy, dentropy, dlogits, T, V, T > 1 ? ld : 0,
+                          T > 1 ? ldo : 0, ignore_index, itype == SWG_I64, 1.0f / temperature};
+  return cuda_status(
+      swg::launch_token_logprobs_bwd(a, static_cast<int>(dtype), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// the three distillation entry points: forward when loss is wanted, backward when dlogits is
+swg_status distill(const void* logits, const void* ids, const void* teacher, const float* weight,
+                   const float* stats_in, float* loss, float* stats, void* dlogits, int64_t T, int64_t V, int64_t ld,
+                   int64_t ldo, int64_t K, float temperature, swg_dtype dtype, swg_dtype tdtype, swg_itype itype,
+                   swg_stream_t stream, bool forward, bool backward) {
+  const swg_status st = check_vocab(logits, T, V, ld, temperature, dtype, itype);
+  if (st != SWG_OK) return st;
+  if (K < 1 || !known_dtype(tdtype)) return SWG_ERR_PARAM_INVALID;
+  if (K > swg::kKdMaxEntries) return SWG_ERR_UNSUPPORTED;
+  if (T == 0) return SWG_OK;
+  if (logits == nullptr || ids == nullptr || teacher == nullptr || (forward && (loss == nullptr || stats == nullptr)) ||
+      (backward && (weight == nullptr || dlogits == nullptr)) || (!forward && stats_in == nullptr))
+    return SWG_ERR_NULLPTR;
+  const int64_t is = itype == SWG_I64 ? 8 : 4, es = dtype_bytes(dtype), ts = dtype_bytes(tdtype);
+  if (!aligned_to(ids, is) || !aligned_to(teacher, ts) || !aligned_to(weight, 4) || !aligned_to(stats_in, 4) ||
+      !aligned_to(loss, 4) || !aligned_to(stats, 4))
+    return SWG_ERR_UNSUPPORTED;
+  const Range ins[] = {rng(ids, T * K * is), rng(teacher, T * K * ts), rng(weight, backward ? T * 4 : 0),
+                       rng(stats_in, forward ? 0 : T * 8), rng(loss, forward ? T * 4 : 0),
+                       rng(stats, forward ? T * 8 : 0)};
+  if (backward) {
+    const swg_status al = check_dlogits(dlogits, ldo, logits, ld, T, V, dtype, ins, 6);
+    if (al != SWG_OK) return al;
+  }
+  const Range in4[] = {ins[0], ins[1], ins[2], rows_rng(logits, T, V, ld, es)};
+  if (forward && any_overlap(ins + 4, 2, in4, 4)) return SWG_ERR_PARAM_INVALID;
+  const swg_status dv = check_device();
+  if (dv != SWG_OK) return dv;
+  const swg::KdArgs a{logits, ids, teacher, weight, stats_in, loss, stats, dlogits, T, V, T > 1 ? ld : 0,
+                      T > 1 ? ldo : 0, static_cast<int>(K), static_cast<int>(tdtype), itype == SWG_I64,
+                      1.0f / temperature};
+  return cuda_status(swg::launch_distill(a, forward, backward, static_cast<int>(dtype),
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+swg_status distill_fwd(const void* logits, const void* ids, const void* teacher, float* loss, float* stats, int64_t T,
+                       int64_t V, int64_t ld, int64_t K, float temperature, swg_dtype dtype, swg_dtype tdtype,
+                       swg_itype itype, swg_stream_t stream) {
+  return distill(logits, ids, teacher, nullptr, nullptr, loss, stats, nullptr, T, V, ld, 0, K, temperature, dtype,
+                 tdtype, itype, stream, true, false);
+}
+
+swg_status distill_bwd(const float* weight, const void* logits, const void* ids, const void* teacher,
+                       const float* stats, void* dlogits, int64_t T, int64_t V, int64_t ld, int64_t ldo, int64_t K,
+                       float temperature, swg_dtype dtype, swg_dtype tdtype, swg_itype itype, swg_stream_t stream) {
+  return distill(logits, ids, teacher, weight, stats, nullptr, nullptr, dlogits, T, V, ld, ldo, K, temperature, dtype,
+                 tdtype, itype, stream, false, true);
+}
+
+swg_status distill_fwd_bwd(const void* logits, const void* ids, const void* teacher, const float* weight, float* loss,
+                           float* stats, void* dlogits, int64_t T, int64_t V, int64_t ld, int64_t ldo, int64_t K,
+                           float temperature, swg_dtype dtype, swg_dtype tdtype, swg_itype itype,
+                           swg_stream_t stream) {
+  return distill(logits, ids, teacher, weight, nullptr, loss, stats, dlogits, T, V, ld, ldo, K, temperature, dtype,
+                 tdtype, itype, stream, true, true);
+}
+
 }  // extern "C"

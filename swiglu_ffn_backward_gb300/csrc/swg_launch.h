@@ -71,6 +71,84 @@ cudaError_t launch_group_norm_bwd(const void* dy, const void* x, const void* gam
                                   void* dbeta, int64_t N, int64_t C, int64_t HxW, int64_t G, float eps, int dtype,
                                   void* ws, cudaStream_t stream);
 
+// ---- layer norm (layer_norm.cu); dtype, wdtype 0 = f32, 1 = f16, 2 = bf16
+struct LnFwdArgs {
+  const void* x;         // [M, N], rows ldx apart
+  const void* residual;  // [M, N], rows ldr apart, or null
+  const void* gamma;     // [N] of wdtype, or null (1)
+  const void* beta;      // [N] of wdtype, or null (0)
+  void* h;               // [M, N] = x + residual (null without a residual)
+  void* y;               // [M, N]
+  float* stats;          // [M, 2]: mean, rstd
+  int64_t M, N, ldx, ldr;
+  float eps;
+  int wdtype;
+};
+struct LnBwdArgs {
+  const void* dy;       // [M, N], rows lddy apart
+  const void* x;        // [M, N], rows ldx apart (the normalised tensor: h when there was a residual)
+  const float* stats;   // [M, 2]: mean, rstd
+  const void* gamma;    // [N] of wdtype, or null (1)
+  const void* dh;       // [M, N], rows lddh apart, or null: added to dx
+  void* dx;             // [M, N]
+  void* dgamma;         // [N] of wdtype, or null
+  void* dbeta;          // [N] of wdtype, or null
+  float* part;          // workspace (when dgamma or dbeta is wanted)
+  int64_t M, N, lddy, ldx, lddh;
+  int wdtype;
+};
+size_t ln_workspace_bytes(int64_t M, int64_t N);
+cudaError_t launch_layer_norm_fwd(const LnFwdArgs& a, int dtype, cudaStream_t stream);
+cudaError_t launch_layer_norm_bwd(const LnBwdArgs& a, int dtype, cudaStream_t stream);
+
+// ---- log probabilities of given tokens (token_logprobs.cu); wide: 64-bit targets
+constexpr int kMaxTop = 32;  // alternatives, at most
+struct TlpFwdArgs {
+  const void* logits;   // [T, V], rows ld apart
+  const void* targets;  // [T], or null
+  float* logp;          // [T] (null without targets)
+  float* entropy;       // [T]
+  float* stats;         // [T, 2]: max, sum exp((z - max) / tau)
+  float* top_logp;      // [T, top]
+  int64_t* top_idx;     // [T, top]
+  int64_t T, V, ld, ignore;
+  int top;
+  bool wide;
+  float inv_temp;
+};
+struct TlpBwdArgs {
+  const void* logits;     // [T, V], rows ld apart
+  const void* targets;    // [T], or null
+  const float* stats;     // [T, 2]
+  const float* dlogp;     // [T] (null without targets)
+  const float* entropy;   // [T] (with dentropy)
+  const float* dentropy;  // [T], or null
+  void* dlogits;          // [T, V], rows ldo apart; may be the logits themselves
+  int64_t T, V, ld, ldo, ignore;
+  bool wide;
+  float inv_temp;
+};
+cudaError_t launch_token_logprobs_fwd(const TlpFwdArgs& a, int dtype, cudaStream_t stream);
+cudaError_t launch_token_logprobs_bwd(const TlpBwdArgs& a, int dtype, cudaStream_t stream);
+
+// ---- distillation from a teacher's top logits (distill.cu); tdtype: the teacher's logits' type
+constexpr int kKdMaxEntries = 1024;
+struct KdArgs {
+  const void* logits;     // [T, V], rows ld apart
+  const void* ids;        // [T, K]
+  const void* teacher;    // [T, K] of tdtype
+  const float* weight;    // [T] (backward)
+  const float* stats_in;  // [T, 2] (backward alone)
+  float* loss;            // [T] (forward)
+  float* stats;           // [T, 2] (forward)
+  void* dlogits;          // [T, V], rows ldo apart (backward); may be the logits themselves
+  int64_t T, V, ld, ldo;
+  int K, tdtype;
+  bool wide;
+  float inv_temp;
+};
+cudaError_t launch_distill(const KdArgs& a, bool forward, bool backward, int dtype, cudaStream_t stream);
+
 // one-shot fault injection for tests of the timeout path (swg_inject_stall): the next
 // launch of `kernel` (1 = x GEMM, 2 = fused x) stops issuing operand copies at ring
 // entry `stall_at` and gives every pipeline wait `wait_limit` cycles. take_injection
