@@ -1,0 +1,268 @@
+// Rows of logits as the kernels of token_logprobs.cu and distill.cu take them.
+//
+// A row is cut into 16-byte vectors at 16-byte aligned addresses, whatever the address of its first
+// element: vector g holds the elements [g E - shift, g E - shift + E), shift being the number of
+// elements between the aligned address at or below the row's start and that start. Only a row's first
+// and last vector can be partial; they are read and written element by element, inside the row. A block
+// takes a run of a row's vectors, kVecs of them in each thread's registers at a time; the S blocks of
+// one row form a cluster and exchange their results through distributed shared memory.
+#pragma once
+
+#include "row_ops.cuh"
+
+namespace swg {
+namespace row {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kVecs = 8;                          // 16-byte vectors a thread holds: 32 registers
+constexpr int kChunk = kRowThreads * kVecs;       // vectors a block holds (32 KB)
+constexpr int kMaxCluster = 8;                    // portable cluster size
+
+template <typename T>
+struct Traits;
+template <>
+struct Traits<float> {
+  static constexpr int E = 4;
+  static constexpr uint32_t kNegInf = 0xff800000u;
+};
+template <>
+struct Traits<__half> {
+  static constexpr int E = 8;
+  static constexpr uint32_t kNegInf = 0xfc00fc00u;
+};
+template <>
+struct Traits<__nv_bfloat16> {
+  static constexpr int E = 8;
+  static constexpr uint32_t kNegInf = 0xff80ff80u;
+};
+
+struct Vec {
+  uint32_t w[4];
+};
+
+template <bool kReadOnly>
+__device__ __forceinline__ Vec ld_vec(const void* p) {
+  Vec v;
+  if (kReadOnly)
+    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+        : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3])
+        : "l"(p));
+  else
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3])
+                 : "l"(p)
+                 : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_vec(void* p, const Vec& v) {
+  asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.w[0]), "r"(v.w[1]),
+               "r"(v.w[2]), "r"(v.w[3])
+               : "memory");
+}
+
+// elements 2 i and 2 i + 1 of a vector
+template <typename T>
+__device__ __forceinline__ float2 vec_pair(const Vec& v, int i);
+template <>
+__device__ __forceinline__ float2 vec_pair<float>(const Vec& v, int i) {
+  return make_float2(__uint_as_float(v.w[2 * i]), __uint_as_float(v.w[2 * i + 1]));
+}
+template <>
+__device__ __forceinline__ float2 vec_pair<__half>(const Vec& v, int i) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v.w[i]));
+}
+template <>
+__device__ __forceinline__ float2 vec_pair<__nv_bfloat16>(const Vec& v, int i) {
+  return bf16x2_to_f2(v.w[i]);
+}
+template <typename T>
+__device__ __forceinline__ void set_pair(Vec& v, int i, float2 x);
+template <>
+__device__ __forceinline__ void set_pair<float>(Vec& v, int i, float2 x) {
+  v.w[2 * i] = __float_as_uint(x.x);
+  v.w[2 * i + 1] = __float_as_uint(x.y);
+}
+template <>
+__device__ __forceinline__ void set_pair<__half>(Vec& v, int i, float2 x) {
+  const __half2 h = __floats2half2_rn(x.x, x.y);
+  v.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ void set_pair<__nv_bfloat16>(Vec& v, int i, float2 x) {
+  v.w[i] = pack_bf16x2(x.x, x.y);
+}
+// the largest element, NaNs passed over
+template <typename T>
+__device__ __forceinline__ float vec_max(const Vec& v);
+template <>
+__device__ __forceinline__ float vec_max<float>(const Vec& v) {
+  return fmaxf(fmaxf(__uint_as_float(v.w[0]), __uint_as_float(v.w[1])),
+               fmaxf(__uint_as_float(v.w[2]), __uint_as_float(v.w[3])));
+}
+template <>
+__device__ __forceinline__ float vec_max<__half>(const Vec& v) {
+  const __half2* h = reinterpret_cast<const __half2*>(v.w);
+  const float2 m = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+  return fmaxf(m.x, m.y);
+}
+template <>
+__device__ __forceinline__ float vec_max<__nv_bfloat16>(const Vec& v) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(v.w);
+  const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
+template <typename T>
+__device__ __forceinline__ int row_shift(const T* row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+}
+
+// the vector whose first element is element e0 of the row; -inf outside the row
+template <typename T, bool kReadOnly>
+__device__ __forceinline__ Vec load_row_vec(const T* row, int64_t e0, int64_t V) {
+  constexpr int E = Traits<T>::E;
+  if (e0 >= 0 && e0 + E <= V) return ld_vec<kReadOnly>(row + e0);
+  Vec v;
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const int64_t e = e0 + 2 * i;
+    set_pair<T>(v, i, make_float2(e >= 0 && e < V ? to_f(row[e]) : neg_inf(),
+                                  e + 1 >= 0 && e + 1 < V ? to_f(row[e + 1]) : neg_inf()));
+  }
+  return v;
+}
+// the same vector of a row of outputs; `aligned`: out + e0 is 16-byte aligned
+template <typename T>
+__device__ __forceinline__ void store_row_vec(T* out, int64_t e0, int64_t V, bool aligned, const Vec& v) {
+  constexpr int E = Traits<T>::E;
+  if (aligned && e0 >= 0 && e0 + E <= V) {
+    st_vec(out + e0, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const int64_t e = e0 + 2 * i;
+    const float2 x = vec_pair<T>(v, i);
+    if (e >= 0 && e < V) out[e] = from_f<T>(x.x);
+    if (e + 1 >= 0 && e + 1 < V) out[e + 1] = from_f<T>(x.y);
+  }
+}
+
+// a block's share of a row
+struct Share {
+  int64_t begin, end;  // its vectors
+  int shift;
+};
+template <typename T>
+__device__ __forceinline__ Share share_of(const T* row, int64_t V, int S, int rank) {
+  Share s;
+  s.shift = row_shift(row);
+  const int64_t n = (s.shift + V + Traits<T>::E - 1) / Traits<T>::E;
+  const int64_t per = (n + S - 1) / S;
+  s.begin = min(n, rank * per);
+  s.end = min(n, s.begin + per);
+  return s;
+}
+// vectors c + i kRowThreads + threadIdx.x of the share -> v[i]; -inf past its end
+template <typename T, bool kReadOnly>
+__device__ __forceinline__ void load_chunk(Vec (&v)[kVecs], const T* row, int64_t V, const Share& s, int64_t c) {
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int64_t g = c + i * kRowThreads + threadIdx.x;
+    if (g < s.end) {
+      v[i] = load_row_vec<T, kReadOnly>(row, g * Traits<T>::E - s.shift, V);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i].w[j] = Traits<T>::kNegInf;
+    }
+  }
+}
+
+__device__ __forceinline__ float finite_or_0(float m) { return m == neg_inf() ? 0.0f : m; }
+// x = (z - max) log2(e) / tau, not below kLeast, where 2^x is 0 already: a -inf would give 0 * inf in
+// sums of 2^x x. A NaN stays one.
+constexpr float kLeast = -200.0f;
+__device__ __forceinline__ float at_least(float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(kLeast));
+  return r;
+}
+
+// ---- clusters: a block of the cluster writes to, and only to, blocks that have started (the barrier's
+// first phase) and that wait for the second one before they read
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_peer_f4(const float4* p, uint32_t rank, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(peer_addr(p, rank)), "f"(v.x), "f"(v.y),
+               "f"(v.z), "f"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void st_peer_u64(const uint64_t* p, uint32_t rank, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer_addr(p, rank)), "l"(v) : "memory");
+}
+
+// A part of a row under the row's maximum: the shift x = (part_max - joint_max) c of its exponents (c =
+// log2(e) / tau), by which its sum of 2^x is scaled. A part with no logit above -inf has a sum of 0.
+__device__ __forceinline__ float part_shift(float part_max, float joint_max, float c) {
+  return part_max == neg_inf() ? 0.0f : at_least((part_max - finite_or_0(joint_max)) * c);
+}
+
+}  // namespace row
+
+// 16-byte vectors of a row of V elements: one more where rows may start inside a vector
+inline int64_t row_vectors(const void* rows, int64_t V, int64_t ld, int elem_bytes) {
+  const bool whole = reinterpret_cast<uintptr_t>(rows) % 16 == 0 && (ld * elem_bytes) % 16 == 0;
+  return (V * elem_bytes + 15) / 16 + (whole ? 0 : 1);
+}
+// Blocks a row is given: enough to hold it in registers (up to the portable cluster size), more when
+// there are so few rows that SMs would stay idle, but no shares below kMinShare vectors.
+constexpr int64_t kMinShare = 256;
+inline int row_blocks(int64_t T, int64_t vectors, int num_sms) {
+  const int64_t useful = (vectors + kMinShare - 1) / kMinShare, spread = num_sms / T;
+  int64_t s = (vectors + row::kChunk - 1) / row::kChunk;
+  if (s < spread && s < useful) s = spread < useful ? spread : useful;
+  return static_cast<int>(s > row::kMaxCluster ? row::kMaxCluster : s);
+}
+
+// launches of at most kMaxLaunchRows rows: their blocks stay below 2^31
+constexpr int64_t kMaxLaunchRows = int64_t(1) << 27;
+
+template <typename Kernel, typename... Args>
+cudaError_t launch_rows(Kernel kernel, int64_t rows, int S, bool cluster, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * S));
+  cfg.blockDim = dim3(row::kRowThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+// all T rows of `a`, S blocks a row
+template <typename Args, typename K32, typename K16, typename KB>
+cudaError_t launch_all_rows(const Args& a, int dtype, int S, bool cluster, cudaStream_t stream, K32 k32, K16 k16,
+                            KB kb) {
+  for (int64_t row0 = 0; row0 < a.T; row0 += kMaxLaunchRows) {
+    const int64_t rows = a.T - row0 < kMaxLaunchRows ? a.T - row0 : kMaxLaunchRows;
+    const cudaError_t e = dtype == 0   ? launch_rows(k32, rows, S, cluster, stream, a, row0, S)
+                          : dtype == 1 ? launch_rows(k16, rows, S, cluster, stream, a, row0, S)
+                                       : launch_rows(kb, rows, S, cluster, stream, a, row0, S);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace swg
