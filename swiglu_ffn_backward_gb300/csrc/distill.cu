@@ -6,70 +6,104 @@
 // with q_j the sum of the entries with i_k = j and Q = 1, or 0 for a row without entries (loss 0, no
 // gradient). A weight w of 0 gives a zero gradient whatever the row holds.
 //
-// Bound by HBM: V elements a row are read, and written where there is a gradient. For loss and gradient
-// at once a cluster of S blocks holds the row in registers (32 KB a block): each block's (max, sum) go to
-// every block of the cluster through distributed shared memory, and the gradient is formed from the
-// registers, so the logits are read once (a row longer than the cluster's registers is read again). One
-// warp takes the teacher's entries while the row is on its way. The gradient's sparse part, at most K
-// elements a row, is written over the dense part by the block that wrote it.
+// Bound by HBM: V elements a row are read, and written where there is a gradient.
+// Loss, and loss with gradient: a persistent kernel streams rows through shared memory (vocab_stream.cuh).
+// With a gradient a row's shares stay in the rings of a cluster of S blocks until it is written, so the
+// logits are read once. The warps' (max, sum) go to every block of the cluster, which each warp joins for
+// itself; the gradient of a row is formed after the sums of the next one, so the exchange is off the
+// path. The gradient's sparse part, at most K elements a row, is written by the warp that wrote the
+// dense part there. One warp takes the teacher's entries a row ahead.
+// The gradient alone needs no exchange: blocks take 32 KB shares of rows in registers.
+#include <mutex>
+
 #include "swg_launch.h"
-#include "vocab_rows.cuh"
+#include "vocab_stream.cuh"
 
 namespace swg {
 namespace {
 
 using namespace row;
 
+constexpr int kPer = kKdMaxEntries / kRowThreads;  // entries a thread may take
+
 struct KdSmem {
-  float lanes[kRowWarps];
-  float sums[kRowWarps];
-  float2 part[kMaxCluster];  // the blocks' max and sum
-  float sq;                  // sum exp((t - max t) / tau), 0 for a row without entries
+  float tmax[kRowWarps];
+  float tsum[kRowWarps];
   int id[kKdMaxEntries];     // -1: absent
-  float q[kKdMaxEntries];    // probabilities
-  float td[kKdMaxEntries];   // teacher logits less their maximum
-  float z[kKdMaxEntries];    // the student's logits at the entries (those that the block needs)
+  float q[kKdMaxEntries];    // exp((t - max t) / tau): probabilities, but for the factor 1 / sq
 };
 
-// One warp: the row's teacher entries -> shared memory. The student's logits are gathered for the ids in
-// [e0, e1): a gradient in their place may overwrite them later.
-template <typename T>
-__device__ __forceinline__ void load_teacher(const KdArgs& a, int64_t r, const T* z, int64_t e0, int64_t e1,
-                                             KdSmem& sm) {
-  const int lane = threadIdx.x & 31;
+// The teacher's entries k = threadIdx.x + n kRowThreads of a thread. The loads are issued before the row's
+// own, and the student's logits at the entries (for the ids in [e0, e1)) as soon as the ids are there.
+struct Entries {
+  int id[kPer];    // -1: absent
+  float t[kPer];   // the teacher's logit, then its difference to their maximum
+  float z[kPer];   // the student's logit
+  float e[kPer];   // exp((t - max t) / tau)
+};
+__device__ __forceinline__ float load_entries(const KdArgs& a, int64_t r, Entries& n, KdSmem& sm) {
   float m = neg_inf();
-  for (int k = lane; k < a.K; k += 32) {
-    const int64_t id = load_index(a.ids, r * a.K + k, a.wide);
-    const bool there = id >= 0 && id < a.V;
-    const float t = there ? load_any(a.teacher, r * a.K + k, a.tdtype) : neg_inf();
-    sm.id[k] = there ? static_cast<int>(id) : -1;
-    sm.td[k] = t;
-    sm.z[k] = id >= e0 && id < e1 ? to_f(z[id]) : 0.0f;
-    m = fmaxf(m, t);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int k = threadIdx.x + i * kRowThreads;
+    n.id[i] = -1;
+    n.t[i] = neg_inf();
+    if (k < a.K) {
+      const int64_t id = load_index(a.ids, r * a.K + k, a.wide);
+      const float t = load_any(a.teacher, r * a.K + k, a.tdtype);
+      if (id >= 0 && id < a.V) {
+        n.id[i] = static_cast<int>(id);
+        n.t[i] = t;
+      }
+      sm.id[k] = n.id[i];
+    }
+    m = fmaxf(m, n.t[i]);
   }
-  const float me = finite_or_0(warp_max(m));
+  return m;
+}
+template <typename T>
+__device__ __forceinline__ void gather_logits(Entries& n, const T* z, int64_t e0, int64_t e1) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) n.z[i] = n.id[i] >= e0 && n.id[i] < e1 && n.id[i] >= 0 ? to_f(z[n.id[i]]) : 0.0f;
+}
+// from the entries' maximum: differences and exponentials, and the thread's sum of them
+__device__ __forceinline__ float exp_entries(const KdArgs& a, float m, Entries& n, KdSmem& sm) {
+  const float me = finite_or_0(m);
   float s = 0.f;
-  for (int k = lane; k < a.K; k += 32) {
-    const float d = sm.td[k] - me;
-    const float e = ex2_approx(d * a.inv_temp * kLog2e);
-    sm.td[k] = d;
-    sm.q[k] = e;
-    s += e;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int k = threadIdx.x + i * kRowThreads;
+    n.t[i] -= me;
+    n.e[i] = ex2_approx(n.t[i] * a.inv_temp * kLog2e);
+    if (k < a.K) {
+      sm.q[k] = n.e[i];
+      s += n.e[i];
+    }
   }
-  s = warp_sum(s);
-  const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-  for (int k = lane; k < a.K; k += 32) sm.q[k] *= inv;
-  if (lane == 0) sm.sq = s;
+  return s;
+}
+__device__ __forceinline__ float warps_max(const float* v) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < kRowWarps; ++i) m = fmaxf(m, v[i]);
+  return m;
+}
+__device__ __forceinline__ float warps_sum(const float* v) {
+  float s = v[0];
+#pragma unroll
+  for (int i = 1; i < kRowWarps; ++i) s += v[i];
+  return s;
 }
 
 struct Gradient {
   float me, c2;  // 2^((z - me) c2) is the unscaled probability
   float dense;   // w Q / (tau s)
-  float sparse;  // w / tau
+  float sparse;  // w / (tau sq)
 };
 __device__ __forceinline__ Gradient make_gradient(const KdArgs& a, float m, float s, float w, float sq) {
   const float wt = w * a.inv_temp;
-  return Gradient{finite_or_0(m), a.inv_temp * kLog2e, s == 0.0f || sq == 0.0f ? 0.0f : wt / s, wt};
+  return Gradient{finite_or_0(m), a.inv_temp * kLog2e, s == 0.0f || sq == 0.0f ? 0.0f : wt / s,
+                  sq == 0.0f ? 0.0f : wt / sq};
 }
 
 // the dense part of the chunk at c
@@ -99,128 +133,301 @@ __device__ __forceinline__ void store_zeros(T* out, int64_t V, bool aligned, con
 }
 // the elements at the entries in [e0, e1); an id that comes twice is written by its first entry
 template <typename T>
-__device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g, const KdSmem& sm, T* out, int64_t e0,
-                                             int64_t e1) {
-  for (int k = threadIdx.x; k < a.K; k += kRowThreads) {
-    const int id = sm.id[k];
+__device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g, const Entries& n, const KdSmem& sm,
+                                             T* out, int64_t e0, int64_t e1) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int k = threadIdx.x + i * kRowThreads, id = n.id[i];
     if (id < 0 || id < e0 || id >= e1) continue;
     float q = 0.f;
     bool first = true;
-    for (int n = 0; n < a.K; ++n) {
-      if (sm.id[n] != id) continue;
-      first = first && n >= k;
-      q += sm.q[n];
+    for (int j = 0; j < a.K; ++j) {
+      if (sm.id[j] != id) continue;
+      first = first && j >= k;
+      q += sm.q[j];
     }
-    if (first)
-      out[id] = from_f<T>(fmaf(g.dense, ex2_approx((sm.z[k] - g.me) * g.c2), -g.sparse * q));
+    if (first) out[id] = from_f<T>(fmaf(g.dense, ex2_approx((n.z[i] - g.me) * g.c2), -g.sparse * q));
   }
 }
 
-// loss and statistics; with kGrad the gradient as well
-template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kRowThreads) kd_fwd_kernel(const KdArgs a, int64_t row0, int S) {
-  constexpr int E = Traits<T>::E;
-  __shared__ KdSmem sm;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  if (S > 1) cluster_arrive();
-  const int64_t r = row0 + blockIdx.x / S;
-  const T* z = static_cast<const T*>(a.logits) + r * a.ld;
-  const Share sh = share_of(z, a.V, S, rank);
-  const int64_t e0 = sh.begin * E - sh.shift, e1 = sh.end * E - sh.shift;  // the elements of the share
-  const float c2 = a.inv_temp * kLog2e;
+// ---- loss, and loss with gradient
 
-  float m = neg_inf(), s = 0.f;  // of the block, the same in every thread
-  Vec v[kVecs];
-  for (int64_t c = sh.begin; c < sh.end || c == sh.begin; c += kChunk) {
-    load_chunk<T, !kGrad>(v, z, a.V, sh, c);
-    // the first block forms the loss: it needs the logits at all entries
-    if (c == sh.begin && warp == kRowWarps - 1) load_teacher(a, r, z, rank == 0 ? 0 : e0, rank == 0 ? a.V : e1, sm);
-    float tm = neg_inf();
+constexpr int kExtraWarps = 2;  // producer, teacher
+constexpr int kFwdThreads = kStreamThreads + 32 * kExtraWarps;
+constexpr int kSlots = 4;       // exchange slots: a slot is written again four rows later
+constexpr int kShareStages = 2; // stages a row's share may hold: two rows' shares, and two stages ahead
+
+struct KdStream {
+  Ring ring;
+  uint64_t joined[kSlots];  // the row's maxima and sums have come from all blocks
+  uint64_t ready[2];        // the row's entries are in shared memory
+  uint64_t spare[2];        // the computing warps are done with them
+  float2 part[kSlots][kMaxCluster][kStreamWarps];  // max and sum of every warp
+  float2 note[kSlots];      // from the first block: its entries' logits have been read
+  float weight[2];
+  float sq[2];              // sum exp((t - max t) / tau), 0 for a row without entries
+};
+// the entries of two rows follow the ring in dynamic shared memory
+struct EntryArrays {
+  int id[kKdMaxEntries];    // -1: absent
+  float td[kKdMaxEntries];  // teacher logits less their maximum; exp(td / tau) / sq are the probabilities
+  float z[kKdMaxEntries];   // the student's logits (first block)
+};
+constexpr size_t kFwdSmem = kRingBytes + 2 * sizeof(EntryArrays);
+
+// one warp: row r's entries; with `gather` the student's logits at them
+template <typename T>
+__device__ __forceinline__ void take_entries(const KdArgs& a, int64_t r, EntryArrays& n, bool gather, float& sq) {
+  const int lane = threadIdx.x & 31;
+  const float c2 = a.inv_temp * kLog2e;
+  const T* z = static_cast<const T*>(a.logits) + r * a.ld;
+  float m = neg_inf();
+  for (int k0 = 0; k0 < a.K; k0 += 128) {  // four loads of a kind in flight
+    int64_t id[4];
+    float t[4], x[4];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) tm = fmaxf(tm, vec_max<T>(v[i]));
-    tm = warp_max(tm);
-    if (lane == 0) sm.lanes[warp] = tm;
-    __syncthreads();
-    float mn = m;
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + i * 32 + lane;
+      id[i] = k < a.K ? load_index(a.ids, r * a.K + k, a.wide) : -1;
+      t[i] = k < a.K ? load_any(a.teacher, r * a.K + k, a.tdtype) : neg_inf();
+    }
 #pragma unroll
-    for (int i = 0; i < kRowWarps; ++i) mn = fmaxf(mn, sm.lanes[i]);
-    const float me = finite_or_0(mn);
-    const float2 nm2 = make_float2(-me, -me), cc2 = make_float2(c2, c2);
-    float2 s2 = make_float2(0.f, 0.f);
+    for (int i = 0; i < 4; ++i) {
+      const bool there = id[i] >= 0 && id[i] < a.V;
+      if (!there) id[i] = -1, t[i] = neg_inf();
+      x[i] = gather && there ? to_f(z[id[i]]) : 0.0f;
+      m = fmaxf(m, t[i]);
+    }
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-#pragma unroll
-      for (int p = 0; p < E / 2; ++p) {
-        const float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
-        s2 = __fadd2_rn(s2, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + i * 32 + lane;
+      if (k < a.K) {
+        n.id[k] = static_cast<int>(id[i]);
+        n.td[k] = t[i];
+        n.z[k] = x[i];
       }
     }
-    const float ws = warp_sum(s2.x + s2.y);
-    if (lane == 0) sm.sums[warp] = ws;
-    __syncthreads();
-    s *= ex2_approx(part_shift(m, mn, c2));
-    float cs = 0.f;
-#pragma unroll
-    for (int i = 0; i < kRowWarps; ++i) cs += sm.sums[i];
-    s += cs;
-    m = mn;
   }
-  if (S > 1) {
-    cluster_wait();  // every block has started
-    if (tid < S) {
-      const uint32_t to = peer_addr(&sm.part[rank], static_cast<uint32_t>(tid));
-      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(m), "f"(s) : "memory");
-    }
-    cluster_arrive();
-    cluster_wait();
-    m = neg_inf();
-    for (int i = 0; i < S; ++i) m = fmaxf(m, sm.part[i].x);
-    s = 0.f;
-    for (int i = 0; i < S; ++i) s = fmaf(ex2_approx(part_shift(sm.part[i].x, m, c2)), sm.part[i].y, s);
+  const float me = finite_or_0(warp_max(m));
+  float s = 0.f;
+  for (int k = lane; k < a.K; k += 32) {
+    const float d = n.td[k] - me;
+    n.td[k] = d;
+    s += ex2_approx(d * c2);
   }
-  const float sq = sm.sq;
-  if (rank == 0 && warp == kRowWarps - 1) {
-    // sum q (ln q - ln p) = sum (q / tau) (td - (z - max z)) - ln sq + ln s: a mask of the type's lowest
-    // value leaves the range of fp32 only where the loss does
-    const float me = finite_or_0(m);
-    float l = 0.f;
-    for (int k = lane; k < a.K; k += 32) {
-      const float q = sm.q[k];
-      if (q == 0.0f || sm.id[k] < 0) continue;
-      l = fmaf(q * a.inv_temp, sm.td[k] - (sm.z[k] - me), l);
-    }
-    l = warp_sum(l);
-    if (lane == 0) {
-      a.stats[2 * r] = m;
-      a.stats[2 * r + 1] = s;
-      a.loss[r] = sq == 0.0f ? 0.0f : l + ((s == 0.0f ? 0.0f : logf(s)) - logf(sq));
-    }
-  }
-  if (kGrad) {
-    T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
-    const bool aligned = row_shift(out) == sh.shift;
-    const float w = a.weight[r];
-    if (w == 0.0f) {
-      store_zeros(out, a.V, aligned, sh);
-      return;
-    }
-    const Gradient g = make_gradient(a, m, s, w, sq);
-    const bool held = sh.end - sh.begin <= kChunk;  // the registers hold the whole share
-    for (int64_t c = sh.begin; c < sh.end; c += kChunk) {
-      if (!held) load_chunk<T, false>(v, z, a.V, sh, c);
-      store_dense(v, g, out, a.V, aligned, sh, c);
-    }
-    __syncthreads();  // the sparse part goes over the dense one
-    store_sparse(a, g, sm, out, e0, e1);
-  }
+  sq = warp_sum(s);
 }
+
+template <typename T, bool kGrad>
+__global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, int S, uint32_t* status) {
+  constexpr int E = Traits<T>::E;
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ KdStream sm;
+  EntryArrays* entries = reinterpret_cast<EntryArrays*>(dyn + kRingBytes);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int64_t first = blockIdx.x / S, step = gridDim.x / S;
+  const uint32_t bytes = static_cast<uint32_t>(S * kStreamWarps * sizeof(float2) + sizeof(float2));
+  if (tid == 0) {
+    ring_init(sm.ring);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&sm.joined[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.ready[i], 1);
+      mbar_init(&sm.spare[i], kStreamWarps);
+    }
+    fence_mbar_init();
+    for (int i = 0; i < kSlots; ++i) mbar_arrive_expect_tx(&sm.joined[i], bytes);
+  }
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  Patience wait;
+
+  if (warp == kStreamWarps) {
+    produce_rows<T>(a.logits, a.ld, a.V, first, a.T, step, S, rank, dyn, sm.ring, wait);
+  } else if (warp == kStreamWarps + 1) {
+    int64_t it = 0;
+    for (int64_t r = first; r < a.T; r += step, ++it) {
+      const int b = static_cast<int>(it & 1), slot = static_cast<int>(it & (kSlots - 1));
+      wait(&sm.spare[b], static_cast<uint32_t>((it >> 1) & 1) ^ 1u);
+      float sq;
+      take_entries<T>(a, r, entries[b], rank == 0, sq);
+      if (lane == 0) {
+        sm.sq[b] = sq;
+        if (kGrad) sm.weight[b] = a.weight[r];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.ready[b]);
+      // a gradient over the logits may be written once the first block has read them here
+      if (rank == 0 && lane < S) send_f2(&sm.note[slot], &sm.joined[slot], static_cast<uint32_t>(lane), 0.f, 0.f);
+      __syncwarp();
+    }
+  } else {
+    const float c2 = a.inv_temp * kLog2e;
+    const float2 cc2 = make_float2(c2, c2);
+    Place in, held;  // the next stage to read, and (with a gradient) the first stage of the row before
+    // max and sum of the warp's part of row r, sent to every block
+    auto sums = [&](int64_t r, int slot) {
+      const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, S, rank);
+      float m = neg_inf();
+      float2 s2 = make_float2(0.f, 0.f);
+      for (int64_t c = sh.begin; c < sh.end; c += kStageVecs) {
+        Vec v[4];
+        wait(&sm.ring.full[in.stage], in.parity);
+        read_stage<T>(v, dyn + in.stage * kStageBytes, static_cast<int>(min(sh.end - c, int64_t(kStageVecs))));
+        const float mn = fmaxf(fmaxf(fmaxf(vec_max<T>(v[0]), vec_max<T>(v[1])), fmaxf(vec_max<T>(v[2]), vec_max<T>(v[3]))), m);
+        const float me = finite_or_0(mn);
+        if (mn > m) {
+          const float f = ex2_approx(part_shift(m, mn, c2));
+          s2 = __fmul2_rn(s2, make_float2(f, f));
+          m = mn;
+        }
+        const float2 nm2 = make_float2(-me, -me);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int p = 0; p < E / 2; ++p) {
+            const float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
+            s2 = __fadd2_rn(s2, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+          }
+        }
+        if (!kGrad) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.ring.empty[in.stage]);
+        }
+        in.next();
+      }
+      const float wm = warp_max(m);
+      const float ws = warp_sum((s2.x + s2.y) * ex2_approx(part_shift(m, wm, c2)));
+      if (lane < S) send_f2(&sm.part[slot][rank][warp], &sm.joined[slot], static_cast<uint32_t>(lane), wm, ws);
+      __syncwarp();
+    };
+    // the rest of row r, the it-th of the block
+    auto finish = [&](int64_t r, int64_t it) {
+      const int b = static_cast<int>(it & 1), slot = static_cast<int>(it & (kSlots - 1));
+      wait.cluster(&sm.joined[slot], static_cast<uint32_t>((it / kSlots) & 1));
+      if (tid == 0) mbar_arrive_expect_tx(&sm.joined[slot], bytes);
+      float m = neg_inf(), s = 0.f;
+      const float2* part = &sm.part[slot][0][0];
+      for (int i = lane; i < S * kStreamWarps; i += 32) m = fmaxf(m, part[i].x);
+      m = warp_max(m);
+      for (int i = lane; i < S * kStreamWarps; i += 32)
+        s = fmaf(ex2_approx(part_shift(part[i].x, m, c2)), part[i].y, s);
+      s = warp_sum(s);
+      wait(&sm.ready[b], static_cast<uint32_t>((it >> 1) & 1));
+      const EntryArrays& n = entries[b];
+      const float sq = sm.sq[b];
+      if (kGrad) {
+        const T* z = static_cast<const T*>(a.logits) + r * a.ld;
+        T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
+        const Share sh = share_of(z, a.V, S, rank);
+        const bool aligned = row_shift(out) == sh.shift;
+        const float w = sm.weight[b];
+        const Gradient g = make_gradient(a, m, s, w, sq);
+        const float2 nm2 = make_float2(-g.me, -g.me), k2 = make_float2(g.dense, g.dense);
+        const Place begin = held;
+        for (int64_t c = sh.begin; c < sh.end; c += kStageVecs) {
+          Vec v[4];
+          const int cnt = static_cast<int>(min(sh.end - c, int64_t(kStageVecs)));
+          read_stage<T>(v, dyn + held.stage * kStageBytes, cnt);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = i * kStreamThreads + tid;
+            if (at >= cnt) break;
+#pragma unroll
+            for (int p = 0; p < E / 2; ++p) {
+              const float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
+              const float2 y = __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), k2);
+              set_pair<T>(v[i], p, w == 0.0f ? make_float2(0.f, 0.f) : y);
+            }
+            store_row_vec(out, (c + at) * E - sh.shift, a.V, aligned, v[i]);
+          }
+          held.next();
+        }
+        // the elements at the entries, over the dense part that this warp has written
+        __syncwarp();
+        if (w != 0.0f) {
+          const int64_t vecs = sh.end - sh.begin;
+          for (int k = lane; k < a.K; k += 32) {
+            const int id = n.id[k];
+            if (id < 0) continue;
+            const int64_t at = (static_cast<int64_t>(id) + sh.shift) / E - sh.begin;  // of the share's vectors
+            if (at < 0 || at >= vecs || static_cast<int>(at % kStreamThreads) >> 5 != warp) continue;
+            float q = 0.f;
+            bool lowest = true;  // an id that comes twice is written by its first entry
+            for (int j = 0; j < a.K; ++j) {
+              if (n.id[j] != id) continue;
+              lowest = lowest && j >= k;
+              q += ex2_approx(n.td[j] * c2);
+            }
+            if (!lowest) continue;
+            int stage = begin.stage + static_cast<int>(at / kStageVecs);
+            if (stage >= kStages) stage -= kStages;
+            const T* p = reinterpret_cast<const T*>(dyn + stage * kStageBytes + (at % kStageVecs) * 16);
+            const float x = (to_f(p[(id + sh.shift) % E]) - g.me) * c2;
+            out[id] = from_f<T>(fmaf(g.dense, ex2_approx(x), -g.sparse * q));
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          Place p = begin;
+          for (int64_t c = sh.begin; c < sh.end; c += kStageVecs, p.next()) mbar_arrive(&sm.ring.empty[p.stage]);
+        }
+      }
+      if (rank == 0 && warp == 0) {
+        // sum q (ln q - ln p) = sum (q / tau) (td - (z - max z)) - ln sq + ln s: a mask of the type's
+        // lowest value leaves the range of fp32 only where the loss does
+        const float me = finite_or_0(m), f = a.inv_temp / sq;
+        float l = 0.f;
+        for (int k = lane; k < a.K; k += 32) {
+          const float e = ex2_approx(n.td[k] * c2);
+          if (n.id[k] >= 0 && e != 0.0f) l = fmaf(e * f, n.td[k] - (n.z[k] - me), l);
+        }
+        l = warp_sum(l);
+        if (lane == 0) {
+          a.stats[2 * r] = m;
+          a.stats[2 * r + 1] = s;
+          a.loss[r] = sq == 0.0f ? 0.0f : l + ((s == 0.0f ? 0.0f : logf(s)) - logf(sq));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.spare[b]);
+    };
+    int64_t it = 0;
+    for (int64_t r = first; r < a.T; r += step, ++it) {
+      sums(r, static_cast<int>(it & (kSlots - 1)));
+      if (it > 0) finish(r - step, it - 1);
+    }
+    if (it > 0) finish(first + (it - 1) * step, it - 1);
+  }
+  __syncwarp();
+  if (wait.lost && status != nullptr) atomicOr(status, kStatusTimeout);
+  cluster_arrive();  // no block leaves while another may still write to it
+  cluster_wait();
+}
+
+template <typename T, bool kGrad>
+cudaError_t launch_fwd(const KdArgs& a, int S, cudaStream_t stream) {
+  static std::mutex mu;  // guards the occupancy cache
+  static StreamCache cache;
+  std::lock_guard<std::mutex> lk(mu);
+  return launch_stream(kd_fwd_kernel<T, kGrad>, cache, kFwdThreads, kFwdSmem, a.T, S, stream, a, S, status_word_ptr());
+}
+template <bool kGrad>
+cudaError_t launch_fwd_any(const KdArgs& a, int dtype, int S, cudaStream_t stream) {
+  return dtype == 0   ? launch_fwd<float, kGrad>(a, S, stream)
+         : dtype == 1 ? launch_fwd<__half, kGrad>(a, S, stream)
+                      : launch_fwd<__nv_bfloat16, kGrad>(a, S, stream);
+}
+
+// ---- gradient alone
 
 // the gradient from saved statistics
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) kd_bwd_kernel(const KdArgs a, int64_t row0, int S) {
+__global__ void __launch_bounds__(kRowThreads, 3) kd_bwd_kernel(const KdArgs a, int64_t row0, int S) {
   constexpr int E = Traits<T>::E;
   __shared__ KdSmem sm;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t r = row0 + blockIdx.x / S;
   const T* z = static_cast<const T*>(a.logits) + r * a.ld;
   T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
@@ -232,31 +439,43 @@ __global__ void __launch_bounds__(kRowThreads) kd_bwd_kernel(const KdArgs a, int
     return;
   }
   const int64_t e0 = sh.begin * E - sh.shift, e1 = sh.end * E - sh.shift;
+  Entries n;
+  const float tmax = load_entries(a, r, n, sm);
   Vec v[kVecs];
   load_chunk<T, false>(v, z, a.V, sh, sh.begin);
-  if (threadIdx.x >= kRowThreads - 32) load_teacher(a, r, z, e0, e1, sm);
+  gather_logits(n, z, e0, e1);
+  const float wm = warp_max(tmax);
+  if (lane == 0) sm.tmax[warp] = wm;
   __syncthreads();
-  const Gradient g = make_gradient(a, a.stats_in[2 * r], a.stats_in[2 * r + 1], w, sm.sq);
+  const float ts = warp_sum(exp_entries(a, warps_max(sm.tmax), n, sm));
+  if (lane == 0) sm.tsum[warp] = ts;
+  __syncthreads();
+  const Gradient g = make_gradient(a, a.stats_in[2 * r], a.stats_in[2 * r + 1], w, warps_sum(sm.tsum));
   for (int64_t c = sh.begin; c < sh.end; c += kChunk) {
     if (c > sh.begin) load_chunk<T, false>(v, z, a.V, sh, c);
     store_dense(v, g, out, a.V, aligned, sh, c);
   }
   __syncthreads();  // the sparse part goes over the dense one
-  store_sparse(a, g, sm, out, e0, e1);
+  store_sparse(a, g, n, sm, out, e0, e1);
 }
 
 }  // namespace
 
 cudaError_t launch_distill(const KdArgs& a, bool forward, bool backward, int dtype, cudaStream_t stream) {
-  const int S = row_blocks(a.T, row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2), device_sm_count());
-  if (!forward)
-    return launch_all_rows(a, dtype, S, false, stream, kd_bwd_kernel<float>, kd_bwd_kernel<__half>,
-                           kd_bwd_kernel<__nv_bfloat16>);
-  if (!backward)
-    return launch_all_rows(a, dtype, S, S > 1, stream, kd_fwd_kernel<float, false>, kd_fwd_kernel<__half, false>,
-                           kd_fwd_kernel<__nv_bfloat16, false>);
-  return launch_all_rows(a, dtype, S, S > 1, stream, kd_fwd_kernel<float, true>, kd_fwd_kernel<__half, true>,
-                         kd_fwd_kernel<__nv_bfloat16, true>);
+  const int sms = device_sm_count();
+  const int64_t vectors = row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2);
+  // the row's shares have to stay in the rings for the gradient: a longer row is read twice
+  const bool once = forward && backward && vectors <= int64_t(kMaxCluster) * kShareStages * kStageVecs;
+  if (once) return launch_fwd_any<true>(a, dtype, stream_blocks(a.T, vectors, kShareStages, sms), stream);
+  if (forward) {
+    const int S = stream_blocks(a.T, vectors, vectors, sms);
+    const cudaError_t e = launch_fwd_any<false>(a, dtype, S, stream);
+    if (e != cudaSuccess || !backward) return e;
+  }
+  KdArgs b = a;
+  if (forward) b.stats_in = a.stats;
+  return launch_all_rows(b, dtype, row_blocks(a.T, vectors, sms), false, stream, kd_bwd_kernel<float>,
+                         kd_bwd_kernel<__half>, kd_bwd_kernel<__nv_bfloat16>);
 }
 
 }  // namespace swg
