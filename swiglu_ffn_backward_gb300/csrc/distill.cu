@@ -109,27 +109,27 @@ __device__ __forceinline__ Gradient make_gradient(const KdArgs& a, float m, floa
 // the dense part of the chunk at c
 template <typename T>
 __device__ __forceinline__ void store_dense(Vec (&v)[kVecs], const Gradient& g, T* out, int64_t V, bool aligned,
-                                            const Share& sh, int64_t c) {
+                                            const Share& sh, int c) {
   constexpr int E = Traits<T>::E;
   const float2 nm2 = make_float2(-g.me, -g.me), cc2 = make_float2(g.c2, g.c2), k2 = make_float2(g.dense, g.dense);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int64_t at = c + i * kRowThreads + threadIdx.x;
+    const int at = c + i * kRowThreads + static_cast<int>(threadIdx.x);
     if (at >= sh.end) break;
 #pragma unroll
     for (int p = 0; p < E / 2; ++p) {
       const float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
       set_pair<T>(v[i], p, __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), k2));
     }
-    store_row_vec(out, at * E - sh.shift, V, aligned, v[i]);
+    store_row_vec(out, first_element<T>(sh, at), V, aligned, v[i]);
   }
 }
 // a gradient of zeros
 template <typename T>
 __device__ __forceinline__ void store_zeros(T* out, int64_t V, bool aligned, const Share& sh) {
   const Vec zero = {{0u, 0u, 0u, 0u}};
-  for (int64_t at = sh.begin + threadIdx.x; at < sh.end; at += kRowThreads)
-    store_row_vec(out, at * Traits<T>::E - sh.shift, V, aligned, zero);
+  for (int at = sh.begin + static_cast<int>(threadIdx.x); at < sh.end; at += kRowThreads)
+    store_row_vec(out, first_element<T>(sh, at), V, aligned, zero);
 }
 // the elements at the entries in [e0, e1); an id that comes twice is written by its first entry
 template <typename T>
@@ -219,10 +219,11 @@ __device__ __forceinline__ void take_entries(const KdArgs& a, int64_t r, EntryAr
 }
 
 template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, int S, uint32_t* status) {
+__global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, Split split, uint32_t* status) {
   constexpr int E = Traits<T>::E;
   extern __shared__ __align__(128) unsigned char dyn[];
   __shared__ KdStream sm;
+  const int S = split.S;
   EntryArrays* entries = reinterpret_cast<EntryArrays*>(dyn + kRingBytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
   Patience wait;
 
   if (warp == kStreamWarps) {
-    produce_rows<T>(a.logits, a.ld, a.V, first, a.T, step, S, rank, dyn, sm.ring, wait);
+    produce_rows<T>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, sm.ring, wait);
   } else if (warp == kStreamWarps + 1) {
     int64_t it = 0;
     for (int64_t r = first; r < a.T; r += step, ++it) {
@@ -268,13 +269,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
     Place in, held;  // the next stage to read, and (with a gradient) the first stage of the row before
     // max and sum of the warp's part of row r, sent to every block
     auto sums = [&](int64_t r, int slot) {
-      const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, S, rank);
+      const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
       float m = neg_inf();
       float2 s2 = make_float2(0.f, 0.f);
-      for (int64_t c = sh.begin; c < sh.end; c += kStageVecs) {
+      for (int c = sh.begin; c < sh.end; c += kStageVecs) {
         Vec v[4];
         wait(&sm.ring.full[in.stage], in.parity);
-        read_stage<T>(v, dyn + in.stage * kStageBytes, static_cast<int>(min(sh.end - c, int64_t(kStageVecs))));
+        read_stage<T>(v, dyn + in.stage * kStageBytes, min(sh.end - c, kStageVecs));
         const float mn = fmaxf(fmaxf(fmaxf(vec_max<T>(v[0]), vec_max<T>(v[1])), fmaxf(vec_max<T>(v[2]), vec_max<T>(v[3]))), m);
         const float me = finite_or_0(mn);
         if (mn > m) {
@@ -320,58 +321,62 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       if (kGrad) {
         const T* z = static_cast<const T*>(a.logits) + r * a.ld;
         T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
-        const Share sh = share_of(z, a.V, S, rank);
+        const Share sh = share_of(z, a.V, split.per, rank);
         const bool aligned = row_shift(out) == sh.shift;
         const float w = sm.weight[b];
         const Gradient g = make_gradient(a, m, s, w, sq);
         const float2 nm2 = make_float2(-g.me, -g.me), k2 = make_float2(g.dense, g.dense);
         const Place begin = held;
-        for (int64_t c = sh.begin; c < sh.end; c += kStageVecs) {
+        for (int c = sh.begin; c < sh.end; c += kStageVecs) {
           Vec v[4];
-          const int cnt = static_cast<int>(min(sh.end - c, int64_t(kStageVecs)));
+          const int cnt = min(sh.end - c, kStageVecs);
           read_stage<T>(v, dyn + held.stage * kStageBytes, cnt);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int at = i * kStreamThreads + tid;
             if (at >= cnt) break;
+            if (w != 0.0f) {
 #pragma unroll
-            for (int p = 0; p < E / 2; ++p) {
-              const float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
-              const float2 y = __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), k2);
-              set_pair<T>(v[i], p, w == 0.0f ? make_float2(0.f, 0.f) : y);
+              for (int p = 0; p < E / 2; ++p) {
+                const float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
+                set_pair<T>(v[i], p, __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), k2));
+              }
+            } else {
+              v[i] = Vec{{0u, 0u, 0u, 0u}};
             }
-            store_row_vec(out, (c + at) * E - sh.shift, a.V, aligned, v[i]);
+            store_row_vec(out, first_element<T>(sh, c + at), a.V, aligned, v[i]);
           }
           held.next();
         }
-        // the elements at the entries, over the dense part that this warp has written
+        // The elements at the entries, over the dense part that this warp has written. The entries of
+        // one id are all of one warp, which adds them together lane by lane.
         __syncwarp();
         if (w != 0.0f) {
-          const int64_t vecs = sh.end - sh.begin;
-          for (int k = lane; k < a.K; k += 32) {
-            const int id = n.id[k];
-            if (id < 0) continue;
-            const int64_t at = (static_cast<int64_t>(id) + sh.shift) / E - sh.begin;  // of the share's vectors
-            if (at < 0 || at >= vecs || static_cast<int>(at % kStreamThreads) >> 5 != warp) continue;
-            float q = 0.f;
-            bool lowest = true;  // an id that comes twice is written by its first entry
-            for (int j = 0; j < a.K; ++j) {
-              if (n.id[j] != id) continue;
-              lowest = lowest && j >= k;
-              q += ex2_approx(n.td[j] * c2);
+          for (int k0 = 0; k0 < a.K; k0 += 32) {
+            const int mine = k0 + lane < a.K ? n.id[k0 + lane] : -1;
+            const int64_t vec = (static_cast<int64_t>(mine) + sh.shift) / E - sh.begin;  // of the share's
+            const bool own = mine >= 0 && vec >= 0 && vec < sh.end - sh.begin &&
+                             (static_cast<int>(vec) % kStreamThreads) >> 5 == warp;
+            for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo != 0; todo &= todo - 1) {
+              const int from = __ffs(todo) - 1;
+              const int id = __shfl_sync(0xffffffffu, mine, from);
+              const int at = __shfl_sync(0xffffffffu, static_cast<int>(vec), from);
+              float q = 0.f;
+              for (int j = lane; j < a.K; j += 32)
+                if (n.id[j] == id) q += ex2_approx(n.td[j] * c2);
+              q = warp_sum(q);
+              int stage = begin.stage + at / kStageVecs;
+              if (stage >= kStages) stage -= kStages;
+              const T* p = reinterpret_cast<const T*>(dyn + stage * kStageBytes + (at % kStageVecs) * 16);
+              const float x = (to_f(p[(id + sh.shift) % E]) - g.me) * c2;
+              if (lane == 0) out[id] = from_f<T>(fmaf(g.dense, ex2_approx(x), -g.sparse * q));
             }
-            if (!lowest) continue;
-            int stage = begin.stage + static_cast<int>(at / kStageVecs);
-            if (stage >= kStages) stage -= kStages;
-            const T* p = reinterpret_cast<const T*>(dyn + stage * kStageBytes + (at % kStageVecs) * 16);
-            const float x = (to_f(p[(id + sh.shift) % E]) - g.me) * c2;
-            out[id] = from_f<T>(fmaf(g.dense, ex2_approx(x), -g.sparse * q));
           }
         }
         __syncwarp();
         if (lane == 0) {
           Place p = begin;
-          for (int64_t c = sh.begin; c < sh.end; c += kStageVecs, p.next()) mbar_arrive(&sm.ring.empty[p.stage]);
+          for (int c = sh.begin; c < sh.end; c += kStageVecs, p.next()) mbar_arrive(&sm.ring.empty[p.stage]);
         }
       }
       if (rank == 0 && warp == 0) {
@@ -407,38 +412,38 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
 }
 
 template <typename T, bool kGrad>
-cudaError_t launch_fwd(const KdArgs& a, int S, cudaStream_t stream) {
+cudaError_t launch_fwd(const KdArgs& a, Split split, cudaStream_t stream) {
   static std::mutex mu;  // guards the occupancy cache
   static StreamCache cache;
   std::lock_guard<std::mutex> lk(mu);
-  return launch_stream(kd_fwd_kernel<T, kGrad>, cache, kFwdThreads, kFwdSmem, a.T, S, stream, a, S, status_word_ptr());
+  return launch_stream(kd_fwd_kernel<T, kGrad>, cache, kFwdThreads, kFwdSmem, a.T, split.S, stream, a, split,
+                       status_word_ptr());
 }
 template <bool kGrad>
-cudaError_t launch_fwd_any(const KdArgs& a, int dtype, int S, cudaStream_t stream) {
-  return dtype == 0   ? launch_fwd<float, kGrad>(a, S, stream)
-         : dtype == 1 ? launch_fwd<__half, kGrad>(a, S, stream)
-                      : launch_fwd<__nv_bfloat16, kGrad>(a, S, stream);
+cudaError_t launch_fwd_any(const KdArgs& a, int dtype, Split split, cudaStream_t stream) {
+  return dtype == 0   ? launch_fwd<float, kGrad>(a, split, stream)
+         : dtype == 1 ? launch_fwd<__half, kGrad>(a, split, stream)
+                      : launch_fwd<__nv_bfloat16, kGrad>(a, split, stream);
 }
 
 // ---- gradient alone
 
 // the gradient from saved statistics
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 3) kd_bwd_kernel(const KdArgs a, int64_t row0, int S) {
-  constexpr int E = Traits<T>::E;
+__global__ void __launch_bounds__(kRowThreads, 3) kd_bwd_kernel(const KdArgs a, int64_t row0, Split split) {
   __shared__ KdSmem sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t r = row0 + blockIdx.x / S;
+  const int64_t r = row0 + blockIdx.x / split.S;
   const T* z = static_cast<const T*>(a.logits) + r * a.ld;
   T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
-  const Share sh = share_of(z, a.V, S, static_cast<int>(blockIdx.x % S));
+  const Share sh = share_of(z, a.V, split.per, static_cast<int>(blockIdx.x % split.S));
   const bool aligned = row_shift(out) == sh.shift;
   const float w = a.weight[r];
   if (w == 0.0f) {
     store_zeros(out, a.V, aligned, sh);
     return;
   }
-  const int64_t e0 = sh.begin * E - sh.shift, e1 = sh.end * E - sh.shift;
+  const int64_t e0 = first_element<T>(sh, sh.begin), e1 = first_element<T>(sh, sh.end);
   Entries n;
   const float tmax = load_entries(a, r, n, sm);
   Vec v[kVecs];
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) kd_bwd_kernel(const KdArgs a, 
   if (lane == 0) sm.tsum[warp] = ts;
   __syncthreads();
   const Gradient g = make_gradient(a, a.stats_in[2 * r], a.stats_in[2 * r + 1], w, warps_sum(sm.tsum));
-  for (int64_t c = sh.begin; c < sh.end; c += kChunk) {
+  for (int c = sh.begin; c < sh.end; c += kChunk) {
     if (c > sh.begin) load_chunk<T, false>(v, z, a.V, sh, c);
     store_dense(v, g, out, a.V, aligned, sh, c);
   }
@@ -466,15 +471,14 @@ cudaError_t launch_distill(const KdArgs& a, bool forward, bool backward, int dty
   const int64_t vectors = row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2);
   // the row's shares have to stay in the rings for the gradient: a longer row is read twice
   const bool once = forward && backward && vectors <= int64_t(kMaxCluster) * kShareStages * kStageVecs;
-  if (once) return launch_fwd_any<true>(a, dtype, stream_blocks(a.T, vectors, kShareStages, sms), stream);
+  if (once) return launch_fwd_any<true>(a, dtype, split_row(a.T, vectors, kShareStages * kStageVecs, sms), stream);
   if (forward) {
-    const int S = stream_blocks(a.T, vectors, vectors, sms);
-    const cudaError_t e = launch_fwd_any<false>(a, dtype, S, stream);
+    const cudaError_t e = launch_fwd_any<false>(a, dtype, split_row(a.T, vectors, vectors, sms), stream);
     if (e != cudaSuccess || !backward) return e;
   }
   KdArgs b = a;
   if (forward) b.stats_in = a.stats;
-  return launch_all_rows(b, dtype, row_blocks(a.T, vectors, sms), false, stream, kd_bwd_kernel<float>,
+  return launch_all_rows(b, dtype, split_row(a.T, vectors, kChunk, sms), false, stream, kd_bwd_kernel<float>,
                          kd_bwd_kernel<__half>, kd_bwd_kernel<__nv_bfloat16>);
 }
 

@@ -40,14 +40,14 @@ struct TlpSmem {
 // One warp: the first `need` logits equal to `bound` in index order -> cand; returns how many there are
 // (at most need).
 template <typename T>
-__device__ __noinline__ int collect_equal(const T* z, int64_t V, const Share& sh, int64_t c, float bound, int need,
+__device__ __noinline__ int collect_equal(const T* z, int64_t V, const Share& sh, int c, float bound, int need,
                                           uint64_t* cand) {
   constexpr int E = Traits<T>::E;
   const int lane = threadIdx.x & 31;
-  const int64_t end = min(sh.end, c + kChunk);
+  const int end = min(sh.end, c + kChunk);
   int found = 0;
-  for (int64_t g0 = c; g0 < end && found < need; g0 += 32) {
-    const int64_t e0 = (g0 + lane) * E - sh.shift;
+  for (int g0 = c; g0 < end && found < need; g0 += 32) {
+    const int64_t e0 = first_element<T>(sh, g0 + lane);
     uint32_t hits = 0;
     if (g0 + lane < end) {
       const Vec v = load_row_vec<T, true>(z, e0, V);
@@ -71,12 +71,12 @@ __device__ __noinline__ int collect_equal(const T* z, int64_t V, const Share& sh
 }
 // the thread's best key below `below` among its logits above -inf, 0 if there is none
 template <typename T>
-__device__ __noinline__ uint64_t best_below(const T* z, int64_t V, const Share& sh, int64_t c, uint64_t below) {
+__device__ __noinline__ uint64_t best_below(const T* z, int64_t V, const Share& sh, int c, uint64_t below) {
   constexpr int E = Traits<T>::E;
-  const int64_t end = min(sh.end, c + kChunk);
+  const int end = min(sh.end, c + kChunk);
   uint64_t best = 0;
-  for (int64_t g = c + threadIdx.x; g < end; g += kRowThreads) {
-    const int64_t e0 = g * E - sh.shift;
+  for (int g = c + static_cast<int>(threadIdx.x); g < end; g += kRowThreads) {
+    const int64_t e0 = first_element<T>(sh, g);
     const Vec v = load_row_vec<T, true>(z, e0, V);
 #pragma unroll
     for (int p = 0; p < E / 2; ++p) {
@@ -91,22 +91,23 @@ __device__ __noinline__ uint64_t best_below(const T* z, int64_t V, const Share& 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 3) tlp_fwd_kernel(const TlpFwdArgs a, int64_t row0, int S) {
+__global__ void __launch_bounds__(kRowThreads, 3) tlp_fwd_kernel(const TlpFwdArgs a, int64_t row0, Split split) {
   constexpr int E = Traits<T>::E;
   __shared__ TlpSmem sm;
+  const int S = split.S;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   if (S > 1) cluster_arrive();
   const int64_t r = row0 + blockIdx.x / S;
   const T* z = static_cast<const T*>(a.logits) + r * a.ld;
-  const Share sh = share_of(z, a.V, S, rank);
+  const Share sh = share_of(z, a.V, split.per, rank);
   const float c2 = a.inv_temp * kLog2e;
 
   // What the block has seen, the same in every thread: max, sum 2^x and sum 2^x x with
   // x = (z - max) log2(e) / tau, number of best keys.
   float m = neg_inf(), s = 0.f, w = 0.f;
   int nbest = 0;
-  for (int64_t c = sh.begin; c < sh.end; c += kChunk) {
+  for (int c = sh.begin; c < sh.end; c += kChunk) {
     Vec v[kVecs];
     load_chunk<T, true>(v, z, a.V, sh, c);
     float tm = neg_inf();
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) tlp_fwd_kernel(const TlpFwdArg
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {
         if (!good(vec_max<T>(v[i]))) continue;
-        const uint32_t e0 = static_cast<uint32_t>((c + i * kRowThreads + tid) * E - sh.shift);
+        const uint32_t e0 = static_cast<uint32_t>(first_element<T>(sh, c + i * kRowThreads + tid));
 #pragma unroll
         for (int p = 0; p < E / 2; ++p) {
           const float2 x = vec_pair<T>(v[i], p);
@@ -312,12 +313,12 @@ static_assert(kMaxTop == 32, "one lane for each alternative");
 
 // Backward: bound by HBM (V elements read and written a row); no block needs another's results.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) tlp_bwd_kernel(const TlpBwdArgs a, int64_t row0, int S) {
+__global__ void __launch_bounds__(kRowThreads) tlp_bwd_kernel(const TlpBwdArgs a, int64_t row0, Split split) {
   constexpr int E = Traits<T>::E;
-  const int64_t r = row0 + blockIdx.x / S;
+  const int64_t r = row0 + blockIdx.x / split.S;
   const T* z = static_cast<const T*>(a.logits) + r * a.ld;
   T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
-  const Share sh = share_of(z, a.V, S, static_cast<int>(blockIdx.x % S));
+  const Share sh = share_of(z, a.V, split.per, static_cast<int>(blockIdx.x % split.S));
   const bool aligned = row_shift(out) == sh.shift;
   const float m = a.stats[2 * r], s = a.stats[2 * r + 1];
   const float me = finite_or_0(m), c2 = a.inv_temp * kLog2e;
@@ -335,14 +336,14 @@ __global__ void __launch_bounds__(kRowThreads) tlp_bwd_kernel(const TlpBwdArgs a
   const int64_t tt = t != a.ignore && valid && s != 0.0f ? t : -1;
   const float2 nm2 = make_float2(-me, -me), cc2 = make_float2(c2, c2), k02 = make_float2(k0, k0);
   const float2 k12 = make_float2(k1, k1);
-  for (int64_t c = sh.begin; c < sh.end; c += kChunk) {
+  for (int c = sh.begin; c < sh.end; c += kChunk) {
     Vec v[kVecs];
     load_chunk<T, false>(v, z, a.V, sh, c);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int64_t g = c + i * kRowThreads + threadIdx.x;
+      const int g = c + i * kRowThreads + static_cast<int>(threadIdx.x);
       if (g >= sh.end) break;
-      const int64_t e0 = g * E - sh.shift;
+      const int64_t e0 = first_element<T>(sh, g);
 #pragma unroll
       for (int p = 0; p < E / 2; ++p) {
         float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
@@ -370,14 +371,14 @@ __global__ void __launch_bounds__(kRowThreads) tlp_bwd_kernel(const TlpBwdArgs a
 }  // namespace
 
 cudaError_t launch_token_logprobs_fwd(const TlpFwdArgs& a, int dtype, cudaStream_t stream) {
-  const int S = row_blocks(a.T, row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2), device_sm_count());
-  return launch_all_rows(a, dtype, S, S > 1, stream, tlp_fwd_kernel<float>, tlp_fwd_kernel<__half>,
+  const Split p = split_row(a.T, row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2), kChunk, device_sm_count());
+  return launch_all_rows(a, dtype, p, p.S > 1, stream, tlp_fwd_kernel<float>, tlp_fwd_kernel<__half>,
                          tlp_fwd_kernel<__nv_bfloat16>);
 }
 
 cudaError_t launch_token_logprobs_bwd(const TlpBwdArgs& a, int dtype, cudaStream_t stream) {
-  const int S = row_blocks(a.T, row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2), device_sm_count());
-  return launch_all_rows(a, dtype, S, false, stream, tlp_bwd_kernel<float>, tlp_bwd_kernel<__half>,
+  const Split p = split_row(a.T, row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2), kChunk, device_sm_count());
+  return launch_all_rows(a, dtype, p, false, stream, tlp_bwd_kernel<float>, tlp_bwd_kernel<__half>,
                          tlp_bwd_kernel<__nv_bfloat16>);
 }
 

@@ -149,29 +149,33 @@ __device__ __forceinline__ void store_row_vec(T* out, int64_t e0, int64_t V, boo
   }
 }
 
-// a block's share of a row
+// A block's share of a row: `per` of its vectors (fewer than 2^30: a row has fewer than 2^31 elements).
 struct Share {
-  int64_t begin, end;  // its vectors
+  int begin, end;
   int shift;
 };
 template <typename T>
-__device__ __forceinline__ Share share_of(const T* row, int64_t V, int S, int rank) {
+__device__ __forceinline__ Share share_of(const T* row, int64_t V, int per, int rank) {
   Share s;
   s.shift = row_shift(row);
   const int64_t n = (s.shift + V + Traits<T>::E - 1) / Traits<T>::E;
-  const int64_t per = (n + S - 1) / S;
-  s.begin = min(n, rank * per);
-  s.end = min(n, s.begin + per);
+  s.begin = static_cast<int>(min(n, static_cast<int64_t>(rank) * per));
+  s.end = static_cast<int>(min(n, static_cast<int64_t>(s.begin) + per));
   return s;
+}
+// the row's element at the start of vector g
+template <typename T>
+__device__ __forceinline__ int64_t first_element(const Share& s, int g) {
+  return static_cast<int64_t>(g) * Traits<T>::E - s.shift;
 }
 // vectors c + i kRowThreads + threadIdx.x of the share -> v[i]; -inf past its end
 template <typename T, bool kReadOnly>
-__device__ __forceinline__ void load_chunk(Vec (&v)[kVecs], const T* row, int64_t V, const Share& s, int64_t c) {
+__device__ __forceinline__ void load_chunk(Vec (&v)[kVecs], const T* row, int64_t V, const Share& s, int c) {
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int64_t g = c + i * kRowThreads + threadIdx.x;
+    const int g = c + i * kRowThreads + static_cast<int>(threadIdx.x);
     if (g < s.end) {
-      v[i] = load_row_vec<T, kReadOnly>(row, g * Traits<T>::E - s.shift, V);
+      v[i] = load_row_vec<T, kReadOnly>(row, first_element<T>(s, g), V);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[i].w[j] = Traits<T>::kNegInf;
@@ -223,14 +227,19 @@ inline int64_t row_vectors(const void* rows, int64_t V, int64_t ld, int elem_byt
   const bool whole = reinterpret_cast<uintptr_t>(rows) % 16 == 0 && (ld * elem_bytes) % 16 == 0;
   return (V * elem_bytes + 15) / 16 + (whole ? 0 : 1);
 }
-// Blocks a row is given: enough to hold it in registers (up to the portable cluster size), more when
-// there are so few rows that SMs would stay idle, but no shares below kMinShare vectors.
+// Blocks a row is given: shares of at most `share` vectors where the portable cluster size allows it,
+// and more blocks when there are so few rows that SMs would stay idle (but no shares below kMinShare).
 constexpr int64_t kMinShare = 256;
-inline int row_blocks(int64_t T, int64_t vectors, int num_sms) {
+struct Split {
+  int S;    // blocks a row
+  int per;  // vectors a block takes
+};
+inline Split split_row(int64_t T, int64_t vectors, int64_t share, int num_sms) {
   const int64_t useful = (vectors + kMinShare - 1) / kMinShare, spread = num_sms / T;
-  int64_t s = (vectors + row::kChunk - 1) / row::kChunk;
+  int64_t s = (vectors + share - 1) / share;
   if (s < spread && s < useful) s = spread < useful ? spread : useful;
-  return static_cast<int>(s > row::kMaxCluster ? row::kMaxCluster : s);
+  if (s > row::kMaxCluster) s = row::kMaxCluster;
+  return Split{static_cast<int>(s), static_cast<int>((vectors + s - 1) / s)};
 }
 
 // launches of at most kMaxLaunchRows rows: their blocks stay below 2^31
@@ -251,15 +260,15 @@ cudaError_t launch_rows(Kernel kernel, int64_t rows, int S, bool cluster, cudaSt
   cfg.numAttrs = cluster ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
-// all T rows of `a`, S blocks a row
+// all T rows of `a`
 template <typename Args, typename K32, typename K16, typename KB>
-cudaError_t launch_all_rows(const Args& a, int dtype, int S, bool cluster, cudaStream_t stream, K32 k32, K16 k16,
+cudaError_t launch_all_rows(const Args& a, int dtype, Split p, bool cluster, cudaStream_t stream, K32 k32, K16 k16,
                             KB kb) {
   for (int64_t row0 = 0; row0 < a.T; row0 += kMaxLaunchRows) {
     const int64_t rows = a.T - row0 < kMaxLaunchRows ? a.T - row0 : kMaxLaunchRows;
-    const cudaError_t e = dtype == 0   ? launch_rows(k32, rows, S, cluster, stream, a, row0, S)
-                          : dtype == 1 ? launch_rows(k16, rows, S, cluster, stream, a, row0, S)
-                                       : launch_rows(kb, rows, S, cluster, stream, a, row0, S);
+    const cudaError_t e = dtype == 0   ? launch_rows(k32, rows, p.S, cluster, stream, a, row0, p)
+                          : dtype == 1 ? launch_rows(k16, rows, p.S, cluster, stream, a, row0, p)
+                                       : launch_rows(kb, rows, p.S, cluster, stream, a, row0, p);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -75,7 +75,7 @@ struct Place {
 // The producer warp: all rows of the block's cluster, row r's share at `rank` of S.
 template <typename T>
 __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int64_t V, int64_t first, int64_t rows,
-                                             int64_t step, int S, int rank, unsigned char* buf, Ring& ring,
+                                             int64_t step, int per, int rank, unsigned char* buf, Ring& ring,
                                              Patience& wait) {
   constexpr int E = Traits<T>::E;
   const int lane = threadIdx.x & 31;
@@ -86,10 +86,10 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
     T x = from_f<T>(neg_inf());
     if (r >= rows) return x;
     const T* z = base + r * ld;
-    const Share sh = share_of(z, V, S, rank);
+    const Share sh = share_of(z, V, per, rank);
     const int at = lane & 15;
     if (at >= E || sh.begin == sh.end) return x;
-    const int64_t e = (lane < 16 ? sh.begin : sh.end - 1) * E - sh.shift + at;
+    const int64_t e = first_element<T>(sh, lane < 16 ? sh.begin : sh.end - 1) + at;
     if (e >= 0 && e < V) x = z[e];
     return x;
   };
@@ -97,15 +97,15 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
   T mine = edge(first);
   for (int64_t r = first; r < rows; r += step) {
     const T* z = base + r * ld;
-    const Share sh = share_of(z, V, S, rank);
+    const Share sh = share_of(z, V, per, rank);
     const T ahead = edge(r + step);
-    const int64_t e0 = sh.begin * E - sh.shift, e1 = sh.end * E - sh.shift;
-    const int64_t whole0 = sh.begin + (e0 < 0 ? 1 : 0), whole1 = max(whole0, sh.end - (e1 > V ? 1 : 0));
-    for (int64_t c = sh.begin; c < sh.end; c += kStageVecs) {
-      const int64_t end = min(sh.end, c + kStageVecs);
+    const int64_t e0 = first_element<T>(sh, sh.begin), e1 = first_element<T>(sh, sh.end);
+    const int whole0 = sh.begin + (e0 < 0 ? 1 : 0), whole1 = max(whole0, sh.end - (e1 > V ? 1 : 0));
+    for (int c = sh.begin; c < sh.end; c += kStageVecs) {
+      const int end = min(sh.end, c + kStageVecs);
       unsigned char* to = buf + p.stage * kStageBytes;
       wait(&ring.empty[p.stage], p.parity ^ 1u);
-      const int64_t w0 = max(c, whole0), w1 = min(end, whole1);
+      const int w0 = max(c, whole0), w1 = min(end, whole1);
       // a partial vector's elements, lane by lane
       const bool head = c == sh.begin && e0 < 0, tail = end == sh.end && e1 > V;
       if (lane < E && head) reinterpret_cast<T*>(to)[lane] = mine;
@@ -116,7 +116,7 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
         fence_proxy_async_smem();
         const uint32_t bytes = w1 > w0 ? static_cast<uint32_t>(w1 - w0) * 16u : 0u;
         mbar_arrive_expect_tx(&ring.full[p.stage], bytes);
-        if (bytes > 0) bulk_g2s(to + (w0 - c) * 16, z + (w0 * E - sh.shift), bytes, &ring.full[p.stage]);
+        if (bytes > 0) bulk_g2s(to + (w0 - c) * 16, z + first_element<T>(sh, w0), bytes, &ring.full[p.stage]);
       }
       __syncwarp();
       p.next();
@@ -150,15 +150,6 @@ __device__ __forceinline__ void send_f2(const float2* to, const uint64_t* bar, u
 }
 
 }  // namespace row
-
-// Shares of at most `stages` stages where the cluster size allows it, more blocks when there are so few
-// rows that SMs would stay idle (but no shares below kMinShare vectors).
-inline int stream_blocks(int64_t T, int64_t vectors, int64_t stages, int num_sms) {
-  const int64_t useful = (vectors + kMinShare - 1) / kMinShare, spread = num_sms / T;
-  int64_t s = (vectors + stages * row::kStageVecs - 1) / (stages * row::kStageVecs);
-  if (s < spread && s < useful) s = spread < useful ? spread : useful;
-  return static_cast<int>(s > row::kMaxCluster ? row::kMaxCluster : s);
-}
 
 // A persistent launch: as many clusters as fit on the device at once, at most one a row. The occupancy of
 // a (kernel, cluster size, shared memory) is asked once for each device.
