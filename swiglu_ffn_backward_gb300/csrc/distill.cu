@@ -9,10 +9,10 @@
 // Bound by HBM: V elements a row are read, and written where there is a gradient.
 // Loss, and loss with gradient: a persistent kernel streams rows through shared memory (vocab_stream.cuh).
 // With a gradient a row's shares stay in the rings of a cluster of S blocks until it is written, so the
-// logits are read once. The warps' (max, sum) go to every block of the cluster, which each warp joins for
-// itself; the gradient of a row is formed after the sums of the next one, so the exchange is off the
-// path. The gradient's sparse part, at most K elements a row, is written by the warp that wrote the
-// dense part there. One warp takes the teacher's entries a row ahead.
+// logits are read once. The warps' (max, sum) go to every block of the cluster, where one warp joins them;
+// the gradient of a row is formed after the sums of the next one, so the exchange is off the path. The
+// gradient's sparse part, at most K elements a row, is written by the warp that wrote the dense part
+// there. One more warp takes the teacher's entries a row ahead.
 // The gradient alone needs no exchange: blocks take 32 KB shares of rows in registers.
 #include <mutex>
 
@@ -96,14 +96,18 @@ __device__ __forceinline__ float warps_sum(const float* v) {
 }
 
 struct Gradient {
-  float me, c2;  // 2^((z - me) c2) is the unscaled probability
+  Scale k;       // 2^fma(z, k.c, -k.ref) / s is the probability
   float dense;   // w Q / (tau s)
   float sparse;  // w / (tau sq)
 };
-__device__ __forceinline__ Gradient make_gradient(const KdArgs& a, float m, float s, float w, float sq) {
+__device__ __forceinline__ Gradient make_gradient(const KdArgs& a, const Scale& k, float s, float w, float sq) {
   const float wt = w * a.inv_temp;
-  return Gradient{finite_or_0(m), a.inv_temp * kLog2e, s == 0.0f || sq == 0.0f ? 0.0f : wt / s,
-                  sq == 0.0f ? 0.0f : wt / sq};
+  return Gradient{k, s == 0.0f || sq == 0.0f ? 0.0f : wt / s, sq == 0.0f ? 0.0f : wt / sq};
+}
+// two elements of the dense part
+__device__ __forceinline__ float2 dense_pair(const Gradient& g, float2 z) {
+  const float2 x = __ffma2_rn(z, make_float2(g.k.c, g.k.c), make_float2(-g.k.ref, -g.k.ref));
+  return __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(g.dense, g.dense));
 }
 
 // the dense part of the chunk at c
@@ -111,16 +115,12 @@ template <typename T>
 __device__ __forceinline__ void store_dense(Vec (&v)[kVecs], const Gradient& g, T* out, int64_t V, bool aligned,
                                             const Share& sh, int c) {
   constexpr int E = Traits<T>::E;
-  const float2 nm2 = make_float2(-g.me, -g.me), cc2 = make_float2(g.c2, g.c2), k2 = make_float2(g.dense, g.dense);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int at = c + i * kRowThreads + static_cast<int>(threadIdx.x);
     if (at >= sh.end) break;
 #pragma unroll
-    for (int p = 0; p < E / 2; ++p) {
-      const float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
-      set_pair<T>(v[i], p, __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), k2));
-    }
+    for (int p = 0; p < E / 2; ++p) set_pair<T>(v[i], p, dense_pair(g, vec_pair<T>(v[i], p)));
     store_row_vec(out, first_element<T>(sh, at), V, aligned, v[i]);
   }
 }
@@ -146,13 +146,13 @@ __device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g,
       first = first && j >= k;
       q += sm.q[j];
     }
-    if (first) out[id] = from_f<T>(fmaf(g.dense, ex2_approx((n.z[i] - g.me) * g.c2), -g.sparse * q));
+    if (first) out[id] = from_f<T>(fmaf(g.dense, ex2_approx(fmaf(n.z[i], g.k.c, -g.k.ref)), -g.sparse * q));
   }
 }
 
 // ---- loss, and loss with gradient
 
-constexpr int kExtraWarps = 2;  // producer, teacher
+constexpr int kExtraWarps = 3;  // producer, teacher, joiner
 constexpr int kFwdThreads = kStreamThreads + 32 * kExtraWarps;
 constexpr int kSlots = 4;       // exchange slots: a slot is written again four rows later
 constexpr int kShareStages = 2; // stages a row's share may hold: two rows' shares, and two stages ahead
@@ -161,9 +161,11 @@ struct KdStream {
   Ring ring;
   uint64_t joined[kSlots];  // the row's maxima and sums have come from all blocks
   uint64_t ready[2];        // the row's entries are in shared memory
-  uint64_t spare[2];        // the computing warps are done with them
+  uint64_t spare[2];        // their readers are done with them
+  uint64_t solved[2];       // the row's gradient constants are in shared memory
   float2 part[kSlots][kMaxCluster][kStreamWarps];  // max and sum of every warp
   float2 note[kSlots];      // from the first block: its entries' logits have been read
+  Gradient grad[2];
   float weight[2];
   float sq[2];              // sum exp((t - max t) / tau), 0 for a row without entries
 };
@@ -234,7 +236,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
     for (int i = 0; i < kSlots; ++i) mbar_init(&sm.joined[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.ready[i], 1);
-      mbar_init(&sm.spare[i], kStreamWarps);
+      mbar_init(&sm.spare[i], kGrad ? kStreamWarps + 1 : 1);
+      mbar_init(&sm.solved[i], 1);
     }
     fence_mbar_init();
     for (int i = 0; i < kSlots; ++i) mbar_arrive_expect_tx(&sm.joined[i], bytes);
@@ -243,6 +246,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
   cluster_arrive();
   cluster_wait();
   Patience wait;
+  const float c2 = a.inv_temp * kLog2e;
 
   if (warp == kStreamWarps) {
     produce_rows<T>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, sm.ring, wait);
@@ -263,32 +267,75 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       if (rank == 0 && lane < S) send_f2(&sm.note[slot], &sm.joined[slot], static_cast<uint32_t>(lane), 0.f, 0.f);
       __syncwarp();
     }
+  } else if (warp == kStreamWarps + 2) {
+    // joins the row's maxima and sums, and forms the constants of its gradient and (first block) its loss
+    int64_t it = 0;
+    for (int64_t r = first; r < a.T; r += step, ++it) {
+      const int b = static_cast<int>(it & 1), slot = static_cast<int>(it & (kSlots - 1));
+      wait.cluster(&sm.joined[slot], static_cast<uint32_t>((it / kSlots) & 1));
+      if (lane == 0) mbar_arrive_expect_tx(&sm.joined[slot], bytes);
+      const float2* part = &sm.part[slot][0][0];
+      float m = neg_inf(), s = 0.f;
+      for (int i = lane; i < S * kStreamWarps; i += 32) m = fmaxf(m, part[i].x);
+      m = warp_max(m);
+      const Scale k = scale_of(m, c2);
+      for (int i = lane; i < S * kStreamWarps; i += 32)
+        s = fmaf(ex2_approx(ref_shift(part[i].x, scale_of(part[i].x, c2), m, k, c2)), part[i].y, s);
+      s = warp_sum(s);
+      wait(&sm.ready[b], static_cast<uint32_t>((it >> 1) & 1));
+      const float sq = sm.sq[b];
+      if (lane == 0) {
+        if (kGrad) sm.grad[b] = make_gradient(a, k, s, sm.weight[b], sq);
+        mbar_arrive(&sm.solved[b]);
+      }
+      if (rank == 0) {
+        // sum q (ln q - ln p) = sum (q / tau) (td - (z - max z)) - ln sq + ln s: a mask of the type's
+        // lowest value leaves the range of fp32 only where the loss does
+        const EntryArrays& n = entries[b];
+        const float me = finite_or_0(m), f = a.inv_temp / sq;
+        float l = 0.f;
+        for (int i = lane; i < a.K; i += 32) {
+          const float e = ex2_approx(n.td[i] * c2);
+          if (n.id[i] >= 0 && e != 0.0f) l = fmaf(e * f, n.td[i] - (n.z[i] - me), l);
+        }
+        l = warp_sum(l);
+        if (lane == 0) {
+          s = sum_at_max(s, m, k);
+          a.stats[2 * r] = m;
+          a.stats[2 * r + 1] = s;
+          a.loss[r] = sq == 0.0f ? 0.0f : l + ((s == 0.0f ? 0.0f : logf(s)) - logf(sq));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.spare[b]);
+    }
   } else {
-    const float c2 = a.inv_temp * kLog2e;
-    const float2 cc2 = make_float2(c2, c2);
     Place in, held;  // the next stage to read, and (with a gradient) the first stage of the row before
     // max and sum of the warp's part of row r, sent to every block
     auto sums = [&](int64_t r, int slot) {
       const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
       float m = neg_inf();
+      Scale k = scale_of(m, c2);
       float2 s2 = make_float2(0.f, 0.f);
-      for (int c = sh.begin; c < sh.end; c += kStageVecs) {
+      for (int at = sh.begin; at < sh.end; at += kStageVecs) {
         Vec v[4];
         wait(&sm.ring.full[in.stage], in.parity);
-        read_stage<T>(v, dyn + in.stage * kStageBytes, min(sh.end - c, kStageVecs));
-        const float mn = fmaxf(fmaxf(fmaxf(vec_max<T>(v[0]), vec_max<T>(v[1])), fmaxf(vec_max<T>(v[2]), vec_max<T>(v[3]))), m);
-        const float me = finite_or_0(mn);
+        read_stage<T>(v, dyn + in.stage * kStageBytes, min(sh.end - at, kStageVecs));
+        const float mn = fmaxf(m, warp_max(fmaxf(fmaxf(vec_max<T>(v[0]), vec_max<T>(v[1])),
+                                                 fmaxf(vec_max<T>(v[2]), vec_max<T>(v[3])))));
         if (mn > m) {
-          const float f = ex2_approx(part_shift(m, mn, c2));
+          const Scale kn = scale_of(mn, c2);
+          const float f = ex2_approx(ref_shift(m, k, mn, kn, c2));
           s2 = __fmul2_rn(s2, make_float2(f, f));
           m = mn;
+          k = kn;
         }
-        const float2 nm2 = make_float2(-me, -me);
+        const float2 c = make_float2(k.c, k.c), ref = make_float2(-k.ref, -k.ref);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
           for (int p = 0; p < E / 2; ++p) {
-            const float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
+            const float2 x = __ffma2_rn(vec_pair<T>(v[i], p), c, ref);
             s2 = __fadd2_rn(s2, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
           }
         }
@@ -298,105 +345,79 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
         }
         in.next();
       }
-      const float wm = warp_max(m);
-      const float ws = warp_sum((s2.x + s2.y) * ex2_approx(part_shift(m, wm, c2)));
-      if (lane < S) send_f2(&sm.part[slot][rank][warp], &sm.joined[slot], static_cast<uint32_t>(lane), wm, ws);
+      const float s = warp_sum(s2.x + s2.y);
+      if (lane < S) send_f2(&sm.part[slot][rank][warp], &sm.joined[slot], static_cast<uint32_t>(lane), m, s);
       __syncwarp();
     };
-    // the rest of row r, the it-th of the block
+    // The gradient of row r, the it-th of the block. Without a gradient only the wait is left: a warp is
+    // at most a row ahead of the joiner, so the exchange slots are read before they are written again.
     auto finish = [&](int64_t r, int64_t it) {
-      const int b = static_cast<int>(it & 1), slot = static_cast<int>(it & (kSlots - 1));
-      wait.cluster(&sm.joined[slot], static_cast<uint32_t>((it / kSlots) & 1));
-      if (tid == 0) mbar_arrive_expect_tx(&sm.joined[slot], bytes);
-      float m = neg_inf(), s = 0.f;
-      const float2* part = &sm.part[slot][0][0];
-      for (int i = lane; i < S * kStreamWarps; i += 32) m = fmaxf(m, part[i].x);
-      m = warp_max(m);
-      for (int i = lane; i < S * kStreamWarps; i += 32)
-        s = fmaf(ex2_approx(part_shift(part[i].x, m, c2)), part[i].y, s);
-      s = warp_sum(s);
-      wait(&sm.ready[b], static_cast<uint32_t>((it >> 1) & 1));
+      const int b = static_cast<int>(it & 1);
+      wait(&sm.solved[b], static_cast<uint32_t>((it >> 1) & 1));
+      if (!kGrad) return;
+      const T* z = static_cast<const T*>(a.logits) + r * a.ld;
+      T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
+      const Share sh = share_of(z, a.V, split.per, rank);
+      const bool aligned = row_shift(out) == sh.shift;
       const EntryArrays& n = entries[b];
-      const float sq = sm.sq[b];
-      if (kGrad) {
-        const T* z = static_cast<const T*>(a.logits) + r * a.ld;
-        T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
-        const Share sh = share_of(z, a.V, split.per, rank);
-        const bool aligned = row_shift(out) == sh.shift;
-        const float w = sm.weight[b];
-        const Gradient g = make_gradient(a, m, s, w, sq);
-        const float2 nm2 = make_float2(-g.me, -g.me), k2 = make_float2(g.dense, g.dense);
-        const Place begin = held;
-        for (int c = sh.begin; c < sh.end; c += kStageVecs) {
-          Vec v[4];
-          const int cnt = min(sh.end - c, kStageVecs);
-          read_stage<T>(v, dyn + held.stage * kStageBytes, cnt);
+      const Gradient g = sm.grad[b];
+      const bool some = sm.weight[b] != 0.0f;
+      const Place begin = held;
+      for (int c = sh.begin; c < sh.end; c += kStageVecs) {
+        Vec v[4];
+        const int cnt = min(sh.end - c, kStageVecs);
+        read_stage<T>(v, dyn + held.stage * kStageBytes, cnt);
+        const int64_t e0 = first_element<T>(sh, c), e1 = first_element<T>(sh, c + cnt);
+        const bool inner = aligned && e0 >= 0 && e1 <= a.V;  // the stage has whole vectors only
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = i * kStreamThreads + tid;
-            if (at >= cnt) break;
-            if (w != 0.0f) {
+        for (int i = 0; i < 4; ++i) {
+          if (some) {
 #pragma unroll
-              for (int p = 0; p < E / 2; ++p) {
-                const float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
-                set_pair<T>(v[i], p, __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), k2));
-              }
-            } else {
-              v[i] = Vec{{0u, 0u, 0u, 0u}};
-            }
-            store_row_vec(out, first_element<T>(sh, c + at), a.V, aligned, v[i]);
-          }
-          held.next();
-        }
-        // The elements at the entries, over the dense part that this warp has written. The entries of
-        // one id are all of one warp, which adds them together lane by lane.
-        __syncwarp();
-        if (w != 0.0f) {
-          for (int k0 = 0; k0 < a.K; k0 += 32) {
-            const int mine = k0 + lane < a.K ? n.id[k0 + lane] : -1;
-            const int64_t vec = (static_cast<int64_t>(mine) + sh.shift) / E - sh.begin;  // of the share's
-            const bool own = mine >= 0 && vec >= 0 && vec < sh.end - sh.begin &&
-                             (static_cast<int>(vec) % kStreamThreads) >> 5 == warp;
-            for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo != 0; todo &= todo - 1) {
-              const int from = __ffs(todo) - 1;
-              const int id = __shfl_sync(0xffffffffu, mine, from);
-              const int at = __shfl_sync(0xffffffffu, static_cast<int>(vec), from);
-              float q = 0.f;
-              for (int j = lane; j < a.K; j += 32)
-                if (n.id[j] == id) q += ex2_approx(n.td[j] * c2);
-              q = warp_sum(q);
-              int stage = begin.stage + at / kStageVecs;
-              if (stage >= kStages) stage -= kStages;
-              const T* p = reinterpret_cast<const T*>(dyn + stage * kStageBytes + (at % kStageVecs) * 16);
-              const float x = (to_f(p[(id + sh.shift) % E]) - g.me) * c2;
-              if (lane == 0) out[id] = from_f<T>(fmaf(g.dense, ex2_approx(x), -g.sparse * q));
-            }
+            for (int p = 0; p < E / 2; ++p) set_pair<T>(v[i], p, dense_pair(g, vec_pair<T>(v[i], p)));
+          } else {
+            v[i] = Vec{{0u, 0u, 0u, 0u}};
           }
         }
-        __syncwarp();
-        if (lane == 0) {
-          Place p = begin;
-          for (int c = sh.begin; c < sh.end; c += kStageVecs, p.next()) mbar_arrive(&sm.ring.empty[p.stage]);
+        T* to = out + e0 + tid * E;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = i * kStreamThreads + tid;
+          if (at >= cnt) break;
+          if (inner) st_vec(to + i * kStreamThreads * E, v[i]);
+          else store_row_vec(out, e0 + at * E, a.V, aligned, v[i]);
         }
+        held.next();
       }
-      if (rank == 0 && warp == 0) {
-        // sum q (ln q - ln p) = sum (q / tau) (td - (z - max z)) - ln sq + ln s: a mask of the type's
-        // lowest value leaves the range of fp32 only where the loss does
-        const float me = finite_or_0(m), f = a.inv_temp / sq;
-        float l = 0.f;
-        for (int k = lane; k < a.K; k += 32) {
-          const float e = ex2_approx(n.td[k] * c2);
-          if (n.id[k] >= 0 && e != 0.0f) l = fmaf(e * f, n.td[k] - (n.z[k] - me), l);
-        }
-        l = warp_sum(l);
-        if (lane == 0) {
-          a.stats[2 * r] = m;
-          a.stats[2 * r + 1] = s;
-          a.loss[r] = sq == 0.0f ? 0.0f : l + ((s == 0.0f ? 0.0f : logf(s)) - logf(sq));
+      // The elements at the entries, over the dense part that this warp has written. The entries of one id
+      // are all of one warp, which adds them together lane by lane.
+      __syncwarp();
+      if (some) {
+        for (int k0 = 0; k0 < a.K; k0 += 32) {
+          const int mine = k0 + lane < a.K ? n.id[k0 + lane] : -1;
+          const int vec = (mine + sh.shift) / E - sh.begin;  // of the share's
+          const bool own = mine >= 0 && vec >= 0 && vec < sh.end - sh.begin && (vec % kStreamThreads) >> 5 == warp;
+          for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo != 0; todo &= todo - 1) {
+            const int from = __ffs(todo) - 1;
+            const int id = __shfl_sync(0xffffffffu, mine, from);
+            const int at = __shfl_sync(0xffffffffu, vec, from);
+            float q = 0.f;
+            for (int j = lane; j < a.K; j += 32)
+              if (n.id[j] == id) q += ex2_approx(n.td[j] * c2);
+            q = warp_sum(q);
+            int stage = begin.stage + at / kStageVecs;
+            if (stage >= kStages) stage -= kStages;
+            const T* p = reinterpret_cast<const T*>(dyn + stage * kStageBytes + (at % kStageVecs) * 16);
+            const float x = fmaf(to_f(p[(id + sh.shift) % E]), g.k.c, -g.k.ref);
+            if (lane == 0) out[id] = from_f<T>(fmaf(g.dense, ex2_approx(x), -g.sparse * q));
+          }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.spare[b]);
+      if (lane == 0) {
+        Place p = begin;
+        for (int c = sh.begin; c < sh.end; c += kStageVecs, p.next()) mbar_arrive(&sm.ring.empty[p.stage]);
+        mbar_arrive(&sm.spare[b]);
+      }
     };
     int64_t it = 0;
     for (int64_t r = first; r < a.T; r += step, ++it) {
@@ -455,7 +476,9 @@ __global__ void __launch_bounds__(kRowThreads, 3) kd_bwd_kernel(const KdArgs a, 
   const float ts = warp_sum(exp_entries(a, warps_max(sm.tmax), n, sm));
   if (lane == 0) sm.tsum[warp] = ts;
   __syncthreads();
-  const Gradient g = make_gradient(a, a.stats_in[2 * r], a.stats_in[2 * r + 1], w, warps_sum(sm.tsum));
+  const float m = a.stats_in[2 * r];
+  const Scale k = scale_of(m, a.inv_temp * kLog2e);
+  const Gradient g = make_gradient(a, k, sum_at_ref(a.stats_in[2 * r + 1], m, k), w, warps_sum(sm.tsum));
   for (int c = sh.begin; c < sh.end; c += kChunk) {
     if (c > sh.begin) load_chunk<T, false>(v, z, a.V, sh, c);
     store_dense(v, g, out, a.V, aligned, sh, c);

@@ -119,15 +119,16 @@ __global__ void __launch_bounds__(kRowThreads, 3) tlp_fwd_kernel(const TlpFwdArg
     float lm = sm.lanes[0][lane];
 #pragma unroll
     for (int i = 1; i < kRowWarps; ++i) lm = fmaxf(lm, sm.lanes[i][lane]);
-    const float mn = fmaxf(m, warp_max(lm)), me = finite_or_0(mn);
+    const float mn = fmaxf(m, warp_max(lm));
+    const Scale kn = scale_of(mn, c2);
 
     float2 s2 = make_float2(0.f, 0.f), w2 = s2;
-    const float2 nm2 = make_float2(-me, -me), cc2 = make_float2(c2, c2);
+    const float2 nref = make_float2(-kn.ref, -kn.ref), kc = make_float2(kn.c, kn.c);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
 #pragma unroll
       for (int p = 0; p < E / 2; ++p) {
-        float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
+        float2 x = __ffma2_rn(vec_pair<T>(v[i], p), kc, nref);
         x = make_float2(at_least(x.x), at_least(x.y));
         const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
         s2 = __fadd2_rn(s2, e);
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) tlp_fwd_kernel(const TlpFwdArg
     __syncthreads();
 
     // join the sums with the earlier chunks'
-    const float x0 = part_shift(m, mn, c2), f = ex2_approx(x0);
+    const float x0 = ref_shift(m, scale_of(m, c2), mn, kn, c2), f = ex2_approx(x0);
     w = f * fmaf(s, x0, w);
     s *= f;
     float cs = 0.f, cw = 0.f;
@@ -256,11 +257,12 @@ __global__ void __launch_bounds__(kRowThreads, 3) tlp_fwd_kernel(const TlpFwdArg
     if (rank != 0) return;
     m = neg_inf();
     for (int i = 0; i < S; ++i) m = fmaxf(m, sm.part[i].x);
+    const Scale k = scale_of(m, c2);
     s = w = 0.f;
     nbest = 0;
     for (int i = 0; i < S; ++i) {
       const float4 p = sm.part[i];
-      const float x0 = part_shift(p.x, m, c2), f = ex2_approx(x0);
+      const float x0 = ref_shift(p.x, scale_of(p.x, c2), m, k, c2), f = ex2_approx(x0);
       s = fmaf(f, p.y, s);
       w = fmaf(f, fmaf(p.y, x0, p.z), w);
       nbest += __float_as_int(p.w);
@@ -282,12 +284,15 @@ __global__ void __launch_bounds__(kRowThreads, 3) tlp_fwd_kernel(const TlpFwdArg
     __syncthreads();
   }
 
+  // H = ln s - (1/s) sum 2^x x ln 2, with s and x of one reference; then s at the maximum
+  const float ent = s == 0.0f ? 0.0f : logf(s) - w * kLn2 / s;
+  s = sum_at_max(s, m, scale_of(m, c2));
   const float me = finite_or_0(m), log_s = logf(s);
   auto logp_of = [&](float x) { return x == neg_inf() && s == s ? neg_inf() : (x - me) * a.inv_temp - log_s; };
   if (tid == 0) {
     a.stats[2 * r] = m;
     a.stats[2 * r + 1] = s;
-    a.entropy[r] = s == 0.0f ? 0.0f : log_s - w * kLn2 / s;
+    a.entropy[r] = ent;
     if (a.targets != nullptr) {
       const int64_t t = load_index(a.targets, r, a.wide);
       a.logp[r] = t == a.ignore ? 0.0f
@@ -320,21 +325,22 @@ __global__ void __launch_bounds__(kRowThreads) tlp_bwd_kernel(const TlpBwdArgs a
   T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
   const Share sh = share_of(z, a.V, split.per, static_cast<int>(blockIdx.x % split.S));
   const bool aligned = row_shift(out) == sh.shift;
-  const float m = a.stats[2 * r], s = a.stats[2 * r + 1];
-  const float me = finite_or_0(m), c2 = a.inv_temp * kLog2e;
+  const float m = a.stats[2 * r];
+  const Scale k = scale_of(m, a.inv_temp * kLog2e);
+  const float s = sum_at_ref(a.stats[2 * r + 1], m, k);
   const int64_t t = a.targets != nullptr ? load_index(a.targets, r, a.wide) : a.ignore;
   const bool valid = t >= 0 && t < a.V;
   const float dl = t == a.ignore ? 0.0f : valid ? a.dlogp[r] : __int_as_float(0x7fc00000);
   const bool ent = a.dentropy != nullptr;
   const float dh = ent ? a.dentropy[r] : 0.0f;
-  // dz = -(p / tau) (dl + dh (ln p + H)) = 2^x (k0 + k1 x), x = (z - max) log2(e) / tau, and dl / tau
+  // dz = -(p / tau) (dl + dh (ln p + H)) = 2^x (k0 + k1 x), x as in scale_of, and dl / tau
   // more at the target
   const float inv_s = s == 0.0f ? 0.0f : 1.0f / s;
   const float scale = -inv_s * a.inv_temp;
   const float k0 = scale * (dl + (ent && s != 0.0f ? dh * (a.entropy[r] - logf(s)) : 0.0f));
   const float k1 = scale * dh * kLn2;
   const int64_t tt = t != a.ignore && valid && s != 0.0f ? t : -1;
-  const float2 nm2 = make_float2(-me, -me), cc2 = make_float2(c2, c2), k02 = make_float2(k0, k0);
+  const float2 nref = make_float2(-k.ref, -k.ref), kc = make_float2(k.c, k.c), k02 = make_float2(k0, k0);
   const float2 k12 = make_float2(k1, k1);
   for (int c = sh.begin; c < sh.end; c += kChunk) {
     Vec v[kVecs];
@@ -346,13 +352,13 @@ __global__ void __launch_bounds__(kRowThreads) tlp_bwd_kernel(const TlpBwdArgs a
       const int64_t e0 = first_element<T>(sh, g);
 #pragma unroll
       for (int p = 0; p < E / 2; ++p) {
-        float2 x = __fmul2_rn(__fadd2_rn(vec_pair<T>(v[i], p), nm2), cc2);
+        float2 x = __ffma2_rn(vec_pair<T>(v[i], p), kc, nref);
         x = make_float2(at_least(x.x), at_least(x.y));
         const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
         set_pair<T>(v[i], p, __fmul2_rn(e, __ffma2_rn(k12, x, k02)));
       }
       if (tt >= e0 && tt < e0 + E) {  // the target: formed anew, rounded once
-        const float x0 = at_least((to_f(z[tt]) - me) * c2);
+        const float x0 = at_least(fmaf(to_f(z[tt]), k.c, -k.ref));
         const float x = fmaf(dl, a.inv_temp, ex2_approx(x0) * fmaf(k1, x0, k0));
         const int at = static_cast<int>(tt - e0);
 #pragma unroll

@@ -193,6 +193,41 @@ __device__ __forceinline__ float at_least(float x) {
   return r;
 }
 
+// Exponents under a maximum m: x = fma(z, c, -ref) with c = log2(e) / tau and ref = m c rounded once, one
+// rounding for an element. Sums of 2^x belong to ref, not to m c: parts are joined by the difference of
+// their refs, and only the reported sum is moved to m itself. From |m c| = 2^30 on (a row of the type's
+// lowest value, for one) that rounding would be too large; there the next smaller logit's x is
+// below -32, so 2^x is 1 at the maximum and 0 elsewhere to all digits kept: c is then a power of two that
+// puts |m c| in [2^40, 2^41), exactly.
+struct Scale {
+  float c, ref;
+};
+__device__ __forceinline__ Scale scale_of(float m, float c) {
+  const float me = m == neg_inf() ? 0.0f : m;
+  Scale s{c, me * c};
+  if (!(fabsf(s.ref) < 1073741824.0f)) {
+    const int e = 294 - static_cast<int>((__float_as_uint(me) >> 23) & 0xffu);
+    s.c = __uint_as_float(static_cast<uint32_t>(min(max(e, 1), 254)) << 23);
+    s.ref = me * s.c;
+  }
+  return s;
+}
+// the exponent by which a sum under the maximum `part` is moved to the joint one (`s`, `joint`: their
+// scales); a part with no logit above -inf has a sum of 0 (or NaN)
+__device__ __forceinline__ float ref_shift(float part_max, const Scale& s, float joint_max, const Scale& joint,
+                                           float c) {
+  if (part_max == neg_inf()) return 0.0f;
+  const bool plain = fabsf(s.ref) < 1073741824.0f && fabsf(joint.ref) < 1073741824.0f;
+  return at_least(plain ? s.ref - joint.ref : part_max == joint_max ? 0.0f : (part_max - joint_max) * c);
+}
+// the sum of exp((z - m) / tau) from the sum of 2^x, and back
+__device__ __forceinline__ float sum_at_max(float s, float m, const Scale& k) {
+  return m == neg_inf() ? s : s * ex2_approx(-fmaf(m, k.c, -k.ref));
+}
+__device__ __forceinline__ float sum_at_ref(float s, float m, const Scale& k) {
+  return m == neg_inf() ? s : s * ex2_approx(fmaf(m, k.c, -k.ref));
+}
+
 // ---- clusters: a block of the cluster writes to, and only to, blocks that have started (the barrier's
 // first phase) and that wait for the second one before they read
 __device__ __forceinline__ void cluster_arrive() {
@@ -212,12 +247,6 @@ __device__ __forceinline__ void st_peer_f4(const float4* p, uint32_t rank, float
 }
 __device__ __forceinline__ void st_peer_u64(const uint64_t* p, uint32_t rank, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer_addr(p, rank)), "l"(v) : "memory");
-}
-
-// A part of a row under the row's maximum: the shift x = (part_max - joint_max) c of its exponents (c =
-// log2(e) / tau), by which its sum of 2^x is scaled. A part with no logit above -inf has a sum of 0.
-__device__ __forceinline__ float part_shift(float part_max, float joint_max, float c) {
-  return part_max == neg_inf() ? 0.0f : at_least((part_max - finite_or_0(joint_max)) * c);
 }
 
 }  // namespace row

@@ -125,19 +125,23 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
   }
 }
 
-// a computing thread's four vectors of a stage that holds n
+// a computing thread's four vectors of a stage that holds n; -inf past them
 template <typename T>
 __device__ __forceinline__ void read_stage(Vec (&v)[4], const unsigned char* stage, int n) {
+  const uint4* p = reinterpret_cast<const uint4*>(stage) + threadIdx.x;
+  if (n == kStageVecs) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 u = p[i * kStreamThreads];
+      v[i] = Vec{{u.x, u.y, u.z, u.w}};
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int at = i * kStreamThreads + static_cast<int>(threadIdx.x);
-    if (at < n) {
-      const uint4 u = reinterpret_cast<const uint4*>(stage)[at];
-      v[i] = Vec{{u.x, u.y, u.z, u.w}};
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[i].w[j] = Traits<T>::kNegInf;
-    }
+    uint4 u = make_uint4(Traits<T>::kNegInf, Traits<T>::kNegInf, Traits<T>::kNegInf, Traits<T>::kNegInf);
+    if (i * kStreamThreads + static_cast<int>(threadIdx.x) < n) u = p[i * kStreamThreads];
+    v[i] = Vec{{u.x, u.y, u.z, u.w}};
   }
 }
 
