@@ -154,16 +154,18 @@ __device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g,
 
 constexpr int kExtraWarps = 3;  // producer, teacher, joiner
 constexpr int kFwdThreads = kStreamThreads + 32 * kExtraWarps;
+constexpr int kStages = 6;      // of the ring
+constexpr int kRingBytes = kStages * kStageBytes;
 constexpr int kSlots = 4;       // exchange slots: a slot is written again four rows later
 constexpr int kShareStages = 2; // stages a row's share may hold: two rows' shares, and two stages ahead
 
 struct KdStream {
-  Ring ring;
+  Ring<kStages> ring;
   uint64_t joined[kSlots];  // the row's maxima and sums have come from all blocks
   uint64_t ready[2];        // the row's entries are in shared memory
   uint64_t spare[2];        // their readers are done with them
   uint64_t solved[2];       // the row's gradient constants are in shared memory
-  float2 part[kSlots][kMaxCluster][kStreamWarps];  // max and sum of every warp
+  float4 part[kSlots][kMaxCluster][kStreamWarps];  // every warp's sums (WarpSums::result)
   float2 note[kSlots];      // from the first block: its entries' logits have been read
   Gradient grad[2];
   float weight[2];
@@ -177,38 +179,92 @@ struct EntryArrays {
 };
 constexpr size_t kFwdSmem = kRingBytes + 2 * sizeof(EntryArrays);
 
-// one warp: row r's entries; with `gather` the student's logits at them
+// One warp takes the entries of row after row: the first kAhead of a row are loaded while the row before
+// is worked on.
+// They are kept as loaded, so that a load does not wait for the one before it.
+constexpr int kAhead = 128;
+struct EntryLoads {
+  int64_t id[kAhead / 32];
+  uint32_t t[kAhead / 32];
+};
+// the entries k0 .. k0 + kAhead - 1 of row r
+__device__ __forceinline__ void load_some(const KdArgs& a, int64_t r, int k0, EntryLoads& n) {
+  const int64_t at = r * a.K;
+  const int k = k0 + static_cast<int>(threadIdx.x & 31);
+  if (a.wide) {
+#pragma unroll
+    for (int i = 0; i < kAhead / 32; ++i)
+      if (k + 32 * i < a.K) n.id[i] = static_cast<const int64_t*>(a.ids)[at + k + 32 * i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kAhead / 32; ++i)
+      if (k + 32 * i < a.K) n.id[i] = static_cast<const uint32_t*>(a.ids)[at + k + 32 * i];
+  }
+  if (a.tdtype == 0) {
+#pragma unroll
+    for (int i = 0; i < kAhead / 32; ++i)
+      if (k + 32 * i < a.K) n.t[i] = static_cast<const uint32_t*>(a.teacher)[at + k + 32 * i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kAhead / 32; ++i)
+      if (k + 32 * i < a.K) n.t[i] = static_cast<const uint16_t*>(a.teacher)[at + k + 32 * i];
+  }
+}
+// what was loaded: ids, -1 for absent entries, and the teacher's and the student's logits
+struct EntryValues {
+  int id[kAhead / 32];
+  float t[kAhead / 32];
+  float z[kAhead / 32];
+};
 template <typename T>
-__device__ __forceinline__ void take_entries(const KdArgs& a, int64_t r, EntryArrays& n, bool gather, float& sq) {
+__device__ __forceinline__ void read_some(const KdArgs& a, const T* z, int k0, bool gather, const EntryLoads& n,
+                                          EntryValues& v) {
+  const int k = k0 + static_cast<int>(threadIdx.x & 31);
+  T x[kAhead / 32];
+#pragma unroll
+  for (int i = 0; i < kAhead / 32; ++i) {
+    const int64_t id = k + 32 * i >= a.K ? -1 : a.wide ? n.id[i] : static_cast<int32_t>(n.id[i]);
+    v.id[i] = id >= 0 && id < a.V ? static_cast<int>(id) : -1;
+    x[i] = from_f<T>(0.0f);
+    if (gather && v.id[i] >= 0) x[i] = z[v.id[i]];
+    const uint32_t u = n.t[i];
+    v.t[i] = v.id[i] < 0 ? neg_inf()
+             : a.tdtype == 0 ? __uint_as_float(u)
+             : a.tdtype == 1 ? __half2float(__ushort_as_half(static_cast<uint16_t>(u)))
+                             : __uint_as_float(u << 16);
+  }
+#pragma unroll
+  for (int i = 0; i < kAhead / 32; ++i) v.z[i] = to_f(x[i]);
+}
+// row r's entries, the first of them in `first`, -> shared memory; `gather`: with the student's logits.
+// Loads the first entries of row `next` into `first`. wait(): the arrays are free.
+template <typename T, typename Wait>
+__device__ __forceinline__ void take_entries(const KdArgs& a, int64_t r, int64_t next, EntryLoads& first,
+                                             EntryArrays& n, bool gather, float& sq, Wait wait) {
   const int lane = threadIdx.x & 31;
   const float c2 = a.inv_temp * kLog2e;
   const T* z = static_cast<const T*>(a.logits) + r * a.ld;
   float m = neg_inf();
-  for (int k0 = 0; k0 < a.K; k0 += 128) {  // four loads of a kind in flight
-    int64_t id[4];
-    float t[4], x[4];
+  EntryLoads now = first;
+  EntryValues v;
+  if (next < a.T) load_some(a, next, 0, first);
+  read_some(a, z, 0, gather, now, v);
+  wait();
+  for (int k0 = 0;;) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kAhead / 32; ++i) {
       const int k = k0 + i * 32 + lane;
-      id[i] = k < a.K ? load_index(a.ids, r * a.K + k, a.wide) : -1;
-      t[i] = k < a.K ? load_any(a.teacher, r * a.K + k, a.tdtype) : neg_inf();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool there = id[i] >= 0 && id[i] < a.V;
-      if (!there) id[i] = -1, t[i] = neg_inf();
-      x[i] = gather && there ? to_f(z[id[i]]) : 0.0f;
-      m = fmaxf(m, t[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = k0 + i * 32 + lane;
+      m = fmaxf(m, v.t[i]);
       if (k < a.K) {
-        n.id[k] = static_cast<int>(id[i]);
-        n.td[k] = t[i];
-        n.z[k] = x[i];
+        n.id[k] = v.id[i];
+        n.td[k] = v.t[i];
+        n.z[k] = v.z[i];
       }
     }
+    k0 += kAhead;
+    if (k0 >= a.K) break;
+    load_some(a, r, k0, now);
+    read_some(a, z, k0, gather, now, v);
   }
   const float me = finite_or_0(warp_max(m));
   float s = 0.f;
@@ -230,7 +286,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank());
   const int64_t first = blockIdx.x / S, step = gridDim.x / S;
-  const uint32_t bytes = static_cast<uint32_t>(S * kStreamWarps * sizeof(float2) + sizeof(float2));
+  const uint32_t bytes = static_cast<uint32_t>(S * kStreamWarps * sizeof(float4) + sizeof(float2));
   if (tid == 0) {
     ring_init(sm.ring);
     for (int i = 0; i < kSlots; ++i) mbar_init(&sm.joined[i], 1);
@@ -251,15 +307,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
   if (warp == kStreamWarps) {
     produce_rows<T>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, sm.ring, wait);
   } else if (warp == kStreamWarps + 1) {
+    EntryLoads ahead;
+    load_some(a, first, 0, ahead);
     int64_t it = 0;
     for (int64_t r = first; r < a.T; r += step, ++it) {
       const int b = static_cast<int>(it & 1), slot = static_cast<int>(it & (kSlots - 1));
-      wait(&sm.spare[b], static_cast<uint32_t>((it >> 1) & 1) ^ 1u);
+      const float w = kGrad ? a.weight[r] : 0.0f;
       float sq;
-      take_entries<T>(a, r, entries[b], rank == 0, sq);
+      take_entries<T>(a, r, r + step, ahead, entries[b], rank == 0, sq,
+                      [&]() { wait(&sm.spare[b], static_cast<uint32_t>((it >> 1) & 1) ^ 1u); });
       if (lane == 0) {
         sm.sq[b] = sq;
-        if (kGrad) sm.weight[b] = a.weight[r];
+        sm.weight[b] = w;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.ready[b]);
@@ -274,14 +333,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       const int b = static_cast<int>(it & 1), slot = static_cast<int>(it & (kSlots - 1));
       wait.cluster(&sm.joined[slot], static_cast<uint32_t>((it / kSlots) & 1));
       if (lane == 0) mbar_arrive_expect_tx(&sm.joined[slot], bytes);
-      const float2* part = &sm.part[slot][0][0];
-      float m = neg_inf(), s = 0.f;
+      // lane by lane (up to four parts each), then the lanes
+      const float4* part = &sm.part[slot][0][0];
+      float m = neg_inf(), s = 0.f, top = neg_inf();
       for (int i = lane; i < S * kStreamWarps; i += 32) m = fmaxf(m, part[i].x);
       m = warp_max(m);
       const Scale k = scale_of(m, c2);
-      for (int i = lane; i < S * kStreamWarps; i += 32)
-        s = fmaf(ex2_approx(ref_shift(part[i].x, scale_of(part[i].x, c2), m, k, c2)), part[i].y, s);
+      for (int i = lane; i < S * kStreamWarps; i += 32) {
+        const float4 p = part[i];
+        s = fmaf(ex2_approx(ref_shift(p.x, scale_of(p.x, c2), m, k, c2)), p.y, s);
+        top = fmaxf(top, p.w);
+      }
       s = warp_sum(s);
+      top = warp_max(top);
       wait(&sm.ready[b], static_cast<uint32_t>((it >> 1) & 1));
       const float sq = sm.sq[b];
       if (lane == 0) {
@@ -292,7 +356,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
         // sum q (ln q - ln p) = sum (q / tau) (td - (z - max z)) - ln sq + ln s: a mask of the type's
         // lowest value leaves the range of fp32 only where the loss does
         const EntryArrays& n = entries[b];
-        const float me = finite_or_0(m), f = a.inv_temp / sq;
+        const float me = finite_or_0(top), f = a.inv_temp / sq;
         float l = 0.f;
         for (int i = lane; i < a.K; i += 32) {
           const float e = ex2_approx(n.td[i] * c2);
@@ -300,8 +364,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
         }
         l = warp_sum(l);
         if (lane == 0) {
-          s = sum_at_max(s, m, k);
-          a.stats[2 * r] = m;
+          s = sum_at_max(s, top, k);
+          a.stats[2 * r] = top;
           a.stats[2 * r + 1] = s;
           a.loss[r] = sq == 0.0f ? 0.0f : l + ((s == 0.0f ? 0.0f : logf(s)) - logf(sq));
         }
@@ -310,43 +374,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       if (lane == 0) mbar_arrive(&sm.spare[b]);
     }
   } else {
-    Place in, held;  // the next stage to read, and (with a gradient) the first stage of the row before
+    Place<kStages> in, held;  // the next stage to read, and (with a gradient) the first stage of the row before
     // max and sum of the warp's part of row r, sent to every block
     auto sums = [&](int64_t r, int slot) {
       const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
-      float m = neg_inf();
-      Scale k = scale_of(m, c2);
-      float2 s2 = make_float2(0.f, 0.f);
+      WarpSums<T, false> sum(c2);
       for (int at = sh.begin; at < sh.end; at += kStageVecs) {
         Vec v[4];
         wait(&sm.ring.full[in.stage], in.parity);
         read_stage<T>(v, dyn + in.stage * kStageBytes, min(sh.end - at, kStageVecs));
-        const float mn = fmaxf(m, warp_max(fmaxf(fmaxf(vec_max<T>(v[0]), vec_max<T>(v[1])),
-                                                 fmaxf(vec_max<T>(v[2]), vec_max<T>(v[3])))));
-        if (mn > m) {
-          const Scale kn = scale_of(mn, c2);
-          const float f = ex2_approx(ref_shift(m, k, mn, kn, c2));
-          s2 = __fmul2_rn(s2, make_float2(f, f));
-          m = mn;
-          k = kn;
-        }
-        const float2 c = make_float2(k.c, k.c), ref = make_float2(-k.ref, -k.ref);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-          for (int p = 0; p < E / 2; ++p) {
-            const float2 x = __ffma2_rn(vec_pair<T>(v[i], p), c, ref);
-            s2 = __fadd2_rn(s2, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
-          }
-        }
+        sum.add(v, c2, false);
         if (!kGrad) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.ring.empty[in.stage]);
         }
         in.next();
       }
-      const float s = warp_sum(s2.x + s2.y);
-      if (lane < S) send_f2(&sm.part[slot][rank][warp], &sm.joined[slot], static_cast<uint32_t>(lane), m, s);
+      const float4 p = sum.result();
+      if (lane < S) send_f4(&sm.part[slot][rank][warp], &sm.joined[slot], static_cast<uint32_t>(lane), p);
       __syncwarp();
     };
     // The gradient of row r, the it-th of the block. Without a gradient only the wait is left: a warp is
@@ -362,7 +407,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       const EntryArrays& n = entries[b];
       const Gradient g = sm.grad[b];
       const bool some = sm.weight[b] != 0.0f;
-      const Place begin = held;
+      const Place<kStages> begin = held;
       for (int c = sh.begin; c < sh.end; c += kStageVecs) {
         Vec v[4];
         const int cnt = min(sh.end - c, kStageVecs);
@@ -414,7 +459,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       }
       __syncwarp();
       if (lane == 0) {
-        Place p = begin;
+        Place<kStages> p = begin;
         for (int c = sh.begin; c < sh.end; c += kStageVecs, p.next()) mbar_arrive(&sm.ring.empty[p.stage]);
         mbar_arrive(&sm.spare[b]);
       }
@@ -437,8 +482,8 @@ cudaError_t launch_fwd(const KdArgs& a, Split split, cudaStream_t stream) {
   static std::mutex mu;  // guards the occupancy cache
   static StreamCache cache;
   std::lock_guard<std::mutex> lk(mu);
-  return launch_stream(kd_fwd_kernel<T, kGrad>, cache, kFwdThreads, kFwdSmem, a.T, split.S, stream, a, split,
-                       status_word_ptr());
+  return launch_stream(kd_fwd_kernel<T, kGrad>, cache, kFwdThreads, kFwdSmem, a.T, split.S, false, stream, a,
+                       split, status_word_ptr());
 }
 template <bool kGrad>
 cudaError_t launch_fwd_any(const KdArgs& a, int dtype, Split split, cudaStream_t stream) {

@@ -6,14 +6,17 @@
 // Logits of -inf have probability 0; a row with no other logit has s = 0, H = 0, logp = -inf, no
 // gradient. A NaN or +inf logit makes its row's results NaN.
 //
-// Forward: bound by HBM (V elements read a row). A cluster of S blocks takes a row, each block its share in
-// registers (32 KB), so the row is read once: the block's maximum, then the two sums under it in one
-// pass over the registers. The alternatives come from the same registers: the block's 32 lane columns
-// have 32 maxima, the k-th largest of which is a bound that at least k logits reach, so the few logits
-// at or above it (about k + k^2 / 64 of them) are collected and ranked against one another. The
-// blocks send (max, sums, best keys) to the first one, which joins them in the blocks' order.
+// Forward: bound by HBM (V elements read a row). A persistent kernel streams rows through shared memory
+// (vocab_stream.cuh); S blocks of a cluster share a row only when there are too few rows for the SMs.
+// The 16 computing warps keep (max, sum 2^x, sum 2^x x) and each thread its best logit and the run of four
+// vectors that has it. Four more warps finish rows in turn, under the work on the next ones: they join
+// the sums, and select the alternatives from the threads' bests. The 32 lane columns' bests have a k-th
+// largest, which at least k logits reach; the few threads with a best at or above it (about k + k^2 / 64)
+// are looked through again (their runs come from L2), and the logits found are ranked against one another.
+#include <mutex>
+
 #include "swg_launch.h"
-#include "vocab_rows.cuh"
+#include "vocab_stream.cuh"
 
 namespace swg {
 namespace {
@@ -21,300 +24,279 @@ namespace {
 using namespace row;
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kCand = 1024;  // candidates collected, at most (else the slower exact search)
+constexpr int kStages = 5;      // of the ring
+constexpr int kRingBytes = kStages * kStageBytes;
+constexpr int kSelectors = 4;   // warps that finish rows
+constexpr int kFwdThreads = kStreamThreads + 32 * (1 + kSelectors);
+constexpr int kCand = 512;      // candidates held; more are cut to the best before the search goes on
 
-struct TlpSmem {
-  float lanes[kRowWarps][32];
-  float2 sums[kRowWarps];
-  uint64_t rounds[2][kRowWarps];
-  uint64_t cand[kCand + kMaxTop];
-  uint64_t best[kMaxTop];
-  float4 part[kMaxCluster];  // of the first block: the blocks' max, sum 2^x, sum 2^x x, number of keys
-  uint64_t part_best[kMaxCluster][kMaxTop];
-  int ncand;
+struct TlpSync {
+  Ring<kStages> ring;
+  uint64_t told[kSelectors];   // the computing warps have written a row's results
+  uint64_t taken[kSelectors];  // the selector has read them
+  uint64_t sent;               // first block: the other blocks' results have come
 };
+// one selector's, behind the ring in dynamic shared memory
+struct Finish {
+  uint64_t keys[kStreamThreads];         // a thread's best logit and its run, 0 for none
+  uint64_t cand[kCand];
+  uint64_t best[kMaxCluster][kMaxTop];   // by block; sorted, the better first
+  float4 block[kMaxCluster];             // the blocks' sums (WarpSums::result)
+  float4 part[kStreamWarps];             // the computing warps'
+  uint16_t who[kStreamThreads];          // threads to look through again
+  int count;
+};
+constexpr size_t kFwdSmem = kRingBytes + kSelectors * sizeof(Finish);
 
-// The rare cases of the selection read the chunk at c again (from L2) instead of holding it in registers
-// beside the sums.
-//
-// One warp: the first `need` logits equal to `bound` in index order -> cand; returns how many there are
-// (at most need).
-template <typename T>
-__device__ __noinline__ int collect_equal(const T* z, int64_t V, const Share& sh, int c, float bound, int need,
-                                          uint64_t* cand) {
+// One warp: the `top` best of cand[0 .. n) -> best, in order; returns how many there are.
+__device__ __forceinline__ int rank_candidates(const uint64_t* cand, int n, int top, uint64_t* best) {
+  __syncwarp();
+  for (int t = threadIdx.x & 31; t < n; t += 32) {
+    const uint64_t key = cand[t];
+    int place = 0;
+    for (int j = 0; j < n; ++j) place += cand[j] > key ? 1 : 0;
+    if (place < top) best[place] = key;
+  }
+  __syncwarp();
+  return n < top ? n : top;
+}
+
+// One warp: the `top` best logits above -inf of a share, from the threads' bests -> best. done(): the
+// threads' bests have been read.
+template <typename T, typename Done>
+__device__ __forceinline__ int select_best(const T* z, int64_t V, const Share& sh, int top, Finish& f, uint64_t* best,
+                                           Done done) {
   constexpr int E = Traits<T>::E;
   const int lane = threadIdx.x & 31;
-  const int end = min(sh.end, c + kChunk);
-  int found = 0;
-  for (int g0 = c; g0 < end && found < need; g0 += 32) {
-    const int64_t e0 = first_element<T>(sh, g0 + lane);
-    uint32_t hits = 0;
-    if (g0 + lane < end) {
-      const Vec v = load_row_vec<T, true>(z, e0, V);
+  uint64_t column = 0;
 #pragma unroll
-      for (int p = 0; p < E / 2; ++p) {
-        const float2 x = vec_pair<T>(v, p);
-        hits |= (x.x == bound ? 1u : 0u) << (2 * p) | (x.y == bound ? 2u : 0u) << (2 * p);
+  for (int i = 0; i < kStreamWarps; ++i) {
+    const uint64_t k = f.keys[i * 32 + lane];
+    column = k > column ? k : column;
+  }
+  int above = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const uint64_t o = __shfl_sync(0xffffffffu, column, j);
+    above += o > column || (o == column && j < lane) ? 1 : 0;
+  }
+  const uint64_t bound = __shfl_sync(0xffffffffu, column, __ffs(__ballot_sync(0xffffffffu, above == top - 1)) - 1);
+  int threads = 0;
+#pragma unroll
+  for (int i = 0; i < kStreamWarps; ++i) {
+    const uint64_t k = f.keys[i * 32 + lane];
+    const bool good = k != 0 && k >= bound;
+    const uint32_t all = __ballot_sync(0xffffffffu, good);
+    if (good) f.who[threads + __popc(all & ((1u << lane) - 1u))] = static_cast<uint16_t>(i * 32 + lane);
+    threads += __popc(all);
+  }
+  if (lane == 0) f.count = 0;
+  __syncwarp();
+  done();
+  // a logit reaches the bound if it is larger, or equal and in the same run or before it
+  float least = bound != 0 ? rank_logit(bound) : neg_inf();
+  uint64_t least_key =
+      bound != 0 ? rank_key(least, static_cast<uint32_t>(first_element<T>(sh, sh.begin + 4 * static_cast<int>(rank_index(bound)) + 4) - 1)) : 0;
+  const int stages = (sh.end - sh.begin + kStageVecs - 1) / kStageVecs, items = threads * stages;
+  for (int i0 = 0; i0 < items; i0 += 32) {  // a run for each lane
+    Vec v[4];
+    const int i = i0 + lane, q = i / stages;
+    const int g = i < items ? sh.begin + (i - q * stages) * kStageVecs + 4 * f.who[q] : sh.end;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (g + u < sh.end) {
+        v[u] = load_row_vec<T, true>(z, first_element<T>(sh, g + u), V);
+      } else {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[u].w[w] = Traits<T>::kNegInf;
       }
     }
-    int upto = __popc(hits);  // of the lanes up to this one
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += t;
-    }
-    for (int at = found + upto - __popc(hits); hits != 0 && at < need; ++at, hits &= hits - 1)
-      cand[at] = rank_key(bound, static_cast<uint32_t>(e0) + __ffs(hits) - 1);
-    found += __shfl_sync(0xffffffffu, upto, 31);
-  }
-  return found < need ? found : need;
-}
-// the thread's best key below `below` among its logits above -inf, 0 if there is none
-template <typename T>
-__device__ __noinline__ uint64_t best_below(const T* z, int64_t V, const Share& sh, int c, uint64_t below) {
-  constexpr int E = Traits<T>::E;
-  const int end = min(sh.end, c + kChunk);
-  uint64_t best = 0;
-  for (int g = c + static_cast<int>(threadIdx.x); g < end; g += kRowThreads) {
-    const int64_t e0 = first_element<T>(sh, g);
-    const Vec v = load_row_vec<T, true>(z, e0, V);
-#pragma unroll
-    for (int p = 0; p < E / 2; ++p) {
-      const float2 x = vec_pair<T>(v, p);
-      const uint32_t at = static_cast<uint32_t>(e0 + 2 * p);
-      const uint64_t k0 = rank_key(x.x, at), k1 = rank_key(x.y, at + 1);
-      if (x.x > neg_inf() && k0 < below && k0 > best) best = k0;
-      if (x.y > neg_inf() && k1 < below && k1 > best) best = k1;
-    }
-  }
-  return best;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 3) tlp_fwd_kernel(const TlpFwdArgs a, int64_t row0, Split split) {
-  constexpr int E = Traits<T>::E;
-  __shared__ TlpSmem sm;
-  const int S = split.S;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  if (S > 1) cluster_arrive();
-  const int64_t r = row0 + blockIdx.x / S;
-  const T* z = static_cast<const T*>(a.logits) + r * a.ld;
-  const Share sh = share_of(z, a.V, split.per, rank);
-  const float c2 = a.inv_temp * kLog2e;
-
-  // What the block has seen, the same in every thread: max, sum 2^x and sum 2^x x with
-  // x = (z - max) log2(e) / tau, number of best keys.
-  float m = neg_inf(), s = 0.f, w = 0.f;
-  int nbest = 0;
-  for (int c = sh.begin; c < sh.end; c += kChunk) {
-    Vec v[kVecs];
-    load_chunk<T, true>(v, z, a.V, sh, c);
-    float tm = neg_inf();
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) tm = fmaxf(tm, vec_max<T>(v[i]));
-    sm.lanes[warp][lane] = tm;
-    if (tid == 0) sm.ncand = 0;
-    __syncthreads();
-    float lm = sm.lanes[0][lane];
-#pragma unroll
-    for (int i = 1; i < kRowWarps; ++i) lm = fmaxf(lm, sm.lanes[i][lane]);
-    const float mn = fmaxf(m, warp_max(lm));
-    const Scale kn = scale_of(mn, c2);
-
-    float2 s2 = make_float2(0.f, 0.f), w2 = s2;
-    const float2 nref = make_float2(-kn.ref, -kn.ref), kc = make_float2(kn.c, kn.c);
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-#pragma unroll
-      for (int p = 0; p < E / 2; ++p) {
-        float2 x = __ffma2_rn(vec_pair<T>(v[i], p), kc, nref);
-        x = make_float2(at_least(x.x), at_least(x.y));
-        const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-        s2 = __fadd2_rn(s2, e);
-        w2 = __ffma2_rn(e, x, w2);
+    for (int u = 0; u < 4; ++u) {
+      int n = f.count;
+      if (n > kCand - 32 * E) {
+        // the list could overflow: only the best stay, and the worst of them is the new bound
+        n = rank_candidates(f.cand, n, top, best);
+        for (int t = lane; t < n; t += 32) f.cand[t] = best[t];
+        if (n == top) {
+          least_key = best[top - 1];
+          least = rank_logit(least_key);
+        }
+        if (lane == 0) f.count = n;
+        __syncwarp();
       }
-    }
-    const float ws = warp_sum(s2.x + s2.y), ww = warp_sum(w2.x + w2.y);
-    if (lane == 0) sm.sums[warp] = make_float2(ws, ww);
-
-    float bound = neg_inf(), kept = neg_inf();
-    // the thread's logits at or above the bound (strict: above it) and above `kept` -> the candidates
-    auto collect = [&](bool strict) {
-      auto good = [&](float x) { return (strict ? x > bound : x >= bound) && x > kept; };
-      if (!good(tm)) return;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        if (!good(vec_max<T>(v[i]))) continue;
-        const uint32_t e0 = static_cast<uint32_t>(first_element<T>(sh, c + i * kRowThreads + tid));
+      const float vm = vec_max<T>(v[u]);
+      if (vm >= least && vm > neg_inf()) {
+        const uint32_t e0 = static_cast<uint32_t>(first_element<T>(sh, g + u));
 #pragma unroll
         for (int p = 0; p < E / 2; ++p) {
-          const float2 x = vec_pair<T>(v[i], p);
-          if (good(x.x)) {
-            const int n = atomicAdd(&sm.ncand, 1);
-            if (n < kCand) sm.cand[n] = rank_key(x.x, e0 + 2 * p);
-          }
-          if (good(x.y)) {
-            const int n = atomicAdd(&sm.ncand, 1);
-            if (n < kCand) sm.cand[n] = rank_key(x.y, e0 + 2 * p + 1);
-          }
+          const float2 x = vec_pair<T>(v[u], p);
+          const uint64_t k0 = rank_key(x.x, e0 + 2 * p), k1 = rank_key(x.y, e0 + 2 * p + 1);
+          if (x.x > neg_inf() && k0 >= least_key) f.cand[atomicAdd(&f.count, 1)] = k0;
+          if (x.y > neg_inf() && k1 >= least_key) f.cand[atomicAdd(&f.count, 1)] = k1;
         }
       }
-    };
-    if (a.top > 0) {
-      // the top-th largest of the lane columns' maxima
-      int above = 0;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float o = __shfl_sync(0xffffffffu, lm, j);
-        above += (o > lm || (o == lm && j < lane)) ? 1 : 0;
-      }
-      const uint32_t at = __ballot_sync(0xffffffffu, above == a.top - 1);
-      bound = __shfl_sync(0xffffffffu, lm, __ffs(at) - 1);
-      // later logits that only equal the worst one kept come after it
-      kept = nbest == a.top ? rank_logit(sm.best[a.top - 1]) : neg_inf();
-      collect(false);
-    }
-    __syncthreads();
-
-    // join the sums with the earlier chunks'
-    const float x0 = ref_shift(m, scale_of(m, c2), mn, kn, c2), f = ex2_approx(x0);
-    w = f * fmaf(s, x0, w);
-    s *= f;
-    float cs = 0.f, cw = 0.f;
-#pragma unroll
-    for (int i = 0; i < kRowWarps; ++i) {
-      const float2 t = sm.sums[i];
-      cs += t.x;
-      cw += t.y;
-    }
-    s += cs;
-    w += cw;
-    m = mn;
-
-    if (a.top > 0) {
-      int n = sm.ncand;
-      if (n > kCand) {
-        // a plateau at the bound: the logits above it, then the first ones equal to it
-        __syncthreads();
-        if (tid == 0) sm.ncand = 0;
-        __syncthreads();
-        collect(true);
-        __syncthreads();
-        n = sm.ncand;
-        if (n < a.top) {
-          __syncthreads();
-          if (warp == 0 && bound > kept) {
-            const int more = collect_equal(z, a.V, sh, c, bound, a.top - n, sm.cand + n);
-            if (lane == 0) sm.ncand = n + more;
-          }
-          __syncthreads();
-          n = sm.ncand;
-        }
-      }
-      if (n > kCand) {
-        // the best logits in few lane columns: one round for each of the best, in which only the thread
-        // that had it looks through its logits again
-        uint64_t mine = best_below(z, a.V, sh, c, ~0ull);
-        for (n = 0; n < a.top; ++n) {
-          const uint64_t wm = warp_max(mine);
-          if (lane == 0) sm.rounds[n & 1][warp] = wm;
-          __syncthreads();
-          uint64_t b = 0;
-#pragma unroll
-          for (int i = 0; i < kRowWarps; ++i) b = sm.rounds[n & 1][i] > b ? sm.rounds[n & 1][i] : b;
-          if (b == 0) break;
-          if (mine == b) {
-            sm.cand[n] = b;
-            mine = best_below(z, a.V, sh, c, b);
-          }
-        }
-        __syncthreads();
-      }
-      if (nbest > 0) {
-        if (tid < nbest) sm.cand[n + tid] = sm.best[tid];
-        n += nbest;
-        __syncthreads();
-      }
-      for (int t = tid; t < n; t += kRowThreads) {
-        const uint64_t key = sm.cand[t];
-        int place = 0;
-        for (int j = 0; j < n; ++j) place += sm.cand[j] > key ? 1 : 0;
-        if (place < a.top) sm.best[place] = key;
-      }
-      nbest = n < a.top ? n : a.top;
-    }
-    __syncthreads();
-  }
-
-  uint64_t* best = sm.best;
-  if (S > 1) {
-    cluster_wait();  // every block has started
-    if (tid == 0) st_peer_f4(&sm.part[rank], 0, make_float4(m, s, w, __int_as_float(nbest)));
-    if (tid < nbest) st_peer_u64(&sm.part_best[rank][tid], 0, sm.best[tid]);
-    cluster_arrive();
-    cluster_wait();
-    if (rank != 0) return;
-    m = neg_inf();
-    for (int i = 0; i < S; ++i) m = fmaxf(m, sm.part[i].x);
-    const Scale k = scale_of(m, c2);
-    s = w = 0.f;
-    nbest = 0;
-    for (int i = 0; i < S; ++i) {
-      const float4 p = sm.part[i];
-      const float x0 = ref_shift(p.x, scale_of(p.x, c2), m, k, c2), f = ex2_approx(x0);
-      s = fmaf(f, p.y, s);
-      w = fmaf(f, fmaf(p.y, x0, p.z), w);
-      nbest += __float_as_int(p.w);
-    }
-    if (a.top > 0) {
-      best = sm.cand;
-      const int mine = tid / kMaxTop, at = tid % kMaxTop;  // kMaxCluster * kMaxTop = kRowThreads
-      if (mine < S && at < __float_as_int(sm.part[mine].w)) {
-        const uint64_t key = sm.part_best[mine][at];
-        int place = 0;
-        for (int i = 0; i < S; ++i) {
-          const int n = __float_as_int(sm.part[i].w);
-          for (int j = 0; j < n; ++j) place += sm.part_best[i][j] > key ? 1 : 0;
-        }
-        if (place < a.top) best[place] = key;
-      }
-      nbest = nbest < a.top ? nbest : a.top;
-    }
-    __syncthreads();
-  }
-
-  // H = ln s - (1/s) sum 2^x x ln 2, with s and x of one reference; then s at the maximum
-  const float ent = s == 0.0f ? 0.0f : logf(s) - w * kLn2 / s;
-  s = sum_at_max(s, m, scale_of(m, c2));
-  const float me = finite_or_0(m), log_s = logf(s);
-  auto logp_of = [&](float x) { return x == neg_inf() && s == s ? neg_inf() : (x - me) * a.inv_temp - log_s; };
-  if (tid == 0) {
-    a.stats[2 * r] = m;
-    a.stats[2 * r + 1] = s;
-    a.entropy[r] = ent;
-    if (a.targets != nullptr) {
-      const int64_t t = load_index(a.targets, r, a.wide);
-      a.logp[r] = t == a.ignore ? 0.0f
-                  : (t >= 0 && t < a.V) ? logp_of(to_f(z[t])) : __int_as_float(0x7fc00000);
-    }
-    // fewer logits above -inf than wanted: all of them are in the list, the lowest other indices follow
-    for (uint32_t j = 0; nbest < a.top; ++j) {
-      bool there = false;
-      for (int i = 0; i < nbest; ++i) there = there || rank_index(best[i]) == j;
-      if (!there) best[nbest++] = rank_key(neg_inf(), j);
+      __syncwarp();
     }
   }
-  if (warp == 0) {
-    __syncwarp();
-    if (lane < a.top) {
-      a.top_idx[r * a.top + lane] = rank_index(best[lane]);
-      a.top_logp[r * a.top + lane] = logp_of(rank_logit(best[lane]));
-    }
-  }
+  return rank_candidates(f.cand, f.count, top, best);
 }
-static_assert(kMaxCluster * kMaxTop == kRowThreads, "one thread for each key of a cluster");
+static_assert(kCand - 32 * 8 >= kMaxTop, "room for the best and one vector of every lane");
+
+template <typename T>
+__global__ void __launch_bounds__(kFwdThreads, 1) tlp_fwd_kernel(const TlpFwdArgs a, Split split, uint32_t* status) {
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ TlpSync sm;
+  Finish* finish = reinterpret_cast<Finish*>(dyn + kRingBytes);
+  const int S = split.S;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int64_t first = blockIdx.x / S, step = gridDim.x / S;
+  const float c2 = a.inv_temp * kLog2e;
+  if (tid == 0) {
+    ring_init(sm.ring);
+    for (int i = 0; i < kSelectors; ++i) {
+      mbar_init(&sm.told[i], kStreamWarps);
+      mbar_init(&sm.taken[i], 1);
+    }
+    mbar_init(&sm.sent, 1);
+    fence_mbar_init();
+    // a cluster of several blocks has one row: the first block hears from the others once
+    mbar_arrive_expect_tx(&sm.sent, static_cast<uint32_t>(S - 1) * (sizeof(float4) + kMaxTop * sizeof(uint64_t)));
+  }
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  Patience wait;
+
+  if (warp == kStreamWarps) {
+    produce_rows<T>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, sm.ring, wait);
+  } else if (warp > kStreamWarps) {
+    const int me = warp - kStreamWarps - 1;
+    Finish& f = finish[me];
+    uint32_t parity = 0;
+    for (int64_t r = first + me * step; r < a.T; r += kSelectors * step, parity ^= 1u) {
+      const T* z = static_cast<const T*>(a.logits) + r * a.ld;
+      const Share sh = share_of(z, a.V, split.per, rank);
+      int64_t t = a.ignore;
+      float zt = 0.0f;
+      bool given = false;
+      if (rank == 0 && a.targets != nullptr) {
+        t = load_index(a.targets, r, a.wide);
+        given = t >= 0 && t < a.V;
+        if (given) zt = to_f(z[t]);
+      }
+      wait(&sm.told[me], parity);
+      const float4 none = make_float4(neg_inf(), 0.f, 0.f, neg_inf());
+      Scale k;
+      float4 p = join_sums(lane < kStreamWarps ? f.part[lane] : none, c2, k);
+      int n = 0;
+      auto taken = [&]() {
+        if (lane == 0) mbar_arrive(&sm.taken[me]);
+      };
+      __syncwarp();
+      if (a.top > 0) n = select_best(z, a.V, sh, a.top, f, f.best[rank], taken);
+      else taken();
+      uint64_t mine = lane < n ? f.best[rank][lane] : 0;  // lane i: the i-th best
+      if (rank != 0) {
+        if (lane == 0) send_f4(&f.block[rank], &sm.sent, 0, p);
+        send_u64(&f.best[rank][lane], &sm.sent, 0, mine);
+        continue;
+      }
+      if (S > 1) {
+        if (lane == 0) f.block[0] = p;
+        f.best[0][lane] = mine;
+        __syncwarp();
+        wait.cluster(&sm.sent, 0);
+        p = join_sums(lane < S ? f.block[lane] : none, c2, k);
+        // the lists' heads against one another, a lane for each list
+        uint64_t all = 0;
+        int at = 0;
+        for (n = 0; n < a.top; ++n) {
+          const uint64_t head = lane < S && at < a.top ? f.best[lane & (kMaxCluster - 1)][at] : 0;  // 0: no more
+          const uint64_t b = warp_max(head);
+          if (b == 0) break;
+          if (head == b) ++at;
+          if (lane == n) all = b;
+        }
+        mine = all;
+      }
+      const float m = p.w;
+      // H = ln s - (1/s) sum 2^x x ln 2, with s and x of one reference; then s at the maximum
+      const float ent = p.y == 0.0f ? 0.0f : logf(p.y) - p.z * kLn2 / p.y;
+      const float s = sum_at_max(p.y, m, k), log_s = logf(s), top = finite_or_0(m);
+      auto logp_of = [&](float x) { return x == neg_inf() && s == s ? neg_inf() : (x - top) * a.inv_temp - log_s; };
+      if (lane == 0) {
+        a.stats[2 * r] = m;
+        a.stats[2 * r + 1] = s;
+        a.entropy[r] = ent;
+        if (a.targets != nullptr)
+          a.logp[r] = t == a.ignore ? 0.0f : given ? logp_of(zt) : __int_as_float(0x7fc00000);
+      }
+      // fewer logits above -inf than wanted: all of them are there, the lowest other indices follow
+      for (uint32_t j = 0; n < a.top; ++j) {
+        if (__any_sync(0xffffffffu, lane < n && rank_index(mine) == j)) continue;
+        if (lane == n) mine = rank_key(neg_inf(), j);
+        ++n;
+      }
+      if (lane < a.top) {
+        a.top_idx[r * a.top + lane] = rank_index(mine);
+        a.top_logp[r * a.top + lane] = logp_of(rank_logit(mine));
+      }
+      __syncwarp();
+    }
+  } else {
+    Place<kStages> in;
+    int sel = 0;            // the selector of the row
+    uint32_t parity = 1;    // of its `taken`
+    for (int64_t r = first; r < a.T; r += step) {
+      const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
+      WarpSums<T, true> sums(c2);
+      float most = neg_inf();  // the thread's maximum and the first run that has it
+      int run = 0;
+      for (int at = sh.begin; at < sh.end; at += kStageVecs) {
+        Vec v[4];
+        const int cnt = min(sh.end - at, kStageVecs);
+        wait(&sm.ring.full[in.stage], in.parity);
+        read_stage_runs<T>(v, dyn + in.stage * kStageBytes, cnt);
+        const float x = sums.add(v, c2, cnt < kStageVecs);
+        if (x > most) {
+          most = x;
+          run = (at - sh.begin) / 4 + tid;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.ring.empty[in.stage]);
+        in.next();
+      }
+      const float4 p = sums.result();
+      Finish& f = finish[sel];
+      wait(&sm.taken[sel], parity);
+      if (lane == 0) f.part[warp] = p;
+      if (a.top > 0) f.keys[tid] = most > neg_inf() ? rank_key(most, static_cast<uint32_t>(run)) : 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.told[sel]);
+      if (++sel == kSelectors) {
+        sel = 0;
+        parity ^= 1u;
+      }
+    }
+  }
+  __syncwarp();
+  if (wait.lost && status != nullptr) atomicOr(status, kStatusTimeout);
+  cluster_arrive();  // no block leaves while another may still write to it
+  cluster_wait();
+}
 static_assert(kMaxTop == 32, "one lane for each alternative");
+
+template <typename T>
+cudaError_t launch_fwd(const TlpFwdArgs& a, Split split, cudaStream_t stream) {
+  static std::mutex mu;  // guards the occupancy cache
+  static StreamCache cache;
+  std::lock_guard<std::mutex> lk(mu);
+  // a cluster of several blocks takes one row
+  return launch_stream(tlp_fwd_kernel<T>, cache, kFwdThreads, kFwdSmem, a.T, split.S, split.S > 1, stream, a, split,
+                       status_word_ptr());
+}
 
 // Backward: bound by HBM (V elements read and written a row); no block needs another's results.
 template <typename T>
@@ -377,9 +359,11 @@ __global__ void __launch_bounds__(kRowThreads) tlp_bwd_kernel(const TlpBwdArgs a
 }  // namespace
 
 cudaError_t launch_token_logprobs_fwd(const TlpFwdArgs& a, int dtype, cudaStream_t stream) {
-  const Split p = split_row(a.T, row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2), kChunk, device_sm_count());
-  return launch_all_rows(a, dtype, p, p.S > 1, stream, tlp_fwd_kernel<float>, tlp_fwd_kernel<__half>,
-                         tlp_fwd_kernel<__nv_bfloat16>);
+  const int64_t vectors = row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2);
+  const Split p = split_row(a.T, vectors, vectors, device_sm_count());
+  return dtype == 0   ? launch_fwd<float>(a, p, stream)
+         : dtype == 1 ? launch_fwd<__half>(a, p, stream)
+                      : launch_fwd<__nv_bfloat16>(a, p, stream);
 }
 
 cudaError_t launch_token_logprobs_bwd(const TlpBwdArgs& a, int dtype, cudaStream_t stream) {

@@ -113,6 +113,34 @@ __device__ __forceinline__ float vec_max<__nv_bfloat16>(const Vec& v) {
   return fmaxf(__low2float(m), __high2float(m));
 }
 
+// the largest element of four vectors
+template <typename T>
+__device__ __forceinline__ float vec_max4(const Vec (&v)[4]);
+template <>
+__device__ __forceinline__ float vec_max4<float>(const Vec (&v)[4]) {
+  return fmaxf(fmaxf(vec_max<float>(v[0]), vec_max<float>(v[1])), fmaxf(vec_max<float>(v[2]), vec_max<float>(v[3])));
+}
+template <typename T, typename T2>
+__device__ __forceinline__ Vec larger_halves(const Vec& a, const Vec& b) {
+  Vec r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const T2 m = __hmax2(*reinterpret_cast<const T2*>(&a.w[i]), *reinterpret_cast<const T2*>(&b.w[i]));
+    r.w[i] = *reinterpret_cast<const uint32_t*>(&m);
+  }
+  return r;
+}
+template <>
+__device__ __forceinline__ float vec_max4<__half>(const Vec (&v)[4]) {
+  return vec_max<__half>(larger_halves<__half, __half2>(larger_halves<__half, __half2>(v[0], v[1]),
+                                                        larger_halves<__half, __half2>(v[2], v[3])));
+}
+template <>
+__device__ __forceinline__ float vec_max4<__nv_bfloat16>(const Vec (&v)[4]) {
+  return vec_max<__nv_bfloat16>(larger_halves<__nv_bfloat16, __nv_bfloat162>(
+      larger_halves<__nv_bfloat16, __nv_bfloat162>(v[0], v[1]), larger_halves<__nv_bfloat16, __nv_bfloat162>(v[2], v[3])));
+}
+
 template <typename T>
 __device__ __forceinline__ int row_shift(const T* row) {
   return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
@@ -193,32 +221,33 @@ __device__ __forceinline__ float at_least(float x) {
   return r;
 }
 
-// Exponents under a maximum m: x = fma(z, c, -ref) with c = log2(e) / tau and ref = m c rounded once, one
-// rounding for an element. Sums of 2^x belong to ref, not to m c: parts are joined by the difference of
-// their refs, and only the reported sum is moved to m itself. From |m c| = 2^30 on (a row of the type's
+// Exponents under a reference logit m (a maximum, or one not far below it): x = fma(z, c, -ref) with
+// c = log2(e) / tau and ref = m c rounded once, one rounding for an element. Sums of 2^x belong to ref, not
+// to m c: parts are joined by the difference of their refs, and only the reported sum is moved to the
+// maximum itself. From |m c| = 2^30 on (a row of the type's
 // lowest value, for one) that rounding would be too large; there the next smaller logit's x is
 // below -32, so 2^x is 1 at the maximum and 0 elsewhere to all digits kept: c is then a power of two that
 // puts |m c| in [2^40, 2^41), exactly.
+constexpr float kLargeRef = 1073741824.0f;
 struct Scale {
   float c, ref;
 };
 __device__ __forceinline__ Scale scale_of(float m, float c) {
   const float me = m == neg_inf() ? 0.0f : m;
   Scale s{c, me * c};
-  if (!(fabsf(s.ref) < 1073741824.0f)) {
+  if (!(fabsf(s.ref) < kLargeRef)) {
     const int e = 294 - static_cast<int>((__float_as_uint(me) >> 23) & 0xffu);
     s.c = __uint_as_float(static_cast<uint32_t>(min(max(e, 1), 254)) << 23);
     s.ref = me * s.c;
   }
   return s;
 }
-// the exponent by which a sum under the maximum `part` is moved to the joint one (`s`, `joint`: their
-// scales); a part with no logit above -inf has a sum of 0 (or NaN)
-__device__ __forceinline__ float ref_shift(float part_max, const Scale& s, float joint_max, const Scale& joint,
-                                           float c) {
-  if (part_max == neg_inf()) return 0.0f;
-  const bool plain = fabsf(s.ref) < 1073741824.0f && fabsf(joint.ref) < 1073741824.0f;
-  return at_least(plain ? s.ref - joint.ref : part_max == joint_max ? 0.0f : (part_max - joint_max) * c);
+// the exponent by which a sum under the reference logit `part` is moved to `joint` (s, k: their scales); a
+// part with no logit above -inf has a sum of 0 (or NaN)
+__device__ __forceinline__ float ref_shift(float part, const Scale& s, float joint, const Scale& k, float c) {
+  if (part == neg_inf()) return 0.0f;
+  const bool plain = fabsf(s.ref) < kLargeRef && fabsf(k.ref) < kLargeRef;
+  return at_least(plain ? s.ref - k.ref : part == joint ? 0.0f : (part - joint) * c);
 }
 // the sum of exp((z - m) / tau) from the sum of 2^x, and back
 __device__ __forceinline__ float sum_at_max(float s, float m, const Scale& k) {

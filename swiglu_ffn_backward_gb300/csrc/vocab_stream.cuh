@@ -1,7 +1,7 @@
 // Rows of logits streamed through shared memory by persistent blocks.
 //
-// A block has 16 computing warps and a producer warp that keeps a ring of six 32 KB stages full with
-// bulk copies, across rows: the copies of the next rows run under the work on this one, so the reads
+// A block has 16 computing warps and a producer warp that keeps a ring of 32 KB stages full with bulk
+// copies, across rows: the copies of the next rows run under the work on this one, so the reads
 // never pause for a reduction. Cluster c takes the rows c, c + #clusters, ...; its S blocks take a share
 // of the row each (vocab_rows.cuh: aligned 16-byte vectors). A row's first and last vector, when they
 // are partial, are put together by the producer warp, with -inf outside the row.
@@ -16,8 +16,6 @@ constexpr int kStreamWarps = 16;
 constexpr int kStreamThreads = kStreamWarps * 32;   // computing threads
 constexpr int kStageVecs = 4 * kStreamThreads;      // vectors a stage holds: four for each thread
 constexpr int kStageBytes = kStageVecs * 16;
-constexpr int kStages = 6;
-constexpr int kRingBytes = kStages * kStageBytes;
 
 // Waits are bounded: after the first one that ran out, the later ones of the thread only look once, so
 // that the block still comes to its end (its results are then void and the status word says so).
@@ -50,22 +48,25 @@ struct Patience {
   }
 };
 
+template <int N>  // stages
 struct Ring {
-  uint64_t full[kStages];   // a stage's copies have landed
-  uint64_t empty[kStages];  // the computing warps have read it
+  uint64_t full[N];   // a stage's copies have landed
+  uint64_t empty[N];  // the computing warps have read it
 };
-__device__ __forceinline__ void ring_init(Ring& ring) {
-  for (int i = 0; i < kStages; ++i) {
+template <int N>
+__device__ __forceinline__ void ring_init(Ring<N>& ring) {
+  for (int i = 0; i < N; ++i) {
     mbar_init(&ring.full[i], 1);
     mbar_init(&ring.empty[i], kStreamWarps);
   }
 }
 // a position in the ring: stage and the parity of its use
+template <int N>
 struct Place {
   int stage = 0;
   uint32_t parity = 0;
   __device__ __forceinline__ void next() {
-    if (++stage == kStages) {
+    if (++stage == N) {
       stage = 0;
       parity ^= 1u;
     }
@@ -73,9 +74,9 @@ struct Place {
 };
 
 // The producer warp: all rows of the block's cluster, row r's share at `rank` of S.
-template <typename T>
+template <typename T, int N>
 __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int64_t V, int64_t first, int64_t rows,
-                                             int64_t step, int per, int rank, unsigned char* buf, Ring& ring,
+                                             int64_t step, int per, int rank, unsigned char* buf, Ring<N>& ring,
                                              Patience& wait) {
   constexpr int E = Traits<T>::E;
   const int lane = threadIdx.x & 31;
@@ -93,7 +94,7 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
     if (e >= 0 && e < V) x = z[e];
     return x;
   };
-  Place p;
+  Place<N> p;
   T mine = edge(first);
   for (int64_t r = first; r < rows; r += step) {
     const T* z = base + r * ld;
@@ -145,7 +146,94 @@ __device__ __forceinline__ void read_stage(Vec (&v)[4], const unsigned char* sta
   }
 }
 
-// 8 bytes into block `rank` of the cluster, counted by its barrier at the offset of `bar`
+// The same with four vectors that follow each other, 4 threadIdx.x .. 4 threadIdx.x + 3, in an order by
+// thread in which the eight lanes of a shared-memory phase meet all banks.
+template <typename T>
+__device__ __forceinline__ void read_stage_runs(Vec (&v)[4], const unsigned char* stage, int n) {
+  const uint4* p = reinterpret_cast<const uint4*>(stage);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = 4 * static_cast<int>(threadIdx.x) + ((i + (static_cast<int>(threadIdx.x) >> 1)) & 3);
+    uint4 u = make_uint4(Traits<T>::kNegInf, Traits<T>::kNegInf, Traits<T>::kNegInf, Traits<T>::kNegInf);
+    if (n == kStageVecs || at < n) u = p[at];
+    v[i] = Vec{{u.x, u.y, u.z, u.w}};
+  }
+}
+
+// A warp's sums over its part of a row, four vectors a thread at a time: sum 2^x, with kSecond sum 2^x x
+// too, under a reference logit that is raised only when a logit passes it by 2^kRoom or more, so that the
+// warp does not have to agree on its maximum every time.
+constexpr float kRoom = 10.0f;
+template <typename T, bool kSecond>
+struct WarpSums {
+  float m = neg_inf();    // reference logit
+  float lim = neg_inf();  // a logit above it raises the reference
+  float top = neg_inf();  // the thread's maximum
+  Scale k;
+  float2 s2{0.f, 0.f}, w2{0.f, 0.f};
+
+  __device__ __forceinline__ explicit WarpSums(float c) : k{c, 0.0f} {}
+
+  template <bool kMasked>
+  __device__ __forceinline__ void add_terms(const Vec (&v)[4]) {
+    const float2 c = make_float2(k.c, k.c), ref = make_float2(-k.ref, -k.ref);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int p = 0; p < Traits<T>::E / 2; ++p) {
+        float2 x = __ffma2_rn(vec_pair<T>(v[i], p), c, ref);
+        if (kMasked) x = make_float2(at_least(x.x), at_least(x.y));
+        const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        s2 = __fadd2_rn(s2, e);
+        if (kSecond) w2 = __ffma2_rn(e, x, w2);
+      }
+    }
+  }
+  // returns the largest of the thread's logits; masked: -infs are likely
+  __device__ __forceinline__ float add(const Vec (&v)[4], float c, bool masked) {
+    const float most = vec_max4<T>(v);
+    if (__any_sync(0xffffffffu, most > lim)) {
+      const float mn = warp_max(fmaxf(most, m));
+      const Scale kn = scale_of(mn, c);
+      const float x0 = ref_shift(m, k, mn, kn, c), f = ex2_approx(x0);
+      if (kSecond) w2 = __fmul2_rn(__ffma2_rn(s2, make_float2(x0, x0), w2), make_float2(f, f));
+      s2 = __fmul2_rn(s2, make_float2(f, f));
+      m = mn;
+      k = kn;
+      lim = fabsf(k.ref) < kLargeRef ? m + kRoom / c : m;
+    }
+    top = fmaxf(top, most);
+    if (!kSecond) {
+      add_terms<false>(v);
+      return most;
+    }
+    // a -inf makes the second sum 0 * inf: only then the exponents are kept above it
+    const float2 s0 = s2, w0 = w2;
+    if (!masked) {
+      add_terms<false>(v);
+      masked = __any_sync(0xffffffffu, !(w2.x + w2.y == w2.x + w2.y));
+    }
+    if (masked) {
+      s2 = s0;
+      w2 = w0;
+      add_terms<true>(v);
+    }
+    return most;
+  }
+  // reference logit, sum 2^x, sum 2^x x, maximum
+  __device__ __forceinline__ float4 result() const {
+    return make_float4(m, warp_sum(s2.x + s2.y), kSecond ? warp_sum(w2.x + w2.y) : 0.f, warp_max(top));
+  }
+};
+// such results, one in each lane (a reference of -inf and sums of 0 for none), joined in every lane
+__device__ __forceinline__ float4 join_sums(const float4& p, float c, Scale& k) {
+  const float m = warp_max(p.x);
+  k = scale_of(m, c);
+  const float x0 = ref_shift(p.x, scale_of(p.x, c), m, k, c), f = ex2_approx(x0);
+  return make_float4(m, warp_sum(f * p.y), warp_sum(f * fmaf(p.y, x0, p.z)), warp_max(p.w));
+}
+
+// Sends into block `rank` of the cluster, their bytes counted by its barrier at the offset of `bar`.
 __device__ __forceinline__ void send_f2(const float2* to, const uint64_t* bar, uint32_t rank, float x, float y) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
                    peer_addr(to, rank)),
@@ -153,9 +241,22 @@ __device__ __forceinline__ void send_f2(const float2* to, const uint64_t* bar, u
                : "memory");
 }
 
+__device__ __forceinline__ void send_f4(const float4* to, const uint64_t* bar, uint32_t rank, float4 v) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                   peer_addr(to, rank)),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(peer_addr(bar, rank))
+               : "memory");
+}
+__device__ __forceinline__ void send_u64(const uint64_t* to, const uint64_t* bar, uint32_t rank, uint64_t v) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(peer_addr(to, rank)),
+               "l"(v), "r"(peer_addr(bar, rank))
+               : "memory");
+}
+
 }  // namespace row
 
-// A persistent launch: as many clusters as fit on the device at once, at most one a row. The occupancy of
+// A persistent launch: as many clusters as fit on the device at once, at most one a row (`all`: one for
+// every row, however many fit). The occupancy of
 // a (kernel, cluster size, shared memory) is asked once for each device.
 struct StreamCache {
   int device = -1, S = 0, clusters = 0;
@@ -163,7 +264,7 @@ struct StreamCache {
 };
 template <typename Kernel, typename... Args>
 cudaError_t launch_stream(Kernel kernel, StreamCache& cache, int threads, size_t smem, int64_t rows, int S,
-                          cudaStream_t stream, const Args&... args) {
+                          bool all, cudaStream_t stream, const Args&... args) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -188,7 +289,7 @@ cudaError_t launch_stream(Kernel kernel, StreamCache& cache, int threads, size_t
     if (n < 1) return cudaErrorLaunchOutOfResources;
     cache = StreamCache{dev, S, n, smem};
   }
-  const int64_t clusters = rows < cache.clusters ? rows : cache.clusters;
+  const int64_t clusters = all || rows < cache.clusters ? rows : cache.clusters;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * S));
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
