@@ -6,6 +6,17 @@
 //   dx = rstd (g - mean(g) - x_hat mean(g x_hat)) (+ dh, the gradient that reaches h by another path)
 //   dgamma = sum over rows of dy x_hat,  dbeta = sum over rows of dy
 // All arithmetic is fp32; h, y and dx are rounded once.
+//
+// Bound by HBM: two to four tensors of M N elements are read or written, with some ten operations an
+// element. A group of 32 to 1024 threads holds a row in registers, so each element is read once: the
+// variance is taken of centred values in a second pass over the registers. Vectors are the widest that
+// the row length, strides and addresses allow (16 bytes, 4 bytes or one element). Rows too long for the
+// registers of a block are read again (ln_fwd_long_kernel, ln_dx_long_kernel).
+// Backward: persistent groups, each thread the same columns of every row, so the columns' sums of
+// dgamma and dbeta stay in registers; the next row is loaded under the work on this one. The blocks'
+// sums go to the workspace and are added by a second kernel in a fixed order.
+#include <mutex>
+
 #include "row_ops.cuh"
 #include "swg_launch.h"
 
@@ -14,13 +25,204 @@ namespace {
 
 using namespace row;
 
-constexpr int kThreads = 256;
-constexpr int kColThreads = 128;    // columns per block of the weight-gradient kernel
-constexpr int64_t kRowChunks = 64;  // row chunks of the weight-gradient kernel, at most
+// E elements in one load
+template <int kBytes>
+struct Raw;
+template <>
+struct Raw<16> {
+  uint4 u;
+};
+template <>
+struct Raw<8> {
+  uint2 u;
+};
+template <>
+struct Raw<4> {
+  uint32_t u;
+};
+template <>
+struct Raw<2> {
+  uint16_t u;
+};
+template <int kBytes>
+__device__ __forceinline__ Raw<kBytes> ld_stream(const void* p);
+template <>
+__device__ __forceinline__ Raw<16> ld_stream<16>(const void* p) {
+  Raw<16> r;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(r.u.x), "=r"(r.u.y), "=r"(r.u.z), "=r"(r.u.w)
+      : "l"(p));
+  return r;
+}
+template <>
+__device__ __forceinline__ Raw<4> ld_stream<4>(const void* p) {
+  return Raw<4>{__ldg(static_cast<const uint32_t*>(p))};
+}
+template <>
+__device__ __forceinline__ Raw<2> ld_stream<2>(const void* p) {
+  return Raw<2>{__ldg(static_cast<const uint16_t*>(p))};
+}
+template <typename T, int E>
+__device__ __forceinline__ void to_floats(const Raw<E * sizeof(T)>& r, float (&f)[E]) {
+  const T* t = reinterpret_cast<const T*>(&r);
+#pragma unroll
+  for (int e = 0; e < E; ++e) f[e] = to_f(t[e]);
+}
+template <typename T, int E>
+__device__ __forceinline__ Raw<E * sizeof(T)> from_floats(const float (&f)[E]) {
+  Raw<E * sizeof(T)> r;
+  T* t = reinterpret_cast<T*>(&r);
+#pragma unroll
+  for (int e = 0; e < E; ++e) t[e] = from_f<T>(f[e]);
+  return r;
+}
+template <int kBytes>
+__device__ __forceinline__ void st_stream(void* p, const Raw<kBytes>& r) {
+  *static_cast<Raw<kBytes>*>(p) = r;
+}
+// E weights of either type (cached: every row uses them)
+template <typename T, int E>
+__device__ __forceinline__ void load_weights(const void* p, int64_t j, bool f32, float (&f)[E]) {
+  if (sizeof(T) == 4 || f32) {
+    const float* w = static_cast<const float*>(p) + j;
+    if constexpr (E % 4 == 0) {
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(w + e));
+        f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = __ldg(w + e);
+    }
+  } else {
+    const T* w = static_cast<const T*>(p) + j;
+    if constexpr (E * sizeof(T) == 16) {
+      Raw<16> r{__ldg(reinterpret_cast<const uint4*>(w))};
+      to_floats<T, E>(r, f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = to_f(w[e]);
+    }
+  }
+}
 
+// Sums over a group of G threads (a power of two from 32 on) in a block; every thread gets them, added in a
+// fixed order. Groups above a warp use two alternating buffers, so that one barrier a sum is enough.
+template <int kSums>
+struct GroupSum {
+  float* buf;  // of the group: 2 x kSums x warps
+  int warps, warp, id, turn = 0;
+  __device__ __forceinline__ GroupSum(float* smem, int G) {
+    warps = G >> 5;
+    warp = (threadIdx.x >> 5) & (warps - 1);
+    id = 1 + static_cast<int>(threadIdx.x) / G;  // barrier of the group; groups above a warp: at most 8
+    buf = smem + (threadIdx.x / G) * (2 * kSums * warps);
+  }
+  __device__ __forceinline__ void operator()(float (&v)[kSums]) {
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) v[i] = warp_sum(v[i]);
+    if (warps == 1) return;
+    float* b = buf + turn * kSums * warps;
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < kSums; ++i) b[i * warps + warp] = v[i];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(warps * 32) : "memory");
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
+      const int lane = threadIdx.x & 31;
+      v[i] = warp_sum(lane < warps ? b[i * warps + lane] : 0.0f);
+    }
+  }
+};
+constexpr int kBlock = 256;       // threads of a block, unless a row takes more
+constexpr int kMaxGroup = 1024;
+constexpr int kMaxBwdGroup = 512;  // the column sums take registers
+
+// ---- forward
+template <typename T, int E, int R>
+__global__ void __launch_bounds__(kMaxGroup) ln_fwd_kernel(const LnFwdArgs a, int G) {
+  __shared__ float smem[2 * 32];
+  constexpr int kBytes = E * sizeof(T);
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + threadIdx.x / G;
+  const int t = threadIdx.x & (G - 1);
+  if (r >= a.M) return;  // whole groups
+  const int n = static_cast<int>(a.N / E);
+  const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+  Raw<kBytes> raw[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (t + i * G < n) raw[i] = ld_stream<kBytes>(x + static_cast<int64_t>(t + i * G) * E);
+  float f[R][E];
+  if (a.residual != nullptr) {
+    const T* res = static_cast<const T*>(a.residual) + r * a.ldr;
+    T* h = static_cast<T*>(a.h) + r * a.N;
+    Raw<kBytes> rr[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (t + i * G < n) rr[i] = ld_stream<kBytes>(res + static_cast<int64_t>(t + i * G) * E);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (t + i * G >= n) continue;
+      float g[E];
+      to_floats<T, E>(raw[i], f[i]);
+      to_floats<T, E>(rr[i], g);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[i][e] += g[e];
+      raw[i] = from_floats<T, E>(f[i]);  // h as it is stored
+      st_stream(h + static_cast<int64_t>(t + i * G) * E, raw[i]);
+    }
+  }
+  float s[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (t + i * G >= n) continue;
+    to_floats<T, E>(raw[i], f[i]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[0] += f[i][e];
+  }
+  GroupSum<1> sum(smem, G);
+  sum(s);
+  const float inv_n = 1.0f / static_cast<float>(a.N), mu = s[0] * inv_n;
+  s[0] = 0.f;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (t + i * G >= n) continue;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      f[i][e] -= mu;
+      s[0] = fmaf(f[i][e], f[i][e], s[0]);
+    }
+  }
+  sum(s);
+  const float rstd = 1.0f / sqrtf(fmaf(s[0], inv_n, a.eps));
+  T* y = static_cast<T*>(a.y) + r * a.N;
+  const bool f32 = a.wdtype == 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (t + i * G >= n) continue;
+    const int64_t j = static_cast<int64_t>(t + i * G) * E;
+    float g[E], b[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) g[e] = 1.0f, b[e] = 0.0f;
+    if (a.gamma != nullptr) load_weights<T, E>(a.gamma, j, f32, g);
+    if (a.beta != nullptr) load_weights<T, E>(a.beta, j, f32, b);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[i][e] = fmaf(f[i][e] * rstd, g[e], b[e]);
+    st_stream(y + j, from_floats<T, E>(f[i]));
+  }
+  if (t == 0) {
+    a.stats[2 * r] = mu;
+    a.stats[2 * r + 1] = rstd;
+  }
+}
+
+// rows of any length, element by element, read three times (from L2 where a row fits)
 template <typename T>
-__global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const LnFwdArgs a) {
-  __shared__ float buf[kThreads / 32];
+__global__ void __launch_bounds__(kMaxGroup) ln_fwd_long_kernel(const LnFwdArgs a) {
+  __shared__ float buf[32];
   const float inv_n = 1.0f / static_cast<float>(a.N);
   for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ldx;
@@ -31,15 +233,15 @@ __global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const LnFwdArgs a) {
       return res == nullptr ? to_f(x[j]) : to_f(from_f<T>(to_f(x[j]) + to_f(res[j])));
     };
     float s = 0.f;
-    for (int64_t j = threadIdx.x; j < a.N; j += kThreads) s += value(j);
+    for (int64_t j = threadIdx.x; j < a.N; j += blockDim.x) s += value(j);
     const float mu = block_sum(s, buf) * inv_n;
     float q = 0.f;
-    for (int64_t j = threadIdx.x; j < a.N; j += kThreads) {
+    for (int64_t j = threadIdx.x; j < a.N; j += blockDim.x) {
       const float d = value(j) - mu;
       q = fmaf(d, d, q);
     }
-    const float rstd = 1.0f / sqrtf(block_sum(q, buf) * inv_n + a.eps);
-    for (int64_t j = threadIdx.x; j < a.N; j += kThreads) {
+    const float rstd = 1.0f / sqrtf(fmaf(block_sum(q, buf), inv_n, a.eps));
+    for (int64_t j = threadIdx.x; j < a.N; j += blockDim.x) {
       const float v = value(j);
       const float g = a.gamma != nullptr ? load_any(a.gamma, j, a.wdtype) : 1.0f;
       const float b = a.beta != nullptr ? load_any(a.beta, j, a.wdtype) : 0.0f;
@@ -53,9 +255,122 @@ __global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const LnFwdArgs a) {
   }
 }
 
+// ---- backward
+// dx, and with a.part the block's column sums: part[block][0][j] of dy x_hat, part[block][1][j] of dy
+template <typename T, int E, int R>
+__global__ void __launch_bounds__(kMaxBwdGroup) ln_bwd_kernel(const LnBwdArgs a, int G) {
+  extern __shared__ float dyn[];  // with several groups a block: 2 N column sums
+  __shared__ float smem[2 * 2 * 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int kBytes = E * sizeof(T);
+  const int groups = blockDim.x / G, group = threadIdx.x / G;
+  const int t = threadIdx.x & (G - 1);
+  const int n = static_cast<int>(a.N / E);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const float inv_n = 1.0f / static_cast<float>(a.N);
+  const bool add = a.dh != nullptr;
+  float gam[R][E], sg[R][E], sb[R][E];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) gam[i][e] = 1.0f, sg[i][e] = sb[i][e] = 0.0f;
+    if (a.gamma != nullptr && t + i * G < n)
+      load_weights<T, E>(a.gamma, static_cast<int64_t>(t + i * G) * E, a.wdtype == 0, gam[i]);
+  }
+  struct Row {
+    Raw<kBytes> x[R], dy[R], dh[R];
+    float mu, rstd;
+  };
+  auto load = [&](Row& w, int64_t r) {
+    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+    const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
+    w.mu = a.stats[2 * r];
+    w.rstd = a.stats[2 * r + 1];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (t + i * G >= n) continue;
+      const int64_t j = static_cast<int64_t>(t + i * G) * E;
+      w.x[i] = ld_stream<kBytes>(x + j);
+      w.dy[i] = ld_stream<kBytes>(dy + j);
+      if (add) w.dh[i] = ld_stream<kBytes>(static_cast<const T*>(a.dh) + r * a.lddh + j);
+    }
+  };
+  GroupSum<2> sum(smem, G);
+  // two rows of 64 bytes a tensor and thread would not fit the registers
+  constexpr bool kAhead = R * kBytes <= 32;
+  Row next;
+  int64_t r = static_cast<int64_t>(blockIdx.x) * groups + group;
+  if (kAhead && r < a.M) load(next, r);
+  for (; r < a.M; r += step) {
+    if (!kAhead) load(next, r);
+    const Row w = next;
+    if (kAhead && r + step < a.M) load(next, r + step);
+    const float mu = w.mu, rstd = w.rstd;
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (t + i * G >= n) continue;
+      float x[E], dy[E];
+      to_floats<T, E>(w.x[i], x);
+      to_floats<T, E>(w.dy[i], dy);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float xh = (x[e] - mu) * rstd, g = dy[e] * gam[i][e];
+        sg[i][e] = fmaf(dy[e], xh, sg[i][e]);
+        sb[i][e] += dy[e];
+        s[0] += g;
+        s[1] = fmaf(g, xh, s[1]);
+      }
+    }
+    sum(s);
+    // dx = rstd (g - mean(g) - x_hat mean(g x_hat))
+    const float c0 = -s[0] * inv_n * rstd, c1 = -s[1] * inv_n * rstd;
+    T* dx = static_cast<T*>(a.dx) + r * a.N;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (t + i * G >= n) continue;
+      float x[E], dy[E];
+      to_floats<T, E>(w.x[i], x);
+      to_floats<T, E>(w.dy[i], dy);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float xh = (x[e] - mu) * rstd;
+        x[e] = fmaf(dy[e] * gam[i][e], rstd, fmaf(xh, c1, c0));
+      }
+      if (add) {
+        to_floats<T, E>(w.dh[i], dy);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] += dy[e];
+      }
+      st_stream(dx + static_cast<int64_t>(t + i * G) * E, from_floats<T, E>(x));
+    }
+  }
+  if (a.part == nullptr) return;
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
+  float* to = groups > 1 ? dyn : part;
+  for (int k = 0; k < groups; ++k) {  // one group after the other: a fixed order
+    if (k == group) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (t + i * G >= n) continue;
+        const int64_t j = static_cast<int64_t>(t + i * G) * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          to[j + e] = k == 0 ? sg[i][e] : to[j + e] + sg[i][e];
+          to[a.N + j + e] = k == 0 ? sb[i][e] : to[a.N + j + e] + sb[i][e];
+        }
+      }
+    }
+    if (groups > 1) __syncthreads();
+  }
+  if (groups > 1)
+    for (int64_t j = threadIdx.x; j < 2 * a.N; j += blockDim.x) part[j] = dyn[j];
+}
+
+// rows of any length, element by element
 template <typename T>
-__global__ void __launch_bounds__(kThreads) ln_dx_kernel(const LnBwdArgs a) {
-  __shared__ float buf[kThreads / 32];
+__global__ void __launch_bounds__(kMaxGroup) ln_dx_long_kernel(const LnBwdArgs a) {
+  __shared__ float buf[32];
   const float inv_n = 1.0f / static_cast<float>(a.N);
   for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ldx;
@@ -64,24 +379,24 @@ __global__ void __launch_bounds__(kThreads) ln_dx_kernel(const LnBwdArgs a) {
     T* dx = static_cast<T*>(a.dx) + r * a.N;
     const float mu = a.stats[2 * r], rstd = a.stats[2 * r + 1];
     float sa = 0.f, sb = 0.f;
-    for (int64_t j = threadIdx.x; j < a.N; j += kThreads) {
+    for (int64_t j = threadIdx.x; j < a.N; j += blockDim.x) {
       const float g = to_f(dy[j]) * (a.gamma != nullptr ? load_any(a.gamma, j, a.wdtype) : 1.0f);
       sa += g;
       sb = fmaf(g, (to_f(x[j]) - mu) * rstd, sb);
     }
-    sa = block_sum(sa, buf) * inv_n;
-    sb = block_sum(sb, buf) * inv_n;
-    for (int64_t j = threadIdx.x; j < a.N; j += kThreads) {
+    const float c0 = -block_sum(sa, buf) * inv_n * rstd, c1 = -block_sum(sb, buf) * inv_n * rstd;
+    for (int64_t j = threadIdx.x; j < a.N; j += blockDim.x) {
       const float g = to_f(dy[j]) * (a.gamma != nullptr ? load_any(a.gamma, j, a.wdtype) : 1.0f);
-      const float v = rstd * (g - sa - (to_f(x[j]) - mu) * rstd * sb);
+      const float v = fmaf(g, rstd, fmaf((to_f(x[j]) - mu) * rstd, c1, c0));
       dx[j] = from_f<T>(dh != nullptr ? v + to_f(dh[j]) : v);
     }
   }
 }
-
-// one row chunk's column sums of dy x_hat and dy -> part [chunks][2][N]
+// one row chunk's column sums, for rows of any length
+constexpr int kColThreads = 128;
 template <typename T>
-__global__ void __launch_bounds__(kColThreads) ln_param_kernel(const LnBwdArgs a, int64_t rows_per_chunk) {
+__global__ void __launch_bounds__(kColThreads) ln_param_long_kernel(const LnBwdArgs a, int64_t rows_per_chunk) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t j = static_cast<int64_t>(blockIdx.x) * kColThreads + threadIdx.x;
   if (j >= a.N) return;
   const int64_t r0 = blockIdx.y * rows_per_chunk, r1 = min(a.M, r0 + rows_per_chunk);
@@ -97,50 +412,190 @@ __global__ void __launch_bounds__(kColThreads) ln_param_kernel(const LnBwdArgs a
   p[a.N + j] = sb;
 }
 
-__global__ void __launch_bounds__(kColThreads) ln_param_reduce_kernel(const float* part, int64_t chunks, int64_t N,
-                                                                      void* dgamma, void* dbeta, int wdtype) {
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * kColThreads + threadIdx.x;
-  if (j >= N) return;
-  float sg = 0.f, sb = 0.f;
-  for (int64_t c = 0; c < chunks; ++c) {
-    sg += part[c * 2 * N + j];
-    sb += part[c * 2 * N + N + j];
+// dgamma, dbeta from part [rows][2 N]: 32 columns a block, eight threads a column take the rows in turn and
+// are added in order. A programmatic dependent of the kernel before it: its writes are visible after
+// griddepcontrol.wait.
+constexpr int kReduceCols = 32, kReduceSlices = 16;
+__global__ void __launch_bounds__(kReduceCols* kReduceSlices) ln_reduce_kernel(const float* part, int rows, int64_t N,
+                                                                               void* dgamma, void* dbeta, int wdtype) {
+  __shared__ float sums[kReduceSlices][kReduceCols];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = threadIdx.x % kReduceCols, k = threadIdx.x / kReduceCols;
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * kReduceCols + c;
+  float s = 0.f;
+  if (j < 2 * N) {
+    const float* p = part + j;
+    int i = k;
+    for (; i + 3 * kReduceSlices < rows; i += 4 * kReduceSlices) {
+      const float v0 = p[static_cast<int64_t>(i) * 2 * N], v1 = p[static_cast<int64_t>(i + kReduceSlices) * 2 * N];
+      const float v2 = p[static_cast<int64_t>(i + 2 * kReduceSlices) * 2 * N];
+      const float v3 = p[static_cast<int64_t>(i + 3 * kReduceSlices) * 2 * N];
+      s += (v0 + v1) + (v2 + v3);
+    }
+    for (; i < rows; i += kReduceSlices) s += p[static_cast<int64_t>(i) * 2 * N];
   }
-  if (dgamma != nullptr) store_any(dgamma, j, wdtype, sg);
-  if (dbeta != nullptr) store_any(dbeta, j, wdtype, sb);
+  sums[k][c] = s;
+  __syncthreads();
+  if (k != 0 || j >= 2 * N) return;
+#pragma unroll
+  for (int i = 1; i < kReduceSlices; ++i) s += sums[i][c];
+  if (j < N) {
+    if (dgamma != nullptr) store_any(dgamma, j, wdtype, s);
+  } else if (dbeta != nullptr) {
+    store_any(dbeta, j - N, wdtype, s);
+  }
 }
 
-int64_t ln_chunks(int64_t M) { return M < kRowChunks ? M : kRowChunks; }
-unsigned row_grid(int64_t M) { return static_cast<unsigned>(M < 65536 ? M : 65536); }
+// ---- host
+// elements of a load: the widest of 16 bytes, 4 bytes and one element that divides the row and that all
+// addresses and row strides are multiples of
+int vector_elems(int64_t N, int es, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds,
+                 std::initializer_list<const void*> weights) {
+  for (int bytes : {16, 4}) {
+    const int e = bytes / es;
+    if (e < 1 || N % e != 0) continue;
+    bool ok = true;
+    for (const void* p : ptrs) ok = ok && reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0;
+    for (int64_t ld : lds) ok = ok && ld % e == 0;
+    // weights are loaded 16 bytes at a time with full vectors, else one by one
+    if (bytes == 16)
+      for (const void* p : weights) ok = ok && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+    if (ok) return e;
+  }
+  return 1;
+}
+// threads a row for R vectors each
+int group_threads(int64_t n, int R) {
+  int g = 32;
+  while (static_cast<int64_t>(g) * R < n && g < kMaxGroup) g *= 2;
+  return g;
+}
+
+template <typename T, int E, int R>
+cudaError_t fwd_one(const LnFwdArgs& a, int G, cudaStream_t stream) {
+  const int block = G > kBlock ? G : kBlock;
+  const int64_t per = block / G, blocks = (a.M + per - 1) / per;
+  ln_fwd_kernel<T, E, R><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a, G);
+  return cudaGetLastError();
+}
+// vectors a thread: as few as let a block of 512 hold the row, two for wide vectors from a warp on
+template <typename T, int E, int R0>
+cudaError_t fwd_any(const LnFwdArgs& a, cudaStream_t stream) {
+  const int64_t n = a.N / E;
+  if (n <= 32 * R0) return fwd_one<T, E, R0>(a, 32, stream);
+  if (n <= 512 * 2 * R0) return fwd_one<T, E, 2 * R0>(a, group_threads(n, 2 * R0), stream);
+  if (n <= kMaxGroup * 4 * R0) return fwd_one<T, E, 4 * R0>(a, group_threads(n, 4 * R0), stream);
+  const unsigned grid = static_cast<unsigned>(a.M < 65536 ? a.M : 65536);
+  ln_fwd_long_kernel<T><<<grid, kMaxGroup, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t fwd_type(const LnFwdArgs& a, cudaStream_t stream) {
+  constexpr int es = sizeof(T);
+  const int e = vector_elems(a.N, es, {a.x, a.residual, a.h, a.y}, {a.ldx, a.ldr}, {a.gamma, a.beta});
+  if (e == 16 / es) return fwd_any<T, 16 / es, 1>(a, stream);
+  if constexpr (es == 2)
+    if (e == 2) return fwd_any<T, 2, 2>(a, stream);
+  return fwd_any<T, 1, 4>(a, stream);
+}
+
+int reduce_grid(int64_t N) { return static_cast<int>((2 * N + kReduceCols - 1) / kReduceCols); }
+cudaError_t launch_reduce(const LnBwdArgs& a, int64_t rows, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(reduce_grid(a.N)));
+  cfg.blockDim = dim3(kReduceCols * kReduceSlices);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ln_reduce_kernel, static_cast<const float*>(a.part), static_cast<int>(rows), a.N,
+                            a.dgamma, a.dbeta, a.wdtype);
+}
+
+constexpr int64_t kMaxBlocks = 4 * 256;  // rows of column sums in the workspace, at most
+constexpr int64_t kLongChunks = 64;      // of them for rows too long for registers
+
+// the persistent kernel's blocks: as many as fit (asked once for each device and block size), at most one
+// group a row
+template <typename T, int E, int R>
+cudaError_t bwd_one(const LnBwdArgs& a, int G, cudaStream_t stream) {
+  const int block = G > kBlock ? G : kBlock, groups = block / G;
+  const size_t smem = groups > 1 && a.part != nullptr ? static_cast<size_t>(2 * a.N) * sizeof(float) : 0;
+  int64_t blocks;
+  {
+    static std::mutex mu;
+    static int device = -1, threads = 0, fit = 0;
+    static size_t bytes = 0;
+    std::lock_guard<std::mutex> lk(mu);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (device != dev || threads != block || bytes != smem) {
+      int per_sm = 0;
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, ln_bwd_kernel<T, E, R>, block, smem);
+      if (e != cudaSuccess) return e;
+      if (per_sm < 1) return cudaErrorLaunchOutOfResources;
+      device = dev, threads = block, bytes = smem;
+      fit = per_sm * device_sm_count();
+    }
+    blocks = fit;
+  }
+  const int64_t most = (a.M + groups - 1) / groups;
+  if (blocks > most) blocks = most;
+  if (blocks > kMaxBlocks) blocks = kMaxBlocks;
+  ln_bwd_kernel<T, E, R><<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, G);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.part == nullptr) return e;
+  return launch_reduce(a, blocks, stream);
+}
+template <typename T>
+cudaError_t bwd_long(const LnBwdArgs& a, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>(a.M < 65536 ? a.M : 65536);
+  ln_dx_long_kernel<T><<<grid, kMaxGroup, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.part == nullptr) return e;
+  const int64_t chunks = a.M < kLongChunks ? a.M : kLongChunks, per = (a.M + chunks - 1) / chunks;
+  const dim3 g(static_cast<unsigned>((a.N + kColThreads - 1) / kColThreads), static_cast<unsigned>(chunks));
+  ln_param_long_kernel<T><<<g, kColThreads, 0, stream>>>(a, per);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_reduce(a, chunks, stream);
+}
+template <typename T, int E, int R0>
+cudaError_t bwd_any(const LnBwdArgs& a, cudaStream_t stream) {
+  const int64_t n = a.N / E;
+  if (n <= 32 * R0) return bwd_one<T, E, R0>(a, 32, stream);
+  if (n <= kMaxBwdGroup * 2 * R0) return bwd_one<T, E, 2 * R0>(a, group_threads(n, 2 * R0), stream);
+  return bwd_long<T>(a, stream);
+}
+template <typename T>
+cudaError_t bwd_type(const LnBwdArgs& a, cudaStream_t stream) {
+  constexpr int es = sizeof(T);
+  const int e = vector_elems(a.N, es, {a.dy, a.x, a.dh, a.dx}, {a.lddy, a.ldx, a.lddh}, {a.gamma});
+  if (e == 16 / es) return bwd_any<T, 16 / es, es == 2 ? 1 : 2>(a, stream);
+  if constexpr (es == 2)
+    if (e == 2) return bwd_any<T, 2, 4>(a, stream);
+  return bwd_any<T, 1, 4>(a, stream);
+}
 
 }  // namespace
 
 size_t ln_workspace_bytes(int64_t M, int64_t N) {
-  return static_cast<size_t>(ln_chunks(M)) * 2 * static_cast<size_t>(N) * sizeof(float);
+  const int64_t rows = M < kMaxBlocks ? M : kMaxBlocks;
+  return static_cast<size_t>(rows) * 2 * static_cast<size_t>(N) * sizeof(float);
 }
 
 cudaError_t launch_layer_norm_fwd(const LnFwdArgs& a, int dtype, cudaStream_t stream) {
-  const unsigned grid = row_grid(a.M);
-  if (dtype == 0) ln_fwd_kernel<float><<<grid, kThreads, 0, stream>>>(a);
-  else if (dtype == 1) ln_fwd_kernel<__half><<<grid, kThreads, 0, stream>>>(a);
-  else ln_fwd_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return dtype == 0   ? fwd_type<float>(a, stream)
+         : dtype == 1 ? fwd_type<__half>(a, stream)
+                      : fwd_type<__nv_bfloat16>(a, stream);
 }
 
 cudaError_t launch_layer_norm_bwd(const LnBwdArgs& a, int dtype, cudaStream_t stream) {
-  const unsigned grid = row_grid(a.M);
-  if (dtype == 0) ln_dx_kernel<float><<<grid, kThreads, 0, stream>>>(a);
-  else if (dtype == 1) ln_dx_kernel<__half><<<grid, kThreads, 0, stream>>>(a);
-  else ln_dx_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-  if (a.dgamma != nullptr || a.dbeta != nullptr) {
-    const int64_t chunks = ln_chunks(a.M), per = (a.M + chunks - 1) / chunks;
-    const dim3 g(static_cast<unsigned>((a.N + kColThreads - 1) / kColThreads), static_cast<unsigned>(chunks));
-    if (dtype == 0) ln_param_kernel<float><<<g, kColThreads, 0, stream>>>(a, per);
-    else if (dtype == 1) ln_param_kernel<__half><<<g, kColThreads, 0, stream>>>(a, per);
-    else ln_param_kernel<__nv_bfloat16><<<g, kColThreads, 0, stream>>>(a, per);
-    ln_param_reduce_kernel<<<g.x, kColThreads, 0, stream>>>(a.part, chunks, a.N, a.dgamma, a.dbeta, a.wdtype);
-  }
-  return cudaGetLastError();
+  return dtype == 0   ? bwd_type<float>(a, stream)
+         : dtype == 1 ? bwd_type<__half>(a, stream)
+                      : bwd_type<__nv_bfloat16>(a, stream);
 }
 
 }  // namespace swg
