@@ -9,7 +9,6 @@ library is missing the import of this module raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -552,35 +551,30 @@ def swiglu_bwd_b_noalloc(dy, g, fc, dg=None, dfc=None, db_g=None, db_fc=None, st
 
 
 # ------------------------------------------------------------- row-wise operators
-def _on_stream(fn):
-    """Give a row-wise operator its `stream` argument: with one, everything the call does (copies of
-    strided inputs, allocations, kernels) is on that stream, and the caller's tensors are recorded
-    on it, so that their memory is not handed out again before it has run."""
-
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
-        if stream is None:
-            return fn(*args, **kwargs)
-        tensors = [t for t in (*args, *kwargs.values(), *(kwargs.get("out") or {}).values())
-                   if isinstance(t, torch.Tensor) and t.is_cuda]
-        if not tensors:
-            return fn(*args, **kwargs)  # raises
-        dev = tensors[0].device
-        handle = _stream(stream, dev)
-        s = torch.cuda.default_stream(dev) if handle == 0 else torch.cuda.ExternalStream(handle, device=dev)
-        with torch.cuda.stream(s):
-            out = fn(*args, **kwargs)
-        for t in tensors:
-            t.record_stream(s)
-        return out
-
-    return call
+def _on_stream(stream, fn, *args, **kwargs):
+    """Run a row-wise operator on `stream`: everything the call does (copies of strided inputs,
+    allocations, kernels) is on that stream, and the caller's tensors are recorded on it, so that their
+    memory is not handed out again before it has run."""
+    tensors = [t for t in (*args, *kwargs.values(), *(kwargs.get("out") or {}).values())
+               if isinstance(t, torch.Tensor) and t.is_cuda]
+    if not tensors:
+        return fn(*args, **kwargs)  # raises
+    dev = tensors[0].device
+    handle = _stream(stream, dev)
+    s = torch.cuda.default_stream(dev) if handle == 0 else torch.cuda.ExternalStream(handle, device=dev)
+    with torch.cuda.stream(s):
+        out = fn(*args, **kwargs)
+    for t in tensors:
+        t.record_stream(s)
+    return out
 
 
 def _run(what, fn, dev, *args):
     """One C call on `dev` and its current stream; raises on an error status."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    index = dev.index
+    # the current stream's handle without building a Stream object around it (2 us of a 10 us call)
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
         status = fn(*args, stream)
     else:
         status = _call(dev, fn, *args, stream)
@@ -650,12 +644,13 @@ def _norm_weights(gamma, beta, N, x):
     return gamma, beta, w.dtype if w is not None else x.dtype
 
 
-@_on_stream
-def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, out: dict | None = None) -> dict:
+def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, out: dict | None = None, stream=None) -> dict:
     """Layer norm of x [..., N] over its last dimension (fp32/fp16/bf16): a dict of y and stats [M, 2]
     (fp32 mean and 1/sqrt(var + eps) of the M rows), and of h = x + residual, the tensor that is
     normalised, when a residual of x's shape is given. gamma, beta [N] (x's dtype or fp32, both the
     same) may be None. `out` may supply any of the outputs; stream: the stream to run on."""
+    if stream is not None:
+        return _on_stream(stream, layer_norm_fwd, x, gamma, beta, eps=eps, residual=residual, out=out)
     shape = x.shape if isinstance(x, torch.Tensor) else None
     xt, M, N, ldx, code = _row_tensor(x, "x")
     res, ldr = _like_rows(residual, "residual", xt, shape)
@@ -684,13 +679,15 @@ def layer_norm_bwd_workspace_size(M: int, N: int) -> int:
     return lib.layer_norm_bwd_workspace_size(M, N)
 
 
-@_on_stream
 def layer_norm_bwd(dy, x, stats, gamma=None, dh=None, params: bool = True, dx=None, dgamma=None, dbeta=None,
-                   workspace=None):
+                   workspace=None, stream=None):
     """Layer norm backward: (dx, dgamma, dbeta) for dy and x [..., N], x being the tensor that was
     normalised (the forward's h when it had a residual) and stats the forward's. gamma may be None (1);
     dgamma and dbeta have its dtype (x's without it) and are None when params is False. dh, if given, is
     the gradient that reaches the normalised tensor past the norm: it is added to dx."""
+    if stream is not None:
+        return _on_stream(stream, layer_norm_bwd, dy, x, stats, gamma=gamma, dh=dh, params=params, dx=dx, dgamma=dgamma,
+                          dbeta=dbeta, workspace=workspace)
     shape = x.shape if isinstance(x, torch.Tensor) else None
     xt, M, N, ldx, code = _row_tensor(x, "x")
     if dy is None:
@@ -731,15 +728,17 @@ def _dlogits(t, shape, x, M, N):
     raise ValueError(f"dlogits must be a {x.dtype} CUDA tensor of shape {tuple(shape)} on {x.device} with dense rows")
 
 
-@_on_stream
 def token_logprobs_fwd(logits, targets=None, top_k: int = 0, temperature: float = 1.0, ignore_index: int = -100,
-                       out: dict | None = None) -> dict:
+                       out: dict | None = None, stream=None) -> dict:
     """Log probabilities of the given tokens under softmax(logits / temperature), logits [..., V]
     (fp32/fp16/bf16, rows may lie apart): a dict of logp [...] (absent without targets; 0 where the
     target is ignore_index, NaN for another target outside the vocabulary), entropy [...], stats [T, 2]
     for the backward, and with top_k (at most 32) top_logp and top_idx [..., top_k], the largest logits
     in descending order, equal ones by the lower index. targets: int64 or int32 of logits' leading
     shape. `out` may supply any of the outputs; stream: the stream to run on."""
+    if stream is not None:
+        return _on_stream(stream, token_logprobs_fwd, logits, targets, top_k=top_k, temperature=temperature,
+                          ignore_index=ignore_index, out=out)
     lead = logits.shape[:-1] if isinstance(logits, torch.Tensor) else None
     z, T, V, ld, code = _row_tensor(logits, "logits")
     dev = z.device
@@ -763,12 +762,14 @@ def _itype(t):
     return 0 if t is not None and t.dtype == torch.int32 else 1
 
 
-@_on_stream
 def token_logprobs_bwd(dlogp, logits, targets, stats, dentropy=None, entropy=None, temperature: float = 1.0,
-                       ignore_index: int = -100, dlogits=None):
+                       ignore_index: int = -100, dlogits=None, stream=None):
     """The gradient of token_logprobs_fwd with respect to the logits, from its stats (and its entropy,
     when dentropy is given). dlogp and targets may be None together. dlogits may be the logits
     themselves."""
+    if stream is not None:
+        return _on_stream(stream, token_logprobs_bwd, dlogp, logits, targets, stats, dentropy=dentropy, entropy=entropy,
+                          temperature=temperature, ignore_index=ignore_index, dlogits=dlogits)
     shape = logits.shape if isinstance(logits, torch.Tensor) else None
     z, T, V, ld, code = _row_tensor(logits, "logits")
     dev = z.device
@@ -796,12 +797,13 @@ def _distill_inputs(logits, teacher_ids, teacher_logits):
     return shape, z, T, V, ld, code, ids, tl, K
 
 
-@_on_stream
-def distill_fwd(logits, teacher_ids, teacher_logits, temperature: float = 1.0, out: dict | None = None) -> dict:
+def distill_fwd(logits, teacher_ids, teacher_logits, temperature: float = 1.0, out: dict | None = None, stream=None) -> dict:
     """Distillation loss of student logits [..., V] (fp32/fp16/bf16, rows may lie apart) against a
     teacher's top logits: teacher_ids [..., K] (int64 or int32; outside the vocabulary: absent) and
     teacher_logits [..., K] (fp32/fp16/bf16). A dict of loss [...] = sum q (ln q - ln p), q the softmax of
     the entries and p the student's, both at `temperature`, and stats [T, 2] for the backward."""
+    if stream is not None:
+        return _on_stream(stream, distill_fwd, logits, teacher_ids, teacher_logits, temperature=temperature, out=out)
     shape, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
     given = out or {}
     out = {"loss": _out(given.get("loss"), shape[:-1], torch.float32, z.device, "loss"),
@@ -811,10 +813,12 @@ def distill_fwd(logits, teacher_ids, teacher_logits, temperature: float = 1.0, o
     return out
 
 
-@_on_stream
-def distill_bwd(weight, logits, teacher_ids, teacher_logits, stats, temperature: float = 1.0, dlogits=None):
+def distill_bwd(weight, logits, teacher_ids, teacher_logits, stats, temperature: float = 1.0, dlogits=None, stream=None):
     """The gradient of sum(weight * loss) with respect to the logits, weight [...] fp32, from the
     forward's stats. dlogits may be the logits themselves."""
+    if stream is not None:
+        return _on_stream(stream, distill_bwd, weight, logits, teacher_ids, teacher_logits, stats, temperature=temperature,
+                          dlogits=dlogits)
     shape, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
     weight, stats = _vector(weight, "weight", T, _F32, z.device), _vector(stats, "stats", 2 * T, _F32, z.device)
     dlogits, ldo = _dlogits(dlogits, shape, z, T, V)
@@ -823,12 +827,13 @@ def distill_bwd(weight, logits, teacher_ids, teacher_logits, stats, temperature:
     return dlogits
 
 
-@_on_stream
 def distill_fwd_bwd(logits, teacher_ids, teacher_logits, weight, temperature: float = 1.0,
-                    out: dict | None = None) -> dict:
+                    out: dict | None = None, stream=None) -> dict:
     """distill_fwd and distill_bwd in one call, for a weight known beforehand (1 / T for a mean): a dict of
     loss, stats and dlogits. Where a row fits on the chip the logits are read once. `out` may supply any
     of the outputs; out["dlogits"] may be the logits themselves."""
+    if stream is not None:
+        return _on_stream(stream, distill_fwd_bwd, logits, teacher_ids, teacher_logits, weight, temperature=temperature, out=out)
     shape, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
     weight = _vector(weight, "weight", T, _F32, z.device)
     given = out or {}

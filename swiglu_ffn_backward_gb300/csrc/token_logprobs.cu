@@ -61,11 +61,24 @@ __device__ __forceinline__ int rank_candidates(const uint64_t* cand, int n, int 
   return n < top ? n : top;
 }
 
+// Two descending lists of 32 keys, one key a lane -> the 32 best of both, descending: the larger of one
+// list and the other one reversed are those, in bitonic order.
+__device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t r = __shfl_sync(0xffffffffu, b, 31 - lane);
+  a = r > a ? r : a;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t p = __shfl_xor_sync(0xffffffffu, a, o);
+    a = ((lane & o) == 0) == (p > a) ? p : a;
+  }
+  return a;
+}
+
 // One warp: the `top` best logits above -inf of a share, from the threads' bests -> best. done(): the
-// threads' bests have been read.
-template <typename T, typename Done>
-__device__ __forceinline__ int select_best(const T* z, int64_t V, const Share& sh, int top, Finish& f, uint64_t* best,
-                                           Done done) {
+// threads' bests have been read; load(g): the row's vector g.
+template <typename T, typename Done, typename Load>
+__device__ __forceinline__ int select_best(const Share& sh, int top, Finish& f, uint64_t* best, Done done, Load load) {
   constexpr int E = Traits<T>::E;
   const int lane = threadIdx.x & 31;
   uint64_t column = 0;
@@ -74,10 +87,12 @@ __device__ __forceinline__ int select_best(const T* z, int64_t V, const Share& s
     const uint64_t k = f.keys[i * 32 + lane];
     column = k > column ? k : column;
   }
+  f.cand[lane] = column;
+  __syncwarp();
   int above = 0;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
-    const uint64_t o = __shfl_sync(0xffffffffu, column, j);
+    const uint64_t o = f.cand[j];
     above += o > column || (o == column && j < lane) ? 1 : 0;
   }
   const uint64_t bound = __shfl_sync(0xffffffffu, column, __ffs(__ballot_sync(0xffffffffu, above == top - 1)) - 1);
@@ -105,7 +120,7 @@ __device__ __forceinline__ int select_best(const T* z, int64_t V, const Share& s
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       if (g + u < sh.end) {
-        v[u] = load_row_vec<T, true>(z, first_element<T>(sh, g + u), V);
+        v[u] = load(g + u);
       } else {
 #pragma unroll
         for (int w = 0; w < 4; ++w) v[u].w[w] = Traits<T>::kNegInf;
@@ -195,8 +210,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1) tlp_fwd_kernel(const TlpFwdArg
         if (lane == 0) mbar_arrive(&sm.taken[me]);
       };
       __syncwarp();
-      if (a.top > 0) n = select_best(z, a.V, sh, a.top, f, f.best[rank], taken);
-      else taken();
+      if (a.top > 0) {
+        // a row of its own is still in the ring; else it has left it for L2
+        const bool held = S > 1 && sh.end - sh.begin <= kStages * kStageVecs;
+        n = select_best<T>(sh, a.top, f, f.best[rank], taken, [&](int g) {
+          if (!held) return load_row_vec<T, true>(z, first_element<T>(sh, g), a.V);
+          const uint4 u = reinterpret_cast<const uint4*>(dyn)[g - sh.begin];
+          return Vec{{u.x, u.y, u.z, u.w}};
+        });
+      } else {
+        taken();
+      }
       uint64_t mine = lane < n ? f.best[rank][lane] : 0;  // lane i: the i-th best
       if (rank != 0) {
         if (lane == 0) send_f4(&f.block[rank], &sm.sent, 0, p);
@@ -209,17 +233,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1) tlp_fwd_kernel(const TlpFwdArg
         __syncwarp();
         wait.cluster(&sm.sent, 0);
         p = join_sums(lane < S ? f.block[lane] : none, c2, k);
-        // the lists' heads against one another, a lane for each list
-        uint64_t all = 0;
-        int at = 0;
-        for (n = 0; n < a.top; ++n) {
-          const uint64_t head = lane < S && at < a.top ? f.best[lane & (kMaxCluster - 1)][at] : 0;  // 0: no more
-          const uint64_t b = warp_max(head);
-          if (b == 0) break;
-          if (head == b) ++at;
-          if (lane == n) all = b;
+        if (a.top > 0) {
+          uint64_t list[kMaxCluster];
+#pragma unroll
+          for (int i = 0; i < kMaxCluster; ++i) list[i] = i < S ? f.best[i][lane] : 0;
+#pragma unroll
+          for (int half = kMaxCluster / 2; half > 0; half /= 2) {
+#pragma unroll
+            for (int i = 0; i < half; ++i) list[i] = merge_lists(list[i], list[i + half]);
+          }
+          mine = list[0];
+          n = min(a.top, __popc(__ballot_sync(0xffffffffu, mine != 0)));
         }
-        mine = all;
       }
       const float m = p.w;
       // H = ln s - (1/s) sum 2^x x ln 2, with s and x of one reference; then s at the maximum
