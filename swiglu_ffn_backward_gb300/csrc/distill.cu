@@ -153,31 +153,34 @@ __device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g,
 // ---- loss, and loss with gradient
 
 constexpr int kExtraWarps = 3;  // producer, teacher, joiner
-constexpr int kFwdThreads = kStreamThreads + 32 * kExtraWarps;
 constexpr int kStages = 6;      // of the ring
-constexpr int kRingBytes = kStages * kStageBytes;
 constexpr int kSlots = 4;       // exchange slots: a slot is written again four rows later
 constexpr int kShareStages = 2; // stages a row's share may hold: two rows' shares, and two stages ahead
 
+template <int W>
 struct KdStream {
-  Ring<kStages> ring;
+  Ring<W, kStages> ring;
   uint64_t joined[kSlots];  // the row's maxima and sums have come from all blocks
   uint64_t ready[2];        // the row's entries are in shared memory
   uint64_t spare[2];        // their readers are done with them
   uint64_t solved[2];       // the row's gradient constants are in shared memory
-  float4 part[kSlots][kMaxCluster][kStreamWarps];  // every warp's sums (WarpSums::result)
+  float4 part[kSlots][kMaxCluster][W];  // every warp's sums (WarpSums::result)
   float2 note[kSlots];      // from the first block: its entries' logits have been read
   Gradient grad[2];
   float weight[2];
+  uint16_t own[W][32];      // a warp's entries of the row
   float sq[2];              // sum exp((t - max t) / tau), 0 for a row without entries
 };
-// the entries of two rows follow the ring in dynamic shared memory
+// the entries of two rows follow the ring in dynamic shared memory, K of each array
 struct EntryArrays {
-  int id[kKdMaxEntries];    // -1: absent
-  float td[kKdMaxEntries];  // teacher logits less their maximum; exp(td / tau) / sq are the probabilities
-  float z[kKdMaxEntries];   // the student's logits (first block)
+  int* id;    // -1: absent
+  float* td;  // teacher logits less their maximum; exp(td / tau) / sq are the probabilities
+  float* z;   // the student's logits (first block)
 };
-constexpr size_t kFwdSmem = kRingBytes + 2 * sizeof(EntryArrays);
+__device__ __forceinline__ EntryArrays entry_arrays(unsigned char* at, int K, int b) {
+  int* p = reinterpret_cast<int*>(at) + b * 3 * K;
+  return EntryArrays{p, reinterpret_cast<float*>(p + K), reinterpret_cast<float*>(p + 2 * K)};
+}
 
 // One warp takes the entries of row after row: the first kAhead of a row are loaded while the row before
 // is worked on.
@@ -240,7 +243,7 @@ __device__ __forceinline__ void read_some(const KdArgs& a, const T* z, int k0, b
 // Loads the first entries of row `next` into `first`. wait(): the arrays are free.
 template <typename T, typename Wait>
 __device__ __forceinline__ void take_entries(const KdArgs& a, int64_t r, int64_t next, EntryLoads& first,
-                                             EntryArrays& n, bool gather, float& sq, Wait wait) {
+                                             const EntryArrays& n, bool gather, float& sq, Wait wait) {
   const int lane = threadIdx.x & 31;
   const float c2 = a.inv_temp * kLog2e;
   const T* z = static_cast<const T*>(a.logits) + r * a.ld;
@@ -267,6 +270,7 @@ __device__ __forceinline__ void take_entries(const KdArgs& a, int64_t r, int64_t
     read_some(a, z, k0, gather, now, v);
   }
   const float me = finite_or_0(warp_max(m));
+  __syncwarp();
   float s = 0.f;
   for (int k = lane; k < a.K; k += 32) {
     const float d = n.td[k] - me;
@@ -276,23 +280,26 @@ __device__ __forceinline__ void take_entries(const KdArgs& a, int64_t r, int64_t
   sq = warp_sum(s);
 }
 
-template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, Split split, uint32_t* status) {
+template <typename T, bool kGrad, int W>
+__global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
+    kd_fwd_kernel(const KdArgs a, Split split, uint32_t* status) {
   constexpr int E = Traits<T>::E;
+  constexpr int kStreamThreads = Shape<W>::kThreads, kStageVecs = Shape<W>::kStageVecs;
+  constexpr int kStageBytes = Shape<W>::kStageBytes;
   extern __shared__ __align__(128) unsigned char dyn[];
-  __shared__ KdStream sm;
+  __shared__ KdStream<W> sm;
   const int S = split.S;
-  EntryArrays* entries = reinterpret_cast<EntryArrays*>(dyn + kRingBytes);
+  auto entries = [&](int b) { return entry_arrays(dyn + kStages * kStageBytes, a.K, b); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank());
   const int64_t first = blockIdx.x / S, step = gridDim.x / S;
-  const uint32_t bytes = static_cast<uint32_t>(S * kStreamWarps * sizeof(float4) + sizeof(float2));
+  const uint32_t bytes = static_cast<uint32_t>(S * W * sizeof(float4) + sizeof(float2));
   if (tid == 0) {
     ring_init(sm.ring);
     for (int i = 0; i < kSlots; ++i) mbar_init(&sm.joined[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.ready[i], 1);
-      mbar_init(&sm.spare[i], kGrad ? kStreamWarps + 1 : 1);
+      mbar_init(&sm.spare[i], kGrad ? W + 1 : 1);
       mbar_init(&sm.solved[i], 1);
     }
     fence_mbar_init();
@@ -304,9 +311,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
   Patience wait;
   const float c2 = a.inv_temp * kLog2e;
 
-  if (warp == kStreamWarps) {
-    produce_rows<T>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, sm.ring, wait);
-  } else if (warp == kStreamWarps + 1) {
+  if (warp == W) {
+    produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, sm.ring, wait);
+  } else if (warp == W + 1) {
     EntryLoads ahead;
     load_some(a, first, 0, ahead);
     int64_t it = 0;
@@ -314,7 +321,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       const int b = static_cast<int>(it & 1), slot = static_cast<int>(it & (kSlots - 1));
       const float w = kGrad ? a.weight[r] : 0.0f;
       float sq;
-      take_entries<T>(a, r, r + step, ahead, entries[b], rank == 0, sq,
+      take_entries<T>(a, r, r + step, ahead, entries(b), rank == 0, sq,
                       [&]() { wait(&sm.spare[b], static_cast<uint32_t>((it >> 1) & 1) ^ 1u); });
       if (lane == 0) {
         sm.sq[b] = sq;
@@ -326,7 +333,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       if (rank == 0 && lane < S) send_f2(&sm.note[slot], &sm.joined[slot], static_cast<uint32_t>(lane), 0.f, 0.f);
       __syncwarp();
     }
-  } else if (warp == kStreamWarps + 2) {
+  } else if (warp == W + 2) {
     // joins the row's maxima and sums, and forms the constants of its gradient and (first block) its loss
     int64_t it = 0;
     for (int64_t r = first; r < a.T; r += step, ++it) {
@@ -336,10 +343,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       // lane by lane (up to four parts each), then the lanes
       const float4* part = &sm.part[slot][0][0];
       float m = neg_inf(), s = 0.f, top = neg_inf();
-      for (int i = lane; i < S * kStreamWarps; i += 32) m = fmaxf(m, part[i].x);
+      for (int i = lane; i < S * W; i += 32) m = fmaxf(m, part[i].x);
       m = warp_max(m);
       const Scale k = scale_of(m, c2);
-      for (int i = lane; i < S * kStreamWarps; i += 32) {
+      for (int i = lane; i < S * W; i += 32) {
         const float4 p = part[i];
         s = fmaf(ex2_approx(ref_shift(p.x, scale_of(p.x, c2), m, k, c2)), p.y, s);
         top = fmaxf(top, p.w);
@@ -355,7 +362,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       if (rank == 0) {
         // sum q (ln q - ln p) = sum (q / tau) (td - (z - max z)) - ln sq + ln s: a mask of the type's
         // lowest value leaves the range of fp32 only where the loss does
-        const EntryArrays& n = entries[b];
+        const EntryArrays n = entries(b);
         const float me = finite_or_0(top), f = a.inv_temp / sq;
         float l = 0.f;
         for (int i = lane; i < a.K; i += 32) {
@@ -382,7 +389,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       for (int at = sh.begin; at < sh.end; at += kStageVecs) {
         Vec v[4];
         wait(&sm.ring.full[in.stage], in.parity);
-        read_stage<T>(v, dyn + in.stage * kStageBytes, min(sh.end - at, kStageVecs));
+        read_stage<T, W>(v, dyn + in.stage * kStageBytes, min(sh.end - at, kStageVecs));
         sum.add(v, c2, false);
         if (!kGrad) {
           __syncwarp();
@@ -404,14 +411,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
       T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
       const Share sh = share_of(z, a.V, split.per, rank);
       const bool aligned = row_shift(out) == sh.shift;
-      const EntryArrays& n = entries[b];
+      const EntryArrays n = entries(b);
       const Gradient g = sm.grad[b];
       const bool some = sm.weight[b] != 0.0f;
       const Place<kStages> begin = held;
       for (int c = sh.begin; c < sh.end; c += kStageVecs) {
         Vec v[4];
         const int cnt = min(sh.end - c, kStageVecs);
-        read_stage<T>(v, dyn + held.stage * kStageBytes, cnt);
+        read_stage<T, W>(v, dyn + held.stage * kStageBytes, cnt);
         const int64_t e0 = first_element<T>(sh, c), e1 = first_element<T>(sh, c + cnt);
         const bool inner = aligned && e0 >= 0 && e1 <= a.V;  // the stage has whole vectors only
 #pragma unroll
@@ -433,28 +440,67 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
         }
         held.next();
       }
-      // The elements at the entries, over the dense part that this warp has written. The entries of one id
-      // are all of one warp, which adds them together lane by lane.
+      // The elements at the entries, over the dense part that this warp has written. All entries of one id
+      // are of one warp; it lists its own ones, 32 at most: where there are more, those of each of a
+      // thread's four vectors by themselves.
       __syncwarp();
       if (some) {
+        auto vec_of = [&](int id) { return (id + sh.shift) / E - sh.begin; };  // of the share's
+        auto store = [&](int id, float q) {
+          const int vec = vec_of(id);
+          int stage = begin.stage + vec / kStageVecs;
+          if (stage >= kStages) stage -= kStages;
+          const T* p = reinterpret_cast<const T*>(dyn + stage * kStageBytes + (vec % kStageVecs) * 16);
+          const float x = fmaf(to_f(p[(id + sh.shift) % E]), g.k.c, -g.k.ref);
+          out[id] = from_f<T>(fmaf(g.dense, ex2_approx(x), -g.sparse * q));
+        };
+        int parts = 1, part = 0;
+        auto own = [&](int id) {
+          const int vec = vec_of(id);
+          return id >= 0 && vec >= 0 && vec < sh.end - sh.begin && (vec % kStreamThreads) >> 5 == warp &&
+                 (vec / kStreamThreads) % parts == part;
+        };
+        for (; part < parts; ++part) {
+        int have = 0;
         for (int k0 = 0; k0 < a.K; k0 += 32) {
-          const int mine = k0 + lane < a.K ? n.id[k0 + lane] : -1;
-          const int vec = (mine + sh.shift) / E - sh.begin;  // of the share's
-          const bool own = mine >= 0 && vec >= 0 && vec < sh.end - sh.begin && (vec % kStreamThreads) >> 5 == warp;
-          for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo != 0; todo &= todo - 1) {
-            const int from = __ffs(todo) - 1;
-            const int id = __shfl_sync(0xffffffffu, mine, from);
-            const int at = __shfl_sync(0xffffffffu, vec, from);
+          const bool mine = k0 + lane < a.K && own(n.id[k0 + lane]);
+          const uint32_t all = __ballot_sync(0xffffffffu, mine);
+          const int at = have + __popc(all & ((1u << lane) - 1u));
+          if (mine && at < 32) sm.own[warp][at] = static_cast<uint16_t>(k0 + lane);
+          have += __popc(all);
+        }
+        __syncwarp();
+        if (have > 32 && parts == 1) {
+          parts = 4;
+          part = -1;
+          continue;
+        }
+        if (have <= 32) {
+          const int k = lane < have ? sm.own[warp][lane] : 0;
+          const int id = lane < have ? n.id[k] : -1 - lane;
+          float q = ex2_approx(n.td[k] * c2);
+          const uint32_t same = __match_any_sync(0xffffffffu, id);
+          if (__any_sync(0xffffffffu, (same & (same - 1)) != 0)) {  // an id comes twice: added in order
+            float t = 0.f;
+            for (int l = 0; l < have; ++l) {
+              const float x = __shfl_sync(0xffffffffu, q, l);
+              if (same >> l & 1u) t += x;
+            }
+            q = t;
+          }
+          if (lane < have && (same & ((1u << lane) - 1u)) == 0) store(id, q);
+        } else {
+          for (int k0 = 0; k0 < a.K; ++k0) {  // one entry after the other
+            const int id = n.id[k0];
+            if (!own(id)) continue;
             float q = 0.f;
             for (int j = lane; j < a.K; j += 32)
               if (n.id[j] == id) q += ex2_approx(n.td[j] * c2);
             q = warp_sum(q);
-            int stage = begin.stage + at / kStageVecs;
-            if (stage >= kStages) stage -= kStages;
-            const T* p = reinterpret_cast<const T*>(dyn + stage * kStageBytes + (at % kStageVecs) * 16);
-            const float x = fmaf(to_f(p[(id + sh.shift) % E]), g.k.c, -g.k.ref);
-            if (lane == 0) out[id] = from_f<T>(fmaf(g.dense, ex2_approx(x), -g.sparse * q));
+            if (lane == 0) store(id, q);
           }
+        }
+        __syncwarp();
         }
       }
       __syncwarp();
@@ -477,19 +523,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kd_fwd_kernel(const KdArgs a, 
   cluster_wait();
 }
 
-template <typename T, bool kGrad>
+template <typename T, bool kGrad, int W>
 cudaError_t launch_fwd(const KdArgs& a, Split split, cudaStream_t stream) {
   static std::mutex mu;  // guards the occupancy cache
   static StreamCache cache;
+  const size_t smem = kStages * Shape<W>::kStageBytes + static_cast<size_t>(2) * 3 * 4 * a.K;
   std::lock_guard<std::mutex> lk(mu);
-  return launch_stream(kd_fwd_kernel<T, kGrad>, cache, kFwdThreads, kFwdSmem, a.T, split.S, false, stream, a,
+  return launch_stream(kd_fwd_kernel<T, kGrad, W>, cache, 32 * (W + kExtraWarps), smem, a.T, split.S, false, stream, a,
                        split, status_word_ptr());
 }
-template <bool kGrad>
+template <bool kGrad, int W>
 cudaError_t launch_fwd_any(const KdArgs& a, int dtype, Split split, cudaStream_t stream) {
-  return dtype == 0   ? launch_fwd<float, kGrad>(a, split, stream)
-         : dtype == 1 ? launch_fwd<__half, kGrad>(a, split, stream)
-                      : launch_fwd<__nv_bfloat16, kGrad>(a, split, stream);
+  return dtype == 0   ? launch_fwd<float, kGrad, W>(a, split, stream)
+         : dtype == 1 ? launch_fwd<__half, kGrad, W>(a, split, stream)
+                      : launch_fwd<__nv_bfloat16, kGrad, W>(a, split, stream);
 }
 
 // ---- gradient alone
@@ -537,11 +584,20 @@ __global__ void __launch_bounds__(kRowThreads, 3) kd_bwd_kernel(const KdArgs a, 
 cudaError_t launch_distill(const KdArgs& a, bool forward, bool backward, int dtype, cudaStream_t stream) {
   const int sms = device_sm_count();
   const int64_t vectors = row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2);
+  // Blocks of four computing warps, three an SM, take short rows (up to 1024 vectors, 16 KB), blocks of 16
+  // long ones: bf16 logits with 64 entries, loss and gradient, 8192 columns 139 us against 285 us with 16
+  // warps (16384 rows), 32768 columns (4096 rows, two blocks of four a row) 144 us against 106 us. Without a
+  // gradient four warps are as fast for long rows too, once each of those blocks has two rows.
+  constexpr int64_t big = kShareStages * Shape<16>::kStageVecs, small = kShareStages * Shape<4>::kStageVecs;
   // the row's shares have to stay in the rings for the gradient: a longer row is read twice
-  const bool once = forward && backward && vectors <= int64_t(kMaxCluster) * kShareStages * kStageVecs;
-  if (once) return launch_fwd_any<true>(a, dtype, split_row(a.T, vectors, kShareStages * kStageVecs, sms), stream);
+  if (forward && backward && vectors <= small)
+    return launch_fwd_any<true, 4>(a, dtype, split_row(a.T, vectors, small, sms), stream);
+  if (forward && backward && vectors <= kMaxCluster * big)
+    return launch_fwd_any<true, 16>(a, dtype, split_row(a.T, vectors, big, sms), stream);
   if (forward) {
-    const cudaError_t e = launch_fwd_any<false>(a, dtype, split_row(a.T, vectors, vectors, sms), stream);
+    const Split all = split_row(a.T, vectors, vectors, sms);
+    const cudaError_t e = vectors <= small || a.T >= 6 * sms ? launch_fwd_any<false, 4>(a, dtype, all, stream)
+                                                             : launch_fwd_any<false, 16>(a, dtype, all, stream);
     if (e != cudaSuccess || !backward) return e;
   }
   KdArgs b = a;

@@ -9,7 +9,7 @@
 // Forward: bound by HBM (V elements read a row). A persistent kernel streams rows through shared memory
 // (vocab_stream.cuh); S blocks of a cluster share a row only when there are too few rows for the SMs.
 // The 16 computing warps keep (max, sum 2^x, sum 2^x x) and each thread its best logit and the run of four
-// vectors that has it. Four more warps finish rows in turn, under the work on the next ones: they join
+// vectors that has it. A few more warps finish rows in turn, under the work on the next ones: they join
 // the sums, and select the alternatives from the threads' bests. The 32 lane columns' bests have a k-th
 // largest, which at least k logits reach; the few threads with a best at or above it (about k + k^2 / 64)
 // are looked through again (their runs come from L2), and the logits found are ranked against one another.
@@ -24,38 +24,58 @@ namespace {
 using namespace row;
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kStages = 5;      // of the ring
-constexpr int kRingBytes = kStages * kStageBytes;
-constexpr int kSelectors = 4;   // warps that finish rows
-constexpr int kFwdThreads = kStreamThreads + 32 * (1 + kSelectors);
 constexpr int kCand = 512;      // candidates held; more are cut to the best before the search goes on
+constexpr int kListed = 288;    // groups of runs listed before they are looked through
 
+// blocks of 16 computing warps take long rows and share a row, those of four take many short ones
+template <int W>
+struct Plan {
+  static constexpr int kStages = W == 16 ? 5 : 4;              // of the ring
+  static constexpr int kSelectors = W == 16 ? 3 : 4;           // warps that finish rows
+  static constexpr int kTableBytes = W == 16 ? 8192 : 4096;
+  static constexpr int kBlocks = W == 16 ? kMaxCluster : 1;    // of a row, at most
+  static constexpr int kThreads = 32 * (W + 1 + kSelectors);
+};
+
+template <int W>
 struct TlpSync {
-  Ring<kStages> ring;
-  uint64_t told[kSelectors];   // the computing warps have written a row's results
-  uint64_t taken[kSelectors];  // the selector has read them
-  uint64_t sent;               // first block: the other blocks' results have come
+  Ring<W, Plan<W>::kStages> ring;
+  uint64_t told[Plan<W>::kSelectors];   // the computing warps have written a row's results
+  uint64_t taken[Plan<W>::kSelectors];  // the selector has read them
+  uint64_t sent;                  // first block: the other blocks' results have come
 };
 // one selector's, behind the ring in dynamic shared memory
+template <int W>
 struct Finish {
-  uint64_t keys[kStreamThreads];         // a thread's best logit and its run, 0 for none
-  uint64_t cand[kCand];
-  uint64_t best[kMaxCluster][kMaxTop];   // by block; sorted, the better first
-  float4 block[kMaxCluster];             // the blocks' sums (WarpSums::result)
-  float4 part[kStreamWarps];             // the computing warps'
-  uint16_t who[kStreamThreads];          // threads to look through again
-  int count;
+  // the largest logit of every group of a thread's runs (as they are in the row, -inf for none): group j
+  // of thread t at j * threads + t
+  unsigned char table[Plan<W>::kTableBytes];
+  uint64_t keys[Shape<W>::kThreads];     // a thread's best logit and its group, 0 for none
+  alignas(16) uint64_t cand[kCand];
+  uint4 runs[4][32];                     // the runs looked at: vector u of lane l at [u][l]
+  uint64_t best[Plan<W>::kBlocks][kMaxTop];  // by block; sorted, the better first
+  float4 block[Plan<W>::kBlocks];        // the blocks' sums (WarpSums::result)
+  float4 part[W];                        // the computing warps'
+  uint16_t list[kListed];                // groups to look through
 };
-constexpr size_t kFwdSmem = kRingBytes + kSelectors * sizeof(Finish);
+template <int W>
+constexpr size_t kFwdSmem = Plan<W>::kStages * Shape<W>::kStageBytes + Plan<W>::kSelectors * sizeof(Finish<W>);
 
 // One warp: the `top` best of cand[0 .. n) -> best, in order; returns how many there are.
 __device__ __forceinline__ int rank_candidates(const uint64_t* cand, int n, int top, uint64_t* best) {
+  const int lane = threadIdx.x & 31;
   __syncwarp();
-  for (int t = threadIdx.x & 31; t < n; t += 32) {
-    const uint64_t key = cand[t];
-    int place = 0;
-    for (int j = 0; j < n; ++j) place += cand[j] > key ? 1 : 0;
-    if (place < top) best[place] = key;
+  for (int t0 = 0; t0 < n; t0 += 64) {  // two keys a lane against all
+    const uint64_t a = t0 + lane < n ? cand[t0 + lane] : 0, b = t0 + 32 + lane < n ? cand[t0 + 32 + lane] : 0;
+    int pa = 0, pb = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const uint64_t o = cand[j];
+      pa += o > a ? 1 : 0;
+      pb += o > b ? 1 : 0;
+    }
+    if (a != 0 && pa < top) best[pa] = a;
+    if (b != 0 && pb < top) best[pb] = b;
   }
   __syncwarp();
   return n < top ? n : top;
@@ -75,15 +95,25 @@ __device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b) {
   return a;
 }
 
-// One warp: the `top` best logits above -inf of a share, from the threads' bests -> best. done(): the
-// threads' bests have been read; load(g): the row's vector g.
-template <typename T, typename Done, typename Load>
-__device__ __forceinline__ int select_best(const Share& sh, int top, Finish& f, uint64_t* best, Done done, Load load) {
-  constexpr int E = Traits<T>::E;
+// stages of one thread's group: one, or as many as let the table hold the share
+template <typename T, int W>
+__device__ __forceinline__ int group_stages(const Share& sh) {
+  const int stages = (sh.end - sh.begin + Shape<W>::kStageVecs - 1) / Shape<W>::kStageVecs;
+  constexpr int kGroups = Plan<W>::kTableBytes / static_cast<int>(sizeof(T)) / Shape<W>::kThreads;  // a thread
+  return stages <= kGroups ? 1 : (stages + kGroups - 1) / kGroups;
+}
+
+// One warp: the `top` best logits above -inf of a share, from the threads' bests and the table -> best.
+// done(): both have been read; load(g): the row's vector g.
+template <typename T, int W, typename Done, typename Load>
+__device__ __forceinline__ int select_best(const Share& sh, int top, Finish<W>& f, uint64_t* best, Done done,
+                                           Load load) {
+  constexpr int E = Traits<T>::E, kThreads = Shape<W>::kThreads, kStageVecs = Shape<W>::kStageVecs;
   const int lane = threadIdx.x & 31;
-  uint64_t column = 0;
+  // the lane columns' bests; an empty one counts as a key of its own below all others
+  uint64_t column = 31 - lane;
 #pragma unroll
-  for (int i = 0; i < kStreamWarps; ++i) {
+  for (int i = 0; i < W; ++i) {
     const uint64_t k = f.keys[i * 32 + lane];
     column = k > column ? k : column;
   }
@@ -91,78 +121,127 @@ __device__ __forceinline__ int select_best(const Share& sh, int top, Finish& f, 
   __syncwarp();
   int above = 0;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const uint64_t o = f.cand[j];
-    above += o > column || (o == column && j < lane) ? 1 : 0;
+  for (int j = 0; j < 32; j += 2) {
+    const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(f.cand + j);
+    above += (o.x > column ? 1 : 0) + (o.y > column ? 1 : 0);
   }
-  const uint64_t bound = __shfl_sync(0xffffffffu, column, __ffs(__ballot_sync(0xffffffffu, above == top - 1)) - 1);
-  int threads = 0;
-#pragma unroll
-  for (int i = 0; i < kStreamWarps; ++i) {
-    const uint64_t k = f.keys[i * 32 + lane];
-    const bool good = k != 0 && k >= bound;
-    const uint32_t all = __ballot_sync(0xffffffffu, good);
-    if (good) f.who[threads + __popc(all & ((1u << lane) - 1u))] = static_cast<uint16_t>(i * 32 + lane);
-    threads += __popc(all);
-  }
-  if (lane == 0) f.count = 0;
+  uint64_t bound = __shfl_sync(0xffffffffu, column, __ffs(__ballot_sync(0xffffffffu, above == top - 1)) - 1);
+  if (bound < 32) bound = 0;
   __syncwarp();
-  done();
-  // a logit reaches the bound if it is larger, or equal and in the same run or before it
-  float least = bound != 0 ? rank_logit(bound) : neg_inf();
-  uint64_t least_key =
-      bound != 0 ? rank_key(least, static_cast<uint32_t>(first_element<T>(sh, sh.begin + 4 * static_cast<int>(rank_index(bound)) + 4) - 1)) : 0;
-  const int stages = (sh.end - sh.begin + kStageVecs - 1) / kStageVecs, items = threads * stages;
-  for (int i0 = 0; i0 < items; i0 += 32) {  // a run for each lane
-    Vec v[4];
-    const int i = i0 + lane, q = i / stages;
-    const int g = i < items ? sh.begin + (i - q * stages) * kStageVecs + 4 * f.who[q] : sh.end;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (g + u < sh.end) {
-        v[u] = load(g + u);
-      } else {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) v[u].w[w] = Traits<T>::kNegInf;
+  // A group reaches the bound with a larger logit, or with an equal one if it is the bound's group or one
+  // before it in the row: groups of one run follow each other, those of several stages only by stages. A
+  // logit reaches it likewise, up to the end of those groups.
+  T least = lowest<T>();
+  int last = 0x7fffffff;  // group
+  uint64_t least_key = 0;
+  const int depth = group_stages<T, W>(sh);  // stages a group
+  if (bound != 0) {
+    least = from_f<T>(rank_logit(bound));
+    last = static_cast<int>(rank_index(bound));
+    if (depth > 1) last |= kThreads - 1;
+    const int64_t stage = static_cast<int64_t>(last / kThreads + 1) * depth - 1;
+    const int64_t end = stage * kStageVecs + 4 * (last % kThreads) + 4;  // of the share's vectors
+    least_key = rank_key(rank_logit(bound), static_cast<uint32_t>(
+                                    min(first_element<T>(sh, sh.begin) + end * E - 1, static_cast<int64_t>(0xfffffffe))));
+  }
+
+  // the runs of the groups listed, one run a lane at a time
+  int have = 0;  // candidates
+  auto look_through = [&](int groups) {
+    const int items = groups * depth;
+    for (int i0 = 0; i0 < items; i0 += 32) {
+      const int i = i0 + lane;
+      int g = sh.end;
+      if (i < items) {
+        const int q = i / depth, group = f.list[q];
+        g = sh.begin + ((group / kThreads) * depth + (i - q * depth)) * kStageVecs + 4 * (group % kThreads);
       }
-    }
+      Vec v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      int n = f.count;
-      if (n > kCand - 32 * E) {
-        // the list could overflow: only the best stay, and the worst of them is the new bound
-        n = rank_candidates(f.cand, n, top, best);
-        for (int t = lane; t < n; t += 32) f.cand[t] = best[t];
-        if (n == top) {
-          least_key = best[top - 1];
-          least = rank_logit(least_key);
-        }
-        if (lane == 0) f.count = n;
-        __syncwarp();
+      for (int u = 0; u < 4; ++u)
+        if (g + u < sh.end) v[u] = load(g + u);
+      uint32_t hits = 0;  // bit by bit, the lane's logits that reach the bound
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (g + u >= sh.end) continue;
+        f.runs[u][lane] = make_uint4(v[u].w[0], v[u].w[1], v[u].w[2], v[u].w[3]);
+        hits |= at_or_above<T>(v[u], least) << (u * E);
       }
-      const float vm = vec_max<T>(v[u]);
-      if (vm >= least && vm > neg_inf()) {
-        const uint32_t e0 = static_cast<uint32_t>(first_element<T>(sh, g + u));
-#pragma unroll
-        for (int p = 0; p < E / 2; ++p) {
-          const float2 x = vec_pair<T>(v[u], p);
-          const uint64_t k0 = rank_key(x.x, e0 + 2 * p), k1 = rank_key(x.y, e0 + 2 * p + 1);
-          if (x.x > neg_inf() && k0 >= least_key) f.cand[atomicAdd(&f.count, 1)] = k0;
-          if (x.y > neg_inf() && k1 >= least_key) f.cand[atomicAdd(&f.count, 1)] = k1;
+      const int64_t e0 = first_element<T>(sh, g);
+      while (__any_sync(0xffffffffu, hits != 0)) {  // one logit a lane at a time
+        uint64_t key = 0;
+        if (hits != 0) {
+          const int at = __ffs(hits) - 1;
+          hits &= hits - 1;
+          const T x = reinterpret_cast<const T*>(&f.runs[at / E][lane])[at % E];
+          key = rank_key(to_f(x), static_cast<uint32_t>(e0 + at));
         }
+        if (have > kCand - 32) {
+          // only the best candidates stay, and the worst of them is the new bound
+          have = rank_candidates(f.cand, have, top, best);
+          for (int t = lane; t < have; t += 32) f.cand[t] = best[t];
+          if (have == top) {
+            least_key = best[top - 1];
+            least = from_f<T>(rank_logit(least_key));
+            last = 0x7fffffff;
+          }
+          __syncwarp();
+        }
+        const bool good = key > least_key || (key != 0 && key == least_key);
+        const uint32_t all = __ballot_sync(0xffffffffu, good);
+        if (good) f.cand[have + __popc(all & ((1u << lane) - 1u))] = key;
+        have += __popc(all);
       }
       __syncwarp();
     }
-  }
-  return rank_candidates(f.cand, f.count, top, best);
-}
-static_assert(kCand - 32 * 8 >= kMaxTop, "room for the best and one vector of every lane");
+  };
 
-template <typename T>
-__global__ void __launch_bounds__(kFwdThreads, 1) tlp_fwd_kernel(const TlpFwdArgs a, Split split, uint32_t* status) {
+  const int groups = ((sh.end - sh.begin + kStageVecs - 1) / kStageVecs + depth - 1) / depth * kThreads;
+  int listed = 0;
+  if (groups == 0) done();
+  for (int i0 = 0; i0 < groups; i0 += 32 * E) {  // E groups a lane
+    const int i = i0 + lane * E;
+    uint32_t hits = 0;
+    if (i < groups) {
+      const uint4 u = reinterpret_cast<const uint4*>(f.table)[i / E];
+      const Vec v = Vec{{u.x, u.y, u.z, u.w}};
+      hits = at_or_above<T>(v, least);
+      if (i + E - 1 > last && hits != 0) {  // behind the bound's group only larger ones count
+#pragma unroll
+        for (int p = 0; p < E / 2; ++p) {
+          const float2 x = vec_pair<T>(v, p);
+          if (i + 2 * p > last && x.x == to_f(least)) hits &= ~(1u << (2 * p));
+          if (i + 2 * p + 1 > last && x.y == to_f(least)) hits &= ~(2u << (2 * p));
+        }
+      }
+    }
+    while (__any_sync(0xffffffffu, hits != 0)) {
+      const bool some = hits != 0;
+      const uint32_t all = __ballot_sync(0xffffffffu, some);
+      if (some) f.list[listed + __popc(all & ((1u << lane) - 1u))] = static_cast<uint16_t>(i + __ffs(hits) - 1);
+      hits &= hits - 1;
+      listed += __popc(all);
+    }
+    __syncwarp();
+    if (i0 + 32 * E >= groups) done();
+    if (listed > kListed - 32 * E || i0 + 32 * E >= groups) {
+      look_through(listed);
+      listed = 0;
+    }
+  }
+  return rank_candidates(f.cand, have, top, best);
+}
+static_assert(kListed >= 32 * 8 && Plan<16>::kTableBytes / 2 <= 65536, "the list takes what one step adds; 16-bit groups");
+static_assert(kListed >= 32 * 8 && Plan<16>::kTableBytes / 2 <= 65536, "the list takes what one step adds; 16-bit groups");
+
+template <typename T, int W>
+__global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 2)
+    tlp_fwd_kernel(const TlpFwdArgs a, Split split, uint32_t* status) {
+  constexpr int kStageVecs = Shape<W>::kStageVecs, kStageBytes = Shape<W>::kStageBytes, kThreads = Shape<W>::kThreads;
+  constexpr int kStages = Plan<W>::kStages, kSelectors = Plan<W>::kSelectors;
   extern __shared__ __align__(128) unsigned char dyn[];
-  __shared__ TlpSync sm;
-  Finish* finish = reinterpret_cast<Finish*>(dyn + kRingBytes);
+  __shared__ TlpSync<W> sm;
+  Finish<W>* finish = reinterpret_cast<Finish<W>*>(dyn + kStages * kStageBytes);
   const int S = split.S;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -171,7 +250,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) tlp_fwd_kernel(const TlpFwdArg
   if (tid == 0) {
     ring_init(sm.ring);
     for (int i = 0; i < kSelectors; ++i) {
-      mbar_init(&sm.told[i], kStreamWarps);
+      mbar_init(&sm.told[i], W);
       mbar_init(&sm.taken[i], 1);
     }
     mbar_init(&sm.sent, 1);
@@ -184,11 +263,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) tlp_fwd_kernel(const TlpFwdArg
   cluster_wait();
   Patience wait;
 
-  if (warp == kStreamWarps) {
-    produce_rows<T>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, sm.ring, wait);
-  } else if (warp > kStreamWarps) {
-    const int me = warp - kStreamWarps - 1;
-    Finish& f = finish[me];
+  if (warp == W) {
+    produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, sm.ring, wait);
+  } else if (warp > W) {
+    const int me = warp - W - 1;
+    Finish<W>& f = finish[me];
     uint32_t parity = 0;
     for (int64_t r = first + me * step; r < a.T; r += kSelectors * step, parity ^= 1u) {
       const T* z = static_cast<const T*>(a.logits) + r * a.ld;
@@ -204,7 +283,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) tlp_fwd_kernel(const TlpFwdArg
       wait(&sm.told[me], parity);
       const float4 none = make_float4(neg_inf(), 0.f, 0.f, neg_inf());
       Scale k;
-      float4 p = join_sums(lane < kStreamWarps ? f.part[lane] : none, c2, k);
+      float4 p = join_sums(lane < W ? f.part[lane] : none, c2, k);
       int n = 0;
       auto taken = [&]() {
         if (lane == 0) mbar_arrive(&sm.taken[me]);
@@ -213,7 +292,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) tlp_fwd_kernel(const TlpFwdArg
       if (a.top > 0) {
         // a row of its own is still in the ring; else it has left it for L2
         const bool held = S > 1 && sh.end - sh.begin <= kStages * kStageVecs;
-        n = select_best<T>(sh, a.top, f, f.best[rank], taken, [&](int g) {
+        n = select_best<T, W>(sh, a.top, f, f.best[rank], taken, [&](int g) {
           if (!held) return load_row_vec<T, true>(z, first_element<T>(sh, g), a.V);
           const uint4 u = reinterpret_cast<const uint4*>(dyn)[g - sh.begin];
           return Vec{{u.x, u.y, u.z, u.w}};
@@ -222,12 +301,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) tlp_fwd_kernel(const TlpFwdArg
         taken();
       }
       uint64_t mine = lane < n ? f.best[rank][lane] : 0;  // lane i: the i-th best
-      if (rank != 0) {
+      if (Plan<W>::kBlocks > 1 && rank != 0) {
         if (lane == 0) send_f4(&f.block[rank], &sm.sent, 0, p);
         send_u64(&f.best[rank][lane], &sm.sent, 0, mine);
         continue;
       }
-      if (S > 1) {
+      if constexpr (Plan<W>::kBlocks > 1) if (S > 1) {
         if (lane == 0) f.block[0] = p;
         f.best[0][lane] = mine;
         __syncwarp();
@@ -276,28 +355,37 @@ __global__ void __launch_bounds__(kFwdThreads, 1) tlp_fwd_kernel(const TlpFwdArg
     uint32_t parity = 1;    // of its `taken`
     for (int64_t r = first; r < a.T; r += step) {
       const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
+      Finish<W>& f = finish[sel];
+      wait(&sm.taken[sel], parity);  // the selector has read the row before in its place
+      T* table = reinterpret_cast<T*>(f.table);
       WarpSums<T, true> sums(c2);
-      float most = neg_inf();  // the thread's maximum and the first run that has it
-      int run = 0;
+      const int depth = group_stages<T, W>(sh);
+      float most = neg_inf(), group_most = neg_inf();  // the thread's maximum, and that of its open group
+      int best = 0, group = tid, left = depth;         // the first group that has it; the open group
       for (int at = sh.begin; at < sh.end; at += kStageVecs) {
         Vec v[4];
         const int cnt = min(sh.end - at, kStageVecs);
         wait(&sm.ring.full[in.stage], in.parity);
-        read_stage_runs<T>(v, dyn + in.stage * kStageBytes, cnt);
+        read_stage_runs<T, W>(v, dyn + in.stage * kStageBytes, cnt);
         const float x = sums.add(v, c2, cnt < kStageVecs);
-        if (x > most) {
-          most = x;
-          run = (at - sh.begin) / 4 + tid;
+        group_most = fmaxf(group_most, x);
+        if (--left == 0 || at + kStageVecs >= sh.end) {
+          if (a.top > 0) table[group] = from_f<T>(group_most);
+          if (group_most > most) {
+            most = group_most;
+            best = group;
+          }
+          group += kThreads;
+          left = depth;
+          group_most = neg_inf();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.ring.empty[in.stage]);
         in.next();
       }
       const float4 p = sums.result();
-      Finish& f = finish[sel];
-      wait(&sm.taken[sel], parity);
       if (lane == 0) f.part[warp] = p;
-      if (a.top > 0) f.keys[tid] = most > neg_inf() ? rank_key(most, static_cast<uint32_t>(run)) : 0;
+      if (a.top > 0) f.keys[tid] = most > neg_inf() ? rank_key(most, static_cast<uint32_t>(best)) : 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.told[sel]);
       if (++sel == kSelectors) {
@@ -313,14 +401,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1) tlp_fwd_kernel(const TlpFwdArg
 }
 static_assert(kMaxTop == 32, "one lane for each alternative");
 
-template <typename T>
+template <typename T, int W>
 cudaError_t launch_fwd(const TlpFwdArgs& a, Split split, cudaStream_t stream) {
   static std::mutex mu;  // guards the occupancy cache
   static StreamCache cache;
   std::lock_guard<std::mutex> lk(mu);
   // a cluster of several blocks takes one row
-  return launch_stream(tlp_fwd_kernel<T>, cache, kFwdThreads, kFwdSmem, a.T, split.S, split.S > 1, stream, a, split,
-                       status_word_ptr());
+  return launch_stream(tlp_fwd_kernel<T, W>, cache, Plan<W>::kThreads, kFwdSmem<W>, a.T, split.S,
+                       split.S > 1, stream, a, split, status_word_ptr());
+}
+template <int W>
+cudaError_t launch_fwd_any(const TlpFwdArgs& a, int dtype, Split split, cudaStream_t stream) {
+  return dtype == 0   ? launch_fwd<float, W>(a, split, stream)
+         : dtype == 1 ? launch_fwd<__half, W>(a, split, stream)
+                      : launch_fwd<__nv_bfloat16, W>(a, split, stream);
 }
 
 // Backward: bound by HBM (V elements read and written a row); no block needs another's results.
@@ -386,9 +480,12 @@ __global__ void __launch_bounds__(kRowThreads) tlp_bwd_kernel(const TlpBwdArgs a
 cudaError_t launch_token_logprobs_fwd(const TlpFwdArgs& a, int dtype, cudaStream_t stream) {
   const int64_t vectors = row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2);
   const Split p = split_row(a.T, vectors, vectors, device_sm_count());
-  return dtype == 0   ? launch_fwd<float>(a, p, stream)
-         : dtype == 1 ? launch_fwd<__half>(a, p, stream)
-                      : launch_fwd<__nv_bfloat16>(a, p, stream);
+  // Blocks of four computing warps, two an SM, take short rows, and rows up to 64 KB when each of those
+  // blocks has several; blocks of 16 take the others. bf16, the 20 best: 8192 columns 103 us against 215 us with
+  // 16 warps (16384 rows), 32768 columns 71 against 77 us (4096 rows), 131072 columns 71 against 58 us (1024).
+  const int64_t sms = device_sm_count();
+  const bool small = p.S == 1 && (vectors <= 1024 || (vectors <= 4096 && a.T >= 6 * sms));
+  return small ? launch_fwd_any<4>(a, dtype, p, stream) : launch_fwd_any<16>(a, dtype, p, stream);
 }
 
 cudaError_t launch_token_logprobs_bwd(const TlpBwdArgs& a, int dtype, cudaStream_t stream) {

@@ -141,6 +141,45 @@ __device__ __forceinline__ float vec_max4<__nv_bfloat16>(const Vec (&v)[4]) {
       larger_halves<__nv_bfloat16, __nv_bfloat162>(v[0], v[1]), larger_halves<__nv_bfloat16, __nv_bfloat162>(v[2], v[3])));
 }
 
+// bit i: element i is at or above `least` (which is not NaN; a NaN element is not)
+template <typename T>
+__device__ __forceinline__ uint32_t at_or_above(const Vec& v, T least);
+template <>
+__device__ __forceinline__ uint32_t at_or_above<float>(const Vec& v, float least) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m |= (__uint_as_float(v.w[i]) >= least ? 1u : 0u) << i;
+  return m;
+}
+__device__ __forceinline__ uint32_t half_bits(uint32_t mask, int i) {  // of elements 2 i and 2 i + 1
+  return (mask & (1u << (2 * i))) | ((mask >> 16) & (2u << (2 * i)));
+}
+template <>
+__device__ __forceinline__ uint32_t at_or_above<__half>(const Vec& v, __half least) {
+  const __half2 l = __half2half2(least);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m |= half_bits(__hge2_mask(*reinterpret_cast<const __half2*>(&v.w[i]), l), i);
+  return m;
+}
+template <>
+__device__ __forceinline__ uint32_t at_or_above<__nv_bfloat16>(const Vec& v, __nv_bfloat16 least) {
+  const __nv_bfloat162 l = __bfloat162bfloat162(least);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m |= half_bits(__hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&v.w[i]), l), i);
+  return m;
+}
+// the type's lowest finite value
+template <typename T>
+__device__ __forceinline__ T lowest();
+template <>
+__device__ __forceinline__ float lowest<float>() { return -3.4028234663852886e38f; }
+template <>
+__device__ __forceinline__ __half lowest<__half>() { return __ushort_as_half(0xfbff); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 lowest<__nv_bfloat16>() { return __ushort_as_bfloat16(0xff7f); }
+
 template <typename T>
 __device__ __forceinline__ int row_shift(const T* row) {
   return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));

@@ -1,8 +1,8 @@
 // Rows of logits streamed through shared memory by persistent blocks.
 //
-// A block has 16 computing warps and a producer warp that keeps a ring of 32 KB stages full with bulk
-// copies, across rows: the copies of the next rows run under the work on this one, so the reads
-// never pause for a reduction. Cluster c takes the rows c, c + #clusters, ...; its S blocks take a share
+// A block has W computing warps and a producer warp that keeps a ring of stages (four vectors for each
+// computing thread) full with bulk copies, across rows: the copies of the next rows run under the work on
+// this one, so the reads never pause for a reduction. Cluster c takes the rows c, c + #clusters, ...; its S blocks take a share
 // of the row each (vocab_rows.cuh: aligned 16-byte vectors). A row's first and last vector, when they
 // are partial, are put together by the producer warp, with -inf outside the row.
 #pragma once
@@ -12,10 +12,12 @@
 namespace swg {
 namespace row {
 
-constexpr int kStreamWarps = 16;
-constexpr int kStreamThreads = kStreamWarps * 32;   // computing threads
-constexpr int kStageVecs = 4 * kStreamThreads;      // vectors a stage holds: four for each thread
-constexpr int kStageBytes = kStageVecs * 16;
+template <int W>
+struct Shape {
+  static constexpr int kThreads = 32 * W;             // computing threads
+  static constexpr int kStageVecs = 4 * kThreads;     // vectors a stage holds: four for each thread
+  static constexpr int kStageBytes = 16 * kStageVecs;
+};
 
 // Waits are bounded: after the first one that ran out, the later ones of the thread only look once, so
 // that the block still comes to its end (its results are then void and the status word says so).
@@ -48,16 +50,16 @@ struct Patience {
   }
 };
 
-template <int N>  // stages
+template <int W, int N>  // N stages
 struct Ring {
   uint64_t full[N];   // a stage's copies have landed
   uint64_t empty[N];  // the computing warps have read it
 };
-template <int N>
-__device__ __forceinline__ void ring_init(Ring<N>& ring) {
+template <int W, int N>
+__device__ __forceinline__ void ring_init(Ring<W, N>& ring) {
   for (int i = 0; i < N; ++i) {
     mbar_init(&ring.full[i], 1);
-    mbar_init(&ring.empty[i], kStreamWarps);
+    mbar_init(&ring.empty[i], W);
   }
 }
 // a position in the ring: stage and the parity of its use
@@ -74,11 +76,11 @@ struct Place {
 };
 
 // The producer warp: all rows of the block's cluster, row r's share at `rank` of S.
-template <typename T, int N>
+template <typename T, int W, int N>
 __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int64_t V, int64_t first, int64_t rows,
-                                             int64_t step, int per, int rank, unsigned char* buf, Ring<N>& ring,
+                                             int64_t step, int per, int rank, unsigned char* buf, Ring<W, N>& ring,
                                              Patience& wait) {
-  constexpr int E = Traits<T>::E;
+  constexpr int E = Traits<T>::E, kStageVecs = Shape<W>::kStageVecs, kStageBytes = Shape<W>::kStageBytes;
   const int lane = threadIdx.x & 31;
   const T* base = static_cast<const T*>(logits);
   // a lane's element of the partial vectors of row r: lanes 0 .. E - 1 the first one's, 16 .. 16 + E - 1
@@ -127,13 +129,14 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
 }
 
 // a computing thread's four vectors of a stage that holds n; -inf past them
-template <typename T>
+template <typename T, int W>
 __device__ __forceinline__ void read_stage(Vec (&v)[4], const unsigned char* stage, int n) {
+  constexpr int kThreads = Shape<W>::kThreads;
   const uint4* p = reinterpret_cast<const uint4*>(stage) + threadIdx.x;
-  if (n == kStageVecs) {
+  if (n == Shape<W>::kStageVecs) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 u = p[i * kStreamThreads];
+      const uint4 u = p[i * kThreads];
       v[i] = Vec{{u.x, u.y, u.z, u.w}};
     }
     return;
@@ -141,21 +144,21 @@ __device__ __forceinline__ void read_stage(Vec (&v)[4], const unsigned char* sta
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint4 u = make_uint4(Traits<T>::kNegInf, Traits<T>::kNegInf, Traits<T>::kNegInf, Traits<T>::kNegInf);
-    if (i * kStreamThreads + static_cast<int>(threadIdx.x) < n) u = p[i * kStreamThreads];
+    if (i * kThreads + static_cast<int>(threadIdx.x) < n) u = p[i * kThreads];
     v[i] = Vec{{u.x, u.y, u.z, u.w}};
   }
 }
 
 // The same with four vectors that follow each other, 4 threadIdx.x .. 4 threadIdx.x + 3, in an order by
 // thread in which the eight lanes of a shared-memory phase meet all banks.
-template <typename T>
+template <typename T, int W>
 __device__ __forceinline__ void read_stage_runs(Vec (&v)[4], const unsigned char* stage, int n) {
   const uint4* p = reinterpret_cast<const uint4*>(stage);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = 4 * static_cast<int>(threadIdx.x) + ((i + (static_cast<int>(threadIdx.x) >> 1)) & 3);
     uint4 u = make_uint4(Traits<T>::kNegInf, Traits<T>::kNegInf, Traits<T>::kNegInf, Traits<T>::kNegInf);
-    if (n == kStageVecs || at < n) u = p[at];
+    if (n == Shape<W>::kStageVecs || at < n) u = p[at];
     v[i] = Vec{{u.x, u.y, u.z, u.w}};
   }
 }
