@@ -12,7 +12,7 @@
 // logits are read once. The warps' (max, sum) go to every block of the cluster, where one warp joins them;
 // the gradient of a row is formed after the sums of the next one, so the exchange is off the path. The
 // gradient's sparse part, at most K elements a row, is written by the warp that wrote the dense part
-// there. One more warp takes the teacher's entries a row ahead.
+// there. Two more warps take the teacher's entries of every other row each, a row ahead.
 // The gradient alone needs no exchange: blocks take 32 KB shares of rows in registers.
 #include <mutex>
 
@@ -152,8 +152,9 @@ __device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g,
 
 // ---- loss, and loss with gradient
 
-constexpr int kExtraWarps = 3;  // producer, teacher, joiner
-constexpr int kStages = 6;      // of the ring
+constexpr int kExtraWarps = 4;  // producer, two teachers, joiner
+constexpr int kStages = 6;      // of the ring (five beside more than kManyEntries entries)
+constexpr int kManyEntries = 512;
 constexpr int kSlots = 4;       // exchange slots: a slot is written again four rows later
 constexpr int kShareStages = 2; // stages a row's share may hold: two rows' shares, and two stages ahead
 
@@ -168,12 +169,13 @@ struct KdStream {
   float2 note[kSlots];      // from the first block: its entries' logits have been read
   Gradient grad[2];
   float weight[2];
-  uint16_t own[W][32];      // a warp's entries of the row
+  bool twice[2];            // an id of the row comes twice
   float sq[2];              // sum exp((t - max t) / tau), 0 for a row without entries
 };
-// the entries of two rows follow the ring in dynamic shared memory, K of each array
+// The entries of two rows follow the ring in dynamic shared memory, K of each array, and behind them the
+// teacher's table of ids. An id that came before in the row is kept as -2 - id, an absent one as -1.
 struct EntryArrays {
-  int* id;    // -1: absent
+  int* id;
   float* td;  // teacher logits less their maximum; exp(td / tau) / sq are the probabilities
   float* z;   // the student's logits (first block)
 };
@@ -181,6 +183,14 @@ __device__ __forceinline__ EntryArrays entry_arrays(unsigned char* at, int K, in
   int* p = reinterpret_cast<int*>(at) + b * 3 * K;
   return EntryArrays{p, reinterpret_cast<float*>(p + K), reinterpret_cast<float*>(p + 2 * K)};
 }
+__device__ __forceinline__ int id_of(int kept) { return kept < -1 ? -2 - kept : kept; }
+// slots of the table of ids: a power of two, twice the entries at least
+__host__ __device__ __forceinline__ int table_slots(int K) {
+  int n = 64;
+  while (n < 2 * K) n *= 2;
+  return n;
+}
+__host__ __device__ constexpr size_t entry_bytes(int K) { return static_cast<size_t>(2) * 3 * 4 * K; }
 
 // One warp takes the entries of row after row: the first kAhead of a row are loaded while the row before
 // is worked on.
@@ -240,10 +250,12 @@ __device__ __forceinline__ void read_some(const KdArgs& a, const T* z, int k0, b
   for (int i = 0; i < kAhead / 32; ++i) v.z[i] = to_f(x[i]);
 }
 // row r's entries, the first of them in `first`, -> shared memory; `gather`: with the student's logits.
-// Loads the first entries of row `next` into `first`. wait(): the arrays are free.
-template <typename T, typename Wait>
+// Loads the first entries of row `next` into `first`. wait(): the arrays are free. twice: an id
+// comes twice (looked for with kTwice).
+template <typename T, bool kTwice, typename Wait>
 __device__ __forceinline__ void take_entries(const KdArgs& a, int64_t r, int64_t next, EntryLoads& first,
-                                             const EntryArrays& n, bool gather, float& sq, Wait wait) {
+                                             const EntryArrays& n, int* table, int slots, bool gather, float& sq,
+                                             bool& twice, Wait wait) {
   const int lane = threadIdx.x & 31;
   const float c2 = a.inv_temp * kLog2e;
   const T* z = static_cast<const T*>(a.logits) + r * a.ld;
@@ -253,22 +265,47 @@ __device__ __forceinline__ void take_entries(const KdArgs& a, int64_t r, int64_t
   if (next < a.T) load_some(a, next, 0, first);
   read_some(a, z, 0, gather, now, v);
   wait();
+  if (kTwice) {
+    for (int i = lane; i < slots; i += 32) table[i] = -1;
+    __syncwarp();
+  }
+  bool same = false;
   for (int k0 = 0;;) {
 #pragma unroll
     for (int i = 0; i < kAhead / 32; ++i) {
+      if (k0 + 32 * i >= a.K) break;
       const int k = k0 + i * 32 + lane;
       m = fmaxf(m, v.t[i]);
+      const int id = v.id[i];
+      bool before = false;
+      if (kTwice) {
+        const uint32_t lanes = __match_any_sync(0xffffffffu, id);
+        before = id >= 0 && (lanes & ((1u << lane) - 1u)) != 0;
+      }
+      // the lowest lane with an id looks for it in the table, where the entries before have theirs
+      if (kTwice && id >= 0 && !before) {
+        int at = static_cast<int>((static_cast<uint32_t>(id) * 2654435761u) >> 16) & (slots - 1);
+        for (int n = 0; n < slots; ++n) {
+          const int old = atomicCAS(&table[at], -1, id);
+          before = old == id;
+          if (old == id || old == -1) break;
+          at = (at + 1) & (slots - 1);
+        }
+      }
+      same = same || before;
       if (k < a.K) {
-        n.id[k] = v.id[i];
+        n.id[k] = before ? -2 - id : id;
         n.td[k] = v.t[i];
         n.z[k] = v.z[i];
       }
     }
     k0 += kAhead;
     if (k0 >= a.K) break;
+    __syncwarp();
     load_some(a, r, k0, now);
     read_some(a, z, k0, gather, now, v);
   }
+  twice = __any_sync(0xffffffffu, same);
   const float me = finite_or_0(warp_max(m));
   __syncwarp();
   float s = 0.f;
@@ -282,14 +319,14 @@ __device__ __forceinline__ void take_entries(const KdArgs& a, int64_t r, int64_t
 
 template <typename T, bool kGrad, int W>
 __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
-    kd_fwd_kernel(const KdArgs a, Split split, uint32_t* status) {
+    kd_fwd_kernel(const KdArgs a, Split split, int stages, int slots, uint32_t* status) {
   constexpr int E = Traits<T>::E;
   constexpr int kStreamThreads = Shape<W>::kThreads, kStageVecs = Shape<W>::kStageVecs;
   constexpr int kStageBytes = Shape<W>::kStageBytes;
   extern __shared__ __align__(128) unsigned char dyn[];
   __shared__ KdStream<W> sm;
   const int S = split.S;
-  auto entries = [&](int b) { return entry_arrays(dyn + kStages * kStageBytes, a.K, b); };
+  auto entries = [&](int b) { return entry_arrays(dyn + stages * kStageBytes, a.K, b); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank());
   const int64_t first = blockIdx.x / S, step = gridDim.x / S;
@@ -312,20 +349,27 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
   const float c2 = a.inv_temp * kLog2e;
 
   if (warp == W) {
-    produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, sm.ring, wait);
-  } else if (warp == W + 1) {
+    produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, stages, sm.ring, wait);
+  } else if (warp == W + 1 || warp == W + 2) {
+    // the teachers take the entries of every other row each, into arrays of their own
+    const int b = warp - W - 1;
+    const EntryArrays n = entries(b);
+    int* table = reinterpret_cast<int*>(dyn + stages * kStageBytes + entry_bytes(a.K)) + b * slots;
+    const int64_t begin = first + b * step;
     EntryLoads ahead;
-    load_some(a, first, 0, ahead);
-    int64_t it = 0;
-    for (int64_t r = first; r < a.T; r += step, ++it) {
-      const int b = static_cast<int>(it & 1), slot = static_cast<int>(it & (kSlots - 1));
+    if (begin < a.T) load_some(a, begin, 0, ahead);
+    int64_t it = b;
+    for (int64_t r = begin; r < a.T; r += 2 * step, it += 2) {
+      const int slot = static_cast<int>(it & (kSlots - 1));
       const float w = kGrad ? a.weight[r] : 0.0f;
       float sq;
-      take_entries<T>(a, r, r + step, ahead, entries(b), rank == 0, sq,
-                      [&]() { wait(&sm.spare[b], static_cast<uint32_t>((it >> 1) & 1) ^ 1u); });
+      bool twice;
+      take_entries<T, kGrad>(a, r, r + 2 * step, ahead, n, table, slots, rank == 0, sq, twice,
+                             [&]() { wait(&sm.spare[b], static_cast<uint32_t>((it >> 1) & 1) ^ 1u); });
       if (lane == 0) {
         sm.sq[b] = sq;
         sm.weight[b] = w;
+        sm.twice[b] = twice;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.ready[b]);
@@ -333,7 +377,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       if (rank == 0 && lane < S) send_f2(&sm.note[slot], &sm.joined[slot], static_cast<uint32_t>(lane), 0.f, 0.f);
       __syncwarp();
     }
-  } else if (warp == W + 2) {
+  } else if (warp == W + 3) {
     // joins the row's maxima and sums, and forms the constants of its gradient and (first block) its loss
     int64_t it = 0;
     for (int64_t r = first; r < a.T; r += step, ++it) {
@@ -367,7 +411,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
         float l = 0.f;
         for (int i = lane; i < a.K; i += 32) {
           const float e = ex2_approx(n.td[i] * c2);
-          if (n.id[i] >= 0 && e != 0.0f) l = fmaf(e * f, n.td[i] - (n.z[i] - me), l);
+          if (n.id[i] != -1 && e != 0.0f) l = fmaf(e * f, n.td[i] - (n.z[i] - me), l);
         }
         l = warp_sum(l);
         if (lane == 0) {
@@ -381,7 +425,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       if (lane == 0) mbar_arrive(&sm.spare[b]);
     }
   } else {
-    Place<kStages> in, held;  // the next stage to read, and (with a gradient) the first stage of the row before
+    Place in, held;  // the next stage to read, and (with a gradient) the first stage of the row before
     // max and sum of the warp's part of row r, sent to every block
     auto sums = [&](int64_t r, int slot) {
       const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
@@ -395,7 +439,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.ring.empty[in.stage]);
         }
-        in.next();
+        in.next(stages);
       }
       const float4 p = sum.result();
       if (lane < S) send_f4(&sm.part[slot][rank][warp], &sm.joined[slot], static_cast<uint32_t>(lane), p);
@@ -414,7 +458,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       const EntryArrays n = entries(b);
       const Gradient g = sm.grad[b];
       const bool some = sm.weight[b] != 0.0f;
-      const Place<kStages> begin = held;
+      const Place begin = held;
       for (int c = sh.begin; c < sh.end; c += kStageVecs) {
         Vec v[4];
         const int cnt = min(sh.end - c, kStageVecs);
@@ -438,75 +482,41 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
           if (inner) st_vec(to + i * kStreamThreads * E, v[i]);
           else store_row_vec(out, e0 + at * E, a.V, aligned, v[i]);
         }
-        held.next();
+        held.next(stages);
       }
-      // The elements at the entries, over the dense part that this warp has written. All entries of one id
-      // are of one warp; it lists its own ones, 32 at most: where there are more, those of each of a
-      // thread's four vectors by themselves.
+      // The elements at the entries, over the dense part that this warp has written; an id that comes
+      // twice is taken at its first entry, its probabilities added lane by lane.
       __syncwarp();
       if (some) {
-        auto vec_of = [&](int id) { return (id + sh.shift) / E - sh.begin; };  // of the share's
-        auto store = [&](int id, float q) {
-          const int vec = vec_of(id);
-          int stage = begin.stage + vec / kStageVecs;
-          if (stage >= kStages) stage -= kStages;
-          const T* p = reinterpret_cast<const T*>(dyn + stage * kStageBytes + (vec % kStageVecs) * 16);
-          const float x = fmaf(to_f(p[(id + sh.shift) % E]), g.k.c, -g.k.ref);
-          out[id] = from_f<T>(fmaf(g.dense, ex2_approx(x), -g.sparse * q));
-        };
-        int parts = 1, part = 0;
-        auto own = [&](int id) {
-          const int vec = vec_of(id);
-          return id >= 0 && vec >= 0 && vec < sh.end - sh.begin && (vec % kStreamThreads) >> 5 == warp &&
-                 (vec / kStreamThreads) % parts == part;
-        };
-        for (; part < parts; ++part) {
-        int have = 0;
+        const bool twice = sm.twice[b];
         for (int k0 = 0; k0 < a.K; k0 += 32) {
-          const bool mine = k0 + lane < a.K && own(n.id[k0 + lane]);
-          const uint32_t all = __ballot_sync(0xffffffffu, mine);
-          const int at = have + __popc(all & ((1u << lane) - 1u));
-          if (mine && at < 32) sm.own[warp][at] = static_cast<uint16_t>(k0 + lane);
-          have += __popc(all);
-        }
-        __syncwarp();
-        if (have > 32 && parts == 1) {
-          parts = 4;
-          part = -1;
-          continue;
-        }
-        if (have <= 32) {
-          const int k = lane < have ? sm.own[warp][lane] : 0;
-          const int id = lane < have ? n.id[k] : -1 - lane;
-          float q = ex2_approx(n.td[k] * c2);
-          const uint32_t same = __match_any_sync(0xffffffffu, id);
-          if (__any_sync(0xffffffffu, (same & (same - 1)) != 0)) {  // an id comes twice: added in order
-            float t = 0.f;
-            for (int l = 0; l < have; ++l) {
-              const float x = __shfl_sync(0xffffffffu, q, l);
-              if (same >> l & 1u) t += x;
+          const int id = k0 + lane < a.K ? n.id[k0 + lane] : -1;
+          const int vec = (id + sh.shift) / E - sh.begin;  // of the share's
+          const bool own = id >= 0 && vec >= 0 && vec < sh.end - sh.begin && (vec % kStreamThreads) >> 5 == warp;
+          float q = own ? ex2_approx(n.td[k0 + lane] * c2) : 0.0f;
+          if (twice) {
+            for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo != 0; todo &= todo - 1) {
+              const int from = __ffs(todo) - 1, its = __shfl_sync(0xffffffffu, id, from);
+              float t = 0.f;
+              for (int j = lane; j < a.K; j += 32)
+                if (id_of(n.id[j]) == its) t += ex2_approx(n.td[j] * c2);
+              t = warp_sum(t);
+              if (lane == from) q = t;
             }
-            q = t;
           }
-          if (lane < have && (same & ((1u << lane) - 1u)) == 0) store(id, q);
-        } else {
-          for (int k0 = 0; k0 < a.K; ++k0) {  // one entry after the other
-            const int id = n.id[k0];
-            if (!own(id)) continue;
-            float q = 0.f;
-            for (int j = lane; j < a.K; j += 32)
-              if (n.id[j] == id) q += ex2_approx(n.td[j] * c2);
-            q = warp_sum(q);
-            if (lane == 0) store(id, q);
+          if (own) {
+            int stage = begin.stage + vec / kStageVecs;
+            if (stage >= stages) stage -= stages;
+            const T* p = reinterpret_cast<const T*>(dyn + stage * kStageBytes + (vec % kStageVecs) * 16);
+            const float x = fmaf(to_f(p[(id + sh.shift) % E]), g.k.c, -g.k.ref);
+            out[id] = from_f<T>(fmaf(g.dense, ex2_approx(x), -g.sparse * q));
           }
-        }
-        __syncwarp();
         }
       }
       __syncwarp();
       if (lane == 0) {
-        Place<kStages> p = begin;
-        for (int c = sh.begin; c < sh.end; c += kStageVecs, p.next()) mbar_arrive(&sm.ring.empty[p.stage]);
+        Place p = begin;
+        for (int c = sh.begin; c < sh.end; c += kStageVecs, p.next(stages)) mbar_arrive(&sm.ring.empty[p.stage]);
         mbar_arrive(&sm.spare[b]);
       }
     };
@@ -527,10 +537,11 @@ template <typename T, bool kGrad, int W>
 cudaError_t launch_fwd(const KdArgs& a, Split split, cudaStream_t stream) {
   static std::mutex mu;  // guards the occupancy cache
   static StreamCache cache;
-  const size_t smem = kStages * Shape<W>::kStageBytes + static_cast<size_t>(2) * 3 * 4 * a.K;
+  const int stages = a.K > kManyEntries ? kStages - 1 : kStages, slots = table_slots(a.K);
+  const size_t smem = stages * Shape<W>::kStageBytes + entry_bytes(a.K) + static_cast<size_t>(2) * slots * sizeof(int);
   std::lock_guard<std::mutex> lk(mu);
   return launch_stream(kd_fwd_kernel<T, kGrad, W>, cache, 32 * (W + kExtraWarps), smem, a.T, split.S, false, stream, a,
-                       split, status_word_ptr());
+                       split, stages, slots, status_word_ptr());
 }
 template <bool kGrad, int W>
 cudaError_t launch_fwd_any(const KdArgs& a, int dtype, Split split, cudaStream_t stream) {

@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 2)
   Patience wait;
 
   if (warp == W) {
-    produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, sm.ring, wait);
+    produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, kStages, sm.ring, wait);
   } else if (warp > W) {
     const int me = warp - W - 1;
     Finish<W>& f = finish[me];
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 2)
       __syncwarp();
     }
   } else {
-    Place<kStages> in;
+    Place in;
     int sel = 0;            // the selector of the row
     uint32_t parity = 1;    // of its `taken`
     for (int64_t r = first; r < a.T; r += step) {
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 2)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.ring.empty[in.stage]);
-        in.next();
+        in.next(kStages);
       }
       const float4 p = sums.result();
       if (lane == 0) f.part[warp] = p;

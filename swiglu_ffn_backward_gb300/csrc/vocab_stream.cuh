@@ -50,7 +50,7 @@ struct Patience {
   }
 };
 
-template <int W, int N>  // N stages
+template <int W, int N>  // up to N stages
 struct Ring {
   uint64_t full[N];   // a stage's copies have landed
   uint64_t empty[N];  // the computing warps have read it
@@ -63,12 +63,11 @@ __device__ __forceinline__ void ring_init(Ring<W, N>& ring) {
   }
 }
 // a position in the ring: stage and the parity of its use
-template <int N>
 struct Place {
   int stage = 0;
   uint32_t parity = 0;
-  __device__ __forceinline__ void next() {
-    if (++stage == N) {
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
       stage = 0;
       parity ^= 1u;
     }
@@ -78,7 +77,8 @@ struct Place {
 // The producer warp: all rows of the block's cluster, row r's share at `rank` of S.
 template <typename T, int W, int N>
 __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int64_t V, int64_t first, int64_t rows,
-                                             int64_t step, int per, int rank, unsigned char* buf, Ring<W, N>& ring,
+                                             int64_t step, int per, int rank, unsigned char* buf, int stages,
+                                             Ring<W, N>& ring,
                                              Patience& wait) {
   constexpr int E = Traits<T>::E, kStageVecs = Shape<W>::kStageVecs, kStageBytes = Shape<W>::kStageBytes;
   const int lane = threadIdx.x & 31;
@@ -96,7 +96,7 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
     if (e >= 0 && e < V) x = z[e];
     return x;
   };
-  Place<N> p;
+  Place p;
   T mine = edge(first);
   for (int64_t r = first; r < rows; r += step) {
     const T* z = base + r * ld;
@@ -122,7 +122,7 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
         if (bytes > 0) bulk_g2s(to + (w0 - c) * 16, z + first_element<T>(sh, w0), bytes, &ring.full[p.stage]);
       }
       __syncwarp();
-      p.next();
+      p.next(stages);
     }
     mine = ahead;
   }
