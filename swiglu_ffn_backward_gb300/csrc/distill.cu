@@ -10,9 +10,9 @@
 // Loss, and loss with gradient: a persistent kernel streams rows through shared memory (vocab_stream.cuh).
 // With a gradient a row's shares stay in the rings of a cluster of S blocks until it is written, so the
 // logits are read once. The warps' (max, sum) go to every block of the cluster, where one warp joins them;
-// the gradient of a row is formed after the sums of the next one, so the exchange is off the path. The
-// gradient's sparse part, at most K elements a row, is written by the warp that wrote the dense part
-// there. Two more warps take the teacher's entries of every other row each, a row ahead.
+// the gradient of a row is formed after the sums of the next one, so the exchange is off the path. Two
+// more warps take the teacher's entries of every other row each, a row ahead, and write the gradient's
+// sparse part, at most K elements a row, over the dense one.
 // The gradient alone needs no exchange: blocks take 32 KB shares of rows in registers.
 #include <mutex>
 
@@ -163,27 +163,26 @@ struct KdStream {
   Ring<W, kStages> ring;
   uint64_t joined[kSlots];  // the row's maxima and sums have come from all blocks
   uint64_t ready[2];        // the row's entries are in shared memory
-  uint64_t spare[2];        // their readers are done with them
+  uint64_t spare[2];        // the joiner is done with them
+  uint64_t dense[2];        // the dense part of the row's gradient is written
   uint64_t solved[2];       // the row's gradient constants are in shared memory
   float4 part[kSlots][kMaxCluster][W];  // every warp's sums (WarpSums::result)
   float2 note[kSlots];      // from the first block: its entries' logits have been read
   Gradient grad[2];
   float weight[2];
-  bool twice[2];            // an id of the row comes twice
   float sq[2];              // sum exp((t - max t) / tau), 0 for a row without entries
 };
-// The entries of two rows follow the ring in dynamic shared memory, K of each array, and behind them the
-// teacher's table of ids. An id that came before in the row is kept as -2 - id, an absent one as -1.
+// the entries of two rows follow the ring in dynamic shared memory, K of each array, and behind them the
+// teachers' tables of ids
 struct EntryArrays {
-  int* id;
+  int* id;    // -1: absent
   float* td;  // teacher logits less their maximum; exp(td / tau) / sq are the probabilities
-  float* z;   // the student's logits (first block)
+  float* z;   // the student's logits (first block: all, else those in the block's share)
 };
 __device__ __forceinline__ EntryArrays entry_arrays(unsigned char* at, int K, int b) {
   int* p = reinterpret_cast<int*>(at) + b * 3 * K;
   return EntryArrays{p, reinterpret_cast<float*>(p + K), reinterpret_cast<float*>(p + 2 * K)};
 }
-__device__ __forceinline__ int id_of(int kept) { return kept < -1 ? -2 - kept : kept; }
 // slots of the table of ids: a power of two, twice the entries at least
 __host__ __device__ __forceinline__ int table_slots(int K) {
   int n = 64;
@@ -192,9 +191,9 @@ __host__ __device__ __forceinline__ int table_slots(int K) {
 }
 __host__ __device__ constexpr size_t entry_bytes(int K) { return static_cast<size_t>(2) * 3 * 4 * K; }
 
-// One warp takes the entries of row after row: the first kAhead of a row are loaded while the row before
-// is worked on.
-// They are kept as loaded, so that a load does not wait for the one before it.
+// A teacher warp takes the entries of row after row. The first kAhead of a row are loaded two rows ahead,
+// and the student's logits at them a row ahead; they are kept as loaded, so that a load does not wait for the
+// one before it.
 constexpr int kAhead = 128;
 struct EntryLoads {
   int64_t id[kAhead / 32];
@@ -223,99 +222,99 @@ __device__ __forceinline__ void load_some(const KdArgs& a, int64_t r, int k0, En
       if (k + 32 * i < a.K) n.t[i] = static_cast<const uint16_t*>(a.teacher)[at + k + 32 * i];
   }
 }
-// what was loaded: ids, -1 for absent entries, and the teacher's and the student's logits
+// ids (-1 for absent entries), the teacher's logits, and the student's at the ids in [e0, e1), as loaded
+template <typename T>
 struct EntryValues {
   int id[kAhead / 32];
-  float t[kAhead / 32];
-  float z[kAhead / 32];
+  uint32_t t[kAhead / 32];
+  T z[kAhead / 32];
 };
 template <typename T>
-__device__ __forceinline__ void read_some(const KdArgs& a, const T* z, int k0, bool gather, const EntryLoads& n,
-                                          EntryValues& v) {
+__device__ __forceinline__ void gather_some(const KdArgs& a, int64_t r, int k0, const EntryLoads& n, int64_t e0,
+                                            int64_t e1, EntryValues<T>& v) {
+  const T* z = static_cast<const T*>(a.logits) + r * a.ld;
   const int k = k0 + static_cast<int>(threadIdx.x & 31);
-  T x[kAhead / 32];
 #pragma unroll
   for (int i = 0; i < kAhead / 32; ++i) {
     const int64_t id = k + 32 * i >= a.K ? -1 : a.wide ? n.id[i] : static_cast<int32_t>(n.id[i]);
     v.id[i] = id >= 0 && id < a.V ? static_cast<int>(id) : -1;
-    x[i] = from_f<T>(0.0f);
-    if (gather && v.id[i] >= 0) x[i] = z[v.id[i]];
-    const uint32_t u = n.t[i];
-    v.t[i] = v.id[i] < 0 ? neg_inf()
-             : a.tdtype == 0 ? __uint_as_float(u)
-             : a.tdtype == 1 ? __half2float(__ushort_as_half(static_cast<uint16_t>(u)))
-                             : __uint_as_float(u << 16);
+    v.t[i] = n.t[i];
+    v.z[i] = from_f<T>(0.0f);
+    if (v.id[i] >= e0 && v.id[i] < e1 && v.id[i] >= 0) v.z[i] = z[v.id[i]];
   }
-#pragma unroll
-  for (int i = 0; i < kAhead / 32; ++i) v.z[i] = to_f(x[i]);
 }
-// row r's entries, the first of them in `first`, -> shared memory; `gather`: with the student's logits.
-// Loads the first entries of row `next` into `first`. wait(): the arrays are free. twice: an id
-// comes twice (looked for with kTwice).
-template <typename T, bool kTwice, typename Wait>
-__device__ __forceinline__ void take_entries(const KdArgs& a, int64_t r, int64_t next, EntryLoads& first,
-                                             const EntryArrays& n, int* table, int slots, bool gather, float& sq,
-                                             bool& twice, Wait wait) {
+__device__ __forceinline__ float teacher_logit(const KdArgs& a, uint32_t u) {
+  return a.tdtype == 0   ? __uint_as_float(u)
+         : a.tdtype == 1 ? __half2float(__ushort_as_half(static_cast<uint16_t>(u)))
+                         : __uint_as_float(u << 16);
+}
+// row r's entries, the first of them in v, -> shared memory; returns sum exp((t - max t) / tau)
+template <typename T>
+__device__ __forceinline__ float take_entries(const KdArgs& a, int64_t r, EntryValues<T>& v, const EntryArrays& n,
+                                              int64_t e0, int64_t e1) {
   const int lane = threadIdx.x & 31;
   const float c2 = a.inv_temp * kLog2e;
-  const T* z = static_cast<const T*>(a.logits) + r * a.ld;
   float m = neg_inf();
-  EntryLoads now = first;
-  EntryValues v;
-  if (next < a.T) load_some(a, next, 0, first);
-  read_some(a, z, 0, gather, now, v);
-  wait();
-  if (kTwice) {
-    for (int i = lane; i < slots; i += 32) table[i] = -1;
-    __syncwarp();
-  }
-  bool same = false;
   for (int k0 = 0;;) {
 #pragma unroll
     for (int i = 0; i < kAhead / 32; ++i) {
-      if (k0 + 32 * i >= a.K) break;
       const int k = k0 + i * 32 + lane;
-      m = fmaxf(m, v.t[i]);
-      const int id = v.id[i];
-      bool before = false;
-      if (kTwice) {
-        const uint32_t lanes = __match_any_sync(0xffffffffu, id);
-        before = id >= 0 && (lanes & ((1u << lane) - 1u)) != 0;
-      }
-      // the lowest lane with an id looks for it in the table, where the entries before have theirs
-      if (kTwice && id >= 0 && !before) {
-        int at = static_cast<int>((static_cast<uint32_t>(id) * 2654435761u) >> 16) & (slots - 1);
-        for (int n = 0; n < slots; ++n) {
-          const int old = atomicCAS(&table[at], -1, id);
-          before = old == id;
-          if (old == id || old == -1) break;
-          at = (at + 1) & (slots - 1);
-        }
-      }
-      same = same || before;
-      if (k < a.K) {
-        n.id[k] = before ? -2 - id : id;
-        n.td[k] = v.t[i];
-        n.z[k] = v.z[i];
-      }
+      if (k >= a.K) break;
+      const float t = v.id[i] < 0 ? neg_inf() : teacher_logit(a, v.t[i]);
+      m = fmaxf(m, t);
+      n.id[k] = v.id[i];
+      n.td[k] = t;
+      n.z[k] = to_f(v.z[i]);
     }
     k0 += kAhead;
     if (k0 >= a.K) break;
-    __syncwarp();
-    load_some(a, r, k0, now);
-    read_some(a, z, k0, gather, now, v);
+    EntryLoads more;
+    load_some(a, r, k0, more);
+    gather_some(a, r, k0, more, e0, e1, v);
   }
-  twice = __any_sync(0xffffffffu, same);
   const float me = finite_or_0(warp_max(m));
-  __syncwarp();
   float s = 0.f;
-  for (int k = lane; k < a.K; k += 32) {
+  for (int k = lane; k < a.K; k += 32) {  // the lane's own entries
     const float d = n.td[k] - me;
     n.td[k] = d;
     s += ex2_approx(d * c2);
   }
-  sq = warp_sum(s);
+  return warp_sum(s);
 }
+// The lane's entries (bit i: entry 32 i + lane) whose id is in [e0, e1) and has not come before in the
+// row; twice: one of them comes again.
+__device__ __forceinline__ uint32_t first_entries(const KdArgs& a, const EntryArrays& n, int* table, int slots,
+                                                  int64_t e0, int64_t e1, bool& twice) {
+  const int lane = threadIdx.x & 31;
+  for (int i = lane; i < slots; i += 32) table[i] = -1;
+  __syncwarp();
+  uint32_t mine = 0;
+  bool again = false;
+  for (int k0 = 0; k0 < a.K; k0 += 32) {
+    const int kept = k0 + lane < a.K ? n.id[k0 + lane] : -1;
+    const int id = kept >= 0 && kept >= e0 && kept < e1 ? kept : -1;
+    // the lowest lane with an id looks for it in the table, where the entries before have theirs
+    const uint32_t lanes = __match_any_sync(0xffffffffu, id);
+    bool before = (lanes & ((1u << lane) - 1u)) != 0;
+    if (id >= 0 && !before) {
+      int at = static_cast<int>((static_cast<uint32_t>(id) * 2654435761u) >> 16) & (slots - 1);
+      for (int step = 0; step < slots; ++step) {
+        const int old = atomicCAS(&table[at], -1, id);
+        before = old == id;
+        if (old == id || old == -1) break;
+        at = (at + 1) & (slots - 1);
+      }
+    }
+    if (id >= 0) {
+      if (before) again = true;
+      else mine |= 1u << (k0 / 32);
+    }
+    __syncwarp();
+  }
+  twice = __any_sync(0xffffffffu, again);
+  return mine;
+}
+static_assert(kKdMaxEntries <= 32 * 32, "a bit for each of a lane's entries");
 
 template <typename T, bool kGrad, int W>
 __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
@@ -336,7 +335,8 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
     for (int i = 0; i < kSlots; ++i) mbar_init(&sm.joined[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.ready[i], 1);
-      mbar_init(&sm.spare[i], kGrad ? W + 1 : 1);
+      mbar_init(&sm.spare[i], 1);
+      mbar_init(&sm.dense[i], W);
       mbar_init(&sm.solved[i], 1);
     }
     fence_mbar_init();
@@ -356,26 +356,69 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
     const EntryArrays n = entries(b);
     int* table = reinterpret_cast<int*>(dyn + stages * kStageBytes + entry_bytes(a.K)) + b * slots;
     const int64_t begin = first + b * step;
-    EntryLoads ahead;
-    if (begin < a.T) load_some(a, begin, 0, ahead);
+    EntryLoads loads;
+    EntryValues<T> next;
+    // the student's logits at row r's entries: the first block forms the loss and needs them all
+    auto gather = [&](int64_t r) {
+      const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
+      gather_some(a, r, 0, loads, rank == 0 ? 0 : first_element<T>(sh, sh.begin),
+                  rank == 0 ? a.V : first_element<T>(sh, sh.end), next);
+    };
+    if (begin < a.T) {
+      load_some(a, begin, 0, loads);
+      gather(begin);
+      if (begin + 2 * step < a.T) load_some(a, begin + 2 * step, 0, loads);
+    }
     int64_t it = b;
     for (int64_t r = begin; r < a.T; r += 2 * step, it += 2) {
       const int slot = static_cast<int>(it & (kSlots - 1));
+      const uint32_t parity = static_cast<uint32_t>((it >> 1) & 1);
       const float w = kGrad ? a.weight[r] : 0.0f;
-      float sq;
-      bool twice;
-      take_entries<T, kGrad>(a, r, r + 2 * step, ahead, n, table, slots, rank == 0, sq, twice,
-                             [&]() { wait(&sm.spare[b], static_cast<uint32_t>((it >> 1) & 1) ^ 1u); });
+      EntryValues<T> now = next;
+      if (r + 2 * step < a.T) {
+        gather(r + 2 * step);
+        if (r + 4 * step < a.T) load_some(a, r + 4 * step, 0, loads);
+      }
+      const T* z = static_cast<const T*>(a.logits) + r * a.ld;
+      const Share sh = share_of(z, a.V, split.per, rank);
+      const int64_t e0 = first_element<T>(sh, sh.begin), e1 = first_element<T>(sh, sh.end);
+      wait(&sm.spare[b], parity ^ 1u);
+      const float sq = take_entries<T>(a, r, now, n, rank == 0 ? 0 : e0, rank == 0 ? a.V : e1);
       if (lane == 0) {
         sm.sq[b] = sq;
         sm.weight[b] = w;
-        sm.twice[b] = twice;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.ready[b]);
       // a gradient over the logits may be written once the first block has read them here
       if (rank == 0 && lane < S) send_f2(&sm.note[slot], &sm.joined[slot], static_cast<uint32_t>(lane), 0.f, 0.f);
       __syncwarp();
+      if (!kGrad) continue;
+      // the elements at the entries, over the dense part; an id that comes twice is taken at its first
+      // entry, its probabilities added lane by lane
+      bool twice;
+      const uint32_t mine = first_entries(a, n, table, slots, e0, e1, twice);
+      wait(&sm.dense[b], parity);
+      if (w == 0.0f) continue;
+      const Gradient g = sm.grad[b];
+      T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
+      for (int k0 = 0; k0 < a.K; k0 += 32) {
+        const bool own = mine >> (k0 / 32) & 1u;
+        const int id = own ? n.id[k0 + lane] : -1;
+        float q = own ? ex2_approx(n.td[k0 + lane] * c2) : 0.0f;
+        if (twice) {
+          for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo != 0; todo &= todo - 1) {
+            const int from = __ffs(todo) - 1, its = __shfl_sync(0xffffffffu, id, from);
+            float t = 0.f;
+            for (int j = lane; j < a.K; j += 32)
+              if (n.id[j] == its) t += ex2_approx(n.td[j] * c2);
+            t = warp_sum(t);
+            if (lane == from) q = t;
+          }
+        }
+        if (own)
+          out[id] = from_f<T>(fmaf(g.dense, ex2_approx(fmaf(n.z[k0 + lane], g.k.c, -g.k.ref)), -g.sparse * q));
+      }
     }
   } else if (warp == W + 3) {
     // joins the row's maxima and sums, and forms the constants of its gradient and (first block) its loss
@@ -425,7 +468,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       if (lane == 0) mbar_arrive(&sm.spare[b]);
     }
   } else {
-    Place in, held;  // the next stage to read, and (with a gradient) the first stage of the row before
+    Place in, held;  // the next stage to read, and (with a gradient) the next one of the row before
     // max and sum of the warp's part of row r, sent to every block
     auto sums = [&](int64_t r, int slot) {
       const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
@@ -455,14 +498,15 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
       const Share sh = share_of(z, a.V, split.per, rank);
       const bool aligned = row_shift(out) == sh.shift;
-      const EntryArrays n = entries(b);
       const Gradient g = sm.grad[b];
       const bool some = sm.weight[b] != 0.0f;
-      const Place begin = held;
       for (int c = sh.begin; c < sh.end; c += kStageVecs) {
         Vec v[4];
         const int cnt = min(sh.end - c, kStageVecs);
         read_stage<T, W>(v, dyn + held.stage * kStageBytes, cnt);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.ring.empty[held.stage]);
+        held.next(stages);
         const int64_t e0 = first_element<T>(sh, c), e1 = first_element<T>(sh, c + cnt);
         const bool inner = aligned && e0 >= 0 && e1 <= a.V;  // the stage has whole vectors only
 #pragma unroll
@@ -482,43 +526,9 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
           if (inner) st_vec(to + i * kStreamThreads * E, v[i]);
           else store_row_vec(out, e0 + at * E, a.V, aligned, v[i]);
         }
-        held.next(stages);
-      }
-      // The elements at the entries, over the dense part that this warp has written; an id that comes
-      // twice is taken at its first entry, its probabilities added lane by lane.
-      __syncwarp();
-      if (some) {
-        const bool twice = sm.twice[b];
-        for (int k0 = 0; k0 < a.K; k0 += 32) {
-          const int id = k0 + lane < a.K ? n.id[k0 + lane] : -1;
-          const int vec = (id + sh.shift) / E - sh.begin;  // of the share's
-          const bool own = id >= 0 && vec >= 0 && vec < sh.end - sh.begin && (vec % kStreamThreads) >> 5 == warp;
-          float q = own ? ex2_approx(n.td[k0 + lane] * c2) : 0.0f;
-          if (twice) {
-            for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo != 0; todo &= todo - 1) {
-              const int from = __ffs(todo) - 1, its = __shfl_sync(0xffffffffu, id, from);
-              float t = 0.f;
-              for (int j = lane; j < a.K; j += 32)
-                if (id_of(n.id[j]) == its) t += ex2_approx(n.td[j] * c2);
-              t = warp_sum(t);
-              if (lane == from) q = t;
-            }
-          }
-          if (own) {
-            int stage = begin.stage + vec / kStageVecs;
-            if (stage >= stages) stage -= stages;
-            const T* p = reinterpret_cast<const T*>(dyn + stage * kStageBytes + (vec % kStageVecs) * 16);
-            const float x = fmaf(to_f(p[(id + sh.shift) % E]), g.k.c, -g.k.ref);
-            out[id] = from_f<T>(fmaf(g.dense, ex2_approx(x), -g.sparse * q));
-          }
-        }
       }
       __syncwarp();
-      if (lane == 0) {
-        Place p = begin;
-        for (int c = sh.begin; c < sh.end; c += kStageVecs, p.next(stages)) mbar_arrive(&sm.ring.empty[p.stage]);
-        mbar_arrive(&sm.spare[b]);
-      }
+      if (lane == 0) mbar_arrive(&sm.dense[b]);
     };
     int64_t it = 0;
     for (int64_t r = first; r < a.T; r += step, ++it) {
