@@ -153,27 +153,26 @@ __device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g,
 // ---- loss, and loss with gradient
 
 constexpr int kExtraWarps = 4;  // producer, two teachers, joiner
-constexpr int kStages = 6;      // of the ring (five beside more than kManyEntries entries)
-constexpr int kManyEntries = 512;
-constexpr int kSlots = 4;       // exchange slots: a slot is written again four rows later
+constexpr int kStages = 6;      // of the ring, at most (fewer beside many entries)
+constexpr int kSlots = 4;       // of exchange and entries: a slot is written again four rows later
 constexpr int kShareStages = 2; // stages a row's share may hold: two rows' shares, and two stages ahead
 
 template <int W>
 struct KdStream {
   Ring<W, kStages> ring;
   uint64_t joined[kSlots];  // the row's maxima and sums have come from all blocks
-  uint64_t ready[2];        // the row's entries are in shared memory
-  uint64_t spare[2];        // the joiner is done with them
-  uint64_t dense[2];        // the dense part of the row's gradient is written
-  uint64_t solved[2];       // the row's gradient constants are in shared memory
+  uint64_t ready[kSlots];   // the row's entries are in shared memory
+  uint64_t spare[kSlots];   // the joiner is done with them
+  uint64_t dense[kSlots];   // the dense part of the row's gradient is written
+  uint64_t solved[kSlots];  // the row's gradient constants are in shared memory
   float4 part[kSlots][kMaxCluster][W];  // every warp's sums (WarpSums::result)
   float2 note[kSlots];      // from the first block: its entries' logits have been read
-  Gradient grad[2];
-  float weight[2];
-  float sq[2];              // sum exp((t - max t) / tau), 0 for a row without entries
+  Gradient grad[kSlots];
+  float weight[kSlots];
+  float sq[kSlots];         // sum exp((t - max t) / tau), 0 for a row without entries
 };
-// the entries of two rows follow the ring in dynamic shared memory, K of each array, and behind them the
-// teachers' tables of ids
+// the entries of kSlots rows follow the ring in dynamic shared memory, K of each array, and behind them
+// the teachers' tables of ids
 struct EntryArrays {
   int* id;    // -1: absent
   float* td;  // teacher logits less their maximum; exp(td / tau) / sq are the probabilities
@@ -189,7 +188,7 @@ __host__ __device__ __forceinline__ int table_slots(int K) {
   while (n < 2 * K) n *= 2;
   return n;
 }
-__host__ __device__ constexpr size_t entry_bytes(int K) { return static_cast<size_t>(2) * 3 * 4 * K; }
+__host__ __device__ constexpr size_t entry_bytes(int K) { return static_cast<size_t>(kSlots) * 3 * 4 * K; }
 
 // A teacher warp takes the entries of row after row. The first kAhead of a row are loaded two rows ahead,
 // and the student's logits at them a row ahead; they are kept as loaded, so that a load does not wait for the
@@ -325,15 +324,15 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
   extern __shared__ __align__(128) unsigned char dyn[];
   __shared__ KdStream<W> sm;
   const int S = split.S;
-  auto entries = [&](int b) { return entry_arrays(dyn + stages * kStageBytes, a.K, b); };
+  auto entries = [&](int slot) { return entry_arrays(dyn + stages * kStageBytes, a.K, slot); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank());
   const int64_t first = blockIdx.x / S, step = gridDim.x / S;
   const uint32_t bytes = static_cast<uint32_t>(S * W * sizeof(float4) + sizeof(float2));
   if (tid == 0) {
     ring_init(sm.ring);
-    for (int i = 0; i < kSlots; ++i) mbar_init(&sm.joined[i], 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sm.joined[i], 1);
       mbar_init(&sm.ready[i], 1);
       mbar_init(&sm.spare[i], 1);
       mbar_init(&sm.dense[i], W);
@@ -351,56 +350,30 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
   if (warp == W) {
     produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, stages, sm.ring, wait);
   } else if (warp == W + 1 || warp == W + 2) {
-    // the teachers take the entries of every other row each, into arrays of their own
-    const int b = warp - W - 1;
-    const EntryArrays n = entries(b);
-    int* table = reinterpret_cast<int*>(dyn + stages * kStageBytes + entry_bytes(a.K)) + b * slots;
-    const int64_t begin = first + b * step;
+    // the teachers take the entries of every other row each; the sparse part of a row comes after the
+    // entries of the teacher's next one, so nothing waits for it
+    const int odd = warp - W - 1;
+    int* table = reinterpret_cast<int*>(dyn + stages * kStageBytes + entry_bytes(a.K)) + odd * slots;
+    const int64_t begin = first + odd * step;
     EntryLoads loads;
     EntryValues<T> next;
+    auto share = [&](int64_t r) {
+      return share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
+    };
     // the student's logits at row r's entries: the first block forms the loss and needs them all
     auto gather = [&](int64_t r) {
-      const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
+      const Share sh = share(r);
       gather_some(a, r, 0, loads, rank == 0 ? 0 : first_element<T>(sh, sh.begin),
                   rank == 0 ? a.V : first_element<T>(sh, sh.end), next);
     };
-    if (begin < a.T) {
-      load_some(a, begin, 0, loads);
-      gather(begin);
-      if (begin + 2 * step < a.T) load_some(a, begin + 2 * step, 0, loads);
-    }
-    int64_t it = b;
-    for (int64_t r = begin; r < a.T; r += 2 * step, it += 2) {
+    // the elements at the entries of row r, the it-th, over the dense part; an id that comes twice is
+    // taken at its first entry, its probabilities added lane by lane
+    auto sparse = [&](int64_t r, int64_t it, uint32_t mine, bool twice) {
       const int slot = static_cast<int>(it & (kSlots - 1));
-      const uint32_t parity = static_cast<uint32_t>((it >> 1) & 1);
-      const float w = kGrad ? a.weight[r] : 0.0f;
-      EntryValues<T> now = next;
-      if (r + 2 * step < a.T) {
-        gather(r + 2 * step);
-        if (r + 4 * step < a.T) load_some(a, r + 4 * step, 0, loads);
-      }
-      const T* z = static_cast<const T*>(a.logits) + r * a.ld;
-      const Share sh = share_of(z, a.V, split.per, rank);
-      const int64_t e0 = first_element<T>(sh, sh.begin), e1 = first_element<T>(sh, sh.end);
-      wait(&sm.spare[b], parity ^ 1u);
-      const float sq = take_entries<T>(a, r, now, n, rank == 0 ? 0 : e0, rank == 0 ? a.V : e1);
-      if (lane == 0) {
-        sm.sq[b] = sq;
-        sm.weight[b] = w;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.ready[b]);
-      // a gradient over the logits may be written once the first block has read them here
-      if (rank == 0 && lane < S) send_f2(&sm.note[slot], &sm.joined[slot], static_cast<uint32_t>(lane), 0.f, 0.f);
-      __syncwarp();
-      if (!kGrad) continue;
-      // the elements at the entries, over the dense part; an id that comes twice is taken at its first
-      // entry, its probabilities added lane by lane
-      bool twice;
-      const uint32_t mine = first_entries(a, n, table, slots, e0, e1, twice);
-      wait(&sm.dense[b], parity);
-      if (w == 0.0f) continue;
-      const Gradient g = sm.grad[b];
+      wait(&sm.dense[slot], static_cast<uint32_t>((it / kSlots) & 1));
+      if (sm.weight[slot] == 0.0f) return;
+      const EntryArrays n = entries(slot);
+      const Gradient g = sm.grad[slot];
       T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
       for (int k0 = 0; k0 < a.K; k0 += 32) {
         const bool own = mine >> (k0 / 32) & 1u;
@@ -419,13 +392,55 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
         if (own)
           out[id] = from_f<T>(fmaf(g.dense, ex2_approx(fmaf(n.z[k0 + lane], g.k.c, -g.k.ref)), -g.sparse * q));
       }
+      __syncwarp();
+    };
+    if (begin < a.T) {
+      load_some(a, begin, 0, loads);
+      gather(begin);
+      if (begin + 2 * step < a.T) load_some(a, begin + 2 * step, 0, loads);
     }
+    int64_t it = odd;
+    uint32_t mine = 0;
+    bool twice = false;
+    for (int64_t r = begin; r < a.T; r += 2 * step, it += 2) {
+      const int slot = static_cast<int>(it & (kSlots - 1));
+      const EntryArrays n = entries(slot);
+      const float w = kGrad ? a.weight[r] : 0.0f;
+      EntryValues<T> now = next;
+      if (r + 2 * step < a.T) {
+        gather(r + 2 * step);
+        if (r + 4 * step < a.T) load_some(a, r + 4 * step, 0, loads);
+      }
+      const Share sh = share(r);
+      const int64_t e0 = first_element<T>(sh, sh.begin), e1 = first_element<T>(sh, sh.end);
+      wait(&sm.spare[slot], static_cast<uint32_t>((it / kSlots) & 1) ^ 1u);
+      const float sq = take_entries<T>(a, r, now, n, rank == 0 ? 0 : e0, rank == 0 ? a.V : e1);
+      if (lane == 0) {
+        sm.sq[slot] = sq;
+        sm.weight[slot] = w;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.ready[slot]);
+      // A gradient over the logits may be written once the first block has read them here. Row it - 2 has
+      // been joined here, so every block has been through row it - 4 and its barrier of this slot is set
+      // for this row.
+      if (rank == 0 && it >= 2)
+        wait(&sm.spare[(it - 2) & (kSlots - 1)], static_cast<uint32_t>(((it - 2) / kSlots) & 1));
+      if (rank == 0 && lane < S) send_f2(&sm.note[slot], &sm.joined[slot], static_cast<uint32_t>(lane), 0.f, 0.f);
+      __syncwarp();
+      if (kGrad) {
+        if (r != begin) sparse(r - 2 * step, it - 2, mine, twice);
+        mine = first_entries(a, n, table, slots, e0, e1, twice);
+      }
+    }
+    if (kGrad && begin < a.T) sparse(first + (it - 2) * step, it - 2, mine, twice);
   } else if (warp == W + 3) {
     // joins the row's maxima and sums, and forms the constants of its gradient and (first block) its loss
     int64_t it = 0;
     for (int64_t r = first; r < a.T; r += step, ++it) {
-      const int b = static_cast<int>(it & 1), slot = static_cast<int>(it & (kSlots - 1));
-      wait.cluster(&sm.joined[slot], static_cast<uint32_t>((it / kSlots) & 1));
+      const int slot = static_cast<int>(it & (kSlots - 1));
+      const uint32_t parity = static_cast<uint32_t>((it / kSlots) & 1);
+      wait.cluster(&sm.joined[slot], parity);
       if (lane == 0) mbar_arrive_expect_tx(&sm.joined[slot], bytes);
       // lane by lane (up to four parts each), then the lanes
       const float4* part = &sm.part[slot][0][0];
@@ -440,16 +455,16 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       }
       s = warp_sum(s);
       top = warp_max(top);
-      wait(&sm.ready[b], static_cast<uint32_t>((it >> 1) & 1));
-      const float sq = sm.sq[b];
+      wait(&sm.ready[slot], parity);
+      const float sq = sm.sq[slot];
       if (lane == 0) {
-        if (kGrad) sm.grad[b] = make_gradient(a, k, s, sm.weight[b], sq);
-        mbar_arrive(&sm.solved[b]);
+        if (kGrad) sm.grad[slot] = make_gradient(a, k, s, sm.weight[slot], sq);
+        mbar_arrive(&sm.solved[slot]);
       }
       if (rank == 0) {
         // sum q (ln q - ln p) = sum (q / tau) (td - (z - max z)) - ln sq + ln s: a mask of the type's
         // lowest value leaves the range of fp32 only where the loss does
-        const EntryArrays n = entries(b);
+        const EntryArrays n = entries(slot);
         const float me = finite_or_0(top), f = a.inv_temp / sq;
         float l = 0.f;
         for (int i = lane; i < a.K; i += 32) {
@@ -465,7 +480,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.spare[b]);
+      if (lane == 0) mbar_arrive(&sm.spare[slot]);
     }
   } else {
     Place in, held;  // the next stage to read, and (with a gradient) the next one of the row before
@@ -491,15 +506,15 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
     // The gradient of row r, the it-th of the block. Without a gradient only the wait is left: a warp is
     // at most a row ahead of the joiner, so the exchange slots are read before they are written again.
     auto finish = [&](int64_t r, int64_t it) {
-      const int b = static_cast<int>(it & 1);
-      wait(&sm.solved[b], static_cast<uint32_t>((it >> 1) & 1));
+      const int slot = static_cast<int>(it & (kSlots - 1));
+      wait(&sm.solved[slot], static_cast<uint32_t>((it / kSlots) & 1));
       if (!kGrad) return;
       const T* z = static_cast<const T*>(a.logits) + r * a.ld;
       T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
       const Share sh = share_of(z, a.V, split.per, rank);
       const bool aligned = row_shift(out) == sh.shift;
-      const Gradient g = sm.grad[b];
-      const bool some = sm.weight[b] != 0.0f;
+      const Gradient g = sm.grad[slot];
+      const bool some = sm.weight[slot] != 0.0f;
       for (int c = sh.begin; c < sh.end; c += kStageVecs) {
         Vec v[4];
         const int cnt = min(sh.end - c, kStageVecs);
@@ -528,7 +543,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.dense[b]);
+      if (lane == 0) mbar_arrive(&sm.dense[slot]);
     };
     int64_t it = 0;
     for (int64_t r = first; r < a.T; r += step, ++it) {
@@ -547,7 +562,8 @@ template <typename T, bool kGrad, int W>
 cudaError_t launch_fwd(const KdArgs& a, Split split, cudaStream_t stream) {
   static std::mutex mu;  // guards the occupancy cache
   static StreamCache cache;
-  const int stages = a.K > kManyEntries ? kStages - 1 : kStages, slots = table_slots(a.K);
+  // two rows' shares need four stages; what the entries leave is for the rows ahead
+  const int stages = a.K <= 256 ? kStages : a.K <= 512 ? kStages - 1 : kStages - 2, slots = table_slots(a.K);
   const size_t smem = stages * Shape<W>::kStageBytes + entry_bytes(a.K) + static_cast<size_t>(2) * slots * sizeof(int);
   std::lock_guard<std::mutex> lk(mu);
   return launch_stream(kd_fwd_kernel<T, kGrad, W>, cache, 32 * (W + kExtraWarps), smem, a.T, split.S, false, stream, a,
