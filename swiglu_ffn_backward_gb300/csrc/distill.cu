@@ -13,7 +13,7 @@
 // the gradient of a row is formed after the sums of the next one, so the exchange is off the path. Two
 // more warps take the teacher's entries of every other row each, a row ahead, and write the gradient's
 // sparse part, at most K elements a row, over the dense one.
-// The gradient alone needs no exchange: blocks take 32 KB shares of rows in registers.
+// The gradient alone needs no exchange: blocks take shares of rows in registers.
 #include <mutex>
 
 #include "swg_launch.h"
@@ -23,77 +23,6 @@ namespace swg {
 namespace {
 
 using namespace row;
-
-constexpr int kPer = kKdMaxEntries / kRowThreads;  // entries a thread may take
-
-struct KdSmem {
-  float tmax[kRowWarps];
-  float tsum[kRowWarps];
-  int id[kKdMaxEntries];     // -1: absent
-  float q[kKdMaxEntries];    // exp((t - max t) / tau): probabilities, but for the factor 1 / sq
-};
-
-// The teacher's entries k = threadIdx.x + n kRowThreads of a thread. The loads are issued before the row's
-// own, and the student's logits at the entries (for the ids in [e0, e1)) as soon as the ids are there.
-struct Entries {
-  int id[kPer];    // -1: absent
-  float t[kPer];   // the teacher's logit, then its difference to their maximum
-  float z[kPer];   // the student's logit
-  float e[kPer];   // exp((t - max t) / tau)
-};
-__device__ __forceinline__ float load_entries(const KdArgs& a, int64_t r, Entries& n, KdSmem& sm) {
-  float m = neg_inf();
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int k = threadIdx.x + i * kRowThreads;
-    n.id[i] = -1;
-    n.t[i] = neg_inf();
-    if (k < a.K) {
-      const int64_t id = load_index(a.ids, r * a.K + k, a.wide);
-      const float t = load_any(a.teacher, r * a.K + k, a.tdtype);
-      if (id >= 0 && id < a.V) {
-        n.id[i] = static_cast<int>(id);
-        n.t[i] = t;
-      }
-      sm.id[k] = n.id[i];
-    }
-    m = fmaxf(m, n.t[i]);
-  }
-  return m;
-}
-template <typename T>
-__device__ __forceinline__ void gather_logits(Entries& n, const T* z, int64_t e0, int64_t e1) {
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) n.z[i] = n.id[i] >= e0 && n.id[i] < e1 && n.id[i] >= 0 ? to_f(z[n.id[i]]) : 0.0f;
-}
-// from the entries' maximum: differences and exponentials, and the thread's sum of them
-__device__ __forceinline__ float exp_entries(const KdArgs& a, float m, Entries& n, KdSmem& sm) {
-  const float me = finite_or_0(m);
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int k = threadIdx.x + i * kRowThreads;
-    n.t[i] -= me;
-    n.e[i] = ex2_approx(n.t[i] * a.inv_temp * kLog2e);
-    if (k < a.K) {
-      sm.q[k] = n.e[i];
-      s += n.e[i];
-    }
-  }
-  return s;
-}
-__device__ __forceinline__ float warps_max(const float* v) {
-  float m = v[0];
-#pragma unroll
-  for (int i = 1; i < kRowWarps; ++i) m = fmaxf(m, v[i]);
-  return m;
-}
-__device__ __forceinline__ float warps_sum(const float* v) {
-  float s = v[0];
-#pragma unroll
-  for (int i = 1; i < kRowWarps; ++i) s += v[i];
-  return s;
-}
 
 struct Gradient {
   Scale k;       // 2^fma(z, k.c, -k.ref) / s is the probability
@@ -108,46 +37,6 @@ __device__ __forceinline__ Gradient make_gradient(const KdArgs& a, const Scale& 
 __device__ __forceinline__ float2 dense_pair(const Gradient& g, float2 z) {
   const float2 x = __ffma2_rn(z, make_float2(g.k.c, g.k.c), make_float2(-g.k.ref, -g.k.ref));
   return __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(g.dense, g.dense));
-}
-
-// the dense part of the chunk at c
-template <typename T>
-__device__ __forceinline__ void store_dense(Vec (&v)[kVecs], const Gradient& g, T* out, int64_t V, bool aligned,
-                                            const Share& sh, int c) {
-  constexpr int E = Traits<T>::E;
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int at = c + i * kRowThreads + static_cast<int>(threadIdx.x);
-    if (at >= sh.end) break;
-#pragma unroll
-    for (int p = 0; p < E / 2; ++p) set_pair<T>(v[i], p, dense_pair(g, vec_pair<T>(v[i], p)));
-    store_row_vec(out, first_element<T>(sh, at), V, aligned, v[i]);
-  }
-}
-// a gradient of zeros
-template <typename T>
-__device__ __forceinline__ void store_zeros(T* out, int64_t V, bool aligned, const Share& sh) {
-  const Vec zero = {{0u, 0u, 0u, 0u}};
-  for (int at = sh.begin + static_cast<int>(threadIdx.x); at < sh.end; at += kRowThreads)
-    store_row_vec(out, first_element<T>(sh, at), V, aligned, zero);
-}
-// the elements at the entries in [e0, e1); an id that comes twice is written by its first entry
-template <typename T>
-__device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g, const Entries& n, const KdSmem& sm,
-                                             T* out, int64_t e0, int64_t e1) {
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int k = threadIdx.x + i * kRowThreads, id = n.id[i];
-    if (id < 0 || id < e0 || id >= e1) continue;
-    float q = 0.f;
-    bool first = true;
-    for (int j = 0; j < a.K; ++j) {
-      if (sm.id[j] != id) continue;
-      first = first && j >= k;
-      q += sm.q[j];
-    }
-    if (first) out[id] = from_f<T>(fmaf(g.dense, ex2_approx(fmaf(n.z[i], g.k.c, -g.k.ref)), -g.sparse * q));
-  }
 }
 
 // ---- loss, and loss with gradient
@@ -314,6 +203,31 @@ __device__ __forceinline__ uint32_t first_entries(const KdArgs& a, const EntryAr
   return mine;
 }
 static_assert(kKdMaxEntries <= 32 * 32, "a bit for each of a lane's entries");
+// One warp: the elements at the entries in `mine`. An id that comes twice is taken at its first entry, its
+// probabilities added lane by lane.
+template <typename T>
+__device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g, const EntryArrays& n, uint32_t mine,
+                                             bool twice, T* out) {
+  const int lane = threadIdx.x & 31;
+  const float c2 = a.inv_temp * kLog2e;
+  for (int k0 = 0; k0 < a.K; k0 += 32) {
+    const bool own = mine >> (k0 / 32) & 1u;
+    const int id = own ? n.id[k0 + lane] : -1;
+    float q = own ? ex2_approx(n.td[k0 + lane] * c2) : 0.0f;
+    if (twice) {
+      for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo != 0; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1, its = __shfl_sync(0xffffffffu, id, from);
+        float t = 0.f;
+        for (int j = lane; j < a.K; j += 32)
+          if (n.id[j] == its) t += ex2_approx(n.td[j] * c2);
+        t = warp_sum(t);
+        if (lane == from) q = t;
+      }
+    }
+    if (own)
+      out[id] = from_f<T>(fmaf(g.dense, ex2_approx(fmaf(n.z[k0 + lane], g.k.c, -g.k.ref)), -g.sparse * q));
+  }
+}
 
 template <typename T, bool kGrad, int W>
 __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
@@ -366,32 +280,14 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       gather_some(a, r, 0, loads, rank == 0 ? 0 : first_element<T>(sh, sh.begin),
                   rank == 0 ? a.V : first_element<T>(sh, sh.end), next);
     };
-    // the elements at the entries of row r, the it-th, over the dense part; an id that comes twice is
-    // taken at its first entry, its probabilities added lane by lane
+    // the elements at the entries of row r, the it-th, over the dense part
     auto sparse = [&](int64_t r, int64_t it, uint32_t mine, bool twice) {
       const int slot = static_cast<int>(it & (kSlots - 1));
       wait(&sm.dense[slot], static_cast<uint32_t>((it / kSlots) & 1));
       if (sm.weight[slot] == 0.0f) return;
       const EntryArrays n = entries(slot);
       const Gradient g = sm.grad[slot];
-      T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
-      for (int k0 = 0; k0 < a.K; k0 += 32) {
-        const bool own = mine >> (k0 / 32) & 1u;
-        const int id = own ? n.id[k0 + lane] : -1;
-        float q = own ? ex2_approx(n.td[k0 + lane] * c2) : 0.0f;
-        if (twice) {
-          for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo != 0; todo &= todo - 1) {
-            const int from = __ffs(todo) - 1, its = __shfl_sync(0xffffffffu, id, from);
-            float t = 0.f;
-            for (int j = lane; j < a.K; j += 32)
-              if (n.id[j] == its) t += ex2_approx(n.td[j] * c2);
-            t = warp_sum(t);
-            if (lane == from) q = t;
-          }
-        }
-        if (own)
-          out[id] = from_f<T>(fmaf(g.dense, ex2_approx(fmaf(n.z[k0 + lane], g.k.c, -g.k.ref)), -g.sparse * q));
-      }
+      store_sparse<T>(a, g, n, mine, twice, static_cast<T*>(a.dlogits) + r * a.ldo);
       __syncwarp();
     };
     if (begin < a.T) {
@@ -578,42 +474,75 @@ cudaError_t launch_fwd_any(const KdArgs& a, int dtype, Split split, cudaStream_t
 
 // ---- gradient alone
 
-// the gradient from saved statistics
+// The gradient from saved statistics: a block of G threads (64 to 256) takes a share of a row, 16 to 32 KB in
+// registers. While it arrives, the first warp takes the teacher's entries; it looks for ids that come twice
+// while the others form the dense part, and writes the sparse part over it.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 3) kd_bwd_kernel(const KdArgs a, int64_t row0, Split split) {
-  __shared__ KdSmem sm;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t r = row0 + blockIdx.x / split.S;
+__global__ void __launch_bounds__(kRowThreads, 4) kd_bwd_kernel(const KdArgs a, int64_t share0, Groups p, int slots) {
+  constexpr int E = Traits<T>::E;
+  extern __shared__ __align__(16) unsigned char dyn[];
+  __shared__ float sq_all;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t at = share0 + blockIdx.x, r = at / p.S;
   const T* z = static_cast<const T*>(a.logits) + r * a.ld;
   T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
-  const Share sh = share_of(z, a.V, split.per, static_cast<int>(blockIdx.x % split.S));
+  const Share sh = share_of(z, a.V, p.per, static_cast<int>(at - r * p.S));
   const bool aligned = row_shift(out) == sh.shift;
-  const float w = a.weight[r];
+  const float w = a.weight[r], c2 = a.inv_temp * kLog2e;
   if (w == 0.0f) {
-    store_zeros(out, a.V, aligned, sh);
+    const Vec zero = {{0u, 0u, 0u, 0u}};
+    for (int g = sh.begin + tid; g < sh.end; g += p.G) store_row_vec(out, first_element<T>(sh, g), a.V, aligned, zero);
     return;
   }
   const int64_t e0 = first_element<T>(sh, sh.begin), e1 = first_element<T>(sh, sh.end);
-  Entries n;
-  const float tmax = load_entries(a, r, n, sm);
+  const EntryArrays n = entry_arrays(dyn, a.K, 0);
+  EntryLoads loads;
+  if (tid < 32) load_some(a, r, 0, loads);
   Vec v[kVecs];
-  load_chunk<T, false>(v, z, a.V, sh, sh.begin);
-  gather_logits(n, z, e0, e1);
-  const float wm = warp_max(tmax);
-  if (lane == 0) sm.tmax[warp] = wm;
-  __syncthreads();
-  const float ts = warp_sum(exp_entries(a, warps_max(sm.tmax), n, sm));
-  if (lane == 0) sm.tsum[warp] = ts;
+  load_chunk<T, false>(v, z, a.V, sh, sh.begin, tid, p.G);
+  if (tid < 32) {
+    EntryValues<T> values;
+    gather_some(a, r, 0, loads, e0, e1, values);
+    const float sq = take_entries<T>(a, r, values, n, e0, e1);
+    if (lane == 0) sq_all = sq;
+  }
   __syncthreads();
   const float m = a.stats_in[2 * r];
-  const Scale k = scale_of(m, a.inv_temp * kLog2e);
-  const Gradient g = make_gradient(a, k, sum_at_ref(a.stats_in[2 * r + 1], m, k), w, warps_sum(sm.tsum));
-  for (int c = sh.begin; c < sh.end; c += kChunk) {
-    if (c > sh.begin) load_chunk<T, false>(v, z, a.V, sh, c);
-    store_dense(v, g, out, a.V, aligned, sh, c);
+  const Scale k = scale_of(m, c2);
+  const Gradient g = make_gradient(a, k, sum_at_ref(a.stats_in[2 * r + 1], m, k), w, sq_all);
+  for (int c = sh.begin; c < sh.end; c += kVecs * p.G) {
+    if (c > sh.begin) load_chunk<T, false>(v, z, a.V, sh, c, tid, p.G);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int at = c + i * p.G + tid;
+      if (at >= sh.end) break;
+#pragma unroll
+      for (int q = 0; q < E / 2; ++q) set_pair<T>(v[i], q, dense_pair(g, vec_pair<T>(v[i], q)));
+      store_row_vec(out, first_element<T>(sh, at), a.V, aligned, v[i]);
+    }
   }
-  __syncthreads();  // the sparse part goes over the dense one
-  store_sparse(a, g, n, sm, out, e0, e1);
+  bool twice = false;
+  uint32_t mine = 0;
+  if (tid < 32) mine = first_entries(a, n, reinterpret_cast<int*>(dyn) + 3 * a.K, slots, e0, e1, twice);
+  __syncthreads();
+  if (tid < 32) store_sparse<T>(a, g, n, mine, twice, out);
+}
+
+cudaError_t launch_bwd(const KdArgs& a, int dtype, int64_t vectors, int sms, cudaStream_t stream) {
+  Groups p = row_groups(a.T, vectors, sms);
+  if (p.G < 64) p.G = 64;
+  const int slots = table_slots(a.K);
+  const size_t smem = static_cast<size_t>(3 * a.K + slots) * sizeof(int);  // 20 KB at most
+  const int64_t total = a.T * p.S, most = int64_t(1) << 30;
+  for (int64_t s0 = 0; s0 < total; s0 += most) {
+    const unsigned blocks = static_cast<unsigned>(total - s0 < most ? total - s0 : most);
+    if (dtype == 0) kd_bwd_kernel<float><<<blocks, p.G, smem, stream>>>(a, s0, p, slots);
+    else if (dtype == 1) kd_bwd_kernel<__half><<<blocks, p.G, smem, stream>>>(a, s0, p, slots);
+    else kd_bwd_kernel<__nv_bfloat16><<<blocks, p.G, smem, stream>>>(a, s0, p, slots);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -639,8 +568,7 @@ cudaError_t launch_distill(const KdArgs& a, bool forward, bool backward, int dty
   }
   KdArgs b = a;
   if (forward) b.stats_in = a.stats;
-  return launch_all_rows(b, dtype, split_row(a.T, vectors, kChunk, sms), false, stream, kd_bwd_kernel<float>,
-                         kd_bwd_kernel<__half>, kd_bwd_kernel<__nv_bfloat16>);
+  return launch_bwd(b, dtype, vectors, sms, stream);
 }
 
 }  // namespace swg

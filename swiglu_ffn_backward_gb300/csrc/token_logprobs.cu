@@ -419,12 +419,15 @@ cudaError_t launch_fwd_any(const TlpFwdArgs& a, int dtype, Split split, cudaStre
 
 // Backward: bound by HBM (V elements read and written a row); no block needs another's results.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) tlp_bwd_kernel(const TlpBwdArgs a, int64_t row0, Split split) {
+__global__ void __launch_bounds__(kRowThreads, 4) tlp_bwd_kernel(const TlpBwdArgs a, int64_t group0, Groups p) {
   constexpr int E = Traits<T>::E;
-  const int64_t r = row0 + blockIdx.x / split.S;
+  const int64_t group = group0 + static_cast<int64_t>(blockIdx.x) * (kRowThreads / p.G) + threadIdx.x / p.G;
+  const int tid = threadIdx.x & (p.G - 1);
+  const int64_t r = group / p.S;
+  if (r >= a.T) return;
   const T* z = static_cast<const T*>(a.logits) + r * a.ld;
   T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
-  const Share sh = share_of(z, a.V, split.per, static_cast<int>(blockIdx.x % split.S));
+  const Share sh = share_of(z, a.V, p.per, static_cast<int>(group - r * p.S));
   const bool aligned = row_shift(out) == sh.shift;
   const float m = a.stats[2 * r];
   const Scale k = scale_of(m, a.inv_temp * kLog2e);
@@ -443,31 +446,31 @@ __global__ void __launch_bounds__(kRowThreads) tlp_bwd_kernel(const TlpBwdArgs a
   const int64_t tt = t != a.ignore && valid && s != 0.0f ? t : -1;
   const float2 nref = make_float2(-k.ref, -k.ref), kc = make_float2(k.c, k.c), k02 = make_float2(k0, k0);
   const float2 k12 = make_float2(k1, k1);
-  for (int c = sh.begin; c < sh.end; c += kChunk) {
+  for (int c = sh.begin; c < sh.end; c += kVecs * p.G) {
     Vec v[kVecs];
-    load_chunk<T, false>(v, z, a.V, sh, c);
+    load_chunk<T, false>(v, z, a.V, sh, c, tid, p.G);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int g = c + i * kRowThreads + static_cast<int>(threadIdx.x);
+      const int g = c + i * p.G + tid;
       if (g >= sh.end) break;
       const int64_t e0 = first_element<T>(sh, g);
 #pragma unroll
-      for (int p = 0; p < E / 2; ++p) {
-        float2 x = __ffma2_rn(vec_pair<T>(v[i], p), kc, nref);
+      for (int n = 0; n < E / 2; ++n) {
+        float2 x = __ffma2_rn(vec_pair<T>(v[i], n), kc, nref);
         x = make_float2(at_least(x.x), at_least(x.y));
         const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-        set_pair<T>(v[i], p, __fmul2_rn(e, __ffma2_rn(k12, x, k02)));
+        set_pair<T>(v[i], n, __fmul2_rn(e, __ffma2_rn(k12, x, k02)));
       }
       if (tt >= e0 && tt < e0 + E) {  // the target: formed anew, rounded once
         const float x0 = at_least(fmaf(to_f(z[tt]), k.c, -k.ref));
         const float x = fmaf(dl, a.inv_temp, ex2_approx(x0) * fmaf(k1, x0, k0));
         const int at = static_cast<int>(tt - e0);
 #pragma unroll
-        for (int p = 0; p < E / 2; ++p) {
-          float2 y = vec_pair<T>(v[i], p);
-          if (at == 2 * p) y.x = x;
-          if (at == 2 * p + 1) y.y = x;
-          set_pair<T>(v[i], p, y);
+        for (int n = 0; n < E / 2; ++n) {
+          float2 y = vec_pair<T>(v[i], n);
+          if (at == 2 * n) y.x = x;
+          if (at == 2 * n + 1) y.y = x;
+          set_pair<T>(v[i], n, y);
         }
       }
       store_row_vec(out, e0, a.V, aligned, v[i]);
@@ -489,9 +492,9 @@ cudaError_t launch_token_logprobs_fwd(const TlpFwdArgs& a, int dtype, cudaStream
 }
 
 cudaError_t launch_token_logprobs_bwd(const TlpBwdArgs& a, int dtype, cudaStream_t stream) {
-  const Split p = split_row(a.T, row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2), kChunk, device_sm_count());
-  return launch_all_rows(a, dtype, p, false, stream, tlp_bwd_kernel<float>, tlp_bwd_kernel<__half>,
-                         tlp_bwd_kernel<__nv_bfloat16>);
+  const int64_t vectors = row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2);
+  return launch_groups(a, dtype, row_groups(a.T, vectors, device_sm_count()), stream, tlp_bwd_kernel<float>,
+                       tlp_bwd_kernel<__half>, tlp_bwd_kernel<__nv_bfloat16>);
 }
 
 }  // namespace swg

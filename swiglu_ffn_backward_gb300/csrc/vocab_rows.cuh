@@ -3,9 +3,8 @@
 // A row is cut into 16-byte vectors at 16-byte aligned addresses, whatever the address of its first
 // element: vector g holds the elements [g E - shift, g E - shift + E), shift being the number of
 // elements between the aligned address at or below the row's start and that start. Only a row's first
-// and last vector can be partial; they are read and written element by element, inside the row. A block
-// takes a run of a row's vectors, kVecs of them in each thread's registers at a time; the S blocks of
-// one row form a cluster and exchange their results through distributed shared memory.
+// and last vector can be partial; they are read and written element by element, inside the row. S blocks
+// (or groups of threads) take a run of a row's vectors each, their share.
 #pragma once
 
 #include "row_ops.cuh"
@@ -16,7 +15,6 @@ namespace row {
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kVecs = 8;                          // 16-byte vectors a thread holds: 32 registers
-constexpr int kChunk = kRowThreads * kVecs;       // vectors a block holds (32 KB)
 constexpr int kMaxCluster = 8;                    // portable cluster size
 
 template <typename T>
@@ -235,12 +233,13 @@ template <typename T>
 __device__ __forceinline__ int64_t first_element(const Share& s, int g) {
   return static_cast<int64_t>(g) * Traits<T>::E - s.shift;
 }
-// vectors c + i kRowThreads + threadIdx.x of the share -> v[i]; -inf past its end
+// vectors c + i G + t of the share, t the thread's number in its group of G -> v[i]; -inf past its end
 template <typename T, bool kReadOnly>
-__device__ __forceinline__ void load_chunk(Vec (&v)[kVecs], const T* row, int64_t V, const Share& s, int c) {
+__device__ __forceinline__ void load_chunk(Vec (&v)[kVecs], const T* row, int64_t V, const Share& s, int c, int t,
+                                           int G) {
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int g = c + i * kRowThreads + static_cast<int>(threadIdx.x);
+    const int g = c + i * G + t;
     if (g < s.end) {
       v[i] = load_row_vec<T, kReadOnly>(row, first_element<T>(s, g), V);
     } else {
@@ -339,33 +338,35 @@ inline Split split_row(int64_t T, int64_t vectors, int64_t share, int num_sms) {
   return Split{static_cast<int>(s), static_cast<int>((vectors + s - 1) / s)};
 }
 
-// launches of at most kMaxLaunchRows rows: their blocks stay below 2^31
-constexpr int64_t kMaxLaunchRows = int64_t(1) << 27;
-
-template <typename Kernel, typename... Args>
-cudaError_t launch_rows(Kernel kernel, int64_t rows, int S, bool cluster, cudaStream_t stream, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * S));
-  cfg.blockDim = dim3(row::kRowThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(S);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+// The kernels that need no exchange (gradients from saved statistics): a group of G threads, 32 to 256,
+// takes a share of up to kVecs vectors a thread of one row; a block of 256 threads has 256 / G such groups.
+struct Groups {
+  int S;    // groups a row
+  int per;  // vectors a group takes
+  int G;
+};
+inline Groups row_groups(int64_t T, int64_t vectors, int num_sms) {
+  int G = 32;
+  while (G < row::kRowThreads && G * row::kVecs < vectors) G *= 2;
+  const int64_t chunk = static_cast<int64_t>(G) * row::kVecs;
+  const int64_t useful = (vectors + G - 1) / G, spread = 4 * num_sms / T;  // at least a vector a thread
+  int64_t s = (vectors + chunk - 1) / chunk;
+  if (s < spread && s < useful) s = spread < useful ? spread : useful;
+  return Groups{static_cast<int>(s), static_cast<int>((vectors + s - 1) / s), G};
 }
-// all T rows of `a`
+// Launches of at most 2^22 blocks or so at a time, whatever the number of rows.
 template <typename Args, typename K32, typename K16, typename KB>
-cudaError_t launch_all_rows(const Args& a, int dtype, Split p, bool cluster, cudaStream_t stream, K32 k32, K16 k16,
-                            KB kb) {
-  for (int64_t row0 = 0; row0 < a.T; row0 += kMaxLaunchRows) {
-    const int64_t rows = a.T - row0 < kMaxLaunchRows ? a.T - row0 : kMaxLaunchRows;
-    const cudaError_t e = dtype == 0   ? launch_rows(k32, rows, p.S, cluster, stream, a, row0, p)
-                          : dtype == 1 ? launch_rows(k16, rows, p.S, cluster, stream, a, row0, p)
-                                       : launch_rows(kb, rows, p.S, cluster, stream, a, row0, p);
+cudaError_t launch_groups(const Args& a, int dtype, const Groups& p, cudaStream_t stream, K32 k32, K16 k16, KB kb) {
+  const int per_block = row::kRowThreads / p.G;
+  const int64_t most = (int64_t(1) << 22) * per_block;  // groups a launch
+  const int64_t total = a.T * p.S;
+  for (int64_t g0 = 0; g0 < total; g0 += most) {
+    const int64_t n = total - g0 < most ? total - g0 : most;
+    const unsigned blocks = static_cast<unsigned>((n + per_block - 1) / per_block);
+    if (dtype == 0) k32<<<blocks, row::kRowThreads, 0, stream>>>(a, g0, p);
+    else if (dtype == 1) k16<<<blocks, row::kRowThreads, 0, stream>>>(a, g0, p);
+    else kb<<<blocks, row::kRowThreads, 0, stream>>>(a, g0, p);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -172,6 +172,7 @@ struct WarpSums {
   float m = neg_inf();    // reference logit
   float lim = neg_inf();  // a logit above it raises the reference
   float top = neg_inf();  // the thread's maximum
+  bool masked = false;    // the row has shown a -inf: more are likely
   Scale k;
   float2 s2{0.f, 0.f}, w2{0.f, 0.f};
 
@@ -192,8 +193,8 @@ struct WarpSums {
       }
     }
   }
-  // returns the largest of the thread's logits; masked: -infs are likely
-  __device__ __forceinline__ float add(const Vec (&v)[4], float c, bool masked) {
+  // returns the largest of the thread's logits; padded: some of them are -inf for being behind the row
+  __device__ __forceinline__ float add(const Vec (&v)[4], float c, bool padded) {
     const float most = vec_max4<T>(v);
     if (__any_sync(0xffffffffu, most > lim)) {
       const float mn = warp_max(fmaxf(most, m));
@@ -212,15 +213,14 @@ struct WarpSums {
     }
     // a -inf makes the second sum 0 * inf: only then the exponents are kept above it
     const float2 s0 = s2, w0 = w2;
-    if (!masked) {
+    if (!masked && !padded) {
       add_terms<false>(v);
       masked = __any_sync(0xffffffffu, !(w2.x + w2.y == w2.x + w2.y));
-    }
-    if (masked) {
+      if (!masked) return most;
       s2 = s0;
       w2 = w0;
-      add_terms<true>(v);
     }
+    add_terms<true>(v);
     return most;
   }
   // reference logit, sum 2^x, sum 2^x x, maximum
