@@ -614,7 +614,14 @@ def _like_rows(t, name, x, shape):
     if isinstance(t, torch.Tensor) and (t.dtype != x.dtype or t.shape != shape):
         raise ValueError(f"{name} must have the shape {tuple(shape)} and dtype {x.dtype}, got {tuple(t.shape)}, {t.dtype}")
     t, _, _, ld, _ = _row_tensor(t, name)
+    if t.device != x.device:
+        _device_of(x, t)  # raises
     return t, ld
+
+
+def _new(x):
+    """An output like x, dense."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _vector(t, name, n, dtypes, device):
@@ -657,21 +664,18 @@ def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, o
     gamma, beta, wdtype = _norm_weights(gamma, beta, N, xt)
     dev = xt.device
     if out is None:
-        out = {"y": torch.empty(shape, dtype=xt.dtype, device=dev),
-               "stats": torch.empty((M, 2), dtype=torch.float32, device=dev)}
+        y, st, h = _new(x), torch.empty((M, 2), dtype=torch.float32, device=dev), None
+        out = {"y": y, "stats": st}
         if res is not None:
-            out["h"] = torch.empty(shape, dtype=xt.dtype, device=dev)
+            out["h"] = h = _new(x)
     else:
-        out = dict(out)
-        out["y"] = _out(out.get("y"), shape, xt.dtype, dev, "y")
-        out["stats"] = _out(out.get("stats"), (M, 2), torch.float32, dev, "stats")
+        out, h = dict(out), None
+        out["y"] = y = _out(out.get("y"), shape, xt.dtype, dev, "y")
+        out["stats"] = st = _out(out.get("stats"), (M, 2), torch.float32, dev, "stats")
         if res is not None:
-            out["h"] = _out(out.get("h"), shape, xt.dtype, dev, "h")
-    if res is not None and res.device != dev:
-        _device_of(xt, res)
-    _run("layer_norm_fwd", lib.layer_norm_fwd, dev, xt.data_ptr(), _ptr(res), _ptr(gamma), _ptr(beta),
-         out["h"].data_ptr() if res is not None else None, out["y"].data_ptr(), out["stats"].data_ptr(), M, N, ldx,
-         ldr, eps, code, _DTYPE[wdtype])
+            out["h"] = h = _out(out.get("h"), shape, xt.dtype, dev, "h")
+    _run("layer_norm_fwd", lib.layer_norm_fwd, dev, xt.data_ptr(), _ptr(res), _ptr(gamma), _ptr(beta), _ptr(h),
+         y.data_ptr(), st.data_ptr(), M, N, ldx, ldr, eps, code, _DTYPE[wdtype])
     return out
 
 
@@ -699,16 +703,16 @@ def layer_norm_bwd(dy, x, stats, gamma=None, dh=None, params: bool = True, dx=No
     if stats is None:
         raise TypeError("stats must be a CUDA tensor")
     gamma, _, wdtype = _norm_weights(gamma, None, N, xt)
-    dx = torch.empty(shape, dtype=xt.dtype, device=dev) if dx is None else _out(dx, shape, xt.dtype, dev, "dx")
+    dx = _new(x) if dx is None else _out(dx, shape, xt.dtype, dev, "dx")
     ws = None
     if params:
         dgamma = _out(dgamma, (N,), wdtype, dev, "dgamma")
         dbeta = _out(dbeta, (N,), wdtype, dev, "dbeta")
-        ws = _workspace(_call(dev, lib.layer_norm_bwd_workspace_size, M, N) if torch.cuda.current_device() != dev.index
-                        else lib.layer_norm_bwd_workspace_size(M, N), dev, workspace)
+        ws = _workspace(lib.layer_norm_bwd_workspace_size(M, N), dev, workspace)
+        if workspace is not None:
+            _device_of(xt, ws)
     else:
         dgamma = dbeta = None
-    _device_of(xt, dyt, dht, ws)
     _run("layer_norm_bwd", lib.layer_norm_bwd, dev, dyt.data_ptr(), xt.data_ptr(), stats.data_ptr(), _ptr(gamma),
          _ptr(dht), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta), M, N, lddy, ldx, lddh, code, _DTYPE[wdtype], _ptr(ws),
          _nbytes(ws))
@@ -743,18 +747,18 @@ def token_logprobs_fwd(logits, targets=None, top_k: int = 0, temperature: float 
     z, T, V, ld, code = _row_tensor(logits, "logits")
     dev = z.device
     targets = _vector(targets, "targets", T, _INDEX, dev)
-    given = out or {}
-    f32, mk = torch.float32, (lambda k, shape, dt: torch.empty(shape, dtype=dt, device=dev) if given.get(k) is None
-                              else _out(given[k], shape, dt, dev, k))
-    out = {"entropy": mk("entropy", lead, f32), "stats": mk("stats", (T, 2), f32)}
+    given, f32 = out or {}, torch.float32
+    out = {"entropy": _out(given.get("entropy"), lead, f32, dev, "entropy"),
+           "stats": _out(given.get("stats"), (T, 2), f32, dev, "stats")}
+    logp = top_logp = top_idx = None
     if targets is not None:
-        out["logp"] = mk("logp", lead, f32)
+        out["logp"] = logp = _out(given.get("logp"), lead, f32, dev, "logp")
     if top_k > 0:
-        out["top_logp"] = mk("top_logp", (*lead, top_k), f32)
-        out["top_idx"] = mk("top_idx", (*lead, top_k), torch.int64)
-    _run("token_logprobs_fwd", lib.token_logprobs_fwd, dev, z.data_ptr(), _ptr(targets), _ptr(out.get("logp")),
-         out["entropy"].data_ptr(), out["stats"].data_ptr(), _ptr(out.get("top_logp")), _ptr(out.get("top_idx")),
-         T, V, ld, top_k, temperature, ignore_index, code, _itype(targets))
+        out["top_logp"] = top_logp = _out(given.get("top_logp"), (*lead, top_k), f32, dev, "top_logp")
+        out["top_idx"] = top_idx = _out(given.get("top_idx"), (*lead, top_k), torch.int64, dev, "top_idx")
+    _run("token_logprobs_fwd", lib.token_logprobs_fwd, dev, z.data_ptr(), _ptr(targets), _ptr(logp),
+         out["entropy"].data_ptr(), out["stats"].data_ptr(), _ptr(top_logp), _ptr(top_idx), T, V, ld, top_k,
+         temperature, ignore_index, code, _itype(targets))
     return out
 
 

@@ -12,9 +12,9 @@
 // variance is taken of centred values in a second pass over the registers. Vectors are the widest that
 // the row length, strides and addresses allow (16 bytes, 4 bytes or one element). Rows too long for the
 // registers of a block are read again (ln_fwd_long_kernel, ln_dx_long_kernel).
-// Backward: persistent groups, each thread the same columns of every row, so the columns' sums of
-// dgamma and dbeta stay in registers; the next row is loaded under the work on this one. The blocks'
-// sums go to the workspace and are added by a second kernel in a fixed order.
+// The groups are persistent and load the next row under the work on this one.
+// Backward: each thread has the same columns of every row, so the columns' sums of dgamma and dbeta stay
+// in registers. The blocks' sums go to the workspace and are added by a second kernel in a fixed order.
 #include <mutex>
 
 #include "row_ops.cuh"
@@ -45,6 +45,8 @@ struct Raw<2> {
   uint16_t u;
 };
 template <int kBytes>
+constexpr int kRegs = (kBytes + 3) / 4;  // registers of one
+template <int kBytes>
 __device__ __forceinline__ Raw<kBytes> ld_stream(const void* p);
 template <>
 __device__ __forceinline__ Raw<16> ld_stream<16>(const void* p) {
@@ -62,47 +64,95 @@ template <>
 __device__ __forceinline__ Raw<2> ld_stream<2>(const void* p) {
   return Raw<2>{__ldg(static_cast<const uint16_t*>(p))};
 }
+// 16-bit elements are widened and narrowed two at a time, word by word
+__device__ __forceinline__ float2 widen(uint32_t u, __half) {
+  const __half2 h = *reinterpret_cast<const __half2*>(&u);
+  return __half22float2(h);
+}
+__device__ __forceinline__ float2 widen(uint32_t u, __nv_bfloat16) { return bf16x2_to_f2(u); }
+__device__ __forceinline__ uint32_t narrow(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t narrow(float a, float b, __nv_bfloat16) { return pack_bf16x2(a, b); }
 template <typename T, int E>
 __device__ __forceinline__ void to_floats(const Raw<E * sizeof(T)>& r, float (&f)[E]) {
-  const T* t = reinterpret_cast<const T*>(&r);
+  if constexpr (sizeof(T) == 2 && E >= 2) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
 #pragma unroll
-  for (int e = 0; e < E; ++e) f[e] = to_f(t[e]);
+    for (int i = 0; i < E / 2; ++i) {
+      const float2 v = widen(w[i], T());
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+  } else {
+    const T* t = reinterpret_cast<const T*>(&r);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = to_f(t[e]);
+  }
 }
 template <typename T, int E>
 __device__ __forceinline__ Raw<E * sizeof(T)> from_floats(const float (&f)[E]) {
   Raw<E * sizeof(T)> r;
-  T* t = reinterpret_cast<T*>(&r);
+  if constexpr (sizeof(T) == 2 && E >= 2) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
-  for (int e = 0; e < E; ++e) t[e] = from_f<T>(f[e]);
+    for (int i = 0; i < E / 2; ++i) w[i] = narrow(f[2 * i], f[2 * i + 1], T());
+  } else {
+    T* t = reinterpret_cast<T*>(&r);
+#pragma unroll
+    for (int e = 0; e < E; ++e) t[e] = from_f<T>(f[e]);
+  }
   return r;
 }
+// The arithmetic is on pairs with the packed fp32x2 operations (half the instructions; a single element is
+// a pair with an idle half): E elements are (E + 1) / 2 pairs.
+template <int E>
+constexpr int kPairs = (E + 1) / 2;
+template <typename T, int E>
+__device__ __forceinline__ void to_pairs(const Raw<E * sizeof(T)>& r, float2 (&p)[kPairs<E>]) {
+  float f[E];
+  to_floats<T, E>(r, f);
+#pragma unroll
+  for (int i = 0; i < kPairs<E>; ++i) p[i] = make_float2(f[2 * i], E > 1 ? f[(2 * i + 1) % E] : 0.0f);
+}
+template <typename T, int E>
+__device__ __forceinline__ Raw<E * sizeof(T)> from_pairs(const float2 (&p)[kPairs<E>]) {
+  float f[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) f[e] = e % 2 == 0 ? p[e / 2].x : p[e / 2].y;
+  return from_floats<T, E>(f);
+}
+__device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+
 template <int kBytes>
 __device__ __forceinline__ void st_stream(void* p, const Raw<kBytes>& r) {
   *static_cast<Raw<kBytes>*>(p) = r;
 }
 // E weights of either type (cached: every row uses them)
 template <typename T, int E>
-__device__ __forceinline__ void load_weights(const void* p, int64_t j, bool f32, float (&f)[E]) {
+__device__ __forceinline__ void load_weights(const void* p, int64_t j, bool f32, float2 (&f)[kPairs<E>]) {
   if (sizeof(T) == 4 || f32) {
     const float* w = static_cast<const float*>(p) + j;
     if constexpr (E % 4 == 0) {
 #pragma unroll
       for (int e = 0; e < E; e += 4) {
         const float4 v = __ldg(reinterpret_cast<const float4*>(w + e));
-        f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
+        f[e / 2] = make_float2(v.x, v.y);
+        f[e / 2 + 1] = make_float2(v.z, v.w);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = __ldg(w + e);
+      for (int i = 0; i < kPairs<E>; ++i) f[i] = make_float2(__ldg(w + 2 * i), E > 1 ? __ldg(w + 2 * i + 1) : 0.0f);
     }
   } else {
     const T* w = static_cast<const T*>(p) + j;
     if constexpr (E * sizeof(T) == 16) {
-      Raw<16> r{__ldg(reinterpret_cast<const uint4*>(w))};
-      to_floats<T, E>(r, f);
+      const Raw<16> r{__ldg(reinterpret_cast<const uint4*>(w))};
+      to_pairs<T, E>(r, f);
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = to_f(w[e]);
+      for (int i = 0; i < kPairs<E>; ++i) f[i] = make_float2(to_f(w[2 * i]), E > 1 ? to_f(w[2 * i + 1]) : 0.0f);
     }
   }
 }
@@ -142,80 +192,94 @@ constexpr int kMaxGroup = 1024;
 constexpr int kMaxBwdGroup = 512;  // the column sums take registers
 
 // ---- forward
-template <typename T, int E, int R>
-__global__ void __launch_bounds__(kMaxGroup) ln_fwd_kernel(const LnFwdArgs a, int G) {
+template <typename T, int E, int R, int kMost>  // kMost: the block's threads, at most
+__global__ void __launch_bounds__(kMost) ln_fwd_kernel(const LnFwdArgs a, int G) {
   __shared__ float smem[2 * 32];
   constexpr int kBytes = E * sizeof(T);
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + threadIdx.x / G;
+  // the next row is loaded under the work on this one where the registers have room for it
+  constexpr bool kAhead = R * kRegs<kBytes> <= 8;
+  const int groups = blockDim.x / G;
   const int t = threadIdx.x & (G - 1);
-  if (r >= a.M) return;  // whole groups
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const int n = static_cast<int>(a.N / E);
-  const T* x = static_cast<const T*>(a.x) + r * a.ldx;
-  Raw<kBytes> raw[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (t + i * G < n) raw[i] = ld_stream<kBytes>(x + static_cast<int64_t>(t + i * G) * E);
-  float f[R][E];
-  if (a.residual != nullptr) {
-    const T* res = static_cast<const T*>(a.residual) + r * a.ldr;
-    T* h = static_cast<T*>(a.h) + r * a.N;
-    Raw<kBytes> rr[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (t + i * G < n) rr[i] = ld_stream<kBytes>(res + static_cast<int64_t>(t + i * G) * E);
+  const bool add = a.residual != nullptr, f32 = a.wdtype == 0;
+  const float inv_n = 1.0f / static_cast<float>(a.N);
+  struct Row {
+    Raw<kBytes> x[R], res[R];
+  };
+  auto load = [&](Row& w, int64_t r) {
+    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
-      float g[E];
-      to_floats<T, E>(raw[i], f[i]);
-      to_floats<T, E>(rr[i], g);
-#pragma unroll
-      for (int e = 0; e < E; ++e) f[i][e] += g[e];
-      raw[i] = from_floats<T, E>(f[i]);  // h as it is stored
-      st_stream(h + static_cast<int64_t>(t + i * G) * E, raw[i]);
+      const int64_t j = static_cast<int64_t>(t + i * G) * E;
+      w.x[i] = ld_stream<kBytes>(x + j);
+      if (add) w.res[i] = ld_stream<kBytes>(static_cast<const T*>(a.residual) + r * a.ldr + j);
     }
-  }
-  float s[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (t + i * G >= n) continue;
-    to_floats<T, E>(raw[i], f[i]);
-#pragma unroll
-    for (int e = 0; e < E; ++e) s[0] += f[i][e];
-  }
+  };
   GroupSum<1> sum(smem, G);
-  sum(s);
-  const float inv_n = 1.0f / static_cast<float>(a.N), mu = s[0] * inv_n;
-  s[0] = 0.f;
+  Row next;
+  int64_t r = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / G;
+  if (kAhead && r < a.M) load(next, r);
+  for (; r < a.M; r += step) {
+    if (!kAhead) load(next, r);
+    Row w = next;
+    if (kAhead && r + step < a.M) load(next, r + step);
+    constexpr int P = kPairs<E>;
+    float2 f[R][P], s2 = pair(0.f);
+    float s[1];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (t + i * G >= n) continue;
+    for (int i = 0; i < R; ++i) {
+      if (t + i * G >= n) continue;
+      if (add) {
+        float2 g[P];
+        to_pairs<T, E>(w.x[i], f[i]);
+        to_pairs<T, E>(w.res[i], g);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      f[i][e] -= mu;
-      s[0] = fmaf(f[i][e], f[i][e], s[0]);
+        for (int e = 0; e < P; ++e) f[i][e] = __fadd2_rn(f[i][e], g[e]);
+        w.x[i] = from_pairs<T, E>(f[i]);  // h as it is stored
+        st_stream(static_cast<T*>(a.h) + r * a.N + static_cast<int64_t>(t + i * G) * E, w.x[i]);
+      }
+      to_pairs<T, E>(w.x[i], f[i]);
+#pragma unroll
+      for (int e = 0; e < P; ++e) s2 = __fadd2_rn(s2, f[i][e]);
     }
-  }
-  sum(s);
-  const float rstd = 1.0f / sqrtf(fmaf(s[0], inv_n, a.eps));
-  T* y = static_cast<T*>(a.y) + r * a.N;
-  const bool f32 = a.wdtype == 0;
+    s[0] = s2.x + s2.y;
+    sum(s);
+    const float mu = s[0] * inv_n;
+    s2 = pair(0.f);
+    const float2 nmu = pair(-mu);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (t + i * G >= n) continue;
-    const int64_t j = static_cast<int64_t>(t + i * G) * E;
-    float g[E], b[E];
+    for (int i = 0; i < R; ++i) {
+      if (t + i * G >= n) continue;
 #pragma unroll
-    for (int e = 0; e < E; ++e) g[e] = 1.0f, b[e] = 0.0f;
-    if (a.gamma != nullptr) load_weights<T, E>(a.gamma, j, f32, g);
-    if (a.beta != nullptr) load_weights<T, E>(a.beta, j, f32, b);
+      for (int e = 0; e < P; ++e) {
+        f[i][e] = __fadd2_rn(f[i][e], nmu);
+        s2 = __ffma2_rn(f[i][e], f[i][e], s2);
+      }
+    }
+    s[0] = E > 1 ? s2.x + s2.y : s2.x;
+    sum(s);
+    const float rstd = rsqrtf(fmaf(s[0], inv_n, a.eps));
+    const float2 scale = pair(rstd);
+    T* y = static_cast<T*>(a.y) + r * a.N;
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[i][e] = fmaf(f[i][e] * rstd, g[e], b[e]);
-    st_stream(y + j, from_floats<T, E>(f[i]));
-  }
-  if (t == 0) {
-    a.stats[2 * r] = mu;
-    a.stats[2 * r + 1] = rstd;
+    for (int i = 0; i < R; ++i) {
+      if (t + i * G >= n) continue;
+      const int64_t j = static_cast<int64_t>(t + i * G) * E;
+      float2 g[P], b[P];
+#pragma unroll
+      for (int e = 0; e < P; ++e) g[e] = pair(1.0f), b[e] = pair(0.0f);
+      if (a.gamma != nullptr) load_weights<T, E>(a.gamma, j, f32, g);
+      if (a.beta != nullptr) load_weights<T, E>(a.beta, j, f32, b);
+#pragma unroll
+      for (int e = 0; e < P; ++e) f[i][e] = __ffma2_rn(__fmul2_rn(f[i][e], scale), g[e], b[e]);
+      st_stream(y + j, from_pairs<T, E>(f[i]));
+    }
+    if (t == 0) {
+      a.stats[2 * r] = mu;
+      a.stats[2 * r + 1] = rstd;
+    }
   }
 }
 
@@ -240,7 +304,7 @@ __global__ void __launch_bounds__(kMaxGroup) ln_fwd_long_kernel(const LnFwdArgs 
       const float d = value(j) - mu;
       q = fmaf(d, d, q);
     }
-    const float rstd = 1.0f / sqrtf(fmaf(block_sum(q, buf), inv_n, a.eps));
+    const float rstd = rsqrtf(fmaf(block_sum(q, buf), inv_n, a.eps));
     for (int64_t j = threadIdx.x; j < a.N; j += blockDim.x) {
       const float v = value(j);
       const float g = a.gamma != nullptr ? load_any(a.gamma, j, a.wdtype) : 1.0f;
@@ -269,11 +333,15 @@ __global__ void __launch_bounds__(kMaxBwdGroup) ln_bwd_kernel(const LnBwdArgs a,
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const float inv_n = 1.0f / static_cast<float>(a.N);
   const bool add = a.dh != nullptr;
-  float gam[R][E], sg[R][E], sb[R][E];
+  constexpr int P = kPairs<E>;
+  float2 gam[R][P], sg[R][P], sb[R][P];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) gam[i][e] = 1.0f, sg[i][e] = sb[i][e] = 0.0f;
+    for (int e = 0; e < P; ++e) {
+      gam[i][e] = pair(1.0f);
+      sg[i][e] = sb[i][e] = pair(0.0f);
+    }
     if (a.gamma != nullptr && t + i * G < n)
       load_weights<T, E>(a.gamma, static_cast<int64_t>(t + i * G) * E, a.wdtype == 0, gam[i]);
   }
@@ -296,8 +364,8 @@ __global__ void __launch_bounds__(kMaxBwdGroup) ln_bwd_kernel(const LnBwdArgs a,
     }
   };
   GroupSum<2> sum(smem, G);
-  // two rows of 64 bytes a tensor and thread would not fit the registers
-  constexpr bool kAhead = R * kBytes <= 32;
+  // two rows of 16 registers a tensor would not fit
+  constexpr bool kAhead = R * kRegs<kBytes> <= 8;
   Row next;
   int64_t r = static_cast<int64_t>(blockIdx.x) * groups + group;
   if (kAhead && r < a.M) load(next, r);
@@ -305,44 +373,45 @@ __global__ void __launch_bounds__(kMaxBwdGroup) ln_bwd_kernel(const LnBwdArgs a,
     if (!kAhead) load(next, r);
     const Row w = next;
     if (kAhead && r + step < a.M) load(next, r + step);
-    const float mu = w.mu, rstd = w.rstd;
-    float s[2] = {0.f, 0.f};
+    const float2 nmu = pair(-w.mu), rstd = pair(w.rstd);
+    float2 s0 = pair(0.f), s1 = s0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
-      float x[E], dy[E];
-      to_floats<T, E>(w.x[i], x);
-      to_floats<T, E>(w.dy[i], dy);
+      float2 x[P], dy[P];
+      to_pairs<T, E>(w.x[i], x);
+      to_pairs<T, E>(w.dy[i], dy);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float xh = (x[e] - mu) * rstd, g = dy[e] * gam[i][e];
-        sg[i][e] = fmaf(dy[e], xh, sg[i][e]);
-        sb[i][e] += dy[e];
-        s[0] += g;
-        s[1] = fmaf(g, xh, s[1]);
+      for (int e = 0; e < P; ++e) {
+        const float2 xh = __fmul2_rn(__fadd2_rn(x[e], nmu), rstd), g = __fmul2_rn(dy[e], gam[i][e]);
+        sg[i][e] = __ffma2_rn(dy[e], xh, sg[i][e]);
+        sb[i][e] = __fadd2_rn(sb[i][e], dy[e]);
+        s0 = __fadd2_rn(s0, g);
+        s1 = __ffma2_rn(g, xh, s1);
       }
     }
+    float s[2] = {s0.x + s0.y, s1.x + s1.y};  // the idle half of a single element has dy = 0
     sum(s);
     // dx = rstd (g - mean(g) - x_hat mean(g x_hat))
-    const float c0 = -s[0] * inv_n * rstd, c1 = -s[1] * inv_n * rstd;
+    const float2 c0 = pair(-s[0] * inv_n * w.rstd), c1 = pair(-s[1] * inv_n * w.rstd);
     T* dx = static_cast<T*>(a.dx) + r * a.N;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
-      float x[E], dy[E];
-      to_floats<T, E>(w.x[i], x);
-      to_floats<T, E>(w.dy[i], dy);
+      float2 x[P], dy[P];
+      to_pairs<T, E>(w.x[i], x);
+      to_pairs<T, E>(w.dy[i], dy);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float xh = (x[e] - mu) * rstd;
-        x[e] = fmaf(dy[e] * gam[i][e], rstd, fmaf(xh, c1, c0));
+      for (int e = 0; e < P; ++e) {
+        const float2 xh = __fmul2_rn(__fadd2_rn(x[e], nmu), rstd);
+        x[e] = __ffma2_rn(__fmul2_rn(dy[e], gam[i][e]), rstd, __ffma2_rn(xh, c1, c0));
       }
       if (add) {
-        to_floats<T, E>(w.dh[i], dy);
+        to_pairs<T, E>(w.dh[i], dy);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] += dy[e];
+        for (int e = 0; e < P; ++e) x[e] = __fadd2_rn(x[e], dy[e]);
       }
-      st_stream(dx + static_cast<int64_t>(t + i * G) * E, from_floats<T, E>(x));
+      st_stream(dx + static_cast<int64_t>(t + i * G) * E, from_pairs<T, E>(x));
     }
   }
   if (a.part == nullptr) return;
@@ -356,8 +425,10 @@ __global__ void __launch_bounds__(kMaxBwdGroup) ln_bwd_kernel(const LnBwdArgs a,
         const int64_t j = static_cast<int64_t>(t + i * G) * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          to[j + e] = k == 0 ? sg[i][e] : to[j + e] + sg[i][e];
-          to[a.N + j + e] = k == 0 ? sb[i][e] : to[a.N + j + e] + sb[i][e];
+          const float vg = e % 2 == 0 ? sg[i][e / 2].x : sg[i][e / 2].y;
+          const float vb = e % 2 == 0 ? sb[i][e / 2].x : sb[i][e / 2].y;
+          to[j + e] = k == 0 ? vg : to[j + e] + vg;
+          to[a.N + j + e] = k == 0 ? vb : to[a.N + j + e] + vb;
         }
       }
     }
@@ -471,20 +542,49 @@ int group_threads(int64_t n, int R) {
   return g;
 }
 
-template <typename T, int E, int R>
+// blocks of a persistent kernel that fit on the device at once (asked once for each device and block size)
+struct FitCache {
+  int device = -1, threads = 0, fit = 0;
+  size_t bytes = 0;
+};
+template <typename Kernel>
+cudaError_t blocks_that_fit(Kernel kernel, FitCache& cache, int block, size_t smem, int64_t& blocks) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (cache.device != dev || cache.threads != block || cache.bytes != smem) {
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, block, smem);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorLaunchOutOfResources;
+    cache = FitCache{dev, block, per_sm * device_sm_count(), smem};
+  }
+  blocks = cache.fit;
+  return cudaSuccess;
+}
+template <typename T, int E, int R, int kMost>
 cudaError_t fwd_one(const LnFwdArgs& a, int G, cudaStream_t stream) {
-  const int block = G > kBlock ? G : kBlock;
-  const int64_t per = block / G, blocks = (a.M + per - 1) / per;
-  ln_fwd_kernel<T, E, R><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a, G);
+  const int block = G > kBlock ? G : kBlock, groups = block / G;
+  int64_t blocks;
+  {
+    static std::mutex mu;
+    static FitCache cache;
+    std::lock_guard<std::mutex> lk(mu);
+    const cudaError_t e = blocks_that_fit(ln_fwd_kernel<T, E, R, kMost>, cache, block, 0, blocks);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t most = (a.M + groups - 1) / groups;
+  if (blocks > most) blocks = most;
+  ln_fwd_kernel<T, E, R, kMost><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a, G);
   return cudaGetLastError();
 }
 // vectors a thread: as few as let a block of 512 hold the row, two for wide vectors from a warp on
 template <typename T, int E, int R0>
 cudaError_t fwd_any(const LnFwdArgs& a, cudaStream_t stream) {
   const int64_t n = a.N / E;
-  if (n <= 32 * R0) return fwd_one<T, E, R0>(a, 32, stream);
-  if (n <= 512 * 2 * R0) return fwd_one<T, E, 2 * R0>(a, group_threads(n, 2 * R0), stream);
-  if (n <= kMaxGroup * 4 * R0) return fwd_one<T, E, 4 * R0>(a, group_threads(n, 4 * R0), stream);
+  if (n <= 32 * R0) return fwd_one<T, E, R0, 512>(a, 32, stream);
+  if (n <= 512 * 2 * R0) return fwd_one<T, E, 2 * R0, 512>(a, group_threads(n, 2 * R0), stream);
+  if (n <= kMaxGroup * 4 * R0) return fwd_one<T, E, 4 * R0, kMaxGroup>(a, group_threads(n, 4 * R0), stream);
   const unsigned grid = static_cast<unsigned>(a.M < 65536 ? a.M : 65536);
   ln_fwd_long_kernel<T><<<grid, kMaxGroup, 0, stream>>>(a);
   return cudaGetLastError();
@@ -517,8 +617,6 @@ cudaError_t launch_reduce(const LnBwdArgs& a, int64_t rows, cudaStream_t stream)
 constexpr int64_t kMaxBlocks = 4 * 256;  // rows of column sums in the workspace, at most
 constexpr int64_t kLongChunks = 64;      // of them for rows too long for registers
 
-// the persistent kernel's blocks: as many as fit (asked once for each device and block size), at most one
-// group a row
 template <typename T, int E, int R>
 cudaError_t bwd_one(const LnBwdArgs& a, int G, cudaStream_t stream) {
   const int block = G > kBlock ? G : kBlock, groups = block / G;
@@ -526,21 +624,10 @@ cudaError_t bwd_one(const LnBwdArgs& a, int G, cudaStream_t stream) {
   int64_t blocks;
   {
     static std::mutex mu;
-    static int device = -1, threads = 0, fit = 0;
-    static size_t bytes = 0;
+    static FitCache cache;
     std::lock_guard<std::mutex> lk(mu);
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = blocks_that_fit(ln_bwd_kernel<T, E, R>, cache, block, smem, blocks);
     if (e != cudaSuccess) return e;
-    if (device != dev || threads != block || bytes != smem) {
-      int per_sm = 0;
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, ln_bwd_kernel<T, E, R>, block, smem);
-      if (e != cudaSuccess) return e;
-      if (per_sm < 1) return cudaErrorLaunchOutOfResources;
-      device = dev, threads = block, bytes = smem;
-      fit = per_sm * device_sm_count();
-    }
-    blocks = fit;
   }
   const int64_t most = (a.M + groups - 1) / groups;
   if (blocks > most) blocks = most;
