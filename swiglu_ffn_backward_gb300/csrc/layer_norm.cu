@@ -8,13 +8,20 @@
 // All arithmetic is fp32; h, y and dx are rounded once.
 //
 // Bound by HBM: two to four tensors of M N elements are read or written, with some ten operations an
-// element. A group of 32 to 1024 threads holds a row in registers, so each element is read once: the
-// variance is taken of centred values in a second pass over the registers. Vectors are the widest that
-// the row length, strides and addresses allow (16 bytes, 4 bytes or one element). Rows too long for the
-// registers of a block are read again (ln_fwd_long_kernel, ln_dx_long_kernel).
-// The groups are persistent and load the next row under the work on this one.
-// Backward: each thread has the same columns of every row, so the columns' sums of dgamma and dbeta stay
-// in registers. The blocks' sums go to the workspace and are added by a second kernel in a fixed order.
+// element. A group of 8 to 1024 threads holds a row in registers, 16-byte vectors of fixed columns, so each
+// element is read once: the variance is taken of centred values in a second pass over the registers. The
+// groups are persistent and, with two vectors or fewer a thread, load a row ahead. Rows too long for a
+// block's registers are read again (ln_fwd_long_kernel, ln_dx_long_kernel).
+// Ragged rows, that begin or end inside 16 bytes: a thread's columns are those of a 16-byte vector of the
+// output, so that its stores are aligned. A group takes rows that lie a multiple of 16 bytes apart: it keeps
+// its columns, and the weights and the column sums that belong to them, in registers. An input with the same
+// offset is loaded as aligned vectors too, the row's first and last one with elements of the neighbours,
+// that are cleared; with another offset it is put together from two. Element by element (groups of one
+// column a lane) took 78 us for 4000 x 4001 bf16 forward and 164 us backward, this takes 31 and 58.
+// Backward: the columns' sums of dgamma and dbeta stay in registers over all of a group's rows. The blocks'
+// sums go to the workspace and are added by a second kernel in a fixed order.
+// Measured, bf16: 16384 x 4096 with residual 87 us, 93% of the copy bandwidth; 220000 x 512 backward with dh
+// 151 us, 89%; 16384 x 8192 backward with dh 186 us, 86%.
 #include <mutex>
 
 #include "row_ops.cuh"
@@ -25,153 +32,199 @@ namespace {
 
 using namespace row;
 
-// E elements in one load
-template <int kBytes>
-struct Raw;
-template <>
-struct Raw<16> {
-  uint4 u;
+struct Raw {  // 16 bytes
+  uint32_t w[4];
 };
-template <>
-struct Raw<8> {
-  uint2 u;
-};
-template <>
-struct Raw<4> {
-  uint32_t u;
-};
-template <>
-struct Raw<2> {
-  uint16_t u;
-};
-template <int kBytes>
-constexpr int kRegs = (kBytes + 3) / 4;  // registers of one
-template <int kBytes>
-__device__ __forceinline__ Raw<kBytes> ld_stream(const void* p);
-template <>
-__device__ __forceinline__ Raw<16> ld_stream<16>(const void* p) {
-  Raw<16> r;
+template <typename T>
+constexpr int kElems = 16 / static_cast<int>(sizeof(T));
+
+__device__ __forceinline__ Raw ld_stream(const void* p) {
+  Raw r;
   asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-      : "=r"(r.u.x), "=r"(r.u.y), "=r"(r.u.z), "=r"(r.u.w)
+      : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
       : "l"(p));
   return r;
 }
-template <>
-__device__ __forceinline__ Raw<4> ld_stream<4>(const void* p) {
-  return Raw<4>{__ldg(static_cast<const uint32_t*>(p))};
+__device__ __forceinline__ Raw ld_cached(const void* p) {
+  const uint4 u = __ldg(static_cast<const uint4*>(p));
+  return Raw{{u.x, u.y, u.z, u.w}};
 }
-template <>
-__device__ __forceinline__ Raw<2> ld_stream<2>(const void* p) {
-  return Raw<2>{__ldg(static_cast<const uint16_t*>(p))};
+__device__ __forceinline__ void st_raw(void* p, const Raw& r) {
+  *static_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
 }
-// 16-bit elements are widened and narrowed two at a time, word by word
+
+// 16-bit elements are widened and narrowed two at a time, and the arithmetic is on pairs with the packed
+// fp32x2 operations (half the instructions)
 __device__ __forceinline__ float2 widen(uint32_t u, __half) {
-  const __half2 h = *reinterpret_cast<const __half2*>(&u);
-  return __half22float2(h);
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 __device__ __forceinline__ float2 widen(uint32_t u, __nv_bfloat16) { return bf16x2_to_f2(u); }
-__device__ __forceinline__ uint32_t narrow(float a, float b, __half) {
-  const __half2 h = __floats2half2_rn(a, b);
+__device__ __forceinline__ uint32_t narrow(float2 v, __half) {
+  const __half2 h = __floats2half2_rn(v.x, v.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t narrow(float a, float b, __nv_bfloat16) { return pack_bf16x2(a, b); }
-template <typename T, int E>
-__device__ __forceinline__ void to_floats(const Raw<E * sizeof(T)>& r, float (&f)[E]) {
-  if constexpr (sizeof(T) == 2 && E >= 2) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const float2 v = widen(w[i], T());
-      f[2 * i] = v.x;
-      f[2 * i + 1] = v.y;
-    }
+__device__ __forceinline__ uint32_t narrow(float2 v, __nv_bfloat16) { return pack_bf16x2(v.x, v.y); }
+template <typename T>
+constexpr int kPairs = kElems<T> / 2;
+template <typename T>
+__device__ __forceinline__ float2 get_pair(const Raw& r, int i) {
+  if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+  else return widen(r.w[i], T());
+}
+template <typename T>
+__device__ __forceinline__ void set_pair(Raw& r, int i, float2 v) {
+  if constexpr (sizeof(T) == 4) {
+    r.w[2 * i] = __float_as_uint(v.x);
+    r.w[2 * i + 1] = __float_as_uint(v.y);
   } else {
-    const T* t = reinterpret_cast<const T*>(&r);
-#pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = to_f(t[e]);
+    r.w[i] = narrow(v, T());
   }
-}
-template <typename T, int E>
-__device__ __forceinline__ Raw<E * sizeof(T)> from_floats(const float (&f)[E]) {
-  Raw<E * sizeof(T)> r;
-  if constexpr (sizeof(T) == 2 && E >= 2) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) w[i] = narrow(f[2 * i], f[2 * i + 1], T());
-  } else {
-    T* t = reinterpret_cast<T*>(&r);
-#pragma unroll
-    for (int e = 0; e < E; ++e) t[e] = from_f<T>(f[e]);
-  }
-  return r;
-}
-// The arithmetic is on pairs with the packed fp32x2 operations (half the instructions; a single element is
-// a pair with an idle half): E elements are (E + 1) / 2 pairs.
-template <int E>
-constexpr int kPairs = (E + 1) / 2;
-template <typename T, int E>
-__device__ __forceinline__ void to_pairs(const Raw<E * sizeof(T)>& r, float2 (&p)[kPairs<E>]) {
-  float f[E];
-  to_floats<T, E>(r, f);
-#pragma unroll
-  for (int i = 0; i < kPairs<E>; ++i) p[i] = make_float2(f[2 * i], E > 1 ? f[(2 * i + 1) % E] : 0.0f);
-}
-template <typename T, int E>
-__device__ __forceinline__ Raw<E * sizeof(T)> from_pairs(const float2 (&p)[kPairs<E>]) {
-  float f[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) f[e] = e % 2 == 0 ? p[e / 2].x : p[e / 2].y;
-  return from_floats<T, E>(f);
 }
 __device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
 
-template <int kBytes>
-__device__ __forceinline__ void st_stream(void* p, const Raw<kBytes>& r) {
-  *static_cast<Raw<kBytes>*>(p) = r;
+// The 16 bytes that begin `shift` elements into the 32 bytes a, b.
+template <typename T>
+__device__ __forceinline__ Raw join(const Raw& a, const Raw& b, int shift) {
+  const int words = shift * static_cast<int>(sizeof(T)) / 4;
+  uint32_t w[7] = {a.w[0], a.w[1], a.w[2], a.w[3], b.w[0], b.w[1], b.w[2]};
+  const uint32_t last = b.w[3];
+  uint32_t v[6];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) v[i] = words & 2 ? w[i + 2] : w[i];
+  v[5] = words & 2 ? last : w[5];
+  uint32_t u[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) u[i] = words & 1 ? v[i + 1] : v[i];
+  Raw r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r.w[i] = sizeof(T) == 2 && (shift & 1) ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
+  return r;
 }
-// E weights of either type (cached: every row uses them)
-template <typename T, int E>
-__device__ __forceinline__ void load_weights(const void* p, int64_t j, bool f32, float2 (&f)[kPairs<E>]) {
-  if (sizeof(T) == 4 || f32) {
-    const float* w = static_cast<const float*>(p) + j;
-    if constexpr (E % 4 == 0) {
+template <typename T>
+__device__ __forceinline__ int shift_of(const T* p) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+}
+// The rows of a tensor.
+template <typename T>
+struct Rows {
+  const T *first, *end;
+  int64_t ld;
+  __device__ __forceinline__ Rows(const void* p, int64_t ld_, int64_t M, int64_t N)
+      : first(static_cast<const T*>(p)), end(first + (M - 1) * ld_ + N), ld(ld_) {}
+};
+// The columns from j on of row r of N, of which the row may have some only (kRagged: j below 0 or j + E above
+// N); anything for the others. Nothing here waits for a load that is one aligned vector.
+template <typename T, bool kRagged>
+__device__ __forceinline__ Raw load_columns(const Rows<T>& rows, int64_t r, int j, int N) {
+  const T *row = rows.first + r * rows.ld, *p = row + j;
+  if (!kRagged) return ld_stream(p);
+  constexpr int E = kElems<T>;
+  const int shift = shift_of(p);
+  if (shift == 0) {
+    if (j >= 0 && j + E <= N) return ld_stream(p);
+    if (p >= rows.first && p + E <= rows.end) return ld_stream(p);
+  } else if (j >= shift && j - shift + 2 * E <= N) {
+    return join<T>(ld_cached(p - shift), ld_cached(p - shift + E), shift);
+  }
+  Raw v;
 #pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(w + e));
-        f[e / 2] = make_float2(v.x, v.y);
-        f[e / 2 + 1] = make_float2(v.z, v.w);
-      }
+  for (int i = 0; i < kPairs<T>; ++i) {
+    const int k = j + 2 * i;
+    const float lo = k >= 0 && k < N ? to_f(row[k]) : 0.0f, hi = k >= -1 && k + 1 < N ? to_f(row[k + 1]) : 0.0f;
+    set_pair<T>(v, i, make_float2(lo, hi));
+  }
+  return v;
+}
+// zeros for the columns that the row does not have
+template <typename T>
+__device__ __forceinline__ void clear_others(Raw& v, int j, int N) {
+  if (j >= 0 && j + kElems<T> <= N) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      if (j + i < 0 || j + i >= N) v.w[i] = 0;
     } else {
-#pragma unroll
-      for (int i = 0; i < kPairs<E>; ++i) f[i] = make_float2(__ldg(w + 2 * i), E > 1 ? __ldg(w + 2 * i + 1) : 0.0f);
-    }
-  } else {
-    const T* w = static_cast<const T*>(p) + j;
-    if constexpr (E * sizeof(T) == 16) {
-      const Raw<16> r{__ldg(reinterpret_cast<const uint4*>(w))};
-      to_pairs<T, E>(r, f);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPairs<E>; ++i) f[i] = make_float2(to_f(w[2 * i]), E > 1 ? to_f(w[2 * i + 1]) : 0.0f);
+      const int k = j + 2 * i;
+      v.w[i] &= (k >= 0 && k < N ? 0xffffu : 0u) | (k >= -1 && k + 1 < N ? 0xffff0000u : 0u);
     }
   }
 }
+template <typename T, bool kRagged>
+__device__ __forceinline__ void store_columns(T* row, int j, int N, const Raw& r) {
+  T* p = row + j;
+  constexpr int E = kElems<T>;
+  if (!kRagged || (shift_of(p) == 0 && j >= 0 && j + E <= N)) {
+    st_raw(p, r);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kPairs<T>; ++i) {
+    const float2 v = get_pair<T>(r, i);
+    const int k = j + 2 * i;
+    if (k >= 0 && k < N) row[k] = from_f<T>(v.x);
+    if (k >= -1 && k + 1 < N) row[k + 1] = from_f<T>(v.y);
+  }
+}
+// weights of either type (cached: every row uses them), 1 or 0 where there are none
+template <typename T, typename W, bool kRagged>
+__device__ __forceinline__ void weights_of(const W* w, int j, int N, float2 (&f)[kPairs<T>]) {
+  constexpr int E = kElems<T>, V = 16 / static_cast<int>(sizeof(W)), L = E / V;
+  const W* p = w + j;
+  const int shift = kRagged ? shift_of(p) : 0;
+  if (kRagged && (j < shift || j - shift + E + (shift > 0 ? V : 0) > N)) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float v = j + e >= 0 && j + e < N ? to_f(p[e]) : 0.0f;
+      if (e % 2 == 0) f[e / 2].x = v;
+      else f[e / 2].y = v;
+    }
+    return;
+  }
+  Raw r[L + 1];
+#pragma unroll
+  for (int i = 0; i < L; ++i) r[i] = ld_cached(p - shift + i * V);
+  if (kRagged && shift > 0) {
+    r[L] = ld_cached(p - shift + E);
+#pragma unroll
+    for (int i = 0; i < L; ++i) r[i] = join<W>(r[i], r[i + 1], shift);
+  }
+#pragma unroll
+  for (int i = 0; i < kPairs<T>; ++i) f[i] = get_pair<W>(r[2 * i / V], i % (V / 2));
+}
+template <typename T, bool kRagged>
+__device__ __forceinline__ void load_weights(const void* w, int j, int N, bool f32, float none,
+                                             float2 (&f)[kPairs<T>]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < kPairs<T>; ++i) f[i] = pair(none);
+  } else if (sizeof(T) == 4 || f32) {
+    weights_of<T, float, kRagged>(static_cast<const float*>(w), j, N, f);
+  } else {
+    weights_of<T, T, kRagged>(static_cast<const T*>(w), j, N, f);
+  }
+}
 
-// Sums over a group of G threads (a power of two from 32 on) in a block; every thread gets them, added in a
-// fixed order. Groups above a warp use two alternating buffers, so that one barrier a sum is enough.
-template <int kSums>
+// Sums over a group of G threads of a block (a power of two up to 256, or all); every thread gets them, added
+// in a fixed order. Groups above a warp use two alternating buffers, so that one barrier a sum is enough.
+template <int kSums, bool kNarrow>  // kNarrow: G below 32 as well
 struct GroupSum {
   float* buf;  // of the group: 2 x kSums x warps
-  int warps, warp, id, turn = 0;
+  int warps, warp, id, width, turn = 0;
   __device__ __forceinline__ GroupSum(float* smem, int G) {
-    warps = G >> 5;
-    warp = (threadIdx.x >> 5) & (warps - 1);
+    warps = G > 32 ? G >> 5 : 1;
+    width = G < 32 ? G : 32;
+    warp = (threadIdx.x >> 5) % warps;
     id = 1 + static_cast<int>(threadIdx.x) / G;  // barrier of the group; groups above a warp: at most 8
     buf = smem + (threadIdx.x / G) * (2 * kSums * warps);
   }
   __device__ __forceinline__ void operator()(float (&v)[kSums]) {
 #pragma unroll
-    for (int i = 0; i < kSums; ++i) v[i] = warp_sum(v[i]);
+    for (int i = 0; i < kSums; ++i) {
+      if (!kNarrow || width == 32) v[i] = warp_sum(v[i]);
+      else
+        for (int o = width >> 1; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
     if (warps == 1) return;
     float* b = buf + turn * kSums * warps;
     turn ^= 1;
@@ -187,78 +240,112 @@ struct GroupSum {
     }
   }
 };
-constexpr int kBlock = 256;       // threads of a block, unless a row takes more
-constexpr int kMaxGroup = 1024;
-constexpr int kMaxBwdGroup = 512;  // the column sums take registers
+constexpr int kBlock = 256;         // threads of a block, unless a row takes more
+constexpr int kMinGroup = 8;        // threads a row
+constexpr int kMaxGroup = 512;
+constexpr int kMaxThreads = 1024;
 
 // ---- forward
-template <typename T, int E, int R, int kMost>  // kMost: the block's threads, at most
-__global__ void __launch_bounds__(kMost) ln_fwd_kernel(const LnFwdArgs a, int G) {
+// kMost: threads of a block, at most. 80 registers a thread keep three blocks of 256 threads on an SM (96:
+// 97 us instead of 87 for 16384 x 4096 bf16 with residual; 64: 91 us).
+template <int R, bool kRagged, int kMost>
+constexpr int kFwdRegs = kMost > kMaxGroup ? 64 : kRagged || R > 2 ? 128 : 80;
+template <typename T, int R, bool kRagged, int kMost>
+__global__ void __maxnreg__((kFwdRegs<R, kRagged, kMost>)) ln_fwd_kernel(const LnFwdArgs a, int G) {
   __shared__ float smem[2 * 32];
-  constexpr int kBytes = E * sizeof(T);
-  // the next row is loaded under the work on this one where the registers have room for it
-  constexpr bool kAhead = R * kRegs<kBytes> <= 8;
-  const int groups = blockDim.x / G;
-  const int t = threadIdx.x & (G - 1);
+  constexpr int E = kElems<T>, P = kPairs<T>;
+  constexpr bool kNarrow = R == 1;  // groups of less than a warp
+  const int groups = blockDim.x / G, t = threadIdx.x % G;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  const int n = static_cast<int>(a.N / E);
+  const int N = static_cast<int>(a.N);
+  int64_t r = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / G;
+  const int shift = kRagged ? shift_of(static_cast<const T*>(a.y) + r * a.N) : 0;
+  int n = (N + shift + E - 1) / E;  // vectors of the row
   const bool add = a.residual != nullptr, f32 = a.wdtype == 0;
   const float inv_n = 1.0f / static_cast<float>(a.N);
+  auto column = [&](int i) { return (t + i * G) * E - shift; };
   struct Row {
-    Raw<kBytes> x[R], res[R];
+    Raw x[R], res[R];
   };
+  const Rows<T> x(a.x, a.ldx, a.M, a.N), res(a.residual, a.ldr, a.M, a.N);
   auto load = [&](Row& w, int64_t r) {
-    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
-      const int64_t j = static_cast<int64_t>(t + i * G) * E;
-      w.x[i] = ld_stream<kBytes>(x + j);
-      if (add) w.res[i] = ld_stream<kBytes>(static_cast<const T*>(a.residual) + r * a.ldr + j);
+      w.x[i] = load_columns<T, kRagged>(x, r, column(i), N);
+      if (add) w.res[i] = load_columns<T, kRagged>(res, r, column(i), N);
     }
   };
-  GroupSum<1> sum(smem, G);
+  // the weights of ragged columns take several loads and a join: they are held, where the registers do
+  constexpr bool kHeld = kRagged && R * E <= 16 && kMost <= kMaxGroup, kAhead = R <= 2;
+  float2 gam[kHeld ? R : 1][P], bet[kHeld ? R : 1][P];
+  auto weights = [&](int i, int to) {
+    load_weights<T, kRagged>(a.gamma, column(i), N, f32, 1.0f, gam[to]);
+    load_weights<T, kRagged>(a.beta, column(i), N, f32, 0.0f, bet[to]);
+  };
+  if constexpr (kHeld) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (t + i * G < n) weights(i, i);
+  }
+  GroupSum<1, kNarrow> sum(smem, G);
   Row next;
-  int64_t r = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / G;
+  const int64_t M = a.M + (kNarrow ? (threadIdx.x & 31) / G : 0);  // the rows of a warp's groups end together
   if (kAhead && r < a.M) load(next, r);
-  for (; r < a.M; r += step) {
+  for (; r < M; r += step) {
+    if (kNarrow && r >= a.M) n = 0;
     if (!kAhead) load(next, r);
     Row w = next;
     if (kAhead && r + step < a.M) load(next, r + step);
-    constexpr int P = kPairs<E>;
-    float2 f[R][P], s2 = pair(0.f);
-    float s[1];
+    if constexpr (kRagged) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        clear_others<T>(w.x[i], column(i), N);
+        if (add) clear_others<T>(w.res[i], column(i), N);
+      }
+    }
+    float2 s2 = pair(0.f), f[kAhead ? R : 1][P];  // the row in fp32, where the registers hold that
+    auto value = [&](int i, int e) { return kAhead ? f[kAhead ? i : 0][e] : get_pair<T>(w.x[i], e); };
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
       if (add) {
-        float2 g[P];
-        to_pairs<T, E>(w.x[i], f[i]);
-        to_pairs<T, E>(w.res[i], g);
 #pragma unroll
-        for (int e = 0; e < P; ++e) f[i][e] = __fadd2_rn(f[i][e], g[e]);
-        w.x[i] = from_pairs<T, E>(f[i]);  // h as it is stored
-        st_stream(static_cast<T*>(a.h) + r * a.N + static_cast<int64_t>(t + i * G) * E, w.x[i]);
+        for (int e = 0; e < P; ++e)  // h as it is stored
+          set_pair<T>(w.x[i], e, __fadd2_rn(get_pair<T>(w.x[i], e), get_pair<T>(w.res[i], e)));
+        store_columns<T, kRagged>(static_cast<T*>(a.h) + r * a.N, column(i), N, w.x[i]);
       }
-      to_pairs<T, E>(w.x[i], f[i]);
 #pragma unroll
-      for (int e = 0; e < P; ++e) s2 = __fadd2_rn(s2, f[i][e]);
+      for (int e = 0; e < P; ++e) {
+        const float2 v = get_pair<T>(w.x[i], e);
+        if (kAhead) f[kAhead ? i : 0][e] = v;
+        s2 = __fadd2_rn(s2, v);
+      }
     }
-    s[0] = s2.x + s2.y;
+    float s[1] = {s2.x + s2.y};
     sum(s);
     const float mu = s[0] * inv_n;
-    s2 = pair(0.f);
     const float2 nmu = pair(-mu);
+    s2 = pair(0.f);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
+      if (kRagged && (column(i) < 0 || column(i) + E > N)) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const int j = column(i) + 2 * e;
+          const float2 d = __fadd2_rn(value(i, e), nmu);
+          s2 = __ffma2_rn(d, make_float2(j >= 0 && j < N ? d.x : 0.0f, j >= -1 && j + 1 < N ? d.y : 0.0f), s2);
+        }
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        f[i][e] = __fadd2_rn(f[i][e], nmu);
-        s2 = __ffma2_rn(f[i][e], f[i][e], s2);
+        const float2 d = __fadd2_rn(value(i, e), nmu);
+        s2 = __ffma2_rn(d, d, s2);
       }
     }
-    s[0] = E > 1 ? s2.x + s2.y : s2.x;
+    s[0] = s2.x + s2.y;
     sum(s);
     const float rstd = rsqrtf(fmaf(s[0], inv_n, a.eps));
     const float2 scale = pair(rstd);
@@ -266,17 +353,15 @@ __global__ void __launch_bounds__(kMost) ln_fwd_kernel(const LnFwdArgs a, int G)
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
-      const int64_t j = static_cast<int64_t>(t + i * G) * E;
-      float2 g[P], b[P];
+      constexpr int k = kHeld ? 1 : 0;
+      if (!kHeld) weights(i, 0);
 #pragma unroll
-      for (int e = 0; e < P; ++e) g[e] = pair(1.0f), b[e] = pair(0.0f);
-      if (a.gamma != nullptr) load_weights<T, E>(a.gamma, j, f32, g);
-      if (a.beta != nullptr) load_weights<T, E>(a.beta, j, f32, b);
-#pragma unroll
-      for (int e = 0; e < P; ++e) f[i][e] = __ffma2_rn(__fmul2_rn(f[i][e], scale), g[e], b[e]);
-      st_stream(y + j, from_pairs<T, E>(f[i]));
+      for (int e = 0; e < P; ++e)
+        set_pair<T>(w.x[i], e,
+                    __ffma2_rn(__fmul2_rn(__fadd2_rn(value(i, e), nmu), scale), gam[k * i][e], bet[k * i][e]));
+      store_columns<T, kRagged>(y, column(i), N, w.x[i]);
     }
-    if (t == 0) {
+    if (t == 0 && (!kNarrow || n > 0)) {
       a.stats[2 * r] = mu;
       a.stats[2 * r + 1] = rstd;
     }
@@ -285,7 +370,7 @@ __global__ void __launch_bounds__(kMost) ln_fwd_kernel(const LnFwdArgs a, int G)
 
 // rows of any length, element by element, read three times (from L2 where a row fits)
 template <typename T>
-__global__ void __launch_bounds__(kMaxGroup) ln_fwd_long_kernel(const LnFwdArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) ln_fwd_long_kernel(const LnFwdArgs a) {
   __shared__ float buf[32];
   const float inv_n = 1.0f / static_cast<float>(a.N);
   for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
@@ -321,76 +406,87 @@ __global__ void __launch_bounds__(kMaxGroup) ln_fwd_long_kernel(const LnFwdArgs 
 
 // ---- backward
 // dx, and with a.part the block's column sums: part[block][0][j] of dy x_hat, part[block][1][j] of dy
-template <typename T, int E, int R>
-__global__ void __launch_bounds__(kMaxBwdGroup) ln_bwd_kernel(const LnBwdArgs a, int G) {
+template <typename T, int R, bool kRagged>
+__global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, int G) {
   extern __shared__ float dyn[];  // with several groups a block: 2 N column sums
   __shared__ float smem[2 * 2 * 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int kBytes = E * sizeof(T);
+  constexpr int E = kElems<T>, P = kPairs<T>;
+  constexpr bool kNarrow = R == 1;  // groups of less than a warp
+  // the registers take up to 16 columns' weights and, of up to 32 bytes a tensor, the next row
+  constexpr bool kWeights = R * E <= 16, kAhead = R <= 2;
   const int groups = blockDim.x / G, group = threadIdx.x / G;
-  const int t = threadIdx.x & (G - 1);
-  const int n = static_cast<int>(a.N / E);
+  const int t = threadIdx.x % G;
+  const int N = static_cast<int>(a.N);
+  int64_t r = static_cast<int64_t>(blockIdx.x) * groups + group;
+  const int shift = kRagged ? shift_of(static_cast<const T*>(a.dx) + r * a.N) : 0;
+  const int vectors = (N + shift + E - 1) / E;
+  int n = vectors;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const float inv_n = 1.0f / static_cast<float>(a.N);
-  const bool add = a.dh != nullptr;
-  constexpr int P = kPairs<E>;
-  float2 gam[R][P], sg[R][P], sb[R][P];
+  const bool add = a.dh != nullptr, f32 = a.wdtype == 0;
+  auto column = [&](int i) { return (t + i * G) * E - shift; };
+  float2 gam[kWeights ? R : 1][P], sg[R][P], sb[R][P];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
 #pragma unroll
-    for (int e = 0; e < P; ++e) {
-      gam[i][e] = pair(1.0f);
-      sg[i][e] = sb[i][e] = pair(0.0f);
-    }
-    if (a.gamma != nullptr && t + i * G < n)
-      load_weights<T, E>(a.gamma, static_cast<int64_t>(t + i * G) * E, a.wdtype == 0, gam[i]);
+    for (int e = 0; e < P; ++e) sg[i][e] = sb[i][e] = pair(0.0f);
+    if (kWeights && t + i * G < n)
+      load_weights<T, kRagged>(a.gamma, column(i), N, f32, 1.0f, gam[kWeights ? i : 0]);
   }
+  auto weights = [&](int i) -> float2 (&)[P] {
+    if (!kWeights) load_weights<T, kRagged>(a.gamma, column(i), N, f32, 1.0f, gam[0]);
+    return gam[kWeights ? i : 0];
+  };
   struct Row {
-    Raw<kBytes> x[R], dy[R], dh[R];
+    Raw x[R], dy[R], dh[R];
     float mu, rstd;
   };
+  const Rows<T> x(a.x, a.ldx, a.M, a.N), dy(a.dy, a.lddy, a.M, a.N), dh(a.dh, a.lddh, a.M, a.N);
   auto load = [&](Row& w, int64_t r) {
-    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
-    const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
     w.mu = a.stats[2 * r];
     w.rstd = a.stats[2 * r + 1];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
-      const int64_t j = static_cast<int64_t>(t + i * G) * E;
-      w.x[i] = ld_stream<kBytes>(x + j);
-      w.dy[i] = ld_stream<kBytes>(dy + j);
-      if (add) w.dh[i] = ld_stream<kBytes>(static_cast<const T*>(a.dh) + r * a.lddh + j);
+      w.x[i] = load_columns<T, kRagged>(x, r, column(i), N);
+      w.dy[i] = load_columns<T, kRagged>(dy, r, column(i), N);
+      if (add) w.dh[i] = load_columns<T, kRagged>(dh, r, column(i), N);
     }
   };
-  GroupSum<2> sum(smem, G);
-  // two rows of 16 registers a tensor would not fit
-  constexpr bool kAhead = R * kRegs<kBytes> <= 8;
+  GroupSum<2, kNarrow> sum(smem, G);
   Row next;
-  int64_t r = static_cast<int64_t>(blockIdx.x) * groups + group;
+  const int64_t M = a.M + (kNarrow ? (threadIdx.x & 31) / G : 0);  // the rows of a warp's groups end together
   if (kAhead && r < a.M) load(next, r);
-  for (; r < a.M; r += step) {
+  for (; r < M; r += step) {
+    if (kNarrow && r >= a.M) n = 0;
     if (!kAhead) load(next, r);
-    const Row w = next;
+    Row w = next;
     if (kAhead && r + step < a.M) load(next, r + step);
+    if constexpr (kRagged) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        clear_others<T>(w.x[i], column(i), N);
+        clear_others<T>(w.dy[i], column(i), N);
+      }
+    }
     const float2 nmu = pair(-w.mu), rstd = pair(w.rstd);
     float2 s0 = pair(0.f), s1 = s0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
-      float2 x[P], dy[P];
-      to_pairs<T, E>(w.x[i], x);
-      to_pairs<T, E>(w.dy[i], dy);
+      const float2 (&gi)[P] = weights(i);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const float2 xh = __fmul2_rn(__fadd2_rn(x[e], nmu), rstd), g = __fmul2_rn(dy[e], gam[i][e]);
-        sg[i][e] = __ffma2_rn(dy[e], xh, sg[i][e]);
-        sb[i][e] = __fadd2_rn(sb[i][e], dy[e]);
+        const float2 xh = __fmul2_rn(__fadd2_rn(get_pair<T>(w.x[i], e), nmu), rstd), d = get_pair<T>(w.dy[i], e);
+        const float2 g = __fmul2_rn(d, gi[e]);
+        sg[i][e] = __ffma2_rn(d, xh, sg[i][e]);
+        sb[i][e] = __fadd2_rn(sb[i][e], d);
         s0 = __fadd2_rn(s0, g);
         s1 = __ffma2_rn(g, xh, s1);
       }
     }
-    float s[2] = {s0.x + s0.y, s1.x + s1.y};  // the idle half of a single element has dy = 0
+    float s[2] = {s0.x + s0.y, s1.x + s1.y};  // columns behind the row have dy = 0
     sum(s);
     // dx = rstd (g - mean(g) - x_hat mean(g x_hat))
     const float2 c0 = pair(-s[0] * inv_n * w.rstd), c1 = pair(-s[1] * inv_n * w.rstd);
@@ -398,49 +494,63 @@ __global__ void __launch_bounds__(kMaxBwdGroup) ln_bwd_kernel(const LnBwdArgs a,
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
-      float2 x[P], dy[P];
-      to_pairs<T, E>(w.x[i], x);
-      to_pairs<T, E>(w.dy[i], dy);
+      const float2 (&gi)[P] = weights(i);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const float2 xh = __fmul2_rn(__fadd2_rn(x[e], nmu), rstd);
-        x[e] = __ffma2_rn(__fmul2_rn(dy[e], gam[i][e]), rstd, __ffma2_rn(xh, c1, c0));
+        const float2 xh = __fmul2_rn(__fadd2_rn(get_pair<T>(w.x[i], e), nmu), rstd);
+        float2 v = __ffma2_rn(__fmul2_rn(get_pair<T>(w.dy[i], e), gi[e]), rstd, __ffma2_rn(xh, c1, c0));
+        if (add) v = __fadd2_rn(v, get_pair<T>(w.dh[i], e));
+        set_pair<T>(w.x[i], e, v);
       }
-      if (add) {
-        to_pairs<T, E>(w.dh[i], dy);
-#pragma unroll
-        for (int e = 0; e < P; ++e) x[e] = __fadd2_rn(x[e], dy[e]);
-      }
-      st_stream(dx + static_cast<int64_t>(t + i * G) * E, from_pairs<T, E>(x));
+      store_columns<T, kRagged>(dx, column(i), N, w.x[i]);
     }
   }
   if (a.part == nullptr) return;
-  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
-  float* to = groups > 1 ? dyn : part;
-  for (int k = 0; k < groups; ++k) {  // one group after the other: a fixed order
-    if (k == group) {
+  // the block's sums, one group after the other: a fixed order. Groups of less than a warp with the same
+  // columns are added first.
+  const bool merge = !kRagged && kNarrow && G < 32;
+  if (merge) {
+    for (int o = 16; o >= G; o >>= 1) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        if (t + i * G >= n) continue;
-        const int64_t j = static_cast<int64_t>(t + i * G) * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float vg = e % 2 == 0 ? sg[i][e / 2].x : sg[i][e / 2].y;
-          const float vb = e % 2 == 0 ? sb[i][e / 2].x : sb[i][e / 2].y;
-          to[j + e] = k == 0 ? vg : to[j + e] + vg;
-          to[a.N + j + e] = k == 0 ? vb : to[a.N + j + e] + vb;
+        for (int e = 0; e < P; ++e) {
+          sg[i][e].x += __shfl_xor_sync(0xffffffffu, sg[i][e].x, o);
+          sg[i][e].y += __shfl_xor_sync(0xffffffffu, sg[i][e].y, o);
+          sb[i][e].x += __shfl_xor_sync(0xffffffffu, sb[i][e].x, o);
+          sb[i][e].y += __shfl_xor_sync(0xffffffffu, sb[i][e].y, o);
         }
       }
     }
-    if (groups > 1) __syncthreads();
   }
-  if (groups > 1)
-    for (int64_t j = threadIdx.x; j < 2 * a.N; j += blockDim.x) part[j] = dyn[j];
+  const int wide = merge ? 32 : G, parts = blockDim.x / wide;
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
+  float* to = parts > 1 ? dyn : part;
+  for (int k = 0; k < parts; ++k) {
+    if (k == static_cast<int>(threadIdx.x) / wide && static_cast<int>(threadIdx.x) % wide < G) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (t + i * G >= vectors) continue;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int j = column(i) + e;
+          if (kRagged && (j < 0 || j >= N)) continue;
+          const float vg = e % 2 == 0 ? sg[i][e / 2].x : sg[i][e / 2].y;
+          const float vb = e % 2 == 0 ? sb[i][e / 2].x : sb[i][e / 2].y;
+          to[j] = k == 0 ? vg : to[j] + vg;
+          to[N + j] = k == 0 ? vb : to[N + j] + vb;
+        }
+      }
+    }
+    if (parts > 1) __syncthreads();
+  }
+  if (parts > 1)
+    for (int j = threadIdx.x; j < 2 * N; j += blockDim.x) part[j] = dyn[j];
 }
 
 // rows of any length, element by element
 template <typename T>
-__global__ void __launch_bounds__(kMaxGroup) ln_dx_long_kernel(const LnBwdArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) ln_dx_long_kernel(const LnBwdArgs a) {
   __shared__ float buf[32];
   const float inv_n = 1.0f / static_cast<float>(a.N);
   for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
@@ -518,28 +628,20 @@ __global__ void __launch_bounds__(kReduceCols* kReduceSlices) ln_reduce_kernel(c
 }
 
 // ---- host
-// elements of a load: the widest of 16 bytes, 4 bytes and one element that divides the row and that all
-// addresses and row strides are multiples of
-int vector_elems(int64_t N, int es, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds,
-                 std::initializer_list<const void*> weights) {
-  for (int bytes : {16, 4}) {
-    const int e = bytes / es;
-    if (e < 1 || N % e != 0) continue;
-    bool ok = true;
-    for (const void* p : ptrs) ok = ok && reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0;
-    for (int64_t ld : lds) ok = ok && ld % e == 0;
-    // weights are loaded 16 bytes at a time with full vectors, else one by one
-    if (bytes == 16)
-      for (const void* p : weights) ok = ok && reinterpret_cast<uintptr_t>(p) % 16 == 0;
-    if (ok) return e;
-  }
-  return 1;
+// whether all rows are whole 16-byte vectors (and the weights can be loaded 16 bytes at a time)
+bool whole_vectors(int64_t N, int es, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds,
+                   std::initializer_list<const void*> weights) {
+  bool ok = N * es % 16 == 0;
+  for (const void* p : ptrs) ok = ok && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+  for (const void* p : weights) ok = ok && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+  for (int64_t ld : lds) ok = ok && ld * es % 16 == 0;
+  return ok;
 }
 // threads a row for R vectors each
 int group_threads(int64_t n, int R) {
-  int g = 32;
-  while (static_cast<int64_t>(g) * R < n && g < kMaxGroup) g *= 2;
-  return g;
+  int g = kMinGroup;
+  while (g < kBlock && static_cast<int64_t>(g) * R < n) g *= 2;
+  return static_cast<int64_t>(g) * R < n ? static_cast<int>((n + R * 32 - 1) / (R * 32)) * 32 : g;
 }
 
 // blocks of a persistent kernel that fit on the device at once (asked once for each device and block size)
@@ -562,41 +664,42 @@ cudaError_t blocks_that_fit(Kernel kernel, FitCache& cache, int block, size_t sm
   blocks = cache.fit;
   return cudaSuccess;
 }
-template <typename T, int E, int R, int kMost>
-cudaError_t fwd_one(const LnFwdArgs& a, int G, cudaStream_t stream) {
-  const int block = G > kBlock ? G : kBlock, groups = block / G;
+template <typename T, int R, bool kRagged, int kMost>
+cudaError_t fwd_one(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
+  const int G = group_threads(n, R), block = G > kBlock ? G : kBlock, groups = block / G;
   int64_t blocks;
   {
     static std::mutex mu;
     static FitCache cache;
     std::lock_guard<std::mutex> lk(mu);
-    const cudaError_t e = blocks_that_fit(ln_fwd_kernel<T, E, R, kMost>, cache, block, 0, blocks);
+    const cudaError_t e = blocks_that_fit(ln_fwd_kernel<T, R, kRagged, kMost>, cache, block, 0, blocks);
     if (e != cudaSuccess) return e;
   }
   const int64_t most = (a.M + groups - 1) / groups;
   if (blocks > most) blocks = most;
-  ln_fwd_kernel<T, E, R, kMost><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a, G);
+  else if (kRagged) blocks -= blocks % kElems<T>;  // a group's rows are a multiple of 16 bytes apart
+  ln_fwd_kernel<T, R, kRagged, kMost><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a, G);
   return cudaGetLastError();
 }
-// vectors a thread: as few as let a block of 512 hold the row, two for wide vectors from a warp on
-template <typename T, int E, int R0>
+// Vectors a thread: one for rows of up to a warp; two up to 512 threads, which leaves registers to load ahead;
+// four up to 2048 vectors a row (ragged fp32) or 4096 (the others, 64 registers: 12288 bf16 columns 57 us
+// for 3000 rows, with 128 registers 68 us, by the kernel for long rows 160 us).
+template <typename T, bool kRagged>
 cudaError_t fwd_any(const LnFwdArgs& a, cudaStream_t stream) {
-  const int64_t n = a.N / E;
-  if (n <= 32 * R0) return fwd_one<T, E, R0, 512>(a, 32, stream);
-  if (n <= 512 * 2 * R0) return fwd_one<T, E, 2 * R0, 512>(a, group_threads(n, 2 * R0), stream);
-  if (n <= kMaxGroup * 4 * R0) return fwd_one<T, E, 4 * R0, kMaxGroup>(a, group_threads(n, 4 * R0), stream);
+  const int64_t n = (a.N + (kRagged ? 2 * kElems<T> - 2 : 0)) / kElems<T>;
+  if (n <= 32) return fwd_one<T, 1, kRagged, kMaxGroup>(a, n, stream);
+  if (n <= 2 * kMaxGroup) return fwd_one<T, 2, kRagged, kMaxGroup>(a, n, stream);
+  if constexpr (kRagged && sizeof(T) == 4)
+    if (n <= 4 * kMaxGroup) return fwd_one<T, 4, kRagged, kMaxGroup>(a, n, stream);
+  if (n <= 4 * kMaxThreads) return fwd_one<T, 4, kRagged, kMaxThreads>(a, n, stream);
   const unsigned grid = static_cast<unsigned>(a.M < 65536 ? a.M : 65536);
-  ln_fwd_long_kernel<T><<<grid, kMaxGroup, 0, stream>>>(a);
+  ln_fwd_long_kernel<T><<<grid, kMaxThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 template <typename T>
 cudaError_t fwd_type(const LnFwdArgs& a, cudaStream_t stream) {
-  constexpr int es = sizeof(T);
-  const int e = vector_elems(a.N, es, {a.x, a.residual, a.h, a.y}, {a.ldx, a.ldr}, {a.gamma, a.beta});
-  if (e == 16 / es) return fwd_any<T, 16 / es, 1>(a, stream);
-  if constexpr (es == 2)
-    if (e == 2) return fwd_any<T, 2, 2>(a, stream);
-  return fwd_any<T, 1, 4>(a, stream);
+  const bool whole = whole_vectors(a.N, sizeof(T), {a.x, a.residual, a.h, a.y}, {a.ldx, a.ldr}, {a.gamma, a.beta});
+  return whole ? fwd_any<T, false>(a, stream) : fwd_any<T, true>(a, stream);
 }
 
 int reduce_grid(int64_t N) { return static_cast<int>((2 * N + kReduceCols - 1) / kReduceCols); }
@@ -617,22 +720,23 @@ cudaError_t launch_reduce(const LnBwdArgs& a, int64_t rows, cudaStream_t stream)
 constexpr int64_t kMaxBlocks = 4 * 256;  // rows of column sums in the workspace, at most
 constexpr int64_t kLongChunks = 64;      // of them for rows too long for registers
 
-template <typename T, int E, int R>
-cudaError_t bwd_one(const LnBwdArgs& a, int G, cudaStream_t stream) {
-  const int block = G > kBlock ? G : kBlock, groups = block / G;
+template <typename T, int R, bool kRagged>
+cudaError_t bwd_one(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {
+  const int G = group_threads(n, R), block = G > kBlock ? G : kBlock, groups = block / G;
   const size_t smem = groups > 1 && a.part != nullptr ? static_cast<size_t>(2 * a.N) * sizeof(float) : 0;
   int64_t blocks;
   {
     static std::mutex mu;
     static FitCache cache;
     std::lock_guard<std::mutex> lk(mu);
-    const cudaError_t e = blocks_that_fit(ln_bwd_kernel<T, E, R>, cache, block, smem, blocks);
+    const cudaError_t e = blocks_that_fit(ln_bwd_kernel<T, R, kRagged>, cache, block, smem, blocks);
     if (e != cudaSuccess) return e;
   }
   const int64_t most = (a.M + groups - 1) / groups;
-  if (blocks > most) blocks = most;
   if (blocks > kMaxBlocks) blocks = kMaxBlocks;
-  ln_bwd_kernel<T, E, R><<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, G);
+  if (blocks > most) blocks = most;
+  else if (kRagged) blocks -= blocks % kElems<T>;  // a group's rows are a multiple of 16 bytes apart
+  ln_bwd_kernel<T, R, kRagged><<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, G);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.part == nullptr) return e;
   return launch_reduce(a, blocks, stream);
@@ -640,7 +744,7 @@ cudaError_t bwd_one(const LnBwdArgs& a, int G, cudaStream_t stream) {
 template <typename T>
 cudaError_t bwd_long(const LnBwdArgs& a, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(a.M < 65536 ? a.M : 65536);
-  ln_dx_long_kernel<T><<<grid, kMaxGroup, 0, stream>>>(a);
+  ln_dx_long_kernel<T><<<grid, kMaxThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.part == nullptr) return e;
   const int64_t chunks = a.M < kLongChunks ? a.M : kLongChunks, per = (a.M + chunks - 1) / chunks;
@@ -649,21 +753,20 @@ cudaError_t bwd_long(const LnBwdArgs& a, cudaStream_t stream) {
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_reduce(a, chunks, stream);
 }
-template <typename T, int E, int R0>
+// Vectors a thread as forward, but up to 512 threads: the column sums take 128 registers (3000 rows of 12288
+// bf16 columns: 113 us; by the kernels for long rows 312 us).
+template <typename T, bool kRagged>
 cudaError_t bwd_any(const LnBwdArgs& a, cudaStream_t stream) {
-  const int64_t n = a.N / E;
-  if (n <= 32 * R0) return bwd_one<T, E, R0>(a, 32, stream);
-  if (n <= kMaxBwdGroup * 2 * R0) return bwd_one<T, E, 2 * R0>(a, group_threads(n, 2 * R0), stream);
+  const int64_t n = (a.N + (kRagged ? 2 * kElems<T> - 2 : 0)) / kElems<T>;
+  if (n <= 32) return bwd_one<T, 1, kRagged>(a, n, stream);
+  if (n <= 2 * kMaxGroup) return bwd_one<T, 2, kRagged>(a, n, stream);
+  if (n <= 4 * kMaxGroup) return bwd_one<T, 4, kRagged>(a, n, stream);
   return bwd_long<T>(a, stream);
 }
 template <typename T>
 cudaError_t bwd_type(const LnBwdArgs& a, cudaStream_t stream) {
-  constexpr int es = sizeof(T);
-  const int e = vector_elems(a.N, es, {a.dy, a.x, a.dh, a.dx}, {a.lddy, a.ldx, a.lddh}, {a.gamma});
-  if (e == 16 / es) return bwd_any<T, 16 / es, es == 2 ? 1 : 2>(a, stream);
-  if constexpr (es == 2)
-    if (e == 2) return bwd_any<T, 2, 4>(a, stream);
-  return bwd_any<T, 1, 4>(a, stream);
+  const bool whole = whole_vectors(a.N, sizeof(T), {a.dy, a.x, a.dh, a.dx}, {a.lddy, a.ldx, a.lddh}, {a.gamma});
+  return whole ? bwd_any<T, false>(a, stream) : bwd_any<T, true>(a, stream);
 }
 
 }  // namespace

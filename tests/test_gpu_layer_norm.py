@@ -113,6 +113,61 @@ def test_many_rows():
     _run(9001, 512, torch.bfloat16, torch.bfloat16)
 
 
+# rows that begin and end inside 16 bytes, more of them than groups of threads: every group has several
+RAGGED = [(20011, 61), (9003, 127), (5002, 250), (5001, 1001), (2003, 2047), (1501, 4001), (701, 8181), (401, 8191),
+          (331, 9001), (301, 16381)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=NAME.get)
+@pytest.mark.parametrize("shape", RAGGED, ids=lambda s: "x".join(map(str, s)))
+def test_ragged_rows(shape, dtype):
+    _run(*shape, dtype, torch.float32, residual=True, dh=True, seed=12)
+    _run(*shape, dtype, dtype, seed=13)
+
+
+@pytest.mark.parametrize("N", [61, 1001, 4001, 8195])
+def test_nan_at_a_ragged_end_stays_in_its_row(N):
+    # the 16 bytes around a row's ends belong to its neighbours as well
+    swg = _swg()
+    for dtype in DTYPES:
+        t = _inputs(9, N, dtype, torch.float32, 14)
+        clean = swg.layer_norm_fwd(t["x"], t["gamma"], t["beta"], residual=t["residual"])
+        dclean = swg.layer_norm_bwd(t["dy"], clean["h"], clean["stats"], gamma=t["gamma"])[0]
+        t["x"][2, 0], t["x"][2, N - 1], t["residual"][5, 0], t["residual"][5, N - 1] = (float("nan"),) * 4
+        out = swg.layer_norm_fwd(t["x"], t["gamma"], t["beta"], residual=t["residual"])
+        h = clean["h"].clone()
+        h[2, 0], h[2, N - 1], t["dy"][5, 0], t["dy"][5, N - 1] = (float("inf"),) * 4
+        dx = swg.layer_norm_bwd(t["dy"], h, clean["stats"], gamma=t["gamma"])[0]
+        rows = [r for r in range(9) if r not in (2, 5)]
+        assert torch.equal(out["y"][rows], clean["y"][rows]) and torch.equal(out["h"][rows], clean["h"][rows])
+        assert torch.equal(dx[rows], dclean[rows])
+        assert out["y"][2].isnan().all() and out["y"][5].isnan().all()
+        assert not dx[2].isfinite().all() and not dx[5].isfinite().all()
+
+
+def test_weights_and_rows_off_16_bytes():
+    # outputs on 16 bytes, inputs and weights not, and the other way round
+    swg = _swg()
+    for dtype in DTYPES:
+        for N in (96, 1000, 1003):
+            t = _inputs(700, N, dtype, dtype, 15)
+            off = {}
+            for k, v in t.items():
+                off[k] = torch.empty(v.numel() + 1, dtype=v.dtype, device="cuda")[1:].view(v.shape).copy_(v)
+            for a in (off, {**t, "gamma": off["gamma"], "beta": off["beta"]}, {**off, "x": t["x"]}):
+                out = swg.layer_norm_fwd(a["x"], a["gamma"], a["beta"], eps=EPS, residual=a["residual"])
+                _check_fwd(t, out, dtype, residual=True)
+                got = swg.layer_norm_bwd(a["dy"], out["h"], out["stats"], gamma=a["gamma"], dh=a["dh"])
+                _check_bwd(t, out["h"], out["stats"], got, dtype, dtype, dh=True)
+            spare = {k: torch.empty(700 * N + 1, dtype=dtype, device="cuda")[1:].view(700, N) for k in ("y", "h", "dx")}
+            stats = torch.empty((700, 2), device="cuda")
+            out = swg.layer_norm_fwd(t["x"], t["gamma"], t["beta"], eps=EPS, residual=t["residual"],
+                                     out={"y": spare["y"], "h": spare["h"], "stats": stats})
+            _check_fwd(t, out, dtype, residual=True)
+            _check_bwd(t, out["h"], stats, swg.layer_norm_bwd(t["dy"], out["h"], stats, gamma=t["gamma"], dh=t["dh"],
+                                                              dx=spare["dx"]), dtype, dtype, dh=True)
+
+
 def test_leading_dimensions_and_shared_rows():
     swg = _swg()
     t = _inputs(12, 72, torch.bfloat16, torch.float32, 5)
