@@ -169,60 +169,65 @@ __device__ __forceinline__ float take_entries(const KdArgs& a, int64_t r, EntryV
   }
   return warp_sum(s);
 }
-// The lane's entries (bit i: entry 32 i + lane) whose id is in [e0, e1) and has not come before in the
-// row; twice: one of them comes again.
+// Of the lane's entries (bit i: entry 32 i + lane) one for each id in [e0, e1); shared: those whose id comes
+// again in the row. Which entry of an id it is may differ from run to run, what comes of it does not.
+// (Finding the lanes of one id with a warp match first, 32 ids at a time, took 6 us more a row of 64 entries.)
 __device__ __forceinline__ uint32_t first_entries(const KdArgs& a, const EntryArrays& n, int* table, int slots,
-                                                  int64_t e0, int64_t e1, bool& twice) {
+                                                  int64_t e0, int64_t e1, uint32_t& shared) {
+  constexpr int kAgain = static_cast<int>(0x80000000u);  // an id that has come again; ids are below 2^31 - 1
   const int lane = threadIdx.x & 31;
   for (int i = lane; i < slots; i += 32) table[i] = -1;
   __syncwarp();
+  auto place = [&](int id) { return static_cast<int>((static_cast<uint32_t>(id) * 2654435761u) >> 16) & (slots - 1); };
   uint32_t mine = 0;
   bool again = false;
   for (int k0 = 0; k0 < a.K; k0 += 32) {
-    const int kept = k0 + lane < a.K ? n.id[k0 + lane] : -1;
-    const int id = kept >= 0 && kept >= e0 && kept < e1 ? kept : -1;
-    // the lowest lane with an id looks for it in the table, where the entries before have theirs
-    const uint32_t lanes = __match_any_sync(0xffffffffu, id);
-    bool before = (lanes & ((1u << lane) - 1u)) != 0;
-    if (id >= 0 && !before) {
-      int at = static_cast<int>((static_cast<uint32_t>(id) * 2654435761u) >> 16) & (slots - 1);
-      for (int step = 0; step < slots; ++step) {
-        const int old = atomicCAS(&table[at], -1, id);
-        before = old == id;
-        if (old == id || old == -1) break;
-        at = (at + 1) & (slots - 1);
+    const int id = k0 + lane < a.K ? n.id[k0 + lane] : -1;
+    if (id < 0 || id < e0 || id >= e1) continue;
+    for (int at = place(id), step = 0; step < slots; at = (at + 1) & (slots - 1), ++step) {
+      const int old = atomicCAS(&table[at], -1, id);
+      if (old == -1) {
+        mine |= 1u << (k0 / 32);
+        break;
+      }
+      if ((old & ~kAgain) == id) {
+        atomicOr(&table[at], kAgain);
+        again = true;
+        break;
       }
     }
-    if (id >= 0) {
-      if (before) again = true;
-      else mine |= 1u << (k0 / 32);
-    }
-    __syncwarp();
   }
-  twice = __any_sync(0xffffffffu, again);
+  shared = 0;
+  if (!__any_sync(0xffffffffu, again)) return mine;
+  __syncwarp();
+  for (uint32_t todo = mine; todo != 0; todo &= todo - 1) {
+    const int i = __ffs(todo) - 1, id = n.id[32 * i + lane];
+    int at = place(id);
+    for (int step = 0; step < slots && (table[at] & ~kAgain) != id; ++step) at = (at + 1) & (slots - 1);
+    if ((table[at] & kAgain) != 0) shared |= 1u << i;
+  }
+  __syncwarp();
   return mine;
 }
 static_assert(kKdMaxEntries <= 32 * 32, "a bit for each of a lane's entries");
-// One warp: the elements at the entries in `mine`. An id that comes twice is taken at its first entry, its
-// probabilities added lane by lane.
+// One warp: the elements at the entries in `mine`; the probabilities of an id in `shared` are added lane by
+// lane.
 template <typename T>
 __device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g, const EntryArrays& n, uint32_t mine,
-                                             bool twice, T* out) {
+                                             uint32_t shared, T* out) {
   const int lane = threadIdx.x & 31;
   const float c2 = a.inv_temp * kLog2e;
   for (int k0 = 0; k0 < a.K; k0 += 32) {
     const bool own = mine >> (k0 / 32) & 1u;
     const int id = own ? n.id[k0 + lane] : -1;
     float q = own ? ex2_approx(n.td[k0 + lane] * c2) : 0.0f;
-    if (twice) {
-      for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo != 0; todo &= todo - 1) {
-        const int from = __ffs(todo) - 1, its = __shfl_sync(0xffffffffu, id, from);
-        float t = 0.f;
-        for (int j = lane; j < a.K; j += 32)
-          if (n.id[j] == its) t += ex2_approx(n.td[j] * c2);
-        t = warp_sum(t);
-        if (lane == from) q = t;
-      }
+    for (uint32_t todo = __ballot_sync(0xffffffffu, shared >> (k0 / 32) & 1u); todo != 0; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1, its = __shfl_sync(0xffffffffu, id, from);
+      float t = 0.f;
+      for (int j = lane; j < a.K; j += 32)
+        if (n.id[j] == its) t += ex2_approx(n.td[j] * c2);
+      t = warp_sum(t);
+      if (lane == from) q = t;
     }
     if (own)
       out[id] = from_f<T>(fmaf(g.dense, ex2_approx(fmaf(n.z[k0 + lane], g.k.c, -g.k.ref)), -g.sparse * q));
@@ -281,13 +286,13 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
                   rank == 0 ? a.V : first_element<T>(sh, sh.end), next);
     };
     // the elements at the entries of row r, the it-th, over the dense part
-    auto sparse = [&](int64_t r, int64_t it, uint32_t mine, bool twice) {
+    auto sparse = [&](int64_t r, int64_t it, uint32_t mine, uint32_t shared) {
       const int slot = static_cast<int>(it & (kSlots - 1));
       wait(&sm.dense[slot], static_cast<uint32_t>((it / kSlots) & 1));
       if (sm.weight[slot] == 0.0f) return;
       const EntryArrays n = entries(slot);
       const Gradient g = sm.grad[slot];
-      store_sparse<T>(a, g, n, mine, twice, static_cast<T*>(a.dlogits) + r * a.ldo);
+      store_sparse<T>(a, g, n, mine, shared, static_cast<T*>(a.dlogits) + r * a.ldo);
       __syncwarp();
     };
     if (begin < a.T) {
@@ -296,8 +301,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       if (begin + 2 * step < a.T) load_some(a, begin + 2 * step, 0, loads);
     }
     int64_t it = odd;
-    uint32_t mine = 0;
-    bool twice = false;
+    uint32_t mine = 0, shared = 0;
     for (int64_t r = begin; r < a.T; r += 2 * step, it += 2) {
       const int slot = static_cast<int>(it & (kSlots - 1));
       const EntryArrays n = entries(slot);
@@ -325,11 +329,11 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       if (rank == 0 && lane < S) send_f2(&sm.note[slot], &sm.joined[slot], static_cast<uint32_t>(lane), 0.f, 0.f);
       __syncwarp();
       if (kGrad) {
-        if (r != begin) sparse(r - 2 * step, it - 2, mine, twice);
-        mine = first_entries(a, n, table, slots, e0, e1, twice);
+        if (r != begin) sparse(r - 2 * step, it - 2, mine, shared);
+        mine = first_entries(a, n, table, slots, e0, e1, shared);
       }
     }
-    if (kGrad && begin < a.T) sparse(first + (it - 2) * step, it - 2, mine, twice);
+    if (kGrad && begin < a.T) sparse(first + (it - 2) * step, it - 2, mine, shared);
   } else if (warp == W + 3) {
     // joins the row's maxima and sums, and forms the constants of its gradient and (first block) its loss
     int64_t it = 0;
@@ -385,10 +389,15 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
       WarpSums<T, false> sum(c2);
       for (int at = sh.begin; at < sh.end; at += kStageVecs) {
-        Vec v[4];
+        const int cnt = min(sh.end - at, kStageVecs);
         wait(&sm.ring.full[in.stage], in.parity);
-        read_stage<T, W>(v, dyn + in.stage * kStageBytes, min(sh.end - at, kStageVecs));
-        sum.add(v, c2, false);
+        // (with a gradient this costs more than it saves: 345 us instead of 325 for 4096 x 131072 bf16)
+        if (kGrad || warp * kWarpVecs < cnt) {
+          Vec v[4];
+          if (kGrad || cnt == kStageVecs) read_stage<T, W>(v, dyn + in.stage * kStageBytes, cnt);
+          else read_stage_runs<T, W>(v, dyn + in.stage * kStageBytes, cnt);  // the last warps have nothing to add
+          sum.add(v, c2, false);
+        }
         if (!kGrad) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.ring.empty[in.stage]);
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
         if (lane == 0) mbar_arrive(&sm.ring.empty[held.stage]);
         held.next(stages);
         const int64_t e0 = first_element<T>(sh, c), e1 = first_element<T>(sh, c + cnt);
-        const bool inner = aligned && e0 >= 0 && e1 <= a.V;  // the stage has whole vectors only
+        T* to = out + e0 + tid * E;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (some) {
@@ -429,13 +438,13 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
             v[i] = Vec{{0u, 0u, 0u, 0u}};
           }
         }
-        T* to = out + e0 + tid * E;
+        // the stage's first and last vector may be partial
+        const int whole0 = e0 < 0 ? 1 : 0, whole1 = e1 > a.V ? cnt - 1 : cnt;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int at = i * kStreamThreads + tid;
-          if (at >= cnt) break;
-          if (inner) st_vec(to + i * kStreamThreads * E, v[i]);
-          else store_row_vec(out, e0 + at * E, a.V, aligned, v[i]);
+          if (aligned && at >= whole0 && at < whole1) st_vec(to + i * kStreamThreads * E, v[i]);
+          else if (at < cnt) store_row_vec(out, e0 + at * E, a.V, aligned, v[i]);
         }
       }
       __syncwarp();
@@ -521,11 +530,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) kd_bwd_kernel(const KdArgs a, 
       store_row_vec(out, first_element<T>(sh, at), a.V, aligned, v[i]);
     }
   }
-  bool twice = false;
-  uint32_t mine = 0;
-  if (tid < 32) mine = first_entries(a, n, reinterpret_cast<int*>(dyn) + 3 * a.K, slots, e0, e1, twice);
+  uint32_t mine = 0, shared = 0;
+  if (tid < 32) mine = first_entries(a, n, reinterpret_cast<int*>(dyn) + 3 * a.K, slots, e0, e1, shared);
   __syncthreads();
-  if (tid < 32) store_sparse<T>(a, g, n, mine, twice, out);
+  if (tid < 32) store_sparse<T>(a, g, n, mine, shared, out);
 }
 
 cudaError_t launch_bwd(const KdArgs& a, int dtype, int64_t vectors, int sms, cudaStream_t stream) {

@@ -2,9 +2,9 @@
 //
 // A block has W computing warps and a producer warp that keeps a ring of stages (four vectors for each
 // computing thread) full with bulk copies, across rows: the copies of the next rows run under the work on
-// this one, so the reads never pause for a reduction. Cluster c takes the rows c, c + #clusters, ...; its S blocks take a share
-// of the row each (vocab_rows.cuh: aligned 16-byte vectors). A row's first and last vector, when they
-// are partial, are put together by the producer warp, with -inf outside the row.
+// this one, so the reads do not pause for a reduction. Cluster c takes the rows c, c + #clusters, ...; its S
+// blocks take a share of the row each (vocab_rows.cuh: aligned 16-byte vectors). A row's first and last
+// vector, when they are partial, are put together by the producer warp, with -inf outside the row.
 #pragma once
 
 #include "vocab_rows.cuh"
@@ -12,6 +12,7 @@
 namespace swg {
 namespace row {
 
+constexpr int kWarpVecs = 4 * 32;  // vectors of a stage that a warp takes
 template <int W>
 struct Shape {
   static constexpr int kThreads = 32 * W;             // computing threads
@@ -78,8 +79,7 @@ struct Place {
 template <typename T, int W, int N>
 __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int64_t V, int64_t first, int64_t rows,
                                              int64_t step, int per, int rank, unsigned char* buf, int stages,
-                                             Ring<W, N>& ring,
-                                             Patience& wait) {
+                                             Ring<W, N>& ring, Patience& wait) {
   constexpr int E = Traits<T>::E, kStageVecs = Shape<W>::kStageVecs, kStageBytes = Shape<W>::kStageBytes;
   const int lane = threadIdx.x & 31;
   const T* base = static_cast<const T*>(logits);
@@ -259,8 +259,8 @@ __device__ __forceinline__ void send_u64(const uint64_t* to, const uint64_t* bar
 }  // namespace row
 
 // A persistent launch: as many clusters as fit on the device at once, at most one a row (`all`: one for
-// every row, however many fit). The occupancy of
-// a (kernel, cluster size, shared memory) is asked once for each device.
+// every row, however many fit). The occupancy of a (kernel, cluster size, shared memory) is asked once for
+// each device.
 struct StreamCache {
   int device = -1, S = 0, clusters = 0;
   size_t smem = 0;
