@@ -31,7 +31,7 @@ constexpr int kListed = 288;    // groups of runs listed before they are looked 
 template <int W>
 struct Plan {
   static constexpr int kStages = W == 16 ? 5 : 4;              // of the ring
-  static constexpr int kSelectors = W == 16 ? 3 : 4;           // warps that finish rows
+  static constexpr int kSelectors = 3;                         // warps that finish rows
   static constexpr int kTableBytes = W == 16 ? 8192 : 4096;
   static constexpr int kBlocks = W == 16 ? kMaxCluster : 1;    // of a row, at most
   static constexpr int kThreads = 32 * (W + 1 + kSelectors);
@@ -141,8 +141,8 @@ __device__ __forceinline__ int select_best(const Share& sh, int top, Finish<W>& 
     if (depth > 1) last |= kThreads - 1;
     const int64_t stage = static_cast<int64_t>(last / kThreads + 1) * depth - 1;
     const int64_t end = stage * kStageVecs + 4 * (last % kThreads) + 4;  // of the share's vectors
-    least_key = rank_key(rank_logit(bound), static_cast<uint32_t>(
-                                    min(first_element<T>(sh, sh.begin) + end * E - 1, static_cast<int64_t>(0xfffffffe))));
+    const int64_t behind = first_element<T>(sh, sh.begin) + end * E - 1;
+    least_key = rank_key(rank_logit(bound), static_cast<uint32_t>(min(behind, static_cast<int64_t>(0xfffffffe))));
   }
 
   // the runs of the groups listed, one run a lane at a time
@@ -231,11 +231,11 @@ __device__ __forceinline__ int select_best(const Share& sh, int top, Finish<W>& 
   }
   return rank_candidates(f.cand, have, top, best);
 }
-static_assert(kListed >= 32 * 8 && Plan<16>::kTableBytes / 2 <= 65536, "the list takes what one step adds; 16-bit groups");
-static_assert(kListed >= 32 * 8 && Plan<16>::kTableBytes / 2 <= 65536, "the list takes what one step adds; 16-bit groups");
+static_assert(kListed >= 32 * 8, "the list takes what one step adds");
+static_assert(Plan<16>::kTableBytes / 2 <= 65536, "16-bit groups");
 
 template <typename T, int W>
-__global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 2)
+__global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 3)
     tlp_fwd_kernel(const TlpFwdArgs a, Split split, uint32_t* status) {
   constexpr int kStageVecs = Shape<W>::kStageVecs, kStageBytes = Shape<W>::kStageBytes, kThreads = Shape<W>::kThreads;
   constexpr int kStages = Plan<W>::kStages, kSelectors = Plan<W>::kSelectors;
@@ -363,12 +363,13 @@ __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 2)
       float most = neg_inf(), group_most = neg_inf();  // the thread's maximum, and that of its open group
       int best = 0, group = tid, left = depth;         // the first group that has it; the open group
       for (int at = sh.begin; at < sh.end; at += kStageVecs) {
-        Vec v[4];
         const int cnt = min(sh.end - at, kStageVecs);
         wait(&sm.ring.full[in.stage], in.parity);
-        read_stage_runs<T, W>(v, dyn + in.stage * kStageBytes, cnt);
-        const float x = sums.add(v, c2, cnt < kStageVecs);
-        group_most = fmaxf(group_most, x);
+        if (warp * kWarpVecs < cnt) {
+          Vec v[4];
+          read_stage_runs<T, W>(v, dyn + in.stage * kStageBytes, cnt);
+          group_most = fmaxf(group_most, sums.add(v, c2, cnt < kStageVecs));
+        }
         if (--left == 0 || at + kStageVecs >= sh.end) {
           if (a.top > 0) table[group] = from_f<T>(group_most);
           if (group_most > most) {
@@ -483,11 +484,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) tlp_bwd_kernel(const TlpBwdArg
 cudaError_t launch_token_logprobs_fwd(const TlpFwdArgs& a, int dtype, cudaStream_t stream) {
   const int64_t vectors = row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2);
   const Split p = split_row(a.T, vectors, vectors, device_sm_count());
-  // Blocks of four computing warps, two an SM, take short rows, and rows up to 64 KB when each of those
-  // blocks has several; blocks of 16 take the others. bf16, the 20 best: 8192 columns 103 us against 215 us with
-  // 16 warps (16384 rows), 32768 columns 71 against 77 us (4096 rows), 131072 columns 71 against 58 us (1024).
+  // Blocks of four computing warps, three an SM, take short rows, and rows up to 100 KB when each of those
+  // blocks has two; blocks of 16 take the others. bf16, the 20 best, L2 cold: 8192 columns 98 us against
+  // 213 us with 16 warps (16384 rows), 32768 columns 68 against 76 us (4096 rows), 50001 columns 109 against
+  // 115 us (4864 rows), 131072 columns 111 against 98 us (2048 rows).
   const int64_t sms = device_sm_count();
-  const bool small = p.S == 1 && (vectors <= 1024 || (vectors <= 4096 && a.T >= 6 * sms));
+  const bool small = p.S == 1 && (vectors <= 1024 || (vectors <= 6400 && a.T >= 6 * sms));
   return small ? launch_fwd_any<4>(a, dtype, p, stream) : launch_fwd_any<16>(a, dtype, p, stream);
 }
 
