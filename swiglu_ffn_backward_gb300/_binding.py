@@ -570,11 +570,12 @@ def _on_stream(stream, fn, *args, **kwargs):
 
 
 def _run(what, fn, dev, *args):
-    """One C call on `dev` and its current stream; raises on an error status."""
+    """One C call on `dev` and its current stream; raises on an error status. A small call's time is
+    spent here on the host, about 20 us with the outputs' allocation: hence the current device and stream
+    are asked for without the objects that torch.cuda builds around them."""
     index = dev.index
-    # the current stream's handle without building a Stream object around it (2 us of a 10 us call)
     stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, stream)
     else:
         status = _call(dev, fn, *args, stream)
@@ -607,12 +608,16 @@ def _row_tensor(t, name):
     return t.contiguous(), M, N, N, code
 
 
-def _like_rows(t, name, x, shape):
-    """A second input of x's shape and dtype: (tensor, row stride); (None, 0) for None."""
+def _like_rows(t, name, x, ldx, shape):
+    """A second input of x's shape and dtype: (tensor, row stride); (None, 0) for None. x and ldx as
+    _row_tensor gave them."""
     if t is None:
         return None, 0
     if isinstance(t, torch.Tensor) and (t.dtype != x.dtype or t.shape != shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape)} and dtype {x.dtype}, got {tuple(t.shape)}, {t.dtype}")
+        raise ValueError(f"{name} must have the shape {tuple(shape)} and dtype {x.dtype}, "
+                         f"got {tuple(t.shape)}, {t.dtype}")
+    if isinstance(t, torch.Tensor) and t.device == x.device and t.stride() == x.stride():
+        return t, ldx  # laid out as x
     t, _, _, ld, _ = _row_tensor(t, name)
     if t.device != x.device:
         _device_of(x, t)  # raises
@@ -651,7 +656,8 @@ def _norm_weights(gamma, beta, N, x):
     return gamma, beta, w.dtype if w is not None else x.dtype
 
 
-def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, out: dict | None = None, stream=None) -> dict:
+def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, out: dict | None = None,
+                   stream=None) -> dict:
     """Layer norm of x [..., N] over its last dimension (fp32/fp16/bf16): a dict of y and stats [M, 2]
     (fp32 mean and 1/sqrt(var + eps) of the M rows), and of h = x + residual, the tensor that is
     normalised, when a residual of x's shape is given. gamma, beta [N] (x's dtype or fp32, both the
@@ -660,7 +666,7 @@ def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, o
         return _on_stream(stream, layer_norm_fwd, x, gamma, beta, eps=eps, residual=residual, out=out)
     shape = x.shape if isinstance(x, torch.Tensor) else None
     xt, M, N, ldx, code = _row_tensor(x, "x")
-    res, ldr = _like_rows(residual, "residual", xt, shape)
+    res, ldr = _like_rows(residual, "residual", xt, ldx, shape)
     gamma, beta, wdtype = _norm_weights(gamma, beta, N, xt)
     dev = xt.device
     if out is None:
@@ -690,14 +696,14 @@ def layer_norm_bwd(dy, x, stats, gamma=None, dh=None, params: bool = True, dx=No
     dgamma and dbeta have its dtype (x's without it) and are None when params is False. dh, if given, is
     the gradient that reaches the normalised tensor past the norm: it is added to dx."""
     if stream is not None:
-        return _on_stream(stream, layer_norm_bwd, dy, x, stats, gamma=gamma, dh=dh, params=params, dx=dx, dgamma=dgamma,
-                          dbeta=dbeta, workspace=workspace)
+        return _on_stream(stream, layer_norm_bwd, dy, x, stats, gamma=gamma, dh=dh, params=params, dx=dx,
+                          dgamma=dgamma, dbeta=dbeta, workspace=workspace)
     shape = x.shape if isinstance(x, torch.Tensor) else None
     xt, M, N, ldx, code = _row_tensor(x, "x")
     if dy is None:
         raise TypeError("dy must be a CUDA tensor")
-    dyt, lddy = _like_rows(dy, "dy", xt, shape)
-    dht, lddh = _like_rows(dh, "dh", xt, shape)
+    dyt, lddy = _like_rows(dy, "dy", xt, ldx, shape)
+    dht, lddh = _like_rows(dh, "dh", xt, ldx, shape)
     dev = xt.device
     stats = _vector(stats, "stats", 2 * M, _F32, dev)
     if stats is None:
@@ -748,16 +754,17 @@ def token_logprobs_fwd(logits, targets=None, top_k: int = 0, temperature: float 
     dev = z.device
     targets = _vector(targets, "targets", T, _INDEX, dev)
     given, f32 = out or {}, torch.float32
-    out = {"entropy": _out(given.get("entropy"), lead, f32, dev, "entropy"),
-           "stats": _out(given.get("stats"), (T, 2), f32, dev, "stats")}
+    entropy = _out(given.get("entropy"), lead, f32, dev, "entropy")
+    out = {"entropy": entropy, "stats": _out(given.get("stats"), (T, 2), f32, dev, "stats")}
     logp = top_logp = top_idx = None
     if targets is not None:
-        out["logp"] = logp = _out(given.get("logp"), lead, f32, dev, "logp")
+        logp = given.get("logp")
+        out["logp"] = logp = torch.empty_like(entropy) if logp is None else _out(logp, lead, f32, dev, "logp")
     if top_k > 0:
         out["top_logp"] = top_logp = _out(given.get("top_logp"), (*lead, top_k), f32, dev, "top_logp")
         out["top_idx"] = top_idx = _out(given.get("top_idx"), (*lead, top_k), torch.int64, dev, "top_idx")
     _run("token_logprobs_fwd", lib.token_logprobs_fwd, dev, z.data_ptr(), _ptr(targets), _ptr(logp),
-         out["entropy"].data_ptr(), out["stats"].data_ptr(), _ptr(top_logp), _ptr(top_idx), T, V, ld, top_k,
+         entropy.data_ptr(), out["stats"].data_ptr(), _ptr(top_logp), _ptr(top_idx), T, V, ld, top_k,
          temperature, ignore_index, code, _itype(targets))
     return out
 
@@ -801,7 +808,8 @@ def _distill_inputs(logits, teacher_ids, teacher_logits):
     return shape, z, T, V, ld, code, ids, tl, K
 
 
-def distill_fwd(logits, teacher_ids, teacher_logits, temperature: float = 1.0, out: dict | None = None, stream=None) -> dict:
+def distill_fwd(logits, teacher_ids, teacher_logits, temperature: float = 1.0, out: dict | None = None,
+                stream=None) -> dict:
     """Distillation loss of student logits [..., V] (fp32/fp16/bf16, rows may lie apart) against a
     teacher's top logits: teacher_ids [..., K] (int64 or int32; outside the vocabulary: absent) and
     teacher_logits [..., K] (fp32/fp16/bf16). A dict of loss [...] = sum q (ln q - ln p), q the softmax of
@@ -817,12 +825,13 @@ def distill_fwd(logits, teacher_ids, teacher_logits, temperature: float = 1.0, o
     return out
 
 
-def distill_bwd(weight, logits, teacher_ids, teacher_logits, stats, temperature: float = 1.0, dlogits=None, stream=None):
+def distill_bwd(weight, logits, teacher_ids, teacher_logits, stats, temperature: float = 1.0, dlogits=None,
+                stream=None):
     """The gradient of sum(weight * loss) with respect to the logits, weight [...] fp32, from the
     forward's stats. dlogits may be the logits themselves."""
     if stream is not None:
-        return _on_stream(stream, distill_bwd, weight, logits, teacher_ids, teacher_logits, stats, temperature=temperature,
-                          dlogits=dlogits)
+        return _on_stream(stream, distill_bwd, weight, logits, teacher_ids, teacher_logits, stats,
+                          temperature=temperature, dlogits=dlogits)
     shape, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
     weight, stats = _vector(weight, "weight", T, _F32, z.device), _vector(stats, "stats", 2 * T, _F32, z.device)
     dlogits, ldo = _dlogits(dlogits, shape, z, T, V)
@@ -837,7 +846,8 @@ def distill_fwd_bwd(logits, teacher_ids, teacher_logits, weight, temperature: fl
     loss, stats and dlogits. Where a row fits on the chip the logits are read once. `out` may supply any
     of the outputs; out["dlogits"] may be the logits themselves."""
     if stream is not None:
-        return _on_stream(stream, distill_fwd_bwd, logits, teacher_ids, teacher_logits, weight, temperature=temperature, out=out)
+        return _on_stream(stream, distill_fwd_bwd, logits, teacher_ids, teacher_logits, weight,
+                          temperature=temperature, out=out)
     shape, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
     weight = _vector(weight, "weight", T, _F32, z.device)
     given = out or {}
