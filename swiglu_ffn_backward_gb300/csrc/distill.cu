@@ -483,15 +483,20 @@ cudaError_t launch_fwd_any(const KdArgs& a, int dtype, Split split, cudaStream_t
 
 // ---- gradient alone
 
+// the block's barrier, from whichever place a warp comes to it
+__device__ __forceinline__ void block_sync() { asm volatile("barrier.sync 0;" ::: "memory"); }
+
 // The gradient from saved statistics: a block of G threads (64 to 256) takes a share of a row, 16 to 32 KB in
-// registers. While it arrives, the first warp takes the teacher's entries; it looks for ids that come twice
-// while the others form the dense part, and writes the sparse part over it.
+// registers. A warp more takes the teacher's entries while it arrives, looks for ids that come again while
+// the others form the dense part, and writes the sparse part over it. (With the first of the G threads' warps
+// doing that too, 4096 x 32768 bf16 with 64 entries took 101 us instead of 85.)
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 4) kd_bwd_kernel(const KdArgs a, int64_t share0, Groups p, int slots) {
+__global__ void __launch_bounds__(kRowThreads + 32, 4)
+    kd_bwd_kernel(const KdArgs a, int64_t share0, Groups p, int slots) {
   constexpr int E = Traits<T>::E;
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ float sq_all;
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int64_t at = share0 + blockIdx.x, r = at / p.S;
   const T* z = static_cast<const T*>(a.logits) + r * a.ld;
   T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
@@ -500,25 +505,35 @@ __global__ void __launch_bounds__(kRowThreads, 4) kd_bwd_kernel(const KdArgs a, 
   const float w = a.weight[r], c2 = a.inv_temp * kLog2e;
   if (w == 0.0f) {
     const Vec zero = {{0u, 0u, 0u, 0u}};
-    for (int g = sh.begin + tid; g < sh.end; g += p.G) store_row_vec(out, first_element<T>(sh, g), a.V, aligned, zero);
+    for (int g = sh.begin + tid; g < sh.end && tid < p.G; g += p.G)
+      store_row_vec(out, first_element<T>(sh, g), a.V, aligned, zero);
     return;
   }
-  const int64_t e0 = first_element<T>(sh, sh.begin), e1 = first_element<T>(sh, sh.end);
-  const EntryArrays n = entry_arrays(dyn, a.K, 0);
-  EntryLoads loads;
-  if (tid < 32) load_some(a, r, 0, loads);
-  Vec v[kVecs];
-  load_chunk<T, false>(v, z, a.V, sh, sh.begin, tid, p.G);
-  if (tid < 32) {
+  const float m = a.stats_in[2 * r], s = a.stats_in[2 * r + 1];
+  auto gradient = [&](float sq) {
+    const Scale k = scale_of(m, c2);
+    return make_gradient(a, k, sum_at_ref(s, m, k), w, sq);
+  };
+  if (tid >= p.G) {
+    const int64_t e0 = first_element<T>(sh, sh.begin), e1 = first_element<T>(sh, sh.end);
+    const EntryArrays n = entry_arrays(dyn, a.K, 0);
+    EntryLoads loads;
+    load_some(a, r, 0, loads);
     EntryValues<T> values;
     gather_some(a, r, 0, loads, e0, e1, values);
     const float sq = take_entries<T>(a, r, values, n, e0, e1);
-    if (lane == 0) sq_all = sq;
+    if (tid == p.G) sq_all = sq;
+    block_sync();
+    uint32_t shared;
+    const uint32_t mine = first_entries(a, n, reinterpret_cast<int*>(dyn) + 3 * a.K, slots, e0, e1, shared);
+    block_sync();
+    store_sparse<T>(a, gradient(sq), n, mine, shared, out);
+    return;
   }
-  __syncthreads();
-  const float m = a.stats_in[2 * r];
-  const Scale k = scale_of(m, c2);
-  const Gradient g = make_gradient(a, k, sum_at_ref(a.stats_in[2 * r + 1], m, k), w, sq_all);
+  Vec v[kVecs];
+  load_chunk<T, false>(v, z, a.V, sh, sh.begin, tid, p.G);
+  block_sync();
+  const Gradient g = gradient(sq_all);
   for (int c = sh.begin; c < sh.end; c += kVecs * p.G) {
     if (c > sh.begin) load_chunk<T, false>(v, z, a.V, sh, c, tid, p.G);
 #pragma unroll
@@ -530,10 +545,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) kd_bwd_kernel(const KdArgs a, 
       store_row_vec(out, first_element<T>(sh, at), a.V, aligned, v[i]);
     }
   }
-  uint32_t mine = 0, shared = 0;
-  if (tid < 32) mine = first_entries(a, n, reinterpret_cast<int*>(dyn) + 3 * a.K, slots, e0, e1, shared);
-  __syncthreads();
-  if (tid < 32) store_sparse<T>(a, g, n, mine, shared, out);
+  block_sync();
 }
 
 cudaError_t launch_bwd(const KdArgs& a, int dtype, int64_t vectors, int sms, cudaStream_t stream) {
@@ -544,9 +556,9 @@ cudaError_t launch_bwd(const KdArgs& a, int dtype, int64_t vectors, int sms, cud
   const int64_t total = a.T * p.S, most = int64_t(1) << 30;
   for (int64_t s0 = 0; s0 < total; s0 += most) {
     const unsigned blocks = static_cast<unsigned>(total - s0 < most ? total - s0 : most);
-    if (dtype == 0) kd_bwd_kernel<float><<<blocks, p.G, smem, stream>>>(a, s0, p, slots);
-    else if (dtype == 1) kd_bwd_kernel<__half><<<blocks, p.G, smem, stream>>>(a, s0, p, slots);
-    else kd_bwd_kernel<__nv_bfloat16><<<blocks, p.G, smem, stream>>>(a, s0, p, slots);
+    if (dtype == 0) kd_bwd_kernel<float><<<blocks, p.G + 32, smem, stream>>>(a, s0, p, slots);
+    else if (dtype == 1) kd_bwd_kernel<__half><<<blocks, p.G + 32, smem, stream>>>(a, s0, p, slots);
+    else kd_bwd_kernel<__nv_bfloat16><<<blocks, p.G + 32, smem, stream>>>(a, s0, p, slots);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
