@@ -96,6 +96,34 @@ def test_shapes(shape, dtype):
     _run(*shape, dtype, tau=2.0, masked=True, index=torch.int32, tdtype=torch.float32, seed=2)
 
 
+# more rows than there are clusters of blocks on the device, so that each takes several: rows of one block (of
+# few and of many warps) and of two, four and eight, and more entries than are loaded ahead
+MANY = [(2001, 1000, 20, torch.bfloat16), (1501, 8000, 64, torch.float16), (1000, 4100, 128, torch.float32),
+        (701, 20000, 40, torch.bfloat16), (401, 50001, 50, torch.float16), (201, 131072, 64, torch.bfloat16),
+        (151, 131075, 20, torch.float32), (601, 3001, 300, torch.bfloat16), (301, 12000, 700, torch.float16),
+        (161, 40001, 1024, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "x".join(map(str, s[:3])) + "-" + NAME[s[3]])
+def test_many_rows(shape):
+    _run(*shape, tau=0.7, masked=True, seed=21)
+
+
+@pytest.mark.parametrize("K", [9, 64, 200, 1024])
+def test_ids_that_come_again(K):
+    # every id several times, in one lane's entries and across lanes; absent ones in between
+    for T, V, dtype in ((900, 3000, torch.bfloat16), (300, 40001, torch.float32)):
+        z, ids, tl, w = _inputs(T, V, min(K, V), dtype, 22)
+        g = torch.Generator(device="cuda")
+        g.manual_seed(23)
+        some = torch.randint(-1, V + 1, (T, max(2, K // 5)), generator=g, device="cuda")
+        ids = some.gather(1, torch.randint(0, some.shape[1], (T, K), generator=g, device="cuda"))
+        ids[: T // 3] = ids[: T // 3, :1]  # one id only
+        out = _swg().distill_fwd_bwd(z, ids, tl, w)
+        _check(z, ids, tl, w, out, dtype, 1.0, out["dlogits"])
+        _check(z, ids, tl, w, None, dtype, 1.0, _swg().distill_bwd(w, z, ids, tl, out["stats"]))
+
+
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("dtype", DTYPES, ids=NAME.get)
 def test_layouts(dtype, layout):

@@ -110,6 +110,16 @@ def test_shapes(shape, dtype):
     _run(*shape, dtype, k=32, tau=0.7, masked=True, index=torch.int32, seed=2)
 
 
+# more rows than there are blocks on the device, so that each takes several: blocks of few and of many warps
+MANY = [(3001, 2048, torch.bfloat16), (1501, 8191, torch.float32), (1001, 32768, torch.float16),
+        (951, 40001, torch.bfloat16), (501, 50001, torch.float16), (401, 100000, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "x".join(map(str, s[:2])) + "-" + NAME[s[2]])
+def test_many_rows(shape):
+    _run(*shape, k=20, tau=0.7, masked=True, seed=21)
+
+
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("dtype", DTYPES, ids=NAME.get)
 def test_layouts(dtype, layout):
