@@ -1,6 +1,8 @@
 /*
  * swiglu_bwd.h -- C ABI of the GB300 (sm_103a) SwiGLU-FFN backward, SwishGrad,
- * the sibling activation gradients and the GroupNorm backward.
+ * the sibling activation gradients, the GroupNorm backward, and the row-wise
+ * operators around such a layer in a language model: layer norm, token log
+ * probabilities and distillation from a teacher's top logits.
  *
  * Operations (sources are web pages; each function cites the section it follows):
  *   [P1] "PyPTO-Gym in practice: the fused SwiGLU backward operator"

@@ -20,8 +20,8 @@
 // column a lane) took 78 us for 4000 x 4001 bf16 forward and 164 us backward, this takes 31 and 58.
 // Backward: the columns' sums of dgamma and dbeta stay in registers over all of a group's rows. The blocks'
 // sums go to the workspace and are added by a second kernel in a fixed order.
-// Measured, bf16: 16384 x 4096 with residual 87 us, 93% of the copy bandwidth; 220000 x 512 backward with dh
-// 151 us, 89%; 16384 x 8192 backward with dh 186 us, 86%.
+// Measured, bf16: 16384 x 4096 with residual 87 us, 92% of the copy bandwidth; backward with dh 220000 x 512
+// 151 us, 89%, 16384 x 4096 94 us, 85%.
 #include <mutex>
 
 #include "row_ops.cuh"
@@ -205,8 +205,8 @@ __device__ __forceinline__ void load_weights(const void* w, int j, int N, bool f
   }
 }
 
-// Sums over a group of G threads of a block (a power of two up to 256, or all); every thread gets them, added
-// in a fixed order. Groups above a warp use two alternating buffers, so that one barrier a sum is enough.
+// Sums over a group of G threads of a block (a power of two up to 32, or whole warps); every thread gets them,
+// added in a fixed order. Groups above a warp use two alternating buffers, so that one barrier a sum is enough.
 template <int kSums, bool kNarrow>  // kNarrow: G below 32 as well
 struct GroupSum {
   float* buf;  // of the group: 2 x kSums x warps
@@ -241,8 +241,7 @@ struct GroupSum {
   }
 };
 constexpr int kBlock = 256;         // threads of a block, unless a row takes more
-constexpr int kMinGroup = 8;        // threads a row
-constexpr int kMaxGroup = 512;
+constexpr int kMaxGroup = 512;      // threads a row and, with more than 64 registers each, a block
 constexpr int kMaxThreads = 1024;
 
 // ---- forward
@@ -408,7 +407,7 @@ __global__ void __launch_bounds__(kMaxThreads) ln_fwd_long_kernel(const LnFwdArg
 // dx, and with a.part the block's column sums: part[block][0][j] of dy x_hat, part[block][1][j] of dy
 template <typename T, int R, bool kRagged>
 __global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, int G) {
-  extern __shared__ float dyn[];  // with several groups a block: 2 N column sums
+  extern __shared__ __align__(16) float dyn[];  // with several groups a block: 2 N column sums
   __shared__ float smem[2 * 2 * 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int E = kElems<T>, P = kPairs<T>;
@@ -531,10 +530,27 @@ __global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, in
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if (t + i * G >= vectors) continue;
+        if constexpr (!kRagged) {  // 16 bytes at a time: 2N and the columns are multiples of 4
+#pragma unroll
+          for (int e = 0; e < P; e += 2) {
+            float4* dg = reinterpret_cast<float4*>(to + column(i) + 2 * e);
+            float4* db = reinterpret_cast<float4*>(to + N + column(i) + 2 * e);
+            float4 vg = make_float4(sg[i][e].x, sg[i][e].y, sg[i][e + 1].x, sg[i][e + 1].y);
+            float4 vb = make_float4(sb[i][e].x, sb[i][e].y, sb[i][e + 1].x, sb[i][e + 1].y);
+            if (k > 0) {
+              const float4 og = *dg, ob = *db;
+              vg = make_float4(og.x + vg.x, og.y + vg.y, og.z + vg.z, og.w + vg.w);
+              vb = make_float4(ob.x + vb.x, ob.y + vb.y, ob.z + vb.z, ob.w + vb.w);
+            }
+            *dg = vg;
+            *db = vb;
+          }
+          continue;
+        }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const int j = column(i) + e;
-          if (kRagged && (j < 0 || j >= N)) continue;
+          if (j < 0 || j >= N) continue;
           const float vg = e % 2 == 0 ? sg[i][e / 2].x : sg[i][e / 2].y;
           const float vb = e % 2 == 0 ? sb[i][e / 2].x : sb[i][e / 2].y;
           to[j] = k == 0 ? vg : to[j] + vg;
@@ -637,11 +653,10 @@ bool whole_vectors(int64_t N, int es, std::initializer_list<const void*> ptrs, s
   for (int64_t ld : lds) ok = ok && ld * es % 16 == 0;
   return ok;
 }
-// threads a row for R vectors each
+// threads a row for R vectors each: 8 or 16, or whole warps
 int group_threads(int64_t n, int R) {
-  int g = kMinGroup;
-  while (g < kBlock && static_cast<int64_t>(g) * R < n) g *= 2;
-  return static_cast<int64_t>(g) * R < n ? static_cast<int>((n + R * 32 - 1) / (R * 32)) * 32 : g;
+  const int64_t g = (n + R - 1) / R;
+  return g <= 8 ? 8 : g <= 16 ? 16 : static_cast<int>((g + 31) / 32) * 32;
 }
 
 // blocks of a persistent kernel that fit on the device at once (asked once for each device and block size)
@@ -666,7 +681,7 @@ cudaError_t blocks_that_fit(Kernel kernel, FitCache& cache, int block, size_t sm
 }
 template <typename T, int R, bool kRagged, int kMost>
 cudaError_t fwd_one(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
-  const int G = group_threads(n, R), block = G > kBlock ? G : kBlock, groups = block / G;
+  const int G = group_threads(n, R), groups = G < kBlock ? kBlock / G : 1, block = groups * G;
   int64_t blocks;
   {
     static std::mutex mu;
@@ -722,7 +737,12 @@ constexpr int64_t kLongChunks = 64;      // of them for rows too long for regist
 
 template <typename T, int R, bool kRagged>
 cudaError_t bwd_one(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {
-  const int G = group_threads(n, R), block = G > kBlock ? G : kBlock, groups = block / G;
+  const int G = group_threads(n, R);
+  // One block an SM, so that there are few rows of column sums to write and add, or smaller ones for few rows
+  // (blocks of 256 threads and sums stored element by element: 2048 x 4096 bf16 with dh 30 us, now 22).
+  int groups = kMaxGroup / G;
+  while (groups > 1 && groups * G > 32 && (a.M + groups - 1) / groups < device_sm_count()) groups = (groups + 1) / 2;
+  const int block = groups * G;
   const size_t smem = groups > 1 && a.part != nullptr ? static_cast<size_t>(2 * a.N) * sizeof(float) : 0;
   int64_t blocks;
   {
