@@ -8,10 +8,11 @@
 // All arithmetic is fp32; h, y and dx are rounded once.
 //
 // Bound by HBM: two to four tensors of M N elements are read or written, with some ten operations an
-// element. A group of 8 to 1024 threads holds a row in registers, 16-byte vectors of fixed columns, so each
-// element is read once: the variance is taken of centred values in a second pass over the registers. The
-// groups are persistent and, with two vectors or fewer a thread, load a row ahead. Rows too long for a
-// block's registers are read again (ln_fwd_long_kernel, ln_dx_long_kernel).
+// element. A group of 8 to 512 threads holds a row in registers, one or two 16-byte vectors of fixed columns
+// a thread, so each element is read once: the variance is taken of centred values in a second pass over the
+// registers. The groups are persistent and load a row ahead. Rows of more than 1024 vectors are shared by a
+// cluster of blocks, which send one another their sums (st.async, counted by an mbarrier). Only rows above
+// 8192 vectors are read again (ln_fwd_long_kernel, ln_dx_long_kernel).
 // Ragged rows, that begin or end inside 16 bytes: a thread's columns are those of a 16-byte vector of the
 // output, so that its stores are aligned. A group takes rows that lie a multiple of 16 bytes apart: it keeps
 // its columns, and the weights and the column sums that belong to them, in registers. An input with the same
@@ -23,9 +24,11 @@
 // Measured, bf16: 16384 x 4096 with residual 87 us, 92% of the copy bandwidth; backward with dh 220000 x 512
 // 151 us, 89%, 16384 x 4096 94 us, 85%.
 #include <mutex>
+#include <numeric>
+#include <type_traits>
 
-#include "row_ops.cuh"
 #include "swg_launch.h"
+#include "vocab_stream.cuh"
 
 namespace swg {
 namespace {
@@ -118,7 +121,7 @@ struct Rows {
 template <typename T, bool kRagged>
 __device__ __forceinline__ Raw load_columns(const Rows<T>& rows, int64_t r, int j, int N) {
   const T *row = rows.first + r * rows.ld, *p = row + j;
-  if (!kRagged) return ld_stream(p);
+  if constexpr (!kRagged) return ld_stream(p);
   constexpr int E = kElems<T>;
   const int shift = shift_of(p);
   if (shift == 0) {
@@ -240,24 +243,82 @@ struct GroupSum {
     }
   }
 };
+// Sums over the S blocks of a cluster, each of which comes with its own; every thread gets them, added in
+// the blocks' order. Two slots alternate: a block sends into one again only after all have sent into the
+// other, and so have read this one.
+struct ClusterSlots {
+  uint64_t come[2];
+  float2 sums[2][kMaxCluster];
+};
+template <int kSums>
+struct ClusterSum {
+  ClusterSlots& slots;
+  int S, rank, turn = 0;
+  uint32_t parity = 0;
+  Patience wait;
+  __device__ __forceinline__ ClusterSum(ClusterSlots& s, int S_) : slots(s), S(S_), rank(cluster_ctarank()) {
+    if (threadIdx.x == 0) {
+      mbar_init(&slots.come[0], 1);
+      mbar_init(&slots.come[1], 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+  }
+  __device__ __forceinline__ void operator()(float (&v)[kSums]) {
+    uint64_t* come = &slots.come[turn];
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(come, static_cast<uint32_t>(S) * sizeof(float2));
+    if (static_cast<int>(threadIdx.x) < S) send_f2(&slots.sums[turn][rank], come, threadIdx.x, v[0], v[kSums - 1]);
+    __syncwarp();
+    wait.cluster(come, parity);
+    float2 t = make_float2(0.f, 0.f);
+    for (int i = 0; i < S; ++i) {
+      t.x += slots.sums[turn][i].x;
+      t.y += slots.sums[turn][i].y;
+    }
+    v[0] = t.x;
+    if (kSums > 1) v[kSums - 1] = t.y;
+    turn ^= 1;
+    parity ^= turn == 0 ? 1u : 0u;
+  }
+  __device__ __forceinline__ void end(uint32_t* status) {  // no block leaves while another may still write to it
+    if (wait.lost && status != nullptr) atomicOr(status, kStatusTimeout);
+    cluster_arrive();
+    cluster_wait();
+  }
+};
+// groups that are blocks of their own have nothing to join
+template <int kSums>
+struct NoSum {
+  __device__ __forceinline__ NoSum(ClusterSlots&, int) {}
+  __device__ __forceinline__ void operator()(float (&)[kSums]) {}
+  __device__ __forceinline__ void end(uint32_t*) {}
+};
+template <bool kShared, int kSums>
+using SharedSum = std::conditional_t<kShared, ClusterSum<kSums>, NoSum<kSums>>;
+
 constexpr int kBlock = 256;         // threads of a block, unless a row takes more
-constexpr int kMaxGroup = 512;      // threads a row and, with more than 64 registers each, a block
-constexpr int kMaxThreads = 1024;
+constexpr int kMaxGroup = 512;      // threads of a group, and of a block
+constexpr int kMaxThreads = 1024;   // of the kernels for longest rows
 
 // ---- forward
-// kMost: threads of a block, at most. 80 registers a thread keep three blocks of 256 threads on an SM (96:
-// 97 us instead of 87 for 16384 x 4096 bf16 with residual; 64: 91 us).
-template <int R, bool kRagged, int kMost>
-constexpr int kFwdRegs = kMost > kMaxGroup ? 64 : kRagged || R > 2 ? 128 : 80;
-template <typename T, int R, bool kRagged, int kMost>
-__global__ void __maxnreg__((kFwdRegs<R, kRagged, kMost>)) ln_fwd_kernel(const LnFwdArgs a, int G) {
+// kShared: the S blocks of a cluster, of one group each, share a row. 80 registers a thread keep three blocks
+// of 256 threads on an SM (96: 97 us instead of 87 for 16384 x 4096 bf16 with residual; 64: 91 us).
+template <bool kRagged>
+constexpr int kFwdRegs = kRagged ? 128 : 80;
+template <typename T, int R, bool kRagged, bool kShared>
+__global__ void __maxnreg__(kFwdRegs<kRagged>)
+    ln_fwd_kernel(const LnFwdArgs a, int G, int S, uint32_t* status) {
   __shared__ float smem[2 * 32];
+  __shared__ ClusterSlots slots;
   constexpr int E = kElems<T>, P = kPairs<T>;
   constexpr bool kNarrow = R == 1;  // groups of less than a warp
-  const int groups = blockDim.x / G, t = threadIdx.x % G;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const int groups = kShared ? 1 : blockDim.x / G;
+  const int t = kShared ? threadIdx.x + cluster_ctarank() * R * G : threadIdx.x % G;  // vectors t, t + G, ...
+  const int64_t step = static_cast<int64_t>(kShared ? gridDim.x / S : gridDim.x) * groups;
   const int N = static_cast<int>(a.N);
-  int64_t r = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / G;
+  int64_t r = kShared ? blockIdx.x / S : static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / G;
   const int shift = kRagged ? shift_of(static_cast<const T*>(a.y) + r * a.N) : 0;
   int n = (N + shift + E - 1) / E;  // vectors of the row
   const bool add = a.residual != nullptr, f32 = a.wdtype == 0;
@@ -275,8 +336,7 @@ __global__ void __maxnreg__((kFwdRegs<R, kRagged, kMost>)) ln_fwd_kernel(const L
       if (add) w.res[i] = load_columns<T, kRagged>(res, r, column(i), N);
     }
   };
-  // the weights of ragged columns take several loads and a join: they are held, where the registers do
-  constexpr bool kHeld = kRagged && R * E <= 16 && kMost <= kMaxGroup, kAhead = R <= 2;
+  constexpr bool kHeld = kRagged;  // the weights: those of ragged columns take several loads and a join
   float2 gam[kHeld ? R : 1][P], bet[kHeld ? R : 1][P];
   auto weights = [&](int i, int to) {
     load_weights<T, kRagged>(a.gamma, column(i), N, f32, 1.0f, gam[to]);
@@ -288,14 +348,14 @@ __global__ void __maxnreg__((kFwdRegs<R, kRagged, kMost>)) ln_fwd_kernel(const L
       if (t + i * G < n) weights(i, i);
   }
   GroupSum<1, kNarrow> sum(smem, G);
+  SharedSum<kShared, 1> join(slots, S);
   Row next;
   const int64_t M = a.M + (kNarrow ? (threadIdx.x & 31) / G : 0);  // the rows of a warp's groups end together
-  if (kAhead && r < a.M) load(next, r);
+  if (r < a.M) load(next, r);
   for (; r < M; r += step) {
     if (kNarrow && r >= a.M) n = 0;
-    if (!kAhead) load(next, r);
     Row w = next;
-    if (kAhead && r + step < a.M) load(next, r + step);
+    if (r + step < a.M) load(next, r + step);
     if constexpr (kRagged) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
@@ -303,8 +363,7 @@ __global__ void __maxnreg__((kFwdRegs<R, kRagged, kMost>)) ln_fwd_kernel(const L
         if (add) clear_others<T>(w.res[i], column(i), N);
       }
     }
-    float2 s2 = pair(0.f), f[kAhead ? R : 1][P];  // the row in fp32, where the registers hold that
-    auto value = [&](int i, int e) { return kAhead ? f[kAhead ? i : 0][e] : get_pair<T>(w.x[i], e); };
+    float2 s2 = pair(0.f), f[R][P];  // the row in fp32
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
@@ -316,13 +375,13 @@ __global__ void __maxnreg__((kFwdRegs<R, kRagged, kMost>)) ln_fwd_kernel(const L
       }
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const float2 v = get_pair<T>(w.x[i], e);
-        if (kAhead) f[kAhead ? i : 0][e] = v;
-        s2 = __fadd2_rn(s2, v);
+        f[i][e] = get_pair<T>(w.x[i], e);
+        s2 = __fadd2_rn(s2, f[i][e]);
       }
     }
     float s[1] = {s2.x + s2.y};
     sum(s);
+    join(s);
     const float mu = s[0] * inv_n;
     const float2 nmu = pair(-mu);
     s2 = pair(0.f);
@@ -333,19 +392,20 @@ __global__ void __maxnreg__((kFwdRegs<R, kRagged, kMost>)) ln_fwd_kernel(const L
 #pragma unroll
         for (int e = 0; e < P; ++e) {
           const int j = column(i) + 2 * e;
-          const float2 d = __fadd2_rn(value(i, e), nmu);
+          const float2 d = __fadd2_rn(f[i][e], nmu);
           s2 = __ffma2_rn(d, make_float2(j >= 0 && j < N ? d.x : 0.0f, j >= -1 && j + 1 < N ? d.y : 0.0f), s2);
         }
         continue;
       }
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const float2 d = __fadd2_rn(value(i, e), nmu);
+        const float2 d = __fadd2_rn(f[i][e], nmu);
         s2 = __ffma2_rn(d, d, s2);
       }
     }
     s[0] = s2.x + s2.y;
     sum(s);
+    join(s);
     const float rstd = rsqrtf(fmaf(s[0], inv_n, a.eps));
     const float2 scale = pair(rstd);
     T* y = static_cast<T*>(a.y) + r * a.N;
@@ -357,7 +417,7 @@ __global__ void __maxnreg__((kFwdRegs<R, kRagged, kMost>)) ln_fwd_kernel(const L
 #pragma unroll
       for (int e = 0; e < P; ++e)
         set_pair<T>(w.x[i], e,
-                    __ffma2_rn(__fmul2_rn(__fadd2_rn(value(i, e), nmu), scale), gam[k * i][e], bet[k * i][e]));
+                    __ffma2_rn(__fmul2_rn(__fadd2_rn(f[i][e], nmu), scale), gam[k * i][e], bet[k * i][e]));
       store_columns<T, kRagged>(y, column(i), N, w.x[i]);
     }
     if (t == 0 && (!kNarrow || n > 0)) {
@@ -365,6 +425,7 @@ __global__ void __maxnreg__((kFwdRegs<R, kRagged, kMost>)) ln_fwd_kernel(const L
       a.stats[2 * r + 1] = rstd;
     }
   }
+  join.end(status);
 }
 
 // rows of any length, element by element, read three times (from L2 where a row fits)
@@ -405,38 +466,33 @@ __global__ void __launch_bounds__(kMaxThreads) ln_fwd_long_kernel(const LnFwdArg
 
 // ---- backward
 // dx, and with a.part the block's column sums: part[block][0][j] of dy x_hat, part[block][1][j] of dy
-template <typename T, int R, bool kRagged>
-__global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, int G) {
+template <typename T, int R, bool kRagged, bool kShared>
+__global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, int G, int S, uint32_t* status) {
   extern __shared__ __align__(16) float dyn[];  // with several groups a block: 2 N column sums
   __shared__ float smem[2 * 2 * 32];
+  __shared__ ClusterSlots slots;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int E = kElems<T>, P = kPairs<T>;
   constexpr bool kNarrow = R == 1;  // groups of less than a warp
-  // the registers take up to 16 columns' weights and, of up to 32 bytes a tensor, the next row
-  constexpr bool kWeights = R * E <= 16, kAhead = R <= 2;
-  const int groups = blockDim.x / G, group = threadIdx.x / G;
-  const int t = threadIdx.x % G;
+  const int groups = kShared ? 1 : blockDim.x / G, group = kShared ? 0 : threadIdx.x / G;
+  const int t = kShared ? threadIdx.x + cluster_ctarank() * R * G : threadIdx.x % G;  // vectors t, t + G, ...
+  const int64_t unit = kShared ? blockIdx.x / S : blockIdx.x;
   const int N = static_cast<int>(a.N);
-  int64_t r = static_cast<int64_t>(blockIdx.x) * groups + group;
+  int64_t r = unit * groups + group;
   const int shift = kRagged ? shift_of(static_cast<const T*>(a.dx) + r * a.N) : 0;
   const int vectors = (N + shift + E - 1) / E;
   int n = vectors;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const int64_t step = static_cast<int64_t>(kShared ? gridDim.x / S : gridDim.x) * groups;
   const float inv_n = 1.0f / static_cast<float>(a.N);
   const bool add = a.dh != nullptr, f32 = a.wdtype == 0;
   auto column = [&](int i) { return (t + i * G) * E - shift; };
-  float2 gam[kWeights ? R : 1][P], sg[R][P], sb[R][P];
+  float2 gam[R][P], sg[R][P], sb[R][P];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
 #pragma unroll
     for (int e = 0; e < P; ++e) sg[i][e] = sb[i][e] = pair(0.0f);
-    if (kWeights && t + i * G < n)
-      load_weights<T, kRagged>(a.gamma, column(i), N, f32, 1.0f, gam[kWeights ? i : 0]);
+    if (t + i * G < n) load_weights<T, kRagged>(a.gamma, column(i), N, f32, 1.0f, gam[i]);
   }
-  auto weights = [&](int i) -> float2 (&)[P] {
-    if (!kWeights) load_weights<T, kRagged>(a.gamma, column(i), N, f32, 1.0f, gam[0]);
-    return gam[kWeights ? i : 0];
-  };
   struct Row {
     Raw x[R], dy[R], dh[R];
     float mu, rstd;
@@ -454,14 +510,14 @@ __global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, in
     }
   };
   GroupSum<2, kNarrow> sum(smem, G);
+  SharedSum<kShared, 2> join(slots, S);
   Row next;
   const int64_t M = a.M + (kNarrow ? (threadIdx.x & 31) / G : 0);  // the rows of a warp's groups end together
-  if (kAhead && r < a.M) load(next, r);
+  if (r < a.M) load(next, r);
   for (; r < M; r += step) {
     if (kNarrow && r >= a.M) n = 0;
-    if (!kAhead) load(next, r);
     Row w = next;
-    if (kAhead && r + step < a.M) load(next, r + step);
+    if (r + step < a.M) load(next, r + step);
     if constexpr (kRagged) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
@@ -474,11 +530,10 @@ __global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, in
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
-      const float2 (&gi)[P] = weights(i);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         const float2 xh = __fmul2_rn(__fadd2_rn(get_pair<T>(w.x[i], e), nmu), rstd), d = get_pair<T>(w.dy[i], e);
-        const float2 g = __fmul2_rn(d, gi[e]);
+        const float2 g = __fmul2_rn(d, gam[i][e]);
         sg[i][e] = __ffma2_rn(d, xh, sg[i][e]);
         sb[i][e] = __fadd2_rn(sb[i][e], d);
         s0 = __fadd2_rn(s0, g);
@@ -487,23 +542,24 @@ __global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, in
     }
     float s[2] = {s0.x + s0.y, s1.x + s1.y};  // columns behind the row have dy = 0
     sum(s);
+    join(s);
     // dx = rstd (g - mean(g) - x_hat mean(g x_hat))
     const float2 c0 = pair(-s[0] * inv_n * w.rstd), c1 = pair(-s[1] * inv_n * w.rstd);
     T* dx = static_cast<T*>(a.dx) + r * a.N;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (t + i * G >= n) continue;
-      const float2 (&gi)[P] = weights(i);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         const float2 xh = __fmul2_rn(__fadd2_rn(get_pair<T>(w.x[i], e), nmu), rstd);
-        float2 v = __ffma2_rn(__fmul2_rn(get_pair<T>(w.dy[i], e), gi[e]), rstd, __ffma2_rn(xh, c1, c0));
+        float2 v = __ffma2_rn(__fmul2_rn(get_pair<T>(w.dy[i], e), gam[i][e]), rstd, __ffma2_rn(xh, c1, c0));
         if (add) v = __fadd2_rn(v, get_pair<T>(w.dh[i], e));
         set_pair<T>(w.x[i], e, v);
       }
       store_columns<T, kRagged>(dx, column(i), N, w.x[i]);
     }
   }
+  join.end(status);
   if (a.part == nullptr) return;
   // the block's sums, one group after the other: a fixed order. Groups of less than a warp with the same
   // columns are added first.
@@ -522,8 +578,8 @@ __global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, in
       }
     }
   }
-  const int wide = merge ? 32 : G, parts = blockDim.x / wide;
-  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
+  const int wide = merge ? 32 : G, parts = kShared ? 1 : blockDim.x / wide;
+  float* part = a.part + unit * 2 * a.N;
   float* to = parts > 1 ? dyn : part;
   for (int k = 0; k < parts; ++k) {
     if (k == static_cast<int>(threadIdx.x) / wide && static_cast<int>(threadIdx.x) % wide < G) {
@@ -545,16 +601,16 @@ __global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, in
             *dg = vg;
             *db = vb;
           }
-          continue;
-        }
+        } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int j = column(i) + e;
-          if (j < 0 || j >= N) continue;
-          const float vg = e % 2 == 0 ? sg[i][e / 2].x : sg[i][e / 2].y;
-          const float vb = e % 2 == 0 ? sb[i][e / 2].x : sb[i][e / 2].y;
-          to[j] = k == 0 ? vg : to[j] + vg;
-          to[N + j] = k == 0 ? vb : to[N + j] + vb;
+          for (int e = 0; e < E; ++e) {
+            const int j = column(i) + e;
+            if (j < 0 || j >= N) continue;
+            const float vg = e % 2 == 0 ? sg[i][e / 2].x : sg[i][e / 2].y;
+            const float vb = e % 2 == 0 ? sb[i][e / 2].x : sb[i][e / 2].y;
+            to[j] = k == 0 ? vg : to[j] + vg;
+            to[N + j] = k == 0 ? vb : to[N + j] + vb;
+          }
         }
       }
     }
@@ -659,6 +715,23 @@ int group_threads(int64_t n, int R) {
   return g <= 8 ? 8 : g <= 16 ? 16 : static_cast<int>((g + 31) / 32) * 32;
 }
 
+// a ragged group's rows are a multiple of 16 bytes apart: of so many rows
+template <typename T>
+int rows_apart(int64_t N) {
+  return kElems<T> / static_cast<int>(std::gcd(N, static_cast<int64_t>(kElems<T>)));
+}
+// Rows shared by a cluster: S blocks of G threads, two vectors each. Several small blocks an SM work on
+// while one waits for its cluster.
+struct Shared {
+  int S, G;
+};
+Shared share_row(int64_t n) {
+  const int64_t half = (n + 1) / 2;  // threads
+  const int S = static_cast<int>(half <= kMaxCluster * kBlock ? (half + kBlock - 1) / kBlock : kMaxCluster);
+  return Shared{S, static_cast<int>((half + 32 * S - 1) / (32 * S)) * 32};
+}
+constexpr int64_t kMostShared = 2 * kMaxCluster * kMaxGroup;  // vectors
+
 // blocks of a persistent kernel that fit on the device at once (asked once for each device and block size)
 struct FitCache {
   int device = -1, threads = 0, fit = 0;
@@ -679,7 +752,7 @@ cudaError_t blocks_that_fit(Kernel kernel, FitCache& cache, int block, size_t sm
   blocks = cache.fit;
   return cudaSuccess;
 }
-template <typename T, int R, bool kRagged, int kMost>
+template <typename T, int R, bool kRagged>
 cudaError_t fwd_one(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
   const int G = group_threads(n, R), groups = G < kBlock ? kBlock / G : 1, block = groups * G;
   int64_t blocks;
@@ -687,26 +760,34 @@ cudaError_t fwd_one(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
     static std::mutex mu;
     static FitCache cache;
     std::lock_guard<std::mutex> lk(mu);
-    const cudaError_t e = blocks_that_fit(ln_fwd_kernel<T, R, kRagged, kMost>, cache, block, 0, blocks);
+    const cudaError_t e = blocks_that_fit(ln_fwd_kernel<T, R, kRagged, false>, cache, block, 0, blocks);
     if (e != cudaSuccess) return e;
   }
   const int64_t most = (a.M + groups - 1) / groups;
   if (blocks > most) blocks = most;
-  else if (kRagged) blocks -= blocks % kElems<T>;  // a group's rows are a multiple of 16 bytes apart
-  ln_fwd_kernel<T, R, kRagged, kMost><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a, G);
+  else if (kRagged) blocks -= blocks % rows_apart<T>(a.N);
+  ln_fwd_kernel<T, R, kRagged, false><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a, G, 1, nullptr);
   return cudaGetLastError();
 }
-// Vectors a thread: one for rows of up to a warp; two up to 512 threads, which leaves registers to load ahead;
-// four up to 2048 vectors a row (ragged fp32) or 4096 (the others, 64 registers: 12288 bf16 columns 57 us
-// for 3000 rows, with 128 registers 68 us, by the kernel for long rows 160 us).
+template <typename T, bool kRagged>
+cudaError_t fwd_shared(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
+  static std::mutex mu;
+  static StreamCache cache;
+  std::lock_guard<std::mutex> lk(mu);
+  const Shared p = share_row(n);
+  return launch_stream(ln_fwd_kernel<T, 2, kRagged, true>, cache, p.G, 0, a.M, p.S, false,
+                       kRagged ? rows_apart<T>(a.N) : 1, stream, a, p.G, p.S, status_word_ptr());
+}
+// Vectors a thread: one for rows of up to a warp, else two. Rows of more than 1024 vectors are shared by a
+// cluster: 3000 x 12288 bf16 with residual 70 us, 88 by a block with four vectors a thread; backward with dh
+// 76 us against 117, and 3000 x 16384 fp32 139 us against 510 by the kernels for longest rows. A shared row
+// below that costs more than it gives (8192 x 6144 bf16, backward with dh: 109 us instead of 83).
 template <typename T, bool kRagged>
 cudaError_t fwd_any(const LnFwdArgs& a, cudaStream_t stream) {
   const int64_t n = (a.N + (kRagged ? 2 * kElems<T> - 2 : 0)) / kElems<T>;
-  if (n <= 32) return fwd_one<T, 1, kRagged, kMaxGroup>(a, n, stream);
-  if (n <= 2 * kMaxGroup) return fwd_one<T, 2, kRagged, kMaxGroup>(a, n, stream);
-  if constexpr (kRagged && sizeof(T) == 4)
-    if (n <= 4 * kMaxGroup) return fwd_one<T, 4, kRagged, kMaxGroup>(a, n, stream);
-  if (n <= 4 * kMaxThreads) return fwd_one<T, 4, kRagged, kMaxThreads>(a, n, stream);
+  if (n <= 32) return fwd_one<T, 1, kRagged>(a, n, stream);
+  if (n <= 2 * kMaxGroup) return fwd_one<T, 2, kRagged>(a, n, stream);
+  if (n <= kMostShared) return fwd_shared<T, kRagged>(a, n, stream);
   const unsigned grid = static_cast<unsigned>(a.M < 65536 ? a.M : 65536);
   ln_fwd_long_kernel<T><<<grid, kMaxThreads, 0, stream>>>(a);
   return cudaGetLastError();
@@ -749,14 +830,14 @@ cudaError_t bwd_one(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {
     static std::mutex mu;
     static FitCache cache;
     std::lock_guard<std::mutex> lk(mu);
-    const cudaError_t e = blocks_that_fit(ln_bwd_kernel<T, R, kRagged>, cache, block, smem, blocks);
+    const cudaError_t e = blocks_that_fit(ln_bwd_kernel<T, R, kRagged, false>, cache, block, smem, blocks);
     if (e != cudaSuccess) return e;
   }
   const int64_t most = (a.M + groups - 1) / groups;
   if (blocks > kMaxBlocks) blocks = kMaxBlocks;
   if (blocks > most) blocks = most;
-  else if (kRagged) blocks -= blocks % kElems<T>;  // a group's rows are a multiple of 16 bytes apart
-  ln_bwd_kernel<T, R, kRagged><<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, G);
+  else if (kRagged) blocks -= blocks % rows_apart<T>(a.N);
+  ln_bwd_kernel<T, R, kRagged, false><<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, G, 1, nullptr);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.part == nullptr) return e;
   return launch_reduce(a, blocks, stream);
@@ -773,14 +854,27 @@ cudaError_t bwd_long(const LnBwdArgs& a, cudaStream_t stream) {
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_reduce(a, chunks, stream);
 }
-// Vectors a thread as forward, but up to 512 threads: the column sums take 128 registers (3000 rows of 12288
-// bf16 columns: 113 us; by the kernels for long rows 312 us).
+template <typename T, bool kRagged>
+cudaError_t bwd_shared(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {
+  int64_t rows;
+  {
+    static std::mutex mu;
+    static StreamCache cache;
+    std::lock_guard<std::mutex> lk(mu);
+    const Shared p = share_row(n);
+    const cudaError_t e = launch_stream(ln_bwd_kernel<T, 2, kRagged, true>, cache, p.G, 0, a.M, p.S, false,
+                                        kRagged ? rows_apart<T>(a.N) : 1, stream, a, p.G, p.S, status_word_ptr());
+    if (e != cudaSuccess) return e;
+    rows = cache.launched;
+  }
+  return a.part == nullptr ? cudaSuccess : launch_reduce(a, rows, stream);
+}
 template <typename T, bool kRagged>
 cudaError_t bwd_any(const LnBwdArgs& a, cudaStream_t stream) {
   const int64_t n = (a.N + (kRagged ? 2 * kElems<T> - 2 : 0)) / kElems<T>;
   if (n <= 32) return bwd_one<T, 1, kRagged>(a, n, stream);
   if (n <= 2 * kMaxGroup) return bwd_one<T, 2, kRagged>(a, n, stream);
-  if (n <= 4 * kMaxGroup) return bwd_one<T, 4, kRagged>(a, n, stream);
+  if (n <= kMostShared) return bwd_shared<T, kRagged>(a, n, stream);
   return bwd_long<T>(a, stream);
 }
 template <typename T>

@@ -259,15 +259,16 @@ __device__ __forceinline__ void send_u64(const uint64_t* to, const uint64_t* bar
 }  // namespace row
 
 // A persistent launch: as many clusters as fit on the device at once, at most one a row (`all`: one for
-// every row, however many fit). The occupancy of a (kernel, cluster size, shared memory) is asked once for
-// each device.
+// every row, however many fit; multiple: where rows are shared out to fewer clusters, their number is one of
+// it). The occupancy of a (kernel, cluster size, block, shared memory) is asked once for each device.
 struct StreamCache {
-  int device = -1, S = 0, clusters = 0;
+  int device = -1, S = 0, threads = 0, clusters = 0;
   size_t smem = 0;
+  int64_t launched = 0;  // clusters of the last launch
 };
 template <typename Kernel, typename... Args>
 cudaError_t launch_stream(Kernel kernel, StreamCache& cache, int threads, size_t smem, int64_t rows, int S,
-                          bool all, cudaStream_t stream, const Args&... args) {
+                          bool all, int multiple, cudaStream_t stream, const Args&... args) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -282,7 +283,7 @@ cudaError_t launch_stream(Kernel kernel, StreamCache& cache, int threads, size_t
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cache.device != dev || cache.S != S || cache.smem != smem) {
+  if (cache.device != dev || cache.S != S || cache.threads != threads || cache.smem != smem) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(S));
@@ -290,9 +291,11 @@ cudaError_t launch_stream(Kernel kernel, StreamCache& cache, int threads, size_t
     e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorLaunchOutOfResources;
-    cache = StreamCache{dev, S, n, smem};
+    cache = StreamCache{dev, S, threads, n, smem};
   }
-  const int64_t clusters = all || rows < cache.clusters ? rows : cache.clusters;
+  const int64_t fit = cache.clusters > multiple ? cache.clusters / multiple * multiple : cache.clusters;
+  const int64_t clusters = all || rows < fit ? rows : fit;
+  cache.launched = clusters;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * S));
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
