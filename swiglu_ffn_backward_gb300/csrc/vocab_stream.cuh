@@ -75,7 +75,8 @@ struct Place {
   }
 };
 
-// The producer warp: all rows of the block's cluster, row r's share at `rank` of S.
+// The producer warp: all rows of the block's cluster, row r's share at `rank` of S. It issues no more copies
+// once a wait has run out, and ends when the copies it has issued have landed.
 template <typename T, int W, int N>
 __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int64_t V, int64_t first, int64_t rows,
                                              int64_t step, int per, int rank, unsigned char* buf, int stages,
@@ -98,7 +99,8 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
   };
   Place p;
   T mine = edge(first);
-  for (int64_t r = first; r < rows; r += step) {
+  bool go = true;
+  for (int64_t r = first; r < rows && go; r += step) {
     const T* z = base + r * ld;
     const Share sh = share_of(z, V, per, rank);
     const T ahead = edge(r + step);
@@ -108,6 +110,8 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
       const int end = min(sh.end, c + kStageVecs);
       unsigned char* to = buf + p.stage * kStageBytes;
       wait(&ring.empty[p.stage], p.parity ^ 1u);
+      go = !__any_sync(0xffffffffu, wait.lost);
+      if (!go) break;
       const int w0 = max(c, whole0), w1 = min(end, whole1);
       // a partial vector's elements, lane by lane
       const bool head = c == sh.begin && e0 < 0, tail = end == sh.end && e1 > V;
@@ -126,6 +130,8 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
     }
     mine = ahead;
   }
+  for (int i = 0; i < stages; ++i)  // the last use of every stage; one that has had none is done
+    if (!mbar_wait(&ring.full[i], i < p.stage ? p.parity : p.parity ^ 1u)) wait.lost = true;
 }
 
 // a computing thread's four vectors of a stage that holds n; -inf past them
