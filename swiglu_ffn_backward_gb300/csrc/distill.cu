@@ -71,12 +71,15 @@ __device__ __forceinline__ EntryArrays entry_arrays(unsigned char* at, int K, in
   int* p = reinterpret_cast<int*>(at) + b * 3 * K;
   return EntryArrays{p, reinterpret_cast<float*>(p + K), reinterpret_cast<float*>(p + 2 * K)};
 }
-// slots of the table of ids: a power of two, twice the entries at least
+// slots of the table of ids: a power of two, eight times the entries, or twice where they are many (an entry's
+// search takes a few hundred cycles a step, and the longest one of a warp counts)
 __host__ __device__ __forceinline__ int table_slots(int K) {
   int n = 64;
-  while (n < 2 * K) n *= 2;
+  while (n < (K <= 128 ? 8 : 2) * K) n *= 2;
   return n;
 }
+// the table behind one row's entries, in words from them (16-byte aligned)
+__host__ __device__ constexpr int table_at(int K) { return (3 * K + 3) / 4 * 4; }
 __host__ __device__ constexpr size_t entry_bytes(int K) { return static_cast<size_t>(kSlots) * 3 * 4 * K; }
 
 // A teacher warp takes the entries of row after row. The first kAhead of a row are loaded two rows ahead,
@@ -176,7 +179,7 @@ __device__ __forceinline__ uint32_t first_entries(const KdArgs& a, const EntryAr
                                                   int64_t e0, int64_t e1, uint32_t& shared) {
   constexpr int kAgain = static_cast<int>(0x80000000u);  // an id that has come again; ids are below 2^31 - 1
   const int lane = threadIdx.x & 31;
-  for (int i = lane; i < slots; i += 32) table[i] = -1;
+  for (int i = lane; i < slots / 4; i += 32) reinterpret_cast<int4*>(table)[i] = make_int4(-1, -1, -1, -1);
   __syncwarp();
   auto place = [&](int id) { return static_cast<int>((static_cast<uint32_t>(id) * 2654435761u) >> 16) & (slots - 1); };
   uint32_t mine = 0;
@@ -494,7 +497,7 @@ template <typename T>
 __global__ void __launch_bounds__(kRowThreads + 32, 4)
     kd_bwd_kernel(const KdArgs a, int64_t share0, Groups p, int slots) {
   constexpr int E = Traits<T>::E;
-  extern __shared__ __align__(16) unsigned char dyn[];
+  extern __shared__ __align__(128) unsigned char dyn[];
   __shared__ float sq_all;
   const int tid = threadIdx.x;
   const int64_t at = share0 + blockIdx.x, r = at / p.S;
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, 4)
     if (tid == p.G) sq_all = sq;
     block_sync();
     uint32_t shared;
-    const uint32_t mine = first_entries(a, n, reinterpret_cast<int*>(dyn) + 3 * a.K, slots, e0, e1, shared);
+    const uint32_t mine = first_entries(a, n, reinterpret_cast<int*>(dyn) + table_at(a.K), slots, e0, e1, shared);
     block_sync();
     store_sparse<T>(a, gradient(sq), n, mine, shared, out);
     return;
@@ -552,7 +555,7 @@ cudaError_t launch_bwd(const KdArgs& a, int dtype, int64_t vectors, int sms, cud
   Groups p = row_groups(a.T, vectors, sms);
   if (p.G < 64) p.G = 64;
   const int slots = table_slots(a.K);
-  const size_t smem = static_cast<size_t>(3 * a.K + slots) * sizeof(int);  // 20 KB at most
+  const size_t smem = static_cast<size_t>(table_at(a.K) + slots) * sizeof(int);  // 20 KB at most
   const int64_t total = a.T * p.S, most = int64_t(1) << 30;
   for (int64_t s0 = 0; s0 < total; s0 += most) {
     const unsigned blocks = static_cast<unsigned>(total - s0 < most ? total - s0 : most);
@@ -570,13 +573,14 @@ cudaError_t launch_bwd(const KdArgs& a, int dtype, int64_t vectors, int sms, cud
 cudaError_t launch_distill(const KdArgs& a, bool forward, bool backward, int dtype, cudaStream_t stream) {
   const int sms = device_sm_count();
   const int64_t vectors = row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2);
-  // Blocks of four computing warps, three an SM, take short rows (up to 1024 vectors, 16 KB), blocks of 16
-  // long ones: bf16 logits with 64 entries, loss and gradient, 8192 columns 139 us against 285 us with 16
-  // warps (16384 rows), 32768 columns (4096 rows, two blocks of four a row) 144 us against 106 us. Without a
-  // gradient four warps are as fast for long rows too, once each of those blocks has two rows.
+  // Blocks of four computing warps, three an SM, take rows of up to 32 KB, one or two blocks a row, blocks of 16
+  // longer ones: bf16 logits with 64 entries, loss and gradient, 8192 columns 126 us against 291 us with 16
+  // warps (16384 rows), 16384 columns 122 against 157 us (8192 rows), 32768 columns (4096 rows, four blocks
+  // a row) 121 us against 98. Without a gradient four warps are as fast for long rows too, once each of those
+  // blocks has two rows.
   constexpr int64_t big = kShareStages * Shape<16>::kStageVecs, small = kShareStages * Shape<4>::kStageVecs;
   // the row's shares have to stay in the rings for the gradient: a longer row is read twice
-  if (forward && backward && vectors <= small)
+  if (forward && backward && vectors <= 2 * small)
     return launch_fwd_any<true, 4>(a, dtype, split_row(a.T, vectors, small, sms), stream);
   if (forward && backward && vectors <= kMaxCluster * big)
     return launch_fwd_any<true, 16>(a, dtype, split_row(a.T, vectors, big, sms), stream);
