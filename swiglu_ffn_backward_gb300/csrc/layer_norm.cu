@@ -12,7 +12,7 @@
 // a thread, so each element is read once: the variance is taken of centred values in a second pass over the
 // registers. The groups are persistent and load a row ahead. Rows of more than 1024 vectors are shared by a
 // cluster of blocks, which send one another their sums (st.async, counted by an mbarrier). Only rows above
-// 8192 vectors are read again (ln_fwd_long_kernel, ln_dx_long_kernel).
+// 8192 vectors (ragged ones forward: 4096) are read again (ln_fwd_long_kernel, ln_dx_long_kernel).
 // Ragged rows, that begin or end inside 16 bytes: a thread's columns are those of a 16-byte vector of the
 // output, so that its stores are aligned. A group takes rows that lie a multiple of 16 bytes apart: it keeps
 // its columns, and the weights and the column sums that belong to them, in registers. An input with the same
@@ -781,13 +781,15 @@ cudaError_t fwd_shared(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
 // Vectors a thread: one for rows of up to a warp, else two. Rows of more than 1024 vectors are shared by a
 // cluster: 3000 x 12288 bf16 with residual 70 us, 88 by a block with four vectors a thread; backward with dh
 // 76 us against 117, and 3000 x 16384 fp32 139 us against 510 by the kernels for longest rows. A shared row
-// below that costs more than it gives (8192 x 6144 bf16, backward with dh: 109 us instead of 83).
+// below that costs more than it gives (8192 x 6144 bf16, backward with dh: 109 us instead of 83), and so does
+// forward a ragged one of more than 256 threads a block (3000 x 16383 fp32 with residual: 514 us, read again
+// 277; backward with dh 443 against 502).
 template <typename T, bool kRagged>
 cudaError_t fwd_any(const LnFwdArgs& a, cudaStream_t stream) {
   const int64_t n = (a.N + (kRagged ? 2 * kElems<T> - 2 : 0)) / kElems<T>;
   if (n <= 32) return fwd_one<T, 1, kRagged>(a, n, stream);
   if (n <= 2 * kMaxGroup) return fwd_one<T, 2, kRagged>(a, n, stream);
-  if (n <= kMostShared) return fwd_shared<T, kRagged>(a, n, stream);
+  if (n <= (kRagged ? kMostShared / 2 : kMostShared)) return fwd_shared<T, kRagged>(a, n, stream);
   const unsigned grid = static_cast<unsigned>(a.M < 65536 ? a.M : 65536);
   ln_fwd_long_kernel<T><<<grid, kMaxThreads, 0, stream>>>(a);
   return cudaGetLastError();

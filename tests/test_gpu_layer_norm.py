@@ -128,7 +128,7 @@ def test_ragged_rows(shape, dtype):
 # rows that a cluster of two to eight blocks shares, several rows each; the last one is too long for that
 @pytest.mark.parametrize("dtype", DTYPES, ids=NAME.get)
 @pytest.mark.parametrize("shape", [(601, 8200), (401, 12288), (261, 20480), (171, 32768), (91, 65536), (61, 32777),
-                                   (20, 70001)], ids=lambda s: "x".join(map(str, s)))
+                                   (101, 32761), (51, 16377), (20, 70001)], ids=lambda s: "x".join(map(str, s)))
 def test_shared_rows(shape, dtype):
     _run(*shape, dtype, torch.float32, residual=True, dh=True, seed=17)
     _run(*shape, dtype, dtype, seed=18, layout="padded")
