@@ -263,6 +263,23 @@ def test_empty():
     assert swg.layer_norm_fwd(torch.empty((3, 0), device="cuda"))["y"].shape == (3, 0)
 
 
+@pytest.mark.parametrize("M,N", [(264000, 8192), (2150000, 1001)], ids=["whole", "ragged"])
+def test_offsets_past_32_bits(M, N):
+    swg = _swg()
+    assert M * N > 2 ** 31
+    g = torch.Generator(device="cuda")
+    g.manual_seed(12)
+    x = torch.empty((M, N), dtype=torch.bfloat16, device="cuda").normal_(0, 1, generator=g)
+    t = _inputs(1, N, torch.bfloat16, torch.float32, 13)
+    out = swg.layer_norm_fwd(x, t["gamma"], t["beta"], eps=EPS, residual=x)
+    dx = swg.layer_norm_bwd(x, out["h"], out["stats"], gamma=t["gamma"], params=False)[0]
+    rows = [0, 1, M // 2, M - 2, M - 1]
+    few = dict(x=x[rows], residual=x[rows], dy=x[rows], gamma=t["gamma"], beta=t["beta"])
+    small = {k: v[rows] for k, v in out.items()}
+    _check_fwd(few, small, torch.bfloat16, residual=True)
+    _check_bwd(few, small["h"], small["stats"], (dx[rows], None, None), torch.bfloat16, torch.float32)
+
+
 def test_on_another_stream():
     swg = _swg()
     t = _inputs(2000, 1024, torch.bfloat16, torch.float32, 10)
