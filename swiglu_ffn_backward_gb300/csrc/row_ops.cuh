@@ -50,32 +50,18 @@ __device__ __forceinline__ float warp_max(float v) {  // one instruction, in pla
   asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
   return v;
 }
-__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = u > v ? u : v;
-  }
-  return v;
-}
 
-// Block-wide reductions: every thread gets the result, added (or compared) in a fixed order. `buf`
-// holds one value a warp; the barriers around it let a caller use it again at once.
-template <typename V, typename F>
-__device__ __forceinline__ V block_reduce(V v, V* buf, F combine) {
+// The block's sum: every thread gets it, added in a fixed order. `buf` holds one value a warp; the barriers
+// around it let a caller use it again at once.
+__device__ __forceinline__ float block_sum(float v, float* buf) {
   const int warps = static_cast<int>(blockDim.x + 31) >> 5;
+  v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
   __syncthreads();
-  V r = buf[0];
-  for (int w = 1; w < warps; ++w) r = combine(r, buf[w]);
+  float r = buf[0];
+  for (int w = 1; w < warps; ++w) r += buf[w];
   __syncthreads();
   return r;
-}
-__device__ __forceinline__ float block_sum(float v, float* buf) {
-  return block_reduce(warp_sum(v), buf, [](float a, float b) { return a + b; });
-}
-__device__ __forceinline__ float block_max(float v, float* buf) {
-  return block_reduce(warp_max(v), buf, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // The order of a row's alternatives: larger logits first, equal ones by the lower index; a NaN counts

@@ -13,6 +13,9 @@
 // the sums, and select the alternatives from the threads' bests. The 32 lane columns' bests have a k-th
 // largest, which at least k logits reach; the few threads with a best at or above it (about k + k^2 / 64)
 // are looked through again (their runs come from L2), and the logits found are ranked against one another.
+// Measured, bf16 with the 20 best: 4096 x 131072 170 us, 95% of the copy bandwidth; 4096 x 32768 65 us, 61% (the
+// computing warps' work on a row and the turn between rows: the schedulers issue in 60% of the cycles); one
+// row of 131072 fp32 12.5 us, shared by eight blocks.
 #include <mutex>
 
 #include "swg_launch.h"
@@ -418,7 +421,9 @@ cudaError_t launch_fwd_any(const TlpFwdArgs& a, int dtype, Split split, cudaStre
                       : launch_fwd<__nv_bfloat16, W>(a, split, stream);
 }
 
-// Backward: bound by HBM (V elements read and written a row); no block needs another's results.
+// Backward: bound by HBM (V elements read and written a row); no block needs another's results, so groups of
+// 32 to 256 threads take shares of rows in registers, read once and written once. Measured with the entropy's
+// gradient: 4096 x 65536 bf16 158 us, 102% of the copy bandwidth, 4096 x 50001 136 us, 90%.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads, 4) tlp_bwd_kernel(const TlpBwdArgs a, int64_t group0, Groups p) {
   constexpr int E = Traits<T>::E;

@@ -13,7 +13,6 @@ namespace swg {
 namespace row {
 
 constexpr int kRowThreads = 256;
-constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kVecs = 8;                          // 16-byte vectors a thread holds: 32 registers
 constexpr int kMaxCluster = 8;                    // portable cluster size
 
@@ -135,8 +134,9 @@ __device__ __forceinline__ float vec_max4<__half>(const Vec (&v)[4]) {
 }
 template <>
 __device__ __forceinline__ float vec_max4<__nv_bfloat16>(const Vec (&v)[4]) {
-  return vec_max<__nv_bfloat16>(larger_halves<__nv_bfloat16, __nv_bfloat162>(
-      larger_halves<__nv_bfloat16, __nv_bfloat162>(v[0], v[1]), larger_halves<__nv_bfloat16, __nv_bfloat162>(v[2], v[3])));
+  const Vec lo = larger_halves<__nv_bfloat16, __nv_bfloat162>(v[0], v[1]);
+  const Vec hi = larger_halves<__nv_bfloat16, __nv_bfloat162>(v[2], v[3]);
+  return vec_max<__nv_bfloat16>(larger_halves<__nv_bfloat16, __nv_bfloat162>(lo, hi));
 }
 
 // bit i: element i is at or above `least` (which is not NaN; a NaN element is not)
