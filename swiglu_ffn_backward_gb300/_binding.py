@@ -9,6 +9,7 @@ library is missing the import of this module raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -629,29 +630,62 @@ def _new(x):
     return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
-def _vector(t, name, n, dtypes, device):
-    """A dense tensor of n elements of one of `dtypes` on `device` (None stays None)."""
+def _same_order(shape, want, lead):
+    """Whether a dense tensor of `shape` has the elements of one of shape `want` in their order: the same
+    shape up to dimensions of one, or with the leading dimensions, or all, counted in one. lead: the leading
+    dimensions as the caller's rows have them (all of `want` when None); where they are one, the tensor's may
+    be several."""
+    if math.prod(shape) != math.prod(want):
+        return False
+    if len(shape) <= 1:
+        return True
+    cut = len(shape)
+    if lead is None:
+        lead = want
+    else:
+        cut -= 1
+        if shape[cut] != want[-1]:
+            return False
+    rows, given = [d for d in shape[:cut] if d != 1], [d for d in lead if d != 1]
+    return rows == given or len(rows) <= 1 or len(given) <= 1
+
+
+def _vector(t, name, want, dtypes, device, lead=None):
+    """A dense tensor of one of `dtypes` on `device` with the elements of one of shape `want` in their order
+    (None stays None). lead: as in _same_order."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes or t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements of {' or '.join(map(str, dtypes))}, "
-                         f"got {t.numel()} of {t.dtype}")
+    shape = t.shape
+    if t.dtype not in dtypes or (shape != want and not _same_order(shape, want, lead)):
+        raise ValueError(f"{name} must have the shape {tuple(want)} and be of {' or '.join(map(str, dtypes))}, "
+                         f"got {tuple(shape)} of {t.dtype}")
     if t.device != device:
         raise ValueError(f"all tensors must be on one device: got {device} and {t.device}")
     return t if t.is_contiguous() else t.contiguous()
 
 
+def _row_out(t, want, dtype, device, name, lead=None):
+    """An output of shape `want`: allocated when None, else the caller's, checked; lead as in _same_order."""
+    if t is None:
+        return torch.empty(want, dtype=dtype, device=device)
+    t = _out(t, want, dtype, device, name)
+    if t.shape != want and not _same_order(t.shape, want, lead):
+        raise ValueError(f"{name} must have the shape {tuple(want)}, got {tuple(t.shape)}")
+    return t
+
+
 _F32 = (torch.float32,)
 _INDEX = (torch.int64, torch.int32)
+_FLOAT = tuple(_DTYPE)
 
 
 def _norm_weights(gamma, beta, N, x):
     """gamma and beta (either None) checked, with their common dtype code."""
     allowed = (x.dtype, torch.float32)
-    gamma = _vector(gamma, "gamma", N, allowed, x.device)
-    beta = _vector(beta, "beta", N, allowed if gamma is None else (gamma.dtype,), x.device)
+    gamma = _vector(gamma, "gamma", (N,), allowed, x.device)
+    beta = _vector(beta, "beta", (N,), allowed if gamma is None else (gamma.dtype,), x.device)
     w = gamma if gamma is not None else beta
     return gamma, beta, w.dtype if w is not None else x.dtype
 
@@ -676,10 +710,10 @@ def layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, o
             out["h"] = h = _new(x)
     else:
         out, h = dict(out), None
-        out["y"] = y = _out(out.get("y"), shape, xt.dtype, dev, "y")
-        out["stats"] = st = _out(out.get("stats"), (M, 2), torch.float32, dev, "stats")
+        out["y"] = y = _row_out(out.get("y"), shape, xt.dtype, dev, "y", shape[:-1])
+        out["stats"] = st = _row_out(out.get("stats"), (M, 2), torch.float32, dev, "stats", shape[:-1])
         if res is not None:
-            out["h"] = h = _out(out.get("h"), shape, xt.dtype, dev, "h")
+            out["h"] = h = _row_out(out.get("h"), shape, xt.dtype, dev, "h", shape[:-1])
     _run("layer_norm_fwd", lib.layer_norm_fwd, dev, xt.data_ptr(), _ptr(res), _ptr(gamma), _ptr(beta), _ptr(h),
          y.data_ptr(), st.data_ptr(), M, N, ldx, ldr, eps, code, _DTYPE[wdtype])
     return out
@@ -705,11 +739,11 @@ def layer_norm_bwd(dy, x, stats, gamma=None, dh=None, params: bool = True, dx=No
     dyt, lddy = _like_rows(dy, "dy", xt, ldx, shape)
     dht, lddh = _like_rows(dh, "dh", xt, ldx, shape)
     dev = xt.device
-    stats = _vector(stats, "stats", 2 * M, _F32, dev)
+    stats = _vector(stats, "stats", (M, 2), _F32, dev, shape[:-1])
     if stats is None:
         raise TypeError("stats must be a CUDA tensor")
     gamma, _, wdtype = _norm_weights(gamma, None, N, xt)
-    dx = _new(x) if dx is None else _out(dx, shape, xt.dtype, dev, "dx")
+    dx = _new(x) if dx is None else _row_out(dx, shape, xt.dtype, dev, "dx", shape[:-1])
     ws = None
     if params:
         dgamma = _out(dgamma, (N,), wdtype, dev, "dgamma")
@@ -745,24 +779,25 @@ def token_logprobs_fwd(logits, targets=None, top_k: int = 0, temperature: float 
     target is ignore_index, NaN for another target outside the vocabulary), entropy [...], stats [T, 2]
     for the backward, and with top_k (at most 32) top_logp and top_idx [..., top_k], the largest logits
     in descending order, equal ones by the lower index. targets: int64 or int32 of logits' leading
-    shape. `out` may supply any of the outputs; stream: the stream to run on."""
+    shape (here as in the other calls, a tensor of values by row may also count the rows in one dimension).
+    `out` may supply any of the outputs; stream: the stream to run on."""
     if stream is not None:
         return _on_stream(stream, token_logprobs_fwd, logits, targets, top_k=top_k, temperature=temperature,
                           ignore_index=ignore_index, out=out)
     lead = logits.shape[:-1] if isinstance(logits, torch.Tensor) else None
     z, T, V, ld, code = _row_tensor(logits, "logits")
     dev = z.device
-    targets = _vector(targets, "targets", T, _INDEX, dev)
+    targets = _vector(targets, "targets", lead, _INDEX, dev)
     given, f32 = out or {}, torch.float32
-    entropy = _out(given.get("entropy"), lead, f32, dev, "entropy")
-    out = {"entropy": entropy, "stats": _out(given.get("stats"), (T, 2), f32, dev, "stats")}
+    entropy = _row_out(given.get("entropy"), lead, f32, dev, "entropy")
+    out = {"entropy": entropy, "stats": _row_out(given.get("stats"), (T, 2), f32, dev, "stats", lead)}
     logp = top_logp = top_idx = None
     if targets is not None:
         logp = given.get("logp")
-        out["logp"] = logp = torch.empty_like(entropy) if logp is None else _out(logp, lead, f32, dev, "logp")
+        out["logp"] = logp = torch.empty_like(entropy) if logp is None else _row_out(logp, lead, f32, dev, "logp")
     if top_k > 0:
-        out["top_logp"] = top_logp = _out(given.get("top_logp"), (*lead, top_k), f32, dev, "top_logp")
-        out["top_idx"] = top_idx = _out(given.get("top_idx"), (*lead, top_k), torch.int64, dev, "top_idx")
+        out["top_logp"] = top_logp = _row_out(given.get("top_logp"), (*lead, top_k), f32, dev, "top_logp", lead)
+        out["top_idx"] = top_idx = _row_out(given.get("top_idx"), (*lead, top_k), torch.int64, dev, "top_idx", lead)
     _run("token_logprobs_fwd", lib.token_logprobs_fwd, dev, z.data_ptr(), _ptr(targets), _ptr(logp),
          entropy.data_ptr(), out["stats"].data_ptr(), _ptr(top_logp), _ptr(top_idx), T, V, ld, top_k,
          temperature, ignore_index, code, _itype(targets))
@@ -783,11 +818,11 @@ def token_logprobs_bwd(dlogp, logits, targets, stats, dentropy=None, entropy=Non
                           temperature=temperature, ignore_index=ignore_index, dlogits=dlogits)
     shape = logits.shape if isinstance(logits, torch.Tensor) else None
     z, T, V, ld, code = _row_tensor(logits, "logits")
-    dev = z.device
-    targets = _vector(targets, "targets", T, _INDEX, dev)
-    dlogp = _vector(dlogp, "dlogp", T, _F32, dev)
-    dentropy, entropy = _vector(dentropy, "dentropy", T, _F32, dev), _vector(entropy, "entropy", T, _F32, dev)
-    stats = _vector(stats, "stats", 2 * T, _F32, dev)
+    dev, lead = z.device, shape[:-1]
+    targets = _vector(targets, "targets", lead, _INDEX, dev)
+    dlogp = _vector(dlogp, "dlogp", lead, _F32, dev)
+    dentropy, entropy = _vector(dentropy, "dentropy", lead, _F32, dev), _vector(entropy, "entropy", lead, _F32, dev)
+    stats = _vector(stats, "stats", (T, 2), _F32, dev, lead)
     dlogits, ldo = _dlogits(dlogits, shape, z, T, V)
     _run("token_logprobs_bwd", lib.token_logprobs_bwd, dev, _ptr(dlogp), z.data_ptr(), _ptr(targets), _ptr(stats),
          _ptr(dentropy), _ptr(entropy), dlogits.data_ptr(), T, V, ld, ldo, temperature, ignore_index, code,
@@ -798,14 +833,15 @@ def token_logprobs_bwd(dlogp, logits, targets, stats, dentropy=None, entropy=Non
 def _distill_inputs(logits, teacher_ids, teacher_logits):
     shape = logits.shape if isinstance(logits, torch.Tensor) else None
     z, T, V, ld, code = _row_tensor(logits, "logits")
-    if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() < 1 or teacher_ids.shape[:-1] != shape[:-1]:
-        raise ValueError(f"teacher_ids must have the shape {tuple(shape[:-1])} + (K,)")
+    lead = shape[:-1]
+    if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() < 1 or teacher_ids.shape[:-1] != lead:
+        raise ValueError(f"teacher_ids must have the shape {tuple(lead)} + (K,)")
     K = teacher_ids.shape[-1]
-    ids = _vector(teacher_ids, "teacher_ids", T * K, _INDEX, z.device)
-    tl = _vector(teacher_logits, "teacher_logits", T * K, tuple(_DTYPE), z.device)
+    ids = _vector(teacher_ids, "teacher_ids", teacher_ids.shape, _INDEX, z.device)
+    tl = _vector(teacher_logits, "teacher_logits", teacher_ids.shape, _FLOAT, z.device, lead)
     if tl is None:
         raise TypeError("teacher_logits must be a CUDA tensor")
-    return shape, z, T, V, ld, code, ids, tl, K
+    return shape, lead, z, T, V, ld, code, ids, tl, K
 
 
 def distill_fwd(logits, teacher_ids, teacher_logits, temperature: float = 1.0, out: dict | None = None,
@@ -816,10 +852,10 @@ def distill_fwd(logits, teacher_ids, teacher_logits, temperature: float = 1.0, o
     the entries and p the student's, both at `temperature`, and stats [T, 2] for the backward."""
     if stream is not None:
         return _on_stream(stream, distill_fwd, logits, teacher_ids, teacher_logits, temperature=temperature, out=out)
-    shape, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
+    shape, lead, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
     given = out or {}
-    out = {"loss": _out(given.get("loss"), shape[:-1], torch.float32, z.device, "loss"),
-           "stats": _out(given.get("stats"), (T, 2), torch.float32, z.device, "stats")}
+    out = {"loss": _row_out(given.get("loss"), lead, torch.float32, z.device, "loss"),
+           "stats": _row_out(given.get("stats"), (T, 2), torch.float32, z.device, "stats", lead)}
     _run("distill_fwd", lib.distill_fwd, z.device, z.data_ptr(), ids.data_ptr(), tl.data_ptr(),
          out["loss"].data_ptr(), out["stats"].data_ptr(), T, V, ld, K, temperature, code, _DTYPE[tl.dtype], _itype(ids))
     return out
@@ -832,8 +868,9 @@ def distill_bwd(weight, logits, teacher_ids, teacher_logits, stats, temperature:
     if stream is not None:
         return _on_stream(stream, distill_bwd, weight, logits, teacher_ids, teacher_logits, stats,
                           temperature=temperature, dlogits=dlogits)
-    shape, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
-    weight, stats = _vector(weight, "weight", T, _F32, z.device), _vector(stats, "stats", 2 * T, _F32, z.device)
+    shape, lead, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
+    weight = _vector(weight, "weight", lead, _F32, z.device)
+    stats = _vector(stats, "stats", (T, 2), _F32, z.device, lead)
     dlogits, ldo = _dlogits(dlogits, shape, z, T, V)
     _run("distill_bwd", lib.distill_bwd, z.device, _ptr(weight), z.data_ptr(), ids.data_ptr(), tl.data_ptr(),
          _ptr(stats), dlogits.data_ptr(), T, V, ld, ldo, K, temperature, code, _DTYPE[tl.dtype], _itype(ids))
@@ -848,11 +885,11 @@ def distill_fwd_bwd(logits, teacher_ids, teacher_logits, weight, temperature: fl
     if stream is not None:
         return _on_stream(stream, distill_fwd_bwd, logits, teacher_ids, teacher_logits, weight,
                           temperature=temperature, out=out)
-    shape, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
-    weight = _vector(weight, "weight", T, _F32, z.device)
+    shape, lead, z, T, V, ld, code, ids, tl, K = _distill_inputs(logits, teacher_ids, teacher_logits)
+    weight = _vector(weight, "weight", lead, _F32, z.device)
     given = out or {}
-    out = {"loss": _out(given.get("loss"), shape[:-1], torch.float32, z.device, "loss"),
-           "stats": _out(given.get("stats"), (T, 2), torch.float32, z.device, "stats")}
+    out = {"loss": _row_out(given.get("loss"), lead, torch.float32, z.device, "loss"),
+           "stats": _row_out(given.get("stats"), (T, 2), torch.float32, z.device, "stats", lead)}
     out["dlogits"], ldo = _dlogits(given.get("dlogits"), shape, z, T, V)
     _run("distill_fwd_bwd", lib.distill_fwd_bwd, z.device, z.data_ptr(), ids.data_ptr(), tl.data_ptr(), _ptr(weight),
          out["loss"].data_ptr(), out["stats"].data_ptr(), out["dlogits"].data_ptr(), T, V, ld, ldo, K, temperature,
