@@ -23,6 +23,8 @@
 // sums go to the workspace and are added by a second kernel in a fixed order.
 // Measured, bf16: 16384 x 4096 with residual 87 us, 92% of the copy bandwidth; backward with dh 220000 x 512
 // 151 us, 89%, 16384 x 4096 94 us, 85%.
+#include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <numeric>
 #include <type_traits>
@@ -465,10 +467,17 @@ __global__ void __launch_bounds__(kMaxThreads) ln_fwd_long_kernel(const LnFwdArg
 }
 
 // ---- backward
-// dx, and with a.part the block's column sums: part[block][0][j] of dy x_hat, part[block][1][j] of dy
-template <typename T, int R, bool kRagged, bool kShared>
-__global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, int G, int S, uint32_t* status) {
-  extern __shared__ __align__(16) float dyn[];  // with several groups a block: 2 N column sums
+// dx, and with a.part the block's column sums: part[block][0][j] of dy x_hat, part[block][1][j] of dy.
+// kFold: a thread's column sums go to slots of its own in shared memory every `fold` rows. Terms that are much
+// alike are rounded the same way, so that one accumulator over n rows may be off by n / 2 ulp: 264000 equal rows
+// of 8192 (1737 a group) gave weight gradients off by 2.6e-5, with a fold every 128 rows 2.1e-6. It costs -3 to
+// +1% (100000 x 8192 bf16 1044 us, 1057 without; ragged rows of a cluster +5%) where whole rows end a run before
+// it and ragged ones go on; with either form for both the registers do not suffice (100000 x 2001 fp32 797 us
+// instead of 559). Rows are counted in 32 bits for the same reason.
+template <typename T, int R, bool kRagged, bool kShared, bool kFold>
+__global__ void __launch_bounds__(kMaxGroup)
+    ln_bwd_kernel(const LnBwdArgs a, int G, int S, int fold, uint32_t* status) {
+  extern __shared__ __align__(16) float dyn[];  // the slots; then, with several groups a block, 2 N column sums
   __shared__ float smem[2 * 2 * 32];
   __shared__ ClusterSlots slots;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -476,13 +485,14 @@ __global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, in
   constexpr bool kNarrow = R == 1;  // groups of less than a warp
   const int groups = kShared ? 1 : blockDim.x / G, group = kShared ? 0 : threadIdx.x / G;
   const int t = kShared ? threadIdx.x + cluster_ctarank() * R * G : threadIdx.x % G;  // vectors t, t + G, ...
-  const int64_t unit = kShared ? blockIdx.x / S : blockIdx.x;
+  using Index = std::conditional_t<kFold, uint32_t, int64_t>;  // of rows
+  const Index unit = kShared ? blockIdx.x / S : blockIdx.x;
   const int N = static_cast<int>(a.N);
-  int64_t r = unit * groups + group;
-  const int shift = kRagged ? shift_of(static_cast<const T*>(a.dx) + r * a.N) : 0;
+  Index r = unit * groups + group;
+  const int shift = kRagged ? shift_of(static_cast<const T*>(a.dx) + static_cast<int64_t>(r) * a.N) : 0;
   const int vectors = (N + shift + E - 1) / E;
   int n = vectors;
-  const int64_t step = static_cast<int64_t>(kShared ? gridDim.x / S : gridDim.x) * groups;
+  const Index step = static_cast<Index>(kShared ? gridDim.x / S : gridDim.x) * groups;
   const float inv_n = 1.0f / static_cast<float>(a.N);
   const bool add = a.dh != nullptr, f32 = a.wdtype == 0;
   auto column = [&](int i) { return (t + i * G) * E - shift; };
@@ -511,56 +521,102 @@ __global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, in
   };
   GroupSum<2, kNarrow> sum(smem, G);
   SharedSum<kShared, 2> join(slots, S);
-  Row next;
-  const int64_t M = a.M + (kNarrow ? (threadIdx.x & 31) / G : 0);  // the rows of a warp's groups end together
-  if (r < a.M) load(next, r);
-  for (; r < M; r += step) {
-    if (kNarrow && r >= a.M) n = 0;
-    Row w = next;
-    if (r + step < a.M) load(next, r + step);
-    if constexpr (kRagged) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        clear_others<T>(w.x[i], column(i), N);
-        clear_others<T>(w.dy[i], column(i), N);
-      }
-    }
-    const float2 nmu = pair(-w.mu), rstd = pair(w.rstd);
-    float2 s0 = pair(0.f), s1 = s0;
+  auto slot = [&](int i, int e) -> float4& {  // of pair e of the thread's vector i
+    return reinterpret_cast<float4*>(dyn)[(i * P + e) * blockDim.x + threadIdx.x];
+  };
+  if (kFold) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (t + i * G >= n) continue;
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        const float2 xh = __fmul2_rn(__fadd2_rn(get_pair<T>(w.x[i], e), nmu), rstd), d = get_pair<T>(w.dy[i], e);
-        const float2 g = __fmul2_rn(d, gam[i][e]);
-        sg[i][e] = __ffma2_rn(d, xh, sg[i][e]);
-        sb[i][e] = __fadd2_rn(sb[i][e], d);
-        s0 = __fadd2_rn(s0, g);
-        s1 = __ffma2_rn(g, xh, s1);
-      }
-    }
-    float s[2] = {s0.x + s0.y, s1.x + s1.y};  // columns behind the row have dy = 0
-    sum(s);
-    join(s);
-    // dx = rstd (g - mean(g) - x_hat mean(g x_hat))
-    const float2 c0 = pair(-s[0] * inv_n * w.rstd), c1 = pair(-s[1] * inv_n * w.rstd);
-    T* dx = static_cast<T*>(a.dx) + r * a.N;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (t + i * G >= n) continue;
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        const float2 xh = __fmul2_rn(__fadd2_rn(get_pair<T>(w.x[i], e), nmu), rstd);
-        float2 v = __ffma2_rn(__fmul2_rn(get_pair<T>(w.dy[i], e), gam[i][e]), rstd, __ffma2_rn(xh, c1, c0));
-        if (add) v = __fadd2_rn(v, get_pair<T>(w.dh[i], e));
-        set_pair<T>(w.x[i], e, v);
-      }
-      store_columns<T, kRagged>(dx, column(i), N, w.x[i]);
+      for (int e = 0; e < P; ++e) slot(i, e) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
+  const Index rows = a.M;
+  const Index M = rows + (kNarrow ? (threadIdx.x & 31) / G : 0);  // the rows of a warp's groups end together
+  auto to_slots = [&]() {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const float4 o = slot(i, e);
+        slot(i, e) = make_float4(o.x + sg[i][e].x, o.y + sg[i][e].y, o.z + sb[i][e].x, o.w + sb[i][e].y);
+        sg[i][e] = sb[i][e] = pair(0.0f);
+      }
+    }
+  };
+  constexpr bool kRuns = kFold && !kRagged;
+  int left = fold;
+#pragma unroll 1
+  do {
+    const Index stop = kRuns ? min(M, r + fold * step) : M;
+    Row next;
+    if (r < rows) load(next, r);
+    for (; r < stop; r += step) {
+      if (kNarrow && r >= rows) n = 0;
+      Row w = next;
+      if ((!kRuns || r + step < stop) && ((kRuns && !kNarrow) || r + step < rows)) load(next, r + step);
+      if constexpr (kRagged) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          clear_others<T>(w.x[i], column(i), N);
+          clear_others<T>(w.dy[i], column(i), N);
+        }
+      }
+      const float2 nmu = pair(-w.mu), rstd = pair(w.rstd);
+      float2 s0 = pair(0.f), s1 = s0;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (t + i * G >= n) continue;
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const float2 xh = __fmul2_rn(__fadd2_rn(get_pair<T>(w.x[i], e), nmu), rstd), d = get_pair<T>(w.dy[i], e);
+          const float2 g = __fmul2_rn(d, gam[i][e]);
+          sg[i][e] = __ffma2_rn(d, xh, sg[i][e]);
+          sb[i][e] = __fadd2_rn(sb[i][e], d);
+          s0 = __fadd2_rn(s0, g);
+          s1 = __ffma2_rn(g, xh, s1);
+        }
+      }
+      float s[2] = {s0.x + s0.y, s1.x + s1.y};  // columns behind the row have dy = 0
+      sum(s);
+      join(s);
+      // dx = rstd (g - mean(g) - x_hat mean(g x_hat))
+      const float2 c0 = pair(-s[0] * inv_n * w.rstd), c1 = pair(-s[1] * inv_n * w.rstd);
+      T* dx = static_cast<T*>(a.dx) + static_cast<int64_t>(r) * a.N;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (t + i * G >= n) continue;
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const float2 xh = __fmul2_rn(__fadd2_rn(get_pair<T>(w.x[i], e), nmu), rstd);
+          float2 v = __ffma2_rn(__fmul2_rn(get_pair<T>(w.dy[i], e), gam[i][e]), rstd, __ffma2_rn(xh, c1, c0));
+          if (add) v = __fadd2_rn(v, get_pair<T>(w.dh[i], e));
+          set_pair<T>(w.x[i], e, v);
+        }
+        store_columns<T, kRagged>(dx, column(i), N, w.x[i]);
+      }
+      if (kFold && !kRuns && --left == 0) {
+        to_slots();
+        left = fold;
+      }
+    }
+    if (kRuns) to_slots();
+  } while (kRuns && r < M);
+  if (kFold && !kRuns) to_slots();
   join.end(status);
   if (a.part == nullptr) return;
+  if (kFold) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const float4 o = slot(i, e);
+        sg[i][e] = make_float2(o.x, o.y);
+        sb[i][e] = make_float2(o.z, o.w);
+      }
+    }
+    __syncthreads();  // the slots' place is written anew
+  }
   // the block's sums, one group after the other: a fixed order. Groups of less than a warp with the same
   // columns are added first.
   const bool merge = !kRagged && kNarrow && G < 32;
@@ -579,7 +635,7 @@ __global__ void __launch_bounds__(kMaxGroup) ln_bwd_kernel(const LnBwdArgs a, in
     }
   }
   const int wide = merge ? 32 : G, parts = kShared ? 1 : blockDim.x / wide;
-  float* part = a.part + unit * 2 * a.N;
+  float* part = a.part + static_cast<int64_t>(unit) * 2 * a.N;
   float* to = parts > 1 ? dyn : part;
   for (int k = 0; k < parts; ++k) {
     if (k == static_cast<int>(threadIdx.x) / wide && static_cast<int>(threadIdx.x) % wide < G) {
@@ -647,18 +703,30 @@ __global__ void __launch_bounds__(kMaxThreads) ln_dx_long_kernel(const LnBwdArgs
 }
 // one row chunk's column sums, for rows of any length
 constexpr int kColThreads = 128;
-template <typename T>
-__global__ void __launch_bounds__(kColThreads) ln_param_long_kernel(const LnBwdArgs a, int64_t rows_per_chunk) {
+template <typename T, bool kFold>  // kFold: as in ln_bwd_kernel
+__global__ void __launch_bounds__(kColThreads) ln_param_long_kernel(const LnBwdArgs a, int64_t rows_per_chunk,
+                                                                   int fold) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t j = static_cast<int64_t>(blockIdx.x) * kColThreads + threadIdx.x;
   if (j >= a.N) return;
   const int64_t r0 = blockIdx.y * rows_per_chunk, r1 = min(a.M, r0 + rows_per_chunk);
-  float sg = 0.f, sb = 0.f;
+  float sg = 0.f, sb = 0.f, all_g = 0.f, all_b = 0.f;
+  int left = fold;
   for (int64_t r = r0; r < r1; ++r) {
     const float d = to_f(static_cast<const T*>(a.dy)[r * a.lddy + j]);
     const float xh = (to_f(static_cast<const T*>(a.x)[r * a.ldx + j]) - a.stats[2 * r]) * a.stats[2 * r + 1];
     sg = fmaf(d, xh, sg);
     sb += d;
+    if (kFold && --left == 0) {
+      all_g += sg;
+      all_b += sb;
+      sg = sb = 0.f;
+      left = fold;
+    }
+  }
+  if (kFold) {
+    sg += all_g;
+    sb += all_b;
   }
   float* p = a.part + static_cast<int64_t>(blockIdx.y) * 2 * a.N;
   p[j] = sg;
@@ -735,6 +803,7 @@ Shared share_row(int64_t n) {
 constexpr int64_t kMostShared = 2 * kMaxCluster * kMaxGroup;  // vectors
 
 // blocks of a persistent kernel that fit on the device at once (asked once for each device and block size)
+constexpr size_t kPlainSmem = 48 * 1024;  // dynamic shared memory that a kernel has without asking
 struct FitCache {
   int device = -1, threads = 0, fit = 0;
   size_t bytes = 0;
@@ -746,6 +815,10 @@ cudaError_t blocks_that_fit(Kernel kernel, FitCache& cache, int block, size_t sm
   if (e != cudaSuccess) return e;
   if (cache.device != dev || cache.threads != block || cache.bytes != smem) {
     int per_sm = 0;
+    if (smem > kPlainSmem) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+    }
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, block, smem);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorLaunchOutOfResources;
@@ -817,9 +890,46 @@ cudaError_t launch_reduce(const LnBwdArgs& a, int64_t rows, cudaStream_t stream)
                             a.dgamma, a.dbeta, a.wdtype);
 }
 
+// Rows between two folds of a thread's column sums where (at least) so many groups share M rows: kFewRows or, if
+// that is more, as many as there are folds; 0 for groups of at most kFewRows rows, that need none.
+constexpr int kFewRows = 128;
+int fold_rows(int64_t M, int64_t groups) {
+  const int64_t rows = (M + groups - 1) / groups;
+  if (rows <= kFewRows) return 0;
+  return std::max(kFewRows, static_cast<int>(std::ceil(std::sqrt(static_cast<double>(rows)))));
+}
+// bytes of the slots of a block of `threads`
+template <typename T, int R>
+constexpr size_t fold_bytes(int threads) {
+  return static_cast<size_t>(threads) * R * kPairs<T> * sizeof(float4);
+}
+
 constexpr int64_t kMaxBlocks = 4 * 256;  // rows of column sums in the workspace, at most
 constexpr int64_t kLongChunks = 64;      // of them for rows too long for registers
 
+template <typename T, int R, bool kRagged, bool kFold>
+cudaError_t bwd_groups(const LnBwdArgs& a, int G, int groups, int fold, cudaStream_t stream) {
+  const int block = groups * G;
+  const size_t sums = groups > 1 && a.part != nullptr ? static_cast<size_t>(2 * a.N) * sizeof(float) : 0;
+  const size_t smem = kFold ? std::max(sums, fold_bytes<T, R>(block)) : sums;
+  int64_t blocks;
+  {
+    static std::mutex mu;
+    static FitCache cache;
+    std::lock_guard<std::mutex> lk(mu);
+    const cudaError_t e = blocks_that_fit(ln_bwd_kernel<T, R, kRagged, false, kFold>, cache, block, smem, blocks);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t most = (a.M + groups - 1) / groups;
+  if (blocks > kMaxBlocks) blocks = kMaxBlocks;
+  if (blocks > most) blocks = most;
+  else if (kRagged) blocks -= blocks % rows_apart<T>(a.N);
+  ln_bwd_kernel<T, R, kRagged, false, kFold>
+      <<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, G, 1, fold, nullptr);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.part == nullptr) return e;
+  return launch_reduce(a, blocks, stream);
+}
 template <typename T, int R, bool kRagged>
 cudaError_t bwd_one(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {
   const int G = group_threads(n, R);
@@ -827,24 +937,9 @@ cudaError_t bwd_one(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {
   // (blocks of 256 threads and sums stored element by element: 2048 x 4096 bf16 with dh 30 us, now 22).
   int groups = kMaxGroup / G;
   while (groups > 1 && groups * G > 32 && (a.M + groups - 1) / groups < device_sm_count()) groups = (groups + 1) / 2;
-  const int block = groups * G;
-  const size_t smem = groups > 1 && a.part != nullptr ? static_cast<size_t>(2 * a.N) * sizeof(float) : 0;
-  int64_t blocks;
-  {
-    static std::mutex mu;
-    static FitCache cache;
-    std::lock_guard<std::mutex> lk(mu);
-    const cudaError_t e = blocks_that_fit(ln_bwd_kernel<T, R, kRagged, false>, cache, block, smem, blocks);
-    if (e != cudaSuccess) return e;
-  }
-  const int64_t most = (a.M + groups - 1) / groups;
-  if (blocks > kMaxBlocks) blocks = kMaxBlocks;
-  if (blocks > most) blocks = most;
-  else if (kRagged) blocks -= blocks % rows_apart<T>(a.N);
-  ln_bwd_kernel<T, R, kRagged, false><<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, G, 1, nullptr);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.part == nullptr) return e;
-  return launch_reduce(a, blocks, stream);
+  const int fold = a.part != nullptr ? fold_rows(a.M, static_cast<int64_t>(groups) * device_sm_count()) : 0;
+  return fold > 0 ? bwd_groups<T, R, kRagged, true>(a, G, groups, fold, stream)
+                  : bwd_groups<T, R, kRagged, false>(a, G, groups, 0, stream);
 }
 template <typename T>
 cudaError_t bwd_long(const LnBwdArgs& a, cudaStream_t stream) {
@@ -854,24 +949,33 @@ cudaError_t bwd_long(const LnBwdArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess || a.part == nullptr) return e;
   const int64_t chunks = a.M < kLongChunks ? a.M : kLongChunks, per = (a.M + chunks - 1) / chunks;
   const dim3 g(static_cast<unsigned>((a.N + kColThreads - 1) / kColThreads), static_cast<unsigned>(chunks));
-  ln_param_long_kernel<T><<<g, kColThreads, 0, stream>>>(a, per);
+  const int fold = fold_rows(per, 1);
+  if (fold > 0) ln_param_long_kernel<T, true><<<g, kColThreads, 0, stream>>>(a, per, fold);
+  else ln_param_long_kernel<T, false><<<g, kColThreads, 0, stream>>>(a, per, 0);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_reduce(a, chunks, stream);
 }
-template <typename T, bool kRagged>
-cudaError_t bwd_shared(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {
+template <typename T, bool kRagged, bool kFold>
+cudaError_t bwd_clusters(const LnBwdArgs& a, const Shared& p, int fold, cudaStream_t stream) {
   int64_t rows;
   {
     static std::mutex mu;
     static StreamCache cache;
     std::lock_guard<std::mutex> lk(mu);
-    const Shared p = share_row(n);
-    const cudaError_t e = launch_stream(ln_bwd_kernel<T, 2, kRagged, true>, cache, p.G, 0, a.M, p.S, false,
-                                        kRagged ? rows_apart<T>(a.N) : 1, stream, a, p.G, p.S, status_word_ptr());
+    const cudaError_t e = launch_stream(ln_bwd_kernel<T, 2, kRagged, true, kFold>, cache, p.G,
+                                        kFold ? fold_bytes<T, 2>(p.G) : 0, a.M, p.S, false,
+                                        kRagged ? rows_apart<T>(a.N) : 1, stream, a, p.G, p.S, fold, status_word_ptr());
     if (e != cudaSuccess) return e;
     rows = cache.launched;
   }
   return a.part == nullptr ? cudaSuccess : launch_reduce(a, rows, stream);
+}
+template <typename T, bool kRagged>
+cudaError_t bwd_shared(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {
+  const Shared p = share_row(n);
+  const int fold = a.part != nullptr ? fold_rows(a.M, std::max(1, device_sm_count() / p.S)) : 0;
+  return fold > 0 ? bwd_clusters<T, kRagged, true>(a, p, fold, stream)
+                  : bwd_clusters<T, kRagged, false>(a, p, 0, stream);
 }
 template <typename T, bool kRagged>
 cudaError_t bwd_any(const LnBwdArgs& a, cudaStream_t stream) {
