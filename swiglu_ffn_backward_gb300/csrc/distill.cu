@@ -240,7 +240,7 @@ __device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g,
   }
 }
 
-template <typename T, bool kGrad, int W>
+template <typename T, bool kGrad, int W, bool kLong>  // kLong: as in WarpSums (with a gradient a share is short)
 __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
     kd_fwd_kernel(const KdArgs a, Split split, int stages, int slots, uint32_t* status) {
   constexpr int E = Traits<T>::E;
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
     // max and sum of the warp's part of row r, sent to every block
     auto sums = [&](int64_t r, int slot) {
       const Share sh = share_of(static_cast<const T*>(a.logits) + r * a.ld, a.V, split.per, rank);
-      WarpSums<T, false> sum(c2);
+      WarpSums<T, false, kLong> sum(c2);
       for (int at = sh.begin; at < sh.end; at += kStageVecs) {
         const int cnt = min(sh.end - at, kStageVecs);
         wait(&sm.ring.full[in.stage], in.parity);
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
   cluster_wait();
 }
 
-template <typename T, bool kGrad, int W>
+template <typename T, bool kGrad, int W, bool kLong>
 cudaError_t launch_fwd(const KdArgs& a, Split split, cudaStream_t stream) {
   static std::mutex mu;  // guards the occupancy cache
   static StreamCache cache;
@@ -477,14 +477,14 @@ cudaError_t launch_fwd(const KdArgs& a, Split split, cudaStream_t stream) {
   const int stages = a.K <= 256 ? kStages : a.K <= 512 ? kStages - 1 : kStages - 2, slots = table_slots(a.K);
   const size_t smem = stages * Shape<W>::kStageBytes + entry_bytes(a.K) + static_cast<size_t>(2) * slots * sizeof(int);
   std::lock_guard<std::mutex> lk(mu);
-  return launch_stream(kd_fwd_kernel<T, kGrad, W>, cache, 32 * (W + kExtraWarps), smem, a.T, split.S, false, 1, stream,
-                       a, split, stages, slots, status_word_ptr());
+  return launch_stream(kd_fwd_kernel<T, kGrad, W, kLong>, cache, 32 * (W + kExtraWarps), smem, a.T, split.S, false, 1,
+                       stream, a, split, stages, slots, status_word_ptr());
 }
-template <bool kGrad, int W>
+template <bool kGrad, int W, bool kLong>
 cudaError_t launch_fwd_any(const KdArgs& a, int dtype, Split split, cudaStream_t stream) {
-  return dtype == 0   ? launch_fwd<float, kGrad, W>(a, split, stream)
-         : dtype == 1 ? launch_fwd<__half, kGrad, W>(a, split, stream)
-                      : launch_fwd<__nv_bfloat16, kGrad, W>(a, split, stream);
+  return dtype == 0   ? launch_fwd<float, kGrad, W, kLong>(a, split, stream)
+         : dtype == 1 ? launch_fwd<__half, kGrad, W, kLong>(a, split, stream)
+                      : launch_fwd<__nv_bfloat16, kGrad, W, kLong>(a, split, stream);
 }
 
 // ---- gradient alone
@@ -580,17 +580,20 @@ cudaError_t launch_distill(const KdArgs& a, bool forward, bool backward, int dty
   // longer ones: bf16 logits with 64 entries, loss and gradient, 8192 columns 126 us against 291 us with 16
   // warps (16384 rows), 16384 columns 122 against 157 us (8192 rows), 32768 columns (4096 rows, four blocks
   // a row) 121 us against 98. Without a gradient four warps are as fast for long rows too, once each of those
-  // blocks has two rows.
+  // blocks has two rows; rows of more stages than add up in one sequence are left to 16.
   constexpr int64_t big = kShareStages * Shape<16>::kStageVecs, small = kShareStages * Shape<4>::kStageVecs;
   // the row's shares have to stay in the rings for the gradient: a longer row is read twice
   if (forward && backward && vectors <= 2 * small)
-    return launch_fwd_any<true, 4>(a, dtype, split_row(a.T, vectors, small, sms), stream);
+    return launch_fwd_any<true, 4, false>(a, dtype, split_row(a.T, vectors, small, sms), stream);
   if (forward && backward && vectors <= kMaxCluster * big)
-    return launch_fwd_any<true, 16>(a, dtype, split_row(a.T, vectors, big, sms), stream);
+    return launch_fwd_any<true, 16, false>(a, dtype, split_row(a.T, vectors, big, sms), stream);
   if (forward) {
     const Split all = split_row(a.T, vectors, vectors, sms);
-    const cudaError_t e = vectors <= small || a.T >= 6 * sms ? launch_fwd_any<false, 4>(a, dtype, all, stream)
-                                                             : launch_fwd_any<false, 16>(a, dtype, all, stream);
+    const bool four = vectors <= small || (a.T >= 6 * sms && vectors <= kFewStages * Shape<4>::kStageVecs);
+    const cudaError_t e = four ? launch_fwd_any<false, 4, false>(a, dtype, all, stream)
+                          : all.per > kFewStages * Shape<16>::kStageVecs
+                              ? launch_fwd_any<false, 16, true>(a, dtype, all, stream)
+                              : launch_fwd_any<false, 16, false>(a, dtype, all, stream);
     if (e != cudaSuccess || !backward) return e;
   }
   KdArgs b = a;

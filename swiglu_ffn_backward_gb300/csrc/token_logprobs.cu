@@ -237,7 +237,7 @@ __device__ __forceinline__ int select_best(const Share& sh, int top, Finish<W>& 
 static_assert(kListed >= 32 * 8, "the list takes what one step adds");
 static_assert(Plan<16>::kTableBytes / 2 <= 65536, "16-bit groups");
 
-template <typename T, int W>
+template <typename T, int W, bool kLong>  // kLong: as in WarpSums
 __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 3)
     tlp_fwd_kernel(const TlpFwdArgs a, Split split, uint32_t* status) {
   constexpr int kStageVecs = Shape<W>::kStageVecs, kStageBytes = Shape<W>::kStageBytes, kThreads = Shape<W>::kThreads;
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 3)
       Finish<W>& f = finish[sel];
       wait(&sm.taken[sel], parity);  // the selector has read the row before in its place
       T* table = reinterpret_cast<T*>(f.table);
-      WarpSums<T, true> sums(c2);
+      WarpSums<T, true, kLong> sums(c2);
       const int depth = group_stages<T, W>(sh);
       float most = neg_inf(), group_most = neg_inf();  // the thread's maximum, and that of its open group
       int best = 0, group = tid, left = depth;         // the first group that has it; the open group
@@ -405,20 +405,20 @@ __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 3)
 }
 static_assert(kMaxTop == 32, "one lane for each alternative");
 
-template <typename T, int W>
+template <typename T, int W, bool kLong>
 cudaError_t launch_fwd(const TlpFwdArgs& a, Split split, cudaStream_t stream) {
   static std::mutex mu;  // guards the occupancy cache
   static StreamCache cache;
   std::lock_guard<std::mutex> lk(mu);
   // a cluster of several blocks takes one row
-  return launch_stream(tlp_fwd_kernel<T, W>, cache, Plan<W>::kThreads, kFwdSmem<W>, a.T, split.S,
+  return launch_stream(tlp_fwd_kernel<T, W, kLong>, cache, Plan<W>::kThreads, kFwdSmem<W>, a.T, split.S,
                        split.S > 1, 1, stream, a, split, status_word_ptr());
 }
-template <int W>
+template <int W, bool kLong>
 cudaError_t launch_fwd_any(const TlpFwdArgs& a, int dtype, Split split, cudaStream_t stream) {
-  return dtype == 0   ? launch_fwd<float, W>(a, split, stream)
-         : dtype == 1 ? launch_fwd<__half, W>(a, split, stream)
-                      : launch_fwd<__nv_bfloat16, W>(a, split, stream);
+  return dtype == 0   ? launch_fwd<float, W, kLong>(a, split, stream)
+         : dtype == 1 ? launch_fwd<__half, W, kLong>(a, split, stream)
+                      : launch_fwd<__nv_bfloat16, W, kLong>(a, split, stream);
 }
 
 // Backward: bound by HBM (V elements read and written a row); no block needs another's results, so groups of
@@ -499,7 +499,10 @@ cudaError_t launch_token_logprobs_fwd(const TlpFwdArgs& a, int dtype, cudaStream
   // 115 us (4864 rows), 131072 columns 111 against 98 us (2048 rows).
   const int64_t sms = device_sm_count();
   const bool small = p.S == 1 && (vectors <= 1024 || (vectors <= 6400 && a.T >= 6 * sms));
-  return small ? launch_fwd_any<4>(a, dtype, p, stream) : launch_fwd_any<16>(a, dtype, p, stream);
+  static_assert(6400 <= kFewStages * Shape<4>::kStageVecs, "rows of four warps are not long");
+  if (small) return launch_fwd_any<4, false>(a, dtype, p, stream);
+  return p.per > kFewStages * Shape<16>::kStageVecs ? launch_fwd_any<16, true>(a, dtype, p, stream)
+                                                    : launch_fwd_any<16, false>(a, dtype, p, stream);
 }
 
 cudaError_t launch_token_logprobs_bwd(const TlpBwdArgs& a, int dtype, cudaStream_t stream) {

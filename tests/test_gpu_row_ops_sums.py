@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from ._row_ops import SUM, check, f64
+from ._row_ops import EXP, SUM, check, f64
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -37,3 +37,48 @@ def test_weight_gradients_of_many_like_rows(M, N, dtype):
     xerr = 2.0 ** -23 * (np.abs(h) + np.abs(s[:, :1])) * s[:, 1:]
     check("dgamma", dgamma, M * (d * xhat)[0], F32, M * (np.abs(d) * (SUM * np.abs(xhat) + 2 * xerr))[0])
     check("dbeta", dbeta, M * d[0], F32, SUM * M * np.abs(d[0]))
+
+
+# a row's first logits are 0, its largest, the others the background, so that every warp of a block has met the
+# maximum before the terms that are all alike; 2^-x of a background is no short fraction
+BACKGROUND = (-0.3125, -0.75, -1.0, -1.375, -2.25)
+FIRST = 17000
+
+
+def _like_rows(V, dtype):
+    """[len(BACKGROUND), V] logits; the sums s of exp(z) and sum p |z| in fp64."""
+    z = torch.tensor(BACKGROUND, device="cuda").unsqueeze(1).repeat(1, V).to(dtype)
+    z[:, :FIRST] = 0
+    e = np.exp(np.asarray(BACKGROUND))
+    s = FIRST + (V - FIRST) * e
+    return z, s, (V - FIRST) * e * -np.asarray(BACKGROUND) / s
+
+
+@pytest.mark.parametrize("T,V,dtype", [(1000, 32768, BF16), (1000, 131072, BF16), (1000, 262144, BF16), (1000, 262147, F32),
+                                       (1000, 2000003, BF16), (200, 2000003, BF16), (1, 4000003, F32)],
+                         ids=lambda v: str(v).replace("torch.", ""))
+def test_distillation_of_like_logits(T, V, dtype):
+    swg = _swg()
+    z, s, ed = _like_rows(V, dtype)
+    ids, tl = torch.full((T, 1), V - 1, device="cuda"), torch.zeros((T, 1), device="cuda")
+    for r in range(len(BACKGROUND)):
+        out = swg.distill_fwd(z[r: r + 1].expand(T, V), ids, tl)
+        rel = SUM + EXP + 2.0 ** -22 * ed[r]
+        check("sum", out["stats"][:, 1], np.full(T, s[r]), F32, rel * s[r])
+        loss = np.log(s[r]) - BACKGROUND[r]
+        check("loss", out["loss"], np.full(T, loss), F32, rel + 2.0 ** -22 * (np.log(s[r]) + 3))
+
+
+@pytest.mark.parametrize("T,V,dtype", [(1000, 51000, BF16), (1000, 25500, F32), (200, 131072, BF16), (200, 1000003, BF16),
+                                       (200, 1000003, F32), (1, 4000003, BF16)], ids=lambda v: str(v).replace("torch.", ""))
+def test_log_probabilities_of_like_logits(T, V, dtype):
+    swg = _swg()
+    z, s, ed = _like_rows(V, dtype)
+    t = torch.full((T,), V - 1, device="cuda")
+    for r in range(len(BACKGROUND)):
+        out = swg.token_logprobs_fwd(z[r: r + 1].expand(T, V), t, top_k=2)
+        rel, ls = SUM + EXP + 2.0 ** -22 * ed[r], np.log(s[r])
+        check("sum", out["stats"][:, 1], np.full(T, s[r]), F32, rel * s[r])
+        check("logp", out["logp"], np.full(T, BACKGROUND[r] - ls), F32, rel + 2.0 ** -22 * (ls + 3))
+        check("entropy", out["entropy"], np.full(T, ls + ed[r]), F32, 2 * rel * (1 + ed[r]) + 2.0 ** -22 * (ls + ed[r]))
+        assert (out["top_idx"] == torch.tensor([0, 1], device="cuda")).all()
