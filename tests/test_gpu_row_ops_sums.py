@@ -6,6 +6,8 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
+
 from ._row_ops import EXP, SUM, check, f64
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +84,44 @@ def test_log_probabilities_of_like_logits(T, V, dtype):
         check("logp", out["logp"], np.full(T, BACKGROUND[r] - ls), F32, rel + 2.0 ** -22 * (ls + 3))
         check("entropy", out["entropy"], np.full(T, ls + ed[r]), F32, 2 * rel * (1 + ed[r]) + 2.0 ** -22 * (ls + ed[r]))
         assert (out["top_idx"] == torch.tensor([0, 1], device="cuda")).all()
+
+
+@pytest.mark.parametrize("N,dtype", [(300007, BF16), (4000003, F32), (4000003, BF16)],
+                         ids=lambda v: str(v).replace("torch.", ""))
+def test_layer_norm_of_long_like_rows(N, dtype):
+    # rows read again: a constant with a few other elements, and a gradient that is all alike
+    swg = _swg()
+    x = torch.full((3, N), 0.45, device="cuda")
+    x[0, ::1000], x[1] = 0.5, 0.1
+    x[1, ::7] = 0.15
+    x[2] += torch.randn(N, generator=torch.Generator("cuda").manual_seed(2), device="cuda")
+    x = x.to(dtype)
+    out = swg.layer_norm_fwd(x)
+    y, mu, rstd, h = oracle.layer_norm_fwd(f64(x), None, None, 1e-5)
+    top = np.abs(h).max(axis=1)
+    check("mean", out["stats"][:, 0], mu, F32, SUM * top)
+    var_err = 2 * SUM + (SUM * top * rstd) ** 2 + 2.0 ** -22 * top * rstd
+    check("rstd", out["stats"][:, 1], rstd, F32, rstd * var_err)
+    dy = torch.full((1, N), 0.1, device="cuda").to(dtype).expand(3, N)
+    dx, _, dbeta = swg.layer_norm_bwd(dy, x, out["stats"])
+    st, d = f64(out["stats"]), f64(dy)
+    rdx, _, rdb = oracle.layer_norm_bwd(d, h, st[:, 0], st[:, 1], None)
+    xhat = np.abs((h - st[:, :1]) * st[:, 1:])
+    xerr = 2.0 ** -23 * (np.abs(h) + np.abs(st[:, :1])) * st[:, 1:]
+    mg, mgx = d.mean(axis=1, keepdims=True), (d * (xhat + xerr)).mean(axis=1, keepdims=True)
+    part = st[:, 1:] * (2.0 ** -22 * d + SUM * mg + (SUM + 2.0 ** -22) * (xhat + xerr) * mgx + xerr * mgx
+                        + xhat * (d * xerr).mean(axis=1, keepdims=True)) + 2.0 ** -23 * np.abs(rdx)
+    check("dx", dx, rdx, dtype, part)
+    check("dbeta", dbeta, rdb, dtype, SUM * np.abs(d).sum(axis=0))
+
+
+@pytest.mark.parametrize("N", [520, 70001, 300007])
+def test_infinite_and_nan_elements_of_long_rows(N):
+    swg = _swg()
+    x = torch.randn((5, N), generator=torch.Generator("cuda").manual_seed(3), device="cuda")
+    clean = swg.layer_norm_fwd(x)
+    x[0, N // 2], x[1, 7], x[2, N - 1], x[3, 0], x[3, N - 1] = (float(v) for v in ("inf", "-inf", "nan", "inf", "-inf"))
+    out = swg.layer_norm_fwd(x)
+    mean = out["stats"][:, 0].tolist()
+    assert mean[0] == float("inf") and mean[1] == float("-inf") and mean[2] != mean[2] and mean[3] != mean[3]
+    assert out["y"][:4].isnan().all() and torch.equal(out["y"][4], clean["y"][4])
