@@ -477,7 +477,7 @@ cudaError_t launch_fwd(const KdArgs& a, Split split, cudaStream_t stream) {
   const int stages = a.K <= 256 ? kStages : a.K <= 512 ? kStages - 1 : kStages - 2, slots = table_slots(a.K);
   const size_t smem = stages * Shape<W>::kStageBytes + entry_bytes(a.K) + static_cast<size_t>(2) * slots * sizeof(int);
   std::lock_guard<std::mutex> lk(mu);
-  return launch_stream(kd_fwd_kernel<T, kGrad, W, kLong>, cache, 32 * (W + kExtraWarps), smem, a.T, split.S, false, 1,
+  return launch_stream(kd_fwd_kernel<T, kGrad, W, kLong>, cache, 32 * (W + kExtraWarps), smem, a.T, split.S, false,
                        stream, a, split, stages, slots, status_word_ptr());
 }
 template <bool kGrad, int W, bool kLong>

@@ -850,6 +850,12 @@ cudaError_t blocks_that_fit(Kernel kernel, FitCache& cache, int block, size_t sm
   blocks = cache.fit;
   return cudaSuccess;
 }
+template <typename T>
+cudaError_t fwd_long(const LnFwdArgs& a, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>(a.M < 65536 ? a.M : 65536);
+  ln_fwd_long_kernel<T><<<grid, kMaxThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
 template <typename T, int R, bool kRagged>
 cudaError_t fwd_one(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
   const int G = group_threads(n, R), groups = G < kBlock ? kBlock / G : 1, block = groups * G;
@@ -861,9 +867,8 @@ cudaError_t fwd_one(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
     const cudaError_t e = blocks_that_fit(ln_fwd_kernel<T, R, kRagged, false>, cache, block, 0, blocks);
     if (e != cudaSuccess) return e;
   }
-  const int64_t most = (a.M + groups - 1) / groups;
-  if (blocks > most) blocks = most;
-  else if (kRagged) blocks -= blocks % rows_apart<T>(a.N);
+  blocks = persistent_blocks(blocks, (a.M + groups - 1) / groups, kRagged ? rows_apart<T>(a.N) : 1);
+  if (blocks == 0) return fwd_long<T>(a, stream);
   ln_fwd_kernel<T, R, kRagged, false><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a, G, 1, nullptr);
   return cudaGetLastError();
 }
@@ -873,8 +878,13 @@ cudaError_t fwd_shared(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
   static StreamCache cache;
   std::lock_guard<std::mutex> lk(mu);
   const Shared p = share_row(n);
-  return launch_stream(ln_fwd_kernel<T, 2, kRagged, true>, cache, p.G, 0, a.M, p.S, false,
-                       kRagged ? rows_apart<T>(a.N) : 1, stream, a, p.G, p.S, status_word_ptr());
+  const auto kernel = ln_fwd_kernel<T, 2, kRagged, true>;
+  const cudaError_t e = clusters_that_fit(kernel, cache, p.G, 0, p.S);
+  if (e != cudaSuccess) return e;
+  const int64_t clusters = persistent_blocks(cache.clusters, a.M, kRagged ? rows_apart<T>(a.N) : 1);
+  if (clusters == 0) return fwd_long<T>(a, stream);
+  ClusterLaunch l(p.G, 0, p.S, clusters, stream);
+  return cudaLaunchKernelEx(&l.cfg, kernel, a, p.G, p.S, status_word_ptr());
 }
 // Vectors a thread: one for rows of up to a warp, else two. Rows of more than 1024 vectors are shared by a
 // cluster: 3000 x 12288 bf16 with residual 70 us, 88 by a block with four vectors a thread; backward with dh
@@ -888,9 +898,7 @@ cudaError_t fwd_any(const LnFwdArgs& a, cudaStream_t stream) {
   if (n <= 32) return fwd_one<T, 1, kRagged>(a, n, stream);
   if (n <= 2 * kMaxGroup) return fwd_one<T, 2, kRagged>(a, n, stream);
   if (n <= (kRagged ? kMostShared / 2 : kMostShared)) return fwd_shared<T, kRagged>(a, n, stream);
-  const unsigned grid = static_cast<unsigned>(a.M < 65536 ? a.M : 65536);
-  ln_fwd_long_kernel<T><<<grid, kMaxThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return fwd_long<T>(a, stream);
 }
 template <typename T>
 cudaError_t fwd_type(const LnFwdArgs& a, cudaStream_t stream) {
@@ -930,6 +938,20 @@ constexpr size_t fold_bytes(int threads) {
 constexpr int64_t kMaxBlocks = 4 * 256;  // rows of column sums in the workspace, at most
 constexpr int64_t kLongChunks = 64;      // of them for rows too long for registers
 
+template <typename T>
+cudaError_t bwd_long(const LnBwdArgs& a, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>(a.M < 65536 ? a.M : 65536);
+  ln_dx_long_kernel<T><<<grid, kMaxThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.part == nullptr) return e;
+  const int64_t chunks = a.M < kLongChunks ? a.M : kLongChunks, per = (a.M + chunks - 1) / chunks;
+  const dim3 g(static_cast<unsigned>((a.N + kColThreads - 1) / kColThreads), static_cast<unsigned>(chunks));
+  const int fold = fold_rows(per, 1);
+  if (fold > 0) ln_param_long_kernel<T, true><<<g, kColThreads, 0, stream>>>(a, per, fold);
+  else ln_param_long_kernel<T, false><<<g, kColThreads, 0, stream>>>(a, per, 0);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_reduce(a, chunks, stream);
+}
 template <typename T, int R, bool kRagged, bool kFold>
 cudaError_t bwd_groups(const LnBwdArgs& a, int G, int groups, int fold, cudaStream_t stream) {
   const int block = groups * G;
@@ -943,10 +965,9 @@ cudaError_t bwd_groups(const LnBwdArgs& a, int G, int groups, int fold, cudaStre
     const cudaError_t e = blocks_that_fit(ln_bwd_kernel<T, R, kRagged, false, kFold>, cache, block, smem, blocks);
     if (e != cudaSuccess) return e;
   }
-  const int64_t most = (a.M + groups - 1) / groups;
   if (blocks > kMaxBlocks) blocks = kMaxBlocks;
-  if (blocks > most) blocks = most;
-  else if (kRagged) blocks -= blocks % rows_apart<T>(a.N);
+  blocks = persistent_blocks(blocks, (a.M + groups - 1) / groups, kRagged ? rows_apart<T>(a.N) : 1);
+  if (blocks == 0) return bwd_long<T>(a, stream);
   ln_bwd_kernel<T, R, kRagged, false, kFold>
       <<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, G, 1, fold, nullptr);
   const cudaError_t e = cudaGetLastError();
@@ -964,34 +985,26 @@ cudaError_t bwd_one(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {
   return fold > 0 ? bwd_groups<T, R, kRagged, true>(a, G, groups, fold, stream)
                   : bwd_groups<T, R, kRagged, false>(a, G, groups, 0, stream);
 }
-template <typename T>
-cudaError_t bwd_long(const LnBwdArgs& a, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(a.M < 65536 ? a.M : 65536);
-  ln_dx_long_kernel<T><<<grid, kMaxThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.part == nullptr) return e;
-  const int64_t chunks = a.M < kLongChunks ? a.M : kLongChunks, per = (a.M + chunks - 1) / chunks;
-  const dim3 g(static_cast<unsigned>((a.N + kColThreads - 1) / kColThreads), static_cast<unsigned>(chunks));
-  const int fold = fold_rows(per, 1);
-  if (fold > 0) ln_param_long_kernel<T, true><<<g, kColThreads, 0, stream>>>(a, per, fold);
-  else ln_param_long_kernel<T, false><<<g, kColThreads, 0, stream>>>(a, per, 0);
-  e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_reduce(a, chunks, stream);
-}
 template <typename T, bool kRagged, bool kFold>
 cudaError_t bwd_clusters(const LnBwdArgs& a, const Shared& p, int fold, cudaStream_t stream) {
-  int64_t rows;
+  const auto kernel = ln_bwd_kernel<T, 2, kRagged, true, kFold>;
+  const size_t smem = kFold ? fold_bytes<T, 2>(p.G) : 0;
+  int64_t clusters;
   {
     static std::mutex mu;
     static StreamCache cache;
     std::lock_guard<std::mutex> lk(mu);
-    const cudaError_t e = launch_stream(ln_bwd_kernel<T, 2, kRagged, true, kFold>, cache, p.G,
-                                        kFold ? fold_bytes<T, 2>(p.G) : 0, a.M, p.S, false,
-                                        kRagged ? rows_apart<T>(a.N) : 1, stream, a, p.G, p.S, fold, status_word_ptr());
+    cudaError_t e = clusters_that_fit(kernel, cache, p.G, smem, p.S);
     if (e != cudaSuccess) return e;
-    rows = cache.launched;
+    clusters = persistent_blocks(cache.clusters, a.M, kRagged ? rows_apart<T>(a.N) : 1);
+    if (clusters > 0) {
+      ClusterLaunch l(p.G, smem, p.S, clusters, stream);
+      e = cudaLaunchKernelEx(&l.cfg, kernel, a, p.G, p.S, fold, status_word_ptr());
+      if (e != cudaSuccess) return e;
+    }
   }
-  return a.part == nullptr ? cudaSuccess : launch_reduce(a, rows, stream);
+  if (clusters == 0) return bwd_long<T>(a, stream);
+  return a.part == nullptr ? cudaSuccess : launch_reduce(a, clusters, stream);
 }
 template <typename T, bool kRagged>
 cudaError_t bwd_shared(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {

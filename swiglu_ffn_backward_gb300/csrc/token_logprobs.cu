@@ -412,7 +412,7 @@ cudaError_t launch_fwd(const TlpFwdArgs& a, Split split, cudaStream_t stream) {
   std::lock_guard<std::mutex> lk(mu);
   // a cluster of several blocks takes one row
   return launch_stream(tlp_fwd_kernel<T, W, kLong>, cache, Plan<W>::kThreads, kFwdSmem<W>, a.T, split.S,
-                       split.S > 1, 1, stream, a, split, status_word_ptr());
+                       split.S > 1, stream, a, split, status_word_ptr());
 }
 template <int W, bool kLong>
 cudaError_t launch_fwd_any(const TlpFwdArgs& a, int dtype, Split split, cudaStream_t stream) {

@@ -7,6 +7,7 @@
 // vector, when they are partial, are put together by the producer warp, with -inf outside the row.
 #pragma once
 
+#include "row_grid.h"
 #include "vocab_rows.cuh"
 
 namespace swg {
@@ -278,46 +279,54 @@ __device__ __forceinline__ void send_u64(const uint64_t* to, const uint64_t* bar
 
 }  // namespace row
 
-// A persistent launch: as many clusters as fit on the device at once, at most one a row (`all`: one for
-// every row, however many fit; multiple: where rows are shared out to fewer clusters, their number is one of
-// it). The occupancy of a (kernel, cluster size, block, shared memory) is asked once for each device.
+// How many clusters of a persistent kernel fit on the device at once: of a (cluster size, block, shared memory)
+// asked once for each device.
 struct StreamCache {
   int device = -1, S = 0, threads = 0, clusters = 0;
   size_t smem = 0;
-  int64_t launched = 0;  // clusters of the last launch
 };
-template <typename Kernel, typename... Args>
-cudaError_t launch_stream(Kernel kernel, StreamCache& cache, int threads, size_t smem, int64_t rows, int S,
-                          bool all, int multiple, cudaStream_t stream, const Args&... args) {
+struct ClusterLaunch {  // a launch of `clusters` clusters of S blocks
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  ClusterLaunch(int threads, size_t smem, int S, int64_t clusters, cudaStream_t stream) {
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * S));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  ClusterLaunch(const ClusterLaunch&) = delete;
+};
+template <typename Kernel>
+cudaError_t clusters_that_fit(Kernel kernel, StreamCache& cache, int threads, size_t smem, int S) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(S);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cache.device != dev || cache.S != S || cache.threads != threads || cache.smem != smem) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(S));
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-    if (e != cudaSuccess) return e;
-    if (n < 1) return cudaErrorLaunchOutOfResources;
-    cache = StreamCache{dev, S, threads, n, smem};
-  }
-  const int64_t fit = cache.clusters > multiple ? cache.clusters / multiple * multiple : cache.clusters;
-  const int64_t clusters = all || rows < fit ? rows : fit;
-  cache.launched = clusters;
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * S));
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (cache.device == dev && cache.S == S && cache.threads == threads && cache.smem == smem) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  ClusterLaunch one(threads, smem, S, 1, nullptr);
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, kernel, &one.cfg);
+  if (e != cudaSuccess) return e;
+  cache = StreamCache{dev, S, threads, n, smem};
+  return cudaSuccess;
+}
+// A persistent launch for `rows` rows: as many clusters as fit, at most one a row (`all`: one for every row,
+// however many fit).
+template <typename Kernel, typename... Args>
+cudaError_t launch_stream(Kernel kernel, StreamCache& cache, int threads, size_t smem, int64_t rows, int S,
+                          bool all, cudaStream_t stream, const Args&... args) {
+  const cudaError_t e = clusters_that_fit(kernel, cache, threads, smem, S);
+  if (e != cudaSuccess) return e;
+  if (cache.clusters < 1) return cudaErrorLaunchOutOfResources;
+  ClusterLaunch l(threads, smem, S, all ? rows : persistent_blocks(cache.clusters, rows, 1), stream);
+  return cudaLaunchKernelEx(&l.cfg, kernel, args...);
 }
 
 }  // namespace swg
