@@ -123,7 +123,15 @@ swg_status swg_check(swg_stream_t stream);
  *           swiglu_bwd_x_fused and the fused swiglu_bwd) or SWG_INJECT_FUSED_W
  *           (the fused w kernel on CTA pairs, swiglu_bwd_w_fused and the fused
  *           swiglu_bwd: both CTAs' producers stop at the entry) or SWG_INJECT_FWD
- *           (the forward on CTA pairs, swiglu_fwd: both producers stop).
+ *           (the forward on CTA pairs, swiglu_fwd: both producers stop). Of the
+ *           row-wise operators' kernels that wait: SWG_INJECT_TOKEN_LOGPROBS
+ *           (token_logprobs_fwd) and SWG_INJECT_DISTILL (distill_fwd,
+ *           distill_fwd_bwd), whose last producer of each cluster stops (a
+ *           block by itself is one), and, where a cluster shares a row,
+ *           SWG_INJECT_LAYER_NORM_FWD and SWG_INJECT_LAYER_NORM_BWD, whose last
+ *           block of each cluster sends no sums from row `entry` on. Their blocks
+ *           go on to the end of their rows; a thread sends nothing behind a wait
+ *           that ran out, and no block leaves before what was sent to it has come.
  * SWG_INJECT_NONE disarms an armed, unused injection (entry and limit are then
  * ignored); a later call replaces it. Returns SWG_ERR_PARAM_INVALID for another
  * kernel, entry < 0 or a limit below 1024 cycles. For tests only. */
@@ -132,7 +140,11 @@ typedef enum {
   SWG_INJECT_X_GEMM = 1,
   SWG_INJECT_FUSED_X = 2,
   SWG_INJECT_FUSED_W = 3,
-  SWG_INJECT_FWD = 4
+  SWG_INJECT_FWD = 4,
+  SWG_INJECT_LAYER_NORM_FWD = 16,
+  SWG_INJECT_LAYER_NORM_BWD = 17,
+  SWG_INJECT_TOKEN_LOGPROBS = 18,
+  SWG_INJECT_DISTILL = 19
 } swg_inject_kernel;
 swg_status swg_inject_stall(swg_inject_kernel kernel, int64_t entry, int64_t wait_limit_cycles);
 

@@ -272,6 +272,10 @@ SWG_INJECT_X_GEMM = 1
 SWG_INJECT_FUSED_X = 2
 SWG_INJECT_FUSED_W = 3
 SWG_INJECT_FWD = 4
+SWG_INJECT_LAYER_NORM_FWD = 16
+SWG_INJECT_LAYER_NORM_BWD = 17
+SWG_INJECT_TOKEN_LOGPROBS = 18
+SWG_INJECT_DISTILL = 19
 
 
 def swg_inject_stall(kernel: int, entry: int, wait_limit_cycles: int) -> None:

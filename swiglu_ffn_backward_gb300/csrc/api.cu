@@ -101,7 +101,8 @@ swg_status swg_inject_stall(swg_inject_kernel kernel, int64_t entry, int64_t wai
     return SWG_OK;
   }
   if (kernel != SWG_INJECT_X_GEMM && kernel != SWG_INJECT_FUSED_X && kernel != SWG_INJECT_FUSED_W &&
-      kernel != SWG_INJECT_FWD)
+      kernel != SWG_INJECT_FWD && kernel != SWG_INJECT_LAYER_NORM_FWD && kernel != SWG_INJECT_LAYER_NORM_BWD &&
+      kernel != SWG_INJECT_TOKEN_LOGPROBS && kernel != SWG_INJECT_DISTILL)
     return SWG_ERR_PARAM_INVALID;
   if (entry < 0 || wait_limit_cycles < 1024) return SWG_ERR_PARAM_INVALID;
   swg::arm_injection(static_cast<int>(kernel), entry, static_cast<long long>(wait_limit_cycles));

@@ -242,7 +242,7 @@ __device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g,
 
 template <typename T, bool kGrad, int W, bool kLong>  // kLong: as in WarpSums (with a gradient a share is short)
 __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
-    kd_fwd_kernel(const KdArgs a, Split split, int stages, int slots, uint32_t* status) {
+    kd_fwd_kernel(const KdArgs a, Split split, int stages, int slots, Stall stall, uint32_t* status) {
   constexpr int E = Traits<T>::E;
   constexpr int kStreamThreads = Shape<W>::kThreads, kStageVecs = Shape<W>::kStageVecs;
   constexpr int kStageBytes = Shape<W>::kStageBytes;
@@ -269,11 +269,12 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
   __syncthreads();
   cluster_arrive();
   cluster_wait();
-  Patience wait;
+  Patience wait(stall.limit, S);
   const float c2 = a.inv_temp * kLog2e;
 
   if (warp == W) {
-    produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, stages, sm.ring, wait);
+    produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, stages, sm.ring, wait,
+                       rank == S - 1 ? stall.at : -1);
   } else if (warp == W + 1 || warp == W + 2) {
     // the teachers take the entries of every other row each; the sparse part of a row comes after the
     // entries of the teacher's next one, so nothing waits for it
@@ -326,13 +327,14 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
         sm.weight[slot] = w;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.ready[slot]);
+      if (lane == 0 && !wait.lost()) mbar_arrive(&sm.ready[slot]);
       // A gradient over the logits may be written once the first block has read them here. Row it - 2 has
       // been joined here, so every block has been through row it - 4 and its barrier of this slot is set
       // for this row.
       if (rank == 0 && it >= 2)
         wait(&sm.spare[(it - 2) & (kSlots - 1)], static_cast<uint32_t>(((it - 2) / kSlots) & 1));
-      if (rank == 0 && lane < S) send_f2(&sm.note[slot], &sm.joined[slot], static_cast<uint32_t>(lane), 0.f, 0.f);
+      if (rank == 0 && lane < wait.open)
+        send_f2(&sm.note[slot], &sm.joined[slot], static_cast<uint32_t>(lane), 0.f, 0.f);
       __syncwarp();
       if (kGrad) {
         if (r != begin) sparse(r - 2 * step, it - 2, mine, shared);
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       const int slot = static_cast<int>(it & (kSlots - 1));
       const uint32_t parity = static_cast<uint32_t>((it / kSlots) & 1);
       wait.cluster(&sm.joined[slot], parity);
-      if (lane == 0) mbar_arrive_expect_tx(&sm.joined[slot], bytes);
+      if (lane == 0 && !wait.lost()) mbar_arrive_expect_tx(&sm.joined[slot], bytes);
       // lane by lane (up to four parts each), then the lanes
       const float4* part = &sm.part[slot][0][0];
       float m = neg_inf(), s = 0.f, top = neg_inf();
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
       const float sq = sm.sq[slot];
       if (lane == 0) {
         if (kGrad) sm.grad[slot] = make_gradient(a, k, s, sm.weight[slot], sq);
-        mbar_arrive(&sm.solved[slot]);
+        if (!wait.lost()) mbar_arrive(&sm.solved[slot]);
       }
       if (rank == 0) {
         // sum q (ln q - ln p) = sum (q / tau) (td - (z - max z)) - ln sq + ln s: a mask of the type's
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.spare[slot]);
+      if (lane == 0 && !wait.lost()) mbar_arrive(&sm.spare[slot]);
     }
   } else {
     Place in, held;  // the next stage to read, and (with a gradient) the next one of the row before
@@ -406,12 +408,12 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
         }
         if (!kGrad) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.ring.empty[in.stage]);
+          if (lane == 0 && !wait.lost()) mbar_arrive(&sm.ring.empty[in.stage]);
         }
         in.next(stages);
       }
       const float4 p = sum.result();
-      if (lane < S) send_f4(&sm.part[slot][rank][warp], &sm.joined[slot], static_cast<uint32_t>(lane), p);
+      if (lane < wait.open) send_f4(&sm.part[slot][rank][warp], &sm.joined[slot], static_cast<uint32_t>(lane), p);
       __syncwarp();
     };
     // The gradient of row r, the it-th of the block. Without a gradient only the wait is left: a warp is
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
         const int cnt = min(sh.end - c, kStageVecs);
         read_stage<T, W>(v, dyn + held.stage * kStageBytes, cnt);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ring.empty[held.stage]);
+        if (lane == 0 && !wait.lost()) mbar_arrive(&sm.ring.empty[held.stage]);
         held.next(stages);
         const int64_t e0 = first_element<T>(sh, c), e1 = first_element<T>(sh, c + cnt);
         T* to = out + e0 + tid * E;
@@ -464,9 +466,10 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
     if (it > 0) finish(first + (it - 1) * step, it - 1);
   }
   __syncwarp();
-  if (wait.lost && status != nullptr) atomicOr(status, kStatusTimeout);
+  if (wait.lost() && status != nullptr) atomicOr(status, kStatusTimeout);
   cluster_arrive();  // no block leaves while another may still write to it
   cluster_wait();
+  wait.leave();
 }
 
 template <typename T, bool kGrad, int W, bool kLong>
@@ -478,7 +481,7 @@ cudaError_t launch_fwd(const KdArgs& a, Split split, cudaStream_t stream) {
   const size_t smem = stages * Shape<W>::kStageBytes + entry_bytes(a.K) + static_cast<size_t>(2) * slots * sizeof(int);
   std::lock_guard<std::mutex> lk(mu);
   return launch_stream(kd_fwd_kernel<T, kGrad, W, kLong>, cache, 32 * (W + kExtraWarps), smem, a.T, split.S, false,
-                       stream, a, split, stages, slots, status_word_ptr());
+                       stream, a, split, stages, slots, take_stall(kInjectDistill), status_word_ptr());
 }
 template <bool kGrad, int W, bool kLong>
 cudaError_t launch_fwd_any(const KdArgs& a, int dtype, Split split, cudaStream_t stream) {

@@ -258,7 +258,8 @@ struct ClusterSum {
   int S, rank, turn = 0;
   uint32_t parity = 0;
   Patience wait;
-  __device__ __forceinline__ ClusterSum(ClusterSlots& s, int S_) : slots(s), S(S_), rank(cluster_ctarank()) {
+  __device__ __forceinline__ ClusterSum(ClusterSlots& s, int S_, const Stall& stall)
+      : slots(s), S(S_), rank(cluster_ctarank()), wait(stall.limit, S_) {
     if (threadIdx.x == 0) {
       mbar_init(&slots.come[0], 1);
       mbar_init(&slots.come[1], 1);
@@ -270,8 +271,9 @@ struct ClusterSum {
   }
   __device__ __forceinline__ void operator()(float (&v)[kSums]) {
     uint64_t* come = &slots.come[turn];
-    if (threadIdx.x == 0) mbar_arrive_expect_tx(come, static_cast<uint32_t>(S) * sizeof(float2));
-    if (static_cast<int>(threadIdx.x) < S) send_f2(&slots.sums[turn][rank], come, threadIdx.x, v[0], v[kSums - 1]);
+    if (threadIdx.x == 0 && !wait.lost()) mbar_arrive_expect_tx(come, static_cast<uint32_t>(S) * sizeof(float2));
+    if (static_cast<int>(threadIdx.x) < wait.open)
+      send_f2(&slots.sums[turn][rank], come, threadIdx.x, v[0], v[kSums - 1]);
     __syncwarp();
     wait.cluster(come, parity);
     float2 t = make_float2(0.f, 0.f);
@@ -285,16 +287,21 @@ struct ClusterSum {
     parity ^= turn == 0 ? 1u : 0u;
   }
   __device__ __forceinline__ void end(uint32_t* status) {  // no block leaves while another may still write to it
-    if (wait.lost && status != nullptr) atomicOr(status, kStatusTimeout);
+    if (wait.lost() && status != nullptr) atomicOr(status, kStatusTimeout);
     cluster_arrive();
     cluster_wait();
+    wait.leave();
+  }
+  __device__ __forceinline__ void silence() {  // for tests: the last block sends nothing any more
+    if (rank == S - 1) wait.open = 0;
   }
 };
 // groups that are blocks of their own have nothing to join
 template <int kSums>
 struct NoSum {
-  __device__ __forceinline__ NoSum(ClusterSlots&, int) {}
+  __device__ __forceinline__ NoSum(ClusterSlots&, int, const Stall&) {}
   __device__ __forceinline__ void operator()(float (&)[kSums]) {}
+  __device__ __forceinline__ void silence() {}
   __device__ __forceinline__ void end(uint32_t*) {}
 };
 template <bool kShared, int kSums>
@@ -311,7 +318,7 @@ template <bool kRagged>
 constexpr int kFwdRegs = kRagged ? 128 : 80;
 template <typename T, int R, bool kRagged, bool kShared>
 __global__ void __maxnreg__(kFwdRegs<kRagged>)
-    ln_fwd_kernel(const LnFwdArgs a, int G, int S, uint32_t* status) {
+    ln_fwd_kernel(const LnFwdArgs a, int G, int S, Stall stall, uint32_t* status) {
   __shared__ float smem[2 * 32];
   __shared__ ClusterSlots slots;
   constexpr int E = kElems<T>, P = kPairs<T>;
@@ -350,12 +357,13 @@ __global__ void __maxnreg__(kFwdRegs<kRagged>)
       if (t + i * G < n) weights(i, i);
   }
   GroupSum<1, kNarrow> sum(smem, G);
-  SharedSum<kShared, 1> join(slots, S);
+  SharedSum<kShared, 1> join(slots, S, stall);
   Row next;
   const int64_t M = a.M + (kNarrow ? (threadIdx.x & 31) / G : 0);  // the rows of a warp's groups end together
   if (r < a.M) load(next, r);
   for (; r < M; r += step) {
     if (kNarrow && r >= a.M) n = 0;
+    if (kShared && static_cast<uint64_t>(r) >= static_cast<uint64_t>(stall.at)) join.silence();
     Row w = next;
     if (r + step < a.M) load(next, r + step);
     if constexpr (kRagged) {
@@ -499,7 +507,7 @@ __global__ void __launch_bounds__(kMaxThreads) ln_fwd_long_kernel(const LnFwdArg
 // instead of 559). Rows are counted in 32 bits for the same reason.
 template <typename T, int R, bool kRagged, bool kShared, bool kFold>
 __global__ void __launch_bounds__(kMaxGroup)
-    ln_bwd_kernel(const LnBwdArgs a, int G, int S, int fold, uint32_t* status) {
+    ln_bwd_kernel(const LnBwdArgs a, int G, int S, int fold, Stall stall, uint32_t* status) {
   extern __shared__ __align__(16) float dyn[];  // the slots; then, with several groups a block, 2 N column sums
   __shared__ float smem[2 * 2 * 32];
   __shared__ ClusterSlots slots;
@@ -543,7 +551,7 @@ __global__ void __launch_bounds__(kMaxGroup)
     }
   };
   GroupSum<2, kNarrow> sum(smem, G);
-  SharedSum<kShared, 2> join(slots, S);
+  SharedSum<kShared, 2> join(slots, S, stall);
   auto slot = [&](int i, int e) -> float4& {  // of pair e of the thread's vector i
     return reinterpret_cast<float4*>(dyn)[(i * P + e) * blockDim.x + threadIdx.x];
   };
@@ -576,6 +584,7 @@ __global__ void __launch_bounds__(kMaxGroup)
     if (r < rows) load(next, r);
     for (; r < stop; r += step) {
       if (kNarrow && r >= rows) n = 0;
+      if (kShared && static_cast<uint64_t>(r) >= static_cast<uint64_t>(stall.at)) join.silence();
       Row w = next;
       if ((!kRuns || r + step < stop) && ((kRuns && !kNarrow) || r + step < rows)) load(next, r + step);
       if constexpr (kRagged) {
@@ -869,7 +878,7 @@ cudaError_t fwd_one(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
   }
   blocks = persistent_blocks(blocks, (a.M + groups - 1) / groups, kRagged ? rows_apart<T>(a.N) : 1);
   if (blocks == 0) return fwd_long<T>(a, stream);
-  ln_fwd_kernel<T, R, kRagged, false><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a, G, 1, nullptr);
+  ln_fwd_kernel<T, R, kRagged, false><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a, G, 1, Stall(), nullptr);
   return cudaGetLastError();
 }
 template <typename T, bool kRagged>
@@ -884,7 +893,7 @@ cudaError_t fwd_shared(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
   const int64_t clusters = persistent_blocks(cache.clusters, a.M, kRagged ? rows_apart<T>(a.N) : 1);
   if (clusters == 0) return fwd_long<T>(a, stream);
   ClusterLaunch l(p.G, 0, p.S, clusters, stream);
-  return cudaLaunchKernelEx(&l.cfg, kernel, a, p.G, p.S, status_word_ptr());
+  return cudaLaunchKernelEx(&l.cfg, kernel, a, p.G, p.S, take_stall(kInjectLayerNormFwd), status_word_ptr());
 }
 // Vectors a thread: one for rows of up to a warp, else two. Rows of more than 1024 vectors are shared by a
 // cluster: 3000 x 12288 bf16 with residual 70 us, 88 by a block with four vectors a thread; backward with dh
@@ -969,7 +978,7 @@ cudaError_t bwd_groups(const LnBwdArgs& a, int G, int groups, int fold, cudaStre
   blocks = persistent_blocks(blocks, (a.M + groups - 1) / groups, kRagged ? rows_apart<T>(a.N) : 1);
   if (blocks == 0) return bwd_long<T>(a, stream);
   ln_bwd_kernel<T, R, kRagged, false, kFold>
-      <<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, G, 1, fold, nullptr);
+      <<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, G, 1, fold, Stall(), nullptr);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.part == nullptr) return e;
   return launch_reduce(a, blocks, stream);
@@ -999,7 +1008,7 @@ cudaError_t bwd_clusters(const LnBwdArgs& a, const Shared& p, int fold, cudaStre
     clusters = persistent_blocks(cache.clusters, a.M, kRagged ? rows_apart<T>(a.N) : 1);
     if (clusters > 0) {
       ClusterLaunch l(p.G, smem, p.S, clusters, stream);
-      e = cudaLaunchKernelEx(&l.cfg, kernel, a, p.G, p.S, fold, status_word_ptr());
+      e = cudaLaunchKernelEx(&l.cfg, kernel, a, p.G, p.S, fold, take_stall(kInjectLayerNormBwd), status_word_ptr());
       if (e != cudaSuccess) return e;
     }
   }

@@ -150,10 +150,11 @@ struct KdArgs {
 cudaError_t launch_distill(const KdArgs& a, bool forward, bool backward, int dtype, cudaStream_t stream);
 
 // one-shot fault injection for tests of the timeout path (swg_inject_stall): the next
-// launch of `kernel` (1 = x GEMM, 2 = fused x) stops issuing operand copies at ring
-// entry `stall_at` and gives every pipeline wait `wait_limit` cycles. take_injection
+// launch of `kernel` (1 = x GEMM, 2 = fused x, 3 = fused w, 4 = forward, and those below) stops
+// issuing copies at ring entry `stall_at` and gives every wait `wait_limit` cycles. take_injection
 // returns the values for that launch (stall_at -1 and the normal limit when none is armed)
 // and disarms it.
+constexpr int kInjectLayerNormFwd = 16, kInjectLayerNormBwd = 17, kInjectTokenLogprobs = 18, kInjectDistill = 19;
 struct Injection {
   int64_t stall_at;
   long long wait_limit;

@@ -239,7 +239,7 @@ static_assert(Plan<16>::kTableBytes / 2 <= 65536, "16-bit groups");
 
 template <typename T, int W, bool kLong>  // kLong: as in WarpSums
 __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 3)
-    tlp_fwd_kernel(const TlpFwdArgs a, Split split, uint32_t* status) {
+    tlp_fwd_kernel(const TlpFwdArgs a, Split split, Stall stall, uint32_t* status) {
   constexpr int kStageVecs = Shape<W>::kStageVecs, kStageBytes = Shape<W>::kStageBytes, kThreads = Shape<W>::kThreads;
   constexpr int kStages = Plan<W>::kStages, kSelectors = Plan<W>::kSelectors;
   extern __shared__ __align__(128) unsigned char dyn[];
@@ -264,10 +264,11 @@ __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 3)
   __syncthreads();
   cluster_arrive();
   cluster_wait();
-  Patience wait;
+  Patience wait(stall.limit);
 
   if (warp == W) {
-    produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, kStages, sm.ring, wait);
+    produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, kStages, sm.ring, wait,
+                       rank == S - 1 ? stall.at : -1);
   } else if (warp > W) {
     const int me = warp - W - 1;
     Finish<W>& f = finish[me];
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 3)
         taken();
       }
       uint64_t mine = lane < n ? f.best[rank][lane] : 0;  // lane i: the i-th best
-      if (Plan<W>::kBlocks > 1 && rank != 0) {
+      if (Plan<W>::kBlocks > 1 && rank != 0) {  // once, whatever was lost: the first block has one row to hear of
         if (lane == 0) send_f4(&f.block[rank], &sm.sent, 0, p);
         send_u64(&f.best[rank][lane], &sm.sent, 0, mine);
         continue;
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 3)
           group_most = neg_inf();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ring.empty[in.stage]);
+        if (lane < wait.open) mbar_arrive(&sm.ring.empty[in.stage]);
         in.next(kStages);
       }
       const float4 p = sums.result();
@@ -399,9 +400,10 @@ __global__ void __launch_bounds__(Plan<W>::kThreads, W == 16 ? 1 : 3)
     }
   }
   __syncwarp();
-  if (wait.lost && status != nullptr) atomicOr(status, kStatusTimeout);
+  if (wait.lost() && status != nullptr) atomicOr(status, kStatusTimeout);
   cluster_arrive();  // no block leaves while another may still write to it
   cluster_wait();
+  wait.leave();
 }
 static_assert(kMaxTop == 32, "one lane for each alternative");
 
@@ -412,7 +414,7 @@ cudaError_t launch_fwd(const TlpFwdArgs& a, Split split, cudaStream_t stream) {
   std::lock_guard<std::mutex> lk(mu);
   // a cluster of several blocks takes one row
   return launch_stream(tlp_fwd_kernel<T, W, kLong>, cache, Plan<W>::kThreads, kFwdSmem<W>, a.T, split.S,
-                       split.S > 1, stream, a, split, status_word_ptr());
+                       split.S > 1, stream, a, split, take_stall(kInjectTokenLogprobs), status_word_ptr());
 }
 template <int W, bool kLong>
 cudaError_t launch_fwd_any(const TlpFwdArgs& a, int dtype, Split split, cudaStream_t stream) {

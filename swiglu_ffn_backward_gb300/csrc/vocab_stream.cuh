@@ -21,17 +21,32 @@ struct Shape {
   static constexpr int kStageBytes = 16 * kStageVecs;
 };
 
-// Waits are bounded: after the first one that ran out, the later ones of the thread only look once, so
-// that the block still comes to its end (its results are then void and the status word says so).
+// What a launch is told for tests of the waits that run out: the ring entry (or row) from which on the last block of
+// each cluster falls silent (-1: none), and the cycles that a wait takes at most.
+struct Stall {
+  int64_t at = -1;
+  uint32_t limit = kWaitLimitCycles;
+};
+
+// Waits are bounded. After one that ran out the thread's later waits only look once, so that the block still comes
+// to its end (its results are then void and the status word says so). A barrier that counts bytes must not be set
+// or fed out of turn by then, or its counts are overrun: such a thread arrives at no barrier that others send or
+// copy behind, and sends nothing. Hence `open`, the lanes that may (the peers to send to, or one): 0 once a wait
+// has run out. The clock is read in 32 bits, which hold the limit: with 64 the waiting warps took 2% of the log
+// probabilities' time at 8192 to 50001 columns, and a flag beside the number of peers 3% of a distillation step.
 struct Patience {
-  bool lost = false;
+  uint32_t limit;
+  int open;
+  __device__ __forceinline__ explicit Patience(uint32_t limit_, int open_ = 1) : limit(limit_), open(open_) {}
+  __device__ __forceinline__ bool lost() const { return open == 0; }
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (!mbar_wait(bar, parity, lost ? 0 : kWaitLimitCycles)) lost = true;
+    const uint32_t at = smem_u32(bar);
+    until([&]() { return mbar_try_wait(at, parity); });
   }
   // of a barrier that other blocks of the cluster complete: what they wrote is visible after it
   __device__ __forceinline__ void cluster(uint64_t* bar, uint32_t parity) {
     const uint32_t at = smem_u32(bar);
-    auto done = [&]() {
+    until([&]() {
       uint32_t ok;
       asm volatile(
           "{\n\t.reg .pred p;\n\t"
@@ -41,16 +56,30 @@ struct Patience {
           : "r"(at), "r"(parity)
           : "memory");
       return ok != 0;
-    };
+    });
+  }
+  // After a wait that ran out, at the end of the kernel behind the cluster's last barrier, when no block sends any
+  // more: what was sent before is given half a millisecond to come (it takes some microseconds), so that no block
+  // leaves while something is on its way into it. A block whose waits all ended has received everything.
+  __device__ __forceinline__ void leave() const {
+    if (!lost()) return;
+    const uint32_t t0 = static_cast<uint32_t>(clock());
+    while (static_cast<uint32_t>(clock()) - t0 < (1u << 20)) __nanosleep(1000);
+  }
+
+ private:
+  template <typename Done>
+  __device__ __forceinline__ void until(Done done) {
     if (done()) return;
-    const long long t0 = clock64();
+    const uint32_t t0 = static_cast<uint32_t>(clock());
     while (!done())
-      if (clock64() - t0 > (lost ? 0 : kWaitLimitCycles)) {
-        lost = true;
+      if (static_cast<uint32_t>(clock()) - t0 > (lost() ? 0u : limit)) {
+        open = 0;
         return;
       }
   }
 };
+static_assert(kWaitLimitCycles < (1LL << 32) - (1LL << 27), "the clock's low half");
 
 template <int W, int N>  // up to N stages
 struct Ring {
@@ -77,11 +106,11 @@ struct Place {
 };
 
 // The producer warp: all rows of the block's cluster, row r's share at `rank` of S. It issues no more copies
-// once a wait has run out, and ends when the copies it has issued have landed.
+// once a wait has run out (or from ring entry `stall` on), and ends when the copies it has issued have landed.
 template <typename T, int W, int N>
 __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int64_t V, int64_t first, int64_t rows,
                                              int64_t step, int per, int rank, unsigned char* buf, int stages,
-                                             Ring<W, N>& ring, Patience& wait) {
+                                             Ring<W, N>& ring, Patience& wait, int64_t stall) {
   constexpr int E = Traits<T>::E, kStageVecs = Shape<W>::kStageVecs, kStageBytes = Shape<W>::kStageBytes;
   const int lane = threadIdx.x & 31;
   const T* base = static_cast<const T*>(logits);
@@ -111,7 +140,7 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
       const int end = min(sh.end, c + kStageVecs);
       unsigned char* to = buf + p.stage * kStageBytes;
       wait(&ring.empty[p.stage], p.parity ^ 1u);
-      go = !__any_sync(0xffffffffu, wait.lost);
+      go = !__any_sync(0xffffffffu, wait.lost()) && stall-- != 0;
       if (!go) break;
       const int w0 = max(c, whole0), w1 = min(end, whole1);
       // a partial vector's elements, lane by lane
@@ -132,7 +161,7 @@ __device__ __forceinline__ void produce_rows(const void* logits, int64_t ld, int
     mine = ahead;
   }
   for (int i = 0; i < stages; ++i)  // the last use of every stage; one that has had none is done
-    if (!mbar_wait(&ring.full[i], i < p.stage ? p.parity : p.parity ^ 1u)) wait.lost = true;
+    if (!mbar_wait(&ring.full[i], i < p.stage ? p.parity : p.parity ^ 1u)) wait.open = 0;
 }
 
 // a computing thread's four vectors of a stage that holds n; -inf past them
@@ -278,6 +307,15 @@ __device__ __forceinline__ void send_u64(const uint64_t* to, const uint64_t* bar
 }
 
 }  // namespace row
+
+// what the next launch of `kernel` is told (one launch)
+inline row::Stall take_stall(int kernel) {
+  const Injection i = take_injection(kernel);
+  row::Stall s;
+  s.at = i.stall_at;
+  if (i.wait_limit < kWaitLimitCycles) s.limit = static_cast<uint32_t>(i.wait_limit);
+  return s;
+}
 
 // How many clusters of a persistent kernel fit on the device at once: of a (cluster size, block, shared memory)
 // asked once for each device.
