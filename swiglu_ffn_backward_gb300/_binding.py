@@ -588,6 +588,26 @@ def _run(what, fn, dev, *args):
         _check(status, what)
 
 
+def _row_distance(t):
+    """The one distance in elements between rows of t [..., N] that follow one another (0: one shared row),
+    or None where rows lie at several distances, overlap, or have their elements apart."""
+    shape, strides = t.shape, t.stride()
+    N, ld, span = shape[-1], None, None
+    if N > 1 and strides[-1] != 1:
+        return None
+    for size, stride in zip(shape[-2::-1], strides[-2::-1]):  # the last leading dimension first
+        if size == 1:
+            continue
+        if ld is None:
+            ld = stride
+        elif stride != span:
+            return None
+        span = stride * size
+    if ld is None:
+        return N
+    return ld if ld >= N or ld == 0 else None
+
+
 def _row_tensor(t, name):
     """A tensor [..., N] as the kernels take it: (tensor, rows, N, row stride in elements, dtype code).
     Rows may lie apart (a slice of wider rows) or be one shared row; anything else is copied."""
@@ -607,10 +627,13 @@ def _row_tensor(t, name):
     if t.dim() == 0:
         raise ValueError(f"{name} must have at least one dimension")
     N = t.shape[-1]
-    M = 1
-    for d in t.shape[:-1]:
-        M *= d
-    return t.contiguous(), M, N, N, code
+    M = math.prod(t.shape[:-1])
+    if t.is_contiguous():
+        return t, M, N, N, code
+    ld = _row_distance(t)
+    if ld is None:
+        t, ld = t.contiguous(), N
+    return t, M, N, ld, code
 
 
 def _like_rows(t, name, x, ldx, shape):
@@ -771,8 +794,9 @@ def _dlogits(t, shape, x, M, N):
     if isinstance(t, torch.Tensor) and t.is_cuda and t.device == x.device and t.dtype == x.dtype and t.shape == shape:
         if t.is_contiguous():
             return t, N
-        if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= N:
-            return t, t.stride(0)
+        ld = _row_distance(t)
+        if ld is not None and ld >= N:
+            return t, ld
     raise ValueError(f"dlogits must be a {x.dtype} CUDA tensor of shape {tuple(shape)} on {x.device} with dense rows")
 
 
