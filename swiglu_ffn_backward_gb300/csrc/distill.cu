@@ -147,7 +147,7 @@ template <typename T>
 __device__ __forceinline__ float take_entries(const KdArgs& a, int64_t r, EntryValues<T>& v, const EntryArrays& n,
                                               int64_t e0, int64_t e1) {
   const int lane = threadIdx.x & 31;
-  const float c2 = a.inv_temp * kLog2e;
+  const float c2 = exponent_scale(a.inv_temp);
   float m = neg_inf();
   for (int k0 = 0;;) {
 #pragma unroll
@@ -222,7 +222,7 @@ template <typename T>
 __device__ __forceinline__ void store_sparse(const KdArgs& a, const Gradient& g, const EntryArrays& n, uint32_t mine,
                                              uint32_t shared, T* out) {
   const int lane = threadIdx.x & 31;
-  const float c2 = a.inv_temp * kLog2e;
+  const float c2 = exponent_scale(a.inv_temp);
   for (int k0 = 0; k0 < a.K; k0 += 32) {
     const bool own = mine >> (k0 / 32) & 1u;
     const int id = own ? n.id[k0 + lane] : -1;
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(32 * (W + kExtraWarps), W == 16 ? 1 : 3)
   cluster_arrive();
   cluster_wait();
   Patience wait(stall.limit, S);
-  const float c2 = a.inv_temp * kLog2e;
+  const float c2 = exponent_scale(a.inv_temp);
 
   if (warp == W) {
     produce_rows<T, W>(a.logits, a.ld, a.V, first, a.T, step, split.per, rank, dyn, stages, sm.ring, wait,
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, 4)
   T* out = static_cast<T*>(a.dlogits) + r * a.ldo;
   const Share sh = share_of(z, a.V, p.per, static_cast<int>(at - r * p.S));
   const bool aligned = row_shift(out) == sh.shift;
-  const float w = a.weight[r], c2 = a.inv_temp * kLog2e;
+  const float w = a.weight[r], c2 = exponent_scale(a.inv_temp);
   if (w == 0.0f) {
     const Vec zero = {{0u, 0u, 0u, 0u}};
     for (int g = sh.begin + tid; g < sh.end && tid < p.G; g += p.G)

@@ -267,6 +267,10 @@ __device__ __forceinline__ float at_least(float x) {
 // below -32, so 2^x is 1 at the maximum and 0 elsewhere to all digits kept: c is then a power of two that
 // puts |m c| in [2^40, 2^41), exactly.
 constexpr float kLargeRef = 1073741824.0f;
+// c of an inverse temperature, finite: a difference of 0 stays one at the smallest temperatures (below 4.3e-39)
+__device__ __forceinline__ float exponent_scale(float inv_temp) {
+  return fminf(inv_temp * kLog2e, 3.4028234663852886e38f);
+}
 struct Scale {
   float c, ref;
 };
