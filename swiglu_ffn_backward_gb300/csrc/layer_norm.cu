@@ -944,8 +944,16 @@ constexpr size_t fold_bytes(int threads) {
   return static_cast<size_t>(threads) * R * kPairs<T> * sizeof(float4);
 }
 
-constexpr int64_t kMaxBlocks = 4 * 256;  // rows of column sums in the workspace, at most
-constexpr int64_t kLongChunks = 64;      // of them for rows too long for registers
+// Rows of column sums in the workspace, at most, for rows of n vectors; no more for longer rows. Groups of up to a
+// warp: several blocks an SM. To 1024 vectors: one block of 512 threads an SM, or for few rows up to twice as many
+// smaller ones. Shared rows: clusters of S blocks, two blocks an SM. Longer ones: chunks.
+constexpr int64_t kLongChunks = 64;
+int64_t most_sums(int64_t n) {
+  if (n <= 32) return 1024;
+  if (n <= 2 * kMaxGroup) return 320;
+  if (n <= kMostShared) return std::max(kLongChunks, static_cast<int64_t>((320 / share_row(n).S + 7) / 8 * 8));
+  return kLongChunks;
+}
 
 template <typename T>
 cudaError_t bwd_long(const LnBwdArgs& a, cudaStream_t stream) {
@@ -962,7 +970,7 @@ cudaError_t bwd_long(const LnBwdArgs& a, cudaStream_t stream) {
   return e != cudaSuccess ? e : launch_reduce(a, chunks, stream);
 }
 template <typename T, int R, bool kRagged, bool kFold>
-cudaError_t bwd_groups(const LnBwdArgs& a, int G, int groups, int fold, cudaStream_t stream) {
+cudaError_t bwd_groups(const LnBwdArgs& a, int64_t n, int G, int groups, int fold, cudaStream_t stream) {
   const int block = groups * G;
   const size_t sums = groups > 1 && a.part != nullptr ? static_cast<size_t>(2 * a.N) * sizeof(float) : 0;
   const size_t smem = kFold ? std::max(sums, fold_bytes<T, R>(block)) : sums;
@@ -974,8 +982,8 @@ cudaError_t bwd_groups(const LnBwdArgs& a, int G, int groups, int fold, cudaStre
     const cudaError_t e = blocks_that_fit(ln_bwd_kernel<T, R, kRagged, false, kFold>, cache, block, smem, blocks);
     if (e != cudaSuccess) return e;
   }
-  if (blocks > kMaxBlocks) blocks = kMaxBlocks;
-  blocks = persistent_blocks(blocks, (a.M + groups - 1) / groups, kRagged ? rows_apart<T>(a.N) : 1);
+  blocks = persistent_blocks(std::min(blocks, most_sums(n)), (a.M + groups - 1) / groups,
+                             kRagged ? rows_apart<T>(a.N) : 1);
   if (blocks == 0) return bwd_long<T>(a, stream);
   ln_bwd_kernel<T, R, kRagged, false, kFold>
       <<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, G, 1, fold, Stall(), nullptr);
@@ -991,11 +999,11 @@ cudaError_t bwd_one(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {
   int groups = kMaxGroup / G;
   while (groups > 1 && groups * G > 32 && (a.M + groups - 1) / groups < device_sm_count()) groups = (groups + 1) / 2;
   const int fold = a.part != nullptr ? fold_rows(a.M, static_cast<int64_t>(groups) * device_sm_count()) : 0;
-  return fold > 0 ? bwd_groups<T, R, kRagged, true>(a, G, groups, fold, stream)
-                  : bwd_groups<T, R, kRagged, false>(a, G, groups, 0, stream);
+  return fold > 0 ? bwd_groups<T, R, kRagged, true>(a, n, G, groups, fold, stream)
+                  : bwd_groups<T, R, kRagged, false>(a, n, G, groups, 0, stream);
 }
 template <typename T, bool kRagged, bool kFold>
-cudaError_t bwd_clusters(const LnBwdArgs& a, const Shared& p, int fold, cudaStream_t stream) {
+cudaError_t bwd_clusters(const LnBwdArgs& a, int64_t n, const Shared& p, int fold, cudaStream_t stream) {
   const auto kernel = ln_bwd_kernel<T, 2, kRagged, true, kFold>;
   const size_t smem = kFold ? fold_bytes<T, 2>(p.G) : 0;
   int64_t clusters;
@@ -1005,7 +1013,8 @@ cudaError_t bwd_clusters(const LnBwdArgs& a, const Shared& p, int fold, cudaStre
     std::lock_guard<std::mutex> lk(mu);
     cudaError_t e = clusters_that_fit(kernel, cache, p.G, smem, p.S);
     if (e != cudaSuccess) return e;
-    clusters = persistent_blocks(cache.clusters, a.M, kRagged ? rows_apart<T>(a.N) : 1);
+    const int64_t fit = std::min(static_cast<int64_t>(cache.clusters), most_sums(n));
+    clusters = persistent_blocks(fit, a.M, kRagged ? rows_apart<T>(a.N) : 1);
     if (clusters > 0) {
       ClusterLaunch l(p.G, smem, p.S, clusters, stream);
       e = cudaLaunchKernelEx(&l.cfg, kernel, a, p.G, p.S, fold, take_stall(kInjectLayerNormBwd), status_word_ptr());
@@ -1019,8 +1028,8 @@ template <typename T, bool kRagged>
 cudaError_t bwd_shared(const LnBwdArgs& a, int64_t n, cudaStream_t stream) {
   const Shared p = share_row(n);
   const int fold = a.part != nullptr ? fold_rows(a.M, std::max(1, device_sm_count() / p.S)) : 0;
-  return fold > 0 ? bwd_clusters<T, kRagged, true>(a, p, fold, stream)
-                  : bwd_clusters<T, kRagged, false>(a, p, 0, stream);
+  return fold > 0 ? bwd_clusters<T, kRagged, true>(a, n, p, fold, stream)
+                  : bwd_clusters<T, kRagged, false>(a, n, p, 0, stream);
 }
 template <typename T, bool kRagged>
 cudaError_t bwd_any(const LnBwdArgs& a, cudaStream_t stream) {
@@ -1039,7 +1048,8 @@ cudaError_t bwd_type(const LnBwdArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t ln_workspace_bytes(int64_t M, int64_t N) {
-  const int64_t rows = M < kMaxBlocks ? M : kMaxBlocks;
+  // of the type with the fewest vectors, aligned: it has the most rows of sums
+  const int64_t rows = std::min(M, most_sums((N + 7) / 8));
   return static_cast<size_t>(rows) * 2 * static_cast<size_t>(N) * sizeof(float);
 }
 
