@@ -14,9 +14,9 @@
 // more warps take the teacher's entries of every other row each, a row ahead, and write the gradient's
 // sparse part, at most K elements a row, over the dense one.
 // The gradient alone needs no exchange: blocks take shares of rows in registers.
-// Measured, bf16 with 64 entries: loss and gradient 4096 x 131072 325 us, 99% of the copy bandwidth, 4096 x 32768
-// 90 us, 90%, 16384 x 8192 126 us, 64% (the teachers' work on a row's entries); loss alone 4096 x 131072
-// 162 us, 99%; gradient alone 2048 x 131072 157 us, 102%.
+// Measured, bf16 with 64 entries: loss and gradient 4096 x 131072 323 us, 99% of the copy bandwidth, 16384 x 32768
+// 328 us, 98%, 10682 x 50257 451 us, 71% (half-full stages), 65536 x 8192 444 us, 74% (the teachers' work on a
+// row's entries); loss alone 4096 x 131072 161 us, gradient alone 314 us: the copy's rate.
 #include <mutex>
 
 #include "swg_launch.h"
@@ -495,10 +495,10 @@ cudaError_t launch_fwd_any(const KdArgs& a, int dtype, Split split, cudaStream_t
 // the block's barrier, from whichever place a warp comes to it
 __device__ __forceinline__ void block_sync() { asm volatile("barrier.sync 0;" ::: "memory"); }
 
-// The gradient from saved statistics: a block of G threads (64 to 256) takes a share of a row, 16 to 32 KB in
-// registers. A warp more takes the teacher's entries while it arrives, looks for ids that come again while
-// the others form the dense part, and writes the sparse part over it. (With the first of the G threads' warps
-// doing that too, 4096 x 32768 bf16 with 64 entries took 101 us instead of 85.)
+// The gradient from saved statistics: a block of G threads (64 to 256) takes a share of a row, up to 128 bytes a
+// thread in registers at a time. A warp more takes the teacher's entries while it arrives, looks for ids that come
+// again while the others form the dense part, and writes the sparse part over it. (With the first of the G threads'
+// warps doing that too, 4096 x 32768 bf16 with 64 entries took 101 us instead of 85.)
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads + 32, 4)
     kd_bwd_kernel(const KdArgs a, int64_t share0, Groups p, int slots) {

@@ -18,11 +18,11 @@
 // its columns, and the weights and the column sums that belong to them, in registers. An input with the same
 // offset is loaded as aligned vectors too, the row's first and last one with elements of the neighbours,
 // that are cleared; with another offset it is put together from two. Element by element (groups of one
-// column a lane) took 78 us for 4000 x 4001 bf16 forward and 164 us backward, this takes 31 and 58.
+// column a lane) took 78 us for 4000 x 4001 bf16 forward and 164 us backward, this takes 33 and 53.
 // Backward: the columns' sums of dgamma and dbeta stay in registers over all of a group's rows. The blocks'
 // sums go to the workspace and are added by a second kernel in a fixed order.
 // Measured, bf16: 16384 x 4096 with residual 87 us, 92% of the copy bandwidth; backward with dh 220000 x 512
-// 151 us, 89%, 16384 x 4096 94 us, 85%.
+// 146 us, 92%, 16384 x 4096 94 us, 85%, 65536 x 4096 344 us, 93%.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -896,11 +896,12 @@ cudaError_t fwd_shared(const LnFwdArgs& a, int64_t n, cudaStream_t stream) {
   return cudaLaunchKernelEx(&l.cfg, kernel, a, p.G, p.S, take_stall(kInjectLayerNormFwd), status_word_ptr());
 }
 // Vectors a thread: one for rows of up to a warp, else two. Rows of more than 1024 vectors are shared by a
-// cluster: 3000 x 12288 bf16 with residual 70 us, 88 by a block with four vectors a thread; backward with dh
-// 76 us against 117, and 3000 x 16384 fp32 139 us against 510 by the kernels for longest rows. A shared row
-// below that costs more than it gives (8192 x 6144 bf16, backward with dh: 109 us instead of 83), and so does
-// forward a ragged one of more than 256 threads a block (3000 x 16383 fp32 with residual: 514 us, read again
-// 277; backward with dh 443 against 502).
+// cluster: 3000 x 12288 bf16 with residual 70 us, 88 by a block with four vectors a thread, 181 read again; backward
+// with dh 74 us against 117 and 240; 3000 x 16384 fp32 151 and 146 us, read again 254 and 320. A shared row below
+// that costs more than it gives (8192 x 6144 bf16, backward with dh: 109 us instead of 83). Ragged rows of more than
+// 256 threads a block have one block an SM: forward 3000 x 16383 fp32 with residual takes 514 us, read again 258.
+// Backward they are shared up to the same length as whole ones: 3000 x 32761 bf16 287 us, read again 563, 3000 x
+// 30001 fp32 501 against 585, though 3000 x 16383 fp32, the shortest with such blocks, 448 against 321.
 template <typename T, bool kRagged>
 cudaError_t fwd_any(const LnFwdArgs& a, cudaStream_t stream) {
   const int64_t n = (a.N + (kRagged ? 2 * kElems<T> - 2 : 0)) / kElems<T>;

@@ -8,14 +8,16 @@
 //
 // Forward: bound by HBM (V elements read a row). A persistent kernel streams rows through shared memory
 // (vocab_stream.cuh); S blocks of a cluster share a row only when there are too few rows for the SMs.
-// The 16 computing warps keep (max, sum 2^x, sum 2^x x) and each thread its best logit and the run of four
+// The computing warps (16, or four) keep (max, sum 2^x, sum 2^x x) and each thread its best logit and the run of four
 // vectors that has it. A few more warps finish rows in turn, under the work on the next ones: they join
 // the sums, and select the alternatives from the threads' bests. The 32 lane columns' bests have a k-th
 // largest, which at least k logits reach; the few threads with a best at or above it (about k + k^2 / 64)
 // are looked through again (their runs come from L2), and the logits found are ranked against one another.
-// Measured, bf16 with the 20 best: 4096 x 131072 170 us, 95% of the copy bandwidth; 4096 x 32768 65 us, 61% (the
-// computing warps' work on a row and the turn between rows: the schedulers issue in 60% of the cycles); one
-// row of 131072 fp32 12.5 us, shared by eight blocks.
+// log2 e / tau is rounded to fp32 once, so that all exponents of a row are off by the same 2^-24 or so of their
+// size, and ex2.approx is the exponential: both within the fp32 error that the tests allow.
+// Measured with the 20 best: bf16 4096 x 131072 172 us, 93% of the copy bandwidth; 16384 x 32768 225 us, 72% (the
+// computing warps' work on a row and the turn between rows: the schedulers issue in 60% of the cycles); fp32 8192
+// x 32768 177 us, 91%; one row of 131072 fp32 12.5 us, shared by eight blocks.
 #include <mutex>
 
 #include "swg_launch.h"
@@ -496,9 +498,10 @@ cudaError_t launch_token_logprobs_fwd(const TlpFwdArgs& a, int dtype, cudaStream
   const int64_t vectors = row_vectors(a.logits, a.V, a.ld, dtype == 0 ? 4 : 2);
   const Split p = split_row(a.T, vectors, vectors, device_sm_count());
   // Blocks of four computing warps, three an SM, take short rows, and rows up to 100 KB when each of those
-  // blocks has two; blocks of 16 take the others. bf16, the 20 best, L2 cold: 8192 columns 98 us against
-  // 213 us with 16 warps (16384 rows), 32768 columns 68 against 76 us (4096 rows), 50001 columns 109 against
-  // 115 us (4864 rows), 131072 columns 111 against 98 us (2048 rows).
+  // blocks has two; blocks of 16 take the others. 1 GB of logits, the 20 best, four warps against 16: bf16 32768
+  // columns 225 us against 255, 51200 (6400 vectors) 222 against 229, 60000 215 against 210, 131072 201 against 172;
+  // fp32 8192 columns 209 against 379, 25600 (6400 vectors) 177 against 205, 32768 174 against 177, 50257 187
+  // against 169.
   const int64_t sms = device_sm_count();
   const bool small = p.S == 1 && (vectors <= 1024 || (vectors <= 6400 && a.T >= 6 * sms));
   static_assert(6400 <= kFewStages * Shape<4>::kStageVecs, "rows of four warps are not long");
