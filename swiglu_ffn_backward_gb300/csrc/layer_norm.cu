@@ -834,8 +834,9 @@ Shared share_row(int64_t n) {
 }
 constexpr int64_t kMostShared = 2 * kMaxCluster * kMaxGroup;  // vectors
 
+// shared memory that a kernel has beside its static one without asking (48 KB with that)
+constexpr size_t kPlainSmem = 40 * 1024;
 // blocks of a persistent kernel that fit on the device at once (asked once for each device and block size)
-constexpr size_t kPlainSmem = 48 * 1024;  // dynamic shared memory that a kernel has without asking
 struct FitCache {
   int device = -1, threads = 0, fit = 0;
   size_t bytes = 0;

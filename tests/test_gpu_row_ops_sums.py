@@ -2,6 +2,10 @@
 accumulator that takes them one after the other is off by its length. The bounds are those of _row_ops.py, which
 hold for some 100 terms in sequence. Rows are shared (a stride of 0), so that many of them take no memory."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -12,6 +16,7 @@ from ._row_ops import EXP, SUM, check, f64
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _swg():
@@ -39,6 +44,47 @@ def test_weight_gradients_of_many_like_rows(M, N, dtype):
     xerr = 2.0 ** -23 * (np.abs(h) + np.abs(s[:, :1])) * s[:, 1:]
     check("dgamma", dgamma, M * (d * xhat)[0], F32, M * (np.abs(d) * (SUM * np.abs(xhat) + 2 * xerr))[0])
     check("dbeta", dbeta, M * d[0], F32, SUM * M * np.abs(d[0]))
+
+
+# every number of threads that a group may have, with more rows than it takes in one sequence
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["float32", "bfloat16"])
+@pytest.mark.parametrize("shift", [0, 3], ids=["whole", "ragged"])
+def test_weight_gradients_of_many_rows_by_any_group(dtype, shift):
+    swg = _swg()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(42)
+    vec = 16 // dtype.itemsize
+    for n in (4, 12, 30, 40, 90, 150, 200, 250, 300, 370, 440, 500, 560, 630, 700, 760, 820, 890, 950, 1000, 1010):
+        N = n * vec + shift
+        M = min(45000, 2 ** 30 // N) if n > 100 else 400000
+        x = torch.randn((1, N), generator=g, device="cuda").to(dtype)
+        dy = torch.randn((1, N), generator=g, device="cuda").to(dtype)
+        st = swg.layer_norm_fwd(x)["stats"]
+        dx, dgamma, dbeta = swg.layer_norm_bwd(dy.expand(M, N), x.expand(M, N), st.expand(M, 2),
+                                               gamma=torch.ones(N, device="cuda"))
+        h, d, s = f64(x), f64(dy), f64(st)
+        xhat = (h - s[:, :1]) * s[:, 1:]
+        xerr = 2.0 ** -23 * (np.abs(h) + np.abs(s[:, :1])) * s[:, 1:]
+        check(f"dgamma {N}", dgamma, M * (d * xhat)[0], F32, M * (np.abs(d) * (SUM * np.abs(xhat) + 2 * xerr))[0])
+        check(f"dbeta {N}", dbeta, M * d[0], F32, SUM * M * np.abs(d[0]))
+        assert torch.equal(dx[M - 1], dx[0]) and torch.equal(dx[M // 2], dx[0]) or shift
+
+
+FIRST_CALL = """
+import torch
+import swiglu_ffn_backward_gb300 as swg
+N = {n}
+x = torch.randn((1, N), device="cuda").bfloat16()
+st = swg.layer_norm_fwd(x)["stats"]
+swg.layer_norm_bwd(x.expand(60000, N), x.expand(60000, N), st.expand(60000, 2))
+torch.cuda.synchronize()
+"""
+
+
+@pytest.mark.parametrize("n", [2960, 2965, 2500, 8000])
+def test_first_call_of_a_process_with_many_rows(n):
+    # the sums' place in shared memory is just what a kernel has without asking (2960, 2965), or more
+    subprocess.run([sys.executable, "-c", FIRST_CALL.format(n=n)], check=True, cwd=ROOT, timeout=200)
 
 
 # a row's first logits are 0, its largest, the others the background, so that every warp of a block has met the
