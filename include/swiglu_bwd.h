@@ -76,7 +76,12 @@ typedef enum {
 typedef enum { SWG_F32 = 0, SWG_F16 = 1, SWG_BF16 = 2 } swg_dtype;
 
 /* activations whose gradient act_grad computes */
-typedef enum { SWG_ACT_SILU = 0, SWG_ACT_GELU = 1, SWG_ACT_HARDSWISH = 2 } swg_act;
+typedef enum {
+  SWG_ACT_SILU = 0,
+  SWG_ACT_GELU = 1,
+  SWG_ACT_HARDSWISH = 2,
+  SWG_ACT_NONE = 16 /* the identity, for linear_fwd and linear_bwd only */
+} swg_act;
 
 /* flags for swiglu_bwd */
 #define SWG_UNFUSED 0u /* b stage, then the w and x GEMMs on the stored dg, dfc */
@@ -144,7 +149,8 @@ typedef enum {
   SWG_INJECT_LAYER_NORM_FWD = 16,
   SWG_INJECT_LAYER_NORM_BWD = 17,
   SWG_INJECT_TOKEN_LOGPROBS = 18,
-  SWG_INJECT_DISTILL = 19
+  SWG_INJECT_DISTILL = 19,
+  SWG_INJECT_LINEAR_SPLIT = 32
 } swg_inject_kernel;
 swg_status swg_inject_stall(swg_inject_kernel kernel, int64_t entry, int64_t wait_limit_cycles);
 
@@ -398,6 +404,93 @@ swg_status layer_norm_bwd(const void* dy, const void* x, const float* stats,
                           void* dbeta, int64_t M, int64_t N, int64_t lddy, int64_t ldx,
                           int64_t lddh, swg_dtype dtype, swg_dtype wdtype, void* workspace,
                           size_t workspace_bytes, swg_stream_t stream);
+
+/* ---- linear layer ---------------------------------------------------------------
+ * No counterpart on the pages: the projection behind a SwiGLU layer, or a layer
+ * with one of act_grad's activations. For x [M, K], w [K, N], both of `dtype` (fp16
+ * or bf16), and b [N] of `bdtype` (dtype or fp32; NULL: 0):
+ *   z = x w + b;  y = f(z) + residual
+ * f is `act` (SWG_ACT_NONE: the identity), residual [M, N] of dtype (NULL: 0).
+ * x's and the residual's rows are ldx / ldr elements apart; w, y [M, N] and z are
+ * dense. z (NULL: not kept) is what linear_bwd takes with an activation. y may be
+ * the residual itself (same pointer and leading dimension). From one row (decoding)
+ * to many: a few rows are multiplied at the rate at which w is read.
+ * linear_bwd, from dy [M, N] (rows lddy apart), x, w and, with an activation, z:
+ *   dz = dy f'(z), rounded to dtype;  dx = dz w^T,  dw = x^T dz,  db = sum over rows of dz
+ * dx [M, K], dw [K, N] and db [N] (of bdtype; of the unrounded dz) are each optional
+ * (NULL: not computed; w is then not read without dx, x not without dw). dy is
+ * also the residual's gradient. With SWG_ACCUMULATE in `flags`, dw and db are read
+ * and replaced by old + this call's, rounded once. With db or an activation,
+ * `workspace` holds linear_bwd_workspace_size(M, K, N, act) bytes (16-byte aligned).
+ * Products are accumulated in fp32 on the tensor cores in a fixed order (bitwise
+ * reproducible), bias, activation and residual are applied in fp32, each output is
+ * rounded once (RNE). Any M >= 0; K and N multiples of 8, leading dimensions too
+ * (where M > 1), pointers 16-byte aligned (SWG_ERR_UNSUPPORTED otherwise, and for K == 0
+ * in linear_fwd). M == 0: dw and db are zeros (left alone with SWG_ACCUMULATE).
+ * Errors: negative sizes, another dtype, bdtype, act or flag, a leading dimension
+ * below the row's length, overlapping buffers -> SWG_ERR_PARAM_INVALID; missing tensors
+ * -> SWG_ERR_NULLPTR; SWG_ERR_WORKSPACE. */
+swg_status linear_fwd(const void* x, const void* w, const void* b, const void* residual,
+                      void* y, void* z, int64_t M, int64_t K, int64_t N, int64_t ldx,
+                      int64_t ldr, swg_act act, swg_dtype dtype, swg_dtype bdtype,
+                      swg_stream_t stream);
+size_t linear_bwd_workspace_size(int64_t M, int64_t K, int64_t N, swg_act act);
+swg_status linear_bwd(const void* dy, const void* x, const void* w, const void* z, void* dx,
+                      void* dw, void* db, int64_t M, int64_t K, int64_t N, int64_t lddy,
+                      int64_t ldx, swg_act act, unsigned flags, swg_dtype dtype,
+                      swg_dtype bdtype, void* workspace, size_t workspace_bytes,
+                      swg_stream_t stream);
+
+/* ---- norms between blocks -------------------------------------------------------
+ * No counterpart on the pages: what lies between two blocks of a transformer. For
+ * M rows of N elements, u the block's output and residual the stream it came from,
+ *   v = u rstd(u) gamma_post with SWG_NORM_POST in `flags`, else v = u
+ *   h = alpha residual + gate v, rounded to `dtype`
+ *   y = h rstd(h) gamma_pre with SWG_NORM_PRE (else no y)
+ * with rstd(t) = 1/sqrt(sum t^2 / N + eps). u, residual: rows ldu / ldr apart (at
+ * least N, or 0 for one row shared by all); residual NULL: 0 (alpha is not used).
+ * gamma_post, gamma_pre [N] of `wdtype` (dtype or fp32), NULL: 1. gate [G, N], dense,
+ * of `gdtype` (dtype or fp32): row g serves the M / G rows from g M / G on (G = 1: a
+ * scale for each column; a row for each sequence; G = M: for each token); NULL with
+ * G = 0: 1. Without SWG_NORM_POST, residual and gate, h is u itself and must be NULL
+ * (the call is then the plain norm of u); otherwise h is required. h, y and stats
+ * [M, 2] = (rstd(u), rstd(h)), fp32, 0 for a norm that is not there, are dense.
+ * block_norm_bwd, from dy (with SWG_NORM_PRE), dh (the gradient that reaches h past the
+ * second norm; NULL: 0, required without SWG_NORM_PRE), u, h (u itself where the
+ * forward had none; with SWG_NORM_PRE) and the stats, with D the gradient of h:
+ *   D = dh + rstd(h) (a - h^ mean(a h^)),  a = dy gamma_pre,  h^ = h rstd(h)
+ *   dresidual = alpha D (NULL: not wanted)
+ *   du = rstd(u) (q D - u^ mean(q D u^)),  q = gate gamma_post,  u^ = u rstd(u)
+ *        (du = gate D without SWG_NORM_POST)
+ *   dgamma_pre = sum dy h^,  dgamma_post = sum gate D u^,  over the M rows
+ *   dgate = sum over its rows of D v
+ * Each parameter gradient is optional; with one, `workspace` must hold
+ * block_norm_bwd_workspace_size(M, N, G) bytes (16-byte aligned), else SWG_ERR_WORKSPACE.
+ * fp32 arithmetic, fixed orders of summation (bitwise reproducible), one rounding (RNE)
+ * for each output. Any M >= 0 and 0 <= N < 2^31; pointers aligned to their element size
+ * (SWG_ERR_UNSUPPORTED otherwise); 16-byte aligned rows are the fast case. M == 0 or
+ * N == 0: nothing is launched but zeros for the parameters' gradients. Errors: negative
+ * sizes, M not a multiple of G, a bad leading dimension, unknown types or flags (or
+ * none), a gamma without its norm, a NaN or infinite alpha, a negative or NaN eps, h or y where they must be NULL,
+ * outputs that overlap inputs or each other -> SWG_ERR_PARAM_INVALID; a missing tensor
+ * -> SWG_ERR_NULLPTR; N or M >= 2^31 - 1 -> SWG_ERR_UNSUPPORTED. */
+#define SWG_NORM_POST 1u
+#define SWG_NORM_PRE 2u
+swg_status block_norm_fwd(const void* u, const void* residual, const void* gamma_post,
+                          const void* gamma_pre, const void* gate, void* h, void* y,
+                          float* stats, int64_t M, int64_t N, int64_t G, int64_t ldu,
+                          int64_t ldr, float alpha, float eps, unsigned flags,
+                          swg_dtype dtype, swg_dtype wdtype, swg_dtype gdtype,
+                          swg_stream_t stream);
+size_t block_norm_bwd_workspace_size(int64_t M, int64_t N, int64_t G);
+swg_status block_norm_bwd(const void* dy, const void* dh, const void* u, const void* h,
+                          const float* stats, const void* gamma_post, const void* gamma_pre,
+                          const void* gate, void* du, void* dresidual, void* dgamma_post,
+                          void* dgamma_pre, void* dgate, int64_t M, int64_t N, int64_t G,
+                          int64_t lddy, int64_t lddh, int64_t ldu, int64_t ldh, float alpha,
+                          unsigned flags, swg_dtype dtype, swg_dtype wdtype,
+                          swg_dtype gdtype, void* workspace, size_t workspace_bytes,
+                          swg_stream_t stream);
 
 /* index types of targets and teacher ids */
 typedef enum { SWG_I32 = 0, SWG_I64 = 1 } swg_itype;

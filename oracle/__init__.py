@@ -23,7 +23,8 @@ It restates, in plain numpy float64, what two pages define:
   by their standard definitions: `group_norm.py`.
 * Layer norm, log probabilities of given tokens and distillation from a
   teacher's top logits by their standard definitions (no page prints them):
-  `layer_norm.py`, `vocabulary.py`.
+  `layer_norm.py`, `vocabulary.py`; so the linear layer with its epilogue and
+  the norms between blocks: `linear.py`, `block_norm.py`.
 
 Library primitives used as steps: numpy.exp, numpy matmul, numpy.sum, numpy.mean.
 Parity status: every function here is pinned by the `-m "not gpu"` tests
@@ -52,6 +53,8 @@ from .swish import swish_fwd, swish_grad  # noqa: F401
 from .activations import act_grad, gelu_grad, hardswish_grad, silu_act_grad  # noqa: F401
 from .group_norm import group_norm_bwd, group_norm_fwd, group_norm_stats  # noqa: F401
 from .layer_norm import layer_norm_bwd, layer_norm_fwd  # noqa: F401
+from .linear import act_fwd, linear_bwd, linear_fwd  # noqa: F401
+from .block_norm import block_norm_bwd, block_norm_fwd  # noqa: F401
 from .vocabulary import (  # noqa: F401
     distill_bwd,
     distill_fwd,

@@ -55,6 +55,8 @@ EXPORTS = (
     "layer_norm_fwd", "layer_norm_bwd_workspace_size", "layer_norm_bwd",
     "token_logprobs_fwd", "token_logprobs_bwd",
     "distill_fwd", "distill_bwd", "distill_fwd_bwd",
+    "linear_fwd", "linear_bwd_workspace_size", "linear_bwd",
+    "block_norm_fwd", "block_norm_bwd_workspace_size", "block_norm_bwd",
 )
 
 
@@ -133,6 +135,18 @@ def _load() -> ctypes.CDLL:
     lib.distill_bwd.restype = st
     lib.distill_fwd_bwd.argtypes = [P] * 7 + [I64] * 5 + [F, I, I, I, P]
     lib.distill_fwd_bwd.restype = st
+    lib.linear_fwd.argtypes = [P] * 6 + [I64] * 5 + [I, I, I, P]
+    lib.linear_fwd.restype = st
+    lib.linear_bwd_workspace_size.argtypes = [I64, I64, I64, I]
+    lib.linear_bwd_workspace_size.restype = SZ
+    lib.linear_bwd.argtypes = [P] * 7 + [I64] * 5 + [I, U, I, I, P, SZ, P]
+    lib.linear_bwd.restype = st
+    lib.block_norm_fwd.argtypes = [P] * 8 + [I64] * 5 + [F, F, U, I, I, I, P]
+    lib.block_norm_fwd.restype = st
+    lib.block_norm_bwd_workspace_size.argtypes = [I64, I64, I64]
+    lib.block_norm_bwd_workspace_size.restype = SZ
+    lib.block_norm_bwd.argtypes = [P] * 13 + [I64] * 7 + [F, U, I, I, I, P, SZ, P]
+    lib.block_norm_bwd.restype = st
     return lib
 
 
@@ -276,6 +290,7 @@ SWG_INJECT_LAYER_NORM_FWD = 16
 SWG_INJECT_LAYER_NORM_BWD = 17
 SWG_INJECT_TOKEN_LOGPROBS = 18
 SWG_INJECT_DISTILL = 19
+SWG_INJECT_LINEAR_SPLIT = 32
 
 
 def swg_inject_stall(kernel: int, entry: int, wait_limit_cycles: int) -> None:
@@ -923,3 +938,272 @@ def distill_fwd_bwd(logits, teacher_ids, teacher_logits, weight, temperature: fl
          out["loss"].data_ptr(), out["stats"].data_ptr(), out["dlogits"].data_ptr(), T, V, ld, ldo, K, temperature,
          code, _DTYPE[tl.dtype], _itype(ids))
     return out
+
+
+# ------------------------------------------------------------- the linear layer
+SWG_ACT_NONE = 16
+_HALVES = (torch.float16, torch.bfloat16)
+
+
+def _act_code(act):
+    if act is None:
+        return SWG_ACT_NONE
+    if act not in SWG_ACT:
+        raise ValueError(f"act must be None or one of {sorted(SWG_ACT)}")
+    return SWG_ACT[act]
+
+
+def _tma_rows(t, name):
+    """A tensor [..., N] of 16-bit elements as the matrix kernels take it: (tensor, rows, N, row stride). Rows may lie
+    apart by a multiple of 16 bytes, from a 16-byte boundary on; anything else is copied."""
+    if isinstance(t, torch.Tensor) and t.dtype not in _HALVES:
+        raise TypeError(f"{name} must be fp16 or bf16, got {t.dtype}")
+    t, M, N, ld, _ = _row_tensor(t, name)
+    if M > 1 and ld < N or ld % 8 or t.data_ptr() % 16:
+        t, ld = t.clone(memory_format=torch.contiguous_format), N
+    return t, M, N, ld
+
+
+def _tma_like(t, name, x, shape):
+    """A second tensor of x's type and the given shape: (tensor, row stride); (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if isinstance(t, torch.Tensor) and (t.dtype != x.dtype or t.shape != shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)} and dtype {x.dtype}, "
+                         f"got {tuple(t.shape)}, {t.dtype}")
+    t, _, _, ld = _tma_rows(t, name)
+    _device_of(x, t)
+    return t, ld
+
+
+def _weight(w, x, K):
+    if not isinstance(w, torch.Tensor) or not w.is_cuda:
+        raise TypeError("w must be a CUDA tensor")
+    if w.dtype != x.dtype or w.dim() != 2 or (K is not None and w.shape[0] != K):
+        raise ValueError(f"w must be [K, N] of {x.dtype}{'' if K is None else f' with K = {K}'}, "
+                         f"got {tuple(w.shape)} of {w.dtype}")
+    _device_of(x, w)
+    return w.contiguous()
+
+
+def linear_fwd(x, w, b=None, act: str | None = None, residual=None, save_z: bool = False, out: dict | None = None,
+               stream=None) -> dict:
+    """y = f(x w + b) + residual for x [..., K] and w [K, N] (fp16 or bf16, K and N multiples of 8): a dict of y
+    [..., N], and of z = x w + b, which linear_bwd takes with an activation, when save_z is True. act: None, or
+    "silu", "gelu", "hardswish"; b [N] (x's dtype or fp32) and residual [..., N] may be None. `out` may supply the
+    outputs; out["y"] may be the residual itself."""
+    if stream is not None:
+        return _on_stream(stream, linear_fwd, x, w, b, act=act, residual=residual, save_z=save_z, out=out)
+    code, shape = _act_code(act), x.shape if isinstance(x, torch.Tensor) else None
+    xt, M, K, ldx = _tma_rows(x, "x")
+    w, dev = _weight(w, xt, K), xt.device
+    N = w.shape[1]
+    want = (*shape[:-1], N)
+    b = _vector(b, "b", (N,), (xt.dtype, torch.float32), dev)
+    res, ldr = _tma_like(residual, "residual", xt, want)
+    given = out or {}
+    out = {"y": _row_out(given.get("y"), want, xt.dtype, dev, "y", shape[:-1])}
+    z = None
+    if save_z:
+        out["z"] = z = _row_out(given.get("z"), want, xt.dtype, dev, "z", shape[:-1])
+    _run("linear_fwd", lib.linear_fwd, dev, xt.data_ptr(), w.data_ptr(), _ptr(b), _ptr(res), out["y"].data_ptr(),
+         _ptr(z), M, K, N, ldx, ldr, code, _DTYPE[xt.dtype], _DTYPE[xt.dtype if b is None else b.dtype])
+    return out
+
+
+def linear_bwd_workspace_size(M: int, K: int, N: int, act: str | None = None) -> int:
+    return lib.linear_bwd_workspace_size(M, K, N, _act_code(act))
+
+
+def linear_bwd(dy, x, w, z=None, act: str | None = None, bias: bool = True, need_dx: bool = True, need_dw: bool = True,
+               accumulate: bool = False, db_dtype=None, out: dict | None = None, workspace=None, stream=None) -> dict:
+    """The gradients of linear_fwd from dy [..., N]: a dict of dx [..., K], dw [K, N] and, with bias, db [N] (of
+    db_dtype: x's dtype, which is the default, or fp32). z is the forward's, needed with an activation; x may be None
+    without need_dw, w without need_dx. dy is also the residual's gradient. accumulate=True adds this call's dw and db
+    into out's, which must then be given."""
+    if stream is not None:
+        return _on_stream(stream, linear_bwd, dy, x, w, z=z, act=act, bias=bias, need_dx=need_dx, need_dw=need_dw,
+                          accumulate=accumulate, db_dtype=db_dtype, out=out, workspace=workspace)
+    code, shape = _act_code(act), dy.shape if isinstance(dy, torch.Tensor) else None
+    g, M, N, lddy = _tma_rows(dy, "dy")
+    dev, lead = g.device, shape[:-1]
+    K, xt, ldx = None, None, 0
+    if need_dw:
+        if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.shape[:-1] != lead:
+            raise ValueError(f"x must have the shape {tuple(lead)} + (K,)")
+        K = x.shape[-1]
+        xt, ldx = _tma_like(x, "x", g, x.shape)
+    wt = None
+    if need_dx:
+        wt = _weight(w, g, K)
+        K = wt.shape[0]
+        if wt.shape[1] != N:
+            raise ValueError(f"w must be [K, {N}], got {tuple(wt.shape)}")
+    if code != SWG_ACT_NONE:
+        if z is None:
+            raise ValueError("z, the forward's, is needed with an activation")
+        z = _vector(z, "z", shape, (g.dtype,), dev, lead)
+        if z.data_ptr() % 16:
+            z = z.clone()
+    else:
+        z = None
+    given, need = dict(out or {}), {}
+    if accumulate and any(given.get(k) is None for k, on in (("dw", need_dw), ("db", bias)) if on):
+        raise ValueError("accumulate=True needs dw and db in `out`")
+    if need_dx:
+        need["dx"] = _row_out(given.get("dx"), (*lead, K), g.dtype, dev, "dx", lead)
+    if need_dw:
+        need["dw"] = _out(given.get("dw"), (K, N), g.dtype, dev, "dw")
+    if bias:
+        old = given.get("db")
+        if db_dtype is None:
+            db_dtype = old.dtype if isinstance(old, torch.Tensor) and old.dtype == torch.float32 else g.dtype
+        if db_dtype not in (g.dtype, torch.float32):
+            raise TypeError(f"db_dtype must be {g.dtype} or torch.float32")
+        need["db"] = _out(old, (N,), db_dtype, dev, "db")
+    else:
+        db_dtype = g.dtype
+    K = 0 if K is None else K
+    ws = None
+    if bias or code != SWG_ACT_NONE:
+        ws = _workspace(lib.linear_bwd_workspace_size(M, K if K > 0 else 8, N, code), dev, workspace)
+        if workspace is not None:
+            _device_of(g, ws)
+    _run("linear_bwd", lib.linear_bwd, dev, g.data_ptr(), _ptr(xt), _ptr(wt), _ptr(z), _ptr(need.get("dx")),
+         _ptr(need.get("dw")), _ptr(need.get("db")), M, K, N, lddy, ldx, code, SWG_ACCUMULATE if accumulate else 0,
+         _DTYPE[g.dtype], _DTYPE[db_dtype], _ptr(ws), _nbytes(ws))
+    return need
+
+
+# ------------------------------------------------------------- norms between blocks
+SWG_NORM_POST, SWG_NORM_PRE = 1, 2
+
+
+def _gate_rows(gate, lead, M, N, x):
+    """A gate whose rows serve equal runs of x's rows: (dense tensor, its number of rows); (None, 0) for None. Its
+    leading shape, without trailing ones, is the first of x's leading dimensions, or counts the runs in one."""
+    if gate is None:
+        return None, 0
+    if not isinstance(gate, torch.Tensor) or not gate.is_cuda:
+        raise TypeError("gate must be a CUDA tensor")
+    g = tuple(gate.shape[:-1])
+    while g and g[-1] == 1:
+        g = g[:-1]
+    G = math.prod(g)
+    fits = g == tuple(lead[:len(g)]) or (len(g) == 1 and (G == M or len(lead) <= 1))
+    if (gate.dim() < 1 or gate.shape[-1] != N or gate.dtype not in (x.dtype, torch.float32) or not fits
+            or (M > 0 and (G == 0 or M % G))):
+        raise ValueError(f"gate must be [..., {N}] of {x.dtype} or torch.float32 with a row for equal runs of the rows "
+                         f"{tuple(lead)}, got {tuple(gate.shape)} of {gate.dtype}")
+    _device_of(x, gate)
+    return gate.contiguous(), G
+
+
+def _two_gammas(gamma_post, gamma_pre, post, pre, N, x):
+    """The gammas checked, with their common dtype code."""
+    if (gamma_post is not None and not post) or (gamma_pre is not None and not pre):
+        raise ValueError("a gamma needs its norm (post, pre)")
+    allowed = (x.dtype, torch.float32)
+    gamma_post = _vector(gamma_post, "gamma_post", (N,), allowed, x.device)
+    gamma_pre = _vector(gamma_pre, "gamma_pre", (N,), allowed if gamma_post is None else (gamma_post.dtype,), x.device)
+    w = gamma_post if gamma_post is not None else gamma_pre
+    return gamma_post, gamma_pre, w.dtype if w is not None else x.dtype
+
+
+def block_norm_fwd(u, residual=None, gamma_post=None, gamma_pre=None, gate=None, alpha: float = 1.0, eps: float = 1e-6,
+                   post: bool = True, pre: bool = True, out: dict | None = None, stream=None) -> dict:
+    """What lies between two blocks, for the output u [..., N] of the first and the residual stream it came from
+    (fp32/fp16/bf16): v = u rstd(u) gamma_post with post, else u; h = alpha residual + gate v; y = h rstd(h) gamma_pre
+    with pre; rstd(t) = 1/sqrt(mean(t^2) + eps). A dict of h (absent without post, residual and gate, where it is u
+    itself: the call is then the plain norm of u), y (with pre) and stats [M, 2] for the backward. The gammas [N] (x's
+    dtype or fp32, both the same), residual and gate may be None. gate (u's dtype or fp32): [N]; or one row for each
+    of equal runs of u's rows, [B, N] or [B, 1, N] for u [B, S, N], [G, N] for u [M, N]; or one for each row, of u's
+    shape. `out` may supply any of the outputs; stream: the stream to run on."""
+    if stream is not None:
+        return _on_stream(stream, block_norm_fwd, u, residual, gamma_post, gamma_pre, gate, alpha=alpha, eps=eps,
+                          post=post, pre=pre, out=out)
+    shape = u.shape if isinstance(u, torch.Tensor) else None
+    ut, M, N, ldu, code = _row_tensor(u, "u")
+    lead, dev = shape[:-1], ut.device
+    res, ldr = _like_rows(residual, "residual", ut, ldu, shape)
+    gamma_post, gamma_pre, wdtype = _two_gammas(gamma_post, gamma_pre, post, pre, N, ut)
+    gate, G = _gate_rows(gate, lead, M, N, ut)
+    given = out or {}
+    h = y = None
+    out = {"stats": _row_out(given.get("stats"), (M, 2), torch.float32, dev, "stats", lead)}
+    if post or res is not None or gate is not None:
+        h = given.get("h")
+        out["h"] = h = _new(u) if h is None else _row_out(h, shape, ut.dtype, dev, "h", lead)
+    if pre:
+        y = given.get("y")
+        out["y"] = y = _new(u) if y is None else _row_out(y, shape, ut.dtype, dev, "y", lead)
+    _run("block_norm_fwd", lib.block_norm_fwd, dev, ut.data_ptr(), _ptr(res), _ptr(gamma_post), _ptr(gamma_pre),
+         _ptr(gate), _ptr(h), _ptr(y), out["stats"].data_ptr(), M, N, G, ldu, ldr, alpha, eps,
+         (SWG_NORM_POST if post else 0) | (SWG_NORM_PRE if pre else 0), code, _DTYPE[wdtype],
+         code if gate is None else _DTYPE[gate.dtype])
+    return out
+
+
+def block_norm_bwd_workspace_size(M: int, N: int, G: int = 0) -> int:
+    return lib.block_norm_bwd_workspace_size(M, N, G)
+
+
+def block_norm_bwd(dy, dh, u, h, stats, gamma_post=None, gamma_pre=None, gate=None, alpha: float = 1.0,
+                   post: bool = True, pre: bool = True, residual: bool = True, params: bool = True,
+                   out: dict | None = None, workspace=None, stream=None) -> dict:
+    """The gradients of block_norm_fwd from dy (None without pre), dh (the gradient that reaches h past the second
+    norm; None: 0, not without pre), u, h (the forward's; None where it had none) and its stats: a dict of du,
+    dresidual (with residual: whether there was one; without post and gate and with alpha = 1 it is du, the same
+    tensor), and with params dgamma_post (with post), dgamma_pre (with pre) and dgate (with a gate), of the gammas'
+    (u's dtype without them) and the gate's dtype and shape."""
+    if stream is not None:
+        return _on_stream(stream, block_norm_bwd, dy, dh, u, h, stats, gamma_post=gamma_post, gamma_pre=gamma_pre,
+                          gate=gate, alpha=alpha, post=post, pre=pre, residual=residual, params=params, out=out,
+                          workspace=workspace)
+    shape = u.shape if isinstance(u, torch.Tensor) else None
+    ut, M, N, ldu, code = _row_tensor(u, "u")
+    lead, dev = shape[:-1], ut.device
+    plain = not post and not residual and gate is None  # h is u
+    if pre and (dy is None or (h is None and not plain)):
+        raise TypeError("dy and h must be CUDA tensors")
+    if not pre and dh is None:
+        raise TypeError("dh must be a CUDA tensor")
+    dyt, lddy = _like_rows(dy if pre else None, "dy", ut, ldu, shape)
+    dht, lddh = _like_rows(dh, "dh", ut, ldu, shape)
+    ht, ldh = _like_rows((u if h is None else h) if pre else None, "h", ut, ldu, shape)
+    stats = _vector(stats, "stats", (M, 2), _F32, dev, lead)
+    if stats is None:
+        raise TypeError("stats must be a CUDA tensor")
+    gamma_post, gamma_pre, wdtype = _two_gammas(gamma_post, gamma_pre, post, pre, N, ut)
+    gate_shape = None if gate is None else gate.shape
+    gate, G = _gate_rows(gate, lead, M, N, ut)
+    given, res = out or {}, {}
+
+    def rows(name):
+        t = given.get(name)
+        return _new(u) if t is None else _row_out(t, shape, ut.dtype, dev, name, lead)
+
+    res["du"] = du = rows("du")
+    dres = dgp = dgn = dgate = ws = None
+    if residual:
+        same = not post and gate is None and alpha == 1.0 and given.get("dresidual") is None
+        res["dresidual"] = du if same else rows("dresidual")
+        dres = None if same else res["dresidual"]
+    if params:
+        if post:
+            res["dgamma_post"] = dgp = _out(given.get("dgamma_post"), (N,), wdtype, dev, "dgamma_post")
+        if pre:
+            res["dgamma_pre"] = dgn = _out(given.get("dgamma_pre"), (N,), wdtype, dev, "dgamma_pre")
+        if gate is not None:
+            t = given.get("dgate")
+            res["dgate"] = dgate = (torch.empty(gate_shape, dtype=gate.dtype, device=dev) if t is None
+                                    else _out(t, tuple(gate_shape), gate.dtype, dev, "dgate"))
+        if dgp is not None or dgn is not None or dgate is not None:
+            ws = _workspace(lib.block_norm_bwd_workspace_size(M, N, G), dev, workspace)
+            if workspace is not None:
+                _device_of(ut, ws)
+    _run("block_norm_bwd", lib.block_norm_bwd, dev, _ptr(dyt), _ptr(dht), ut.data_ptr(), _ptr(ht), stats.data_ptr(),
+         _ptr(gamma_post), _ptr(gamma_pre), _ptr(gate), du.data_ptr(), _ptr(dres), _ptr(dgp), _ptr(dgn), _ptr(dgate),
+         M, N, G, lddy, lddh, ldu, ldh, alpha, (SWG_NORM_POST if post else 0) | (SWG_NORM_PRE if pre else 0), code,
+         _DTYPE[wdtype], code if gate is None else _DTYPE[gate.dtype], _ptr(ws), _nbytes(ws))
+    return res

@@ -102,7 +102,7 @@ swg_status swg_inject_stall(swg_inject_kernel kernel, int64_t entry, int64_t wai
   }
   if (kernel != SWG_INJECT_X_GEMM && kernel != SWG_INJECT_FUSED_X && kernel != SWG_INJECT_FUSED_W &&
       kernel != SWG_INJECT_FWD && kernel != SWG_INJECT_LAYER_NORM_FWD && kernel != SWG_INJECT_LAYER_NORM_BWD &&
-      kernel != SWG_INJECT_TOKEN_LOGPROBS && kernel != SWG_INJECT_DISTILL)
+      kernel != SWG_INJECT_TOKEN_LOGPROBS && kernel != SWG_INJECT_DISTILL && kernel != SWG_INJECT_LINEAR_SPLIT)
     return SWG_ERR_PARAM_INVALID;
   if (entry < 0 || wait_limit_cycles < 1024) return SWG_ERR_PARAM_INVALID;
   swg::arm_injection(static_cast<int>(kernel), entry, static_cast<long long>(wait_limit_cycles));
@@ -1052,6 +1052,254 @@ swg_status distill_fwd_bwd(const void* logits, const void* ids, const void* teac
                            swg_stream_t stream) {
   return distill(logits, ids, teacher, weight, nullptr, loss, stats, dlogits, T, V, ld, ldo, K, temperature, dtype,
                  tdtype, itype, stream, true, true);
+}
+
+// ---------------------------------------------------------------- norms between blocks
+namespace {
+
+inline bool finite(float v) { return v - v == 0.0f; }
+
+// sizes, types and flags that block_norm_fwd and block_norm_bwd share
+swg_status check_block_norm(int64_t M, int64_t N, int64_t G, const void* gate, const void* gamma_post,
+                            const void* gamma_pre, float alpha, unsigned flags, int dtype, int wdtype, int gdtype) {
+  if (!known_dtype(dtype) || (wdtype != dtype && wdtype != SWG_F32) || (gdtype != dtype && gdtype != SWG_F32))
+    return SWG_ERR_PARAM_INVALID;
+  if (M < 0 || N < 0 || G < 0 || !finite(alpha)) return SWG_ERR_PARAM_INVALID;
+  if (flags == 0 || (flags & ~(SWG_NORM_POST | SWG_NORM_PRE)) != 0) return SWG_ERR_PARAM_INVALID;
+  if ((gamma_post != nullptr && !(flags & SWG_NORM_POST)) || (gamma_pre != nullptr && !(flags & SWG_NORM_PRE)))
+    return SWG_ERR_PARAM_INVALID;
+  if (M >= kMaxDim || N >= kMaxDim || too_large(M, N)) return SWG_ERR_UNSUPPORTED;
+  if (G > 0 && M % G != 0) return SWG_ERR_PARAM_INVALID;
+  if (gate != nullptr && G == 0 && M > 0) return SWG_ERR_PARAM_INVALID;
+  const int64_t ws = dtype_bytes(wdtype);
+  if (!aligned_to(gamma_post, ws) || !aligned_to(gamma_pre, ws) || !aligned_to(gate, dtype_bytes(gdtype)))
+    return SWG_ERR_UNSUPPORTED;
+  return SWG_OK;
+}
+
+}  // namespace
+
+swg_status block_norm_fwd(const void* u, const void* residual, const void* gamma_post, const void* gamma_pre,
+                          const void* gate, void* h, void* y, float* stats, int64_t M, int64_t N, int64_t G,
+                          int64_t ldu, int64_t ldr, float alpha, float eps, unsigned flags, swg_dtype dtype,
+                          swg_dtype wdtype, swg_dtype gdtype, swg_stream_t stream) {
+  swg_status st = check_block_norm(M, N, G, gate, gamma_post, gamma_pre, alpha, flags, dtype, wdtype, gdtype);
+  if (st != SWG_OK) return st;
+  if (!(eps >= 0.0f)) return SWG_ERR_PARAM_INVALID;
+  if (!ld_ok(ldu, M, N, false) || (residual != nullptr && !ld_ok(ldr, M, N, false))) return SWG_ERR_PARAM_INVALID;
+  for (const int64_t ld : {ldu, residual != nullptr ? ldr : 0})
+    if (M > 1 && (ld > kMaxLd || too_large(M, ld))) return SWG_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return SWG_OK;
+  const bool post = (flags & SWG_NORM_POST) != 0, pre = (flags & SWG_NORM_PRE) != 0;
+  if (u == nullptr || stats == nullptr || (pre && y == nullptr) || (G > 0 && gate == nullptr)) return SWG_ERR_NULLPTR;
+  if ((!pre && y != nullptr) || (h != nullptr) != (post || residual != nullptr || gate != nullptr))
+    return SWG_ERR_PARAM_INVALID;
+  const int64_t es = dtype_bytes(dtype), ws = dtype_bytes(wdtype);
+  if (!aligned_to(u, es) || !aligned_to(residual, es) || !aligned_to(h, es) || !aligned_to(y, es) ||
+      !aligned_to(stats, 4))
+    return SWG_ERR_UNSUPPORTED;
+  const Range outs[] = {rng(y, y ? M * N * es : 0), rng(h, h ? M * N * es : 0), rng(stats, M * 8)};
+  const Range ins[] = {rows_rng(u, M, N, ldu, es), rows_rng(residual, M, N, ldr, es),
+                       rng(gamma_post, gamma_post ? N * ws : 0), rng(gamma_pre, gamma_pre ? N * ws : 0),
+                       rng(gate, gate ? G * N * dtype_bytes(gdtype) : 0)};
+  if (any_overlap(outs, 3, ins, 5)) return SWG_ERR_PARAM_INVALID;
+  st = check_device();
+  if (st != SWG_OK) return st;
+  const swg::BnFwdArgs a{u, residual, gamma_post, gamma_pre, gate, h, y, stats, M, N, M > 1 ? ldu : 0,
+                         M > 1 ? ldr : 0, gate != nullptr ? M / G : M, alpha, eps, static_cast<int>(wdtype),
+                         static_cast<int>(gdtype), post, pre};
+  return cuda_status(swg::launch_block_norm_fwd(a, static_cast<int>(dtype), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t block_norm_bwd_workspace_size(int64_t M, int64_t N, int64_t G) {
+  if (M <= 0 || N <= 0 || G < 0 || M >= kMaxDim || N >= kMaxDim || (G > 0 && M % G != 0)) return 0;
+  return swg::bn_workspace_bytes(M, N, G > 0 ? M / G : M);
+}
+
+swg_status block_norm_bwd(const void* dy, const void* dh, const void* u, const void* h, const float* stats,
+                          const void* gamma_post, const void* gamma_pre, const void* gate, void* du, void* dresidual,
+                          void* dgamma_post, void* dgamma_pre, void* dgate, int64_t M, int64_t N, int64_t G,
+                          int64_t lddy, int64_t lddh, int64_t ldu, int64_t ldh, float alpha, unsigned flags,
+                          swg_dtype dtype, swg_dtype wdtype, swg_dtype gdtype, void* workspace,
+                          size_t workspace_bytes, swg_stream_t stream) {
+  swg_status st = check_block_norm(M, N, G, gate, gamma_post, gamma_pre, alpha, flags, dtype, wdtype, gdtype);
+  if (st != SWG_OK) return st;
+  const bool post = (flags & SWG_NORM_POST) != 0, pre = (flags & SWG_NORM_PRE) != 0;
+  if (!ld_ok(ldu, M, N, false) || (pre && (!ld_ok(lddy, M, N, false) || !ld_ok(ldh, M, N, false))) ||
+      (dh != nullptr && !ld_ok(lddh, M, N, false)))
+    return SWG_ERR_PARAM_INVALID;
+  for (const int64_t ld : {ldu, pre ? lddy : 0, pre ? ldh : 0, dh != nullptr ? lddh : 0})
+    if (M > 1 && (ld > kMaxLd || too_large(M, ld))) return SWG_ERR_UNSUPPORTED;
+  if ((!pre && (dy != nullptr || h != nullptr || dgamma_pre != nullptr)) || (!post && dgamma_post != nullptr) ||
+      (dgate != nullptr && G == 0 && M > 0))
+    return SWG_ERR_PARAM_INVALID;
+  if (N == 0) return SWG_OK;
+  const int64_t es = dtype_bytes(dtype), ws = dtype_bytes(wdtype), gs = dtype_bytes(gdtype);
+  if (!aligned_to(dy, es) || !aligned_to(dh, es) || !aligned_to(u, es) || !aligned_to(h, es) || !aligned_to(du, es) ||
+      !aligned_to(dresidual, es) || !aligned_to(stats, 4) || !aligned_to(dgamma_post, ws) ||
+      !aligned_to(dgamma_pre, ws) || !aligned_to(dgate, gs))
+    return SWG_ERR_UNSUPPORTED;
+  if (M > 0 && (u == nullptr || stats == nullptr || du == nullptr || (pre && (dy == nullptr || h == nullptr)) ||
+                (!pre && dh == nullptr) || (G > 0 && gate == nullptr)))
+    return SWG_ERR_NULLPTR;
+  const Range outs[] = {rng(du, M * N * es), rng(dresidual, dresidual ? M * N * es : 0),
+                        rng(dgamma_post, dgamma_post ? N * ws : 0), rng(dgamma_pre, dgamma_pre ? N * ws : 0),
+                        rng(dgate, dgate ? G * N * gs : 0)};
+  const Range ins[] = {rows_rng(dy, M, N, lddy, es), rows_rng(dh, M, N, lddh, es), rows_rng(u, M, N, ldu, es),
+                       rows_rng(h, M, N, ldh, es), rng(stats, M * 8), rng(gamma_post, gamma_post ? N * ws : 0),
+                       rng(gamma_pre, gamma_pre ? N * ws : 0), rng(gate, gate ? G * N * gs : 0)};
+  if (any_overlap(outs, 5, ins, 8)) return SWG_ERR_PARAM_INVALID;
+  const bool params = dgamma_post != nullptr || dgamma_pre != nullptr || dgate != nullptr;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    if (!params) return SWG_OK;
+    st = check_device();
+    if (st != SWG_OK) return st;
+    const struct {
+      void* p;
+      int64_t bytes;
+    } zero[] = {{dgamma_post, N * ws}, {dgamma_pre, N * ws}, {dgate, G * N * gs}};
+    for (const auto& z : zero)
+      if (z.p != nullptr && z.bytes > 0 && cudaMemsetAsync(z.p, 0, static_cast<size_t>(z.bytes), s) != cudaSuccess)
+        return SWG_ERR_CUDA;
+    return SWG_OK;
+  }
+  const int64_t per_gate = gate != nullptr ? M / G : M;
+  if (params) {
+    const size_t need = swg::bn_workspace_bytes(M, N, per_gate);
+    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return SWG_ERR_WORKSPACE;
+    const Range w = rng(workspace, static_cast<int64_t>(need));
+    if (any_overlap(&w, 1, outs, 5) || any_overlap(&w, 1, ins, 8)) return SWG_ERR_PARAM_INVALID;
+  }
+  st = check_device();
+  if (st != SWG_OK) return st;
+  const swg::BnBwdArgs a{dy, dh, u, h, stats, gamma_post, gamma_pre, gate, du, dresidual, dgamma_post, dgamma_pre,
+                         dgate, M, N, M > 1 ? lddy : 0, M > 1 ? lddh : 0, M > 1 ? ldu : 0, M > 1 ? ldh : 0, per_gate,
+                         alpha, static_cast<int>(wdtype), static_cast<int>(gdtype), post, pre, nullptr, nullptr};
+  return cuda_status(swg::launch_block_norm_bwd(a, params ? workspace : nullptr, static_cast<int>(dtype), s));
+}
+
+// ---------------------------------------------------------------- linear layer
+namespace {
+
+inline bool known_act(int act) {
+  return act == SWG_ACT_SILU || act == SWG_ACT_GELU || act == SWG_ACT_HARDSWISH || act == SWG_ACT_NONE;
+}
+// rows of n elements that TMA reads: 16-byte multiples apart
+inline swg_status tma_ld(int64_t ld, int64_t rows, int64_t n) {
+  if (rows > 1 && ld < n) return SWG_ERR_PARAM_INVALID;
+  return rows > 1 && (ld % 8 != 0 || ld > kMaxLd / 2 || too_large(rows, ld)) ? SWG_ERR_UNSUPPORTED : SWG_OK;
+}
+swg_status check_linear(int64_t M, int64_t K, int64_t N, int act, int dtype, int bdtype) {
+  if ((dtype != SWG_F16 && dtype != SWG_BF16) || (bdtype != dtype && bdtype != SWG_F32) || !known_act(act))
+    return SWG_ERR_PARAM_INVALID;
+  const swg_status st = check_shape(M, K, N);
+  if (st != SWG_OK) return st;
+  // every tile's index fits 32 bits
+  return too_large(M, std::max(K, N)) || too_large(K, N) || M > kMaxDim - 512 || K > kMaxDim - 512 || N > kMaxDim - 512
+             ? SWG_ERR_UNSUPPORTED
+             : SWG_OK;
+}
+
+}  // namespace
+
+swg_status linear_fwd(const void* x, const void* w, const void* b, const void* residual, void* y, void* z, int64_t M,
+                      int64_t K, int64_t N, int64_t ldx, int64_t ldr, swg_act act, swg_dtype dtype, swg_dtype bdtype,
+                      swg_stream_t stream) {
+  swg_status st = check_linear(M, K, N, act, dtype, bdtype);
+  if (st == SWG_OK) st = tma_ld(ldx, M, K);
+  if (st == SWG_OK && residual != nullptr) st = tma_ld(ldr, M, N);
+  if (st != SWG_OK) return st;
+  if (K == 0) return SWG_ERR_UNSUPPORTED;  // the product needs a reduction of positive length
+  if (M == 0 || N == 0) return SWG_OK;
+  if (!x || !w || !y) return SWG_ERR_NULLPTR;
+  for (const void* p : {x, w, b, residual, static_cast<const void*>(y), static_cast<const void*>(z)})
+    if (!aligned16(p)) return SWG_ERR_UNSUPPORTED;
+  const int64_t mn = M * N * 2;
+  const Range outs[] = {rng(y, mn), rng(z, z ? mn : 0)};
+  const Range ins[] = {rows_rng(x, M, K, ldx, 2), rng(w, K * N * 2), rng(b, b ? N * dtype_bytes(bdtype) : 0)};
+  const Range res = rows_rng(residual, M, N, ldr, 2);
+  if (any_overlap(outs, 2, ins, 3) || overlap(outs[1], res)) return SWG_ERR_PARAM_INVALID;
+  // the residual may be y itself
+  if (overlap(outs[0], res) && !(residual == y && (M == 1 || ldr == N))) return SWG_ERR_PARAM_INVALID;
+  st = check_device();
+  if (st != SWG_OK) return st;
+  const swg::LinearEpilogue e{b, residual, y, z, M > 1 ? ldr : N, static_cast<int>(act), dtype == SWG_F16,
+                              bdtype == SWG_F32};
+  return cuda_status(swg::launch_linear_fwd(x, w, e, M, K, N, M > 1 ? ldx : K, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t linear_bwd_workspace_size(int64_t M, int64_t K, int64_t N, swg_act act) {
+  if (M <= 0 || K <= 0 || N <= 0 || check_linear(M, K, N, act, SWG_BF16, SWG_BF16) != SWG_OK) return 0;
+  return align256(swg::linear_dz_workspace_bytes(M, N)) +
+         (act != SWG_ACT_NONE ? align256(static_cast<size_t>(M) * static_cast<size_t>(N) * 2) : 0);
+}
+
+swg_status linear_bwd(const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw, void* db,
+                      int64_t M, int64_t K, int64_t N, int64_t lddy, int64_t ldx, swg_act act, unsigned flags,
+                      swg_dtype dtype, swg_dtype bdtype, void* workspace, size_t workspace_bytes,
+                      swg_stream_t stream) {
+  swg_status st = check_linear(M, K, N, act, dtype, bdtype);
+  if (st == SWG_OK) st = tma_ld(lddy, M, N);
+  if (st == SWG_OK && dw != nullptr) st = tma_ld(ldx, M, K);
+  if (st != SWG_OK) return st;
+  if ((flags & ~SWG_ACCUMULATE) != 0) return SWG_ERR_PARAM_INVALID;
+  const bool acc = (flags & SWG_ACCUMULATE) != 0;
+  const bool want_dx = dx != nullptr && K > 0 && M > 0, want_dw = dw != nullptr && K > 0 && N > 0,
+             want_db = db != nullptr && N > 0;
+  if (!want_dx && !want_dw && !want_db) return SWG_OK;
+  const bool some = M > 0 && N > 0;  // dz has elements
+  if (some && (!dy || (want_dw && !x) || (want_dx && !w) || (act != SWG_ACT_NONE && !z))) return SWG_ERR_NULLPTR;
+  for (const void* p : {dy, x, w, z, static_cast<const void*>(dx), static_cast<const void*>(dw),
+                        static_cast<const void*>(db)})
+    if (!aligned16(p)) return SWG_ERR_UNSUPPORTED;
+  const int64_t mn = M * N * 2, mk = M * K * 2, kn = K * N * 2;
+  const Range outs[] = {rng(dx, dx ? mk : 0), rng(dw, dw ? kn : 0), rng(db, db ? N * dtype_bytes(bdtype) : 0)};
+  const Range ins[] = {rows_rng(dy, M, N, lddy, 2), rows_rng(x, M, K, ldx, 2), rng(w, w ? kn : 0),
+                       rng(z, z ? mn : 0)};
+  if (any_overlap(outs, 3, ins, 4)) return SWG_ERR_PARAM_INVALID;
+  const bool act_on = act != SWG_ACT_NONE;
+  const size_t part = align256(swg::linear_dz_workspace_bytes(M, N));
+  if (some && (want_db || act_on)) {
+    const size_t need = linear_bwd_workspace_size(M, K > 0 ? K : 8, N, act);
+    if (workspace == nullptr || workspace_bytes < need) return SWG_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SWG_ERR_UNSUPPORTED;
+    const Range ws = rng(workspace, static_cast<int64_t>(need));
+    if (any_overlap(&ws, 1, outs, 3) || any_overlap(&ws, 1, ins, 4)) return SWG_ERR_PARAM_INVALID;
+  }
+  st = check_device();
+  if (st != SWG_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!some) {  // sums over nothing
+    cudaError_t e = cudaSuccess;
+    if (want_dx) e = cudaMemsetAsync(dx, 0, static_cast<size_t>(mk), s);
+    if (e == cudaSuccess && want_dw && !acc) e = cudaMemsetAsync(dw, 0, static_cast<size_t>(kn), s);
+    if (e == cudaSuccess && want_db && !acc)
+      e = cudaMemsetAsync(db, 0, static_cast<size_t>(N * dtype_bytes(bdtype)), s);
+    return cuda_status(e);
+  }
+  const bool f16 = dtype == SWG_F16;
+  const void* dz = dy;
+  int64_t lddz = M > 1 ? lddy : N;
+  cudaError_t e = cudaSuccess;
+  if (want_db || act_on) {
+    void* to = act_on ? static_cast<char*>(workspace) + part : nullptr;
+    e = swg::launch_linear_dz(dy, z, to, want_db ? db : nullptr, M, N, lddz, static_cast<int>(act), f16,
+                              bdtype == SWG_F32, acc, static_cast<float*>(workspace), s);
+    if (act_on) {
+      dz = to;
+      lddz = N;
+    }
+  }
+  if (e == cudaSuccess && want_dw) {
+    const swg::LinearEpilogue epi{nullptr, acc ? dw : nullptr, dw, nullptr, N, swg::kLinearNoAct, f16, false};
+    e = swg::launch_linear_dw(x, dz, epi, M, K, N, M > 1 ? ldx : K, lddz, s);
+  }
+  if (e == cudaSuccess && want_dx) {
+    const swg::LinearEpilogue epi{nullptr, nullptr, dx, nullptr, K, swg::kLinearNoAct, f16, false};
+    e = swg::launch_linear_dx(dz, w, epi, M, K, N, lddz, s);
+  }
+  return cuda_status(e);
 }
 
 }  // extern "C"

@@ -1,0 +1,148 @@
+// The element-wise part of the linear layer's backward:
+//   dz = dy f'(z), rounded to the element type;  db = sum over rows of dz (in fp32, before the rounding)
+// HBM-bound: reads dy (and z), writes dz (without an activation dz is dy itself, and only the sums are taken).
+// A block takes 256 columns of a run of rows: warp w the columns (w & 3) 64 .. + 63 and the row group w >> 2, a lane
+// one 16-byte vector of them, so that eight rows are under way at once, with eight such steps in flight. No sum takes
+// more than 128 rows in one accumulator (like terms are rounded the same way, and a longer chain drifts); a second
+// kernel adds the blocks' partial rows in fp64 in a fixed order.
+#include <algorithm>
+
+#include "linear.cuh"
+
+namespace swg {
+namespace {
+
+using namespace lin;
+
+constexpr int kThreads = 256;
+constexpr int kCols = 256;    // columns of a block
+constexpr int kRowStep = 8;   // rows of one step
+constexpr int kMaxRows = 128 * kRowStep;  // rows of a block, at most
+
+__device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <bool kAct>
+__global__ void __launch_bounds__(kThreads)
+    linear_dz_kernel(const uint16_t* dy, const uint16_t* z, uint16_t* dz, float* part, int64_t M, int64_t N,
+                     int64_t lddy, int64_t rows_per_block, int act, bool f16) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = (warp & 3) * 64 + (lane & 7) * 8;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * kCols + c;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows_per_block, r1 = min(M, r0 + rows_per_block);
+  float2 sum[4] = {};
+  if (col < N) {
+    auto step = [&](const uint4& g, const uint4& v, int64_t row) {
+      float2 d[4], t[4];
+      widen8(g, f16, d);
+      if (kAct) {
+        widen8(v, f16, t);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = __fmul2_rn(d[e], activate_grad(t[e], act));
+        *reinterpret_cast<uint4*>(dz + row * N + col) = narrow8(d, f16);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = __fadd2_rn(sum[e], d[e]);
+    };
+    int64_t row = r0 + (warp >> 2) * 4 + (lane >> 3);
+    constexpr int kDeep = 8;
+    for (; row + (kDeep - 1) * kRowStep < r1; row += kDeep * kRowStep) {
+      uint4 g[kDeep], v[kDeep];
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+        g[u] = ld_stream(dy + (row + u * kRowStep) * lddy + col);
+        if (kAct) v[u] = ld_stream(z + (row + u * kRowStep) * N + col);
+      }
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) step(g[u], v[u], row + u * kRowStep);
+    }
+    for (; row < r1; row += kRowStep)
+      step(ld_stream(dy + row * lddy + col), kAct ? ld_stream(z + row * N + col) : make_uint4(0u, 0u, 0u, 0u), row);
+  }
+  if (part == nullptr) return;
+  // the four row lanes of a warp, then the two row groups
+  __shared__ float red[2][kCols];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+#pragma unroll
+    for (int o = 8; o <= 16; o *= 2) {
+      sum[e].x += __shfl_xor_sync(0xffffffffu, sum[e].x, o);
+      sum[e].y += __shfl_xor_sync(0xffffffffu, sum[e].y, o);
+    }
+    if (lane < 8) {
+      red[warp >> 2][c + 2 * e] = sum[e].x;
+      red[warp >> 2][c + 2 * e + 1] = sum[e].y;
+    }
+  }
+  __syncthreads();
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * kCols + threadIdx.x;
+  if (j < N) part[static_cast<int64_t>(blockIdx.y) * N + j] = red[0][threadIdx.x] + red[1][threadIdx.x];
+}
+
+// db from part [rows][N]: 32 columns a block, 32 threads a column take the rows in turn and are added in order
+__global__ void __launch_bounds__(1024) linear_db_kernel(const float* part, int64_t rows, int64_t N, void* db, int dtype,
+                                                         bool accumulate) {
+  __shared__ double acc[32][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + tx;
+  double s = 0.0;
+  if (j < N)
+    for (int64_t i = ty; i < rows; i += 32) s += static_cast<double>(part[i * N + j]);
+  acc[ty][tx] = s;
+  __syncthreads();
+  if (ty != 0 || j >= N) return;
+  double t = 0.0;
+  for (int k = 0; k < 32; ++k) t += acc[k][tx];
+  if (accumulate) t += static_cast<double>(row::load_any(db, j, dtype));
+  // rounded once: from fp64
+  if (dtype == 0) static_cast<float*>(db)[j] = static_cast<float>(t);
+  else if (dtype == 1) static_cast<__half*>(db)[j] = __double2half(t);
+  else static_cast<__nv_bfloat16*>(db)[j] = __double2bfloat16(t);
+}
+
+// rows of a block: about four blocks on each of 152 SMs (a plan that does not depend on the device, so that the
+// workspace's size does not either)
+int64_t rows_per_block(int64_t M, int64_t N) {
+  const int64_t gx = (N + kCols - 1) / kCols, blocks = std::max<int64_t>(1, 608 / gx);
+  const int64_t rows = ((M + blocks - 1) / blocks + kRowStep - 1) / kRowStep * kRowStep;
+  return std::min<int64_t>(kMaxRows, std::max<int64_t>(rows, 4 * kRowStep));
+}
+
+}  // namespace
+
+size_t linear_dz_workspace_bytes(int64_t M, int64_t N) {
+  const int64_t per = rows_per_block(M, N);
+  return static_cast<size_t>((M + per - 1) / per) * static_cast<size_t>(N) * sizeof(float);
+}
+
+cudaError_t launch_linear_dz(const void* dy, const void* z, void* dz, void* db, int64_t M, int64_t N, int64_t lddy,
+                             int act, bool f16, bool db_f32, bool accumulate, float* part, cudaStream_t stream) {
+  const int64_t per = rows_per_block(M, N);
+  // blocks beyond the grid's second dimension go in further launches
+  const int64_t chunks = (M + per - 1) / per;
+  for (int64_t c = 0; c < chunks; c += 65535) {
+    const int64_t n = std::min<int64_t>(65535, chunks - c), r = c * per, rows = std::min(M - r, n * per);
+    const dim3 grid(static_cast<unsigned>((N + kCols - 1) / kCols), static_cast<unsigned>(n));
+    const uint16_t* g = static_cast<const uint16_t*>(dy) + r * lddy;
+    float* p = db != nullptr ? part + c * N : nullptr;
+    if (act != kLinearNoAct)
+      linear_dz_kernel<true><<<grid, kThreads, 0, stream>>>(g, static_cast<const uint16_t*>(z) + r * N,
+                                                            static_cast<uint16_t*>(dz) + r * N, p, rows, N, lddy, per,
+                                                            act, f16);
+    else
+      linear_dz_kernel<false><<<grid, kThreads, 0, stream>>>(g, nullptr, nullptr, p, rows, N, lddy, per, act, f16);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (db == nullptr) return cudaSuccess;
+  linear_db_kernel<<<static_cast<unsigned>((N + 31) / 32), 1024, 0, stream>>>(part, chunks, N, db,
+                                                                              db_f32 ? 0 : (f16 ? 1 : 2), accumulate);
+  return cudaGetLastError();
+}
+
+}  // namespace swg

@@ -1,0 +1,308 @@
+// The linear layer's products with a small result: few rows (decoding, short batches), or a weight gradient
+// with a long reduction. out[c][l] = sum_r A[l, r] B[c, r], where l runs over the contiguous dimension of out
+// and c over its rows:
+//   forward  y[m][n]:  l = n, c = m, r = k   A = w (r outermost), B = x (r innermost)
+//   dx[m][k]:          l = k, c = m, r = n   A = w (r innermost), B = dz (r innermost)
+//   dw[k][n]:          l = n, c = k, r = m   A = dz, B = x (r outermost in both)
+// so that the weights, which are most of what a small call reads, are the 128-wide operand of the tensor
+// instruction (tcgen05.mma M = 128), and the rows of out its N: 16 to 256, as many as there are.
+//
+// What bounds it: reading w once, for few rows. One tile [128 l x NT c] is shared by a cluster of S blocks, each of
+// which takes a part of the reduction, so that all SMs read although there are only N / 128 tiles; the parts are
+// added in the cluster through shared memory in the blocks' order (no atomics, no workspace, one launch).
+//
+// A block: warp 0 lane 0 copies operand tiles (64 of r) into a ring with TMA, warp 1 lane 0 issues the tensor
+// instructions into TMEM, warps 4-7 move the sums from TMEM into the ring's memory; then all threads add the
+// cluster's parts, each block a share of the tile, and apply the epilogue: 16-byte loads and stores.
+//
+// Every wait is bounded: a block whose wait ran out sets the status word, issues nothing more, waits (bounded) for
+// its copies and products in flight and goes through the cluster's barriers like the others.
+#include <algorithm>
+
+#include "linear.cuh"
+
+namespace swg {
+namespace {
+
+using namespace lin;
+
+constexpr int kLanes = 128;               // of l in a tile
+constexpr int kRed = 64;                  // of r in a stage
+constexpr int kABytes = kLanes * kRed * 2;
+constexpr int kMaxStages = 16;
+constexpr int kThreads = 256;
+constexpr int kBoxBytes = 64 * kRed * 2;  // a box of 64 x 64 elements
+constexpr int kMaxSplit = 8;              // portable cluster size
+
+struct SplitArgs {
+  Epilogue epi;
+  uint32_t* status;
+  int L, C;              // sizes of l and c
+  int NT;                // c in a tile: 16, 32, 64, 128 or 256
+  int tiles_l, tiles_c;
+  int nkb, S;            // blocks of 64 of r; blocks of a cluster
+  int stages;
+  long long wait_limit;
+  int64_t stall_at;      // test injection: the producer of a cluster's last block stops there (-1: never)
+};
+
+struct SplitControl {
+  uint64_t full[kMaxStages], empty[kMaxStages], done;
+  uint32_t tmem_base;
+  volatile uint32_t abort_flag, issued, consumed;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <bool kAOuter, bool kBOuter>  // whether r is the outermost dimension of the operand in memory
+__global__ void __launch_bounds__(kThreads)
+    linear_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                        const SplitArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ SplitControl s;
+  uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = a.S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = static_cast<int>(blockIdx.x) / a.S;
+  const int l0 = (tile % a.tiles_l) * kLanes, c0 = (tile / a.tiles_l) * a.NT;
+  const int stage_bytes = kABytes + a.NT * kRed * 2;
+  // this block's part of the reduction: at least one block of 64
+  const int kb0 = static_cast<int>(static_cast<int64_t>(a.nkb) * rank / a.S);
+  const int n = static_cast<int>(static_cast<int64_t>(a.nkb) * (rank + 1) / a.S) - kb0;
+  const uint32_t tmem_cols = a.NT < 32 ? 32 : a.NT;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    mbar_init(&s.done, 1);
+    s.abort_flag = s.issued = s.consumed = 0u;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 1) {
+    tmem_alloc(&s.tmem_base, tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  auto timeout = [&]() {
+    if (a.status != nullptr) atomicOr(a.status, kStatusTimeout);
+    s.abort_flag = 1u;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < n && !s.abort_flag; ++i) {
+        if (rank == a.S - 1 && i == a.stall_at) break;
+        const int st = i % a.stages;
+        if (i >= a.stages && !mbar_wait(&s.empty[st], ((i / a.stages) - 1) & 1, a.wait_limit)) {
+          timeout();
+          break;
+        }
+        mbar_arrive_expect_tx(&s.full[st], stage_bytes);
+        uint8_t *pa = ring + st * stage_bytes, *pb = pa + kABytes;
+        const int r = (kb0 + i) * kRed;
+        if (kAOuter) {
+          tma_load_2d(pa, &tm_a, &s.full[st], l0, r);
+          tma_load_2d(pa + kBoxBytes, &tm_a, &s.full[st], l0 + 64, r);
+        } else {
+          tma_load_2d(pa, &tm_a, &s.full[st], r, l0);
+        }
+        if (kBOuter) {
+          for (int j = 0; j < a.NT / 64; ++j) tma_load_2d(pb + j * kBoxBytes, &tm_b, &s.full[st], c0 + 64 * j, r);
+        } else {
+          tma_load_2d(pb, &tm_b, &s.full[st], r, c0);
+        }
+        s.issued = i + 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f32(kLanes, a.NT, kAOuter, kBOuter, a.epi.f16);
+      for (int i = 0; i < n; ++i) {
+        const int st = i % a.stages;
+        if (!mbar_wait(&s.full[st], (i / a.stages) & 1, a.wait_limit)) {
+          timeout();
+          break;
+        }
+        s.consumed = i + 1;
+        tc_fence_after();
+        const uint32_t pa = smem_u32(ring + st * stage_bytes), pb = pa + kABytes;
+#pragma unroll
+        for (int k = 0; k < kRed / 16; ++k) {
+          const uint64_t da = kAOuter ? smem_desc(pa + 2048 * k, kBoxBytes, 1024) : smem_desc(pa + 32 * k, 16, 1024);
+          const uint64_t db = kBOuter ? smem_desc(pb + 2048 * k, kBoxBytes, 1024) : smem_desc(pb + 32 * k, 16, 1024);
+          umma_bf16(tmem, da, db, idesc, (i > 0 || k > 0) ? 1u : 0u);
+        }
+        umma_commit(&s.empty[st]);
+      }
+      umma_commit(&s.done);  // also after a timeout: what was issued has to be done before TMEM and the ring are reused
+    }
+  }
+  // every thread waits for the products, and so for the copies that they read: as long as they come on
+  __syncwarp();
+  uint32_t seen = ~0u;
+  while (!mbar_wait(&s.done, 0, a.wait_limit)) {
+    const uint32_t now = s.consumed;
+    if (now == seen) {
+      timeout();
+      break;
+    }
+    seen = now;
+  }
+  __syncthreads();
+  if (s.abort_flag) {  // copies that nothing reads
+    if (threadIdx.x == 0)
+      for (uint32_t i = s.consumed; i < s.issued; ++i)
+        if (!mbar_wait(&s.full[i % a.stages], (i / a.stages) & 1, a.wait_limit)) break;
+    __syncthreads();
+  }
+  // the sums into the ring's place, [c][l]
+  float* const part = reinterpret_cast<float*>(ring);
+  const int cols = min(a.NT, a.C - c0);
+  tc_fence_after();
+  if (warp >= 4) {
+    const int q = warp & 3;  // TMEM lane quarter
+    for (int c = 0; c < cols; c += 32) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+      tmem_ld_wait();
+      float* to = part + c * kLanes + q * 32 + lane;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (c + j < cols) to[j * kLanes] = __uint_as_float(v[j]);
+    }
+  }
+  tc_fence_before();
+  if (a.S > 1) cluster_sync();
+  else __syncthreads();
+  // this block's share of the tile: vectors of eight elements of a row
+  uint32_t peers[kMaxSplit];
+#pragma unroll
+  for (int i = 0; i < kMaxSplit; ++i) peers[i] = i < a.S && a.S > 1 ? cluster_addr(part, i) : smem_u32(part);
+  const Epilogue& p = a.epi;
+  for (int i = rank * kThreads + static_cast<int>(threadIdx.x); i < cols * (kLanes / 8); i += a.S * kThreads) {
+    const int c = i / (kLanes / 8), l = (i % (kLanes / 8)) * 8;
+    if (l0 + l >= a.L) continue;
+    const int64_t row = c0 + c, at = row * a.L + l0 + l;
+    uint4 res = make_uint4(0u, 0u, 0u, 0u);
+    if (p.residual != nullptr) res = *reinterpret_cast<const uint4*>(p.residual + row * p.ldr + l0 + l);
+    const uint32_t off = static_cast<uint32_t>(c * kLanes + l) * sizeof(float);
+    float2 v[4] = {};
+#pragma unroll
+    for (int k = 0; k < kMaxSplit; ++k) {
+      if (k >= a.S) break;
+      const float4 x = ld_cluster_f4(peers[k] + off), y = ld_cluster_f4(peers[k] + off + 16);
+      v[0] = __fadd2_rn(v[0], make_float2(x.x, x.y));
+      v[1] = __fadd2_rn(v[1], make_float2(x.z, x.w));
+      v[2] = __fadd2_rn(v[2], make_float2(y.x, y.y));
+      v[3] = __fadd2_rn(v[3], make_float2(y.z, y.w));
+    }
+    add_bias(p, l0 + l, v);
+    if (p.z != nullptr) *reinterpret_cast<uint4*>(p.z + at) = narrow8(v, p.f16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = activate(v[e], p.act);
+    if (p.residual != nullptr) {
+      float2 r[4];
+      widen8(res, p.f16, r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(v[e], r[e]);
+    }
+    *reinterpret_cast<uint4*>(p.y + at) = narrow8(v, p.f16);
+  }
+  if (a.S > 1) cluster_sync();  // no block leaves while another reads its sums
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+}
+
+struct SplitPlan {
+  int NT, S, stages, tiles_l, tiles_c, nkb;
+  int64_t tiles;
+};
+// NT: the rows of out (a multiple of 64 where they are read 64 at a time), up to 256. S: as many blocks a tile as
+// there is room for, two on an SM where the ring is small enough (NT <= 64), with at least one stage each.
+SplitPlan split_plan(int64_t L, int64_t C, int64_t R, bool b_outer, int sms) {
+  SplitPlan p;
+  p.NT = b_outer ? 64 : 16;
+  while (p.NT < 256 && p.NT < C) p.NT *= 2;
+  p.tiles_l = static_cast<int>((L + kLanes - 1) / kLanes);
+  p.tiles_c = static_cast<int>((C + p.NT - 1) / p.NT);
+  p.tiles = static_cast<int64_t>(p.tiles_l) * p.tiles_c;
+  p.nkb = static_cast<int>((R + kRed - 1) / kRed);
+  const int64_t room = (p.NT <= 64 ? 2 : 1) * sms;
+  p.S = static_cast<int>(std::min<int64_t>({kMaxSplit, std::max<int64_t>(1, room / p.tiles), p.nkb}));
+  const int ring = p.NT <= 64 ? 108 * 1024 : 192 * 1024;
+  p.stages = std::min(kMaxStages, ring / (kABytes + p.NT * kRed * 2));
+  return p;
+}
+
+template <bool kAOuter, bool kBOuter>
+cudaError_t launch_split(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t L, int64_t C, int64_t R,
+                         const Epilogue& epi, cudaStream_t stream) {
+  const SplitPlan p = split_plan(L, C, R, kBOuter, device_sm_count());
+  CUtensorMap ma, mb;
+  const uint64_t l = L, c = C, r = R, sa = lda * 2, sb = ldb * 2;
+  if (!(kAOuter ? encode_tmap_2d_bf16(&ma, A, l, r, sa, 64, kRed) : encode_tmap_2d_bf16(&ma, A, r, l, sa, kRed, kLanes)) ||
+      !(kBOuter ? encode_tmap_2d_bf16(&mb, B, c, r, sb, 64, kRed) : encode_tmap_2d_bf16(&mb, B, r, c, sb, kRed, p.NT)))
+    return cudaErrorInvalidValue;
+  const Injection inj = take_injection(kInjectLinearSplit);
+  const SplitArgs a{epi,       status_word_ptr(), static_cast<int>(L), static_cast<int>(C), p.NT,          p.tiles_l,
+                    p.tiles_c, p.nkb,             p.S,                 p.stages,            inj.wait_limit, inj.stall_at};
+  const size_t smem = static_cast<size_t>(p.stages) * (kABytes + p.NT * kRed * 2) + 1024;
+  const auto kernel = linear_split_kernel<kAOuter, kBOuter>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.tiles * p.S));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.S);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
+}
+
+Epilogue epilogue_of(const LinearEpilogue& e) {
+  return Epilogue{e.bias, static_cast<const uint16_t*>(e.residual), static_cast<uint16_t*>(e.y),
+                  static_cast<uint16_t*>(e.z), e.ldr, e.act, e.f16, e.bias_f32};
+}
+
+}  // namespace
+
+cudaError_t launch_linear_fwd(const void* x, const void* w, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
+                              int64_t ldx, cudaStream_t stream) {
+  return launch_split<true, false>(w, N, x, ldx, N, M, K, epilogue_of(epi), stream);
+}
+
+cudaError_t launch_linear_dx(const void* dz, const void* w, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
+                             int64_t lddz, cudaStream_t stream) {
+  return launch_split<false, false>(w, N, dz, lddz, K, M, N, epilogue_of(epi), stream);
+}
+
+cudaError_t launch_linear_dw(const void* x, const void* dz, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
+                             int64_t ldx, int64_t lddz, cudaStream_t stream) {
+  return launch_split<true, true>(dz, lddz, x, ldx, N, K, M, epilogue_of(epi), stream);
+}
+
+}  // namespace swg

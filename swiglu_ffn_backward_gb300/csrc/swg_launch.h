@@ -149,12 +149,83 @@ struct KdArgs {
 };
 cudaError_t launch_distill(const KdArgs& a, bool forward, bool backward, int dtype, cudaStream_t stream);
 
+// ---- norms between blocks (block_norm.cu); dtype, wdtype, gdtype 0 = f32, 1 = f16, 2 = bf16
+struct BnFwdArgs {
+  const void* u;           // [M, N], rows ldu apart
+  const void* residual;    // [M, N], rows ldr apart, or null (0)
+  const void* gamma_post;  // [N] of wdtype, or null (1)
+  const void* gamma_pre;   // [N] of wdtype, or null (1)
+  const void* gate;        // [M / rows_per_gate, N] of gdtype, or null (1)
+  void* h;                 // [M, N]; null: h is u
+  void* y;                 // [M, N] (with pre)
+  float* stats;            // [M, 2]: rstd of u (0 without post), of h (0 without pre)
+  int64_t M, N, ldu, ldr, rows_per_gate;  // rows_per_gate: M without a gate
+  float alpha, eps;
+  int wdtype, gdtype;
+  bool post, pre;
+};
+struct BnBwdArgs {
+  const void* dy;  // [M, N], rows lddy apart (with pre)
+  const void* dh;  // [M, N], rows lddh apart, or null (0)
+  const void* u;   // [M, N], rows ldu apart
+  const void* h;   // [M, N], rows ldh apart (with pre)
+  const float* stats;
+  const void *gamma_post, *gamma_pre, *gate;  // as in the forward
+  void* du;                                   // [M, N]
+  void* dres;                                 // [M, N], or null
+  void *dgamma_post, *dgamma_pre, *dgate;     // of the parameters' types, or null
+  int64_t M, N, lddy, lddh, ldu, ldh, rows_per_gate;
+  float alpha;
+  int wdtype, gdtype;
+  bool post, pre;
+  float* part;  // set by the launcher: the chunks' column sums (null: no parameter gradients)
+  float* mean;  // and the rows' rstd(h) mean(a h^), for rows of any length
+};
+// rows whose column sums are taken together
+struct BnChunks {
+  int64_t segment;      // rows of a gate row, or all
+  int64_t rows;         // of a chunk, at most
+  int64_t per_segment;  // chunks
+  int64_t chunks;
+};
+size_t bn_workspace_bytes(int64_t M, int64_t N, int64_t rows_per_gate);
+cudaError_t launch_block_norm_fwd(const BnFwdArgs& a, int dtype, cudaStream_t stream);
+// workspace: bn_workspace_bytes, or null where no parameter gradient is wanted
+cudaError_t launch_block_norm_bwd(const BnBwdArgs& a, void* workspace, int dtype, cudaStream_t stream);
+
+// ---- linear layer (linear_split.cu): fp16 (f16) or bf16, ld's multiples of 8 elements
+struct LinearEpilogue {  // z = product + bias, y = f(z) + residual; y, z dense
+  const void* bias;      // of the element type or fp32 (bias_f32), or null
+  const void* residual;  // rows ldr apart, or null; may be y itself
+  void* y;
+  void* z;               // or null
+  int64_t ldr;
+  int act;               // an activation, or kLinearNoAct
+  bool f16, bias_f32;
+};
+constexpr int kLinearNoAct = 16;
+// y [M, N] of x [M, K] w [K, N]
+cudaError_t launch_linear_fwd(const void* x, const void* w, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
+                              int64_t ldx, cudaStream_t stream);
+// y [M, K] of dz [M, N] w^T
+cudaError_t launch_linear_dx(const void* dz, const void* w, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
+                             int64_t lddz, cudaStream_t stream);
+// y [K, N] of x^T dz
+cudaError_t launch_linear_dw(const void* x, const void* dz, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
+                             int64_t ldx, int64_t lddz, cudaStream_t stream);
+// dz = dy f'(z), rounded (dz null: not stored), and db (or null) = its column sums before the rounding, plus the old
+// db with accumulate; part: linear_dz_workspace_bytes (with db). act kLinearNoAct: dz is dy, z is not read
+size_t linear_dz_workspace_bytes(int64_t M, int64_t N);
+cudaError_t launch_linear_dz(const void* dy, const void* z, void* dz, void* db, int64_t M, int64_t N, int64_t lddy,
+                             int act, bool f16, bool db_f32, bool accumulate, float* part, cudaStream_t stream);
+
 // one-shot fault injection for tests of the timeout path (swg_inject_stall): the next
 // launch of `kernel` (1 = x GEMM, 2 = fused x, 3 = fused w, 4 = forward, and those below) stops
 // issuing copies at ring entry `stall_at` and gives every wait `wait_limit` cycles. take_injection
 // returns the values for that launch (stall_at -1 and the normal limit when none is armed)
 // and disarms it.
 constexpr int kInjectLayerNormFwd = 16, kInjectLayerNormBwd = 17, kInjectTokenLogprobs = 18, kInjectDistill = 19;
+constexpr int kInjectLinearSplit = 32;
 struct Injection {
   int64_t stall_at;
   long long wait_limit;

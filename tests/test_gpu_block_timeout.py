@@ -1,0 +1,50 @@
+"""The timeout path of the linear layer's bounded waits: a producer that stops (armed on the host by swg_inject_stall)
+lets the waits of the next launch run out. The status, guard bands around the outputs and the same call afterwards."""
+
+import pytest
+import torch
+
+from ._block import check_linear_bwd, check_linear_fwd, linear_inputs
+from ._guard import check_all, guarded
+
+pytestmark = pytest.mark.gpu
+LIMIT = 1 << 20  # cycles, about half a millisecond
+BF16 = torch.bfloat16
+
+
+def _swg():
+    import swiglu_ffn_backward_gb300 as swg
+    return swg
+
+
+def _expect_timeout(swg):
+    with pytest.raises(swg.SwgError) as e:
+        swg.swg_check()
+    assert e.value.status == 6  # SWG_ERR_TIMEOUT
+    swg.swg_check()  # the status word was cleared
+
+
+# few rows by clusters of eight blocks, with rings that wrap, and rows by blocks on their own
+@pytest.mark.parametrize("M,K,N,entry", [(1, 4096, 256, 0), (1, 4096, 256, 2), (40, 16384, 128, 7), (256, 16384, 256, 5),
+                                         (200, 512, 128, 0)])
+def test_split_forward(M, K, N, entry):
+    swg, t = _swg(), linear_inputs(M, K, N, BF16)
+    g = {"y": guarded((M, N), BF16)}
+    swg.swg_inject_stall(swg.SWG_INJECT_LINEAR_SPLIT, entry, LIMIT)
+    swg.linear_fwd(t["x"], t["w"], out={"y": g["y"].t})
+    _expect_timeout(swg)
+    check_all(g)
+    check_linear_fwd(t, swg.linear_fwd(t["x"], t["w"], out={"y": g["y"].t}), BF16, None)
+    swg.swg_check()
+    check_all(g)
+
+
+@pytest.mark.parametrize("entry", [0, 3])
+def test_split_backward(entry):
+    # the armed launch is the first of the call, that of dw
+    swg, t = _swg(), linear_inputs(4096, 128, 256, BF16)
+    swg.swg_inject_stall(swg.SWG_INJECT_LINEAR_SPLIT, entry, LIMIT)
+    swg.linear_bwd(t["dy"], t["x"], t["w"])
+    _expect_timeout(swg)
+    check_linear_bwd(t, swg.linear_bwd(t["dy"], t["x"], t["w"]), BF16, None)
+    swg.swg_check()
