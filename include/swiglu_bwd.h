@@ -133,10 +133,15 @@ swg_status swg_check(swg_stream_t stream);
  *           (token_logprobs_fwd) and SWG_INJECT_DISTILL (distill_fwd,
  *           distill_fwd_bwd), whose last producer of each cluster stops (a
  *           block by itself is one), and, where a cluster shares a row,
- *           SWG_INJECT_LAYER_NORM_FWD and SWG_INJECT_LAYER_NORM_BWD, whose last
+ *           SWG_INJECT_LAYER_NORM_FWD and SWG_INJECT_LAYER_NORM_BWD, and
+ *           SWG_INJECT_BLOCK_NORM_FWD and SWG_INJECT_BLOCK_NORM_BWD, whose last
  *           block of each cluster sends no sums from row `entry` on. Their blocks
  *           go on to the end of their rows; a thread sends nothing behind a wait
  *           that ran out, and no block leaves before what was sent to it has come.
+ *           Of the linear layer: SWG_INJECT_LINEAR_SPLIT (the kernel for small
+ *           results: the last block of each cluster stops at its own entry) and
+ *           SWG_INJECT_LINEAR (the one on CTA pairs: both producers stop); linear_bwd's
+ *           first such launch is that of dw.
  * SWG_INJECT_NONE disarms an armed, unused injection (entry and limit are then
  * ignored); a later call replaces it. Returns SWG_ERR_PARAM_INVALID for another
  * kernel, entry < 0 or a limit below 1024 cycles. For tests only. */
@@ -150,7 +155,10 @@ typedef enum {
   SWG_INJECT_LAYER_NORM_BWD = 17,
   SWG_INJECT_TOKEN_LOGPROBS = 18,
   SWG_INJECT_DISTILL = 19,
-  SWG_INJECT_LINEAR_SPLIT = 32
+  SWG_INJECT_LINEAR_SPLIT = 32,
+  SWG_INJECT_LINEAR = 33,
+  SWG_INJECT_BLOCK_NORM_FWD = 34,
+  SWG_INJECT_BLOCK_NORM_BWD = 35
 } swg_inject_kernel;
 swg_status swg_inject_stall(swg_inject_kernel kernel, int64_t entry, int64_t wait_limit_cycles);
 

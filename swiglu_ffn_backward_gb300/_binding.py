@@ -291,6 +291,9 @@ SWG_INJECT_LAYER_NORM_BWD = 17
 SWG_INJECT_TOKEN_LOGPROBS = 18
 SWG_INJECT_DISTILL = 19
 SWG_INJECT_LINEAR_SPLIT = 32
+SWG_INJECT_LINEAR = 33
+SWG_INJECT_BLOCK_NORM_FWD = 34
+SWG_INJECT_BLOCK_NORM_BWD = 35
 
 
 def swg_inject_stall(kernel: int, entry: int, wait_limit_cycles: int) -> None:

@@ -102,7 +102,8 @@ swg_status swg_inject_stall(swg_inject_kernel kernel, int64_t entry, int64_t wai
   }
   if (kernel != SWG_INJECT_X_GEMM && kernel != SWG_INJECT_FUSED_X && kernel != SWG_INJECT_FUSED_W &&
       kernel != SWG_INJECT_FWD && kernel != SWG_INJECT_LAYER_NORM_FWD && kernel != SWG_INJECT_LAYER_NORM_BWD &&
-      kernel != SWG_INJECT_TOKEN_LOGPROBS && kernel != SWG_INJECT_DISTILL && kernel != SWG_INJECT_LINEAR_SPLIT)
+      kernel != SWG_INJECT_TOKEN_LOGPROBS && kernel != SWG_INJECT_DISTILL && kernel != SWG_INJECT_LINEAR_SPLIT &&
+      kernel != SWG_INJECT_LINEAR && kernel != SWG_INJECT_BLOCK_NORM_FWD && kernel != SWG_INJECT_BLOCK_NORM_BWD)
     return SWG_ERR_PARAM_INVALID;
   if (entry < 0 || wait_limit_cycles < 1024) return SWG_ERR_PARAM_INVALID;
   swg::arm_injection(static_cast<int>(kernel), entry, static_cast<long long>(wait_limit_cycles));

@@ -185,7 +185,8 @@ struct BnBwdArgs {
 struct BnChunks {
   int64_t segment;      // rows of a gate row, or all
   int64_t rows;         // of a chunk, at most
-  int64_t per_segment;  // chunks
+  int64_t apart;        // distance of a chunk's rows
+  int64_t per_segment;  // chunks: chunk c of a segment has its rows c % apart + apart (c / apart rows + i)
   int64_t chunks;
 };
 size_t bn_workspace_bytes(int64_t M, int64_t N, int64_t rows_per_gate);
@@ -225,7 +226,7 @@ cudaError_t launch_linear_dz(const void* dy, const void* z, void* dz, void* db, 
 // returns the values for that launch (stall_at -1 and the normal limit when none is armed)
 // and disarms it.
 constexpr int kInjectLayerNormFwd = 16, kInjectLayerNormBwd = 17, kInjectTokenLogprobs = 18, kInjectDistill = 19;
-constexpr int kInjectLinearSplit = 32;
+constexpr int kInjectLinearSplit = 32, kInjectLinear = 33, kInjectBlockNormFwd = 34, kInjectBlockNormBwd = 35;
 struct Injection {
   int64_t stall_at;
   long long wait_limit;

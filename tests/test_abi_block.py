@@ -109,8 +109,9 @@ def test_block_norm_bwd(b):
     assert f(*([None] * 13), 0, 16, 0, 16, 16, 16, 16, 1.0, both, 0, 0, 0, None, 0, None) == b.SWG_OK
 
 
-def test_linear_kernels_can_be_armed(b):
-    for kernel in (b.SWG_INJECT_LINEAR_SPLIT,):
+def test_kernels_can_be_armed(b):
+    for kernel in (b.SWG_INJECT_LINEAR_SPLIT, b.SWG_INJECT_LINEAR, b.SWG_INJECT_BLOCK_NORM_FWD,
+                   b.SWG_INJECT_BLOCK_NORM_BWD):
         assert b.lib.swg_inject_stall(kernel, 3, 1 << 20) == b.SWG_OK
         assert b.lib.swg_inject_stall(kernel, -1, 1 << 20) == b.SWG_ERR_PARAM_INVALID
     assert b.lib.swg_inject_stall(0, 0, 0) == b.SWG_OK

@@ -1,10 +1,10 @@
-"""The timeout path of the linear layer's bounded waits: a producer that stops (armed on the host by swg_inject_stall)
-lets the waits of the next launch run out. The status, guard bands around the outputs and the same call afterwards."""
+"""The timeout path of the bounded waits of the linear layer and of the norms between blocks: a producer that stops, or
+a block that sends no sums (armed on the host by swg_inject_stall), lets the waits of the next launch run out. The status, guard bands around the outputs and the same call afterwards."""
 
 import pytest
 import torch
 
-from ._block import check_linear_bwd, check_linear_fwd, linear_inputs
+from ._block import check_linear_bwd, check_linear_fwd, check_norm_bwd, check_norm_fwd, linear_inputs, norm_inputs
 from ._guard import check_all, guarded
 
 pytestmark = pytest.mark.gpu
@@ -47,4 +47,28 @@ def test_split_backward(entry):
     swg.linear_bwd(t["dy"], t["x"], t["w"])
     _expect_timeout(swg)
     check_linear_bwd(t, swg.linear_bwd(t["dy"], t["x"], t["w"]), BF16, None)
+    swg.swg_check()
+
+
+# rows shared by three to eight blocks, whole and ragged
+@pytest.mark.parametrize("M,N,row", [(30, 12288, 0), (30, 12288, 7), (9, 32768, 3), (12, 20001, 0), (12, 20001, 5)])
+def test_block_norm(M, N, row):
+    swg, t = _swg(), norm_inputs(M, N, BF16, torch.float32, 3)
+    kw = dict(gamma_post=t["gamma_post"], gamma_pre=t["gamma_pre"], gate=t["gate"])
+    g = {"h": guarded((M, N), BF16), "y": guarded((M, N), BF16), "stats": guarded((M, 2), torch.float32)}
+    swg.swg_inject_stall(swg.SWG_INJECT_BLOCK_NORM_FWD, row, LIMIT)
+    swg.block_norm_fwd(t["u"], t["residual"], out={k: v.t for k, v in g.items()}, **kw)
+    _expect_timeout(swg)
+    check_all(g)
+    out = swg.block_norm_fwd(t["u"], t["residual"], out={k: v.t for k, v in g.items()}, **kw)
+    check_norm_fwd(t, out, BF16)
+    gb = {"du": guarded((M, N), BF16), "dresidual": guarded((M, N), BF16), "dgamma_pre": guarded((N,), torch.float32)}
+    swg.swg_inject_stall(swg.SWG_INJECT_BLOCK_NORM_BWD, row, LIMIT)
+    args = (t["dy"], t["dh"], t["u"], out["h"], out["stats"])
+    swg.block_norm_bwd(*args, out={k: v.t for k, v in gb.items()}, **kw)
+    _expect_timeout(swg)
+    check_all(gb)
+    got = swg.block_norm_bwd(*args, out={k: v.t for k, v in gb.items()}, **kw)
+    check_norm_bwd(t, out["h"], out["stats"], got, BF16, torch.float32, BF16)
+    check_all(gb)
     swg.swg_check()
