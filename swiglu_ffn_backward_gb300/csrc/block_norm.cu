@@ -203,6 +203,285 @@ __global__ void __launch_bounds__(kMaxThreads) bn_fwd_long_kernel(const BnFwdArg
   }
 }
 
+// ---- many whole rows: a group's next rows are on their way into shared memory
+// A thread that holds a row's vectors has but one more row of them under way; four rows of all tensors in a ring of
+// shared memory, one bulk copy a tensor and row, keep the memory busy over a row's reductions. The group's first thread
+// issues the next copy into a row's stage behind the barrier of the next row's first sum, when the whole group has
+// read it. The stage is read again for each pass over the row, so that the row takes no registers between them.
+struct RingPlan {
+  int stages;        // rows of the ring of a group
+  int stage_bytes;   // of a row's tensors
+  int group_bytes;   // of a group's ring
+};
+constexpr int kMaxStages = 8;
+template <int kTensors>
+struct Ring {
+  uint64_t* full;
+  unsigned char* buf;
+  int stages, stage_bytes, at = 0;  // stage of the row that is read next
+  uint32_t parity = 0;
+  int64_t issued = 0;
+  Patience wait;
+  __device__ __forceinline__ Ring(unsigned char* smem, uint64_t* bars, const RingPlan& p, int group, const Stall& stall)
+      : full(bars + group * kMaxStages), buf(smem + group * p.group_bytes), stages(p.stages), stage_bytes(p.stage_bytes),
+        wait(stall.limit) {}
+  __device__ __forceinline__ void init() {
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+  }
+  // by the group's first thread: the next row's tensors, `bytes` of each from `from` (null: none) into the stage's
+  // slots of `slot` bytes
+  __device__ __forceinline__ void issue(const void* const (&from)[kTensors], const uint32_t (&bytes)[kTensors], int slot,
+                                        int64_t stall_at) {
+    if (wait.lost() || issued == stall_at) return;
+    const int st = static_cast<int>(issued % stages);
+    uint32_t all = 0;
+#pragma unroll
+    for (int i = 0; i < kTensors; ++i) all += from[i] != nullptr ? bytes[i] : 0u;
+    mbar_arrive_expect_tx(&full[st], all);
+#pragma unroll
+    for (int i = 0; i < kTensors; ++i)
+      if (from[i] != nullptr && bytes[i] > 0) bulk_g2s(buf + st * stage_bytes + i * slot, from[i], bytes[i], &full[st]);
+    ++issued;
+  }
+  // the stage of the next row, landed
+  __device__ __forceinline__ const unsigned char* next() {
+    wait(&full[at], parity);
+    const unsigned char* p = buf + at * stage_bytes;
+    if (++at == stages) {
+      at = 0;
+      parity ^= 1u;
+    }
+    return p;
+  }
+  // copies that nothing waited for have to land before the block ends
+  __device__ __forceinline__ void end(uint32_t* status) {
+    if (!wait.lost()) return;
+    if (status != nullptr) atomicOr(status, kStatusTimeout);
+    for (int64_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
+      if (!mbar_wait(&full[i % stages], static_cast<uint32_t>(i / stages) & 1u)) break;
+  }
+};
+__device__ __forceinline__ Raw ld_stage(const unsigned char* p) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  return Raw{{u.x, u.y, u.z, u.w}};
+}
+// eight or four columns of a gate in a stage, of the tensor's type or fp32
+template <typename T>
+__device__ __forceinline__ void stage_pairs(const unsigned char* p, int vector, bool f32, float2 (&f)[kPairs<T>]) {
+  if (sizeof(T) == 2 && f32) {
+    const Raw a = ld_stage(p + vector * 32), b = ld_stage(p + vector * 32 + 16);
+    f[0] = get_pair<float>(a, 0);
+    f[1] = get_pair<float>(a, 1);
+    f[2 % kPairs<T>] = get_pair<float>(b, 0);
+    f[3 % kPairs<T>] = get_pair<float>(b, 1);
+    return;
+  }
+  const Raw a = ld_stage(p + vector * 16);
+#pragma unroll
+  for (int e = 0; e < kPairs<T>; ++e) f[e] = get_pair<T>(a, e);
+}
+// Sums over a group of whole warps, up to eight; every thread gets them, added in a fixed order. Two buffers alternate,
+// so that one barrier a sum is enough.
+struct WarpRows {
+  float* buf;  // of the group: 2 x 32
+  int warps, id, turn = 0;
+  __device__ __forceinline__ WarpRows(float* smem, int G)
+      : buf(smem + (threadIdx.x / G) * 64), warps(G >> 5), id(1 + static_cast<int>(threadIdx.x) / G) {}
+  __device__ __forceinline__ float* next() {
+    float* b = buf + turn;
+    turn ^= 32;
+    return b;
+  }
+  __device__ __forceinline__ void meet() const {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(warps * 32) : "memory");
+  }
+  __device__ __forceinline__ float one(float v) {
+    v = warp_sum(v);
+    if (warps == 1) {
+      __syncwarp();
+      return v;
+    }
+    float* b = next();
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) b[threadIdx.x / 32 % warps] = v;
+    meet();
+    v = (lane & 7) < warps ? b[lane & 7] : 0.0f;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  // Three at once: lanes exchange halves of what they hold, so that it takes six shuffles in place of fifteen.
+  __device__ __forceinline__ void three(float (&v)[3]) {
+    const int lane = threadIdx.x & 31;
+    const bool b4 = (lane & 16) != 0, b3 = (lane & 8) != 0;
+    // lanes with bit 4: v[2] (and nothing), the others v[0] and v[1]
+    float x = (b4 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, b4 ? v[0] : v[2], 16);
+    float y = (b4 ? 0.0f : v[1]) + __shfl_xor_sync(0xffffffffu, b4 ? v[1] : 0.0f, 16);
+    x = (b3 ? y : x) + __shfl_xor_sync(0xffffffffu, b3 ? x : y, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    // lanes 0 .. 7: v[0], 8 .. 15: v[1], 16 .. 23: v[2]
+    if (warps > 1) {
+      float* b = next();
+      if ((lane & 7) == 0) b[(threadIdx.x / 32 % warps) * 4 + (lane >> 3)] = x;
+      meet();
+      x = (lane & 7) < warps ? b[(lane & 7) * 4 + (lane >> 3)] : 0.0f;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    } else {
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] = __shfl_sync(0xffffffffu, x, 8 * i);
+  }
+};
+
+// Forward: a group takes rows one after the other, so that it keeps its gate row's columns in registers until the next
+// gate row begins; kRowGate: a gate for each row is one more tensor in the ring.
+constexpr int kFwdBlocks = 3;  // blocks of 256 threads an SM, with 80 registers a thread
+template <bool kRowGate>
+constexpr int kFwdRingBlocks = 2;
+template <typename T, int R, bool kShared, bool kRowGate, bool kFull>
+__global__ void __maxnreg__(128)
+    bn_fwd_ring_kernel(const BnFwdArgs a, const RingPlan plan, int G, int S, Stall stall, uint32_t* status) {
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ uint64_t bars[8 * kMaxStages];
+  __shared__ float smem[8 * 64];
+  __shared__ ClusterSlots slots;
+  constexpr int E = kElems<T>, P = kPairs<T>, kTensors = kRowGate ? 3 : 2;
+  const int groups = kShared ? 1 : blockDim.x / G, group = kShared ? 0 : threadIdx.x / G;
+  const int rank = kShared ? static_cast<int>(cluster_ctarank()) : 0, in = kShared ? threadIdx.x : threadIdx.x % G;
+  const int64_t units = static_cast<int64_t>(kShared ? gridDim.x / S : gridDim.x) * groups;
+  const int64_t unit = kShared ? blockIdx.x / S : static_cast<int64_t>(blockIdx.x) * groups + group;
+  const int64_t begin = a.M * unit / units, end = a.M * (unit + 1) / units;
+  const int n = static_cast<int>(a.N) / E, n0 = rank * R * G;  // vectors of a row, and the first of this block's
+  const int mine = min(R * G, n - n0);
+  const bool add = kFull || a.residual != nullptr, post_norm = kFull || a.post, pre_norm = kFull || a.pre;
+  const bool f32 = a.wdtype == 0, gated = a.gate != nullptr, gate32 = a.gdtype == 0;
+  const float inv_n = 1.0f / static_cast<float>(a.N);
+  const float2 alpha = pair(a.alpha);
+  const uint32_t per_gate = static_cast<uint32_t>(a.rows_per_gate);
+  Ring<kTensors> ring(dyn, bars, plan, group, stall);
+  const bool first = in == 0;
+  if (first) {
+    ring.init();
+    fence_mbar_init();
+  }
+  __syncthreads();
+  WarpRows sums(smem, G);
+  SharedSum<kShared, 1> share(slots, S, stall);
+  const int64_t stop_at = kShared ? -1 : stall.at;
+  auto issue = [&](int64_t r) {
+    const void* from[kTensors];
+    uint32_t bytes[kTensors];
+    from[0] = static_cast<const T*>(a.u) + r * a.ldu + n0 * E;
+    from[1] = add ? static_cast<const T*>(a.residual) + r * a.ldr + n0 * E : nullptr;
+    bytes[0] = bytes[1] = static_cast<uint32_t>(mine) * 16u;
+    if constexpr (kRowGate) {
+      const int64_t es = gate32 ? 4 : sizeof(T);
+      from[2] = static_cast<const char*>(a.gate) + (r * a.N + n0 * E) * es;
+      bytes[2] = static_cast<uint32_t>(mine) * static_cast<uint32_t>(E * es);
+    }
+    ring.issue(from, bytes, R * G * 16, stop_at);
+  };
+  if (first)
+    for (int64_t r = begin; r < min(end, begin + ring.stages); ++r) issue(r);
+  float2 pre[R][P], q[R][P];  // gamma_pre; gamma_post, or (without kRowGate) that times the gate
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (in + i * G < mine) {
+      load_weights<T, false>(a.gamma_pre, (n0 + in + i * G) * E, a.N, f32, 1.0f, pre[i]);
+      if (kRowGate || !gated) load_weights<T, false>(a.gamma_post, (n0 + in + i * G) * E, a.N, f32, 1.0f, q[i]);
+    }
+  int64_t gate_end = gated && !kRowGate ? begin : INT64_MAX;  // the row from which on another gate row holds
+  int64_t ahead = begin + ring.stages;  // the row to copy next
+  bool refill = false;
+  auto rstd_of = [&](float2 s2) {
+    float s[1] = {sums.one(s2.x + s2.y)};
+    if (refill && ahead < end) issue(ahead++);
+    refill = false;
+    share(s);
+    return rsqrtf(fmaf(s[0], inv_n, a.eps));
+  };
+  T *h = static_cast<T*>(a.h) + begin * a.N + (n0 + in) * E, *y = static_cast<T*>(a.y) + begin * a.N + (n0 + in) * E;
+  for (int64_t r = begin; r < end; ++r, h += a.N, y += a.N) {
+    if (kShared && static_cast<uint64_t>(r) >= static_cast<uint64_t>(stall.at)) share.silence();
+    const unsigned char* stage = ring.next();
+    refill = first && r > begin;  // behind the row's first sum the group has read the row before
+    if (!kRowGate && r >= gate_end) {
+      const int64_t g = static_cast<uint32_t>(r) / per_gate;
+      gate_end = (g + 1) * per_gate;
+      const char* gate = static_cast<const char*>(a.gate) + g * a.N * (gate32 ? 4 : sizeof(T));
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (in + i * G >= mine) continue;
+        float2 post[P];
+        load_weights<T, false>(gate, (n0 + in + i * G) * E, a.N, gate32, 1.0f, q[i]);
+        load_weights<T, false>(a.gamma_post, (n0 + in + i * G) * E, a.N, f32, 1.0f, post);
+#pragma unroll
+        for (int e = 0; e < P; ++e) q[i][e] = __fmul2_rn(q[i][e], post[e]);
+      }
+    }
+    Raw w[R];
+    float2 s2 = pair(0.0f);
+    float ru = 1.0f, rh = 0.0f;
+    if (post_norm) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (in + i * G >= mine) continue;
+        const Raw u = ld_stage(stage + (in + i * G) * 16);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const float2 v = get_pair<T>(u, e);
+          s2 = __ffma2_rn(v, v, s2);
+        }
+      }
+      ru = rstd_of(s2);
+      s2 = pair(0.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (in + i * G >= mine) continue;
+      w[i] = ld_stage(stage + (in + i * G) * 16);
+      Raw res = {};
+      if (add) res = ld_stage(stage + (R * G + in + i * G) * 16);
+      float2 gate[P];
+      if constexpr (kRowGate) stage_pairs<T>(stage + 2 * R * G * 16, in + i * G, gate32, gate);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        float2 v = get_pair<T>(w[i], e);
+        if (post_norm || gated) {
+          v = __fmul2_rn(v, __fmul2_rn(pair(ru), q[i][e]));
+          if constexpr (kRowGate) v = __fmul2_rn(v, gate[e]);
+        }
+        if (add) v = __ffma2_rn(alpha, get_pair<T>(res, e), v);
+        set_pair<T>(w[i], e, v);  // h as it is stored
+        v = get_pair<T>(w[i], e);
+        s2 = __ffma2_rn(v, v, s2);
+      }
+      if (kFull || a.h != nullptr) st_raw(h + i * G * E, w[i]);
+    }
+    if (pre_norm) {
+      rh = rstd_of(s2);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (in + i * G >= mine) continue;
+#pragma unroll
+        for (int e = 0; e < P; ++e)
+          set_pair<T>(w[i], e, __fmul2_rn(get_pair<T>(w[i], e), __fmul2_rn(pair(rh), pre[i][e])));
+        st_raw(y + i * G * E, w[i]);
+      }
+    }
+    if (in + n0 == 0) {
+      a.stats[2 * r] = post_norm ? ru : 0.0f;
+      a.stats[2 * r + 1] = rh;
+    }
+  }
+  if (first) ring.end(status);
+  else if (ring.wait.lost() && status != nullptr) atomicOr(status, kStatusTimeout);
+  share.end(status);
+}
+
 // ---- backward: a row in the registers of a group of threads, one vector of each tensor a thread
 // A group takes chunks of rows, chunk after chunk, and writes the chunk's two column sums. kShared: as in the forward.
 struct Sums4 {
@@ -404,6 +683,202 @@ __global__ void __launch_bounds__(kMaxGroup)
   share.end(status);
 }
 
+// Backward over a ring, R vectors of a row a thread. The gate row is the chunk's own (kRowGate: one more tensor in the
+// ring), so that its columns and gamma_post's are one factor in registers.
+constexpr int kBwdBlock = 256, kBwdBlocks = 2;  // threads of a block, at most, and such blocks an SM
+template <typename T, int R, bool kShared, bool kRowGate, bool kFull>
+__global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
+    bn_bwd_ring_kernel(const BnBwdArgs a, const BnChunks k, const RingPlan plan, int G, int S, Stall stall,
+                       uint32_t* status) {
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ uint64_t bars[8 * kMaxStages];
+  __shared__ float smem[8 * 64];
+  __shared__ Sums4 slots;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int E = kElems<T>, P = kPairs<T>, kTensors = kRowGate ? 5 : 4;
+  const int groups = kShared ? 1 : blockDim.x / G, group = kShared ? 0 : threadIdx.x / G;
+  const int rank = kShared ? static_cast<int>(cluster_ctarank()) : 0, in = kShared ? threadIdx.x : threadIdx.x % G;
+  const uint32_t units = (kShared ? gridDim.x / S : gridDim.x) * groups;
+  const uint32_t unit = kShared ? blockIdx.x / S : blockIdx.x * groups + group;
+  const int n = static_cast<int>(a.N) / E, n0 = rank * R * G, mine = min(R * G, n - n0);
+  const bool first = in == 0;
+  const float inv_n = 1.0f / static_cast<float>(a.N);
+  const bool post_norm = kFull || a.post, pre_norm = kFull || a.pre, add = kFull || a.dh != nullptr;
+  const bool f32 = a.wdtype == 0, gate32 = a.gdtype == 0, dgate_rows = kRowGate && a.dgate != nullptr;
+  auto column = [&](int i) { return (n0 + in + i * G) * E; };
+  Ring<kTensors> ring(dyn, bars, plan, group, stall);
+  if (first) {
+    ring.init();
+    fence_mbar_init();
+  }
+  __syncthreads();
+  WarpRows sums(smem, G);
+  std::conditional_t<kShared, ClusterSum3, NoSum3> share(slots, S, stall);
+  const int64_t stop_at = kShared ? -1 : stall.at;
+  // the rows of the group's chunks in turn: chunk c, rows r .. end - 1
+  struct Walk {  // 32 bits hold them: at most as many chunks as rows
+    uint32_t c, r, end;
+  };
+  const uint32_t chunks = static_cast<uint32_t>(k.chunks), per_segment = static_cast<uint32_t>(k.per_segment);
+  const uint32_t segment = static_cast<uint32_t>(k.segment), chunk_rows = static_cast<uint32_t>(k.rows);
+  auto enter = [&](Walk& w) {
+    const uint32_t seg = w.c / per_segment;
+    w.r = seg * segment + (w.c - seg * per_segment) * chunk_rows;
+    w.end = min((seg + 1) * segment, w.r + chunk_rows);
+  };
+  Walk ahead{unit, 0, 0};
+  if (ahead.c < chunks) enter(ahead);
+  auto issue = [&]() {
+    if (ahead.c >= chunks) return;
+    const int64_t r = ahead.r;
+    const void* from[kTensors];
+    uint32_t bytes[kTensors];
+    from[0] = static_cast<const T*>(a.u) + r * a.ldu + n0 * E;
+    from[1] = pre_norm ? static_cast<const T*>(a.h) + r * a.ldh + n0 * E : nullptr;
+    from[2] = pre_norm ? static_cast<const T*>(a.dy) + r * a.lddy + n0 * E : nullptr;
+    from[3] = add ? static_cast<const T*>(a.dh) + r * a.lddh + n0 * E : nullptr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bytes[i] = static_cast<uint32_t>(mine) * 16u;
+    if constexpr (kRowGate) {
+      const int64_t es = gate32 ? 4 : sizeof(T);
+      from[4] = static_cast<const char*>(a.gate) + (r * a.N + n0 * E) * es;
+      bytes[4] = static_cast<uint32_t>(mine) * static_cast<uint32_t>(E * es);
+    }
+    ring.issue(from, bytes, R * G * 16, stop_at);
+    if (++ahead.r == ahead.end) {
+      ahead.c += units;
+      if (ahead.c < chunks) enter(ahead);
+    }
+  };
+  if (first)
+    for (int i = 0; i < ring.stages; ++i) issue();
+  float2 pre[R][P], post[R][P];  // gamma_pre; gamma_post, without kRowGate times the gate
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (in + i * G < mine) load_weights<T, false>(a.gamma_pre, column(i), a.N, f32, 1.0f, pre[i]);
+  bool refill = false;
+  struct Vectors {  // a thread's vector of each tensor, from the stage
+    Raw u, h, dy, dh;
+  };
+  auto vectors = [&](const unsigned char* stage, int i) {
+    Vectors v = {};
+    const unsigned char* p = stage + (in + i * G) * 16;
+    v.u = ld_stage(p);
+    if (pre_norm) {
+      v.h = ld_stage(p + R * G * 16);
+      v.dy = ld_stage(p + 2 * R * G * 16);
+    }
+    if (add) v.dh = ld_stage(p + 3 * R * G * 16);
+    return v;
+  };
+  for (Walk w{unit, 0, 0}; w.c < chunks; w.c += units) {
+    enter(w);
+    float2 ss[R][P], sp[R][P];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) ss[i][e] = sp[i][e] = pair(0.0f);
+      if (in + i * G >= mine) continue;
+      load_weights<T, false>(a.gamma_post, column(i), a.N, f32, 1.0f, post[i]);
+      if (!kRowGate && a.gate != nullptr) {
+        float2 g[P];
+        const int64_t row = static_cast<uint32_t>(w.r) / static_cast<uint32_t>(a.rows_per_gate);
+        load_weights<T, false>(static_cast<const char*>(a.gate) + row * a.N * (gate32 ? 4 : sizeof(T)), column(i), a.N,
+                               gate32, 1.0f, g);
+#pragma unroll
+        for (int e = 0; e < P; ++e) post[i][e] = __fmul2_rn(g[e], post[i][e]);
+      }
+    }
+    auto rstds = [&](uint32_t r) {  // 4-byte aligned
+      const float* p = a.stats + 2 * static_cast<int64_t>(r);
+      return make_float2(p[0], p[1]);
+    };
+    float2 stats = rstds(w.r);
+    int64_t at = static_cast<int64_t>(w.r) * a.N + column(0);
+    for (uint32_t r = w.r; r < w.end; ++r) {
+      if (kShared && static_cast<uint64_t>(r) >= static_cast<uint64_t>(stall.at)) share.silence();
+      const float fu = post_norm ? stats.x : 1.0f, fh = pre_norm ? stats.y : 0.0f;
+      if (r + 1 < w.end) stats = rstds(r + 1);
+      const unsigned char* stage = ring.next();
+      const float2 rh = pair(fh);
+      // sums of dy gamma_pre h, of q u (dh + rstd(h) dy gamma_pre) and of q u h: the rows' factors come behind them
+      float2 s0 = pair(0.0f), s1 = s0, s2 = s0;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (in + i * G >= mine) continue;
+        const Vectors v = vectors(stage, i);
+        float2 q[P];
+        if constexpr (kRowGate) stage_pairs<T>(stage + 4 * R * G * 16, in + i * G, gate32, q);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const float2 h = get_pair<T>(v.h, e), dy = get_pair<T>(v.dy, e), x = __fmul2_rn(dy, h);
+          float2 qu = __fmul2_rn(post[i][e], get_pair<T>(v.u, e));
+          if constexpr (kRowGate) qu = __fmul2_rn(q[e], qu);
+          sp[i][e] = __ffma2_rn(x, rh, sp[i][e]);
+          s0 = __ffma2_rn(x, pre[i][e], s0);
+          s1 = __ffma2_rn(qu, __ffma2_rn(__fmul2_rn(rh, pre[i][e]), dy, get_pair<T>(v.dh, e)), s1);
+          s2 = __ffma2_rn(qu, h, s2);
+        }
+      }
+      float s[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
+      sums.three(s);
+      if (first && refill) issue();  // the group has read the row before
+      refill = true;
+      share(s);
+      const float m1 = s[0] * fh * inv_n * fh;  // rstd(h) mean(a h^)
+      // d = dh + rstd(h) a - m1 h^;  du = rstd(u) q d - u c2
+      const float2 c1 = pair(-m1 * fh), ru = pair(fu);
+      const float2 c2 = pair(post_norm ? -fmaf(-m1 * fh, s[2], s[1]) * fu * inv_n : 0.0f);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (in + i * G >= mine) continue;
+        Vectors x = vectors(stage, i);
+        float2 q[P];
+        if constexpr (kRowGate) stage_pairs<T>(stage + 4 * R * G * 16, in + i * G, gate32, q);
+        Raw dg;
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const float2 d = __ffma2_rn(__fmul2_rn(rh, pre[i][e]), get_pair<T>(x.dy, e),
+                                      __ffma2_rn(c1, get_pair<T>(x.h, e), get_pair<T>(x.dh, e)));
+          const float2 uh = __fmul2_rn(get_pair<T>(x.u, e), ru);
+          float2 qd = __fmul2_rn(post[i][e], d);
+          if constexpr (kRowGate) {
+            const float2 du_hat = __fmul2_rn(d, uh);
+            ss[i][e] = __ffma2_rn(du_hat, q[e], ss[i][e]);
+            qd = __fmul2_rn(q[e], qd);
+            const float2 v = __fmul2_rn(du_hat, post[i][e]);
+            if (gate32 && dgate_rows) *reinterpret_cast<float2*>(static_cast<float*>(a.dgate) + (at + i * G * E) + 2 * e) = v;
+            else set_pair<T>(dg, e, v);
+          } else {
+            ss[i][e] = __ffma2_rn(d, uh, ss[i][e]);
+          }
+          set_pair<T>(x.dh, e, __fmul2_rn(pair(a.alpha), d));
+          const float2 v = __ffma2_rn(uh, c2, qd);
+          set_pair<T>(x.u, e, post_norm ? __fmul2_rn(ru, v) : v);
+        }
+        st_raw(static_cast<T*>(a.du) + at + i * G * E, x.u);
+        if (kFull || a.dres != nullptr) st_raw(static_cast<T*>(a.dres) + at + i * G * E, x.dh);
+        if (dgate_rows && !gate32) st_raw(static_cast<T*>(a.dgate) + at + i * G * E, dg);
+      }
+      at += a.N;
+    }
+    if (a.part == nullptr) continue;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (in + i * G >= mine) continue;
+      float* to = a.part + static_cast<int64_t>(w.c) * 2 * a.N + column(i);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        *reinterpret_cast<float2*>(to + 2 * e) = ss[i][e];
+        *reinterpret_cast<float2*>(to + a.N + 2 * e) = sp[i][e];
+      }
+    }
+  }
+  if (first) ring.end(status);
+  else if (ring.wait.lost() && status != nullptr) atomicOr(status, kStatusTimeout);
+  share.end(status);
+}
+
 // What belongs to element j of row r in the backward, for rows of any length. u^ is u where there is no norm after the block.
 template <typename T>
 struct Element {
@@ -471,59 +946,150 @@ __global__ void __launch_bounds__(kColThreads) bn_param_long_kernel(const BnBwdA
   to[a.N + j] = p;
 }
 
-// The parameters' gradients from the chunks' sums: 32 columns a block, 32 threads a column take the chunks in turn and
-// are added in order. Blocks of the first row sum all chunks, for dgamma_post (each times its gate row) and
-// dgamma_pre; those of row 1 + g the chunks of gate row g. At most 64 terms are added in fp32, these parts in fp64. A
-// programmatic dependent of the kernel before it, whose writes are visible after griddepcontrol.wait.
-constexpr int kReduceCols = 32, kReduceSlices = 32;
-__global__ void __launch_bounds__(kReduceCols* kReduceSlices)
-    bn_reduce_kernel(const BnBwdArgs a, const BnChunks k, int64_t first_gate, bool sums) {
-  __shared__ double acc[kReduceSlices][kReduceCols];
-  const int c = threadIdx.x % kReduceCols, slice = threadIdx.x / kReduceCols;
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * kReduceCols + c;
-  const bool whole = sums && blockIdx.y == 0;  // over all chunks
-  const int64_t g = first_gate + blockIdx.y - (sums ? 1 : 0);
-  const int64_t begin = whole ? 0 : g * k.per_segment, end = whole ? k.chunks : begin + k.per_segment;
-  const bool weigh = whole && a.gate != nullptr && a.rows_per_gate > 1 && j < a.N;
-  const int64_t most = whole ? 2 * a.N : a.N;
+// The parameters' gradients from the chunks' sums, 128 columns a block (four a lane), sixteen warps. The first
+// `sum_blocks` blocks sum all chunks, for dgamma_post (each times its gate row) and dgamma_pre: a cluster of Q blocks
+// takes 128 columns, its 16 Q warps the chunks in turn. In the others `slices` warps sum the chunks of a gate row. A
+// lane adds 64 terms in sequence, then these parts, then the warps' and the blocks' sums: a fixed order. A programmatic dependent of the kernel before it, whose
+// writes are visible after griddepcontrol.wait. Its time is that of a few loads in turn: 304 chunks of 4096 columns,
+// eight gate rows 6 us; by blocks of 1024 threads for 32 columns and each gate row it took 36.
+constexpr int kReduceCols = 128, kReduceWarps = 16;
+__global__ void __launch_bounds__(32 * kReduceWarps)
+    bn_reduce_kernel(const BnBwdArgs a, const BnChunks k, int Q, int64_t sum_blocks, int slices, int64_t first_gate) {
+  __shared__ float acc[kReduceWarps][kReduceCols];
+  __shared__ float all[kReduceCols];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  double t = 0.0;
-  if (j < most) {
-    const float* part = a.part + j;
-    auto term = [&](int64_t n) {
-      const float v = part[n * 2 * a.N];
-      return weigh ? v * load_any(a.gate, n / k.per_segment * a.N + j, a.gdtype) : v;
-    };
-    for (int64_t i = begin + slice; i < end; i += 64 * kReduceSlices) {
-      const int64_t stop = min(end, i + 64 * kReduceSlices);
-      float s = 0.0f;
-      int64_t n = i;
-      for (; n + 7 * kReduceSlices < stop; n += 8 * kReduceSlices) {
-        float v[8];
+  // the warp's sums of the chunks begin, begin + step, ... before end, at columns j0 + lane + 32 e below most; eight
+  // chunks' loads at once (anything behind the last column)
+  auto sum = [&](int64_t begin, int64_t end, int64_t step, int64_t j0, int64_t most, bool weigh) {
+    constexpr int kDeep = 8;
+    const float* part[4];
+    int64_t col[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = term(n + e * kReduceSlices);
-        s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-      }
-      for (; n < stop; n += kReduceSlices) s += term(n);
-      t += static_cast<double>(s);
+    for (int e = 0; e < 4; ++e) {
+      col[e] = min(j0 + lane + 32 * e, most - 1);
+      part[e] = a.part + col[e];
     }
+    const uint32_t per_segment = static_cast<uint32_t>(k.per_segment);
+    // the chunk's gate at the lane's columns (1 for those of dgamma_pre): bits, and as values
+    auto gate_bits = [&](int64_t n, int e) -> uint32_t {
+      const int64_t at = static_cast<uint32_t>(n) / per_segment * a.N + min(col[e], a.N - 1);
+      return a.gdtype == 0 ? static_cast<const uint32_t*>(a.gate)[at] : static_cast<const uint16_t*>(a.gate)[at];
+    };
+    auto gate_of = [&](uint32_t bits, int e) {
+      if (col[e] >= a.N) return 1.0f;
+      const unsigned short h = static_cast<unsigned short>(bits);
+      return a.gdtype == 0   ? __uint_as_float(bits)
+             : a.gdtype == 1 ? __half2float(__ushort_as_half(h))
+                             : __uint_as_float(bits << 16);
+    };
+    float t[4] = {}, s[4] = {};
+    int64_t n = begin;
+    for (int count = 1; n + (kDeep - 1) * step < end; n += kDeep * step, ++count) {
+      float v[kDeep][4];
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[u][e] = part[e][(n + u * step) * 2 * a.N];
+      }
+      if (weigh) {
+        uint32_t g[kDeep][4];
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[u][e] = gate_bits(n + u * step, e);
+        }
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[u][e] *= gate_of(g[u][e], e);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s[e] += ((v[0][e] + v[1][e]) + (v[2][e] + v[3][e])) + ((v[4][e] + v[5][e]) + (v[6][e] + v[7][e]));
+      if (count % 8 == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          t[e] += s[e];
+          s[e] = 0.0f;
+        }
+      }
+    }
+    float v[kDeep][4];
+    uint32_t g[kDeep][4] = {};
+#pragma unroll
+    for (int u = 0; u < kDeep - 1; ++u) {
+      if (n + u * step >= end) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[u][e] = part[e][(n + u * step) * 2 * a.N];
+        if (weigh) g[u][e] = gate_bits(n + u * step, e);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kDeep - 1; ++u) {
+      if (n + u * step >= end) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += weigh ? v[u][e] * gate_of(g[u][e], e) : v[u][e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[warp][lane + 32 * e] = t[e] + s[e];
+    __syncthreads();
+  };
+  if (blockIdx.x < sum_blocks) {
+    const int rank = static_cast<int>(blockIdx.x % Q);
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x / Q) * kReduceCols;
+    sum(rank * kReduceWarps + warp, k.chunks, static_cast<int64_t>(Q) * kReduceWarps, j0, 2 * a.N,
+        a.gate != nullptr && a.rows_per_gate > 1 && j0 < a.N);
+    float t = 0.0f;
+    if (threadIdx.x < kReduceCols) {
+#pragma unroll
+      for (int w = 0; w < kReduceWarps; ++w) t += acc[w][threadIdx.x];
+      all[threadIdx.x] = t;
+    }
+    if (Q > 1) {
+      cluster_sync();
+      if (rank == 0 && threadIdx.x < kReduceCols)
+        for (int i = 1; i < Q; ++i) t += ld_cluster_f32(&all[threadIdx.x], i);
+      cluster_sync();  // no block leaves before its sums have been read
+    }
+    const int64_t j = j0 + threadIdx.x;
+    if (rank != 0 || threadIdx.x >= kReduceCols || j >= 2 * a.N) return;
+    if (j < a.N) {
+      if (a.dgamma_post != nullptr) store_any(a.dgamma_post, j, a.wdtype, t);
+    } else if (a.dgamma_pre != nullptr) {
+      store_any(a.dgamma_pre, j - a.N, a.wdtype, t);
+    }
+    return;
   }
-  acc[slice][c] = t;
-  __syncthreads();
-  if (slice != 0 || j >= most) return;
-  for (int i = 1; i < kReduceSlices; ++i) t += acc[i][c];
-  const float v = static_cast<float>(t);
-  if (!whole) {
+  const int64_t id = blockIdx.x - sum_blocks, blocks = (a.N + kReduceCols - 1) / kReduceCols;
+  const int rows = kReduceWarps / slices;  // gate rows of a block
+  const int64_t g0 = first_gate + id / blocks * rows, gates = a.M / a.rows_per_gate, j0 = id % blocks * kReduceCols;
+  const int64_t g = g0 + warp / slices, begin = g * k.per_segment;
+  sum(begin + warp % slices, g < gates ? begin + k.per_segment : begin, slices, j0, a.N, false);
+  for (int i = threadIdx.x; i < rows * kReduceCols; i += blockDim.x) {
+    const int row = i / kReduceCols, c = i % kReduceCols;
+    const int64_t j = j0 + c;
+    if (g0 + row >= gates || j >= a.N) continue;
+    float t = 0.0f;
+    for (int w = 0; w < slices; ++w) t += acc[row * slices + w][c];
     const float post = a.post && a.gamma_post != nullptr ? load_any(a.gamma_post, j, a.wdtype) : 1.0f;
-    store_any(a.dgate, g * a.N + j, a.gdtype, v * post);
-  } else if (j < a.N) {
-    if (a.dgamma_post != nullptr) store_any(a.dgamma_post, j, a.wdtype, v);
-  } else if (a.dgamma_pre != nullptr) {
-    store_any(a.dgamma_pre, j - a.N, a.wdtype, v);
+    store_any(a.dgate, (g0 + row) * a.N + j, a.gdtype, t * post);
   }
 }
 
 // ---- host
+// Rows shared by a cluster: S blocks of G threads, R vectors each
+struct Shared {
+  int S, G;
+};
+Shared share_row(int64_t n, int R) {
+  const int64_t threads = (n + R - 1) / R;
+  const int S = static_cast<int>(threads <= kMaxCluster * kBlock ? (threads + kBlock - 1) / kBlock : kMaxCluster);
+  return Shared{S, static_cast<int>((threads + 32 * S - 1) / (32 * S)) * 32};
+}
+
 // Chunks of rows whose column sums are taken together: of one gate row where the gate has fewer rows than M, of at most
 // 128 rows (like terms are rounded the same way, and a longer chain drifts), and such that `units` groups that take
 // them in turn have nearly equal work: rows, and for each chunk the writing of its sums, about one row's.
@@ -557,37 +1123,49 @@ int64_t units_of(int64_t n) {
   return std::max<int64_t>(1, kSms / ((n + kMaxGroup - 1) / kMaxGroup));
 }
 constexpr int64_t kLongUnits = 304;  // for rows of any length
+// the same for whole rows in rings: groups of two vectors a thread, 512 threads an SM
+int64_t ring_units(int64_t n) {
+  constexpr int64_t kSms = 152;
+  if (n <= 2 * kBwdBlock) return kSms * (kBwdBlocks * kBwdBlock / group_threads(n, 2));
+  const Shared s = share_row(n, 2);
+  return std::max<int64_t>(1, kSms * (kBwdBlocks * kBwdBlock / s.G) / s.S);
+}
 
 cudaError_t launch_reduce(const BnBwdArgs& a, const BnChunks& k, cudaStream_t stream) {
   const bool sums = a.dgamma_post != nullptr || a.dgamma_pre != nullptr;
   const int64_t gates = a.dgate != nullptr && a.rows_per_gate > 1 ? a.M / a.rows_per_gate : 0;
-  const int64_t all = gates + (sums ? 1 : 0);
-  const unsigned gx = static_cast<unsigned>(((sums ? 2 : 1) * a.N + kReduceCols - 1) / kReduceCols);
-  for (int64_t y = 0; y < all; y += 65535) {
-    const bool first = sums && y == 0;
+  int Q = 1;  // eight chunks a warp or more
+  while (Q < kMaxCluster && k.chunks >= 2 * Q * kReduceWarps * 8) Q *= 2;
+  int slices = 1;
+  while (slices < kReduceWarps && k.per_segment >= 2 * slices * 4) slices *= 2;
+  const int64_t rows = kReduceWarps / slices, columns = (a.N + kReduceCols - 1) / kReduceCols;
+  const int64_t sum_blocks = sums ? (2 * a.N + kReduceCols - 1) / kReduceCols * Q : 0;
+  const int64_t most = std::max<int64_t>(1, (int64_t(1) << 30) / columns);  // groups of gate rows of a launch
+  int64_t from = 0;
+  const int64_t all = (gates + rows - 1) / rows;
+  do {
+    const int64_t n = std::min(most, all - from);
+    const bool first = from == 0;
+    const int64_t lead = first ? sum_blocks : 0, blocks = (lead + n * columns + Q - 1) / Q * Q;
+    if (blocks == 0) break;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(gx, static_cast<unsigned>(std::min<int64_t>(65535, all - y)));
-    cfg.blockDim = dim3(kReduceCols * kReduceSlices);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(32 * kReduceWarps);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(Q);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = y == 0 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, bn_reduce_kernel, a, k, first ? int64_t(0) : y - (sums ? 1 : 0), first);
+    cfg.numAttrs = first ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, bn_reduce_kernel, a, k, Q, lead, slices, from * rows);
     if (e != cudaSuccess) return e;
-  }
+    from += n;
+  } while (from < all);
   return cudaSuccess;
-}
-
-// Rows shared by a cluster: S blocks of G threads, R vectors each
-struct Shared {
-  int S, G;
-};
-Shared share_row(int64_t n, int R) {
-  const int64_t threads = (n + R - 1) / R;
-  const int S = static_cast<int>(threads <= kMaxCluster * kBlock ? (threads + kBlock - 1) / kBlock : kMaxCluster);
-  return Shared{S, static_cast<int>((threads + 32 * S - 1) / (32 * S)) * 32};
 }
 
 template <typename T>
@@ -595,6 +1173,66 @@ cudaError_t fwd_long(const BnFwdArgs& a, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.M, 65536));
   bn_fwd_long_kernel<T><<<grid, kMaxThreads, 0, stream>>>(a);
   return cudaGetLastError();
+}
+// The ring of a group: as many rows of `row` bytes as fit beside one another in the memory of `blocks` blocks an SM,
+// `groups` groups each.
+constexpr int64_t kRingMemory = 220 * 1024;  // of an SM's 228 KB: what is static and 1 KB a block stay free
+RingPlan ring_plan(int64_t row, int blocks, int groups) {
+  const int64_t fit = kRingMemory / blocks / groups / row;
+  RingPlan p;
+  p.stages = static_cast<int>(std::min<int64_t>(kMaxStages, fit));
+  p.stage_bytes = static_cast<int>(row);
+  p.group_bytes = p.stages * p.stage_bytes;
+  return p;
+}
+// Rows from which on a group's ring pays: below, the first rows' copies cost more than loads (1 to 2 us).
+constexpr int64_t kRingRows = 4;
+
+// bytes of a row of a gate for each row, in those of the row itself
+template <typename T>
+int64_t gate_slots(int gdtype) {
+  return gdtype == 0 ? 4 / sizeof(T) : 1;
+}
+template <typename T, bool kRowGate, bool kFull>
+cudaError_t fwd_ring_one(const BnFwdArgs& a, int64_t n, cudaStream_t stream) {
+  const auto kernel = bn_fwd_ring_kernel<T, 2, false, kRowGate, kFull>;
+  const int G = group_threads(n, 2), groups = G < kBlock ? kBlock / G : 1, block = groups * G;
+  const RingPlan p = ring_plan((2 + (kRowGate ? gate_slots<T>(a.gdtype) : 0)) * 2 * G * 16,
+                               std::max(1, kFwdRingBlocks<kRowGate> * kBlock / block), groups);
+  const size_t smem = static_cast<size_t>(groups) * p.group_bytes;
+  int64_t blocks;
+  {
+    static std::mutex mu;
+    static FitCache cache;
+    std::lock_guard<std::mutex> lk(mu);
+    const cudaError_t e = blocks_that_fit(kernel, cache, block, smem, blocks);
+    if (e != cudaSuccess) return e;
+  }
+  blocks = std::min(blocks, (a.M + groups - 1) / groups);
+  kernel<<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, p, G, 1, take_stall(kInjectBlockNormFwd),
+                                                                status_word_ptr());
+  return cudaGetLastError();
+}
+template <typename T, bool kRowGate, bool kFull>
+cudaError_t fwd_ring_shared(const BnFwdArgs& a, int64_t n, cudaStream_t stream) {
+  const auto kernel = bn_fwd_ring_kernel<T, 2, true, kRowGate, kFull>;
+  const Shared s = share_row(n, 2);
+  const RingPlan p = ring_plan((2 + (kRowGate ? gate_slots<T>(a.gdtype) : 0)) * 2 * s.G * 16,
+                               std::max(1, kFwdRingBlocks<kRowGate> * kBlock / s.G), 1);
+  static std::mutex mu;
+  static StreamCache cache;
+  std::lock_guard<std::mutex> lk(mu);
+  const cudaError_t e = clusters_that_fit(kernel, cache, s.G, p.group_bytes, s.S);
+  if (e != cudaSuccess) return e;
+  if (cache.clusters < 1) return fwd_long<T>(a, stream);
+  ClusterLaunch l(s.G, p.group_bytes, s.S, std::min<int64_t>(cache.clusters, a.M), stream);
+  return cudaLaunchKernelEx(&l.cfg, kernel, a, p, s.G, s.S, take_stall(kInjectBlockNormFwd), status_word_ptr());
+}
+
+template <typename T, bool kRowGate, bool kFull>
+cudaError_t fwd_ring(const BnFwdArgs& a, int64_t n, cudaStream_t stream) {
+  return n <= 2 * kBlock ? fwd_ring_one<T, kRowGate, kFull>(a, n, stream)
+                         : fwd_ring_shared<T, kRowGate, kFull>(a, n, stream);
 }
 template <typename T, int R, bool kRagged>
 cudaError_t fwd_one(const BnFwdArgs& a, int64_t n, cudaStream_t stream) {
@@ -630,6 +1268,13 @@ template <typename T, bool kRagged>
 cudaError_t fwd_any(const BnFwdArgs& a, cudaStream_t stream) {
   const int64_t n = (a.N + (kRagged ? 2 * kElems<T> - 2 : 0)) / kElems<T>;
   if (n <= 32) return fwd_one<T, 1, kRagged>(a, n, stream);
+  if (!kRagged && n <= 2 * kMaxCluster * kBlock) {
+    if (a.M * ((n + 1) / 2) >= kRingRows * kFwdBlocks * kBlock * device_sm_count()) {
+      const bool row_gate = a.gate != nullptr && a.rows_per_gate == 1, full = a.post && a.pre && a.residual != nullptr;
+      if (row_gate) return full ? fwd_ring<T, true, true>(a, n, stream) : fwd_ring<T, true, false>(a, n, stream);
+      return full ? fwd_ring<T, false, true>(a, n, stream) : fwd_ring<T, false, false>(a, n, stream);
+    }
+  }
   if (n <= 2 * kMaxGroup) return fwd_one<T, 2, kRagged>(a, n, stream);
   if (n <= 2 * kMaxCluster * kMaxGroup) return fwd_shared<T, kRagged>(a, n, stream);
   return fwd_long<T>(a, stream);
@@ -698,9 +1343,60 @@ cudaError_t bwd_shared(const BnBwdArgs& a, int64_t n, cudaStream_t stream) {
   }
   return a.part == nullptr ? cudaSuccess : launch_reduce(a, k, stream);
 }
+template <typename T, bool kRowGate, bool kFull>
+cudaError_t bwd_ring_one(const BnBwdArgs& a, const BnChunks& k, int64_t n, cudaStream_t stream) {
+  const auto kernel = bn_bwd_ring_kernel<T, 2, false, kRowGate, kFull>;
+  const int G = group_threads(n, 2), groups = kBwdBlock / G, block = groups * G;
+  const RingPlan p = ring_plan((4 + (kRowGate ? gate_slots<T>(a.gdtype) : 0)) * 2 * G * 16,
+                               std::max(kBwdBlocks, kBwdBlocks * kBwdBlock / block), groups);
+  const size_t smem = static_cast<size_t>(groups) * p.group_bytes;
+  int64_t blocks;
+  {
+    static std::mutex mu;
+    static FitCache cache;
+    std::lock_guard<std::mutex> lk(mu);
+    const cudaError_t e = blocks_that_fit(kernel, cache, block, smem, blocks);
+    if (e != cudaSuccess) return e;
+  }
+  blocks = std::min(blocks, (k.chunks + groups - 1) / groups);
+  kernel<<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, k, p, G, 1, take_stall(kInjectBlockNormBwd),
+                                                                status_word_ptr());
+  return cudaGetLastError();
+}
+template <typename T, bool kRowGate, bool kFull>
+cudaError_t bwd_ring_shared(const BnBwdArgs& a, const BnChunks& k, int64_t n, cudaStream_t stream) {
+  const auto kernel = bn_bwd_ring_kernel<T, 2, true, kRowGate, kFull>;
+  const Shared s = share_row(n, 2);
+  const RingPlan p = ring_plan((4 + (kRowGate ? gate_slots<T>(a.gdtype) : 0)) * 2 * s.G * 16,
+                               std::max(kBwdBlocks, kBwdBlocks * kBwdBlock / s.G), 1);
+  static std::mutex mu;
+  static StreamCache cache;
+  std::lock_guard<std::mutex> lk(mu);
+  const cudaError_t e = clusters_that_fit(kernel, cache, s.G, p.group_bytes, s.S);
+  if (e != cudaSuccess) return e;
+  if (cache.clusters < 1) return cudaErrorLaunchOutOfResources;
+  ClusterLaunch l(s.G, p.group_bytes, s.S, std::min<int64_t>(cache.clusters, k.chunks), stream);
+  return cudaLaunchKernelEx(&l.cfg, kernel, a, k, p, s.G, s.S, take_stall(kInjectBlockNormBwd), status_word_ptr());
+}
+template <typename T, bool kRowGate, bool kFull>
+cudaError_t bwd_ring(const BnBwdArgs& a, const BnChunks& k, int64_t n, cudaStream_t stream) {
+  const cudaError_t e = n <= 2 * kBwdBlock ? bwd_ring_one<T, kRowGate, kFull>(a, k, n, stream)
+                                           : bwd_ring_shared<T, kRowGate, kFull>(a, k, n, stream);
+  return e != cudaSuccess || a.part == nullptr ? e : launch_reduce(a, k, stream);
+}
 template <typename T, bool kRagged>
 cudaError_t bwd_any(const BnBwdArgs& a, cudaStream_t stream) {
   const int64_t n = (a.N + (kRagged ? 2 * kElems<T> - 2 : 0)) / kElems<T>;
+  if (!kRagged && n > 32 && n <= 2 * kMaxCluster * kBwdBlock) {
+    const int64_t units = ring_units(n);
+    if (a.M >= kRingRows * units) {
+      const BnChunks k = chunks_of(a.M, a.rows_per_gate, units, 1);
+      const bool row_gate = a.gate != nullptr && a.rows_per_gate == 1;
+      const bool full = a.post && a.pre && a.dh != nullptr && a.dres != nullptr;
+      if (row_gate) return full ? bwd_ring<T, true, true>(a, k, n, stream) : bwd_ring<T, true, false>(a, k, n, stream);
+      return full ? bwd_ring<T, false, true>(a, k, n, stream) : bwd_ring<T, false, false>(a, k, n, stream);
+    }
+  }
   if (n <= 16) return bwd_groups<T, kRagged, true>(a, n, stream);
   if (n <= kMaxGroup) return bwd_groups<T, kRagged, false>(a, n, stream);
   if (n <= kMaxCluster * kMaxGroup) return bwd_shared<T, kRagged>(a, n, stream);
@@ -720,6 +1416,7 @@ int64_t most_chunks(int64_t M, int64_t N, int64_t rows_per_gate) {
     for (const int64_t ragged : {0, 1}) {
       const int64_t n = (N + (ragged ? 2 * e - 2 : e - 1)) / e, apart = ragged ? e / std::gcd(N, e) : 1;
       most = std::max(most, chunks_of(M, rows_per_gate, units_of(n), apart).chunks);
+      if (!ragged) most = std::max(most, chunks_of(M, rows_per_gate, ring_units(n), 1).chunks);
     }
   }
   return most;

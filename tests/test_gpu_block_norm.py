@@ -156,6 +156,33 @@ def test_many_rows(M, N, gates):
     _run(M, N, BF16, F32, gates)
 
 
+# many whole rows: their loads go through a ring in shared memory, for groups of one warp to clusters of eight blocks
+@pytest.mark.parametrize("M,N,dtype", [(20011, 264, BF16), (40000, 132, F32), (9001, 512, F16), (2003, 4096, BF16), (1200, 2048, F32),
+                                       (900, 5120, BF16), (1801, 8192, F16), (700, 12288, BF16), (640, 12288, F32), (300, 32768, BF16)])
+@pytest.mark.parametrize("gates", ["none", "one", "some", "rows"])
+def test_ring(M, N, dtype, gates):
+    divisor = next(d for d in (7, 5, 3, 2, 1) if M % d == 0)
+    G = {"none": 0, "one": 1, "some": divisor if divisor > 1 else 1, "rows": M}[gates]
+    _run(M, N, dtype, F32 if gates == "one" else dtype, G, F32 if gates != "some" else dtype, alpha=0.9)
+
+
+@pytest.mark.parametrize("residual,post,pre,dh", [(False, True, True, True), (True, False, True, True), (True, True, False, True),
+                                                  (True, True, True, False), (False, False, True, False)])
+@pytest.mark.parametrize("gates", [0, 4, 2400])
+def test_ring_parts(residual, post, pre, dh, gates):
+    _run(2400, 4096, BF16, BF16, gates, residual=residual, post=post, pre=pre, dh=dh)
+    _run(2400, 8192, F16, F32, gates, residual=residual, post=post, pre=pre, dh=dh)
+
+
+def test_ring_layouts():
+    for layout in ("padded", "dense"):
+        _run(2003, 4096, BF16, BF16, 1, layout=layout)
+    swg, t = _swg(), norm_inputs(3000, 4096, BF16, F32, 3)
+    a = swg.block_norm_fwd(t["u"], t["residual"][:1].expand(3000, 4096), gate=t["gate"])
+    b = swg.block_norm_fwd(t["u"], t["residual"][:1].expand(3000, 4096).contiguous(), gate=t["gate"])
+    assert all(torch.equal(a[k], b[k]) for k in a)
+
+
 def test_like_rows_do_not_drift():
     # parameter gradients of equal rows: in one chain of fp32 additions like terms are rounded the same way
     swg, M, N = _swg(), 200000, 64
@@ -199,7 +226,8 @@ def test_rows_of_zeros_and_non_finite_rows():
     assert torch.equal(got["du"][keep], cleanb["du"][keep])
 
 
-@pytest.mark.parametrize("M,N,dtype", [(300, 264, BF16), (300, 101, F32), (20, 9000, BF16)])
+@pytest.mark.parametrize("M,N,dtype", [(300, 264, BF16), (300, 101, F32), (20, 9000, BF16), (3000, 4096, BF16),
+                                       (800, 12288, BF16)])
 def test_same_bits_every_time(M, N, dtype):
     swg, t = _swg(), norm_inputs(M, N, dtype, F32, 4)
     kw = dict(gamma_post=t["gamma_post"], gamma_pre=t["gamma_pre"], gate=t["gate"])

@@ -50,8 +50,10 @@ def test_split_backward(entry):
     swg.swg_check()
 
 
-# rows shared by three to eight blocks, whole and ragged
-@pytest.mark.parametrize("M,N,row", [(30, 12288, 0), (30, 12288, 7), (9, 32768, 3), (12, 20001, 0), (12, 20001, 5)])
+# rows shared by three to eight blocks, whole and ragged; many rows in rings, by blocks on their own (the entry is a
+# ring's then) and by clusters
+@pytest.mark.parametrize("M,N,row", [(30, 12288, 0), (30, 12288, 7), (9, 32768, 3), (12, 20001, 0), (12, 20001, 5),
+                                     (2400, 4096, 0), (2400, 4096, 3), (2400, 4096, 5), (21000, 512, 2), (699, 12288, 200)])
 def test_block_norm(M, N, row):
     swg, t = _swg(), norm_inputs(M, N, BF16, torch.float32, 3)
     kw = dict(gamma_post=t["gamma_post"], gamma_pre=t["gamma_pre"], gate=t["gate"])
