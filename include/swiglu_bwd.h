@@ -428,8 +428,9 @@ swg_status layer_norm_bwd(const void* dy, const void* x, const float* stats,
  * dx [M, K], dw [K, N] and db [N] (of bdtype; of the unrounded dz) are each optional
  * (NULL: not computed; w is then not read without dx, x not without dw). dy is
  * also the residual's gradient. With SWG_ACCUMULATE in `flags`, dw and db are read
- * and replaced by old + this call's, rounded once. With db or an activation,
- * `workspace` holds linear_bwd_workspace_size(M, K, N, act) bytes (16-byte aligned).
+ * and replaced by old + this call's, rounded once. `workspace` holds
+ * linear_bwd_workspace_size(M, K, N, act) bytes (16-byte aligned); it may be NULL for
+ * dx alone without an activation.
  * Products are accumulated in fp32 on the tensor cores in a fixed order (bitwise
  * reproducible), bias, activation and residual are applied in fp32, each output is
  * rounded once (RNE). Any M >= 0; K and N multiples of 8, leading dimensions too

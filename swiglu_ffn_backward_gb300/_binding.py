@@ -1068,7 +1068,7 @@ def linear_bwd(dy, x, w, z=None, act: str | None = None, bias: bool = True, need
         db_dtype = g.dtype
     K = 0 if K is None else K
     ws = None
-    if bias or code != SWG_ACT_NONE:
+    if bias or need_dw or code != SWG_ACT_NONE:
         ws = _workspace(lib.linear_bwd_workspace_size(M, K if K > 0 else 8, N, code), dev, workspace)
         if workspace is not None:
             _device_of(g, ws)

@@ -1232,7 +1232,7 @@ swg_status linear_fwd(const void* x, const void* w, const void* b, const void* r
 
 size_t linear_bwd_workspace_size(int64_t M, int64_t K, int64_t N, swg_act act) {
   if (M <= 0 || K <= 0 || N <= 0 || check_linear(M, K, N, act, SWG_BF16, SWG_BF16) != SWG_OK) return 0;
-  return align256(swg::linear_dz_workspace_bytes(M, N)) +
+  return align256(swg::linear_dz_workspace_bytes(M, N)) + align256(swg::linear_dw_workspace_bytes(M, K, N)) +
          (act != SWG_ACT_NONE ? align256(static_cast<size_t>(M) * static_cast<size_t>(N) * 2) : 0);
 }
 
@@ -1260,8 +1260,10 @@ swg_status linear_bwd(const void* dy, const void* x, const void* w, const void* 
                        rng(z, z ? mn : 0)};
   if (any_overlap(outs, 3, ins, 4)) return SWG_ERR_PARAM_INVALID;
   const bool act_on = act != SWG_ACT_NONE;
-  const size_t part = align256(swg::linear_dz_workspace_bytes(M, N));
-  if (some && (want_db || act_on)) {
+  // the column sums' parts, those of dw, and dz
+  const size_t sums = align256(swg::linear_dz_workspace_bytes(M, N));
+  const size_t parts = some && K > 0 ? align256(swg::linear_dw_workspace_bytes(M, K, N)) : 0;
+  if (some && (want_db || act_on || (want_dw && parts > 0))) {
     const size_t need = linear_bwd_workspace_size(M, K > 0 ? K : 8, N, act);
     if (workspace == nullptr || workspace_bytes < need) return SWG_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SWG_ERR_UNSUPPORTED;
@@ -1284,7 +1286,7 @@ swg_status linear_bwd(const void* dy, const void* x, const void* w, const void* 
   int64_t lddz = M > 1 ? lddy : N;
   cudaError_t e = cudaSuccess;
   if (want_db || act_on) {
-    void* to = act_on ? static_cast<char*>(workspace) + part : nullptr;
+    void* to = act_on ? static_cast<char*>(workspace) + sums + parts : nullptr;
     e = swg::launch_linear_dz(dy, z, to, want_db ? db : nullptr, M, N, lddz, static_cast<int>(act), f16,
                               bdtype == SWG_F32, acc, static_cast<float*>(workspace), s);
     if (act_on) {
@@ -1294,7 +1296,8 @@ swg_status linear_bwd(const void* dy, const void* x, const void* w, const void* 
   }
   if (e == cudaSuccess && want_dw) {
     const swg::LinearEpilogue epi{nullptr, acc ? dw : nullptr, dw, nullptr, N, swg::kLinearNoAct, f16, false};
-    e = swg::launch_linear_dw(x, dz, epi, M, K, N, M > 1 ? ldx : K, lddz, s);
+    e = swg::launch_linear_dw(x, dz, epi, M, K, N, M > 1 ? ldx : K, lddz,
+                              reinterpret_cast<float*>(static_cast<char*>(workspace) + sums), s);
   }
   if (e == cudaSuccess && want_dx) {
     const swg::LinearEpilogue epi{nullptr, nullptr, dx, nullptr, K, swg::kLinearNoAct, f16, false};

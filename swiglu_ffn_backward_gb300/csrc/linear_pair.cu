@@ -1,0 +1,462 @@
+// The linear layer's products with a large result, on CTA pairs: out[i][j] = sum_r A[i, r] B[j, r] with
+//   forward  y[m][n]:  i = m, j = n, r = k   A = x (r innermost), B = w (r outermost)
+//   dx[m][k]:          i = m, j = k, r = n   A = dz, B = w (r innermost in both)
+//   dw[k][n]:          i = k, j = n, r = m   A = x, B = dz (r outermost in both)
+// Bound by the tensor cores. One persistent pair (a cluster of two) for every two SMs walks over tiles of 256 x 256
+// outputs, ten warps a CTA:
+//   warp 0 lane 0   copies, for every 64 of r, this CTA's 128 rows of A and its 128 of the 256 columns of B (16 KB each)
+//                   into a ring of five stages with TMA, counted on the leader's barrier: each SM copies half of B
+//   warp 1          tensor memory (512 columns in each CTA: two accumulators of 256); lane 0 of the leader issues
+//                   tcgen05.mma.cta_group::2 (M = 256, N = 256, K = 16)
+//   warps 2-9       drain the finished accumulator (each CTA its own 128 rows; two warps a quarter of the lanes, each on
+//                   half of the columns) while the tensor cores fill the other one: bias, activation and residual in
+//                   fp32, blocks of 32 x 32 through two staging blocks a warp and TMA stores. A residual (or the old dw)
+//                   comes by TMA loads into two blocks a warp, one block ahead.
+// Tiles in flight share operands: eight tile rows at a time, the row index fastest (tile_of).
+// A reduction too long for too few tiles (dw) is cut into parts: fp32 partial results, added by a second kernel in a
+// fixed order.
+//
+// Every wait is bounded; a timeout sets the status word, stops issuing, drains the pair's copies, frees TMEM and returns.
+#include <algorithm>
+
+#include "linear.cuh"
+
+namespace swg {
+namespace {
+
+using namespace lin;
+
+constexpr int BM = 128;                // rows of a tile in each CTA
+constexpr int BN = 256;                // columns of a tile
+constexpr int BK = 64;                 // reduction block
+constexpr int STAGES = 5;
+constexpr int kHalf = 128 * BK * 2;    // 16 KB: an operand's share of a stage in a CTA
+constexpr int kBox = 64 * BK * 2;      // a box of 64 x 64 elements
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kBlock = 2048;           // a staged block of 32 x 32 elements
+constexpr uint32_t kTmemCols = 512;
+
+struct __align__(1024) PairSmem {
+  uint8_t a[STAGES][kHalf];
+  uint8_t b[STAGES][kHalf];
+  uint8_t out[kEpiWarps][2][kBlock];  // for TMA stores
+  uint8_t res[kEpiWarps][2][kBlock];  // residual blocks
+  uint64_t full[STAGES];              // leader: both CTAs' copies of the stage have landed
+  uint64_t empty[STAGES];             // the MMAs reading the stage are done (committed to both CTAs)
+  uint64_t tmem_full[2];              // the tile's MMAs into this accumulator are done (both CTAs)
+  uint64_t tmem_empty[2];             // leader: both CTAs' epilogue warps have read it out
+  uint64_t res_full[kEpiWarps][2];    // a residual block has landed
+  uint32_t tmem_base;
+  volatile uint32_t abort_flag;
+  volatile uint32_t issued, consumed;
+};
+
+struct PairArgs {
+  Epilogue epi;
+  uint32_t* status;
+  float* part;             // fp32 partial results [parts][I][J], or null
+  int I, J;
+  int tiles_i, tiles_j;    // tiles of 256 x 256
+  int tiles, parts;        // tiles of all parts
+  int nkb, per;            // blocks of 64 of r, of a part
+  long long wait_limit;
+  int64_t stall_at;        // test injection: the producers stop before this ring entry (-1: never)
+};
+
+struct Tile {
+  int i0, j0, kb, n, part;  // first row and column; first block of r and their number
+};
+// Tile t: parts one after the other; in a part bands of eight tile rows, in a band column after column, the row index
+// fastest, so that the tiles in flight (76 pairs) read a square of some eight rows and ten columns of operand tiles.
+__device__ __forceinline__ Tile tile_of(int t, const PairArgs& a) {
+  constexpr int kBand = 8;
+  const int per_part = a.tiles_i * a.tiles_j;
+  Tile w;
+  w.part = t / per_part;
+  t -= w.part * per_part;
+  const int band = t / (kBand * a.tiles_j), rows = min(kBand, a.tiles_i - band * kBand);
+  const int in = t - band * kBand * a.tiles_j;
+  w.i0 = (band * kBand + in % rows) * 2 * BM;
+  w.j0 = in / rows * BN;
+  w.kb = w.part * a.per;
+  w.n = min(a.per, a.nkb - w.kb);
+  return w;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+template <bool kAOuter, bool kBOuter>  // whether r is the outermost dimension of the operand in memory
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                       const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_z,
+                       const __grid_constant__ CUtensorMap tm_r, const PairArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  PairSmem& s = *reinterpret_cast<PairSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const bool leader = crank == 0;
+  const int pair_id = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+  const Epilogue& p = args.epi;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.tmem_full[i], 1);
+      mbar_init(&s.tmem_empty[i], 2 * kEpiWarps);
+      for (int w = 0; w < kEpiWarps; ++w) mbar_init(&s.res_full[w][i], 1);
+    }
+    s.abort_flag = s.issued = s.consumed = 0u;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&s.tmem_base, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync();  // both CTAs' barriers are initialised before any remote arrival, commit or copy
+  const uint32_t tmem = s.tmem_base;
+  auto timeout = [&]() {
+    if (args.status != nullptr) atomicOr(args.status, kStatusTimeout);
+    s.abort_flag = 1u;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t gj = 0;
+      bool stopped = false;
+      for (int t = pair_id; t < args.tiles && !s.abort_flag && !stopped; t += pairs) {
+        const Tile w = tile_of(t, args);
+        const int i0 = w.i0 + BM * static_cast<int>(crank), j0 = w.j0 + 128 * static_cast<int>(crank);
+        for (int i = 0; i < w.n && !s.abort_flag; ++i, ++gj) {
+          if (static_cast<int64_t>(gj) == args.stall_at) {
+            stopped = true;
+            break;
+          }
+          const int st = gj % STAGES;
+          if (gj >= STAGES && !mbar_wait(&s.empty[st], ((gj / STAGES) - 1) & 1, args.wait_limit)) {
+            timeout();
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(&s.full[st], 4 * kHalf);  // both CTAs' copies
+          const uint32_t full = cluster_addr(&s.full[st], 0);
+          const int r = (w.kb + i) * BK;
+          if (kAOuter) {
+            tma_load_2d_pair(s.a[st], &tm_a, full, i0, r);
+            tma_load_2d_pair(s.a[st] + kBox, &tm_a, full, i0 + 64, r);
+          } else {
+            tma_load_2d_pair(s.a[st], &tm_a, full, r, i0);
+          }
+          if (kBOuter) {
+            tma_load_2d_pair(s.b[st], &tm_b, full, j0, r);
+            tma_load_2d_pair(s.b[st] + kBox, &tm_b, full, j0 + 64, r);
+          } else {
+            tma_load_2d_pair(s.b[st], &tm_b, full, r, j0);
+          }
+          s.issued = gj + 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      const uint32_t idesc = idesc_f32(2 * BM, BN, kAOuter, kBOuter, p.f16);
+      auto commit2 = [](uint64_t* bar) {  // to the barrier at the same offset in both CTAs
+        umma_commit_pair(cluster_addr(bar, 0));
+        umma_commit_pair(cluster_addr(bar, 1));
+      };
+      uint32_t gj = 0, it = 0;
+      bool ok = true;
+      for (int t = pair_id; t < args.tiles && ok; t += pairs, ++it) {
+        const Tile w = tile_of(t, args);
+        const uint32_t buf = it & 1;
+        if (it >= 2) {
+          if (!mbar_wait(&s.tmem_empty[buf], ((it >> 1) - 1) & 1, args.wait_limit)) {
+            timeout();
+            break;
+          }
+          tc_fence_after();
+        }
+        const uint32_t d = tmem + buf * BN;
+        for (int i = 0; i < w.n; ++i, ++gj) {
+          const int st = gj % STAGES;
+          if (!mbar_wait(&s.full[st], (gj / STAGES) & 1, args.wait_limit)) {
+            timeout();
+            ok = false;
+            break;
+          }
+          s.consumed = gj + 1;
+          tc_fence_after();
+          const uint32_t pa = smem_u32(s.a[st]), pb = smem_u32(s.b[st]);
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k) {
+            const uint64_t da = kAOuter ? smem_desc(pa + 2048 * k, kBox, 1024) : smem_desc(pa + 32 * k, 16, 1024);
+            const uint64_t db = kBOuter ? smem_desc(pb + 2048 * k, kBox, 1024) : smem_desc(pb + 32 * k, 16, 1024);
+            umma_pair(d, da, db, idesc, (i > 0 || k > 0) ? 1u : 0u);
+          }
+          commit2(&s.empty[st]);
+        }
+        if (ok) commit2(&s.tmem_full[buf]);
+      }
+    }
+  } else {
+    const int q = warp & 3;            // TMEM lane quarter this warp may read
+    const int e = warp - 2, half = e >> 2;
+    const bool add = p.residual != nullptr && args.part == nullptr;
+    bool dead = false;
+    uint32_t it = 0, nb = 0, nr = 0;   // tiles, staged blocks, residual blocks read
+    // the four blocks of 32 columns of this warp in tile t: block c
+    auto fetch = [&](const Tile& w, int c, uint32_t slot) {
+      mbar_arrive_expect_tx(&s.res_full[e][slot], kBlock);
+      tma_load_2d(s.res[e][slot], &tm_r, &s.res_full[e][slot], w.j0 + half * 128 + c * 32,
+                  w.i0 + BM * static_cast<int>(crank) + q * 32);
+    };
+    uint32_t nf = 0;                   // residual blocks asked for
+    if (add && pair_id < args.tiles) {
+      if (lane == 0) fetch(tile_of(pair_id, args), 0, 0);
+      ++nf;
+    }
+    for (int t = pair_id; t < args.tiles; t += pairs, ++it) {
+      const Tile w = tile_of(t, args);
+      const uint32_t buf = it & 1;
+      const int row0 = w.i0 + BM * static_cast<int>(crank) + q * 32, col0 = w.j0 + half * 128;
+      bool ready = false;
+      if (!dead && !s.abort_flag) {
+        ready = mbar_wait(&s.tmem_full[buf], (it >> 1) & 1, args.wait_limit);
+        if (!ready) {
+          timeout();
+          dead = true;
+        }
+      }
+      tc_fence_after();
+      // tcgen05.ld is warp-collective: decide for the whole warp
+      if (__all_sync(0xffffffffu, ready && !s.abort_flag)) {
+        const uint32_t d = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + half * 128;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col = col0 + c * 32;
+          if (add) {  // the next block: of this tile, or the first of the next one
+            const bool more = c < 3 || t + pairs < args.tiles;
+            if (lane == 0 && more) fetch(c < 3 ? w : tile_of(t + pairs, args), (c + 1) & 3, nf & 1);
+            nf += more ? 1 : 0;
+            __syncwarp();
+          }
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(d + c * 32, v);
+          tmem_ld_wait();
+          if (args.part != nullptr) {
+            const int row = row0 + lane;
+            if (row < args.I) {
+              float* to = args.part + (static_cast<int64_t>(w.part) * args.I + row) * args.J + col;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (col + 4 * j < args.J)
+                  reinterpret_cast<uint4*>(to)[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+            continue;
+          }
+          const uint32_t swz = (lane >> 1) & 3;  // 64-byte swizzle of this lane's row: 16-byte chunk j ^ swz
+          uint4 res[4] = {};
+          if (add) {
+            if (!mbar_wait(&s.res_full[e][nr & 1], (nr >> 1) & 1, args.wait_limit)) {
+              timeout();
+              dead = true;
+            }
+            const uint32_t rb = smem_u32(s.res[e][nr & 1]) + lane * 64;
+            ++nr;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) res[j] = lds128(rb + ((j ^ swz) << 4));
+          }
+          uint4 z[4], y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float2 f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              f[i] = make_float2(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
+            if (col + 8 * j < args.J) add_bias(p, col + 8 * j, f);
+            z[j] = narrow8(f, p.f16);
+            if (p.act != kActNone) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) f[i] = activate(f[i], p.act);
+            }
+            if (add) {
+              float2 r[4];
+              widen8(res[j], p.f16, r);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) f[i] = __fadd2_rn(f[i], r[i]);
+            }
+            y[j] = narrow8(f, p.f16);
+          }
+          for (int o = p.z != nullptr ? 0 : 1; o < 2; ++o, ++nb) {
+            uint8_t* blk = s.out[e][nb & 1];
+            if (nb >= 2) {
+              if (lane == 0) bulk_wait_read<1>();  // the store that used this block has read it
+              __syncwarp();
+            }
+            const uint32_t sb = smem_u32(blk) + lane * 64;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sts128(sb + ((j ^ swz) << 4), o == 0 ? z[j] : y[j]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (row0 < args.I) tma_store_2d(o == 0 ? &tm_z : &tm_y, blk, col, row0);
+              bulk_commit();
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {  // this warp has read its part of the accumulator: tell the leader's MMA issuer
+        if (leader) mbar_arrive(&s.tmem_empty[buf]);
+        else mbar_arrive_remote(cluster_addr(&s.tmem_empty[buf], 0));
+      }
+    }
+    if (lane == 0) {
+      bulk_wait_all();  // every store has landed before the CTA exits
+      for (; nr < nf; ++nr)  // and every residual block that was asked for
+        if (!mbar_wait(&s.res_full[e][nr & 1], (nr >> 1) & 1, args.wait_limit)) break;
+    }
+  }
+
+  __syncthreads();
+  cluster_sync();  // both CTAs are done with their roles: no more remote arrivals or commits
+  if (leader && threadIdx.x == 0) {
+    const uint32_t peer_abort = ld_cluster_u32(&s.abort_flag, 1);
+    if (s.abort_flag || peer_abort) {
+      const uint32_t peer_issued = ld_cluster_u32(&s.issued, 1);
+      const uint32_t issued = s.issued > peer_issued ? s.issued : peer_issued;
+      for (uint32_t i = s.consumed; i < issued; ++i)
+        if (!mbar_wait(&s.full[i % STAGES], (i / STAGES) & 1, args.wait_limit)) break;
+    }
+  }
+  cluster_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// out = the sum of the parts in order (+ the old out), rounded once
+__global__ void __launch_bounds__(256) linear_parts_kernel(const float4* part, int parts, int64_t n4, uint2* out,
+                                                           bool accumulate, bool f16) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n4;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    float4 s = part[i];
+    for (int k = 1; k < parts; ++k) {
+      const float4 v = part[k * n4 + i];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    if (accumulate) {
+      const uint2 o = out[i];
+      const float2 a = widen2(o.x, f16), b = widen2(o.y, f16);
+      s.x += a.x;
+      s.y += a.y;
+      s.z += b.x;
+      s.w += b.y;
+    }
+    out[i] = make_uint2(narrow2(make_float2(s.x, s.y), f16), narrow2(make_float2(s.z, s.w), f16));
+  }
+}
+
+}  // namespace
+
+PairPlan linear_pair_plan(int64_t I, int64_t J, int64_t R, bool cut, int sms) {
+  PairPlan p;
+  p.tiles_i = (I + 2 * BM - 1) / (2 * BM);
+  p.tiles_j = (J + BN - 1) / BN;
+  p.nkb = (R + BK - 1) / BK;
+  p.parts = 1;
+  const int64_t tiles = p.tiles_i * p.tiles_j, pairs = std::max(1, sms / 2);
+  // cut only where whole tiles leave half of the pairs without work, and into parts of 16 blocks or more
+  if (cut && 2 * tiles <= pairs) p.parts = std::max<int64_t>(1, std::min(pairs / tiles, p.nkb / 16));
+  p.per = (p.nkb + p.parts - 1) / p.parts;
+  p.parts = (p.nkb + p.per - 1) / p.per;
+  p.part_bytes = p.parts > 1 ? static_cast<size_t>(p.parts) * I * J * sizeof(float) : 0;
+  return p;
+}
+
+template <bool kAOuter, bool kBOuter>
+cudaError_t launch_linear_pair(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t I, int64_t J, int64_t R,
+                        const LinearEpilogue& e, const PairPlan& plan, float* part, cudaStream_t stream) {
+  CUtensorMap ma, mb, my, mz, mr;
+  const uint64_t i = I, j = J, r = R, sa = lda * 2, sb = ldb * 2;
+  const bool ok =
+      (kAOuter ? encode_tmap_2d_bf16(&ma, A, i, r, sa, 64, BK) : encode_tmap_2d_bf16(&ma, A, r, i, sa, BK, BM)) &&
+      (kBOuter ? encode_tmap_2d_bf16(&mb, B, j, r, sb, 64, BK) : encode_tmap_2d_bf16(&mb, B, r, j, sb, BK, 128)) &&
+      encode_tmap_2d_bf16(&my, e.y, j, i, j * 2, 32, 32, 64) &&
+      encode_tmap_2d_bf16(&mz, e.z != nullptr ? e.z : e.y, j, i, j * 2, 32, 32, 64) &&
+      encode_tmap_2d_bf16(&mr, e.residual != nullptr ? e.residual : e.y, j, i, (e.residual != nullptr ? e.ldr : J) * 2, 32,
+                          32, 64);
+  if (!ok) return cudaErrorInvalidValue;
+  const Injection inj = take_injection(kInjectLinear);
+  PairArgs a{};
+  a.epi = Epilogue{e.bias,       static_cast<const uint16_t*>(e.residual), static_cast<uint16_t*>(e.y),
+                   static_cast<uint16_t*>(e.z), e.ldr, e.act, e.f16, e.bias_f32};
+  a.status = status_word_ptr();
+  a.part = plan.parts > 1 ? part : nullptr;
+  a.I = static_cast<int>(I);
+  a.J = static_cast<int>(J);
+  a.tiles_i = static_cast<int>(plan.tiles_i);
+  a.tiles_j = static_cast<int>(plan.tiles_j);
+  a.parts = static_cast<int>(plan.parts);
+  a.tiles = static_cast<int>(plan.tiles_i * plan.tiles_j * plan.parts);
+  a.nkb = static_cast<int>(plan.nkb);
+  a.per = static_cast<int>(plan.per);
+  a.wait_limit = inj.wait_limit;
+  a.stall_at = inj.stall_at;
+  constexpr size_t smem = sizeof(PairSmem) + 1024;
+  static_assert(smem <= 232448, "linear pair kernel shared memory");
+  const auto kernel = linear_pair_kernel<kAOuter, kBOuter>;
+  cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  const int pairs = std::max(1, std::min(device_sm_count() / 2, a.tiles));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, my, mz, mr, a);
+  if (err != cudaSuccess || plan.parts == 1) return err;
+  const int64_t n4 = I * J / 4;
+  linear_parts_kernel<<<static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, 4096)), 256, 0, stream>>>(
+      reinterpret_cast<const float4*>(part), a.parts, n4, static_cast<uint2*>(e.y), e.residual != nullptr, e.f16);
+  return cudaGetLastError();
+}
+
+template cudaError_t launch_linear_pair<false, true>(const void*, int64_t, const void*, int64_t, int64_t, int64_t, int64_t,
+                                              const LinearEpilogue&, const PairPlan&, float*, cudaStream_t);
+template cudaError_t launch_linear_pair<false, false>(const void*, int64_t, const void*, int64_t, int64_t, int64_t, int64_t,
+                                               const LinearEpilogue&, const PairPlan&, float*, cudaStream_t);
+template cudaError_t launch_linear_pair<true, true>(const void*, int64_t, const void*, int64_t, int64_t, int64_t, int64_t,
+                                             const LinearEpilogue&, const PairPlan&, float*, cudaStream_t);
+
+}  // namespace swg

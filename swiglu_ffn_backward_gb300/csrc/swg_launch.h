@@ -205,6 +205,20 @@ struct LinearEpilogue {  // z = product + bias, y = f(z) + residual; y, z dense
   bool f16, bias_f32;
 };
 constexpr int kLinearNoAct = 16;
+// the kernel for large results (linear_pair.cu): out [I, J], a reduction of length R, cut into parts where that helps
+// (fp32 partial results: part_bytes of workspace)
+struct PairPlan {
+  int64_t tiles_i, tiles_j, nkb, per, parts;
+  size_t part_bytes;
+};
+PairPlan linear_pair_plan(int64_t I, int64_t J, int64_t R, bool cut, int sms);
+// out[i][j] = sum_r A[i, r] B[j, r]; kAOuter, kBOuter: r is the operand's outermost dimension, its rows lda, ldb apart.
+// With plan.parts > 1 the epilogue is a residual that is y itself, at most.
+template <bool kAOuter, bool kBOuter>
+cudaError_t launch_linear_pair(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t I, int64_t J, int64_t R,
+                               const LinearEpilogue& epi, const PairPlan& plan, float* part, cudaStream_t stream);
+// workspace of launch_linear_dw
+size_t linear_dw_workspace_bytes(int64_t M, int64_t K, int64_t N);
 // y [M, N] of x [M, K] w [K, N]
 cudaError_t launch_linear_fwd(const void* x, const void* w, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
                               int64_t ldx, cudaStream_t stream);
@@ -213,7 +227,7 @@ cudaError_t launch_linear_dx(const void* dz, const void* w, const LinearEpilogue
                              int64_t lddz, cudaStream_t stream);
 // y [K, N] of x^T dz
 cudaError_t launch_linear_dw(const void* x, const void* dz, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
-                             int64_t ldx, int64_t lddz, cudaStream_t stream);
+                             int64_t ldx, int64_t lddz, float* part, cudaStream_t stream);
 // dz = dy f'(z), rounded (dz null: not stored), and db (or null) = its column sums before the rounding, plus the old
 // db with accumulate; part: linear_dz_workspace_bytes (with db). act kLinearNoAct: dz is dy, z is not read
 size_t linear_dz_workspace_bytes(int64_t M, int64_t N);

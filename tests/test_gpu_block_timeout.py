@@ -50,6 +50,34 @@ def test_split_backward(entry):
     swg.swg_check()
 
 
+@pytest.mark.parametrize("entry", [0, 1, 7, 20])
+@pytest.mark.parametrize("residual", [False, True])
+def test_pair_forward(entry, residual):
+    # 128 tiles of sixteen blocks on 76 pairs, a ring of five stages: entry 7 follows a wait for a released slot, entry 20
+    # lies in a pair's second tile
+    swg, t = _swg(), linear_inputs(8192, 1024, 1024, BF16)
+    r = t["residual"] if residual else None
+    g = {"y": guarded((8192, 1024), BF16)}
+    swg.swg_inject_stall(swg.SWG_INJECT_LINEAR, entry, LIMIT)
+    swg.linear_fwd(t["x"], t["w"], residual=r, out={"y": g["y"].t})
+    _expect_timeout(swg)
+    check_all(g)
+    check_linear_fwd(t, swg.linear_fwd(t["x"], t["w"], residual=r, out={"y": g["y"].t}), BF16, None, None, r)
+    swg.swg_check()
+    check_all(g)
+
+
+@pytest.mark.parametrize("entry", [0, 40])
+def test_pair_backward(entry):
+    # the armed launch is that of dw, cut into parts
+    swg, t = _swg(), linear_inputs(70000, 512, 1024, BF16)
+    swg.swg_inject_stall(swg.SWG_INJECT_LINEAR, entry, LIMIT)
+    swg.linear_bwd(t["dy"], t["x"], t["w"])
+    _expect_timeout(swg)
+    check_linear_bwd(t, swg.linear_bwd(t["dy"], t["x"], t["w"]), BF16, None)
+    swg.swg_check()
+
+
 # rows shared by three to eight blocks, whole and ragged; many rows in rings, by blocks on their own (the entry is a
 # ring's then) and by clusters
 @pytest.mark.parametrize("M,N,row", [(30, 12288, 0), (30, 12288, 7), (9, 32768, 3), (12, 20001, 0), (12, 20001, 5),

@@ -55,6 +55,39 @@ def test_backward(M, K, N, dtype):
     swg.swg_check()
 
 
+# results of many tiles, which go to the kernel on CTA pairs: whole tiles and ragged ones, several waves, bands
+LARGE = [(8192, 512, 1024), (8100, 264, 2056), (5001, 1032, 1528), (20000, 64, 264), (2600, 72, 8008), (300, 200, 40008)]
+
+
+@pytest.mark.parametrize("M,K,N", LARGE)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_large_forward(M, K, N, dtype):
+    swg, t = _swg(), linear_inputs(M, K, N, dtype, seed=33)
+    check_linear_fwd(t, swg.linear_fwd(t["x"], t["w"]), dtype, None)
+    out = swg.linear_fwd(t["x"], t["w"], t["b"].float(), act="gelu", residual=t["residual"], save_z=True)
+    check_linear_fwd(t, out, dtype, "gelu", t["b"].float(), t["residual"])
+    r = t["residual"].clone()
+    again = swg.linear_fwd(t["x"], t["w"], t["b"].float(), act="gelu", residual=r, out={"y": r})["y"]
+    assert torch.equal(again, out["y"])
+    swg.swg_check()
+
+
+@pytest.mark.parametrize("M,K,N", [(8192, 512, 1024), (5001, 1032, 1528), (2600, 8008, 72), (9000, 2056, 264), (70000, 512, 520)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_large_backward(M, K, N, dtype):
+    swg, t = _swg(), linear_inputs(M, K, N, dtype, seed=35)
+    check_linear_bwd(t, swg.linear_bwd(t["dy"], t["x"], t["w"], z=t["z"], act="silu"), dtype, "silu")
+    g = {"dx": guarded((M, K), dtype), "dw": guarded((K, N), dtype), "db": guarded((N,), dtype),
+         "ws": workspace(swg.linear_bwd_workspace_size(M, K, N))}
+    g["dw"].t.fill_(0.5)
+    g["db"].t.fill_(-0.25)
+    got = swg.linear_bwd(t["dy"], t["x"], t["w"], accumulate=True, workspace=g["ws"].t,
+                         out={k: g[k].t for k in ("dx", "dw", "db")})
+    check_all(g)
+    check_linear_bwd(t, got, dtype, None, old={"dw": 0.5, "db": -0.25})
+    swg.swg_check()
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("M,K,N", [(3, 136, 72), (515, 200, 392), (2500, 64, 72)])
 def test_backward_activations(M, K, N, act):
