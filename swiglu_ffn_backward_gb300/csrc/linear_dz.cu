@@ -27,10 +27,11 @@ __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
   return v;
 }
 
-template <bool kAct>
+template <int kActOf, bool kF16>
 __global__ void __launch_bounds__(kThreads)
     linear_dz_kernel(const uint16_t* dy, const uint16_t* z, uint16_t* dz, float* part, int64_t M, int64_t N,
-                     int64_t lddy, int64_t rows_per_block, int act, bool f16) {
+                     int64_t lddy, int64_t rows_per_block) {
+  constexpr bool kAct = kActOf != kActNone;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = (warp & 3) * 64 + (lane & 7) * 8;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * kCols + c;
@@ -39,12 +40,12 @@ __global__ void __launch_bounds__(kThreads)
   if (col < N) {
     auto step = [&](const uint4& g, const uint4& v, int64_t row) {
       float2 d[4], t[4];
-      widen8(g, f16, d);
+      widen8<kF16>(g, d);
       if (kAct) {
-        widen8(v, f16, t);
+        widen8<kF16>(v, t);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] = __fmul2_rn(d[e], activate_grad(t[e], act));
-        *reinterpret_cast<uint4*>(dz + row * N + col) = narrow8(d, f16);
+        for (int e = 0; e < 4; ++e) d[e] = __fmul2_rn(d[e], activate_grad<kActOf>(t[e]));
+        *reinterpret_cast<uint4*>(dz + row * N + col) = narrow8<kF16>(d);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[e] = __fadd2_rn(sum[e], d[e]);
@@ -113,6 +114,17 @@ int64_t rows_per_block(int64_t M, int64_t N) {
   return std::min<int64_t>(kMaxRows, std::max<int64_t>(rows, 4 * kRowStep));
 }
 
+template <bool kF16>
+cudaError_t launch_dz(const dim3& grid, const uint16_t* dy, const uint16_t* z, uint16_t* dz, float* part, int64_t M,
+                      int64_t N, int64_t lddy, int64_t per, int act, cudaStream_t stream) {
+  const auto kernel = act == kLinearNoAct ? linear_dz_kernel<kActNone, kF16>
+                      : act == 0          ? linear_dz_kernel<0, kF16>
+                      : act == 1          ? linear_dz_kernel<1, kF16>
+                                          : linear_dz_kernel<2, kF16>;
+  kernel<<<grid, kThreads, 0, stream>>>(dy, z, dz, part, M, N, lddy, per);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 size_t linear_dz_workspace_bytes(int64_t M, int64_t N) {
@@ -125,18 +137,16 @@ cudaError_t launch_linear_dz(const void* dy, const void* z, void* dz, void* db, 
   const int64_t per = rows_per_block(M, N);
   // blocks beyond the grid's second dimension go in further launches
   const int64_t chunks = (M + per - 1) / per;
+  const bool store = act != kLinearNoAct;
   for (int64_t c = 0; c < chunks; c += 65535) {
     const int64_t n = std::min<int64_t>(65535, chunks - c), r = c * per, rows = std::min(M - r, n * per);
     const dim3 grid(static_cast<unsigned>((N + kCols - 1) / kCols), static_cast<unsigned>(n));
     const uint16_t* g = static_cast<const uint16_t*>(dy) + r * lddy;
+    const uint16_t* v = store ? static_cast<const uint16_t*>(z) + r * N : nullptr;
+    uint16_t* to = store ? static_cast<uint16_t*>(dz) + r * N : nullptr;
     float* p = db != nullptr ? part + c * N : nullptr;
-    if (act != kLinearNoAct)
-      linear_dz_kernel<true><<<grid, kThreads, 0, stream>>>(g, static_cast<const uint16_t*>(z) + r * N,
-                                                            static_cast<uint16_t*>(dz) + r * N, p, rows, N, lddy, per,
-                                                            act, f16);
-    else
-      linear_dz_kernel<false><<<grid, kThreads, 0, stream>>>(g, nullptr, nullptr, p, rows, N, lddy, per, act, f16);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = f16 ? launch_dz<true>(grid, g, v, to, p, rows, N, lddy, per, act, stream)
+                              : launch_dz<false>(grid, g, v, to, p, rows, N, lddy, per, act, stream);
     if (e != cudaSuccess) return e;
   }
   if (db == nullptr) return cudaSuccess;

@@ -10,8 +10,9 @@
 //                   tcgen05.mma.cta_group::2 (M = 256, N = 256, K = 16)
 //   warps 2-9       drain the finished accumulator (each CTA its own 128 rows; two warps a quarter of the lanes, each on
 //                   half of the columns) while the tensor cores fill the other one: bias, activation and residual in
-//                   fp32, blocks of 32 x 32 through two staging blocks a warp and TMA stores. A residual (or the old dw)
-//                   comes by TMA loads into two blocks a warp, one block ahead.
+//                   fp32, 64 columns at a time, through staging blocks of 32 rows x 128 bytes and TMA stores. The bias is
+//                   loaded under the products and passed around by shuffles (loads behind the products took half of
+//                   the epilogue); a residual (or the old dw) comes by TMA loads two blocks ahead.
 // Tiles in flight share operands: eight tile rows at a time, the row index fastest (tile_of).
 // A reduction too long for too few tiles (dw) is cut into parts: fp32 partial results, added by a second kernel in a
 // fixed order.
@@ -34,14 +35,14 @@ constexpr int kHalf = 128 * BK * 2;    // 16 KB: an operand's share of a stage i
 constexpr int kBox = 64 * BK * 2;      // a box of 64 x 64 elements
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
-constexpr int kBlock = 2048;           // a staged block of 32 x 32 elements
+constexpr int kOut = 4096;             // a staged block of 32 rows x 64 columns
+constexpr int kRes = 2048;             // a residual block of 32 x 32
 constexpr uint32_t kTmemCols = 512;
 
 struct __align__(1024) PairSmem {
   uint8_t a[STAGES][kHalf];
   uint8_t b[STAGES][kHalf];
-  uint8_t out[kEpiWarps][2][kBlock];  // for TMA stores
-  uint8_t res[kEpiWarps][2][kBlock];  // residual blocks
+  uint8_t stage[kEpiWarps][8192];     // two blocks for TMA stores; or, with a residual, one and two residual blocks
   uint64_t full[STAGES];              // leader: both CTAs' copies of the stage have landed
   uint64_t empty[STAGES];             // the MMAs reading the stage are done (committed to both CTAs)
   uint64_t tmem_full[2];              // the tile's MMAs into this accumulator are done (both CTAs)
@@ -95,7 +96,18 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
                : "memory");
 }
 
-template <bool kAOuter, bool kBOuter>  // whether r is the outermost dimension of the operand in memory
+// waits for the loads from tensor memory; what they read is not touched before
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// kAOuter, kBOuter: whether r is the outermost dimension of the operand in memory
+template <bool kAOuter, bool kBOuter, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                        const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_z,
@@ -175,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
-      const uint32_t idesc = idesc_f32(2 * BM, BN, kAOuter, kBOuter, p.f16);
+      const uint32_t idesc = idesc_f32(2 * BM, BN, kAOuter, kBOuter, kF16);
       auto commit2 = [](uint64_t* bar) {  // to the barrier at the same offset in both CTAs
         umma_commit_pair(cluster_addr(bar, 0));
         umma_commit_pair(cluster_addr(bar, 1));
@@ -219,22 +231,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int e = warp - 2, half = e >> 2;
     const bool add = p.residual != nullptr && args.part == nullptr;
     bool dead = false;
-    uint32_t it = 0, nb = 0, nr = 0;   // tiles, staged blocks, residual blocks read
-    // the four blocks of 32 columns of this warp in tile t: block c
-    auto fetch = [&](const Tile& w, int c, uint32_t slot) {
-      mbar_arrive_expect_tx(&s.res_full[e][slot], kBlock);
-      tma_load_2d(s.res[e][slot], &tm_r, &s.res_full[e][slot], w.j0 + half * 128 + c * 32,
-                  w.i0 + BM * static_cast<int>(crank) + q * 32);
+    uint32_t it = 0, nb = 0;           // tiles, staged blocks
+    // the residual's blocks of 32 columns, four a tile: two of them are under way
+    uint32_t nf = 0, nr = 0;           // asked for, read
+    int ft = pair_id;                  // the tile of the next one
+    auto fetch = [&]() {
+      if (ft >= args.tiles) return;
+      if (lane == 0) {
+        const Tile w = tile_of(ft, args);
+        uint64_t* bar = &s.res_full[e][nf & 1];
+        mbar_arrive_expect_tx(bar, kRes);
+        tma_load_2d(s.stage[e] + kOut + (nf & 1) * kRes, &tm_r, bar, w.j0 + half * 128 + (nf & 3) * 32,
+                    w.i0 + BM * static_cast<int>(crank) + q * 32);
+      }
+      if ((++nf & 3) == 0) ft += pairs;
     };
-    uint32_t nf = 0;                   // residual blocks asked for
-    if (add && pair_id < args.tiles) {
-      if (lane == 0) fetch(tile_of(pair_id, args), 0, 0);
-      ++nf;
+    if (add) {
+      fetch();
+      fetch();
     }
+    // the next block for a store, which the store that used it has read
+    auto staged = [&]() -> uint8_t* {
+      if (lane == 0) {
+        if (add) bulk_wait_read<0>();
+        else bulk_wait_read<1>();
+      }
+      __syncwarp();
+      return s.stage[e] + (add ? 0 : (nb & 1) * kOut);
+    };
+    auto store = [&](const CUtensorMap* tm, const uint8_t* blk, int col, int row0) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (row0 < args.I) tma_store_2d(tm, blk, col, row0);
+        bulk_commit();
+      }
+      ++nb;
+    };
     for (int t = pair_id; t < args.tiles; t += pairs, ++it) {
       const Tile w = tile_of(t, args);
       const uint32_t buf = it & 1;
       const int row0 = w.i0 + BM * static_cast<int>(crank) + q * 32, col0 = w.j0 + half * 128;
+      // the bias of this lane's column in each block of 32 (loaded once a tile, under the products)
+      float bias[4] = {};
+      if (p.bias != nullptr && args.part == nullptr) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int j = col0 + c * 32 + lane;
+          if (j < args.J)
+            bias[c] = p.bias_f32 ? static_cast<const float*>(p.bias)[j]
+                                 : widen2<kF16>(static_cast<const uint16_t*>(p.bias)[j]).x;
+        }
+      }
       bool ready = false;
       if (!dead && !s.abort_flag) {
         ready = mbar_wait(&s.tmem_full[buf], (it >> 1) & 1, args.wait_limit);
@@ -247,78 +295,86 @@ __global__ void __launch_bounds__(kThreads, 1)
       // tcgen05.ld is warp-collective: decide for the whole warp
       if (__all_sync(0xffffffffu, ready && !s.abort_flag)) {
         const uint32_t d = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + half * 128;
+        const uint32_t swz = lane & 7;           // 128-byte swizzle of this lane's row: 16-byte chunk j ^ swz
+        const uint32_t swr = (lane >> 1) & 3;    // 64-byte swizzle
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 4; c += 2) {         // 64 columns at a time
+          uint32_t v[2][32];
+          tmem_ld_32x32b_x32(d + c * 32, v[0]);
+          tmem_ld_32x32b_x32(d + c * 32 + 32, v[1]);
+          tmem_loaded(v[0]);
+          tmem_loaded(v[1]);
           const int col = col0 + c * 32;
-          if (add) {  // the next block: of this tile, or the first of the next one
-            const bool more = c < 3 || t + pairs < args.tiles;
-            if (lane == 0 && more) fetch(c < 3 ? w : tile_of(t + pairs, args), (c + 1) & 3, nf & 1);
-            nf += more ? 1 : 0;
-            __syncwarp();
-          }
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(d + c * 32, v);
-          tmem_ld_wait();
           if (args.part != nullptr) {
             const int row = row0 + lane;
             if (row < args.I) {
               float* to = args.part + (static_cast<int64_t>(w.part) * args.I + row) * args.J + col;
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (col + 4 * j < args.J)
-                  reinterpret_cast<uint4*>(to)[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              for (int j = 0; j < 16; ++j) {
+                const uint32_t* x = v[j >> 3] + 4 * (j & 7);
+                if (col + 4 * j < args.J) reinterpret_cast<uint4*>(to)[j] = make_uint4(x[0], x[1], x[2], x[3]);
+              }
             }
+            __syncwarp();
             continue;
           }
-          const uint32_t swz = (lane >> 1) & 3;  // 64-byte swizzle of this lane's row: 16-byte chunk j ^ swz
-          uint4 res[4] = {};
+          float2 f[2][16];
+          const float b0 = c == 0 ? bias[0] : bias[2], b1 = c == 0 ? bias[1] : bias[3];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            f[0][i] = make_float2(__uint_as_float(v[0][2 * i]), __uint_as_float(v[0][2 * i + 1]));
+            f[1][i] = make_float2(__uint_as_float(v[1][2 * i]), __uint_as_float(v[1][2 * i + 1]));
+            if (p.bias != nullptr) {
+              f[0][i] = __fadd2_rn(f[0][i], make_float2(__shfl_sync(0xffffffffu, b0, 2 * i),
+                                                        __shfl_sync(0xffffffffu, b0, 2 * i + 1)));
+              f[1][i] = __fadd2_rn(f[1][i], make_float2(__shfl_sync(0xffffffffu, b1, 2 * i),
+                                                        __shfl_sync(0xffffffffu, b1, 2 * i + 1)));
+            }
+          }
+          if (p.z != nullptr) {
+            uint8_t* blk = staged();
+            const uint32_t to = smem_u32(blk) + lane * 128;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float2* x = f[j >> 2] + 4 * (j & 3);
+              sts128(to + ((j ^ swz) << 4), make_uint4(narrow2<kF16>(x[0]), narrow2<kF16>(x[1]), narrow2<kF16>(x[2]),
+                                                       narrow2<kF16>(x[3])));
+            }
+            store(&tm_z, blk, col, row0);
+          }
+          with_act(p.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i >> 4][i & 15] = activate<decltype(act)::value>(f[i >> 4][i & 15]);
+          });
           if (add) {
-            if (!mbar_wait(&s.res_full[e][nr & 1], (nr >> 1) & 1, args.wait_limit)) {
-              timeout();
-              dead = true;
-            }
-            const uint32_t rb = smem_u32(s.res[e][nr & 1]) + lane * 64;
-            ++nr;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) res[j] = lds128(rb + ((j ^ swz) << 4));
-          }
-          uint4 z[4], y[4];
+            for (int k = 0; k < 2; ++k) {
+              if (!mbar_wait(&s.res_full[e][nr & 1], (nr >> 1) & 1, args.wait_limit)) {
+                timeout();
+                dead = true;
+              }
+              const uint32_t rb = smem_u32(s.stage[e] + kOut + (nr & 1) * kRes) + lane * 64;
+              ++nr;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float2 f[4];
+              for (int j = 0; j < 4; ++j) {
+                float2 r[4];
+                widen8<kF16>(lds128(rb + ((j ^ swr) << 4)), r);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              f[i] = make_float2(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
-            if (col + 8 * j < args.J) add_bias(p, col + 8 * j, f);
-            z[j] = narrow8(f, p.f16);
-            if (p.act != kActNone) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) f[i] = activate(f[i], p.act);
-            }
-            if (add) {
-              float2 r[4];
-              widen8(res[j], p.f16, r);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) f[i] = __fadd2_rn(f[i], r[i]);
-            }
-            y[j] = narrow8(f, p.f16);
-          }
-          for (int o = p.z != nullptr ? 0 : 1; o < 2; ++o, ++nb) {
-            uint8_t* blk = s.out[e][nb & 1];
-            if (nb >= 2) {
-              if (lane == 0) bulk_wait_read<1>();  // the store that used this block has read it
-              __syncwarp();
-            }
-            const uint32_t sb = smem_u32(blk) + lane * 64;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sts128(sb + ((j ^ swz) << 4), o == 0 ? z[j] : y[j]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (row0 < args.I) tma_store_2d(o == 0 ? &tm_z : &tm_y, blk, col, row0);
-              bulk_commit();
+                for (int i = 0; i < 4; ++i) f[k][4 * j + i] = __fadd2_rn(f[k][4 * j + i], r[i]);
+              }
+              __syncwarp();  // the block has been read by every lane
+              fetch();
             }
           }
+          uint8_t* blk = staged();
+          const uint32_t to = smem_u32(blk) + lane * 128;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2* x = f[j >> 2] + 4 * (j & 3);
+            sts128(to + ((j ^ swz) << 4), make_uint4(narrow2<kF16>(x[0]), narrow2<kF16>(x[1]), narrow2<kF16>(x[2]),
+                                                     narrow2<kF16>(x[3])));
+          }
+          store(&tm_y, blk, col, row0);
         }
       }
       tc_fence_before();
@@ -330,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) {
       bulk_wait_all();  // every store has landed before the CTA exits
-      for (; nr < nf; ++nr)  // and every residual block that was asked for
+      for (; add && nr < nf; ++nr)  // and every residual block that was asked for
         if (!mbar_wait(&s.res_full[e][nr & 1], (nr >> 1) & 1, args.wait_limit)) break;
     }
   }
@@ -355,8 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // out = the sum of the parts in order (+ the old out), rounded once
+template <bool kF16>
 __global__ void __launch_bounds__(256) linear_parts_kernel(const float4* part, int parts, int64_t n4, uint2* out,
-                                                           bool accumulate, bool f16) {
+                                                           bool accumulate) {
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n4;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     float4 s = part[i];
@@ -369,13 +426,13 @@ __global__ void __launch_bounds__(256) linear_parts_kernel(const float4* part, i
     }
     if (accumulate) {
       const uint2 o = out[i];
-      const float2 a = widen2(o.x, f16), b = widen2(o.y, f16);
+      const float2 a = widen2<kF16>(o.x), b = widen2<kF16>(o.y);
       s.x += a.x;
       s.y += a.y;
       s.z += b.x;
       s.w += b.y;
     }
-    out[i] = make_uint2(narrow2(make_float2(s.x, s.y), f16), narrow2(make_float2(s.z, s.w), f16));
+    out[i] = make_uint2(narrow2<kF16>(make_float2(s.x, s.y)), narrow2<kF16>(make_float2(s.z, s.w)));
   }
 }
 
@@ -404,15 +461,14 @@ cudaError_t launch_linear_pair(const void* A, int64_t lda, const void* B, int64_
   const bool ok =
       (kAOuter ? encode_tmap_2d_bf16(&ma, A, i, r, sa, 64, BK) : encode_tmap_2d_bf16(&ma, A, r, i, sa, BK, BM)) &&
       (kBOuter ? encode_tmap_2d_bf16(&mb, B, j, r, sb, 64, BK) : encode_tmap_2d_bf16(&mb, B, r, j, sb, BK, 128)) &&
-      encode_tmap_2d_bf16(&my, e.y, j, i, j * 2, 32, 32, 64) &&
-      encode_tmap_2d_bf16(&mz, e.z != nullptr ? e.z : e.y, j, i, j * 2, 32, 32, 64) &&
+      encode_tmap_2d_bf16(&my, e.y, j, i, j * 2, 64, 32) &&
+      encode_tmap_2d_bf16(&mz, e.z != nullptr ? e.z : e.y, j, i, j * 2, 64, 32) &&
       encode_tmap_2d_bf16(&mr, e.residual != nullptr ? e.residual : e.y, j, i, (e.residual != nullptr ? e.ldr : J) * 2, 32,
                           32, 64);
   if (!ok) return cudaErrorInvalidValue;
   const Injection inj = take_injection(kInjectLinear);
   PairArgs a{};
-  a.epi = Epilogue{e.bias,       static_cast<const uint16_t*>(e.residual), static_cast<uint16_t*>(e.y),
-                   static_cast<uint16_t*>(e.z), e.ldr, e.act, e.f16, e.bias_f32};
+  a.epi = epilogue_of(e);
   a.status = status_word_ptr();
   a.part = plan.parts > 1 ? part : nullptr;
   a.I = static_cast<int>(I);
@@ -427,7 +483,7 @@ cudaError_t launch_linear_pair(const void* A, int64_t lda, const void* B, int64_
   a.stall_at = inj.stall_at;
   constexpr size_t smem = sizeof(PairSmem) + 1024;
   static_assert(smem <= 232448, "linear pair kernel shared memory");
-  const auto kernel = linear_pair_kernel<kAOuter, kBOuter>;
+  const auto kernel = e.f16 ? linear_pair_kernel<kAOuter, kBOuter, true> : linear_pair_kernel<kAOuter, kBOuter, false>;
   cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
@@ -447,8 +503,9 @@ cudaError_t launch_linear_pair(const void* A, int64_t lda, const void* B, int64_
   err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, my, mz, mr, a);
   if (err != cudaSuccess || plan.parts == 1) return err;
   const int64_t n4 = I * J / 4;
-  linear_parts_kernel<<<static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, 4096)), 256, 0, stream>>>(
-      reinterpret_cast<const float4*>(part), a.parts, n4, static_cast<uint2*>(e.y), e.residual != nullptr, e.f16);
+  const auto add = e.f16 ? linear_parts_kernel<true> : linear_parts_kernel<false>;
+  add<<<static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, 4096)), 256, 0, stream>>>(
+      reinterpret_cast<const float4*>(part), a.parts, n4, static_cast<uint2*>(e.y), e.residual != nullptr);
   return cudaGetLastError();
 }
 

@@ -61,7 +61,8 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-template <bool kAOuter, bool kBOuter>  // whether r is the outermost dimension of the operand in memory
+// kAOuter, kBOuter: whether r is the outermost dimension of the operand in memory
+template <bool kAOuter, bool kBOuter, bool kF16>
 __global__ void __launch_bounds__(kThreads)
     linear_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                         const SplitArgs a) {
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_f32(kLanes, a.NT, kAOuter, kBOuter, a.epi.f16);
+      const uint32_t idesc = idesc_f32(kLanes, a.NT, kAOuter, kBOuter, kF16);
       for (int i = 0; i < n; ++i) {
         const int st = i % a.stages;
         if (!mbar_wait(&s.full[st], (i / a.stages) & 1, a.wait_limit)) {
@@ -193,35 +194,37 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int i = 0; i < kMaxSplit; ++i) peers[i] = i < a.S && a.S > 1 ? cluster_addr(part, i) : smem_u32(part);
   const Epilogue& p = a.epi;
-  for (int i = rank * kThreads + static_cast<int>(threadIdx.x); i < cols * (kLanes / 8); i += a.S * kThreads) {
-    const int c = i / (kLanes / 8), l = (i % (kLanes / 8)) * 8;
-    if (l0 + l >= a.L) continue;
-    const int64_t row = c0 + c, at = row * a.L + l0 + l;
-    uint4 res = make_uint4(0u, 0u, 0u, 0u);
-    if (p.residual != nullptr) res = *reinterpret_cast<const uint4*>(p.residual + row * p.ldr + l0 + l);
-    const uint32_t off = static_cast<uint32_t>(c * kLanes + l) * sizeof(float);
-    float2 v[4] = {};
+  with_act(p.act, [&](auto act) {
+    for (int i = rank * kThreads + static_cast<int>(threadIdx.x); i < cols * (kLanes / 8); i += a.S * kThreads) {
+      const int c = i / (kLanes / 8), l = (i % (kLanes / 8)) * 8;
+      if (l0 + l >= a.L) continue;
+      const int64_t row = c0 + c, at = row * a.L + l0 + l;
+      uint4 res = make_uint4(0u, 0u, 0u, 0u);
+      if (p.residual != nullptr) res = *reinterpret_cast<const uint4*>(p.residual + row * p.ldr + l0 + l);
+      const uint32_t off = static_cast<uint32_t>(c * kLanes + l) * sizeof(float);
+      float2 v[4] = {};
 #pragma unroll
-    for (int k = 0; k < kMaxSplit; ++k) {
-      if (k >= a.S) break;
-      const float4 x = ld_cluster_f4(peers[k] + off), y = ld_cluster_f4(peers[k] + off + 16);
-      v[0] = __fadd2_rn(v[0], make_float2(x.x, x.y));
-      v[1] = __fadd2_rn(v[1], make_float2(x.z, x.w));
-      v[2] = __fadd2_rn(v[2], make_float2(y.x, y.y));
-      v[3] = __fadd2_rn(v[3], make_float2(y.z, y.w));
+      for (int k = 0; k < kMaxSplit; ++k) {
+        if (k >= a.S) break;
+        const float4 x = ld_cluster_f4(peers[k] + off), y = ld_cluster_f4(peers[k] + off + 16);
+        v[0] = __fadd2_rn(v[0], make_float2(x.x, x.y));
+        v[1] = __fadd2_rn(v[1], make_float2(x.z, x.w));
+        v[2] = __fadd2_rn(v[2], make_float2(y.x, y.y));
+        v[3] = __fadd2_rn(v[3], make_float2(y.z, y.w));
+      }
+      add_bias<kF16>(p, l0 + l, a.L, v);
+      if (p.z != nullptr) *reinterpret_cast<uint4*>(p.z + at) = narrow8<kF16>(v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = activate<decltype(act)::value>(v[e]);
+      if (p.residual != nullptr) {
+        float2 r[4];
+        widen8<kF16>(res, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(v[e], r[e]);
+      }
+      *reinterpret_cast<uint4*>(p.y + at) = narrow8<kF16>(v);
     }
-    add_bias(p, l0 + l, v);
-    if (p.z != nullptr) *reinterpret_cast<uint4*>(p.z + at) = narrow8(v, p.f16);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = activate(v[e], p.act);
-    if (p.residual != nullptr) {
-      float2 r[4];
-      widen8(res, p.f16, r);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(v[e], r[e]);
-    }
-    *reinterpret_cast<uint4*>(p.y + at) = narrow8(v, p.f16);
-  }
+  });
   if (a.S > 1) cluster_sync();  // no block leaves while another reads its sums
   else __syncthreads();
   if (warp == 1) {
@@ -251,8 +254,8 @@ SplitPlan split_plan(int64_t L, int64_t C, int64_t R, bool b_outer, int sms) {
   return p;
 }
 
-template <bool kAOuter, bool kBOuter>
-cudaError_t launch_split(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t L, int64_t C, int64_t R,
+template <bool kAOuter, bool kBOuter, bool kF16>
+cudaError_t launch_split_of(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t L, int64_t C, int64_t R,
                          const Epilogue& epi, cudaStream_t stream) {
   const SplitPlan p = split_plan(L, C, R, kBOuter, device_sm_count());
   CUtensorMap ma, mb;
@@ -264,7 +267,7 @@ cudaError_t launch_split(const void* A, int64_t lda, const void* B, int64_t ldb,
   const SplitArgs a{epi,       status_word_ptr(), static_cast<int>(L), static_cast<int>(C), p.NT,          p.tiles_l,
                     p.tiles_c, p.nkb,             p.S,                 p.stages,            inj.wait_limit, inj.stall_at};
   const size_t smem = static_cast<size_t>(p.stages) * (kABytes + p.NT * kRed * 2) + 1024;
-  const auto kernel = linear_split_kernel<kAOuter, kBOuter>;
+  const auto kernel = linear_split_kernel<kAOuter, kBOuter, kF16>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -283,9 +286,12 @@ cudaError_t launch_split(const void* A, int64_t lda, const void* B, int64_t ldb,
   return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
 }
 
-Epilogue epilogue_of(const LinearEpilogue& e) {
-  return Epilogue{e.bias, static_cast<const uint16_t*>(e.residual), static_cast<uint16_t*>(e.y),
-                  static_cast<uint16_t*>(e.z), e.ldr, e.act, e.f16, e.bias_f32};
+template <bool kAOuter, bool kBOuter>
+cudaError_t launch_split(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t L, int64_t C, int64_t R,
+                         const LinearEpilogue& e, cudaStream_t stream) {
+  const Epilogue epi = epilogue_of(e);
+  return e.f16 ? launch_split_of<kAOuter, kBOuter, true>(A, lda, B, ldb, L, C, R, epi, stream)
+               : launch_split_of<kAOuter, kBOuter, false>(A, lda, B, ldb, L, C, R, epi, stream);
 }
 
 // Whether the kernel on CTA pairs is the faster one. In units of a 64-block of a 128 x 256 tile on one SM (0.33 us at the
@@ -310,7 +316,7 @@ cudaError_t launch_linear_fwd(const void* x, const void* w, const LinearEpilogue
   const PairPlan p = linear_pair_plan(M, N, K, false, sms);
   if (use_pairs(p, N, M, K, false, sms))
     return launch_linear_pair<false, true>(x, ldx, w, N, M, N, K, epi, p, nullptr, stream);
-  return launch_split<true, false>(w, N, x, ldx, N, M, K, epilogue_of(epi), stream);
+  return launch_split<true, false>(w, N, x, ldx, N, M, K, epi, stream);
 }
 
 cudaError_t launch_linear_dx(const void* dz, const void* w, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
@@ -319,7 +325,7 @@ cudaError_t launch_linear_dx(const void* dz, const void* w, const LinearEpilogue
   const PairPlan p = linear_pair_plan(M, K, N, false, sms);
   if (use_pairs(p, K, M, N, false, sms))
     return launch_linear_pair<false, false>(dz, lddz, w, N, M, K, N, epi, p, nullptr, stream);
-  return launch_split<false, false>(w, N, dz, lddz, K, M, N, epilogue_of(epi), stream);
+  return launch_split<false, false>(w, N, dz, lddz, K, M, N, epi, stream);
 }
 
 size_t linear_dw_workspace_bytes(int64_t M, int64_t K, int64_t N) {
@@ -334,7 +340,7 @@ cudaError_t launch_linear_dw(const void* x, const void* dz, const LinearEpilogue
   const PairPlan p = linear_pair_plan(K, N, M, true, sms);
   if (use_pairs(p, N, K, M, true, sms))
     return launch_linear_pair<true, true>(x, ldx, dz, lddz, K, N, M, epi, p, part, stream);
-  return launch_split<true, true>(dz, lddz, x, ldx, N, K, M, epilogue_of(epi), stream);
+  return launch_split<true, true>(dz, lddz, x, ldx, N, K, M, epi, stream);
 }
 
 }  // namespace swg
