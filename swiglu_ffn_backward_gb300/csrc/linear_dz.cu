@@ -2,9 +2,9 @@
 //   dz = dy f'(z), rounded to the element type;  db = sum over rows of dz (in fp32, before the rounding)
 // HBM-bound: reads dy (and z), writes dz (without an activation dz is dy itself, and only the sums are taken).
 // A block takes 256 columns of a run of rows: warp w the columns (w & 3) 64 .. + 63 and the row group w >> 2, a lane
-// one 16-byte vector of them, so that eight rows are under way at once, with eight such steps in flight. No sum takes
+// one 16-byte vector of them, so that eight rows are under way at once, with four or eight such steps in flight. No sum takes
 // more than 128 rows in one accumulator (like terms are rounded the same way, and a longer chain drifts); a second
-// kernel adds the blocks' partial rows in fp64 in a fixed order.
+// kernel adds the blocks' partial rows in a fixed order.
 #include <algorithm>
 
 #include "linear.cuh"
@@ -17,6 +17,7 @@ using namespace lin;
 constexpr int kThreads = 256;
 constexpr int kCols = 256;    // columns of a block
 constexpr int kRowStep = 8;   // rows of one step
+constexpr int kBlocks = 3;    // blocks an SM: 80 registers a thread (64 or 128 spill or leave too few loads under way)
 constexpr int kMaxRows = 128 * kRowStep;  // rows of a block, at most
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
@@ -28,7 +29,7 @@ __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
 }
 
 template <int kActOf, bool kF16>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocks)
     linear_dz_kernel(const uint16_t* dy, const uint16_t* z, uint16_t* dz, float* part, int64_t M, int64_t N,
                      int64_t lddy, int64_t rows_per_block) {
   constexpr bool kAct = kActOf != kActNone;
@@ -37,6 +38,8 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t col = static_cast<int64_t>(blockIdx.x) * kCols + c;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows_per_block, r1 = min(M, r0 + rows_per_block);
   float2 sum[4] = {};
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (col < N) {
     auto step = [&](const uint4& g, const uint4& v, int64_t row) {
       float2 d[4], t[4];
@@ -51,7 +54,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int e = 0; e < 4; ++e) sum[e] = __fadd2_rn(sum[e], d[e]);
     };
     int64_t row = r0 + (warp >> 2) * 4 + (lane >> 3);
-    constexpr int kDeep = 8;
+    constexpr int kDeep = kAct ? 4 : 8;
     for (; row + (kDeep - 1) * kRowStep < r1; row += kDeep * kRowStep) {
       uint4 g[kDeep], v[kDeep];
 #pragma unroll
@@ -85,35 +88,64 @@ __global__ void __launch_bounds__(kThreads)
   if (j < N) part[static_cast<int64_t>(blockIdx.y) * N + j] = red[0][threadIdx.x] + red[1][threadIdx.x];
 }
 
-// db from part [rows][N]: 32 columns a block, 32 threads a column take the rows in turn and are added in order
-__global__ void __launch_bounds__(1024) linear_db_kernel(const float* part, int64_t rows, int64_t N, void* db, int dtype,
-                                                         bool accumulate) {
-  __shared__ double acc[32][33];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + tx;
-  double s = 0.0;
-  if (j < N)
-    for (int64_t i = ty; i < rows; i += 32) s += static_cast<double>(part[i * N + j]);
-  acc[ty][tx] = s;
+// db from part [rows][N]: 32 columns a block, sixteen warps take the rows in turn, eight loads under way, and are added in
+// order; at most 64 terms in sequence, then these parts.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(32 * kSumWarps) linear_db_kernel(const float* part, int64_t rows, int64_t N, void* db,
+                                                                   int dtype, bool accumulate) {
+  __shared__ float acc[kSumWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float* p = part + min(j, N - 1);
+  float t = 0.0f, s = 0.0f;
+  int64_t i = warp;
+  for (int n = 1; i + 7 * kSumWarps < rows; i += 8 * kSumWarps, ++n) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = p[(i + u * kSumWarps) * N];
+    s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    if (n % 8 == 0) {
+      t += s;
+      s = 0.0f;
+    }
+  }
+  float v[7];
+#pragma unroll
+  for (int u = 0; u < 7; ++u) v[u] = i + u * kSumWarps < rows ? p[(i + u * kSumWarps) * N] : 0.0f;
+#pragma unroll
+  for (int u = 0; u < 7; ++u) s += v[u];
+  acc[warp][lane] = t + s;
   __syncthreads();
-  if (ty != 0 || j >= N) return;
-  double t = 0.0;
-  for (int k = 0; k < 32; ++k) t += acc[k][tx];
-  if (accumulate) t += static_cast<double>(row::load_any(db, j, dtype));
-  // rounded once: from fp64
-  if (dtype == 0) static_cast<float*>(db)[j] = static_cast<float>(t);
-  else if (dtype == 1) static_cast<__half*>(db)[j] = __double2half(t);
-  else static_cast<__nv_bfloat16*>(db)[j] = __double2bfloat16(t);
+  if (warp != 0 || j >= N) return;
+  t = acc[0][lane];
+#pragma unroll
+  for (int w = 1; w < kSumWarps; ++w) t += acc[w][lane];
+  if (accumulate) t += row::load_any(db, j, dtype);
+  row::store_any(db, j, dtype, t);
 }
 
-// rows of a block: about four blocks on each of 152 SMs (a plan that does not depend on the device, so that the
+// rows of a block: about three blocks on each of 152 SMs (a plan that does not depend on the device, so that the
 // workspace's size does not either)
 int64_t rows_per_block(int64_t M, int64_t N) {
-  const int64_t gx = (N + kCols - 1) / kCols, blocks = std::max<int64_t>(1, 608 / gx);
+  const int64_t gx = (N + kCols - 1) / kCols, blocks = std::max<int64_t>(1, 152 * kBlocks / gx);
   const int64_t rows = ((M + blocks - 1) / blocks + kRowStep - 1) / kRowStep * kRowStep;
   return std::min<int64_t>(kMaxRows, std::max<int64_t>(rows, 4 * kRowStep));
 }
 
+// a programmatic dependent launch: its blocks may come while the kernel before it ends, and wait for it
+cudaLaunchConfig_t dependent_launch(const dim3& grid, int threads, cudaStream_t stream, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
 template <bool kF16>
 cudaError_t launch_dz(const dim3& grid, const uint16_t* dy, const uint16_t* z, uint16_t* dz, float* part, int64_t M,
                       int64_t N, int64_t lddy, int64_t per, int act, cudaStream_t stream) {
@@ -121,8 +153,9 @@ cudaError_t launch_dz(const dim3& grid, const uint16_t* dy, const uint16_t* z, u
                       : act == 0          ? linear_dz_kernel<0, kF16>
                       : act == 1          ? linear_dz_kernel<1, kF16>
                                           : linear_dz_kernel<2, kF16>;
-  kernel<<<grid, kThreads, 0, stream>>>(dy, z, dz, part, M, N, lddy, per);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = dependent_launch(grid, kThreads, stream, attr);
+  return cudaLaunchKernelEx(&cfg, kernel, dy, z, dz, part, M, N, lddy, per);
 }
 
 }  // namespace
@@ -150,9 +183,10 @@ cudaError_t launch_linear_dz(const void* dy, const void* z, void* dz, void* db, 
     if (e != cudaSuccess) return e;
   }
   if (db == nullptr) return cudaSuccess;
-  linear_db_kernel<<<static_cast<unsigned>((N + 31) / 32), 1024, 0, stream>>>(part, chunks, N, db,
-                                                                              db_f32 ? 0 : (f16 ? 1 : 2), accumulate);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = dependent_launch(dim3(static_cast<unsigned>((N + 31) / 32)), 32 * kSumWarps, stream, attr);
+  return cudaLaunchKernelEx(&cfg, linear_db_kernel, static_cast<const float*>(part), chunks, N, db,
+                            db_f32 ? 0 : (f16 ? 1 : 2), accumulate);
 }
 
 }  // namespace swg

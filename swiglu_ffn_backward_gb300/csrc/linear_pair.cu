@@ -144,6 +144,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   cluster_sync();  // both CTAs' barriers are initialised before any remote arrival, commit or copy
   const uint32_t tmem = s.tmem_base;
+  // what the kernel before this one wrote is visible from here on
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   auto timeout = [&]() {
     if (args.status != nullptr) atomicOr(args.status, kStatusTimeout);
     s.abort_flag = 1u;
@@ -493,13 +496,15 @@ cudaError_t launch_linear_pair(const void* A, int64_t lda, const void* B, int64_
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, my, mz, mr, a);
   if (err != cudaSuccess || plan.parts == 1) return err;
   const int64_t n4 = I * J / 4;

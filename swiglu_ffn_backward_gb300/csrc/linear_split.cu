@@ -12,8 +12,9 @@
 // added in the cluster through shared memory in the blocks' order (no atomics, no workspace, one launch).
 //
 // A block: warp 0 lane 0 copies operand tiles (64 of r) into a ring with TMA, warp 1 lane 0 issues the tensor
-// instructions into TMEM, warps 4-7 move the sums from TMEM into the ring's memory; then all threads add the
-// cluster's parts, each block a share of the tile, and apply the epilogue: 16-byte loads and stores.
+// instructions into TMEM; then all warps move the sums from TMEM into the ring's memory, add the cluster's parts, each
+// block a share of the tile, and apply the epilogue: 16-byte loads and stores. A programmatic dependent launch: its
+// set-up runs beside the end of the kernel before it.
 //
 // Every wait is bounded: a block whose wait ran out sets the status word, issues nothing more, waits (bounded) for
 // its copies and products in flight and goes through the cluster's barriers like the others.
@@ -38,7 +39,7 @@ struct SplitArgs {
   Epilogue epi;
   uint32_t* status;
   int L, C;              // sizes of l and c
-  int NT;                // c in a tile: 16, 32, 64, 128 or 256
+  int NT;                // c in a tile: a multiple of 16 (of 64 where r is B's outermost dimension), up to 256
   int tiles_l, tiles_c;
   int nkb, S;            // blocks of 64 of r; blocks of a cluster
   int stages;
@@ -52,18 +53,17 @@ struct SplitControl {
   volatile uint32_t abort_flag, issued, consumed;
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {  // volatile: it stays between the cluster's barriers
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
   return v;
 }
 
 // kAOuter, kBOuter: whether r is the outermost dimension of the operand in memory
 template <bool kAOuter, bool kBOuter, bool kF16>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                         const SplitArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads)
   // this block's part of the reduction: at least one block of 64
   const int kb0 = static_cast<int>(static_cast<int64_t>(a.nkb) * rank / a.S);
   const int n = static_cast<int>(static_cast<int64_t>(a.nkb) * (rank + 1) / a.S) - kb0;
-  const uint32_t tmem_cols = a.NT < 32 ? 32 : a.NT;
+  const uint32_t tmem_cols = a.NT <= 32 ? 32 : a.NT <= 64 ? 64 : a.NT <= 128 ? 128 : 256;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
@@ -98,6 +98,9 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
+  // everything above ran beside the end of the kernel before this one; its writes are visible from here on
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   auto timeout = [&]() {
     if (a.status != nullptr) atomicOr(a.status, kStatusTimeout);
     s.abort_flag = 1u;
@@ -174,9 +177,9 @@ __global__ void __launch_bounds__(kThreads)
   float* const part = reinterpret_cast<float*>(ring);
   const int cols = min(a.NT, a.C - c0);
   tc_fence_after();
-  if (warp >= 4) {
+  {
     const int q = warp & 3;  // TMEM lane quarter
-    for (int c = 0; c < cols; c += 32) {
+    for (int c = (warp >> 2) * 32; c < cols; c += 64) {
       uint32_t v[32];
       tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
       tmem_ld_wait();
@@ -202,15 +205,25 @@ __global__ void __launch_bounds__(kThreads)
       uint4 res = make_uint4(0u, 0u, 0u, 0u);
       if (p.residual != nullptr) res = *reinterpret_cast<const uint4*>(p.residual + row * p.ldr + l0 + l);
       const uint32_t off = static_cast<uint32_t>(c * kLanes + l) * sizeof(float);
-      float2 v[4] = {};
+      // all parts' loads are under way at once
+      float4 x[kMaxSplit], y[kMaxSplit];
 #pragma unroll
       for (int k = 0; k < kMaxSplit; ++k) {
-        if (k >= a.S) break;
-        const float4 x = ld_cluster_f4(peers[k] + off), y = ld_cluster_f4(peers[k] + off + 16);
-        v[0] = __fadd2_rn(v[0], make_float2(x.x, x.y));
-        v[1] = __fadd2_rn(v[1], make_float2(x.z, x.w));
-        v[2] = __fadd2_rn(v[2], make_float2(y.x, y.y));
-        v[3] = __fadd2_rn(v[3], make_float2(y.z, y.w));
+        if (k < a.S) {
+          x[k] = ld_cluster_f4(peers[k] + off);
+          y[k] = ld_cluster_f4(peers[k] + off + 16);
+        }
+      }
+      float2 v[4] = {make_float2(x[0].x, x[0].y), make_float2(x[0].z, x[0].w), make_float2(y[0].x, y[0].y),
+                     make_float2(y[0].z, y[0].w)};
+#pragma unroll
+      for (int k = 1; k < kMaxSplit; ++k) {
+        if (k < a.S) {
+          v[0] = __fadd2_rn(v[0], make_float2(x[k].x, x[k].y));
+          v[1] = __fadd2_rn(v[1], make_float2(x[k].z, x[k].w));
+          v[2] = __fadd2_rn(v[2], make_float2(y[k].x, y[k].y));
+          v[3] = __fadd2_rn(v[3], make_float2(y[k].z, y[k].w));
+        }
       }
       add_bias<kF16>(p, l0 + l, a.L, v);
       if (p.z != nullptr) *reinterpret_cast<uint4*>(p.z + at) = narrow8<kF16>(v);
@@ -233,25 +246,69 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// What a product costs with tiles of 128 x NT, S blocks each, in microseconds: estimates that order the choices, from
+// the rates of the tensor cores (0.36 us for 64 of r in a 128 x 256 tile on one SM), of HBM and of L2, the copies under
+// way in a ring, and from what a block's start, its epilogue and the exchange in a cluster take. Measured (w from HBM):
+// 1 x 14336 x 4096 by 16/6 (NT/S) 22.0 us, 16/4 24.7, 16/2 43; 77 x 4096 x 14336 by 80/2 23.7, 80/1 30, 48/2 39 (two waves);
+// 257 x 512 x 1024 by 48/1 6.2, 256/8 17.6 (eight blocks of 200 KB a cluster: two waves).
 struct SplitPlan {
-  int NT, S, stages, tiles_l, tiles_c, nkb;
+  int NT, S, stages, per_sm, tiles_l, tiles_c, nkb;
   int64_t tiles;
+  double us;
 };
-// NT: the rows of out (a multiple of 64 where they are read 64 at a time), up to 256. S: as many blocks a tile as
-// there is room for, two on an SM where the ring is small enough (NT <= 64), with at least one stage each.
-SplitPlan split_plan(int64_t L, int64_t C, int64_t R, bool b_outer, int sms) {
+SplitPlan split_cost(int64_t L, int64_t C, int64_t R, int NT, int S, int per_sm, int sms) {
   SplitPlan p;
-  p.NT = b_outer ? 64 : 16;
-  while (p.NT < 256 && p.NT < C) p.NT *= 2;
+  p.NT = NT;
+  p.S = S;
   p.tiles_l = static_cast<int>((L + kLanes - 1) / kLanes);
-  p.tiles_c = static_cast<int>((C + p.NT - 1) / p.NT);
+  p.tiles_c = static_cast<int>((C + NT - 1) / NT);
   p.tiles = static_cast<int64_t>(p.tiles_l) * p.tiles_c;
   p.nkb = static_cast<int>((R + kRed - 1) / kRed);
-  const int64_t room = (p.NT <= 64 ? 2 : 1) * sms;
-  p.S = static_cast<int>(std::min<int64_t>({kMaxSplit, std::max<int64_t>(1, room / p.tiles), p.nkb}));
-  const int ring = p.NT <= 64 ? 108 * 1024 : 192 * 1024;
-  p.stages = std::min(kMaxStages, ring / (kABytes + p.NT * kRed * 2));
+  const int stage = kABytes + NT * kRed * 2;
+  p.per_sm = per_sm;
+  p.stages = std::min(kMaxStages, (p.per_sm == 2 ? 108 : 196) * 1024 / stage);
+  // blocks that run at once, of 152 and 304: a cluster's lie in one part of the device (cudaOccupancyMaxActiveClusters)
+  constexpr int kRoom[2][kMaxSplit] = {{152, 152, 138, 144, 140, 138, 105, 120}, {304, 304, 291, 296, 290, 276, 266, 288}};
+  const int64_t blocks = p.tiles * S;
+  const int64_t slots = std::max<int64_t>(S, static_cast<int64_t>(kRoom[p.per_sm - 1][S - 1]) * sms / 152);
+  const double waves = static_cast<double>((blocks + slots - 1) / slots);
+  const double on_sm = static_cast<double>(std::min<int64_t>(p.per_sm, (blocks + sms - 1) / sms));
+  const double kb = static_cast<double>((p.nkb + S - 1) / S);
+  const double tensor = waves * on_sm * kb * std::max(NT, 96) / 256.0 * 0.36;
+  // what several tiles along c read of A comes from L2 in part
+  const double again = std::min(2.0, 1.0 + 0.3 * (p.tiles_c - 1));
+  // 64 of r: A at most at 48 KB/us a block and 65 an SM, whatever the ring's depth, everything at 130 an SM, and the
+  // ring's copies have to cover their latency
+  const double from_hbm = kABytes * again / p.tiles_c;
+  const double block = std::max(on_sm > 1 ? from_hbm * 2.0 / 65e3 : from_hbm / 48e3, on_sm * stage / 130e3);
+  const double stream = waves * kb * std::max(block, (1.0 + 0.7 * kABytes / stage) / p.stages);
+  const double l2 = static_cast<double>(p.tiles) * (kLanes + NT) * R * 2 / 14e6;
+  const double hbm = (static_cast<double>(p.tiles_l) * kLanes * again + static_cast<double>(C)) * R * 2 /
+                     6.5e6;
+  const double finish = 1.0 + 0.02 * NT + (S > 1 ? 0.5 + 0.007 * NT * S : 0.0);
+  p.us = std::max(std::max(tensor, stream), std::max(l2, hbm)) + waves * (2.5 + finish);
   return p;
+}
+// The cheapest of the tiles that cover C evenly and of the cluster sizes.
+SplitPlan split_plan(int64_t L, int64_t C, int64_t R, bool b_outer, int sms) {
+  const int unit = b_outer ? 64 : 16;
+  const int64_t nkb = (R + kRed - 1) / kRed, least = (C + 255) / 256;
+  SplitPlan best;
+  best.us = -1.0;
+  int last = 0;
+  for (int64_t n = least; n < least + 8; ++n) {  // tiles along c
+    int NT = static_cast<int>(((C + n - 1) / n + unit - 1) / unit * unit);
+    if (NT > 128) NT = 256;  // 160 to 208 took as long for 64 of r (200 x 4096 x 14336 34.8 us by 208, 32.7 by 256)
+    if (NT == last) continue;
+    last = NT;
+    for (int S = 1; S <= kMaxSplit && S <= nkb; ++S) {
+      for (int per_sm = 1; per_sm <= (NT <= 128 ? 2 : 1); ++per_sm) {  // blocks an SM: with three stages or more each
+        const SplitPlan p = split_cost(L, C, R, NT, S, per_sm, sms);
+        if (best.us < 0.0 || p.us < best.us) best = p;
+      }
+    }
+  }
+  return best;
 }
 
 template <bool kAOuter, bool kBOuter, bool kF16>
@@ -276,13 +333,15 @@ cudaError_t launch_split_of(const void* A, int64_t lda, const void* B, int64_t l
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(p.S);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
 }
 
@@ -294,18 +353,14 @@ cudaError_t launch_split(const void* A, int64_t lda, const void* B, int64_t ldb,
                : launch_split_of<kAOuter, kBOuter, false>(A, lda, B, ldb, L, C, R, epi, stream);
 }
 
-// Whether the kernel on CTA pairs is the faster one. In units of a 64-block of a 128 x 256 tile on one SM (0.33 us at the
-// measured peak): it takes whole waves of tiles; the one above a wave of blocks, each with its part of the reduction
-// and the exchange of sums behind it.
+// Whether the kernel on CTA pairs is the faster one: it takes whole waves of tiles of 256 x 256, 64 of r in 0.35 us,
+// and the last tile's epilogue comes behind its products.
 bool use_pairs(const PairPlan& p, int64_t L, int64_t C, int64_t R, bool b_outer, int sms) {
-  const SplitPlan q = split_plan(L, C, R, b_outer, sms);
-  if (q.NT <= 64) return false;
+  if (C <= 128) return false;  // half of a tile's rows and more would be empty
   const int64_t pairs = std::max(1, sms / 2);
   const double waves = static_cast<double>((p.tiles_i * p.tiles_j * p.parts + pairs - 1) / pairs);
-  const double pair = waves * p.per + 10.0 + (p.parts > 1 ? 12.0 : 0.0);
-  const double split_waves = static_cast<double>((q.tiles * q.S + sms - 1) / sms);
-  const double split = split_waves * (static_cast<double>((q.nkb + q.S - 1) / q.S) * q.NT / 256.0 * 1.15 + 10.0);
-  return pair < split;
+  const double pair = waves * std::max(static_cast<double>(p.per) * 0.35, 4.0) + 5.5 + (p.parts > 1 ? 5.0 : 0.0);
+  return pair < split_plan(L, C, R, b_outer, sms).us;
 }
 
 }  // namespace
