@@ -1,486 +1,10 @@
-// The junction of two blocks of a transformer: the norm after a block, its gate, the scaled residual, and the norm
-// before the next block (root mean square norms, over the last dimension), forward and backward.
-//   rstd(t) = 1 / sqrt(sum t^2 / N + eps)
-//   v = u rstd(u) gamma_post  (v = u without the norm after the block)
-//   h = alpha r + gate v, rounded to the I/O type;  y = h rstd(h) gamma_pre
-// A row of the gate serves M / G rows, one after the other. Backward, with u^ = u rstd(u), h^ = h rstd(h),
-// a = dy gamma_pre and q = gate gamma_post, from dy and dh, the gradient that reaches h past the second norm:
-//   D  = dh + rstd(h) (a - h^ mean(a h^)),  dr = alpha D
-//   du = rstd(u) (q D - u^ mean(q D u^))
-//   dgamma_pre = sum dy h^;  with S = sum D u^ over the rows of a gate row: dgate = gamma_post S, and
-//   dgamma_post = the sum of gate S over the gate's rows
-// so that two column sums give all three parameter gradients. The second mean needs no second round over the row:
-//   sum q D u^ = sum q u^ (dh + rstd(h) a) - rstd(h) mean(a h^) sum q h^ u^
-// All arithmetic is fp32; h, y, dr, du and the parameters' gradients are rounded once.
-#include <algorithm>
-
-#include "row_vectors.cuh"
+// Backward of the norms between blocks (block_norm_fwd.cu has the formulas).
+#include "block_norm.cuh"
 
 namespace swg {
 namespace {
 
-using namespace row;
-
-constexpr int kMaxThreads = 1024;
-
-// ---- forward: a row in the registers of a group of threads, R vectors each
-// kShared: the S blocks of a cluster, of one group each, share a row.
-constexpr int kBlock = 256;      // threads of a block, unless a row takes more
-constexpr int kMaxGroup = 512;   // threads of a group, and of a block
-template <bool kRagged>
-constexpr int kFwdRegs = kRagged ? 128 : 80;
-template <typename T, int R, bool kRagged, bool kShared>
-__global__ void __maxnreg__(kFwdRegs<kRagged>)
-    bn_fwd_kernel(const BnFwdArgs a, int G, int S, Stall stall, uint32_t* status) {
-  __shared__ float smem[2 * 32];
-  __shared__ ClusterSlots slots;
-  constexpr int E = kElems<T>, P = kPairs<T>;
-  constexpr bool kNarrow = R == 1;  // groups of less than a warp
-  const int groups = kShared ? 1 : blockDim.x / G;
-  const int t = kShared ? threadIdx.x + cluster_ctarank() * R * G : threadIdx.x % G;  // vectors t, t + G, ...
-  const int64_t step = static_cast<int64_t>(kShared ? gridDim.x / S : gridDim.x) * groups;
-  const int N = static_cast<int>(a.N);
-  int64_t r = kShared ? blockIdx.x / S : static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / G;
-  const int shift = kRagged ? shift_of(static_cast<const T*>(a.pre ? a.y : a.h) + r * a.N) : 0;
-  int n = (N + shift + E - 1) / E;  // vectors of the row
-  const bool add = a.residual != nullptr, f32 = a.wdtype == 0, gated = a.gate != nullptr, join = a.h != nullptr;
-  const float inv_n = 1.0f / static_cast<float>(a.N);
-  const float2 alpha = pair(a.alpha);
-  const uint32_t per_gate = static_cast<uint32_t>(a.rows_per_gate);
-  auto column = [&](int i) { return (t + i * G) * E - shift; };
-  struct Row {
-    Raw u[R], res[R];
-  };
-  const Rows<T> u(a.u, a.ldu, a.M, a.N), res(a.residual, a.ldr, a.M, a.N);
-  auto load = [&](Row& w, int64_t r) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (t + i * G >= n) continue;
-      w.u[i] = load_columns<T, kRagged>(u, r, column(i), N);
-      if (add) w.res[i] = load_columns<T, kRagged>(res, r, column(i), N);
-    }
-  };
-  GroupSum<1, kNarrow> sum(smem, G);
-  SharedSum<kShared, 1> share(slots, S, stall);
-  auto rstd_of = [&](float2 s2) {
-    float s[1] = {s2.x + s2.y};
-    sum(s);
-    share(s);
-    return rsqrtf(fmaf(s[0], inv_n, a.eps));
-  };
-  Row next;
-  const int64_t M = a.M + (kNarrow ? (threadIdx.x & 31) / G : 0);  // the rows of a warp's groups end together
-  if (r < a.M) load(next, r);
-  for (; r < M; r += step) {
-    if (kNarrow && r >= a.M) n = 0;
-    if (kShared && static_cast<uint64_t>(r) >= static_cast<uint64_t>(stall.at)) share.silence();
-    Row w = next;
-    if (r + step < a.M) load(next, r + step);
-    if constexpr (kRagged) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        clear_others<T>(w.u[i], column(i), N);
-        if (add) clear_others<T>(w.res[i], column(i), N);
-      }
-    }
-    // the gate's columns and those of its norm: under way while the row's sum is taken
-    float2 q[R][P];
-    const char* gate = static_cast<const char*>(a.gate) +
-                       (gated ? static_cast<int64_t>(static_cast<uint32_t>(r) / per_gate) * a.N * (a.gdtype == 0 ? 4 : 2) : 0);
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (gated && t + i * G < n) load_weights<T, kRagged>(gate, column(i), N, a.gdtype == 0, 1.0f, q[i]);
-    float ru = 0.0f, rh = 0.0f;
-    if (a.post) {
-      float2 s2 = pair(0.0f);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (t + i * G >= n) continue;
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const float2 v = get_pair<T>(w.u[i], e);
-          s2 = __ffma2_rn(v, v, s2);
-        }
-      }
-      ru = rstd_of(s2);
-    }
-    float2 s2 = pair(0.0f);
-    if (join) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (t + i * G >= n) continue;
-        float2 post[P];
-        if (a.post) load_weights<T, kRagged>(a.gamma_post, column(i), N, f32, 1.0f, post);
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-          float2 v = get_pair<T>(w.u[i], e);
-          if (a.post) v = __fmul2_rn(v, __fmul2_rn(pair(ru), post[e]));
-          if (gated) v = __fmul2_rn(v, q[i][e]);
-          if (add) v = __ffma2_rn(alpha, get_pair<T>(w.res[i], e), v);
-          set_pair<T>(w.u[i], e, v);  // h as it is stored
-          v = get_pair<T>(w.u[i], e);
-          s2 = __ffma2_rn(v, v, s2);
-        }
-        store_columns<T, kRagged>(static_cast<T*>(a.h) + r * a.N, column(i), N, w.u[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (t + i * G >= n) continue;
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const float2 v = get_pair<T>(w.u[i], e);
-          s2 = __ffma2_rn(v, v, s2);
-        }
-      }
-    }
-    if (a.pre) {
-      rh = rstd_of(s2);
-      T* y = static_cast<T*>(a.y) + r * a.N;
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (t + i * G >= n) continue;
-        float2 pre[P];
-        load_weights<T, kRagged>(a.gamma_pre, column(i), N, f32, 1.0f, pre);
-#pragma unroll
-        for (int e = 0; e < P; ++e)
-          set_pair<T>(w.u[i], e, __fmul2_rn(get_pair<T>(w.u[i], e), __fmul2_rn(pair(rh), pre[e])));
-        store_columns<T, kRagged>(y, column(i), N, w.u[i]);
-      }
-    }
-    if (t == 0 && (!kNarrow || n > 0)) {
-      a.stats[2 * r] = ru;
-      a.stats[2 * r + 1] = rh;
-    }
-  }
-  share.end(status);
-}
-
-// ---- rows of any length, element by element, read three times (from L2 where a row fits)
-template <typename T>
-__global__ void __launch_bounds__(kMaxThreads) bn_fwd_long_kernel(const BnFwdArgs a) {
-  __shared__ float buf[32];
-  const float inv_n = 1.0f / static_cast<float>(a.N);
-  for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
-    const T* u = static_cast<const T*>(a.u) + r * a.ldu;
-    const T* res = a.residual != nullptr ? static_cast<const T*>(a.residual) + r * a.ldr : nullptr;
-    const int64_t gate = r / a.rows_per_gate * a.N;
-    T* h = a.h != nullptr ? static_cast<T*>(a.h) + r * a.N : nullptr;
-    float s[1], ru = 0.0f, rh = 0.0f;
-    if (a.post) {
-      long_sums(a.N, s, [&](float (&p)[1], int64_t j) {
-        const float v = to_f(u[j]);
-        p[0] = fmaf(v, v, p[0]);
-      });
-      ru = rsqrtf(fmaf(block_sum(s[0], buf), inv_n, a.eps));
-    }
-    auto value = [&](int64_t j) {  // h_j, rounded as it is stored
-      if (a.h == nullptr) return to_f(u[j]);
-      float v = to_f(u[j]);
-      if (a.post) v *= ru * (a.gamma_post != nullptr ? load_any(a.gamma_post, j, a.wdtype) : 1.0f);
-      if (a.gate != nullptr) v *= load_any(a.gate, gate + j, a.gdtype);
-      if (res != nullptr) v = fmaf(a.alpha, to_f(res[j]), v);
-      return to_f(from_f<T>(v));
-    };
-    if (a.pre) {
-      long_sums(a.N, s, [&](float (&p)[1], int64_t j) {
-        const float v = value(j);
-        p[0] = fmaf(v, v, p[0]);
-      });
-      rh = rsqrtf(fmaf(block_sum(s[0], buf), inv_n, a.eps));
-    }
-    for (int64_t j = threadIdx.x; j < a.N; j += blockDim.x) {
-      const float v = value(j);
-      if (h != nullptr) h[j] = from_f<T>(v);
-      if (a.pre)
-        static_cast<T*>(a.y)[r * a.N + j] =
-            from_f<T>(v * (rh * (a.gamma_pre != nullptr ? load_any(a.gamma_pre, j, a.wdtype) : 1.0f)));
-    }
-    if (threadIdx.x == 0) {
-      a.stats[2 * r] = ru;
-      a.stats[2 * r + 1] = rh;
-    }
-  }
-}
-
-// ---- many whole rows: a group's next rows are on their way into shared memory
-// A thread that holds a row's vectors has but one more row of them under way; four rows of all tensors in a ring of
-// shared memory, one bulk copy a tensor and row, keep the memory busy over a row's reductions. The group's first thread
-// issues the next copy into a row's stage behind the barrier of the next row's first sum, when the whole group has
-// read it. The stage is read again for each pass over the row, so that the row takes no registers between them.
-struct RingPlan {
-  int stages;        // rows of the ring of a group
-  int stage_bytes;   // of a row's tensors
-  int group_bytes;   // of a group's ring
-};
-constexpr int kMaxStages = 8;
-template <int kTensors>
-struct Ring {
-  uint64_t* full;
-  unsigned char* buf;
-  int stages, stage_bytes, at = 0;  // stage of the row that is read next
-  uint32_t parity = 0;
-  int64_t issued = 0;
-  Patience wait;
-  __device__ __forceinline__ Ring(unsigned char* smem, uint64_t* bars, const RingPlan& p, int group, const Stall& stall)
-      : full(bars + group * kMaxStages), buf(smem + group * p.group_bytes), stages(p.stages), stage_bytes(p.stage_bytes),
-        wait(stall.limit) {}
-  __device__ __forceinline__ void init() {
-    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
-  }
-  // by the group's first thread: the next row's tensors, `bytes` of each from `from` (null: none) into the stage's
-  // slots of `slot` bytes
-  __device__ __forceinline__ void issue(const void* const (&from)[kTensors], const uint32_t (&bytes)[kTensors], int slot,
-                                        int64_t stall_at) {
-    if (wait.lost() || issued == stall_at) return;
-    const int st = static_cast<int>(issued % stages);
-    uint32_t all = 0;
-#pragma unroll
-    for (int i = 0; i < kTensors; ++i) all += from[i] != nullptr ? bytes[i] : 0u;
-    mbar_arrive_expect_tx(&full[st], all);
-#pragma unroll
-    for (int i = 0; i < kTensors; ++i)
-      if (from[i] != nullptr && bytes[i] > 0) bulk_g2s(buf + st * stage_bytes + i * slot, from[i], bytes[i], &full[st]);
-    ++issued;
-  }
-  // the stage of the next row, landed
-  __device__ __forceinline__ const unsigned char* next() {
-    wait(&full[at], parity);
-    const unsigned char* p = buf + at * stage_bytes;
-    if (++at == stages) {
-      at = 0;
-      parity ^= 1u;
-    }
-    return p;
-  }
-  // copies that nothing waited for have to land before the block ends
-  __device__ __forceinline__ void end(uint32_t* status) {
-    if (!wait.lost()) return;
-    if (status != nullptr) atomicOr(status, kStatusTimeout);
-    for (int64_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
-      if (!mbar_wait(&full[i % stages], static_cast<uint32_t>(i / stages) & 1u)) break;
-  }
-};
-__device__ __forceinline__ Raw ld_stage(const unsigned char* p) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  return Raw{{u.x, u.y, u.z, u.w}};
-}
-// eight or four columns of a gate in a stage, of the tensor's type or fp32
-template <typename T>
-__device__ __forceinline__ void stage_pairs(const unsigned char* p, int vector, bool f32, float2 (&f)[kPairs<T>]) {
-  if (sizeof(T) == 2 && f32) {
-    const Raw a = ld_stage(p + vector * 32), b = ld_stage(p + vector * 32 + 16);
-    f[0] = get_pair<float>(a, 0);
-    f[1] = get_pair<float>(a, 1);
-    f[2 % kPairs<T>] = get_pair<float>(b, 0);
-    f[3 % kPairs<T>] = get_pair<float>(b, 1);
-    return;
-  }
-  const Raw a = ld_stage(p + vector * 16);
-#pragma unroll
-  for (int e = 0; e < kPairs<T>; ++e) f[e] = get_pair<T>(a, e);
-}
-// Sums over a group of whole warps, up to eight; every thread gets them, added in a fixed order. Two buffers alternate,
-// so that one barrier a sum is enough.
-struct WarpRows {
-  float* buf;  // of the group: 2 x 32
-  int warps, id, turn = 0;
-  __device__ __forceinline__ WarpRows(float* smem, int G)
-      : buf(smem + (threadIdx.x / G) * 64), warps(G >> 5), id(1 + static_cast<int>(threadIdx.x) / G) {}
-  __device__ __forceinline__ float* next() {
-    float* b = buf + turn;
-    turn ^= 32;
-    return b;
-  }
-  __device__ __forceinline__ void meet() const {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(warps * 32) : "memory");
-  }
-  __device__ __forceinline__ float one(float v) {
-    v = warp_sum(v);
-    if (warps == 1) {
-      __syncwarp();
-      return v;
-    }
-    float* b = next();
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) b[threadIdx.x / 32 % warps] = v;
-    meet();
-    v = (lane & 7) < warps ? b[lane & 7] : 0.0f;
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  }
-  // Three at once: lanes exchange halves of what they hold, so that it takes six shuffles in place of fifteen.
-  __device__ __forceinline__ void three(float (&v)[3]) {
-    const int lane = threadIdx.x & 31;
-    const bool b4 = (lane & 16) != 0, b3 = (lane & 8) != 0;
-    // lanes with bit 4: v[2] (and nothing), the others v[0] and v[1]
-    float x = (b4 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, b4 ? v[0] : v[2], 16);
-    float y = (b4 ? 0.0f : v[1]) + __shfl_xor_sync(0xffffffffu, b4 ? v[1] : 0.0f, 16);
-    x = (b3 ? y : x) + __shfl_xor_sync(0xffffffffu, b3 ? x : y, 8);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    // lanes 0 .. 7: v[0], 8 .. 15: v[1], 16 .. 23: v[2]
-    if (warps > 1) {
-      float* b = next();
-      if ((lane & 7) == 0) b[(threadIdx.x / 32 % warps) * 4 + (lane >> 3)] = x;
-      meet();
-      x = (lane & 7) < warps ? b[(lane & 7) * 4 + (lane >> 3)] : 0.0f;
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    } else {
-      __syncwarp();
-    }
-#pragma unroll
-    for (int i = 0; i < 3; ++i) v[i] = __shfl_sync(0xffffffffu, x, 8 * i);
-  }
-};
-
-// Forward: a group takes rows one after the other, so that it keeps its gate row's columns in registers until the next
-// gate row begins; kRowGate: a gate for each row is one more tensor in the ring.
-constexpr int kFwdBlocks = 3;  // blocks of 256 threads an SM, with 80 registers a thread
-template <bool kRowGate>
-constexpr int kFwdRingBlocks = 2;
-template <typename T, int R, bool kShared, bool kRowGate, bool kFull>
-__global__ void __maxnreg__(128)
-    bn_fwd_ring_kernel(const BnFwdArgs a, const RingPlan plan, int G, int S, Stall stall, uint32_t* status) {
-  extern __shared__ __align__(128) unsigned char dyn[];
-  __shared__ uint64_t bars[8 * kMaxStages];
-  __shared__ float smem[8 * 64];
-  __shared__ ClusterSlots slots;
-  constexpr int E = kElems<T>, P = kPairs<T>, kTensors = kRowGate ? 3 : 2;
-  const int groups = kShared ? 1 : blockDim.x / G, group = kShared ? 0 : threadIdx.x / G;
-  const int rank = kShared ? static_cast<int>(cluster_ctarank()) : 0, in = kShared ? threadIdx.x : threadIdx.x % G;
-  const int64_t units = static_cast<int64_t>(kShared ? gridDim.x / S : gridDim.x) * groups;
-  const int64_t unit = kShared ? blockIdx.x / S : static_cast<int64_t>(blockIdx.x) * groups + group;
-  const int64_t begin = a.M * unit / units, end = a.M * (unit + 1) / units;
-  const int n = static_cast<int>(a.N) / E, n0 = rank * R * G;  // vectors of a row, and the first of this block's
-  const int mine = min(R * G, n - n0);
-  const bool add = kFull || a.residual != nullptr, post_norm = kFull || a.post, pre_norm = kFull || a.pre;
-  const bool f32 = a.wdtype == 0, gated = a.gate != nullptr, gate32 = a.gdtype == 0;
-  const float inv_n = 1.0f / static_cast<float>(a.N);
-  const float2 alpha = pair(a.alpha);
-  const uint32_t per_gate = static_cast<uint32_t>(a.rows_per_gate);
-  Ring<kTensors> ring(dyn, bars, plan, group, stall);
-  const bool first = in == 0;
-  if (first) {
-    ring.init();
-    fence_mbar_init();
-  }
-  __syncthreads();
-  WarpRows sums(smem, G);
-  SharedSum<kShared, 1> share(slots, S, stall);
-  const int64_t stop_at = kShared ? -1 : stall.at;
-  auto issue = [&](int64_t r) {
-    const void* from[kTensors];
-    uint32_t bytes[kTensors];
-    from[0] = static_cast<const T*>(a.u) + r * a.ldu + n0 * E;
-    from[1] = add ? static_cast<const T*>(a.residual) + r * a.ldr + n0 * E : nullptr;
-    bytes[0] = bytes[1] = static_cast<uint32_t>(mine) * 16u;
-    if constexpr (kRowGate) {
-      const int64_t es = gate32 ? 4 : sizeof(T);
-      from[2] = static_cast<const char*>(a.gate) + (r * a.N + n0 * E) * es;
-      bytes[2] = static_cast<uint32_t>(mine) * static_cast<uint32_t>(E * es);
-    }
-    ring.issue(from, bytes, R * G * 16, stop_at);
-  };
-  if (first)
-    for (int64_t r = begin; r < min(end, begin + ring.stages); ++r) issue(r);
-  float2 pre[R][P], q[R][P];  // gamma_pre; gamma_post, or (without kRowGate) that times the gate
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (in + i * G < mine) {
-      load_weights<T, false>(a.gamma_pre, (n0 + in + i * G) * E, a.N, f32, 1.0f, pre[i]);
-      if (kRowGate || !gated) load_weights<T, false>(a.gamma_post, (n0 + in + i * G) * E, a.N, f32, 1.0f, q[i]);
-    }
-  int64_t gate_end = gated && !kRowGate ? begin : INT64_MAX;  // the row from which on another gate row holds
-  int64_t ahead = begin + ring.stages;  // the row to copy next
-  bool refill = false;
-  auto rstd_of = [&](float2 s2) {
-    float s[1] = {sums.one(s2.x + s2.y)};
-    if (refill && ahead < end) issue(ahead++);
-    refill = false;
-    share(s);
-    return rsqrtf(fmaf(s[0], inv_n, a.eps));
-  };
-  T *h = static_cast<T*>(a.h) + begin * a.N + (n0 + in) * E, *y = static_cast<T*>(a.y) + begin * a.N + (n0 + in) * E;
-  for (int64_t r = begin; r < end; ++r, h += a.N, y += a.N) {
-    if (kShared && static_cast<uint64_t>(r) >= static_cast<uint64_t>(stall.at)) share.silence();
-    const unsigned char* stage = ring.next();
-    refill = first && r > begin;  // behind the row's first sum the group has read the row before
-    if (!kRowGate && r >= gate_end) {
-      const int64_t g = static_cast<uint32_t>(r) / per_gate;
-      gate_end = (g + 1) * per_gate;
-      const char* gate = static_cast<const char*>(a.gate) + g * a.N * (gate32 ? 4 : sizeof(T));
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (in + i * G >= mine) continue;
-        float2 post[P];
-        load_weights<T, false>(gate, (n0 + in + i * G) * E, a.N, gate32, 1.0f, q[i]);
-        load_weights<T, false>(a.gamma_post, (n0 + in + i * G) * E, a.N, f32, 1.0f, post);
-#pragma unroll
-        for (int e = 0; e < P; ++e) q[i][e] = __fmul2_rn(q[i][e], post[e]);
-      }
-    }
-    Raw w[R];
-    float2 s2 = pair(0.0f);
-    float ru = 1.0f, rh = 0.0f;
-    if (post_norm) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (in + i * G >= mine) continue;
-        const Raw u = ld_stage(stage + (in + i * G) * 16);
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const float2 v = get_pair<T>(u, e);
-          s2 = __ffma2_rn(v, v, s2);
-        }
-      }
-      ru = rstd_of(s2);
-      s2 = pair(0.0f);
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (in + i * G >= mine) continue;
-      w[i] = ld_stage(stage + (in + i * G) * 16);
-      Raw res = {};
-      if (add) res = ld_stage(stage + (R * G + in + i * G) * 16);
-      float2 gate[P];
-      if constexpr (kRowGate) stage_pairs<T>(stage + 2 * R * G * 16, in + i * G, gate32, gate);
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        float2 v = get_pair<T>(w[i], e);
-        if (post_norm || gated) {
-          v = __fmul2_rn(v, __fmul2_rn(pair(ru), q[i][e]));
-          if constexpr (kRowGate) v = __fmul2_rn(v, gate[e]);
-        }
-        if (add) v = __ffma2_rn(alpha, get_pair<T>(res, e), v);
-        set_pair<T>(w[i], e, v);  // h as it is stored
-        v = get_pair<T>(w[i], e);
-        s2 = __ffma2_rn(v, v, s2);
-      }
-      if (kFull || a.h != nullptr) st_raw(h + i * G * E, w[i]);
-    }
-    if (pre_norm) {
-      rh = rstd_of(s2);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (in + i * G >= mine) continue;
-#pragma unroll
-        for (int e = 0; e < P; ++e)
-          set_pair<T>(w[i], e, __fmul2_rn(get_pair<T>(w[i], e), __fmul2_rn(pair(rh), pre[i][e])));
-        st_raw(y + i * G * E, w[i]);
-      }
-    }
-    if (in + n0 == 0) {
-      a.stats[2 * r] = post_norm ? ru : 0.0f;
-      a.stats[2 * r + 1] = rh;
-    }
-  }
-  if (first) ring.end(status);
-  else if (ring.wait.lost() && status != nullptr) atomicOr(status, kStatusTimeout);
-  share.end(status);
-}
+using namespace bn;
 
 // ---- backward: a row in the registers of a group of threads, one vector of each tensor a thread
 // A group takes chunks of rows, chunk after chunk, and writes the chunk's two column sums. kShared: as in the forward.
@@ -686,7 +210,7 @@ __global__ void __launch_bounds__(kMaxGroup)
 // Backward over a ring, R vectors of a row a thread. The gate row is the chunk's own (kRowGate: one more tensor in the
 // ring), so that its columns and gamma_post's are one factor in registers.
 constexpr int kBwdBlock = 256, kBwdBlocks = 2;  // threads of a block, at most, and such blocks an SM
-template <typename T, int R, bool kShared, bool kRowGate, bool kFull>
+template <typename T, int R, bool kShared, bool kRowGate, bool kFull, bool kRagged>
 __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
     bn_bwd_ring_kernel(const BnBwdArgs a, const BnChunks k, const RingPlan plan, int G, int S, Stall stall,
                        uint32_t* status) {
@@ -700,13 +224,12 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
   const int rank = kShared ? static_cast<int>(cluster_ctarank()) : 0, in = kShared ? threadIdx.x : threadIdx.x % G;
   const uint32_t units = (kShared ? gridDim.x / S : gridDim.x) * groups;
   const uint32_t unit = kShared ? blockIdx.x / S : blockIdx.x * groups + group;
-  const int n = static_cast<int>(a.N) / E, n0 = rank * R * G, mine = min(R * G, n - n0);
+  const int N = static_cast<int>(a.N), n0 = rank * R * G;
   const bool first = in == 0;
   const float inv_n = 1.0f / static_cast<float>(a.N);
   const bool post_norm = kFull || a.post, pre_norm = kFull || a.pre, add = kFull || a.dh != nullptr;
   const bool f32 = a.wdtype == 0, gate32 = a.gdtype == 0, dgate_rows = kRowGate && a.dgate != nullptr;
-  auto column = [&](int i) { return (n0 + in + i * G) * E; };
-  Ring<kTensors> ring(dyn, bars, plan, group, stall);
+  RowRing<kTensors, kRagged> ring(dyn, bars, plan, group, stall);
   if (first) {
     ring.init();
     fence_mbar_init();
@@ -715,76 +238,101 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
   WarpRows sums(smem, G);
   std::conditional_t<kShared, ClusterSum3, NoSum3> share(slots, S, stall);
   const int64_t stop_at = kShared ? -1 : stall.at;
-  // the rows of the group's chunks in turn: chunk c, rows r .. end - 1
-  struct Walk {  // 32 bits hold them: at most as many chunks as rows
-    uint32_t c, r, end;
-  };
+  // the rows of the group's chunks in turn: of chunk c r, r + apart, ... below end
   const uint32_t chunks = static_cast<uint32_t>(k.chunks), per_segment = static_cast<uint32_t>(k.per_segment);
   const uint32_t segment = static_cast<uint32_t>(k.segment), chunk_rows = static_cast<uint32_t>(k.rows);
-  auto enter = [&](Walk& w) {
-    const uint32_t seg = w.c / per_segment;
-    w.r = seg * segment + (w.c - seg * per_segment) * chunk_rows;
-    w.end = min((seg + 1) * segment, w.r + chunk_rows);
+  const uint32_t apart = kRagged ? static_cast<uint32_t>(k.apart) : 1u;
+  struct Walk {  // 32 bits hold them
+    uint32_t c, r, end;
+    int shift, n, mine;  // elements from the 16-byte boundary before a row, its vectors, and this block's
   };
-  Walk ahead{unit, 0, 0};
-  if (ahead.c < chunks) enter(ahead);
+  auto enter = [&](Walk& w) {
+    const uint32_t seg = w.c / per_segment, in_seg = w.c - seg * per_segment;
+    const uint32_t block = kRagged ? in_seg / apart : in_seg, phase = kRagged ? in_seg - block * apart : 0u;
+    w.r = seg * segment + phase + block * chunk_rows * apart;
+    w.end = min((seg + 1) * segment, w.r + chunk_rows * apart);
+    w.shift = kRagged ? shift_of(static_cast<const T*>(a.du) + static_cast<int64_t>(w.r) * a.N) : 0;
+    w.n = (N + w.shift + E - 1) / E;
+    w.mine = min(R * G, w.n - n0);
+  };
+  // a walk behind its chunk's last row goes on to the next chunk that has rows (a phase of ragged rows may have none)
+  auto settle = [&](Walk& w) {
+    while (w.c < chunks && w.r >= w.end) {
+      w.c += units;
+      if (w.c < chunks) enter(w);
+    }
+  };
+  Walk ahead{unit, 0, 0, 0, 0, 0};
+  if (ahead.c < chunks) {
+    enter(ahead);
+    if (kRagged) settle(ahead);
+  }
   auto issue = [&]() {
     if (ahead.c >= chunks) return;
     const int64_t r = ahead.r;
     const void* from[kTensors];
     uint32_t bytes[kTensors];
-    from[0] = static_cast<const T*>(a.u) + r * a.ldu + n0 * E;
-    from[1] = pre_norm ? static_cast<const T*>(a.h) + r * a.ldh + n0 * E : nullptr;
-    from[2] = pre_norm ? static_cast<const T*>(a.dy) + r * a.lddy + n0 * E : nullptr;
-    from[3] = add ? static_cast<const T*>(a.dh) + r * a.lddh + n0 * E : nullptr;
+    const Span span = kRagged ? span_of(r, a.M, ahead.n, n0, ahead.mine, ahead.shift, ahead.n * E - ahead.shift - N)
+                              : Span{0, ahead.mine};
+    const int j0 = (n0 + span.first) * E - ahead.shift;  // the first column that is copied
+    from[0] = static_cast<const T*>(a.u) + r * a.ldu + j0;
+    from[1] = pre_norm ? static_cast<const T*>(a.h) + r * a.ldh + j0 : nullptr;
+    from[2] = pre_norm ? static_cast<const T*>(a.dy) + r * a.lddy + j0 : nullptr;
+    from[3] = add ? static_cast<const T*>(a.dh) + r * a.lddh + j0 : nullptr;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bytes[i] = static_cast<uint32_t>(mine) * 16u;
+    for (int i = 0; i < 4; ++i) bytes[i] = static_cast<uint32_t>(span.count) * 16u;
     if constexpr (kRowGate) {
       const int64_t es = gate32 ? 4 : sizeof(T);
-      from[4] = static_cast<const char*>(a.gate) + (r * a.N + n0 * E) * es;
-      bytes[4] = static_cast<uint32_t>(mine) * static_cast<uint32_t>(E * es);
+      from[4] = static_cast<const char*>(a.gate) + (r * a.N + j0) * es;
+      bytes[4] = static_cast<uint32_t>(span.count) * static_cast<uint32_t>(E * es);
     }
-    ring.issue(from, bytes, R * G * 16, stop_at);
-    if (++ahead.r == ahead.end) {
-      ahead.c += units;
-      if (ahead.c < chunks) enter(ahead);
-    }
+    ring.issue(from, bytes, R * G * 16, stop_at, span.first * 16);
+    ahead.r += apart;
+    settle(ahead);
   };
   if (first)
     for (int i = 0; i < ring.stages; ++i) issue();
+  Walk w{unit, 0, 0, 0, 0, 0};
+  if (w.c < chunks) enter(w);
+  auto column = [&](int i) { return (n0 + in + i * G) * E - w.shift; };
   float2 pre[R][P], post[R][P];  // gamma_pre; gamma_post, without kRowGate times the gate
+  if (!kRagged) {
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (in + i * G < mine) load_weights<T, false>(a.gamma_pre, column(i), a.N, f32, 1.0f, pre[i]);
+    for (int i = 0; i < R; ++i)
+      if (in + i * G < w.mine) load_weights<T, false>(a.gamma_pre, column(i), N, f32, 1.0f, pre[i]);
+  }
   bool refill = false;
   struct Vectors {  // a thread's vector of each tensor, from the stage
     Raw u, h, dy, dh;
   };
-  auto vectors = [&](const unsigned char* stage, int i) {
+  const Rows<T> rows_u(a.u, a.ldu, a.M, a.N), rows_h(a.h, a.ldh, a.M, a.N), rows_y(a.dy, a.lddy, a.M, a.N);
+  const Rows<T> rows_d(a.dh, a.lddh, a.M, a.N), rows_g(a.gate, a.N, a.M, a.N);
+  auto place_of = [&](unsigned char* stage, int tensor, int i) { return stage + (tensor * R * G + in + i * G) * 16; };
+  auto vectors = [&](unsigned char* stage, int i) {
     Vectors v = {};
-    const unsigned char* p = stage + (in + i * G) * 16;
-    v.u = ld_stage(p);
+    v.u = ld_stage(place_of(stage, 0, i));
     if (pre_norm) {
-      v.h = ld_stage(p + R * G * 16);
-      v.dy = ld_stage(p + 2 * R * G * 16);
+      v.h = ld_stage(place_of(stage, 1, i));
+      v.dy = ld_stage(place_of(stage, 2, i));
     }
-    if (add) v.dh = ld_stage(p + 3 * R * G * 16);
+    if (add) v.dh = ld_stage(place_of(stage, 3, i));
     return v;
   };
-  for (Walk w{unit, 0, 0}; w.c < chunks; w.c += units) {
+  for (; w.c < chunks; w.c += units) {
     enter(w);
     float2 ss[R][P], sp[R][P];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int e = 0; e < P; ++e) ss[i][e] = sp[i][e] = pair(0.0f);
-      if (in + i * G >= mine) continue;
-      load_weights<T, false>(a.gamma_post, column(i), a.N, f32, 1.0f, post[i]);
+      if (in + i * G >= w.mine) continue;
+      if (kRagged) load_weights<T, kRagged>(a.gamma_pre, column(i), N, f32, 1.0f, pre[i]);
+      load_weights<T, kRagged>(a.gamma_post, column(i), N, f32, 1.0f, post[i]);
       if (!kRowGate && a.gate != nullptr) {
         float2 g[P];
         const int64_t row = static_cast<uint32_t>(w.r) / static_cast<uint32_t>(a.rows_per_gate);
-        load_weights<T, false>(static_cast<const char*>(a.gate) + row * a.N * (gate32 ? 4 : sizeof(T)), column(i), a.N,
-                               gate32, 1.0f, g);
+        load_weights<T, kRagged>(static_cast<const char*>(a.gate) + row * a.N * (gate32 ? 4 : sizeof(T)), column(i), N,
+                                 gate32, 1.0f, g);
 #pragma unroll
         for (int e = 0; e < P; ++e) post[i][e] = __fmul2_rn(g[e], post[i][e]);
       }
@@ -793,22 +341,37 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
       const float* p = a.stats + 2 * static_cast<int64_t>(r);
       return make_float2(p[0], p[1]);
     };
-    float2 stats = rstds(w.r);
-    int64_t at = static_cast<int64_t>(w.r) * a.N + column(0);
-    for (uint32_t r = w.r; r < w.end; ++r) {
+    float2 stats = make_float2(0.0f, 0.0f);
+    if (!kRagged || w.r < w.end) stats = rstds(w.r);
+    int64_t at = static_cast<int64_t>(w.r) * a.N;  // the row's
+    for (uint32_t r = w.r; r < w.end; r += apart, at += static_cast<int64_t>(apart) * a.N) {
       if (kShared && static_cast<uint64_t>(r) >= static_cast<uint64_t>(stall.at)) share.silence();
       const float fu = post_norm ? stats.x : 1.0f, fh = pre_norm ? stats.y : 0.0f;
-      if (r + 1 < w.end) stats = rstds(r + 1);
-      const unsigned char* stage = ring.next();
+      if (r + apart < w.end) stats = rstds(r + apart);
+      unsigned char* stage = ring.next();
+      if constexpr (kRagged) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int j = column(i);
+          if (in + i * G >= w.mine || (j >= 0 && j + E <= N)) continue;
+          mend_edge(place_of(stage, 0, i), rows_u, r, a.M, j, N);
+          if (pre_norm) {
+            mend_edge(place_of(stage, 1, i), rows_h, r, a.M, j, N);
+            mend_edge(place_of(stage, 2, i), rows_y, r, a.M, j, N);
+          }
+          if (add) mend_edge(place_of(stage, 3, i), rows_d, r, a.M, j, N);
+          if (kRowGate) mend_edge(place_of(stage, 4, i), rows_g, r, a.M, j, N);
+        }
+      }
       const float2 rh = pair(fh);
       // sums of dy gamma_pre h, of q u (dh + rstd(h) dy gamma_pre) and of q u h: the rows' factors come behind them
       float2 s0 = pair(0.0f), s1 = s0, s2 = s0;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        if (in + i * G >= mine) continue;
+        if (in + i * G >= w.mine) continue;
         const Vectors v = vectors(stage, i);
         float2 q[P];
-        if constexpr (kRowGate) stage_pairs<T>(stage + 4 * R * G * 16, in + i * G, gate32, q);
+        if constexpr (kRowGate) stage_pairs<T>(stage + 4 * R * G * 16, in + i * G, !kRagged && gate32, q);
 #pragma unroll
         for (int e = 0; e < P; ++e) {
           const float2 h = get_pair<T>(v.h, e), dy = get_pair<T>(v.dy, e), x = __fmul2_rn(dy, h);
@@ -831,10 +394,10 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
       const float2 c2 = pair(post_norm ? -fmaf(-m1 * fh, s[2], s[1]) * fu * inv_n : 0.0f);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        if (in + i * G >= mine) continue;
+        if (in + i * G >= w.mine) continue;
         Vectors x = vectors(stage, i);
         float2 q[P];
-        if constexpr (kRowGate) stage_pairs<T>(stage + 4 * R * G * 16, in + i * G, gate32, q);
+        if constexpr (kRowGate) stage_pairs<T>(stage + 4 * R * G * 16, in + i * G, !kRagged && gate32, q);
         Raw dg;
 #pragma unroll
         for (int e = 0; e < P; ++e) {
@@ -847,7 +410,7 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
             ss[i][e] = __ffma2_rn(du_hat, q[e], ss[i][e]);
             qd = __fmul2_rn(q[e], qd);
             const float2 v = __fmul2_rn(du_hat, post[i][e]);
-            if (gate32 && dgate_rows) *reinterpret_cast<float2*>(static_cast<float*>(a.dgate) + (at + i * G * E) + 2 * e) = v;
+            if (!kRagged && sizeof(T) == 2 && gate32 && dgate_rows) *reinterpret_cast<float2*>(static_cast<float*>(a.dgate) + at + column(i) + 2 * e) = v;
             else set_pair<T>(dg, e, v);
           } else {
             ss[i][e] = __ffma2_rn(d, uh, ss[i][e]);
@@ -856,21 +419,33 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
           const float2 v = __ffma2_rn(uh, c2, qd);
           set_pair<T>(x.u, e, post_norm ? __fmul2_rn(ru, v) : v);
         }
-        st_raw(static_cast<T*>(a.du) + at + i * G * E, x.u);
-        if (kFull || a.dres != nullptr) st_raw(static_cast<T*>(a.dres) + at + i * G * E, x.dh);
-        if (dgate_rows && !gate32) st_raw(static_cast<T*>(a.dgate) + at + i * G * E, dg);
+        store_vector<T, kRagged>(static_cast<T*>(a.du) + at, column(i), N, x.u);
+        if (kFull || a.dres != nullptr) store_vector<T, kRagged>(static_cast<T*>(a.dres) + at, column(i), N, x.dh);
+        if (dgate_rows && (sizeof(T) == 4 || !gate32))
+          store_vector<T, kRagged>(static_cast<T*>(a.dgate) + at, column(i), N, dg);
       }
-      at += a.N;
     }
     if (a.part == nullptr) continue;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (in + i * G >= mine) continue;
+      if (in + i * G >= w.mine) continue;
       float* to = a.part + static_cast<int64_t>(w.c) * 2 * a.N + column(i);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        *reinterpret_cast<float2*>(to + 2 * e) = ss[i][e];
-        *reinterpret_cast<float2*>(to + a.N + 2 * e) = sp[i][e];
+        if constexpr (!kRagged) {
+          *reinterpret_cast<float2*>(to + 2 * e) = ss[i][e];
+          *reinterpret_cast<float2*>(to + N + 2 * e) = sp[i][e];
+        } else {
+          const int j = column(i) + 2 * e;
+          if (j >= 0 && j < N) {
+            to[2 * e] = ss[i][e].x;
+            to[N + 2 * e] = sp[i][e].x;
+          }
+          if (j >= -1 && j + 1 < N) {
+            to[2 * e + 1] = ss[i][e].y;
+            to[N + 2 * e + 1] = sp[i][e].y;
+          }
+        }
       }
     }
   }
@@ -1080,16 +655,6 @@ __global__ void __launch_bounds__(32 * kReduceWarps)
 }
 
 // ---- host
-// Rows shared by a cluster: S blocks of G threads, R vectors each
-struct Shared {
-  int S, G;
-};
-Shared share_row(int64_t n, int R) {
-  const int64_t threads = (n + R - 1) / R;
-  const int S = static_cast<int>(threads <= kMaxCluster * kBlock ? (threads + kBlock - 1) / kBlock : kMaxCluster);
-  return Shared{S, static_cast<int>((threads + 32 * S - 1) / (32 * S)) * 32};
-}
-
 // Chunks of rows whose column sums are taken together: of one gate row where the gate has fewer rows than M, of at most
 // 128 rows (like terms are rounded the same way, and a longer chain drifts), and such that `units` groups that take
 // them in turn have nearly equal work: rows, and for each chunk the writing of its sums, about one row's.
@@ -1169,123 +734,6 @@ cudaError_t launch_reduce(const BnBwdArgs& a, const BnChunks& k, cudaStream_t st
 }
 
 template <typename T>
-cudaError_t fwd_long(const BnFwdArgs& a, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.M, 65536));
-  bn_fwd_long_kernel<T><<<grid, kMaxThreads, 0, stream>>>(a);
-  return cudaGetLastError();
-}
-// The ring of a group: as many rows of `row` bytes as fit beside one another in the memory of `blocks` blocks an SM,
-// `groups` groups each.
-constexpr int64_t kRingMemory = 220 * 1024;  // of an SM's 228 KB: what is static and 1 KB a block stay free
-RingPlan ring_plan(int64_t row, int blocks, int groups) {
-  const int64_t fit = kRingMemory / blocks / groups / row;
-  RingPlan p;
-  p.stages = static_cast<int>(std::min<int64_t>(kMaxStages, fit));
-  p.stage_bytes = static_cast<int>(row);
-  p.group_bytes = p.stages * p.stage_bytes;
-  return p;
-}
-// Rows from which on a group's ring pays: below, the first rows' copies cost more than loads (1 to 2 us).
-constexpr int64_t kRingRows = 4;
-
-// bytes of a row of a gate for each row, in those of the row itself
-template <typename T>
-int64_t gate_slots(int gdtype) {
-  return gdtype == 0 ? 4 / sizeof(T) : 1;
-}
-template <typename T, bool kRowGate, bool kFull>
-cudaError_t fwd_ring_one(const BnFwdArgs& a, int64_t n, cudaStream_t stream) {
-  const auto kernel = bn_fwd_ring_kernel<T, 2, false, kRowGate, kFull>;
-  const int G = group_threads(n, 2), groups = G < kBlock ? kBlock / G : 1, block = groups * G;
-  const RingPlan p = ring_plan((2 + (kRowGate ? gate_slots<T>(a.gdtype) : 0)) * 2 * G * 16,
-                               std::max(1, kFwdRingBlocks<kRowGate> * kBlock / block), groups);
-  const size_t smem = static_cast<size_t>(groups) * p.group_bytes;
-  int64_t blocks;
-  {
-    static std::mutex mu;
-    static FitCache cache;
-    std::lock_guard<std::mutex> lk(mu);
-    const cudaError_t e = blocks_that_fit(kernel, cache, block, smem, blocks);
-    if (e != cudaSuccess) return e;
-  }
-  blocks = std::min(blocks, (a.M + groups - 1) / groups);
-  kernel<<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, p, G, 1, take_stall(kInjectBlockNormFwd),
-                                                                status_word_ptr());
-  return cudaGetLastError();
-}
-template <typename T, bool kRowGate, bool kFull>
-cudaError_t fwd_ring_shared(const BnFwdArgs& a, int64_t n, cudaStream_t stream) {
-  const auto kernel = bn_fwd_ring_kernel<T, 2, true, kRowGate, kFull>;
-  const Shared s = share_row(n, 2);
-  const RingPlan p = ring_plan((2 + (kRowGate ? gate_slots<T>(a.gdtype) : 0)) * 2 * s.G * 16,
-                               std::max(1, kFwdRingBlocks<kRowGate> * kBlock / s.G), 1);
-  static std::mutex mu;
-  static StreamCache cache;
-  std::lock_guard<std::mutex> lk(mu);
-  const cudaError_t e = clusters_that_fit(kernel, cache, s.G, p.group_bytes, s.S);
-  if (e != cudaSuccess) return e;
-  if (cache.clusters < 1) return fwd_long<T>(a, stream);
-  ClusterLaunch l(s.G, p.group_bytes, s.S, std::min<int64_t>(cache.clusters, a.M), stream);
-  return cudaLaunchKernelEx(&l.cfg, kernel, a, p, s.G, s.S, take_stall(kInjectBlockNormFwd), status_word_ptr());
-}
-
-template <typename T, bool kRowGate, bool kFull>
-cudaError_t fwd_ring(const BnFwdArgs& a, int64_t n, cudaStream_t stream) {
-  return n <= 2 * kBlock ? fwd_ring_one<T, kRowGate, kFull>(a, n, stream)
-                         : fwd_ring_shared<T, kRowGate, kFull>(a, n, stream);
-}
-template <typename T, int R, bool kRagged>
-cudaError_t fwd_one(const BnFwdArgs& a, int64_t n, cudaStream_t stream) {
-  const int G = group_threads(n, R), groups = G < kBlock ? kBlock / G : 1, block = groups * G;
-  int64_t blocks;
-  {
-    static std::mutex mu;
-    static FitCache cache;
-    std::lock_guard<std::mutex> lk(mu);
-    const cudaError_t e = blocks_that_fit(bn_fwd_kernel<T, R, kRagged, false>, cache, block, 0, blocks);
-    if (e != cudaSuccess) return e;
-  }
-  blocks = persistent_blocks(blocks, (a.M + groups - 1) / groups, kRagged ? rows_apart<T>(a.N) : 1);
-  if (blocks == 0) return fwd_long<T>(a, stream);
-  bn_fwd_kernel<T, R, kRagged, false><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a, G, 1, Stall(), nullptr);
-  return cudaGetLastError();
-}
-template <typename T, bool kRagged>
-cudaError_t fwd_shared(const BnFwdArgs& a, int64_t n, cudaStream_t stream) {
-  static std::mutex mu;
-  static StreamCache cache;
-  std::lock_guard<std::mutex> lk(mu);
-  const Shared p = share_row(n, 2);
-  const auto kernel = bn_fwd_kernel<T, 2, kRagged, true>;
-  const cudaError_t e = clusters_that_fit(kernel, cache, p.G, 0, p.S);
-  if (e != cudaSuccess) return e;
-  const int64_t clusters = persistent_blocks(cache.clusters, a.M, kRagged ? rows_apart<T>(a.N) : 1);
-  if (clusters == 0) return fwd_long<T>(a, stream);
-  ClusterLaunch l(p.G, 0, p.S, clusters, stream);
-  return cudaLaunchKernelEx(&l.cfg, kernel, a, p.G, p.S, take_stall(kInjectBlockNormFwd), status_word_ptr());
-}
-template <typename T, bool kRagged>
-cudaError_t fwd_any(const BnFwdArgs& a, cudaStream_t stream) {
-  const int64_t n = (a.N + (kRagged ? 2 * kElems<T> - 2 : 0)) / kElems<T>;
-  if (n <= 32) return fwd_one<T, 1, kRagged>(a, n, stream);
-  if (!kRagged && n <= 2 * kMaxCluster * kBlock) {
-    if (a.M * ((n + 1) / 2) >= kRingRows * kFwdBlocks * kBlock * device_sm_count()) {
-      const bool row_gate = a.gate != nullptr && a.rows_per_gate == 1, full = a.post && a.pre && a.residual != nullptr;
-      if (row_gate) return full ? fwd_ring<T, true, true>(a, n, stream) : fwd_ring<T, true, false>(a, n, stream);
-      return full ? fwd_ring<T, false, true>(a, n, stream) : fwd_ring<T, false, false>(a, n, stream);
-    }
-  }
-  if (n <= 2 * kMaxGroup) return fwd_one<T, 2, kRagged>(a, n, stream);
-  if (n <= 2 * kMaxCluster * kMaxGroup) return fwd_shared<T, kRagged>(a, n, stream);
-  return fwd_long<T>(a, stream);
-}
-template <typename T>
-cudaError_t fwd_type(const BnFwdArgs& a, cudaStream_t stream) {
-  const bool whole = whole_vectors(a.N, sizeof(T), {a.u, a.residual, a.h, a.y}, {a.ldu, a.ldr},
-                                   {a.gamma_post, a.gamma_pre, a.gate});
-  return whole ? fwd_any<T, false>(a, stream) : fwd_any<T, true>(a, stream);
-}
-template <typename T>
 cudaError_t bwd_long(const BnBwdArgs& a, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.M, 65536));
   bn_dx_long_kernel<T><<<grid, kMaxThreads, 0, stream>>>(a);
@@ -1343,9 +791,9 @@ cudaError_t bwd_shared(const BnBwdArgs& a, int64_t n, cudaStream_t stream) {
   }
   return a.part == nullptr ? cudaSuccess : launch_reduce(a, k, stream);
 }
-template <typename T, bool kRowGate, bool kFull>
+template <typename T, bool kRowGate, bool kFull, bool kRagged>
 cudaError_t bwd_ring_one(const BnBwdArgs& a, const BnChunks& k, int64_t n, cudaStream_t stream) {
-  const auto kernel = bn_bwd_ring_kernel<T, 2, false, kRowGate, kFull>;
+  const auto kernel = bn_bwd_ring_kernel<T, 2, false, kRowGate, kFull, kRagged>;
   const int G = group_threads(n, 2), groups = kBwdBlock / G, block = groups * G;
   const RingPlan p = ring_plan((4 + (kRowGate ? gate_slots<T>(a.gdtype) : 0)) * 2 * G * 16,
                                std::max(kBwdBlocks, kBwdBlocks * kBwdBlock / block), groups);
@@ -1363,9 +811,9 @@ cudaError_t bwd_ring_one(const BnBwdArgs& a, const BnChunks& k, int64_t n, cudaS
                                                                 status_word_ptr());
   return cudaGetLastError();
 }
-template <typename T, bool kRowGate, bool kFull>
+template <typename T, bool kRowGate, bool kFull, bool kRagged>
 cudaError_t bwd_ring_shared(const BnBwdArgs& a, const BnChunks& k, int64_t n, cudaStream_t stream) {
-  const auto kernel = bn_bwd_ring_kernel<T, 2, true, kRowGate, kFull>;
+  const auto kernel = bn_bwd_ring_kernel<T, 2, true, kRowGate, kFull, kRagged>;
   const Shared s = share_row(n, 2);
   const RingPlan p = ring_plan((4 + (kRowGate ? gate_slots<T>(a.gdtype) : 0)) * 2 * s.G * 16,
                                std::max(kBwdBlocks, kBwdBlocks * kBwdBlock / s.G), 1);
@@ -1378,23 +826,31 @@ cudaError_t bwd_ring_shared(const BnBwdArgs& a, const BnChunks& k, int64_t n, cu
   ClusterLaunch l(s.G, p.group_bytes, s.S, std::min<int64_t>(cache.clusters, k.chunks), stream);
   return cudaLaunchKernelEx(&l.cfg, kernel, a, k, p, s.G, s.S, take_stall(kInjectBlockNormBwd), status_word_ptr());
 }
-template <typename T, bool kRowGate, bool kFull>
+template <typename T, bool kRowGate, bool kFull, bool kRagged>
 cudaError_t bwd_ring(const BnBwdArgs& a, const BnChunks& k, int64_t n, cudaStream_t stream) {
-  const cudaError_t e = n <= 2 * kBwdBlock ? bwd_ring_one<T, kRowGate, kFull>(a, k, n, stream)
-                                           : bwd_ring_shared<T, kRowGate, kFull>(a, k, n, stream);
+  const cudaError_t e = n <= 2 * kBwdBlock ? bwd_ring_one<T, kRowGate, kFull, kRagged>(a, k, n, stream)
+                                           : bwd_ring_shared<T, kRowGate, kFull, kRagged>(a, k, n, stream);
   return e != cudaSuccess || a.part == nullptr ? e : launch_reduce(a, k, stream);
 }
 template <typename T, bool kRagged>
 cudaError_t bwd_any(const BnBwdArgs& a, cudaStream_t stream) {
   const int64_t n = (a.N + (kRagged ? 2 * kElems<T> - 2 : 0)) / kElems<T>;
-  if (!kRagged && n > 32 && n <= 2 * kMaxCluster * kBwdBlock) {
-    const int64_t units = ring_units(n);
-    if (a.M >= kRingRows * units) {
-      const BnChunks k = chunks_of(a.M, a.rows_per_gate, units, 1);
-      const bool row_gate = a.gate != nullptr && a.rows_per_gate == 1;
+  const bool row_gate = a.gate != nullptr && a.rows_per_gate == 1;
+  const bool ring = !kRagged || (same_offsets(a.M, a.N, sizeof(T), a.du,
+                                              {a.u, a.h, a.dy, a.dh, a.dres, row_gate ? a.gate : nullptr,
+                                               row_gate ? a.dgate : nullptr},
+                                              {a.ldu, a.pre ? a.ldh : a.N, a.pre ? a.lddy : a.N,
+                                               a.dh != nullptr ? a.lddh : a.N}) &&
+                                 (!row_gate || sizeof(T) == 4 || a.gdtype != 0));
+  const int64_t units = ring_units(n);
+  if (ring && n > 32 && n <= 2 * kMaxCluster * kBwdBlock && a.M >= kRingRows * units) {
+    const BnChunks k = chunks_of(a.M, a.rows_per_gate, units, kRagged ? rows_apart<T>(a.N) : 1);
+    if constexpr (kRagged) {
+      return row_gate ? bwd_ring<T, true, false, true>(a, k, n, stream) : bwd_ring<T, false, false, true>(a, k, n, stream);
+    } else {
       const bool full = a.post && a.pre && a.dh != nullptr && a.dres != nullptr;
-      if (row_gate) return full ? bwd_ring<T, true, true>(a, k, n, stream) : bwd_ring<T, true, false>(a, k, n, stream);
-      return full ? bwd_ring<T, false, true>(a, k, n, stream) : bwd_ring<T, false, false>(a, k, n, stream);
+      if (row_gate) return full ? bwd_ring<T, true, true, false>(a, k, n, stream) : bwd_ring<T, true, false, false>(a, k, n, stream);
+      return full ? bwd_ring<T, false, true, false>(a, k, n, stream) : bwd_ring<T, false, false, false>(a, k, n, stream);
     }
   }
   if (n <= 16) return bwd_groups<T, kRagged, true>(a, n, stream);
@@ -1416,7 +872,7 @@ int64_t most_chunks(int64_t M, int64_t N, int64_t rows_per_gate) {
     for (const int64_t ragged : {0, 1}) {
       const int64_t n = (N + (ragged ? 2 * e - 2 : e - 1)) / e, apart = ragged ? e / std::gcd(N, e) : 1;
       most = std::max(most, chunks_of(M, rows_per_gate, units_of(n), apart).chunks);
-      if (!ragged) most = std::max(most, chunks_of(M, rows_per_gate, ring_units(n), 1).chunks);
+      most = std::max(most, chunks_of(M, rows_per_gate, ring_units(n), apart).chunks);
     }
   }
   return most;
@@ -1426,12 +882,6 @@ int64_t most_chunks(int64_t M, int64_t N, int64_t rows_per_gate) {
 
 size_t bn_workspace_bytes(int64_t M, int64_t N, int64_t rows_per_gate) {
   return (static_cast<size_t>(most_chunks(M, N, rows_per_gate)) * 2 * N + M) * sizeof(float);
-}
-
-cudaError_t launch_block_norm_fwd(const BnFwdArgs& a, int dtype, cudaStream_t stream) {
-  return dtype == 0   ? fwd_type<float>(a, stream)
-         : dtype == 1 ? fwd_type<__half>(a, stream)
-                      : fwd_type<__nv_bfloat16>(a, stream);
 }
 
 cudaError_t launch_block_norm_bwd(const BnBwdArgs& given, void* workspace, int dtype, cudaStream_t stream) {

@@ -290,7 +290,7 @@ SplitPlan split_cost(int64_t L, int64_t C, int64_t R, int NT, int S, int per_sm,
   return p;
 }
 // The cheapest of the tiles that cover C evenly and of the cluster sizes.
-SplitPlan split_plan(int64_t L, int64_t C, int64_t R, bool b_outer, int sms) {
+SplitPlan split_search(int64_t L, int64_t C, int64_t R, bool b_outer, int sms) {
   const int unit = b_outer ? 64 : 16;
   const int64_t nkb = (R + kRed - 1) / kRed, least = (C + 255) / 256;
   SplitPlan best;
@@ -309,6 +309,31 @@ SplitPlan split_plan(int64_t L, int64_t C, int64_t R, bool b_outer, int sms) {
     }
   }
   return best;
+}
+
+// The same, remembered for the sizes that a thread used last (a search takes some 8 us of the host, as much as a small
+// product): a function of the sizes alone.
+SplitPlan split_plan(int64_t L, int64_t C, int64_t R, bool b_outer, int sms) {
+  struct Entry {
+    int64_t L = -1, C, R;
+    int sms;
+    bool b_outer;
+    SplitPlan plan;
+  };
+  constexpr uint64_t kEntries = 64;
+  static thread_local Entry entries[kEntries];
+  const uint64_t h = (static_cast<uint64_t>(L) * 0x9e3779b97f4a7c15ull ^ static_cast<uint64_t>(C) * 0xc2b2ae3d27d4eb4full ^
+                      static_cast<uint64_t>(R) * 0x165667b19e3779f9ull) + (b_outer ? 1u : 0u);
+  Entry& e = entries[(h ^ (h >> 32)) % kEntries];
+  if (e.L != L || e.C != C || e.R != R || e.sms != sms || e.b_outer != b_outer) {
+    e.plan = split_search(L, C, R, b_outer, sms);
+    e.L = L;
+    e.C = C;
+    e.R = R;
+    e.sms = sms;
+    e.b_outer = b_outer;
+  }
+  return e.plan;
 }
 
 template <bool kAOuter, bool kBOuter, bool kF16>

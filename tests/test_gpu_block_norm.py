@@ -174,6 +174,47 @@ def test_ring_parts(residual, post, pre, dh, gates):
     _run(2400, 8192, F16, F32, gates, residual=residual, post=post, pre=pre, dh=dh)
 
 
+# ragged rows take the ring where all tensors' rows lie on the same offsets within 16 bytes
+@pytest.mark.parametrize("M,N,dtype", [(20011, 265, BF16), (40000, 133, F32), (9001, 515, F16), (2003, 4001, BF16), (1200, 2047, F32),
+                                       (1801, 8190, F16), (700, 12289, BF16), (640, 10001, F32), (301, 32700, BF16)])
+@pytest.mark.parametrize("gates", ["none", "some", "rows"])
+def test_ragged_ring(M, N, dtype, gates):
+    divisor = next(d for d in (7, 5, 3, 2, 1) if M % d == 0)
+    G = {"none": 0, "some": divisor, "rows": M}[gates]
+    _run(M, N, dtype, F32 if gates == "some" else dtype, G, dtype, alpha=0.9)
+
+
+@pytest.mark.parametrize("residual,post,pre,dh", [(False, True, True, True), (True, False, True, True), (True, True, False, True),
+                                                  (True, True, True, False), (False, False, True, False)])
+def test_ragged_ring_parts(residual, post, pre, dh):
+    for gates in (0, 4, 2400):
+        _run(2400, 4003, BF16, F32, gates, residual=residual, post=post, pre=pre, dh=dh)
+
+
+def test_ragged_ring_stays_inside():
+    # every tensor begins and ends inside 16 bytes, between others' bytes, which are NaN: nothing outside it is written
+    # and nothing of its neighbours enters
+    swg = _swg()
+    for M, N, dtype in ((2003, 4001, BF16), (1200, 2047, F32)):
+        t = norm_inputs(M, N, dtype, F32, M)
+        pad = {}
+        for k in ("u", "residual", "dy", "dh", "gate"):
+            pad[k] = guarded(t[k].shape, dtype, offset_elems=1)
+            pad[k].raw.fill_(0xFF)
+            pad[k].t.copy_(t[k])
+        kw = dict(gamma_post=t["gamma_post"], gamma_pre=t["gamma_pre"], gate=pad["gate"].t)
+        g = {k: guarded((M, N), dtype, offset_elems=1) for k in ("h", "y")}
+        out = swg.block_norm_fwd(pad["u"].t, pad["residual"].t, out={k: v.t for k, v in g.items()}, **kw)
+        check_all(g)
+        check_norm_fwd(t, out, dtype)
+        gb = {k: guarded((M, N), dtype, offset_elems=1) for k in ("du", "dresidual", "dgate")}
+        gb["ws"] = workspace(swg.block_norm_bwd_workspace_size(M, N, M))
+        got = swg.block_norm_bwd(pad["dy"].t, pad["dh"].t, pad["u"].t, out["h"], out["stats"], workspace=gb["ws"].t,
+                                 out={k: v.t for k, v in gb.items() if k != "ws"}, **kw)
+        check_all(gb)
+        check_norm_bwd(t, out["h"], out["stats"], got, dtype, F32, dtype)
+
+
 def test_ring_layouts():
     for layout in ("padded", "dense"):
         _run(2003, 4096, BF16, BF16, 1, layout=layout)
@@ -227,7 +268,7 @@ def test_rows_of_zeros_and_non_finite_rows():
 
 
 @pytest.mark.parametrize("M,N,dtype", [(300, 264, BF16), (300, 101, F32), (20, 9000, BF16), (3000, 4096, BF16),
-                                       (800, 12288, BF16)])
+                                       (800, 12288, BF16), (3000, 4001, BF16)])
 def test_same_bits_every_time(M, N, dtype):
     swg, t = _swg(), norm_inputs(M, N, dtype, F32, 4)
     kw = dict(gamma_post=t["gamma_post"], gamma_pre=t["gamma_pre"], gate=t["gate"])
