@@ -106,8 +106,8 @@ __device__ __forceinline__ void mend_edge(unsigned char* p, const Rows<T>& rows,
 }
 // an output's vector at column j; of a first or last one the row's elements
 template <typename T, bool kRagged>
-__device__ __forceinline__ void store_vector(T* row, int j, int N, const Raw& v) {
-  if (!kRagged || (j >= 0 && j + kElems<T> <= N)) {
+__device__ __forceinline__ void store_vector(T* row, int j, int N, bool edge, const Raw& v) {
+  if (!kRagged || !edge) {
     st_raw(row + j, v);
     return;
   }

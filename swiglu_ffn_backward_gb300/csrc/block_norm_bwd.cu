@@ -320,6 +320,9 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
   };
   for (; w.c < chunks; w.c += units) {
     enter(w);
+    bool edge[R];  // vectors that reach beyond the row
+#pragma unroll
+    for (int i = 0; i < R; ++i) edge[i] = kRagged && in + i * G < w.mine && (column(i) < 0 || column(i) + E > N);
     float2 ss[R][P], sp[R][P];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -352,8 +355,8 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
       if constexpr (kRagged) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+          if (!edge[i]) continue;
           const int j = column(i);
-          if (in + i * G >= w.mine || (j >= 0 && j + E <= N)) continue;
           mend_edge(place_of(stage, 0, i), rows_u, r, a.M, j, N);
           if (pre_norm) {
             mend_edge(place_of(stage, 1, i), rows_h, r, a.M, j, N);
@@ -419,10 +422,10 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
           const float2 v = __ffma2_rn(uh, c2, qd);
           set_pair<T>(x.u, e, post_norm ? __fmul2_rn(ru, v) : v);
         }
-        store_vector<T, kRagged>(static_cast<T*>(a.du) + at, column(i), N, x.u);
-        if (kFull || a.dres != nullptr) store_vector<T, kRagged>(static_cast<T*>(a.dres) + at, column(i), N, x.dh);
+        store_vector<T, kRagged>(static_cast<T*>(a.du) + at, column(i), N, edge[i], x.u);
+        if (kFull || a.dres != nullptr) store_vector<T, kRagged>(static_cast<T*>(a.dres) + at, column(i), N, edge[i], x.dh);
         if (dgate_rows && (sizeof(T) == 4 || !gate32))
-          store_vector<T, kRagged>(static_cast<T*>(a.dgate) + at, column(i), N, dg);
+          store_vector<T, kRagged>(static_cast<T*>(a.dgate) + at, column(i), N, edge[i], dg);
       }
     }
     if (a.part == nullptr) continue;
@@ -845,13 +848,10 @@ cudaError_t bwd_any(const BnBwdArgs& a, cudaStream_t stream) {
   const int64_t units = ring_units(n);
   if (ring && n > 32 && n <= 2 * kMaxCluster * kBwdBlock && a.M >= kRingRows * units) {
     const BnChunks k = chunks_of(a.M, a.rows_per_gate, units, kRagged ? rows_apart<T>(a.N) : 1);
-    if constexpr (kRagged) {
-      return row_gate ? bwd_ring<T, true, false, true>(a, k, n, stream) : bwd_ring<T, false, false, true>(a, k, n, stream);
-    } else {
-      const bool full = a.post && a.pre && a.dh != nullptr && a.dres != nullptr;
-      if (row_gate) return full ? bwd_ring<T, true, true, false>(a, k, n, stream) : bwd_ring<T, true, false, false>(a, k, n, stream);
-      return full ? bwd_ring<T, false, true, false>(a, k, n, stream) : bwd_ring<T, false, false, false>(a, k, n, stream);
-    }
+    const bool full = a.post && a.pre && a.dh != nullptr && a.dres != nullptr;
+    if (row_gate)
+      return full ? bwd_ring<T, true, true, kRagged>(a, k, n, stream) : bwd_ring<T, true, false, kRagged>(a, k, n, stream);
+    return full ? bwd_ring<T, false, true, kRagged>(a, k, n, stream) : bwd_ring<T, false, false, kRagged>(a, k, n, stream);
   }
   if (n <= 16) return bwd_groups<T, kRagged, true>(a, n, stream);
   if (n <= kMaxGroup) return bwd_groups<T, kRagged, false>(a, n, stream);

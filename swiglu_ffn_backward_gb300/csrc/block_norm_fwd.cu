@@ -280,6 +280,9 @@ __global__ void __maxnreg__(sizeof(T) == 4 ? 80 : 128)
   };
   T *h = static_cast<T*>(a.h) + begin * a.N, *y = static_cast<T*>(a.y) + begin * a.N;  // of the row
   const Rows<T> rows_u(a.u, a.ldu, a.M, a.N), rows_r(a.residual, a.ldr, a.M, a.N), rows_g(a.gate, a.N, a.M, a.N);
+  bool edge[R];  // vectors that reach beyond the row
+#pragma unroll
+  for (int i = 0; i < R; ++i) edge[i] = kRagged && in + i * G < mine && (column(i) < 0 || column(i) + E > N);
   auto place_of = [&](unsigned char* stage, int tensor, int i) { return stage + (tensor * R * G + in + i * G) * 16; };
   for (int64_t r = begin; r < end; r += step, h += step * a.N, y += step * a.N) {
     if (kShared && static_cast<uint64_t>(r) >= static_cast<uint64_t>(stall.at)) share.silence();
@@ -287,8 +290,8 @@ __global__ void __maxnreg__(sizeof(T) == 4 ? 80 : 128)
     if constexpr (kRagged) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
+        if (!edge[i]) continue;
         const int j = column(i);
-        if (in + i * G >= mine || (j >= 0 && j + E <= N)) continue;
         mend_edge(place_of(stage, 0, i), rows_u, r, a.M, j, N);
         if (add) mend_edge(place_of(stage, 1, i), rows_r, r, a.M, j, N);
         if (kRowGate) mend_edge(place_of(stage, 2, i), rows_g, r, a.M, j, N);
@@ -346,7 +349,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 ? 80 : 128)
         v = get_pair<T>(w[i], e);
         s2 = __ffma2_rn(v, v, s2);
       }
-      if (kFull || a.h != nullptr) store_vector<T, kRagged>(h, column(i), N, w[i]);
+      if (kFull || a.h != nullptr) store_vector<T, kRagged>(h, column(i), N, edge[i], w[i]);
     }
     if (pre_norm) {
       rh = rstd_of(s2);
@@ -356,7 +359,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 ? 80 : 128)
 #pragma unroll
         for (int e = 0; e < P; ++e)
           set_pair<T>(w[i], e, __fmul2_rn(get_pair<T>(w[i], e), __fmul2_rn(pair(rh), pre[i][e])));
-        store_vector<T, kRagged>(y, column(i), N, w[i]);
+        store_vector<T, kRagged>(y, column(i), N, edge[i], w[i]);
       }
     }
     if (in + n0 == 0) {
@@ -461,13 +464,10 @@ cudaError_t fwd_any(const BnFwdArgs& a, cudaStream_t stream) {
                                               {a.ldu, a.residual != nullptr ? a.ldr : a.N}) &&
                                  (!row_gate || sizeof(T) == 4 || a.gdtype != 0));
   if (ring && n <= 2 * kMaxCluster * kBlock && a.M * ((n + 1) / 2) >= kRingRows * kFwdBlocks * kBlock * device_sm_count()) {
-    if constexpr (kRagged) {
-      return row_gate ? fwd_ring<T, true, false, true>(a, n, stream) : fwd_ring<T, false, false, true>(a, n, stream);
-    } else {
-      const bool full = a.post && a.pre && a.residual != nullptr;
-      if (row_gate) return full ? fwd_ring<T, true, true, false>(a, n, stream) : fwd_ring<T, true, false, false>(a, n, stream);
-      return full ? fwd_ring<T, false, true, false>(a, n, stream) : fwd_ring<T, false, false, false>(a, n, stream);
-    }
+    const bool full = a.post && a.pre && a.residual != nullptr;
+    if (row_gate)
+      return full ? fwd_ring<T, true, true, kRagged>(a, n, stream) : fwd_ring<T, true, false, kRagged>(a, n, stream);
+    return full ? fwd_ring<T, false, true, kRagged>(a, n, stream) : fwd_ring<T, false, false, kRagged>(a, n, stream);
   }
   if (n <= 2 * kMaxGroup) return fwd_one<T, 2, kRagged>(a, n, stream);
   if (n <= 2 * kMaxCluster * kMaxGroup) return fwd_shared<T, kRagged>(a, n, stream);
