@@ -1068,10 +1068,11 @@ def linear_bwd(dy, x, w, z=None, act: str | None = None, bias: bool = True, need
         db_dtype = g.dtype
     K = 0 if K is None else K
     ws = None
-    if bias or need_dw or code != SWG_ACT_NONE:
-        ws = _workspace(lib.linear_bwd_workspace_size(M, K if K > 0 else 8, N, code), dev, workspace)
-        if workspace is not None:
-            _device_of(g, ws)
+    if workspace is not None:
+        _device_of(g, workspace)
+        ws = workspace
+    elif bias or need_dw or code != SWG_ACT_NONE:
+        ws = _workspace(lib.linear_bwd_workspace_size(M, K if K > 0 else 8, N, code), dev, None)
     _run("linear_bwd", lib.linear_bwd, dev, g.data_ptr(), _ptr(xt), _ptr(wt), _ptr(z), _ptr(need.get("dx")),
          _ptr(need.get("dw")), _ptr(need.get("db")), M, K, N, lddy, ldx, code, SWG_ACCUMULATE if accumulate else 0,
          _DTYPE[g.dtype], _DTYPE[db_dtype], _ptr(ws), _nbytes(ws))
@@ -1089,11 +1090,11 @@ def _gate_rows(gate, lead, M, N, x):
         return None, 0
     if not isinstance(gate, torch.Tensor) or not gate.is_cuda:
         raise TypeError("gate must be a CUDA tensor")
-    g = tuple(gate.shape[:-1])
+    g = gate.shape[:-1]
     while g and g[-1] == 1:
         g = g[:-1]
-    G = math.prod(g)
-    fits = g == tuple(lead[:len(g)]) or (len(g) == 1 and (G == M or len(lead) <= 1))
+    G = g[0] if len(g) == 1 else math.prod(g)
+    fits = g == lead[:len(g)] or (len(g) == 1 and (G == M or len(lead) <= 1))
     if (gate.dim() < 1 or gate.shape[-1] != N or gate.dtype not in (x.dtype, torch.float32) or not fits
             or (M > 0 and (G == 0 or M % G))):
         raise ValueError(f"gate must be [..., {N}] of {x.dtype} or torch.float32 with a row for equal runs of the rows "
@@ -1181,17 +1182,15 @@ def block_norm_bwd(dy, dh, u, h, stats, gamma_post=None, gamma_pre=None, gate=No
     gate_shape = None if gate is None else gate.shape
     gate, G = _gate_rows(gate, lead, M, N, ut)
     given, res = out or {}, {}
-
-    def rows(name):
-        t = given.get(name)
-        return _new(u) if t is None else _row_out(t, shape, ut.dtype, dev, name, lead)
-
-    res["du"] = du = rows("du")
+    du = given.get("du")
+    res["du"] = du = _new(u) if du is None else _row_out(du, shape, ut.dtype, dev, "du", lead)
     dres = dgp = dgn = dgate = ws = None
     if residual:
-        same = not post and gate is None and alpha == 1.0 and given.get("dresidual") is None
-        res["dresidual"] = du if same else rows("dresidual")
-        dres = None if same else res["dresidual"]
+        dres = given.get("dresidual")
+        if dres is None and not post and gate is None and alpha == 1.0:
+            res["dresidual"] = du  # the same
+        else:
+            res["dresidual"] = dres = _new(u) if dres is None else _row_out(dres, shape, ut.dtype, dev, "dresidual", lead)
     if params:
         if post:
             res["dgamma_post"] = dgp = _out(given.get("dgamma_post"), (N,), wdtype, dev, "dgamma_post")
@@ -1202,9 +1201,11 @@ def block_norm_bwd(dy, dh, u, h, stats, gamma_post=None, gamma_pre=None, gate=No
             res["dgate"] = dgate = (torch.empty(gate_shape, dtype=gate.dtype, device=dev) if t is None
                                     else _out(t, tuple(gate_shape), gate.dtype, dev, "dgate"))
         if dgp is not None or dgn is not None or dgate is not None:
-            ws = _workspace(lib.block_norm_bwd_workspace_size(M, N, G), dev, workspace)
-            if workspace is not None:
-                _device_of(ut, ws)
+            if workspace is None:
+                ws = _workspace(lib.block_norm_bwd_workspace_size(M, N, G), dev, None)
+            else:
+                _device_of(ut, workspace)
+                ws = workspace
     _run("block_norm_bwd", lib.block_norm_bwd, dev, _ptr(dyt), _ptr(dht), ut.data_ptr(), _ptr(ht), stats.data_ptr(),
          _ptr(gamma_post), _ptr(gamma_pre), _ptr(gate), du.data_ptr(), _ptr(dres), _ptr(dgp), _ptr(dgn), _ptr(dgate),
          M, N, G, lddy, lddh, ldu, ldh, alpha, (SWG_NORM_POST if post else 0) | (SWG_NORM_PRE if pre else 0), code,

@@ -15,6 +15,12 @@ constexpr int kMaxThreads = 1024;  // of the kernels for longest rows
 constexpr int kBlock = 256;        // threads of a block, unless a row takes more
 constexpr int kMaxGroup = 512;     // threads of a group, and of a block
 
+// 1 / sqrt(x): rsqrtf with a Newton step, to about an ulp, as its error is a whole row's (0 for infinity)
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x), e = fmaf(-x * r, r, 1.0f);
+  return e == e ? fmaf(0.5f * r, e, r) : r;
+}
+
 // ---- many whole rows: a group's next rows are on their way into shared memory
 // A thread that holds a row's vectors has but one more row of them under way; four rows of all tensors in a ring of
 // shared memory, one bulk copy a tensor and row, keep the memory busy over a row's reductions. The group's first thread

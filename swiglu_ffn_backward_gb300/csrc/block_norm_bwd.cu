@@ -251,10 +251,15 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
     const uint32_t block = kRagged ? in_seg / apart : in_seg, phase = kRagged ? in_seg - block * apart : 0u;
     w.r = seg * segment + phase + block * chunk_rows * apart;
     w.end = min((seg + 1) * segment, w.r + chunk_rows * apart);
-    w.shift = kRagged ? shift_of(static_cast<const T*>(a.du) + static_cast<int64_t>(w.r) * a.N) : 0;
-    w.n = (N + w.shift + E - 1) / E;
-    w.mine = min(R * G, w.n - n0);
+    if constexpr (kRagged) {
+      w.shift = shift_of(static_cast<const T*>(a.du) + static_cast<int64_t>(w.r) * a.N);
+      w.n = (N + w.shift + E - 1) / E;
+      w.mine = min(R * G, w.n - n0);
+    }
   };
+  const int whole = min(R * G, N / E - n0);  // the block's vectors of a whole row
+  auto mine_of = [&](const Walk& w) { return kRagged ? w.mine : whole; };
+  auto shift_in = [&](const Walk& w) { return kRagged ? w.shift : 0; };
   // a walk behind its chunk's last row goes on to the next chunk that has rows (a phase of ragged rows may have none)
   auto settle = [&](Walk& w) {
     while (w.c < chunks && w.r >= w.end) {
@@ -273,8 +278,8 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
     const void* from[kTensors];
     uint32_t bytes[kTensors];
     const Span span = kRagged ? span_of(r, a.M, ahead.n, n0, ahead.mine, ahead.shift, ahead.n * E - ahead.shift - N)
-                              : Span{0, ahead.mine};
-    const int j0 = (n0 + span.first) * E - ahead.shift;  // the first column that is copied
+                              : Span{0, whole};
+    const int j0 = (n0 + span.first) * E - shift_in(ahead);  // the first column that is copied
     from[0] = static_cast<const T*>(a.u) + r * a.ldu + j0;
     from[1] = pre_norm ? static_cast<const T*>(a.h) + r * a.ldh + j0 : nullptr;
     from[2] = pre_norm ? static_cast<const T*>(a.dy) + r * a.lddy + j0 : nullptr;
@@ -294,12 +299,12 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
     for (int i = 0; i < ring.stages; ++i) issue();
   Walk w{unit, 0, 0, 0, 0, 0};
   if (w.c < chunks) enter(w);
-  auto column = [&](int i) { return (n0 + in + i * G) * E - w.shift; };
+  auto column = [&](int i) { return (n0 + in + i * G) * E - shift_in(w); };
   float2 pre[R][P], post[R][P];  // gamma_pre; gamma_post, without kRowGate times the gate
   if (!kRagged) {
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      if (in + i * G < w.mine) load_weights<T, false>(a.gamma_pre, column(i), N, f32, 1.0f, pre[i]);
+      if (in + i * G < mine_of(w)) load_weights<T, false>(a.gamma_pre, column(i), N, f32, 1.0f, pre[i]);
   }
   bool refill = false;
   struct Vectors {  // a thread's vector of each tensor, from the stage
@@ -322,13 +327,13 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
     enter(w);
     bool edge[R];  // vectors that reach beyond the row
 #pragma unroll
-    for (int i = 0; i < R; ++i) edge[i] = kRagged && in + i * G < w.mine && (column(i) < 0 || column(i) + E > N);
+    for (int i = 0; i < R; ++i) edge[i] = kRagged && in + i * G < mine_of(w) && (column(i) < 0 || column(i) + E > N);
     float2 ss[R][P], sp[R][P];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int e = 0; e < P; ++e) ss[i][e] = sp[i][e] = pair(0.0f);
-      if (in + i * G >= w.mine) continue;
+      if (in + i * G >= mine_of(w)) continue;
       if (kRagged) load_weights<T, kRagged>(a.gamma_pre, column(i), N, f32, 1.0f, pre[i]);
       load_weights<T, kRagged>(a.gamma_post, column(i), N, f32, 1.0f, post[i]);
       if (!kRowGate && a.gate != nullptr) {
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
       float2 s0 = pair(0.0f), s1 = s0, s2 = s0;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        if (in + i * G >= w.mine) continue;
+        if (in + i * G >= mine_of(w)) continue;
         const Vectors v = vectors(stage, i);
         float2 q[P];
         if constexpr (kRowGate) stage_pairs<T>(stage + 4 * R * G * 16, in + i * G, !kRagged && gate32, q);
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
       const float2 c2 = pair(post_norm ? -fmaf(-m1 * fh, s[2], s[1]) * fu * inv_n : 0.0f);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        if (in + i * G >= w.mine) continue;
+        if (in + i * G >= mine_of(w)) continue;
         Vectors x = vectors(stage, i);
         float2 q[P];
         if constexpr (kRowGate) stage_pairs<T>(stage + 4 * R * G * 16, in + i * G, !kRagged && gate32, q);
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
     if (a.part == nullptr) continue;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (in + i * G >= w.mine) continue;
+      if (in + i * G >= mine_of(w)) continue;
       float* to = a.part + static_cast<int64_t>(w.c) * 2 * a.N + column(i);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
@@ -666,18 +671,18 @@ BnChunks chunks_of(int64_t M, int64_t rows_per_gate, int64_t units, int64_t apar
   BnChunks k;
   k.segment = rows_per_gate > 1 ? rows_per_gate : M;
   k.apart = apart;
-  const int64_t segments = M / k.segment, rows = (k.segment + apart - 1) / apart;  // of a phase, at most
-  int64_t best = INT64_MAX;
+  const int64_t phases = M / k.segment * apart, rows = (k.segment + apart - 1) / apart;  // of a phase, at most
   const int64_t least = (rows + kMostRows - 1) / kMostRows;
-  const int64_t most = std::min(rows, std::max(least, (2 * units + segments * apart - 1) / (segments * apart)));
-  const int64_t step = std::max<int64_t>(1, (most - least) / 64);
-  for (int64_t n = least; n <= most; n += step) {
-    const int64_t per = (rows + n - 1) / n, chunks = segments * apart * ((rows + per - 1) / per);
+  int64_t best = INT64_MAX;
+  // one or two chunks a group, or as few as may be
+  for (const int64_t n : {least, units / phases, (units + phases - 1) / phases, 2 * units / phases}) {
+    const int64_t m = std::min(rows, std::max(least, n));
+    const int64_t per = (rows + m - 1) / m, of = (rows + per - 1) / per, chunks = phases * of;
     const int64_t cost = (chunks + units - 1) / units * (per + 1);
     if (cost < best) {
       best = cost;
       k.rows = per;
-      k.per_segment = apart * ((rows + per - 1) / per);
+      k.per_segment = apart * of;
       k.chunks = chunks;
     }
   }
@@ -878,17 +883,20 @@ int64_t most_chunks(int64_t M, int64_t N, int64_t rows_per_gate) {
   return most;
 }
 
+// the rows' means, whose place is a multiple of 16 bytes
+int64_t mean_floats(int64_t M) { return (M + 3) / 4 * 4; }
+
 }  // namespace
 
 size_t bn_workspace_bytes(int64_t M, int64_t N, int64_t rows_per_gate) {
-  return (static_cast<size_t>(most_chunks(M, N, rows_per_gate)) * 2 * N + M) * sizeof(float);
+  return (static_cast<size_t>(most_chunks(M, N, rows_per_gate)) * 2 * N + mean_floats(M)) * sizeof(float);
 }
 
 cudaError_t launch_block_norm_bwd(const BnBwdArgs& given, void* workspace, int dtype, cudaStream_t stream) {
   BnBwdArgs a = given;
   if (workspace != nullptr) {  // the rows' means, then the chunks' sums
-    a.part = static_cast<float*>(workspace);
-    a.mean = a.part + most_chunks(a.M, a.N, a.rows_per_gate) * 2 * a.N;
+    a.mean = static_cast<float*>(workspace);
+    a.part = a.mean + mean_floats(a.M);
   }
   return dtype == 0   ? bwd_type<float>(a, stream)
          : dtype == 1 ? bwd_type<__half>(a, stream)

@@ -60,7 +60,7 @@ __global__ void __maxnreg__(kFwdRegs<kRagged>)
     float s[1] = {s2.x + s2.y};
     sum(s);
     share(s);
-    return __frsqrt_rn(fmaf(s[0], inv_n, a.eps));
+    return inverse_root(fmaf(s[0], inv_n, a.eps));
   };
   Row next;
   const int64_t M = a.M + (kNarrow ? (threadIdx.x & 31) / G : 0);  // the rows of a warp's groups end together
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kMaxThreads) bn_fwd_long_kernel(const BnFwdArg
         const float v = to_f(u[j]);
         p[0] = fmaf(v, v, p[0]);
       });
-      ru = __frsqrt_rn(fmaf(block_sum(s[0], buf), inv_n, a.eps));
+      ru = inverse_root(fmaf(block_sum(s[0], buf), inv_n, a.eps));
     }
     auto value = [&](int64_t j) {  // h_j, rounded as it is stored
       if (a.h == nullptr) return to_f(u[j]);
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kMaxThreads) bn_fwd_long_kernel(const BnFwdArg
         const float v = value(j);
         p[0] = fmaf(v, v, p[0]);
       });
-      rh = __frsqrt_rn(fmaf(block_sum(s[0], buf), inv_n, a.eps));
+      rh = inverse_root(fmaf(block_sum(s[0], buf), inv_n, a.eps));
     }
     for (int64_t j = threadIdx.x; j < a.N; j += blockDim.x) {
       const float v = value(j);
@@ -276,7 +276,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 ? 80 : 128)
     }
     refill = false;
     share(s);
-    return __frsqrt_rn(fmaf(s[0], inv_n, a.eps));
+    return inverse_root(fmaf(s[0], inv_n, a.eps));
   };
   T *h = static_cast<T*>(a.h) + begin * a.N, *y = static_cast<T*>(a.y) + begin * a.N;  // of the row
   const Rows<T> rows_u(a.u, a.ldu, a.M, a.N), rows_r(a.residual, a.ldr, a.M, a.N), rows_g(a.gate, a.N, a.M, a.N);
