@@ -378,14 +378,10 @@ cudaError_t launch_split(const void* A, int64_t lda, const void* B, int64_t ldb,
                : launch_split_of<kAOuter, kBOuter, false>(A, lda, B, ldb, L, C, R, epi, stream);
 }
 
-// Whether the kernel on CTA pairs is the faster one: it takes whole waves of tiles of 256 x 256, 64 of r in 0.35 us,
-// and the last tile's epilogue comes behind its products.
+// Whether the kernel on CTA pairs is the faster one, by the estimates of both.
 bool use_pairs(const PairPlan& p, int64_t L, int64_t C, int64_t R, bool b_outer, int sms) {
   if (C <= 128) return false;  // half of a tile's rows and more would be empty
-  const int64_t pairs = std::max(1, sms / 2);
-  const double waves = static_cast<double>((p.tiles_i * p.tiles_j * p.parts + pairs - 1) / pairs);
-  const double pair = waves * std::max(static_cast<double>(p.per) * 0.35, 4.0) + 5.5 + (p.parts > 1 ? 5.0 : 0.0);
-  return pair < split_plan(L, C, R, b_outer, sms).us;
+  return p.us < split_plan(L, C, R, b_outer, sms).us;
 }
 
 }  // namespace
@@ -393,7 +389,7 @@ bool use_pairs(const PairPlan& p, int64_t L, int64_t C, int64_t R, bool b_outer,
 cudaError_t launch_linear_fwd(const void* x, const void* w, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
                               int64_t ldx, cudaStream_t stream) {
   const int sms = device_sm_count();
-  const PairPlan p = linear_pair_plan(M, N, K, false, sms);
+  const PairPlan p = linear_pair_plan(M, N, K, false, false, sms);
   if (use_pairs(p, N, M, K, false, sms))
     return launch_linear_pair<false, true>(x, ldx, w, N, M, N, K, epi, p, nullptr, stream);
   return launch_split<true, false>(w, N, x, ldx, N, M, K, epi, stream);
@@ -402,7 +398,7 @@ cudaError_t launch_linear_fwd(const void* x, const void* w, const LinearEpilogue
 cudaError_t launch_linear_dx(const void* dz, const void* w, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
                              int64_t lddz, cudaStream_t stream) {
   const int sms = device_sm_count();
-  const PairPlan p = linear_pair_plan(M, K, N, false, sms);
+  const PairPlan p = linear_pair_plan(M, K, N, true, false, sms);
   if (use_pairs(p, K, M, N, false, sms))
     return launch_linear_pair<false, false>(dz, lddz, w, N, M, K, N, epi, p, nullptr, stream);
   return launch_split<false, false>(w, N, dz, lddz, K, M, N, epi, stream);
@@ -410,14 +406,14 @@ cudaError_t launch_linear_dx(const void* dz, const void* w, const LinearEpilogue
 
 size_t linear_dw_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   const int sms = device_sm_count();
-  const PairPlan p = linear_pair_plan(K, N, M, true, sms);
+  const PairPlan p = linear_pair_plan(K, N, M, true, true, sms);
   return use_pairs(p, N, K, M, true, sms) ? p.part_bytes : 0;
 }
 
 cudaError_t launch_linear_dw(const void* x, const void* dz, const LinearEpilogue& epi, int64_t M, int64_t K, int64_t N,
                              int64_t ldx, int64_t lddz, float* part, cudaStream_t stream) {
   const int sms = device_sm_count();
-  const PairPlan p = linear_pair_plan(K, N, M, true, sms);
+  const PairPlan p = linear_pair_plan(K, N, M, true, true, sms);
   if (use_pairs(p, N, K, M, true, sms))
     return launch_linear_pair<true, true>(x, ldx, dz, lddz, K, N, M, epi, p, part, stream);
   return launch_split<true, true>(dz, lddz, x, ldx, N, K, M, epi, stream);

@@ -210,8 +210,10 @@ constexpr int kLinearNoAct = 16;
 struct PairPlan {
   int64_t tiles_i, tiles_j, nkb, per, parts;
   size_t part_bytes;
+  bool wide;  // tiles of 256 x 512
+  double us;  // an estimate of its time
 };
-PairPlan linear_pair_plan(int64_t I, int64_t J, int64_t R, bool cut, int sms);
+PairPlan linear_pair_plan(int64_t I, int64_t J, int64_t R, bool gradient, bool cut, int sms);
 // out[i][j] = sum_r A[i, r] B[j, r]; kAOuter, kBOuter: r is the operand's outermost dimension, its rows lda, ldb apart.
 // With plan.parts > 1 the epilogue is a residual that is y itself, at most.
 template <bool kAOuter, bool kBOuter>

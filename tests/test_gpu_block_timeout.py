@@ -67,6 +67,21 @@ def test_pair_forward(entry, residual):
     check_all(g)
 
 
+@pytest.mark.parametrize("entry,residual", [(0, False), (3, True), (40, False)])
+def test_wide_pair_forward(entry, residual):
+    # wide tiles: 141 blocks of 64, a ring of four stages
+    swg, t = _swg(), linear_inputs(2000, 9000, 4000, BF16)
+    r = t["residual"] if residual else None
+    g = {"y": guarded((2000, 4000), BF16)}
+    swg.swg_inject_stall(swg.SWG_INJECT_LINEAR, entry, LIMIT)
+    swg.linear_fwd(t["x"], t["w"], residual=r, out={"y": g["y"].t})
+    _expect_timeout(swg)
+    check_all(g)
+    check_linear_fwd(t, swg.linear_fwd(t["x"], t["w"], residual=r, out={"y": g["y"].t}), BF16, None, None, r)
+    swg.swg_check()
+    check_all(g)
+
+
 @pytest.mark.parametrize("entry", [0, 40])
 def test_pair_backward(entry):
     # the armed launch is that of dw, cut into parts

@@ -55,8 +55,10 @@ def test_backward(M, K, N, dtype):
     swg.swg_check()
 
 
-# results of many tiles, which go to the kernel on CTA pairs: whole tiles and ragged ones, several waves, bands
-LARGE = [(8192, 512, 1024), (8100, 264, 2056), (5001, 1032, 1528), (20000, 64, 264), (2600, 72, 8008), (300, 200, 40008)]
+# results of many tiles, which go to the kernel on CTA pairs: whole tiles and ragged ones, several waves, bands; the last
+# one in wide tiles
+LARGE = [(8192, 512, 1024), (8100, 264, 2056), (5001, 1032, 1528), (20000, 64, 264), (2600, 72, 8008), (300, 200, 40008),
+         (2000, 9000, 4000)]
 
 
 @pytest.mark.parametrize("M,K,N", LARGE)
@@ -72,7 +74,8 @@ def test_large_forward(M, K, N, dtype):
     swg.swg_check()
 
 
-@pytest.mark.parametrize("M,K,N", [(8192, 512, 1024), (5001, 1032, 1528), (2600, 8008, 72), (9000, 2056, 264), (70000, 512, 520)])
+@pytest.mark.parametrize("M,K,N", [(8192, 512, 1024), (5001, 1032, 1528), (2600, 8008, 72), (9000, 2056, 264), (70000, 512, 520), (70000, 1000, 1000),
+                                   (2000, 4000, 4104)])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_large_backward(M, K, N, dtype):
     swg, t = _swg(), linear_inputs(M, K, N, dtype, seed=35)
