@@ -4,15 +4,15 @@ logits, and scoring of given tokens with the result:
     h  = u + r                            layer_norm_fwd (adds the residual)
     x  = LN(h)
     a  = SiLU(x W_g) (x W_fc)             swiglu_fwd
-    h' = h + a W_out                      layer_norm_fwd
+    h' = h + a W_out                      linear_fwd; the sum inside the next norm
     z  = LN(h') E^T                       the logits
     loss, dz                              distill_fwd_bwd (dz over z)
-    ... back through layer_norm_bwd, swiglu_bwd, layer_norm_bwd
+    ... back through layer_norm_bwd, linear_bwd, swiglu_bwd, layer_norm_bwd
 
     python examples/distill_step.py [--tokens 2048 --cols 512 --hidden 1024 --vocab 32000 --steps 20]
 
-u and r stand for what attention and the residual stream bring. The matrix products by W_out and E are
-plain library ones.
+u and r stand for what attention and the residual stream bring. The matrix products by E are plain library
+ones.
 """
 
 import argparse
@@ -43,7 +43,7 @@ def forward(p, u, r):
     """The logits, and what the backward needs."""
     n1 = swg.layer_norm_fwd(u, p["gamma1"], p["beta1"], residual=r)
     f = swg.swiglu_fwd(n1["y"], p["w_g"], p["w_fc"])
-    n2 = swg.layer_norm_fwd(f["y"] @ p["w_out"], p["gamma2"], p["beta2"], residual=n1["h"])
+    n2 = swg.layer_norm_fwd(swg.linear_fwd(f["y"], p["w_out"])["y"], p["gamma2"], p["beta2"], residual=n1["h"])
     return n2["y"] @ p["embed"].t(), (n1, f, n2)
 
 
@@ -52,8 +52,9 @@ def backward(p, saved, dz):
     n1, f, n2 = saved
     grads = {"embed": dz.t() @ n2["y"]}
     dh2, grads["gamma2"], grads["beta2"] = swg.layer_norm_bwd(dz @ p["embed"], n2["h"], n2["stats"], gamma=p["gamma2"])
-    grads["w_out"] = f["y"].t() @ dh2
-    ffn = swg.swiglu_bwd(n1["y"], p["w_g"], p["w_fc"], dh2 @ p["w_out"].t(), f["g"], f["fc"], return_dg=False)
+    down = swg.linear_bwd(dh2, f["y"], p["w_out"], bias=False)
+    grads["w_out"] = down["dw"]
+    ffn = swg.swiglu_bwd(n1["y"], p["w_g"], p["w_fc"], down["dx"], f["g"], f["fc"], return_dg=False)
     grads["w_g"], grads["w_fc"] = ffn["dw_g"], ffn["dw_fc"]
     # dh2 also reaches h past the block: it is added inside the kernel
     grads["u"], grads["gamma1"], grads["beta1"] = swg.layer_norm_bwd(ffn["dx"], n1["h"], n1["stats"],

@@ -1,8 +1,9 @@
 /*
  * swiglu_bwd.h -- C ABI of the GB300 (sm_103a) SwiGLU-FFN backward, SwishGrad,
- * the sibling activation gradients, the GroupNorm backward, and the row-wise
- * operators around such a layer in a language model: layer norm, token log
- * probabilities and distillation from a teacher's top logits.
+ * the sibling activation gradients, the GroupNorm backward, and the operators
+ * around such a layer in a language model: the linear layer with its epilogue,
+ * the norms between blocks, layer norm, token log probabilities and
+ * distillation from a teacher's top logits.
  *
  * Operations (sources are web pages; each function cites the section it follows):
  *   [P1] "PyPTO-Gym in practice: the fused SwiGLU backward operator"

@@ -14,7 +14,7 @@ namespace lin {
 // |x| = 13.5, where e^{-x^2/2} leaves fp32), so that x Phi(x) keeps its relative accuracy in the negative tail, where
 // 1 + erf would cancel.
 struct Gauss2 {
-  float2 cdf, e;
+  float2 cdf, e, tail;
 };
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ Gauss2 gauss2(float2 x) {
@@ -29,8 +29,8 @@ __device__ __forceinline__ Gauss2 gauss2(float2 x) {
   q = __ffma2_rn(q, t, both(0.14123354852199554f));
   q = __ffma2_rn(q, t, both(0.1387006789445877f));
   q = __ffma2_rn(q, t, both(0.14117228984832764f));
-  const float2 tail = __fmul2_rn(__fmul2_rn(q, t), g.e);
-  g.cdf = make_float2(x.x >= 0.0f ? 1.0f - tail.x : tail.x, x.y >= 0.0f ? 1.0f - tail.y : tail.y);
+  g.tail = __fmul2_rn(__fmul2_rn(q, t), g.e);
+  g.cdf = make_float2(x.x >= 0.0f ? 1.0f - g.tail.x : g.tail.x, x.y >= 0.0f ? 1.0f - g.tail.y : g.tail.y);
   return g;
 }
 
@@ -39,7 +39,11 @@ constexpr int kActNone = kLinearNoAct;
 template <int kAct>
 __device__ __forceinline__ float2 activate(float2 z) {
   if constexpr (kAct == 0) return __fmul2_rn(z, sigmoid_pair2(z).s);
-  if constexpr (kAct == 1) return __fmul2_rn(z, gauss2(z).cdf);
+  if constexpr (kAct == 1) {  // z Phi(z) = max(z, 0) - |z| Phi(-|z|); |z| held finite, as Phi(-inf) is 0
+    const float2 m = make_float2(fmaxf(z.x, 0.0f), fmaxf(z.y, 0.0f));
+    const float2 n = make_float2(-fminf(fabsf(z.x), 3e38f), -fminf(fabsf(z.y), 3e38f));
+    return __ffma2_rn(n, gauss2(z).tail, m);
+  }
   if constexpr (kAct == 2) {
     auto f = [](float v) { return v <= -3.0f ? 0.0f : (v < 3.0f ? v * fmaf(v, 1.0f / 6.0f, 0.5f) : v); };
     return make_float2(f(z.x), f(z.y));

@@ -11,9 +11,9 @@
 //   warps 2-9       drain the finished accumulator (each CTA its own 128 rows; two warps a quarter of the lanes, each on
 //                   half of the columns) while the tensor cores fill the other one: bias, activation and residual in
 //                   fp32, 64 columns at a time, through staging blocks of 32 rows x 128 bytes and TMA stores. The bias is
-//                   loaded under the products and passed around by shuffles (loads behind the products took half of
-//                   the epilogue); a residual (or the old dw) comes by TMA loads two blocks ahead.
-// Tiles in flight share operands: eight tile rows at a time, the row index fastest (tile_of).
+//                   loaded under the products and passed around through shared memory (by shuffles: 1130
+//                   clocks for 64 columns instead of 550); a residual (or the old dw) comes by TMA loads two blocks ahead.
+// Tiles in flight share operands: eight tile rows at a time, the row index fastest (Walk).
 // A reduction too long for too few tiles (dw) is cut into parts: fp32 partial results, added by a second kernel in a
 // fixed order.
 //
@@ -54,6 +54,7 @@ struct __align__(1024) PairSmem {
   uint8_t b[STAGES][Form<kWide>::kHalves * kHalf];
   // a warp's blocks for TMA stores: two, or with a residual one and two residual blocks; of wide tiles one
   uint8_t stage[kEpiWarps][Form<kWide>::kStaged];
+  float bias[kEpiWarps][32];          // of a warp's 32 columns
   uint64_t full[STAGES];              // leader: both CTAs' copies of the stage have landed
   uint64_t empty[STAGES];             // the MMAs reading the stage are done (committed to both CTAs)
   uint64_t tmem_full[2];              // the tile's MMAs into this accumulator are done (both CTAs)
@@ -79,23 +80,40 @@ struct PairArgs {
 struct Tile {
   int i0, j0, kb, n, part;  // first row and column; first block of r and their number
 };
-// Tile t: parts one after the other; in a part bands of eight tile rows, in a band column after column, the row index
-// fastest, so that the tiles in flight (76 pairs) read a square of some eight rows and ten columns of operand tiles.
+// The walk over the tiles: parts one after the other; in a part bands of eight tile rows, in a band column after column, the
+// row index fastest, so that the tiles in flight (76 pairs) read a square of some eight rows and ten columns of operand
+// tiles. Kept as a position, not found by divisions (four of them took a sixth of a short tile's epilogue).
 template <bool kWide>
-__device__ __forceinline__ Tile tile_of(int t, const PairArgs& a) {
-  constexpr int kBand = 8;
-  const int per_part = a.tiles_i * a.tiles_j;
-  Tile w;
-  w.part = t / per_part;
-  t -= w.part * per_part;
-  const int band = t / (kBand * a.tiles_j), rows = min(kBand, a.tiles_i - band * kBand);
-  const int in = t - band * kBand * a.tiles_j;
-  w.i0 = (band * kBand + in % rows) * 2 * BM;
-  w.j0 = in / rows * Form<kWide>::kColumns;
-  w.kb = w.part * a.per;
-  w.n = min(a.per, a.nkb - w.kb);
-  return w;
-}
+struct Walk {
+  static constexpr int kBand = 8;
+  int t = 0, part = 0, band = 0, in = 0;  // the tile, its part, the first row of its band, its place in the band
+  __device__ __forceinline__ Walk(int first, const PairArgs& a) { step(first, a); }
+  __device__ __forceinline__ void step(int n, const PairArgs& a) {
+    t += n;
+    in += n;
+    while (t < a.tiles) {
+      const int size = min(kBand, a.tiles_i - band) * a.tiles_j;
+      if (in < size) break;
+      in -= size;
+      if ((band += kBand) >= a.tiles_i) {
+        band = 0;
+        ++part;
+      }
+    }
+  }
+  __device__ __forceinline__ bool more(const PairArgs& a) const { return t < a.tiles; }
+  __device__ __forceinline__ Tile tile(const PairArgs& a) const {
+    const int rows = min(kBand, a.tiles_i - band);
+    const int j = rows == kBand ? in / kBand : in / rows;
+    Tile w;
+    w.i0 = (band + in - j * rows) * 2 * BM;
+    w.j0 = j * Form<kWide>::kColumns;
+    w.part = part;
+    w.kb = part * a.per;
+    w.n = min(a.per, a.nkb - w.kb);
+    return w;
+  }
+};
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -170,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t gj = 0;
       bool stopped = false;
-      for (int t = pair_id; t < args.tiles && !s.abort_flag && !stopped; t += pairs) {
-        const Tile w = tile_of<kWide>(t, args);
+      for (Walk<kWide> at(pair_id, args); at.more(args) && !s.abort_flag && !stopped; at.step(pairs, args)) {
+        const Tile w = at.tile(args);
         const int i0 = w.i0 + BM * static_cast<int>(crank);
         for (int i = 0; i < w.n && !s.abort_flag; ++i, ++gj) {
           if (static_cast<int64_t>(gj) == args.stall_at) {
@@ -216,8 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       uint32_t gj = 0, it = 0;
       bool ok = true;
-      for (int t = pair_id; t < args.tiles && ok; t += pairs, ++it) {
-        const Tile w = tile_of<kWide>(t, args);
+      for (Walk<kWide> at(pair_id, args); at.more(args) && ok; at.step(pairs, args), ++it) {
+        const Tile w = at.tile(args);
         const uint32_t buf = it % F::kBuffers;
         if (it >= F::kBuffers) {
           if (!mbar_wait(&s.tmem_empty[buf], (it / F::kBuffers - 1) & 1, args.wait_limit)) {
@@ -262,17 +280,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, nb = 0;           // tiles, staged blocks
     // the residual's blocks of 32 columns, four a tile: two of them are under way
     uint32_t nf = 0, nr = 0;           // asked for, read
-    int ft = pair_id;                  // the tile of the next one
+    Walk<kWide> ft(pair_id, args);     // the tile of the next one
     auto fetch = [&]() {
-      if (ft >= args.tiles) return;
+      if (!ft.more(args)) return;
       if (lane == 0) {
-        const Tile w = tile_of<kWide>(ft, args);
+        const Tile w = ft.tile(args);
         uint64_t* bar = &s.res_full[e][nf & 1];
         mbar_arrive_expect_tx(bar, kRes);
         tma_load_2d(s.stage[e] + kOut + (nf & 1) * kRes, &tm_r, bar, w.j0 + half * 128 + (nf & 3) * 32,
                     w.i0 + BM * static_cast<int>(crank) + q * 32);
       }
-      if ((++nf & 3) == 0) ft += pairs;
+      if ((++nf & 3) == 0) ft.step(pairs, args);
     };
     if (ahead) {
       fetch();
@@ -296,22 +314,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++nb;
     };
-    for (int t = pair_id; t < args.tiles; t += pairs, ++it) {
-      const Tile w = tile_of<kWide>(t, args);
+    // the bias of this lane's column in a block of 32 of a tile, as it is in memory: widened where it is used, so that
+    // nothing waits for the load before
+    auto bias_of = [&](const Tile& w, int c) -> uint32_t {
+      const int j = w.j0 + half * kMine + c * 32 + lane;
+      if (p.bias == nullptr || j >= args.J) return 0u;
+      return p.bias_f32 ? static_cast<const uint32_t*>(p.bias)[j] : static_cast<const uint16_t*>(p.bias)[j];
+    };
+    Walk<kWide> at(pair_id, args);
+    Tile next = at.tile(args);
+    uint32_t b0 = bias_of(next, 0), b1 = bias_of(next, 1);  // loaded under the columns before them
+    for (bool more = at.more(args); more; ++it) {
+      const Tile w = next;
+      at.step(pairs, args);
+      if ((more = at.more(args))) next = at.tile(args);
       const uint32_t buf = it % F::kBuffers;
       const int row0 = w.i0 + BM * static_cast<int>(crank) + q * 32, col0 = w.j0 + half * kMine;
-      // the bias of this lane's column in a block of 32
-      auto bias_of = [&](int c) {
-        const int j = col0 + c * 32 + lane;
-        if (p.bias == nullptr || args.part != nullptr || j >= args.J) return 0.0f;
-        return p.bias_f32 ? static_cast<const float*>(p.bias)[j]
-                          : widen2<kF16>(static_cast<const uint16_t*>(p.bias)[j]).x;
-      };
-      float bias[4];  // loaded once a tile, under the products
-      if constexpr (!kWide) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) bias[c] = bias_of(c);
-      }
       bool ready = false;
       if (!dead && !s.abort_flag) {
         ready = mbar_wait(&s.tmem_full[buf], (it / F::kBuffers) & 1, args.wait_limit);
@@ -329,11 +347,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < kMine / 32; c += 2) {  // 64 columns at a time
           const int col = col0 + c * 32;
-          float b0 = 0.0f, b1 = 0.0f;
-          if constexpr (kWide) {
-            b0 = bias_of(c);
-            b1 = bias_of(c + 1);
-          }
           uint4 res[8] = {};
           if (kWide && add && row0 + lane < args.I) {
             const uint16_t* from = p.residual + static_cast<int64_t>(row0 + lane) * p.ldr + col;
@@ -360,20 +373,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
           float2 f[2][16];
-          if constexpr (!kWide) {
-            b0 = c == 0 ? bias[0] : bias[2];
-            b1 = c == 0 ? bias[1] : bias[3];
-          }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             f[0][i] = make_float2(__uint_as_float(v[0][2 * i]), __uint_as_float(v[0][2 * i + 1]));
             f[1][i] = make_float2(__uint_as_float(v[1][2 * i]), __uint_as_float(v[1][2 * i + 1]));
-            if (p.bias != nullptr) {
-              f[0][i] = __fadd2_rn(f[0][i], make_float2(__shfl_sync(0xffffffffu, b0, 2 * i),
-                                                        __shfl_sync(0xffffffffu, b0, 2 * i + 1)));
-              f[1][i] = __fadd2_rn(f[1][i], make_float2(__shfl_sync(0xffffffffu, b1, 2 * i),
-                                                        __shfl_sync(0xffffffffu, b1, 2 * i + 1)));
+          }
+          if (p.bias != nullptr) {  // from each lane's register to all lanes, through shared memory
+            float* row = s.bias[e];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t raw = h == 0 ? b0 : b1;
+              row[lane] = p.bias_f32 ? __uint_as_float(raw) : widen2<kF16>(raw).x;
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 b = *reinterpret_cast<const float4*>(row + 4 * i);
+                f[h][2 * i] = __fadd2_rn(f[h][2 * i], make_float2(b.x, b.y));
+                f[h][2 * i + 1] = __fadd2_rn(f[h][2 * i + 1], make_float2(b.z, b.w));
+              }
+              __syncwarp();
             }
+            const bool last = c + 2 == kMine / 32;
+            b0 = bias_of(last ? next : w, last ? 0 : c + 2);
+            b1 = bias_of(last ? next : w, last ? 1 : c + 3);
           }
           if (p.z != nullptr) {
             uint8_t* blk = staged();
