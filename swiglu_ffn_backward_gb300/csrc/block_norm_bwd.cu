@@ -8,6 +8,8 @@ using namespace bn;
 
 // ---- backward: a row in the registers of a group of threads, one vector of each tensor a thread
 // A group takes chunks of rows, chunk after chunk, and writes the chunk's two column sums. kShared: as in the forward.
+// For few rows and rows that a cluster shares (257 x 1001 fp32 10 us with the sums); 16384 x 4096 bf16, 8 gates, 265 us
+// against the ring's 144.
 struct Sums4 {
   uint64_t come[2];
   float4 sums[2][kMaxCluster];
@@ -207,7 +209,8 @@ __global__ void __launch_bounds__(kMaxGroup)
   share.end(status);
 }
 
-// Backward over a ring, R vectors of a row a thread. The gate row is the chunk's own (kRowGate: one more tensor in the
+// Backward over a ring, R vectors of a row a thread. HBM-bound: 16384 x 4096 bf16, 8 gates, 144 us with the sums (83% of
+// the copy rate), 220000 x 512 224 to 253 us (79 to 89%). The gate row is the chunk's own (kRowGate: one more tensor in the
 // ring), so that its columns and gamma_post's are one factor in registers.
 constexpr int kBwdBlock = 256, kBwdBlocks = 2;  // threads of a block, at most, and such blocks an SM
 template <typename T, int R, bool kShared, bool kRowGate, bool kFull, bool kRagged>

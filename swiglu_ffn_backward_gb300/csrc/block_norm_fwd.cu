@@ -19,7 +19,9 @@ namespace {
 
 using namespace bn;
 
-// ---- forward: a row in the registers of a group of threads, R vectors each
+// ---- forward: a row in the registers of a group of threads, R vectors each: for few rows and for rows that a cluster
+// shares (1 x 4096 bf16 4.1 us). With many rows the reads pause for each row's reductions: 16384 x 4096 bf16, 8 gates,
+// 111.6 us against the ring's 97.6.
 // kShared: the S blocks of a cluster, of one group each, share a row.
 template <bool kRagged>
 constexpr int kFwdRegs = kRagged ? 128 : 80;
@@ -197,7 +199,8 @@ __global__ void __launch_bounds__(kMaxThreads) bn_fwd_long_kernel(const BnFwdArg
   }
 }
 
-// Forward: a group takes rows one after the other, so that it keeps its gate row's columns in registers until the next
+// Forward, HBM-bound: 16384 x 4096 bf16, 8 gates, 97.6 us (81% of the copy rate), with a gate for each row 105 (94%). A
+// group takes rows one after the other, so that it keeps its gate row's columns in registers until the next
 // gate row begins; kRowGate: a gate for each row is one more tensor in the ring.
 constexpr int kFwdBlocks = 3;  // blocks of 256 threads an SM, with 80 registers a thread
 // Such blocks an SM over a ring: in 16 bits two with 128 registers a thread (16384 x 4096 bf16, 8 gates, 95 us, three with

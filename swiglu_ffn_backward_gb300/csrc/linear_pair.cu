@@ -14,6 +14,9 @@
 //                   loaded under the products and passed around through shared memory (by shuffles: 1130
 //                   clocks for 64 columns instead of 550); a residual (or the old dw) comes by TMA loads two blocks ahead.
 // Tiles in flight share operands: eight tile rows at a time, the row index fastest (Walk).
+// Measured, bf16: 16384 x 14336 x 4096 with residual 1013 us (97% of the measured tensor rate; up to 1150 where the power
+// cap slows the clock), 220000 x 512 x 1024 with GELU and z 274 us, bound by the epilogue: of 11000 clocks a tile
+// 7800 are the activation's.
 // A reduction too long for too few tiles (dw) is cut into parts: fp32 partial results, added by a second kernel in a
 // fixed order.
 //

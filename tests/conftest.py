@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -25,3 +26,11 @@ def pytest_collection_modifyitems(config, items):
     for item in items:
         if "gpu" in item.keywords:
             item.add_marker(skip)
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _no_garbage():
+    """An exception that a test keeps holds the test's tensors until the collector runs. It runs between modules, so that
+    a later test that measures memory does not see them go at a time that depends on the tests before it."""
+    yield
+    gc.collect()
