@@ -289,3 +289,21 @@ def test_refusals():
     with pytest.raises(swg.SwgError):  # a residual that overlaps y without being it
         swg.linear_fwd(x, w, residual=buf[1:5], out={"y": buf[:4]})
     swg.swg_check()
+
+
+# the column sums of up to 512 rows by one cluster, of more by a second launch; added to what is there
+@pytest.mark.parametrize("M", [1, 8, 9, 63, 65, 500, 512, 513])
+@pytest.mark.parametrize("N", [8, 264, 1032])
+@pytest.mark.parametrize("act", [None, "gelu"])
+def test_bias_gradient(M, N, act):
+    swg, t = _swg(), linear_inputs(M, 16, N, BF16, seed=71)
+    for db_dtype in (BF16, F32):
+        g = {"db": guarded((N,), db_dtype), "ws": workspace(swg.linear_bwd_workspace_size(M, 16, N, act))}
+        kw = dict(z=t["z"], act=act, need_dx=False, need_dw=False, workspace=g["ws"].t, out={"db": g["db"].t})
+        got = swg.linear_bwd(t["dy"], t["x"], t["w"], db_dtype=db_dtype, **kw)
+        check_linear_bwd(t, got, BF16, act, db_dtype=db_dtype)
+        old = f64(g["db"].t)
+        got = swg.linear_bwd(t["dy"], t["x"], t["w"], accumulate=True, db_dtype=db_dtype, **kw)
+        check_linear_bwd(t, got, BF16, act, old={"db": old}, db_dtype=db_dtype)
+        swg.swg_check()
+        check_all(g)
