@@ -994,7 +994,7 @@ def linear_fwd(x, w, b=None, act: str | None = None, residual=None, save_z: bool
     """y = f(x w + b) + residual for x [..., K] and w [K, N] (fp16 or bf16, K and N multiples of 8): a dict of y
     [..., N], and of z = x w + b, which linear_bwd takes with an activation, when save_z is True. act: None, or
     "silu", "gelu", "hardswish"; b [N] (x's dtype or fp32) and residual [..., N] may be None. `out` may supply the
-    outputs; out["y"] may be the residual itself."""
+    outputs; out["y"] may be the residual itself. A w that is not dense (a transposed view) is copied at every call."""
     if stream is not None:
         return _on_stream(stream, linear_fwd, x, w, b, act=act, residual=residual, save_z=save_z, out=out)
     code, shape = _act_code(act), x.shape if isinstance(x, torch.Tensor) else None
