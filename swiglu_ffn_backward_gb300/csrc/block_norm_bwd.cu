@@ -868,7 +868,9 @@ cudaError_t bwd_any(const BnBwdArgs& a, cudaStream_t stream) {
 }
 template <typename T>
 cudaError_t bwd_type(const BnBwdArgs& a, cudaStream_t stream) {
-  const bool whole = whole_vectors(a.N, sizeof(T), {a.dy, a.dh, a.u, a.h, a.du, a.dres, a.gdtype != 0 ? a.dgate : nullptr},
+  // dgate with a row for each row goes out as vectors, whatever its type (a shared one element by element)
+  const bool whole = whole_vectors(a.N, sizeof(T),
+                                   {a.dy, a.dh, a.u, a.h, a.du, a.dres, a.rows_per_gate == 1 ? a.dgate : nullptr},
                                    {a.lddy, a.lddh, a.ldu, a.ldh}, {a.gamma_post, a.gamma_pre, a.gate});
   return whole ? bwd_any<T, false>(a, stream) : bwd_any<T, true>(a, stream);
 }
