@@ -1,5 +1,6 @@
 // Backward of the norms between blocks (block_norm_fwd.cu has the formulas).
 #include "block_norm.cuh"
+#include "row_chunks.h"
 
 namespace swg {
 namespace {
@@ -92,11 +93,9 @@ __global__ void __launch_bounds__(kMaxGroup)
        c < k.chunks + late; c += units) {
     const bool mine = !kNarrow || c < k.chunks;
     // the chunk's rows: count of them, `apart` rows from one to the next
-    const int64_t seg = c / k.per_segment, in = c - seg * k.per_segment, block = in / k.apart;
-    const int64_t first = in - block * k.apart + k.apart * block * k.rows;  // within the segment
-    const int64_t left = (k.segment - first + k.apart - 1) / k.apart;
-    int count = mine ? static_cast<int>(max(static_cast<int64_t>(0), min(left, k.rows))) : 0;
-    const int64_t r0 = seg * k.segment + first;
+    const ChunkRows<int64_t> rows = chunk_rows<true>(k, c);
+    int count = mine && rows.first < rows.end ? static_cast<int>((rows.end - rows.first + k.apart - 1) / k.apart) : 0;
+    const int64_t r0 = rows.first;
     const int shift = kRagged ? shift_of(static_cast<const T*>(a.du) + r0 * a.N) : 0;
     const int j = t * E - shift;
     const bool in_row = mine && j < N;
@@ -242,18 +241,16 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
   std::conditional_t<kShared, ClusterSum3, NoSum3> share(slots, S, stall);
   const int64_t stop_at = kShared ? -1 : stall.at;
   // the rows of the group's chunks in turn: of chunk c r, r + apart, ... below end
-  const uint32_t chunks = static_cast<uint32_t>(k.chunks), per_segment = static_cast<uint32_t>(k.per_segment);
-  const uint32_t segment = static_cast<uint32_t>(k.segment), chunk_rows = static_cast<uint32_t>(k.rows);
+  const uint32_t chunks = static_cast<uint32_t>(k.chunks);
   const uint32_t apart = kRagged ? static_cast<uint32_t>(k.apart) : 1u;
   struct Walk {  // 32 bits hold them
     uint32_t c, r, end;
     int shift, n, mine;  // elements from the 16-byte boundary before a row, its vectors, and this block's
   };
   auto enter = [&](Walk& w) {
-    const uint32_t seg = w.c / per_segment, in_seg = w.c - seg * per_segment;
-    const uint32_t block = kRagged ? in_seg / apart : in_seg, phase = kRagged ? in_seg - block * apart : 0u;
-    w.r = seg * segment + phase + block * chunk_rows * apart;
-    w.end = min((seg + 1) * segment, w.r + chunk_rows * apart);
+    const ChunkRows<uint32_t> rows = chunk_rows<kRagged>(k, w.c);
+    w.r = rows.first;
+    w.end = rows.end;
     if constexpr (kRagged) {
       w.shift = shift_of(static_cast<const T*>(a.du) + static_cast<int64_t>(w.r) * a.N);
       w.n = (N + w.shift + E - 1) / E;
@@ -341,7 +338,8 @@ __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)
       load_weights<T, kRagged>(a.gamma_post, column(i), N, f32, 1.0f, post[i]);
       if (!kRowGate && a.gate != nullptr) {
         float2 g[P];
-        const int64_t row = static_cast<uint32_t>(w.r) / static_cast<uint32_t>(a.rows_per_gate);
+        // the chunk's segment: a chunk without rows has its first row elsewhere, or nowhere
+        const int64_t row = w.c / static_cast<uint32_t>(k.per_segment);
         load_weights<T, kRagged>(static_cast<const char*>(a.gate) + row * a.N * (gate32 ? 4 : sizeof(T)), column(i), N,
                                  gate32, 1.0f, g);
 #pragma unroll
@@ -516,11 +514,10 @@ template <typename T>
 __global__ void __launch_bounds__(kColThreads) bn_param_long_kernel(const BnBwdArgs a, const BnChunks k, int64_t first) {
   const int64_t j = static_cast<int64_t>(blockIdx.x) * kColThreads + threadIdx.x, chunk = first + blockIdx.y;
   if (j >= a.N) return;
-  const int64_t seg = chunk / k.per_segment, r0 = seg * k.segment + chunk % k.per_segment * k.rows;  // apart is 1
-  const int64_t r1 = min((seg + 1) * k.segment, r0 + k.rows);
+  const ChunkRows<int64_t> rows = chunk_rows<false>(k, chunk);  // apart is 1
   const float pre = a.pre && a.gamma_pre != nullptr ? load_any(a.gamma_pre, j, a.wdtype) : 1.0f;
   float s = 0.0f, p = 0.0f;
-  for (int64_t r = r0; r < r1; ++r) {
+  for (int64_t r = rows.first; r < rows.end; ++r) {
     const float ru = a.post ? a.stats[2 * r] : 0.0f, rh = a.pre ? a.stats[2 * r + 1] : 0.0f;
     const Element<T> e(a, r, j, ru, rh);
     const float d = fmaf(rh, e.a * pre, fmaf(-a.mean[r], e.hh, e.dh));
@@ -666,31 +663,6 @@ __global__ void __launch_bounds__(32 * kReduceWarps)
 }
 
 // ---- host
-// Chunks of rows whose column sums are taken together: of one gate row where the gate has fewer rows than M, of at most
-// 128 rows (like terms are rounded the same way, and a longer chain drifts), and such that `units` groups that take
-// them in turn have nearly equal work: rows, and for each chunk the writing of its sums, about one row's.
-constexpr int64_t kMostRows = 128;
-BnChunks chunks_of(int64_t M, int64_t rows_per_gate, int64_t units, int64_t apart) {
-  BnChunks k;
-  k.segment = rows_per_gate > 1 ? rows_per_gate : M;
-  k.apart = apart;
-  const int64_t phases = M / k.segment * apart, rows = (k.segment + apart - 1) / apart;  // of a phase, at most
-  const int64_t least = (rows + kMostRows - 1) / kMostRows;
-  int64_t best = INT64_MAX;
-  // one or two chunks a group, or as few as may be
-  for (const int64_t n : {least, units / phases, (units + phases - 1) / phases, 2 * units / phases}) {
-    const int64_t m = std::min(rows, std::max(least, n));
-    const int64_t per = (rows + m - 1) / m, of = (rows + per - 1) / per, chunks = phases * of;
-    const int64_t cost = (chunks + units - 1) / units * (per + 1);
-    if (cost < best) {
-      best = cost;
-      k.rows = per;
-      k.per_segment = apart * of;
-      k.chunks = chunks;
-    }
-  }
-  return k;
-}
 // The groups of threads that take chunks: those of one block of 512 threads (or a cluster of blocks) on each of 152
 // SMs, for rows of n vectors. A plan that does not depend on the device, so that the workspace's size does not.
 int64_t units_of(int64_t n) {

@@ -181,14 +181,6 @@ struct BnBwdArgs {
   float* part;  // set by the launcher: the chunks' column sums (null: no parameter gradients)
   float* mean;  // and the rows' rstd(h) mean(a h^), for rows of any length
 };
-// rows whose column sums are taken together
-struct BnChunks {
-  int64_t segment;      // rows of a gate row, or all
-  int64_t rows;         // of a chunk, at most
-  int64_t apart;        // distance of a chunk's rows
-  int64_t per_segment;  // chunks: chunk c of a segment has its rows c % apart + apart (c / apart rows + i)
-  int64_t chunks;
-};
 size_t bn_workspace_bytes(int64_t M, int64_t N, int64_t rows_per_gate);
 cudaError_t launch_block_norm_fwd(const BnFwdArgs& a, int dtype, cudaStream_t stream);
 // workspace: bn_workspace_bytes, or null where no parameter gradient is wanted

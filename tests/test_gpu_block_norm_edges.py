@@ -1,10 +1,11 @@
-"""The norms between blocks where outputs lie on their elements' alignment only, as slices of a flat buffer do (GPU)."""
+"""The norms between blocks at the edges of what the kernels plan for: outputs that lie on their elements' alignment only, as
+slices of a flat buffer do, and rows that do not fill the chunks whose column sums are taken together (GPU)."""
 
 import pytest
 import torch
 
 from ._block import check_norm_bwd, norm_inputs
-from ._guard import check_all, guarded
+from ._guard import check_all, guarded, workspace
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -44,3 +45,18 @@ def test_gradient_of_a_shared_gate(dtype, gdtype):
     swg.swg_check()
     check_all(g)
     assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+# ragged rows in rings whose chunks are not all of one length, or have no rows: one gate row for all, and gate rows of fewer
+# rows than there are offsets within 16 bytes
+@pytest.mark.parametrize("M,N,gates,dtype,gdtype", [(60001, 515, 1, BF16, F32), (20000, 1001, 10000, BF16, BF16),
+                                                    (21000, 515, 7000, F16, F32), (9800, 2047, 1400, F32, F32)])
+def test_gates_of_chunks_without_rows(M, N, gates, dtype, gdtype):
+    swg, t = _swg(), norm_inputs(M, N, dtype, F32, gates, gdtype)
+    kw = dict(gamma_post=t["gamma_post"], gamma_pre=t["gamma_pre"], gate=t["gate"])
+    out = swg.block_norm_fwd(t["u"], t["residual"], **kw)
+    ws = workspace(swg.block_norm_bwd_workspace_size(M, N, gates))
+    got = swg.block_norm_bwd(t["dy"], t["dh"], t["u"], out["h"], out["stats"], workspace=ws.t, **kw)
+    swg.swg_check()
+    ws.check("workspace")
+    check_norm_bwd(t, out["h"], out["stats"], got, dtype, F32, gdtype)
