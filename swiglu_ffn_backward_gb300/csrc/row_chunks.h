@@ -19,6 +19,7 @@ struct BnChunks {
   int64_t segment;      // rows of a gate row, or all
   int64_t rows;         // of a chunk, at most
   int64_t apart;        // distance of a chunk's rows
+  int64_t phases;       // runs of such rows in a segment: apart, or as many as it has rows
   int64_t per_segment;  // chunks
   int64_t chunks;
 };
@@ -29,16 +30,16 @@ template <typename Int>
 struct ChunkRows {
   Int segment, first, end;
 };
-// chunk c of all: chunk i of a segment has the rows (i % apart) + apart (i / apart rows + 0, 1, ...) of it. kApart: the
+// chunk c of all: chunk i of a segment has the rows (i % phases) + apart (i / phases rows + 0, 1, ...) of it. kApart: the
 // plan's apart is not 1. Int: 32 bits hold every row and chunk.
 template <bool kApart, typename Int>
 SWG_HOST_DEVICE ChunkRows<Int> chunk_rows(const BnChunks& k, Int c) {
   const Int per = static_cast<Int>(k.per_segment), segment = static_cast<Int>(k.segment);
-  const Int apart = kApart ? static_cast<Int>(k.apart) : 1;
+  const Int phases = kApart ? static_cast<Int>(k.phases) : 1;
   ChunkRows<Int> w;
   w.segment = c / per;
-  const Int in = c - w.segment * per, block = kApart ? in / apart : in, phase = in - block * apart;
-  const Int rows = static_cast<Int>(k.rows) * apart, last = (w.segment + 1) * segment;
+  const Int in = c - w.segment * per, block = kApart ? in / phases : in, phase = in - block * phases;
+  const Int rows = static_cast<Int>(k.rows) * (kApart ? static_cast<Int>(k.apart) : 1), last = (w.segment + 1) * segment;
   w.first = w.segment * segment + phase + block * rows;
   w.end = w.first + rows < last ? w.first + rows : last;
   return w;
@@ -46,13 +47,14 @@ SWG_HOST_DEVICE ChunkRows<Int> chunk_rows(const BnChunks& k, Int c) {
 
 // Chunks of one gate row where the gate has fewer rows than M, of at most 128 rows (like terms are rounded the same way,
 // and a longer chain drifts), and such that `units` groups that take them in turn have nearly equal work: rows, and for
-// each chunk the writing of its sums, about one row's.
+// each chunk the writing of its sums, about one row's. Segments of fewer rows than `apart` have one chunk a row.
 constexpr int64_t kMostRows = 128;
 inline BnChunks chunks_of(int64_t M, int64_t rows_per_gate, int64_t units, int64_t apart) {
   BnChunks k;
   k.segment = rows_per_gate > 1 ? rows_per_gate : M;
   k.apart = apart;
-  const int64_t phases = M / k.segment * apart, rows = (k.segment + apart - 1) / apart;  // of a phase, at most
+  k.phases = std::min(apart, k.segment);
+  const int64_t phases = M / k.segment * k.phases, rows = (k.segment + apart - 1) / apart;  // of a phase, at most
   const int64_t least = (rows + kMostRows - 1) / kMostRows;
   int64_t best = INT64_MAX;
   // one or two chunks a group, or as few as may be
@@ -63,7 +65,7 @@ inline BnChunks chunks_of(int64_t M, int64_t rows_per_gate, int64_t units, int64
     if (cost < best) {
       best = cost;
       k.rows = per;
-      k.per_segment = apart * of;
+      k.per_segment = k.phases * of;
       k.chunks = chunks;
     }
   }

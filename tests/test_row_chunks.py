@@ -88,3 +88,19 @@ def test_a_chunks_gate_row_is_there(plans):
     assert any(p["empty"] > 0 for p in plans)
     for p in plans:
         assert p["bad_gate"] == 0, p
+
+
+def test_no_more_chunks_than_rows(plans):
+    # a chunk's column sums are two fp32 rows of the workspace
+    for p in plans:
+        # a segment's runs of rows `apart` from one another differ by one row, and are cut alike
+        assert p["chunks"] <= p["M"] + (p["apart"] - 1) * p["segments"], p
+        if p["per_gate"] < p["apart"] and p["per_gate"] > 1:
+            assert p["chunks"] == p["M"] and p["empty"] == 0, p
+
+
+def test_workspace_of_short_runs():
+    # ragged rows whose gate rows serve two or three each: below four 16-bit tensors and a bit
+    from swiglu_ffn_backward_gb300 import _binding as b
+    for M, N, G in ((40000, 1001, 20000), (21000, 1001, 7000), (33000, 515, 16500), (9000, 4003, 1800)):
+        assert b.lib.block_norm_bwd_workspace_size(M, N, G) <= M * (8 * N + 4) + 16
