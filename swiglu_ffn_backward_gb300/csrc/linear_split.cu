@@ -37,6 +37,7 @@ constexpr int kMaxStages = 16;
 constexpr int kThreads = 256;
 constexpr int kBoxBytes = 64 * kRed * 2;  // a box of 64 x 64 elements
 constexpr int kMaxSplit = 8;              // portable cluster size
+constexpr int kMostRing = 196 * 1024;     // bytes of a ring
 
 struct SplitArgs {
   Epilogue epi;
@@ -269,7 +270,7 @@ SplitPlan split_cost(int64_t L, int64_t C, int64_t R, int NT, int S, int per_sm,
   p.nkb = static_cast<int>((R + kRed - 1) / kRed);
   const int stage = kABytes + NT * kRed * 2;
   p.per_sm = per_sm;
-  p.stages = std::min(kMaxStages, (p.per_sm == 2 ? 108 : 196) * 1024 / stage);
+  p.stages = std::min(kMaxStages, (p.per_sm == 2 ? 108 * 1024 : kMostRing) / stage);
   // blocks that run at once, of 152 and 304: a cluster's lie in one part of the device (cudaOccupancyMaxActiveClusters)
   constexpr int kRoom[2][kMaxSplit] = {{152, 152, 138, 144, 140, 138, 105, 120}, {304, 304, 291, 296, 290, 276, 266, 288}};
   const int64_t blocks = p.tiles * S;
@@ -353,8 +354,9 @@ cudaError_t launch_split_of(const void* A, int64_t lda, const void* B, int64_t l
                     p.tiles_c, p.nkb,             p.S,                 p.stages,            inj.wait_limit, inj.stall_at};
   const size_t smem = static_cast<size_t>(p.stages) * (kABytes + p.NT * kRed * 2) + 1024;
   const auto kernel = linear_split_kernel<kAOuter, kBOuter, kF16>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // any plan's limit, not this one's: the limit is the kernel's, so a smaller one would fail the launch of another host
+  // thread's larger plan
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRing + 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.tiles * p.S));

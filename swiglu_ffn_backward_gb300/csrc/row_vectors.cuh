@@ -333,6 +333,18 @@ int rows_apart(int64_t N) {
 }
 // shared memory that a kernel has beside its static one without asking (48 KB with that)
 constexpr size_t kPlainSmem = 40 * 1024;
+// Lets a kernel take all shared memory that a block can have beside its static one. Always as much, whatever this call's
+// plan takes: the limit is the kernel's, so a smaller one would fail the launch of another host thread's larger plan.
+template <typename Kernel>
+cudaError_t allow_all_smem(Kernel kernel, int dev) {
+  cudaFuncAttributes of;
+  int most = 0;
+  cudaError_t e = cudaFuncGetAttributes(&of, kernel);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              most - static_cast<int>(of.sharedSizeBytes));
+}
 // blocks of a persistent kernel that fit on the device at once (asked once for each device and block size)
 struct FitCache {
   int device = -1, threads = 0, fit = 0;
@@ -346,7 +358,7 @@ cudaError_t blocks_that_fit(Kernel kernel, FitCache& cache, int block, size_t sm
   if (cache.device != dev || cache.threads != block || cache.bytes != smem) {
     int per_sm = 0;
     if (smem > kPlainSmem) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      e = allow_all_smem(kernel, dev);
       if (e != cudaSuccess) return e;
     }
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, block, smem);
