@@ -17,8 +17,8 @@
 // Measured, bf16: 16384 x 14336 x 4096 with residual 1013 us (97% of the measured tensor rate; up to 1150 where the power
 // cap slows the clock), 220000 x 512 x 1024 with GELU and z 274 us, bound by the epilogue: of 11000 clocks a tile
 // 7800 are the activation's.
-// A reduction too long for too few tiles (dw) is cut into parts: fp32 partial results, added by a second kernel in a
-// fixed order.
+// A reduction too long for too few tiles, or for one accumulator (dw), is cut into parts: fp32 partial results, added by a
+// second kernel in a fixed order.
 //
 // Every wait is bounded; a timeout sets the status word, stops issuing, drains the pair's copies, frees TMEM and returns.
 #include <algorithm>
@@ -494,14 +494,19 @@ __global__ void __launch_bounds__(256) linear_parts_kernel(const float4* part, i
                                                            bool accumulate) {
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n4;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    float4 s = part[i];
+    float4 s = part[i], t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // 64 in sequence, and these sums
     for (int k = 1; k < parts; ++k) {
+      if (k % 64 == 0) {
+        t = make_float4(t.x + s.x, t.y + s.y, t.z + s.z, t.w + s.w);
+        s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
       const float4 v = part[k * n4 + i];
       s.x += v.x;
       s.y += v.y;
       s.z += v.z;
       s.w += v.w;
     }
+    s = make_float4(t.x + s.x, t.y + s.y, t.z + s.z, t.w + s.w);
     if (accumulate) {
       const uint2 o = out[i];
       const float2 a = widen2<kF16>(o.x), b = widen2<kF16>(o.y);
@@ -534,8 +539,10 @@ PairPlan pair_plan_of(int64_t I, int64_t J, int64_t R, bool gradient, bool cut, 
   p.nkb = (R + BK - 1) / BK;
   p.parts = 1;
   const int64_t tiles = p.tiles_i * p.tiles_j, pairs = std::max(1, sms / 2);
-  // cut only where whole tiles leave half of the pairs without work, and into parts of 16 blocks or more
+  // cut where whole tiles leave half of the pairs without work, into parts of 16 blocks or more, and where one accumulator
+  // would take more than kMostBlocks
   if (cut && 2 * tiles <= pairs) p.parts = std::max<int64_t>(1, std::min(pairs / tiles, p.nkb / 16));
+  if (cut) p.parts = std::max(p.parts, (p.nkb + kMostBlocks - 1) / kMostBlocks);
   p.per = (p.nkb + p.parts - 1) / p.parts;
   p.parts = (p.nkb + p.per - 1) / p.per;
   p.part_bytes = p.parts > 1 ? static_cast<size_t>(p.parts) * I * J * sizeof(float) : 0;

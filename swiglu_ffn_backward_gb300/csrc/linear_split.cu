@@ -383,10 +383,13 @@ cudaError_t launch_split(const void* A, int64_t lda, const void* B, int64_t ldb,
                : launch_split_of<kAOuter, kBOuter, false>(A, lda, B, ldb, L, C, R, epi, stream);
 }
 
-// Whether the kernel on CTA pairs is the faster one, by the estimates of both.
+// Whether the kernel on CTA pairs takes a product: by the estimates of both, and for dw (b_outer) where a block here would
+// take too many rows in one accumulator.
 bool use_pairs(const PairPlan& p, int64_t L, int64_t C, int64_t R, bool b_outer, int sms) {
-  if (C <= 128) return false;  // half of a tile's rows and more would be empty
-  return p.us < split_plan(L, C, R, b_outer, sms).us;
+  if (C <= 128 && !b_outer) return false;  // half of a tile's rows and more would be empty
+  const SplitPlan s = split_plan(L, C, R, b_outer, sms);
+  if (b_outer && (s.nkb + s.S - 1) / s.S > kMostBlocks) return true;
+  return C > 128 && p.us < s.us;
 }
 
 }  // namespace

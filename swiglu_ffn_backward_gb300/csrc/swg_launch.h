@@ -197,6 +197,10 @@ struct LinearEpilogue {  // z = product + bias, y = f(z) + residual; y, z dense
   bool f16, bias_f32;
 };
 constexpr int kLinearNoAct = 16;
+// Blocks of 64 rows that one accumulator takes for dw, at most. The tensor cores cut off what an addition to it leaves below
+// fp32, for some four rows at a time, so that terms of one sign lose 5e-9 of their sum a row: after 32768 rows 1.8e-4, a
+// third of fp16's rounding (without this limit 4194304 x 64 x 64 fp16 was off by 3.2e-3, and 16777216 rows by 1.1e-2).
+constexpr int64_t kMostBlocks = 512;
 // the kernel for large results (linear_pair.cu): out [I, J], a reduction of length R, cut into parts where that helps
 // (fp32 partial results: part_bytes of workspace)
 struct PairPlan {
