@@ -1072,7 +1072,7 @@ def linear_bwd(dy, x, w, z=None, act: str | None = None, bias: bool = True, need
         _device_of(g, workspace)
         ws = workspace
     elif bias or need_dw or code != SWG_ACT_NONE:
-        ws = _workspace(lib.linear_bwd_workspace_size(M, K if K > 0 else 8, N, code), dev, None)
+        ws = _workspace(lib.linear_bwd_workspace_size(M, K, N, code), dev, None)
     _run("linear_bwd", lib.linear_bwd, dev, g.data_ptr(), _ptr(xt), _ptr(wt), _ptr(z), _ptr(need.get("dx")),
          _ptr(need.get("dw")), _ptr(need.get("db")), M, K, N, lddy, ldx, code, SWG_ACCUMULATE if accumulate else 0,
          _DTYPE[g.dtype], _DTYPE[db_dtype], _ptr(ws), _nbytes(ws))

@@ -1231,8 +1231,9 @@ swg_status linear_fwd(const void* x, const void* w, const void* b, const void* r
 }
 
 size_t linear_bwd_workspace_size(int64_t M, int64_t K, int64_t N, swg_act act) {
-  if (M <= 0 || K <= 0 || N <= 0 || check_linear(M, K, N, act, SWG_BF16, SWG_BF16) != SWG_OK) return 0;
-  return align256(swg::linear_dz_workspace_bytes(M, N)) + align256(swg::linear_dw_workspace_bytes(M, K, N)) +
+  if (M <= 0 || K < 0 || N <= 0 || check_linear(M, K, N, act, SWG_BF16, SWG_BF16) != SWG_OK) return 0;
+  return align256(swg::linear_dz_workspace_bytes(M, N)) +
+         (K > 0 ? align256(swg::linear_dw_workspace_bytes(M, K, N)) : 0) +
          (act != SWG_ACT_NONE ? align256(static_cast<size_t>(M) * static_cast<size_t>(N) * 2) : 0);
 }
 
@@ -1264,7 +1265,7 @@ swg_status linear_bwd(const void* dy, const void* x, const void* w, const void* 
   const size_t sums = align256(swg::linear_dz_workspace_bytes(M, N));
   const size_t parts = some && K > 0 ? align256(swg::linear_dw_workspace_bytes(M, K, N)) : 0;
   if (some && (want_db || act_on || (want_dw && parts > 0))) {
-    const size_t need = linear_bwd_workspace_size(M, K > 0 ? K : 8, N, act);
+    const size_t need = linear_bwd_workspace_size(M, K, N, act);
     if (workspace == nullptr || workspace_bytes < need) return SWG_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SWG_ERR_UNSUPPORTED;
     const Range ws = rng(workspace, static_cast<int64_t>(need));
