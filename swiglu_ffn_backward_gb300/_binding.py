@@ -979,6 +979,11 @@ def _tma_like(t, name, x, shape):
     return t, ld
 
 
+def _on_16_bytes(t):
+    """A dense tensor, copied where it does not lie on a 16-byte boundary (a slice of a flat buffer); None stays None."""
+    return t.clone() if t is not None and t.data_ptr() % 16 else t
+
+
 def _weight(w, x, K):
     if not isinstance(w, torch.Tensor) or not w.is_cuda:
         raise TypeError("w must be a CUDA tensor")
@@ -986,7 +991,7 @@ def _weight(w, x, K):
         raise ValueError(f"w must be [K, N] of {x.dtype}{'' if K is None else f' with K = {K}'}, "
                          f"got {tuple(w.shape)} of {w.dtype}")
     _device_of(x, w)
-    return w.contiguous()
+    return _on_16_bytes(w.contiguous())
 
 
 def linear_fwd(x, w, b=None, act: str | None = None, residual=None, save_z: bool = False, out: dict | None = None,
@@ -994,7 +999,8 @@ def linear_fwd(x, w, b=None, act: str | None = None, residual=None, save_z: bool
     """y = f(x w + b) + residual for x [..., K] and w [K, N] (fp16 or bf16, K and N multiples of 8): a dict of y
     [..., N], and of z = x w + b, which linear_bwd takes with an activation, when save_z is True. act: None, or
     "silu", "gelu", "hardswish"; b [N] (x's dtype or fp32) and residual [..., N] may be None. `out` may supply the
-    outputs; out["y"] may be the residual itself. A w that is not dense (a transposed view) is copied at every call."""
+    outputs; out["y"] may be the residual itself. A w that is not dense (a transposed view) is copied at every call, and
+    so is any input off a 16-byte boundary."""
     if stream is not None:
         return _on_stream(stream, linear_fwd, x, w, b, act=act, residual=residual, save_z=save_z, out=out)
     code, shape = _act_code(act), x.shape if isinstance(x, torch.Tensor) else None
@@ -1002,7 +1008,7 @@ def linear_fwd(x, w, b=None, act: str | None = None, residual=None, save_z: bool
     w, dev = _weight(w, xt, K), xt.device
     N = w.shape[1]
     want = (*shape[:-1], N)
-    b = _vector(b, "b", (N,), (xt.dtype, torch.float32), dev)
+    b = _on_16_bytes(_vector(b, "b", (N,), (xt.dtype, torch.float32), dev))
     res, ldr = _tma_like(residual, "residual", xt, want)
     given = out or {}
     out = {"y": _row_out(given.get("y"), want, xt.dtype, dev, "y", shape[:-1])}
@@ -1045,9 +1051,7 @@ def linear_bwd(dy, x, w, z=None, act: str | None = None, bias: bool = True, need
     if code != SWG_ACT_NONE:
         if z is None:
             raise ValueError("z, the forward's, is needed with an activation")
-        z = _vector(z, "z", shape, (g.dtype,), dev, lead)
-        if z.data_ptr() % 16:
-            z = z.clone()
+        z = _on_16_bytes(_vector(z, "z", shape, (g.dtype,), dev, lead))
     else:
         z = None
     given, need = dict(out or {}), {}
