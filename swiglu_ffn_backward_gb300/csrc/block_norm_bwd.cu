@@ -792,7 +792,8 @@ cudaError_t bwd_ring_one(const BnBwdArgs& a, const BnChunks& k, int64_t n, cudaS
   blocks = std::min(blocks, (k.chunks + groups - 1) / groups);
   kernel<<<static_cast<unsigned>(blocks), block, smem, stream>>>(a, k, p, G, 1, take_stall(kInjectBlockNormBwd),
                                                                 status_word_ptr());
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess || a.part == nullptr ? e : launch_reduce(a, k, stream);
 }
 template <typename T, bool kRowGate, bool kFull, bool kRagged>
 cudaError_t bwd_ring_shared(const BnBwdArgs& a, const BnChunks& k, int64_t n, cudaStream_t stream) {
@@ -800,20 +801,23 @@ cudaError_t bwd_ring_shared(const BnBwdArgs& a, const BnChunks& k, int64_t n, cu
   const Shared s = share_row(n, 2);
   const RingPlan p = ring_plan((4 + (kRowGate ? gate_slots<T>(a.gdtype) : 0)) * 2 * s.G * 16,
                                std::max(kBwdBlocks, kBwdBlocks * kBwdBlock / s.G), 1);
-  static std::mutex mu;
-  static StreamCache cache;
-  std::lock_guard<std::mutex> lk(mu);
-  const cudaError_t e = clusters_that_fit(kernel, cache, s.G, p.group_bytes, s.S);
-  if (e != cudaSuccess) return e;
-  if (cache.clusters < 1) return cudaErrorLaunchOutOfResources;
-  ClusterLaunch l(s.G, p.group_bytes, s.S, std::min<int64_t>(cache.clusters, k.chunks), stream);
-  return cudaLaunchKernelEx(&l.cfg, kernel, a, k, p, s.G, s.S, take_stall(kInjectBlockNormBwd), status_word_ptr());
+  {
+    static std::mutex mu;
+    static StreamCache cache;
+    std::lock_guard<std::mutex> lk(mu);
+    cudaError_t e = clusters_that_fit(kernel, cache, s.G, p.group_bytes, s.S);
+    if (e != cudaSuccess) return e;
+    if (cache.clusters < 1) return bwd_long<T>(a, stream);
+    ClusterLaunch l(s.G, p.group_bytes, s.S, std::min<int64_t>(cache.clusters, k.chunks), stream);
+    e = cudaLaunchKernelEx(&l.cfg, kernel, a, k, p, s.G, s.S, take_stall(kInjectBlockNormBwd), status_word_ptr());
+    if (e != cudaSuccess) return e;
+  }
+  return a.part == nullptr ? cudaSuccess : launch_reduce(a, k, stream);
 }
 template <typename T, bool kRowGate, bool kFull, bool kRagged>
 cudaError_t bwd_ring(const BnBwdArgs& a, const BnChunks& k, int64_t n, cudaStream_t stream) {
-  const cudaError_t e = n <= 2 * kBwdBlock ? bwd_ring_one<T, kRowGate, kFull, kRagged>(a, k, n, stream)
-                                           : bwd_ring_shared<T, kRowGate, kFull, kRagged>(a, k, n, stream);
-  return e != cudaSuccess || a.part == nullptr ? e : launch_reduce(a, k, stream);
+  return n <= 2 * kBwdBlock ? bwd_ring_one<T, kRowGate, kFull, kRagged>(a, k, n, stream)
+                            : bwd_ring_shared<T, kRowGate, kFull, kRagged>(a, k, n, stream);
 }
 template <typename T, bool kRagged>
 cudaError_t bwd_any(const BnBwdArgs& a, cudaStream_t stream) {
