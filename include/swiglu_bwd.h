@@ -433,9 +433,9 @@ swg_status layer_norm_bwd(const void* dy, const void* x, const float* stats,
  * linear_bwd_workspace_size(M, K, N, act) bytes (16-byte aligned); it may be NULL for
  * dx alone without an activation.
  * Products are accumulated in fp32 on the tensor cores in a fixed order (bitwise
- * reproducible; dw's by parts of at most 32768 rows, as a longer chain of terms of one
- * sign drifts), bias, activation and residual are applied in fp32, each output is
- * rounded once (RNE). Any M >= 0; K and N multiples of 8, leading dimensions too
+ * reproducible; of terms of one sign an accumulator loses 5e-9 of their sum a term,
+ * along K and N as they are, along M, for dw, in parts of at most 32768 rows), bias,
+ * activation and residual are applied in fp32, each output is rounded once (RNE). Any M >= 0; K and N multiples of 8, leading dimensions too
  * (where M > 1), pointers 16-byte aligned (SWG_ERR_UNSUPPORTED otherwise, and for K == 0
  * in linear_fwd). M == 0: dw and db are zeros (left alone with SWG_ACCUMULATE).
  * Errors: negative sizes, another dtype, bdtype, act or flag, a leading dimension

@@ -209,8 +209,10 @@ __global__ void __launch_bounds__(kMaxGroup)
 }
 
 // Backward over a ring, R vectors of a row a thread. HBM-bound: 16384 x 4096 bf16, 8 gates, 144 us with the sums (83% of
-// the copy rate), 220000 x 512 224 to 253 us (79 to 89%). The gate row is the chunk's own (kRowGate: one more tensor in the
-// ring), so that its columns and gamma_post's are one factor in registers.
+// the copy rate), 220000 x 512 248 us (80%), 8192 x 4096 fp32 140 us (85%). Forms of 16 bits that spill at 128 registers are
+// slower: a gate for each row 222 us (71%; 104 bytes of stores a thread), ragged rows 231 us for 16384 x 4001 (50%; 72 bytes, with
+// a gate for each row 144; in fp32, without spills, 8192 x 4001 173 to 185 us, 63 to 67%). The gate row is the chunk's own (kRowGate: one more
+// tensor in the ring), so that its columns and gamma_post's are one factor in registers.
 constexpr int kBwdBlock = 256, kBwdBlocks = 2;  // threads of a block, at most, and such blocks an SM
 template <typename T, int R, bool kShared, bool kRowGate, bool kFull, bool kRagged>
 __global__ void __launch_bounds__(kBwdBlock, kBwdBlocks)

@@ -21,7 +21,7 @@ using namespace bn;
 
 // ---- forward: a row in the registers of a group of threads, R vectors each: for few rows and for rows that a cluster
 // shares (1 x 4096 bf16 4.1 us). With many rows the reads pause for each row's reductions: 16384 x 4096 bf16, 8 gates,
-// 111.6 us against the ring's 97.6.
+// 111.6 us against the ring's 97.6 to 100.
 // kShared: the S blocks of a cluster, of one group each, share a row.
 template <bool kRagged>
 constexpr int kFwdRegs = kRagged ? 128 : 80;
@@ -199,12 +199,14 @@ __global__ void __launch_bounds__(kMaxThreads) bn_fwd_long_kernel(const BnFwdArg
   }
 }
 
-// Forward, HBM-bound: 16384 x 4096 bf16, 8 gates, 97.6 us (81% of the copy rate), with a gate for each row 105 (94%). A
+// Forward, HBM-bound: 16384 x 4096 bf16, 8 gates, 97.6 to 100 us (79 to 81% of the copy rate), with a gate for each row 105
+// (94%; the gate in fp32 137, 87%), 8192 x 4096 fp32 97 (82%); ragged, 16384 x 4001 bf16 131 (59%), 8192 x 4001 fp32 164 (47%). A
 // group takes rows one after the other, so that it keeps its gate row's columns in registers until the next
 // gate row begins; kRowGate: a gate for each row is one more tensor in the ring.
 constexpr int kFwdBlocks = 3;  // blocks of 256 threads an SM, with 80 registers a thread
 // Such blocks an SM over a ring: in 16 bits two with 128 registers a thread (16384 x 4096 bf16, 8 gates, 95 us, three with
-// 80 spill: 109), in fp32 three (8192 x 4096 90 us, two 116).
+// 80 spill: 109), in fp32 three (8192 x 4096 90 us, two 116; whole rows only were measured: ragged fp32 ones spill with 80
+// registers, 220 bytes of stores a thread at most).
 template <typename T>
 constexpr int kFwdRingBlocks = sizeof(T) == 4 ? 3 : 2;
 template <typename T, int R, bool kShared, bool kRowGate, bool kFull, bool kRagged>

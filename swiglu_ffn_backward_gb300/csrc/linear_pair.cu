@@ -14,9 +14,10 @@
 //                   loaded under the products and passed around through shared memory (by shuffles: 1130
 //                   clocks for 64 columns instead of 550); a residual (or the old dw) comes by TMA loads two blocks ahead.
 // Tiles in flight share operands: eight tile rows at a time, the row index fastest (Walk).
-// Measured, bf16: 16384 x 14336 x 4096 with residual 1013 us (97% of the measured tensor rate; up to 1150 where the power
-// cap slows the clock), 220000 x 512 x 1024 with GELU and z 274 us, bound by the epilogue: of 11000 clocks a tile
-// 7800 are the activation's.
+// Measured, bf16: 16384 x 14336 x 4096 with residual 1128 to 1157 us a call, which runs under the power cap (85 to 87% of the
+// measured tensor rate, 97 to 100% of the sustained one; 1010 us before the clock slows), 220000 x 512 x 1024 with GELU and z
+// 274 to 299 us, bound by the epilogue: of 11000 clocks a tile 7800 are the activation's. The wide form's epilogue spills 240
+// bytes a thread and loads 300, for its residual's registers.
 // A reduction too long for too few tiles, or for one accumulator (dw), is cut into parts: fp32 partial results, added by a
 // second kernel in a fixed order.
 //
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(256) linear_parts_kernel(const float4* part, i
 //   wide    0.62 us for twice the products, as a pair's copies of A serve 512 columns (96 KB); the accumulator is the
 //           whole of tensor memory, so that the epilogue stops the tensor cores, 3.5 us a tile for a gradient's plain
 //           rounding, 9 with bias, activation or residual
-// Measured, us, narrow and wide: forward 16384x14336x4096 1105 and 1056, 4096x4096x14336 285 and 318; dx of
+// Measured, us, narrow and wide, in short runs of each: forward 16384x14336x4096 1105 and 1056, 4096x4096x14336 285 and 318; dx of
 // 4096x4096x14336 300 and 277, of 220000x1024x512 174 and 206; dw of 16384x14336x4096 1160 and 1020, of 2048x4096x4096
 // 62 and 48.
 PairPlan pair_plan_of(int64_t I, int64_t J, int64_t R, bool gradient, bool cut, bool wide, int sms) {

@@ -16,8 +16,9 @@
 // block a share of the tile, and apply the epilogue: 16-byte loads and stores. A programmatic dependent launch: its
 // set-up runs beside the end of the kernel before it.
 //
-// Measured, bf16: 1 x 14336 x 4096 21.6 us and 77 x 4096 x 14336 24.3 us with 117 MB of w from HBM (80 and 73% of the copy
-// rate); 257 x 512 x 1024 with everything in L2 6.2 us, which is three launches' latencies and no rate.
+// Measured, bf16: 1 x 14336 x 4096 22 us and 77 x 4096 x 14336 25.4 us a call (79 and 70% of the copy rate, on one w of 117
+// MB, a part of which L2 still holds); with three w's in turn 24.1 and 26.7 us (72 and 66%). 257 x 512 x 1024 with
+// everything in L2 6.2 us, which is three launches' latencies and no rate.
 //
 // Every wait is bounded: a block whose wait ran out sets the status word, issues nothing more, waits (bounded) for
 // its copies and products in flight and goes through the cluster's barriers like the others.

@@ -149,7 +149,7 @@ struct KdArgs {
 };
 cudaError_t launch_distill(const KdArgs& a, bool forward, bool backward, int dtype, cudaStream_t stream);
 
-// ---- norms between blocks (block_norm.cu); dtype, wdtype, gdtype 0 = f32, 1 = f16, 2 = bf16
+// ---- norms between blocks (block_norm_fwd.cu, block_norm_bwd.cu); dtype, wdtype, gdtype 0 = f32, 1 = f16, 2 = bf16
 struct BnFwdArgs {
   const void* u;           // [M, N], rows ldu apart
   const void* residual;    // [M, N], rows ldr apart, or null (0)
