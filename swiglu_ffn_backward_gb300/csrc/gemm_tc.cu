@@ -362,7 +362,7 @@ static CUtensorMapSwizzle swizzle_mode(int bytes) {
                        : CU_TENSOR_MAP_SWIZZLE_128B;
 }
 
-// Encoding is a driver call that asks for a current context, which a host thread has none of before its first runtime
+// Encoding is a CUDA driver call that asks for a current context, which a host thread has none of before its first runtime
 // call that binds one: then the current device's is bound, and the map encoded again.
 template <typename Encode>
 static bool with_context(Encode encode) {
